@@ -322,7 +322,8 @@ def _plain_decode(s):
 
 def _plain_append(s):
     case = s["case"]
-    f = torch.float64  # a value next to a code's border must not fall on its other side
+    # 64 bits for the quantised types: a value next to a code's border must not fall on its other side
+    f = torch.float64 if case["kt"] in ("q8_0", "q4_0") else torch.float32
     k = s["xk"].to(f)
     if s["wk"] is not None:
         k = _normed(k, s["wk"].to(f))
@@ -331,7 +332,7 @@ def _plain_append(s):
     page = s["table"][s["seq"].long(), s["pos"].long() // case["page"]].long()
     row = s["pos"].long() % case["page"]
     s["k"][page, row] = _quantise(k, case["kt"])
-    s["v"][page, row] = _quantise(s["xv"].to(f), case["vt"])
+    s["v"][page, row] = _quantise(s["xv"].to(torch.float64), case["vt"])
     return {"k": _decoded(s["k"][page, row], case["kt"], torch.float32).to(torch.float16),
             "v": _decoded(s["v"][page, row], case["vt"], torch.float32).to(torch.float16)}
 
