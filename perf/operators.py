@@ -167,7 +167,8 @@ def _quantise(x, t):
         y = torch.where(d > 0, b / torch.where(d > 0, d, 1), 0)
         c = torch.trunc(y + torch.copysign(torch.full_like(y, 0.5), y)).clamp(-127, 127).to(torch.int8).view(torch.uint8)
     else:
-        at = b.abs().argmax(-1, keepdim=True)
+        mag = b.abs()
+        at = torch.where(mag == mag.amax(-1, keepdim=True), torch.arange(32, device=x.device), 31).amin(-1, keepdim=True)  # the first of equals
         d = b.gather(-1, at) / -8
         y = torch.where(d != 0, b / torch.where(d != 0, d, 1), 0)
         n = torch.floor(y + 8.5).clamp(0, 15).to(torch.uint8)
@@ -427,7 +428,8 @@ def _stored64(x, t):
         c = torch.sign(b) * torch.floor(mag / d.clamp_min(1e-300) + 0.5)
         c = c.clamp(-127, 127)
     else:
-        m = torch.gather(b, -1, mag.max(-1, keepdim=True).indices)
+        lead = torch.argmax((mag == mag.max(-1, keepdim=True).values) * torch.arange(32, 0, -1, device=x.device), -1, keepdim=True)
+        m = torch.gather(b, -1, lead)
         d = -m / 8.0
         c = torch.floor(b / torch.where(d == 0, torch.ones_like(d), d) + 8.5).clamp(0, 15) - 8.0
         c = torch.where(d == 0, torch.zeros_like(c), c)
