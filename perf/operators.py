@@ -163,8 +163,9 @@ def _quantise(x, t):
         return x.to(torch.float16).contiguous().view(torch.uint8)
     b = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     if t == "q8_0":
-        d = b.abs().amax(-1, keepdim=True) / 127
-        y = torch.where(d > 0, b / torch.where(d > 0, d, 1), 0)
+        top = b.abs().amax(-1, keepdim=True)
+        d = top / 127
+        y = torch.where(top > 0, b * 127 / torch.where(top > 0, top, 1), 0)  # one rounding: half of the largest is a tie
         c = torch.trunc(y + torch.copysign(torch.full_like(y, 0.5), y)).clamp(-127, 127).to(torch.int8).view(torch.uint8)
     else:
         mag = b.abs()
@@ -424,8 +425,9 @@ def _stored64(x, t):
     b = x.reshape(*x.shape[:-1], -1, 32)
     mag = b.abs()
     if t == "q8_0":
-        d = mag.max(-1, keepdim=True).values / 127.0
-        c = torch.sign(b) * torch.floor(mag / d.clamp_min(1e-300) + 0.5)
+        most = mag.max(-1, keepdim=True).values
+        d = most / 127.0
+        c = torch.sign(b) * torch.floor((127.0 * mag) / most.clamp_min(1e-300) + 0.5)
         c = c.clamp(-127, 127)
     else:
         lead = torch.argmax((mag == mag.max(-1, keepdim=True).values) * torch.arange(32, 0, -1, device=x.device), -1, keepdim=True)
