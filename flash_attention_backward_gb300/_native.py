@@ -10,9 +10,13 @@ LIB_PATH = os.path.join(_HERE, "libfa_back.so")
 FA_F32, FA_F16, FA_Q8_0, FA_Q4_0 = 0, 1, 2, 3
 STATUS = {0: "FA_OK", 1: "FA_ERR_NULL", 2: "FA_ERR_TYPE", 3: "FA_ERR_SHAPE", 4: "FA_ERR_ALIGN",
           5: "FA_ERR_UNSUPPORTED", 6: "FA_ERR_DEVICE", 7: "FA_ERR_CUDA", 8: "FA_ERR_TIMEOUT",
-          9: "FA_ERR_WORKSPACE"}
+          9: "FA_ERR_WORKSPACE", 10: "FA_ERR_PAGE"}
 
 FA_MASK_F16, FA_MASK_BITS = 0, 1
+
+# fa_paged.h
+FA_ACT_F32, FA_ACT_F16, FA_ACT_BF16, FA_ACT_RAW = 0, 1, 2, 3
+FA_ROPE_PAIRS, FA_ROPE_HALVES = 0, 1
 
 _lib = None
 
@@ -22,6 +26,27 @@ class fa_strides(ctypes.Structure):
     rows, word strides of the mask."""
     _fields_ = [(n, ctypes.c_int64) for n in ("q_row", "q_head", "q_comp", "do_row", "do_head", "do_comp",
                                              "k_cell", "k_head", "v_cell", "v_head", "mask_head", "mask_row")]
+
+
+class fa_rope(ctypes.Structure):
+    """struct fa_rope of fa_paged.h."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("n_rot", ctypes.c_int32), ("style", ctypes.c_int32)]
+
+
+class fa_qk_views(ctypes.Structure):
+    """struct fa_qk_views of fa_paged.h (element strides)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_row", "k_head")]
+
+
+class fa_kv_views(ctypes.Structure):
+    """struct fa_kv_views of fa_paged.h (element strides)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("k_row", "k_head", "v_row", "v_head")]
+
+
+class fa_paged_cache(ctypes.Structure):
+    """struct fa_paged_cache of fa_paged.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "page_table")] + [
+        (n, ctypes.c_int32) for n in ("k_type", "v_type", "num_pages", "page_size", "B", "max_pages", "Hkv", "D", "Dv")]
 
 
 class NativeLibraryMissing(RuntimeError):
@@ -86,6 +111,24 @@ def lib():
     L.fa_back_profile.argtypes = [i]
     L.fa_back_profile_read.restype = i
     L.fa_back_profile_read.argtypes = [vp, vp, vp, i]
+    P, i64 = ctypes.POINTER, ctypes.c_int64
+    L.fa_rope_frequencies.restype = i
+    L.fa_rope_frequencies.argtypes = [i, ctypes.c_double, ctypes.c_double, vp, vp]
+    L.fa_qk_norm_rope.restype = i
+    L.fa_qk_norm_rope.argtypes = [vp, vp, i, P(fa_qk_views), vp, vp, f, vp, P(fa_rope), i, i, i, i, vp, vp, i, vp]
+    L.fa_qk_norm_rope_backward_workspace_size.restype = sz
+    L.fa_qk_norm_rope_backward_workspace_size.argtypes = [i] * 4
+    L.fa_qk_norm_rope_backward.restype = i
+    L.fa_qk_norm_rope_backward.argtypes = [vp, vp, i, vp, vp, i, P(fa_qk_views), vp, vp, f, vp, P(fa_rope), i, i, i, i,
+                                           vp, vp, vp, vp, vp, sz, vp]
+    L.fa_cache_append.restype = i
+    L.fa_cache_append.argtypes = [vp, vp, i, P(fa_kv_views), P(fa_paged_cache), vp, vp, i, vp, f, P(fa_rope), vp]
+    L.fa_cache_read.restype = i
+    L.fa_cache_read.argtypes = [P(fa_paged_cache), vp, vp, i, i, vp, vp, vp]
+    L.fa_paged_decode_workspace_size.restype = sz
+    L.fa_paged_decode_workspace_size.argtypes = [P(fa_paged_cache), i]
+    L.fa_paged_decode.restype = i
+    L.fa_paged_decode.argtypes = [vp, i, i64, i64, P(fa_paged_cache), vp, i, f, vp, f, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -213,3 +256,47 @@ def fa_back_selftest_timeout(limit_ns: int, stream=None) -> int:
 def fa_back_test_wait_limit(limit_ns: int) -> int:
     """Failure-detection hook: the next call's kernels give up on waits longer than limit_ns."""
     return int(lib().fa_back_test_wait_limit(limit_ns))
+
+
+# ---- fa_paged.h: structures are passed by reference (None: a NULL pointer)
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def fa_rope_frequencies(n_rot: int, base: float, scale: float, factors, out) -> int:
+    """factors, out: host addresses (float32 and uint64 arrays of n_rot / 2) or None."""
+    return int(lib().fa_rope_frequencies(n_rot, base, scale, factors, out))
+
+
+def fa_qk_norm_rope(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, q_out, k_out, y_type, stream) -> int:
+    return lib().fa_qk_norm_rope(q, k, x_type, _ref(views), wq, wk, eps, pos, _ref(rope), N, H, Hkv, D, q_out, k_out,
+                                 y_type, stream)
+
+
+def fa_qk_norm_rope_backward_workspace_size(N: int, H: int, Hkv: int, D: int) -> int:
+    return lib().fa_qk_norm_rope_backward_workspace_size(N, H, Hkv, D)
+
+
+def fa_qk_norm_rope_backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, dq, dk, dwq,
+                             dwk, workspace, workspace_bytes, stream) -> int:
+    return lib().fa_qk_norm_rope_backward(gq, gk, y_type, q, k, x_type, _ref(views), wq, wk, eps, pos, _ref(rope), N, H,
+                                          Hkv, D, dq, dk, dwq, dwk, workspace, workspace_bytes, stream)
+
+
+def fa_cache_append(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, rope, stream) -> int:
+    return lib().fa_cache_append(k, v, x_type, _ref(views), _ref(cache), seq, pos, T, k_norm, eps, _ref(rope), stream)
+
+
+def fa_cache_read(cache, seq, pos, T, y_type, k_out, v_out, stream) -> int:
+    return lib().fa_cache_read(_ref(cache), seq, pos, T, y_type, k_out, v_out, stream)
+
+
+def fa_paged_decode_workspace_size(cache, H: int) -> int:
+    return lib().fa_paged_decode_workspace_size(_ref(cache), H)
+
+
+def fa_paged_decode(q, act, q_row, q_head, cache, seq_lens, H, scale, alibi_slopes, softcap, sinks, O, lse, workspace,
+                    workspace_bytes, stream) -> int:
+    return lib().fa_paged_decode(q, act, q_row, q_head, _ref(cache), seq_lens, H, scale, alibi_slopes, softcap, sinks, O,
+                                 lse, workspace, workspace_bytes, stream)

@@ -439,6 +439,14 @@ extern "C" fa_status fa_back_test_wait_limit(unsigned long long limit_ns) {
   return FA_OK;
 }
 
+extern "C" fa_status fab_device(int* nsm, int** err) {
+  int major = 0, minor = 0;
+  *nsm = device_sms(&major, &minor);
+  if (*nsm <= 0) return FA_ERR_CUDA;
+  if (major != 10 || minor != 3) return FA_ERR_DEVICE;
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(err), g_err) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 extern "C" fa_status fa_back_get_error(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
   int v = 0, zero = 0;
@@ -459,6 +467,7 @@ extern "C" const char* fa_back_status_string(int status) {
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
+    case FA_ERR_PAGE: return "invalid page, sequence or position of a paged cache";
   }
   return "unknown status";
 }

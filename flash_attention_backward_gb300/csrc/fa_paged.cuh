@@ -1,0 +1,177 @@
+// Device code shared by the paged-cache and the norm / rotation kernels: activation types, the
+// rotation of a head, page lookup and the host-side checks of a paged cache.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/fa_paged.h"
+#include "fa_internal.h"
+
+namespace fap {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------------------------------------
+// activations: eight consecutive elements of a row as f32.  One lane owns eight elements (16 bytes
+// of a 16-bit type, 32 of f32), so a head of D is held by D / 8 neighbouring lanes.
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <typename T>
+struct alignas(16) Oct {
+  T v[8];
+};
+
+// vec: p is 16-byte aligned (warp-uniform); otherwise element by element
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
+  if (vec) {
+    Oct<T> o;
+    constexpr int n = sizeof(Oct<T>) / 16;
+#pragma unroll
+    for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(&o)[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(o.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(p[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  Oct<T> o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o.v[i] = from_f32<T>(x[i]);
+  constexpr int n = sizeof(Oct<T>) / 16;
+#pragma unroll
+  for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&o)[i];
+}
+
+// ------------------------------------------------------------------------------------------------
+// rotation
+
+struct Rope {
+  const uint64_t* freqs;
+  int n_rot, style;
+};
+
+// Factors of a lane's eight elements e0 .. e0+7: y[i] = x[i] c[i] + partner[i] s[i], the sign of the
+// pair's first / second member in s.  The angle is pos * freq modulo 2^64 in units of 2^-64 turns:
+// the wrap of the integer product is the reduction modulo one turn, with no rounding, so the
+// error is that of the 32 bits kept (1.5e-9 rad) and of sincospi, at every position.
+struct Turn8 {
+  float c[8], s[8];
+  int lane_off;  // partner lane (FA_ROPE_HALVES), relative
+
+  __device__ __forceinline__ void set(const Rope& r, int pos, int e0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    lane_off = 0;
+    if (e0 >= r.n_rot) return;
+    const int half = r.n_rot >> 1;
+    if (r.style == FA_ROPE_HALVES) {  // n_rot % 16 == 0: a lane lies in one half
+      const bool second = e0 >= half;
+      const int p0 = second ? e0 - half : e0;
+      lane_off = second ? -(half >> 3) : half >> 3;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float sn;
+        angle(r.freqs[p0 + i], pos, sn, c[i]);
+        s[i] = second ? sn : -sn;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        if (e0 + i >= r.n_rot) break;  // n_rot is even, not always a multiple of 8
+        float sn, cs;
+        angle(r.freqs[(e0 + i) >> 1], pos, sn, cs);
+        c[i] = c[i + 1] = cs;
+        s[i] = -sn, s[i + 1] = sn;
+      }
+    }
+  }
+  static __device__ __forceinline__ void angle(uint64_t f, int pos, float& sn, float& cs) {
+    const uint64_t a = (uint64_t)(int64_t)pos * f;
+    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
+  }
+  // sign +1: rotate; -1: rotate back (the transpose).  All lanes of the warp take part.
+  __device__ __forceinline__ void apply(float (&x)[8], int style, float sign) const {
+    float p[8];
+    if (style == FA_ROPE_HALVES) {
+      const int src = (threadIdx.x & 31) + lane_off;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(kFull, x[i], src);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(p[i], sign * s[i], x[i] * c[i]);
+  }
+};
+
+// Sum over the LG lanes (a power of two) that hold one head.
+template <int LG>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// 1 / sqrt(v): the hardware approximation and one Newton step (it alone is off by up to two units,
+// and the whole head is scaled by it)
+__device__ __forceinline__ float inv_rms(float sum, float inv_n, float eps) {
+  const float v = fmaf(sum, inv_n, eps);
+  const float r = rsqrtf(v);
+  const float h = fmaf(-v * r, r, 1.f);
+  return (h == h) ? fmaf(0.5f * r, h, r) : r;  // v = 0 or inf: r is the limit itself
+}
+
+// ------------------------------------------------------------------------------------------------
+// paged cache
+
+struct Cache {
+  uint8_t* k;
+  uint8_t* v;
+  const int32_t* table;
+  int k_type, v_type, num_pages, page_size, B, max_pages, Hkv, D, Dv;
+  int rbk, rbv;  // bytes of a row
+  int* err;
+};
+
+// Row (page * page_size + offset) of position j of sequence b, or -1 (and FA_ERR_PAGE recorded)
+__device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
+  const int p = j / c.page_size;
+  if (b < c.B && p < c.max_pages) {
+    const int page = __ldg(c.table + (long long)b * c.max_pages + p);
+    if (page >= 0 && page < c.num_pages) return (long long)page * c.page_size + (j - p * c.page_size);
+  }
+  *c.err = FA_ERR_PAGE;
+  return -1;
+}
+
+// ---- host
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool head_size(int d) { return d == 64 || d == 128 || d == 256; }
+inline int act_bytes(int t) { return t == FA_ACT_F32 ? 4 : 2; }
+inline bool act_type(int t) { return t >= FA_ACT_F32 && t <= FA_ACT_BF16; }
+
+// The argument checks of a paged cache, and its device form but for `err`.
+fa_status check_cache(const fa_paged_cache* c, Cache* out);
+fa_status check_rope(const fa_rope* r, int D, const int32_t* pos, int N, Rope* out);
+
+}  // namespace fap

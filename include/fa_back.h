@@ -76,7 +76,8 @@ typedef enum {
   FA_ERR_DEVICE = 6,      /* the current device is not compute capability 10.3                  */
   FA_ERR_CUDA = 7,        /* a CUDA runtime call or kernel launch failed                        */
   FA_ERR_TIMEOUT = 8,     /* a kernel gave up on a bounded wait (see fa_back_get_error)         */
-  FA_ERR_WORKSPACE = 9    /* workspace is NULL or smaller than fa_back_workspace_size_min()     */
+  FA_ERR_WORKSPACE = 9,   /* workspace is NULL or smaller than fa_back_workspace_size_min()     */
+  FA_ERR_PAGE = 10        /* a paged-cache kernel met an invalid page, sequence or position     */
 } fa_status;
 
 /* Bytes in one cache row of `type` holding D values (-1 if D does not fit the format). */
@@ -260,8 +261,9 @@ fa_status fa_back_strided(const float* q, const void* k, int k_type, const void*
                           int Dv, int causal, float* dQ, float* dK, float* dV, float* lse, float* delta,
                           void* workspace, size_t workspace_bytes, void* stream);
 
-/* Sticky device-side status of the kernels enqueued so far on the current device
- * (FA_OK or FA_ERR_TIMEOUT).  Synchronises the device, then clears the word. */
+/* Sticky device-side status of the kernels enqueued so far on the current device (FA_OK,
+ * FA_ERR_TIMEOUT or, from the operators of fa_paged.h, FA_ERR_PAGE; the last recorded where there
+ * were several).  Synchronises the device, then clears the word. */
 fa_status fa_back_get_error(void);
 
 /* Human-readable name of a status code. */
