@@ -1,0 +1,802 @@
+// Single-token attention over a paged raw cache: the tile arithmetic.
+//
+// A warp takes 16 keys of one KV head at a time and up to eight query heads of its group.  Both
+// products run on the tensor core with keys (S^T = K Q^T) or value components (O^T += V^T P) as the
+// 16 rows and the query heads as the 8 columns, so a group of one to eight heads costs the same and
+// a cache row is decoded once for all of them.  One new token means 8 columns at most: a tcgen05
+// product has 128 rows of A in shared memory, so its operand would have to be decoded, scaled and
+// stored there first, where mma.sync takes the decoded codes from registers.
+//
+// Precision.  Codes are exact in binary16 (q8_0, q4_0 keys) and in bf16 (values), and block scales
+// are applied in f32, to the product (keys) or to the weight (values).  q is split into two binary16
+// parts (22 bits of the head's largest magnitude, after an exact power-of-two scale), a weight times
+// block scale into two bf16 parts (16 bits, with f32's range), a weight alone into two binary16
+// parts (22 bits), and for f32 rows all operands into two tf32 parts (three products).
+#pragma once
+#include "fa_paged.cuh"
+#include "sm100.cuh"
+
+namespace fap {
+
+using fab::lds_u16;
+using fab::lds_u32;
+using fab::lds_v4;
+using fab::smem_u32;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {  // a in the low half
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float lo_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
+__device__ __forceinline__ float hi_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Which component of a head each operand element is.  The order inside a product is free as long as
+// both operands agree, so it follows the words that a lane loads.  q8_0 and q4_0 blocks are 34 and
+// 18 bytes: only every other block starts on a word, so words are taken from pairs of blocks (17 and 9
+// words).  The first block's first and last half-word share one virtual word.
+
+// q8_0: component of byte c of virtual word i (0..7) of block parity odd
+__host__ __device__ __forceinline__ int q8_comp(bool odd, int i, int c) {
+  return odd ? 4 * i + c : i == 0 ? (c < 2 ? c : 28 + c) : 4 * i - 2 + c;
+}
+// q4_0: byte (0..15) at byte c of virtual word i (0..3)
+__host__ __device__ __forceinline__ int q4_byte(bool odd, int i, int c) {
+  return odd ? 4 * i + c : i == 0 ? (c < 2 ? c : 12 + c) : 4 * i - 2 + c;
+}
+
+// Component of element e (0, 1) of B register r (0, 1) that lane t = lane & 3 holds at k16 step ks
+__device__ __forceinline__ int k_comp16(int type, int ks, int t, int r, int e) {
+  if (type == FA_F16) return ks * 16 + 2 * t + 8 * r + e;
+  const int blk = ks >> 1, st = ks & 1;
+  const bool odd = blk & 1;
+  if (type == FA_Q8_0) return blk * 32 + q8_comp(odd, t + 4 * st, r + 2 * e);
+  return blk * 32 + q4_byte(odd, t, st + 2 * e) + 16 * r;
+}
+
+// Component of the output tile n (16 rows), row g + 8 half
+__device__ __forceinline__ int v_comp(int type, int n, int g, int half) {
+  if (type == FA_F16 || type == FA_F32) return 16 * n + g + 8 * half;
+  const int blk = n >> 1, T = n & 1;
+  if (type == FA_Q8_0) return blk * 32 + q8_comp(blk & 1, g, 2 * T + half);
+  return blk * 32 + 2 * g + T + 16 * half;
+}
+
+// ------------------------------------------------------------------------------------------------
+// scores: s[i] of keys g, g, g + 8, g + 8 and heads 2t, 2t + 1, 2t, 2t + 1 (the C fragment)
+
+template <int D>
+__device__ __forceinline__ void scores_f16(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+  const uint32_t at = tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * pitch + (lane >> 4) * 16;
+  float c2[4] = {};
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    uint32_t a0, a1, a2, a3;
+    ldsm4(at + ks * 32, a0, a1, a2, a3);
+    const uint4 b = lds_v4(qf + ks * 512);
+    mma_f16(s, a0, a1, a2, a3, b.x, b.y);
+    mma_f16(c2, a0, a1, a2, a3, b.z, b.w);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] += c2[i];
+}
+
+// the word's bytes 0, 2 and 1, 3 as binary16 pairs of signed codes: 1024 + (c + 128) - 1152
+__device__ __forceinline__ void q8_h2(uint32_t w, uint32_t& x0, uint32_t& x1) {
+  constexpr uint32_t kBias = 0x64806480u;  // 1152, 1152; xor with it sets the exponent and flips the sign bit
+  x0 = hsub2((w & 0x00ff00ffu) ^ kBias, kBias);
+  x1 = hsub2(((w >> 8) & 0x00ff00ffu) ^ kBias, kBias);
+}
+
+template <int D>
+__device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t r0 = tile + g * pitch, r1 = r0 + 8 * pitch;
+#pragma unroll
+  for (int pr = 0; pr < D / 64; ++pr) {
+    const uint32_t p0 = r0 + pr * 68, p1 = r1 + pr * 68;
+    const uint32_t h0 = lds_u32(p0), h1 = lds_u32(p1), m0 = lds_u32(p0 + 32), m1 = lds_u32(p1 + 32);
+    uint32_t u0 = lds_u32(p0 + 4 * t), u1 = lds_u32(p1 + 4 * t);
+    if (t == 0) u0 = __byte_perm(u0, m0, 0x5432), u1 = __byte_perm(u1, m1, 0x5432);
+    uint32_t a0, a1, a2, a3;
+    float c[4] = {};
+    uint4 b = lds_v4(qf + (pr * 4 + 0) * 512);
+    q8_h2(u0, a0, a2), q8_h2(u1, a1, a3);
+    mma_f16(c, a0, a1, a2, a3, b.x, b.y);
+    mma_f16(c, a0, a1, a2, a3, b.z, b.w);
+    b = lds_v4(qf + (pr * 4 + 1) * 512);
+    q8_h2(lds_u32(p0 + 16 + 4 * t), a0, a2), q8_h2(lds_u32(p1 + 16 + 4 * t), a1, a3);
+    mma_f16(c, a0, a1, a2, a3, b.x, b.y);
+    mma_f16(c, a0, a1, a2, a3, b.z, b.w);
+    float d0 = lo_h(h0), d1 = lo_h(h1);
+    s[0] = fmaf(d0, c[0], s[0]), s[1] = fmaf(d0, c[1], s[1]), s[2] = fmaf(d1, c[2], s[2]), s[3] = fmaf(d1, c[3], s[3]);
+    float e[4] = {};
+    b = lds_v4(qf + (pr * 4 + 2) * 512);
+    q8_h2(lds_u32(p0 + 36 + 4 * t), a0, a2), q8_h2(lds_u32(p1 + 36 + 4 * t), a1, a3);
+    mma_f16(e, a0, a1, a2, a3, b.x, b.y);
+    mma_f16(e, a0, a1, a2, a3, b.z, b.w);
+    b = lds_v4(qf + (pr * 4 + 3) * 512);
+    q8_h2(lds_u32(p0 + 52 + 4 * t), a0, a2), q8_h2(lds_u32(p1 + 52 + 4 * t), a1, a3);
+    mma_f16(e, a0, a1, a2, a3, b.x, b.y);
+    mma_f16(e, a0, a1, a2, a3, b.z, b.w);
+    d0 = hi_h(m0), d1 = hi_h(m1);
+    s[0] = fmaf(d0, e[0], s[0]), s[1] = fmaf(d0, e[1], s[1]), s[2] = fmaf(d1, e[2], s[2]), s[3] = fmaf(d1, e[3], s[3]);
+  }
+}
+
+// bytes 0, 2 of the word: low and high nibbles as binary16 pairs, minus 8
+__device__ __forceinline__ void q4_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  constexpr uint32_t kExp = 0x64006400u, kBias = 0x64086408u;  // 1024, 1032
+  lo = hsub2((w & 0x000f000fu) | kExp, kBias);
+  hi = hsub2(((w >> 4) & 0x000f000fu) | kExp, kBias);
+}
+
+template <int D>
+__device__ __forceinline__ void scores_q4(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t r0 = tile + g * pitch, r1 = r0 + 8 * pitch;
+#pragma unroll
+  for (int pr = 0; pr < D / 64; ++pr) {
+    const uint32_t p0 = r0 + pr * 36, p1 = r1 + pr * 36;
+    const uint32_t h0 = lds_u32(p0), h1 = lds_u32(p1), m0 = lds_u32(p0 + 16), m1 = lds_u32(p1 + 16);
+    uint32_t u0 = lds_u32(p0 + 4 * t), u1 = lds_u32(p1 + 4 * t);
+    if (t == 0) u0 = __byte_perm(u0, m0, 0x5432), u1 = __byte_perm(u1, m1, 0x5432);
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      uint32_t a0, a1, a2, a3;
+      float c[4] = {};
+      uint4 b = lds_v4(qf + (pr * 4 + 2 * o) * 512);
+      q4_h2(u0, a0, a2), q4_h2(u1, a1, a3);
+      mma_f16(c, a0, a1, a2, a3, b.x, b.y);
+      mma_f16(c, a0, a1, a2, a3, b.z, b.w);
+      b = lds_v4(qf + (pr * 4 + 2 * o + 1) * 512);
+      q4_h2(u0 >> 8, a0, a2), q4_h2(u1 >> 8, a1, a3);
+      mma_f16(c, a0, a1, a2, a3, b.x, b.y);
+      mma_f16(c, a0, a1, a2, a3, b.z, b.w);
+      const float d0 = o ? hi_h(m0) : lo_h(h0), d1 = o ? hi_h(m1) : lo_h(h1);
+      s[0] = fmaf(d0, c[0], s[0]), s[1] = fmaf(d0, c[1], s[1]), s[2] = fmaf(d1, c[2], s[2]), s[3] = fmaf(d1, c[3], s[3]);
+      if (o == 0) u0 = lds_u32(p0 + 20 + 4 * t), u1 = lds_u32(p1 + 20 + 4 * t);
+    }
+  }
+}
+
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  hi = x & 0xffffe000u;
+  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+}
+
+template <int D>
+__device__ __forceinline__ void scores_f32(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t r0 = tile + g * pitch + 4 * t, r1 = r0 + 8 * pitch;
+  float c2[4] = {}, c3[4] = {};
+#pragma unroll 8
+  for (int ks = 0; ks < D / 8; ++ks) {
+    uint32_t h[4], l[4];
+    split_tf32(lds_u32(r0 + ks * 32), h[0], l[0]);
+    split_tf32(lds_u32(r1 + ks * 32), h[1], l[1]);
+    split_tf32(lds_u32(r0 + ks * 32 + 16), h[2], l[2]);
+    split_tf32(lds_u32(r1 + ks * 32 + 16), h[3], l[3]);
+    const uint4 b = lds_v4(qf + ks * 512);
+    mma_tf32(s, h[0], h[1], h[2], h[3], b.x, b.y);
+    mma_tf32(c2, h[0], h[1], h[2], h[3], b.z, b.w);
+    mma_tf32(c3, l[0], l[1], l[2], l[3], b.x, b.y);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] += c2[i] + c3[i];
+}
+
+// C fragment (keys x heads) to weights' ownership: head g, keys 2t, 2t + 1, 2t + 8, 2t + 9.  Each f32 goes
+// through the 16-bit transposition as its two halves.
+__device__ __forceinline__ void transpose_scores(float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t a = __float_as_uint(s[i]), b = __float_as_uint(s[i + 1]);
+    const uint32_t lo = movm_t(__byte_perm(a, b, 0x5410)), hi = movm_t(__byte_perm(a, b, 0x7632));
+    s[i] = __uint_as_float(__byte_perm(lo, hi, 0x5410)), s[i + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// values: o[n] += V^T P for the DV / 16 tiles of 16 components; p: head g, keys 2t, 2t+1, 2t+8, 2t+9
+
+template <int DV>
+__device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+  const uint32_t at = tile + ((lane & 7) + (lane >> 4) * 8) * pitch + ((lane >> 3) & 1) * 16;
+  const uint32_t h0 = pack_h2(p[0], p[1]), h1 = pack_h2(p[2], p[3]);
+  const uint32_t l0 = pack_h2(p[0] - lo_h(h0), p[1] - hi_h(h0)), l1 = pack_h2(p[2] - lo_h(h1), p[3] - hi_h(h1));
+#pragma unroll
+  for (int n = 0; n < DV / 16; ++n) {
+    uint32_t a0, a1, a2, a3;
+    ldsm4_t(at + n * 32, a0, a1, a2, a3);
+    mma_f16(o[n], a0, a1, a2, a3, h0, h1);
+    mma_f16(o[n], a0, a1, a2, a3, l0, l1);
+  }
+}
+
+template <int DV>
+__device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t ph[4], pl[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_tf32(__float_as_uint(p[i]), ph[i], pl[i]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t r0 = tile + (8 * k + 2 * t) * pitch + 4 * g, r1 = r0 + pitch;
+#pragma unroll
+    for (int n = 0; n < DV / 16; ++n) {
+      uint32_t h[4], l[4];
+      split_tf32(lds_u32(r0 + n * 64), h[0], l[0]);
+      split_tf32(lds_u32(r0 + n * 64 + 32), h[1], l[1]);
+      split_tf32(lds_u32(r1 + n * 64), h[2], l[2]);
+      split_tf32(lds_u32(r1 + n * 64 + 32), h[3], l[3]);
+      mma_tf32(o[n], h[0], h[1], h[2], h[3], ph[2 * k], ph[2 * k + 1]);
+      mma_tf32(o[n], h[0], h[1], h[2], h[3], pl[2 * k], pl[2 * k + 1]);
+      mma_tf32(o[n], l[0], l[1], l[2], l[3], ph[2 * k], ph[2 * k + 1]);
+    }
+  }
+}
+
+// weights times block scales as two bf16 parts
+struct Scaled {
+  uint32_t h0, h1, l0, l1;
+  __device__ __forceinline__ Scaled(const float (&p)[4], float d0, float d1, float d2, float d3) {
+    const float x0 = p[0] * d0, x1 = p[1] * d1, x2 = p[2] * d2, x3 = p[3] * d3;
+    h0 = pack_b2(x0, x1), h1 = pack_b2(x2, x3);
+    l0 = pack_b2(x0 - __uint_as_float(h0 << 16), x1 - __uint_as_float(h0 & 0xffff0000u));
+    l1 = pack_b2(x2 - __uint_as_float(h1 << 16), x3 - __uint_as_float(h1 & 0xffff0000u));
+  }
+};
+
+// byte B of two keys' words as a bf16 pair of signed codes: (128 + low seven bits) - (128 or 256)
+template <int B>
+__device__ __forceinline__ uint32_t q8_b2(uint32_t k0, uint32_t k1) {
+  const uint32_t v = __byte_perm(k0, k1, B * 0x11 + (4 + B) * 0x1100);  // to bytes 0 and 2
+  return bsub2((v & 0x007f007fu) | 0x43004300u, (v & 0x00800080u) | 0x43004300u);
+}
+
+template <int DV>
+__device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t r[4] = {tile + (2 * t) * pitch, tile + (2 * t + 1) * pitch, tile + (2 * t + 8) * pitch,
+                         tile + (2 * t + 9) * pitch};
+#pragma unroll
+  for (int pr = 0; pr < DV / 64; ++pr) {
+    uint32_t w[4], x[4];
+    float d[4], e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = r[i] + pr * 68, h = lds_u32(at), m = lds_u32(at + 32);
+      w[i] = lds_u32(at + 4 * g);
+      if (g == 0) w[i] = __byte_perm(h, m, 0x5432);
+      x[i] = lds_u32(at + 36 + 4 * g);
+      d[i] = lo_h(h), e[i] = hi_h(m);
+    }
+    {
+      const Scaled b(p, d[0], d[1], d[2], d[3]);
+      const uint32_t a0 = q8_b2<0>(w[0], w[1]), a1 = q8_b2<1>(w[0], w[1]), a2 = q8_b2<0>(w[2], w[3]), a3 = q8_b2<1>(w[2], w[3]);
+      mma_bf16(o[4 * pr], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[4 * pr], a0, a1, a2, a3, b.l0, b.l1);
+      const uint32_t c0 = q8_b2<2>(w[0], w[1]), c1 = q8_b2<3>(w[0], w[1]), c2 = q8_b2<2>(w[2], w[3]), c3 = q8_b2<3>(w[2], w[3]);
+      mma_bf16(o[4 * pr + 1], c0, c1, c2, c3, b.h0, b.h1);
+      mma_bf16(o[4 * pr + 1], c0, c1, c2, c3, b.l0, b.l1);
+    }
+    {
+      const Scaled b(p, e[0], e[1], e[2], e[3]);
+      const uint32_t a0 = q8_b2<0>(x[0], x[1]), a1 = q8_b2<1>(x[0], x[1]), a2 = q8_b2<0>(x[2], x[3]), a3 = q8_b2<1>(x[2], x[3]);
+      mma_bf16(o[4 * pr + 2], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[4 * pr + 2], a0, a1, a2, a3, b.l0, b.l1);
+      const uint32_t c0 = q8_b2<2>(x[0], x[1]), c1 = q8_b2<3>(x[0], x[1]), c2 = q8_b2<2>(x[2], x[3]), c3 = q8_b2<3>(x[2], x[3]);
+      mma_bf16(o[4 * pr + 3], c0, c1, c2, c3, b.h0, b.h1);
+      mma_bf16(o[4 * pr + 3], c0, c1, c2, c3, b.l0, b.l1);
+    }
+  }
+}
+
+// nibble at bit SH of bytes 0 and 2 as a bf16 pair, minus 8
+template <int SH>
+__device__ __forceinline__ uint32_t q4_b2(uint32_t w) {
+  return bsub2(((w >> SH) & 0x000f000fu) | 0x43004300u, 0x43084308u);
+}
+
+template <int DV>
+__device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t r[4] = {tile + (2 * t) * pitch, tile + (2 * t + 1) * pitch, tile + (2 * t + 8) * pitch,
+                         tile + (2 * t + 9) * pitch};
+#pragma unroll
+  for (int blk = 0; blk < DV / 32; ++blk) {
+    uint32_t w[4];
+    float d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = lds_u16(r[i] + blk * 18 + 2 + 2 * g);  // components 2g, 2g + 1 and 2g + 16, 2g + 17
+      d[i] = lo_h(lds_u16(r[i] + blk * 18));
+    }
+    const Scaled b(p, d[0], d[1], d[2], d[3]);
+    const uint32_t u = w[0] | w[1] << 16, v = w[2] | w[3] << 16;
+    {
+      const uint32_t a0 = q4_b2<0>(u), a1 = q4_b2<4>(u), a2 = q4_b2<0>(v), a3 = q4_b2<4>(v);
+      mma_bf16(o[2 * blk], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[2 * blk], a0, a1, a2, a3, b.l0, b.l1);
+    }
+    {
+      const uint32_t a0 = q4_b2<8>(u), a1 = q4_b2<12>(u), a2 = q4_b2<8>(v), a3 = q4_b2<12>(v);
+      mma_bf16(o[2 * blk + 1], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[2 * blk + 1], a0, a1, a2, a3, b.l0, b.l1);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// the kernel
+
+constexpr int kUnit = 128;      // keys that a range of work is counted in
+constexpr int kMinUnits = 2;    // a range has at least this many units (where the work is that much)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLift = 7.f;    // weights are exp2(x - max + 7): the parts' small end moves out of the way
+constexpr float kRescale = 8.f; // the running maximum moves when a score exceeds it by this (weights <= 2^15)
+
+struct DecodeArgs {
+  Cache c;
+  const void* q;
+  int act;
+  long long q_row, q_head;
+  const int32_t* lens;
+  int H, G, HG, chunks;  // query heads, heads of a group, (KV head, chunk of 8 heads) pairs, chunks of a group
+  float scale, softcap;
+  const float *alibi, *sinks;
+  void* O;
+  float* lse;
+  float* part;  // [R][HG][2]: partial O [8][DV], then maxima [8] and sums [8]
+  int4* jobs;   // [R]: the sequence that range r begins and a later one ends: {b, last range, slot, 0}, or b = -1
+  int R;        // ranges of the grid
+  int pk, pv, slots;  // bytes of a key / value row in shared memory, slots of each ring
+  int csk, csv;       // bytes of one asynchronous copy
+};
+
+__device__ __forceinline__ float act_load(const void* p, int act, long long i) {
+  if (act == FA_ACT_F32) return static_cast<const float*>(p)[i];
+  if (act == FA_ACT_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void act_store(void* p, int act, long long i, float x) {
+  if (act == FA_ACT_F32) static_cast<float*>(p)[i] = x;
+  else if (act == FA_ACT_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+}
+
+// Keys of sequence b: its length, 0 for padding, at most the table's capacity
+__device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
+  const int L = __ldg(a.lens + b);
+  return min(max(L, 0), a.c.max_pages * a.c.page_size);
+}
+__device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
+
+__device__ __forceinline__ long long range_begin(long long r, long long U, int Re) { return r * U / Re; }
+__device__ __forceinline__ int range_of(long long u, long long U, int Re) { return (int)(((u + 1) * Re - 1) / U); }
+
+__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src, int size, bool on) {
+  const int n = on ? size : 0;  // the rest is filled with zeros
+  if (size == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else if (size == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest 2 slots - 1 groups have arrived
+__device__ __forceinline__ void cp_wait(int slots) {
+  if (slots == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (slots == 2) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (slots == 3) asm volatile("cp.async.wait_group 5;" ::: "memory");
+  else asm volatile("cp.async.wait_group 7;" ::: "memory");
+}
+
+template <int CS>
+__device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, const uint8_t* pool, int rb, int Hkv, int hk, int row,
+                                          int lane) {
+  const int per = rb / CS, n = 16 * per;
+  const uint32_t inv = (65536 + per - 1) / per;  // i / per for i < 16 per <= 4096
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const int k = min((int)(((uint32_t)i * inv) >> 16), 15);
+    const int src_row = __shfl_sync(kFull, row, k);
+    const int off = (i - k * per) * CS;
+    if (i < n)
+      cp_async(dst + k * pitch + off, pool + ((long long)max(src_row, 0) * Hkv + hk) * rb + off, CS, src_row >= 0);
+  }
+}
+
+// One range of keys (blockIdx.x / HG) of one (KV head, chunk of eight query heads) (blockIdx.x % HG).
+//
+// The work is the list of all sequences' keys in units of 128, cut into equal ranges whatever the
+// lengths are; consecutive CTAs take the same keys of the different heads, so a page's neighbouring
+// rows are read at the same time.  Within a range each warp takes every NW-th tile of 16 keys with a
+// ring, a running maximum and sums of its own: no barrier until the range or the sequence ends.
+template <int D, int DV, int NW>
+__global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_scan[NW];
+  __shared__ int s_seq, s_off;
+  __shared__ float s_qs[8], s_ml[NW][16];
+  __shared__ uint32_t s_valid[NW][4];
+  constexpr int QF = (D / 8) * 512;  // operand fragments of q: f32 keys take one per 8 components, others per 16
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int hg = blockIdx.x % a.HG, r = blockIdx.x / a.HG, hk = hg / a.chunks;
+  const int head0 = hk * a.G + (hg - hk * a.chunks) * 8, nh = min(8, a.G - (hg - hk * a.chunks) * 8);
+  const int B = a.c.B;
+  const uint32_t qf = smem_u32(smem), ring = qf + QF;
+
+  // ---- the range: U units in all, of which this CTA takes [u0, u1)
+  long long U = 0;
+  for (int c0 = 0; c0 < B; c0 += NW * 32) {
+    const int b = c0 + threadIdx.x;
+    int n = b < B ? units_of(seq_keys(a, b)) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
+    if (lane == 0) s_scan[warp] = n;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) U += s_scan[w];
+    __syncthreads();
+  }
+  // sequences without keys: their rows, by the CTA whose turn it is
+  for (int b = r + a.R * threadIdx.x; b < B; b += a.R * NW * 32) {
+    const int L = __ldg(a.lens + b);
+    if (L > a.c.max_pages * a.c.page_size && hg == 0) *a.c.err = FA_ERR_PAGE;
+    if (L < 0 || seq_keys(a, b) > 0) continue;
+    for (int h = head0; h < head0 + nh; ++h) {
+      const long long at = (long long)b * a.H + h;
+      for (int d = 0; d < DV; ++d) act_store(a.O, a.act, at * DV + d, 0.f);
+      if (a.lse) a.lse[at] = a.sinks ? a.sinks[h] : -INFINITY;
+    }
+  }
+  const int Re = (int)max(1LL, min((long long)a.R, U / kMinUnits));
+  const long long u0 = r < Re ? range_begin(r, U, Re) : 0, u1 = r < Re ? range_begin(r + 1, U, Re) : 0;
+  if (u0 >= u1) {
+    if (hg == 0 && threadIdx.x == 0) a.jobs[r] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  // the sequence that u0 lies in
+  long long base = 0;
+  for (int c0 = 0; c0 < B; c0 += NW * 32) {
+    const int b = c0 + threadIdx.x;
+    const int n = b < B ? units_of(seq_keys(a, b)) : 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    long long before = base + x - n;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += s_scan[w];
+      base += s_scan[w];
+    }
+    if (before <= u0 && u0 < before + n) s_seq = b, s_off = (int)(u0 - before);
+    __syncthreads();
+    if (base > u0) break;
+  }
+
+  const int slot_k = 16 * a.pk, slot_v = 16 * a.pv;
+  const uint32_t ring_k = ring + warp * a.slots * (slot_k + slot_v), ring_v = ring_k + a.slots * slot_k;
+  const float lnscale = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  int b = s_seq, off = s_off, seg = 0;
+  int4 job = make_int4(-1, 0, 0, 0);
+  for (long long u = u0; u < u1; ++seg) {
+    int keys = seq_keys(a, b);
+    while (keys == 0 && b + 1 < B) keys = seq_keys(a, ++b), off = 0;
+    if (keys == 0) break;  // (the lengths changed while the kernel ran)
+    const int nu = units_of(keys), take = (int)min((long long)(nu - off), u1 - u);
+    const int j0 = off * kUnit, j1 = min(keys, (off + take) * kUnit), ntile = (j1 - j0 + 15) >> 4;
+    const bool whole = take == nu;
+    const long long ub = u - off;  // the sequence's first unit
+    if (off == 0 && !whole) job = make_int4(b, range_of(ub + nu - 1, U, Re), seg == 0 ? 0 : 1, 0);
+
+    // ---- rows of a tile, one key a lane; page numbers are fetched a tile ahead of their copies
+    const int32_t* table = a.c.table + (long long)b * a.c.max_pages;
+    auto page_of = [&](int tile) {
+      const int j = j0 + tile * 16 + (lane & 15);
+      return tile < ntile && j < j1 ? __ldg(table + j / a.c.page_size) : -1;
+    };
+    auto row_of = [&](int tile, int page) {
+      const int j = j0 + tile * 16 + (lane & 15);
+      const bool in = tile < ntile && j < j1;
+      const bool ok = in && page >= 0 && page < a.c.num_pages;
+      if (in && !ok) *a.c.err = FA_ERR_PAGE;
+      return ok ? page * a.c.page_size + j % a.c.page_size : -1;
+    };
+    auto fetch_k = [&](int slot, int row, bool on) {
+      if (on) {
+        const uint32_t ok = __ballot_sync(kFull, row >= 0) & 0xffffu;
+        if (lane == 0) s_valid[warp][slot] = ok;
+        const uint32_t dst = ring_k + slot * slot_k;
+        if (a.csk == 16) copy_rows<16>(dst, a.pk, a.c.k, a.c.rbk, a.c.Hkv, hk, row, lane);
+        else if (a.csk == 8) copy_rows<8>(dst, a.pk, a.c.k, a.c.rbk, a.c.Hkv, hk, row, lane);
+        else copy_rows<4>(dst, a.pk, a.c.k, a.c.rbk, a.c.Hkv, hk, row, lane);
+      }
+      cp_commit();
+    };
+    auto fetch_v = [&](int slot, int row, bool on) {
+      if (on) {
+        const uint32_t dst = ring_v + slot * slot_v;
+        if (a.csv == 16) copy_rows<16>(dst, a.pv, a.c.v, a.c.rbv, a.c.Hkv, hk, row, lane);
+        else if (a.csv == 8) copy_rows<8>(dst, a.pv, a.c.v, a.c.rbv, a.c.Hkv, hk, row, lane);
+        else copy_rows<4>(dst, a.pv, a.c.v, a.c.rbv, a.c.Hkv, hk, row, lane);
+      }
+      cp_commit();
+    };
+    for (int s = 0; s < a.slots; ++s) {
+      const int tile = warp + s * NW, row = row_of(tile, page_of(tile));
+      fetch_k(s, row, tile < ntile);
+      fetch_v(s, row, tile < ntile);
+    }
+    int next = warp + a.slots * NW, page = page_of(next);
+
+    // ---- q of the chunk's heads: scaled by a power of two into range, split into parts
+    for (int h = warp; h < 8; h += NW) {
+      float m = 0.f;
+      const long long at = b * a.q_row + (head0 + h) * a.q_head;
+      if (h < nh)
+        for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(act_load(a.q, a.act, at + d)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      if (lane == 0) s_qs[h] = m > 0.f && m < INFINITY ? ldexpf(1.f, (a.c.k_type == FA_F32 ? 0 : 8) - ilogbf(m)) : 1.f;
+    }
+    __syncthreads();
+    {
+      const int steps = a.c.k_type == FA_F32 ? D / 8 : D / 16;
+      const long long at = b * a.q_row + (long long)(head0 + g) * a.q_head;
+      const float qs = s_qs[g];
+      for (int ks = warp; ks < steps; ks += NW) {
+        uint32_t w[4];
+        if (a.c.k_type == FA_F32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x = g < nh ? act_load(a.q, a.act, at + ks * 8 + t + 4 * i) * qs : 0.f;
+            split_tf32(__float_as_uint(x), w[i], w[2 + i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x = g < nh ? act_load(a.q, a.act, at + k_comp16(a.c.k_type, ks, t, i, 0)) * qs : 0.f;
+            const float y = g < nh ? act_load(a.q, a.act, at + k_comp16(a.c.k_type, ks, t, i, 1)) * qs : 0.f;
+            w[i] = pack_h2(x, y);
+            w[2 + i] = pack_h2(x - lo_h(w[i]), y - hi_h(w[i]));
+          }
+        }
+        fab::sts_v4(qf + ks * 512 + lane * 16, w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncthreads();
+    // ---- the warp's tiles
+    const float qscale = a.scale / s_qs[g];
+    const float slope = a.alibi && g < nh ? a.alibi[head0 + g] : 0.f;
+    float o[DV / 16][4];
+#pragma unroll
+    for (int n = 0; n < DV / 16; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+    float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
+    int slot = 0;
+    for (int tile = warp; tile < ntile; tile += NW, next += NW) {
+      const int row = row_of(next, page);
+      page = page_of(next + NW);
+      cp_wait(a.slots);
+      __syncwarp();
+      float s[4] = {};
+      const uint32_t tk = ring_k + slot * slot_k, tv = ring_v + slot * slot_v, qa = qf + lane * 16;
+      if (a.c.k_type == FA_Q8_0) scores_q8<D>(s, tk, a.pk, qa, lane);
+      else if (a.c.k_type == FA_F16) scores_f16<D>(s, tk, a.pk, qa, lane);
+      else if (a.c.k_type == FA_Q4_0) scores_q4<D>(s, tk, a.pk, qa, lane);
+      else scores_f32<D>(s, tk, a.pk, qa, lane);
+      transpose_scores(s);
+      const uint32_t ok = s_valid[warp][slot];
+      __syncwarp();
+      fetch_k(slot, row, next < ntile);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+        float x = s[i] * qscale;
+        if (a.softcap > 0.f) x = a.softcap * tanhf(x * lnscale);
+        if (a.alibi) x = fmaf(slope, (float)(j0 + tile * 16 + key - (keys - 1)), x);
+        s[i] = (ok >> key) & 1 ? x * kLog2e : -INFINITY;
+        mx = fmaxf(mx, s[i]);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+      const bool move = mx > m + kRescale || (m == -INFINITY && mx > m);
+      if (__any_sync(kFull, move)) {
+        const float f = move ? (m == -INFINITY ? 0.f : exp2f(m - mx)) : 1.f;
+        if (move) m = mx;
+        l *= f;
+        const float f0 = __shfl_sync(kFull, f, 8 * t), f1 = __shfl_sync(kFull, f, 8 * t + 4);
+#pragma unroll
+        for (int n = 0; n < DV / 16; ++n) o[n][0] *= f0, o[n][1] *= f1, o[n][2] *= f0, o[n][3] *= f1;
+      }
+      const float ref = m == -INFINITY ? 0.f : m - kLift;
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = exp2f(s[i] - ref), l += p[i];
+      cp_wait(a.slots);
+      __syncwarp();
+      if (a.c.v_type == FA_Q8_0) values_q8<DV>(o, p, tv, a.pv, lane);
+      else if (a.c.v_type == FA_F16) values_f16<DV>(o, p, tv, a.pv, lane);
+      else if (a.c.v_type == FA_Q4_0) values_q4<DV>(o, p, tv, a.pv, lane);
+      else values_f32<DV>(o, p, tv, a.pv, lane);
+      __syncwarp();
+      fetch_v(slot, row, next < ntile);
+      if (++slot == a.slots) slot = 0;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    if (t == 0) s_ml[warp][g] = m, s_ml[warp][8 + g] = l;
+    __syncthreads();  // the rings are free: they take the warps' sums
+    float* acc = reinterpret_cast<float*>(smem + QF);
+#pragma unroll
+    for (int n = 0; n < DV / 16; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[((warp * (DV / 16) + n) * 4 + i) * 32 + lane] = o[n][i];
+    // heads 2t, 2t + 1 of the columns that this lane joins
+    float M[2] = {-INFINITY, -INFINITY}, S[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      for (int w = 0; w < NW; ++w) M[i] = fmaxf(M[i], s_ml[w][2 * t + i]);
+      const float ref = M[i] == -INFINITY ? 0.f : M[i];
+      for (int w = 0; w < NW; ++w) S[i] += s_ml[w][8 + 2 * t + i] * exp2f(s_ml[w][2 * t + i] - ref);
+    }
+    __syncthreads();
+    float* part = a.part + ((long long)(r * a.HG + hg) * 2 + (seg == 0 ? 0 : 1)) * (8 * DV + 16);
+    float fin[2], lse[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float total = S[i], top = M[i], f = 1.f;
+      if (whole && a.sinks && 2 * t + i < nh) {  // one more term of the sum, without a value
+        const float sk = a.sinks[head0 + 2 * t + i] * kLog2e;
+        top = fmaxf(M[i], sk);
+        f = M[i] == -INFINITY ? 0.f : exp2f(M[i] - top);
+        total = S[i] * f + exp2f(sk - top + kLift);
+      }
+      fin[i] = whole ? (total > 0.f ? f / total : 0.f) : 1.f;
+      lse[i] = total > 0.f ? (top - kLift + log2f(total)) * kLn2 : -INFINITY;
+    }
+    for (int n = warp; n < DV / 16; n += NW) {
+      float x[4] = {};
+      for (int w = 0; w < NW; ++w) {
+        const float f0 = s_ml[w][2 * t] == -INFINITY ? 0.f : exp2f(s_ml[w][2 * t] - M[0]);
+        const float f1 = s_ml[w][2 * t + 1] == -INFINITY ? 0.f : exp2f(s_ml[w][2 * t + 1] - M[1]);
+        const float* p = acc + (w * (DV / 16) + n) * 128 + lane;
+        x[0] = fmaf(p[0], f0, x[0]), x[1] = fmaf(p[32], f1, x[1]), x[2] = fmaf(p[64], f0, x[2]), x[3] = fmaf(p[96], f1, x[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = 2 * t + (i & 1), d = v_comp(a.c.v_type, n, g, i >> 1);
+        if (h < nh) {
+          if (whole) act_store(a.O, a.act, ((long long)b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
+          else part[h * DV + d] = x[i];
+        }
+      }
+    }
+    if (warp == 0 && g == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = 2 * t + i;
+        if (h < nh && whole && a.lse) a.lse[(long long)b * a.H + head0 + h] = lse[i];
+        if (!whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
+      }
+    }
+    __syncthreads();
+    u += take, ++b, off = 0;
+  }
+  if (hg == 0 && threadIdx.x == 0) a.jobs[r] = job;
+}
+
+// Joins the partial sums of a sequence that several ranges took, in the ranges' order.  blockIdx.x: the
+// range that begins it, blockIdx.y: query head.
+template <int DV>
+__global__ void __launch_bounds__(256) k_decode_join(const DecodeArgs a) {
+  const int4 job = a.jobs[blockIdx.x];
+  if (job.x < 0) return;
+  const int h = blockIdx.y, hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
+  constexpr int GR = 256 / DV;  // 4, 2 or 1 groups of threads take parts in turn
+  const int d = threadIdx.x % DV, gr = threadIdx.x / DV, r0 = blockIdx.x, np = job.y - r0 + 1;
+  auto part = [&](int i) {
+    return a.part + ((long long)((r0 + i) * a.HG + hg) * 2 + (i == 0 ? job.z : 0)) * (8 * DV + 16);
+  };
+  float M = -INFINITY;
+  for (int i = 0; i < np; ++i) M = fmaxf(M, part(i)[8 * DV + c]);
+  float S = 0.f, x = 0.f, top = M;
+  if (a.sinks) top = fmaxf(M, a.sinks[h] * kLog2e);
+  const float ref = top == -INFINITY ? 0.f : top;
+  for (int i = 0; i < np; ++i) {
+    const float* p = part(i);
+    const float f = exp2f(p[8 * DV + c] - ref);
+    S = fmaf(p[8 * DV + 8 + c], f, S);
+    if (i % GR == gr) x = fmaf(p[c * DV + d], f, x);
+  }
+  if (a.sinks) S += exp2f(a.sinks[h] * kLog2e - ref + kLift);
+  __shared__ float red[256];
+  if (GR > 1) {
+    red[threadIdx.x] = x;
+    __syncthreads();
+    if (gr == 0)
+      for (int i = 1; i < GR; ++i) x += red[i * DV + d];
+  }
+  if (gr == 0) act_store(a.O, a.act, ((long long)job.x * a.H + h) * DV + d, S > 0.f ? x / S : 0.f);
+  if (threadIdx.x == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
+}
+
+cudaError_t run_decode_d64(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s);
+cudaError_t run_decode_d128(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s);
+cudaError_t run_decode_d256(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s);
+
+template <int D, int DV, int NW>
+cudaError_t run_decode(const DecodeArgs& a, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k_decode<D, DV, NW><<<a.R * a.HG, NW * 32, smem, s>>>(a);
+  if (a.R > 1) k_decode_join<DV><<<dim3(a.R, a.H), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t pick_decode(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s) {
+  switch (a.c.Dv) {
+    case 64: return nw == 8 ? run_decode<D, 64, 8>(a, smem, s) : run_decode<D, 64, 4>(a, smem, s);
+    case 128: return nw == 8 ? run_decode<D, 128, 8>(a, smem, s) : run_decode<D, 128, 4>(a, smem, s);
+  }
+  return nw == 8 ? run_decode<D, 256, 8>(a, smem, s) : run_decode<D, 256, 4>(a, smem, s);
+}
+
+}  // namespace fap

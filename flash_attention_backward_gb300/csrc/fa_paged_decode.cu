@@ -1,82 +1,45 @@
-// Attention of one new token per sequence over a paged raw cache (include/fa_paged.h).
+// Host side of fa_paged_decode(): checks, the plan and the launch (kernels: fa_decode.cuh).
 #include <algorithm>
 #include <cmath>
 
-#include "fa_paged.cuh"
+#include "fa_decode.cuh"
 
 namespace fap {
 
-struct DecodeArgs {
-  Cache c;
-  const void* q;
-  long long q_row, q_head;
-  const int32_t* lens;
-  int H, G;
-  float scale, softcap;
-  const float *alibi, *sinks;
-  void* O;
-  float* lse;
+// Rows in shared memory start 16 bytes (mod 128) after one another: the eight rows that a fragment
+// load touches then lie in different banks.
+static int smem_pitch(int rb) {
+  int p = (rb + 15) / 16 * 16;
+  while (p % 128 % 32 != 16) p += 16;
+  return p;
+}
+static int copy_size(int rb) { return rb % 16 == 0 ? 16 : rb % 8 == 0 ? 8 : 4; }
+
+struct DecodePlan {
+  int nw, slots, R, HG, chunks, pk, pv;
+  size_t smem, off_jobs, bytes;
 };
 
-__device__ __forceinline__ float cache_value(const uint8_t* row, int type, int e) {
-  if (type == FA_F32) return reinterpret_cast<const float*>(row)[e];
-  if (type == FA_F16) return __half2float(reinterpret_cast<const __half*>(row)[e]);
-  const uint8_t* blk = row + (e >> 5) * (type == FA_Q8_0 ? 34 : 18);
-  const float d = __half2float(*reinterpret_cast<const __half*>(blk));
-  e &= 31;
-  if (type == FA_Q8_0) return d * (float)(int8_t)blk[2 + e];
-  return d * (float)((int)((blk[2 + (e & 15)] >> (e < 16 ? 0 : 4)) & 15) - 8);
-}
-
-// One CTA per (sequence, query head); its warps take keys in turn, each with its own running
-// maximum and sum, joined at the end.
-template <typename T>
-__global__ void __launch_bounds__(256) k_decode_simple(const DecodeArgs a) {
-  const int b = blockIdx.y, h = blockIdx.x, hk = h / a.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int L = a.lens[b];
-  if (L < 0) return;
-  if (L > a.c.max_pages * a.c.page_size) {
-    L = a.c.max_pages * a.c.page_size;
-    *a.c.err = FA_ERR_PAGE;
-  }
-  const T* q = static_cast<const T*>(a.q) + b * a.q_row + h * a.q_head;
-  float qv[8], o[8] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) qv[i] = lane + 32 * i < a.c.D ? to_f32(q[lane + 32 * i]) : 0.f;
-  for (int j = warp; j < L; j += 8) {
-    const long long cell = cache_row(a.c, b, j);
-    if (cell < 0) continue;
-    const uint8_t* kr = a.c.k + (cell * a.c.Hkv + hk) * (long long)a.c.rbk;
-    const uint8_t* vr = a.c.v + (cell * a.c.Hkv + hk) * (long long)a.c.rbv;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < a.c.D) s = fmaf(qv[i], cache_value(kr, a.c.k_type, lane + 32 * i), s);
-    s = group_sum<32>(s) * a.scale;
-    if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-    if (a.alibi) s = fmaf(a.alibi[h], (float)(j - (L - 1)), s);
-    const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - mn), p = mn == -INFINITY ? 0.f : expf(s - mn);
-    l = l * f + p, m = mn;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < a.c.Dv) o[i] = fmaf(p, cache_value(vr, a.c.v_type, lane + 32 * i), o[i] * f);
-  }
-  __shared__ float sm[8], sl[8], so[8][256];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) so[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  float M = a.sinks ? a.sinks[h] : -INFINITY, S = 0.f, x = 0.f;
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-  const float Mf = M == -INFINITY ? 0.f : M;
-  if (a.sinks) S = expf(a.sinks[h] - Mf);
-  for (int w = 0; w < 8; ++w) {
-    const float f = expf(sm[w] - Mf);
-    S += sl[w] * f, x += so[w][threadIdx.x] * f;
-  }
-  if (threadIdx.x < a.c.Dv)
-    static_cast<T*>(a.O)[((long long)b * a.H + h) * a.c.Dv + threadIdx.x] = from_f32<T>(S > 0.f ? x / S : 0.f);
-  if (threadIdx.x == 0 && a.lse) a.lse[(long long)b * a.H + h] = Mf + logf(S);
+// One CTA an SM: eight warps with up to four slots of 16 keys each in what shared memory holds beside
+// q's fragments, or four warps where a tile of wide rows leaves no room for eight.
+static DecodePlan plan_decode(const Cache& c, int H, int nsm) {
+  DecodePlan p;
+  const int G = H / c.Hkv;
+  p.chunks = (G + 7) / 8;
+  p.HG = c.Hkv * p.chunks;
+  p.pk = smem_pitch(c.rbk), p.pv = smem_pitch(c.rbv);
+  const size_t qf = (size_t)(c.D / 8) * 512, room = 200 * 1024, stage = 16 * (size_t)(p.pk + p.pv);
+  p.nw = 8 * stage + qf <= room ? 8 : 4;
+  p.slots = (int)std::max<size_t>(1, std::min<size_t>(4, (room - qf) / (p.nw * stage)));
+  const size_t ring = p.nw * p.slots * stage, sums = (size_t)p.nw * c.Dv * 8 * sizeof(float);
+  p.smem = qf + std::max(ring, sums);
+  // ranges: what the SMs hold at a time, but no more than units of work can exist
+  const long long units = (long long)c.B * (((long long)c.max_pages * c.page_size + kUnit - 1) / kUnit);
+  long long R = std::max(1, nsm / p.HG);
+  p.R = (int)std::max(1LL, std::min(R, units / kMinUnits));
+  p.off_jobs = (size_t)p.R * p.HG * 2 * (8 * c.Dv + 16) * sizeof(float);
+  p.bytes = (p.off_jobs + p.R * sizeof(int4) + 255) / 256 * 256;
+  return p;
 }
 
 }  // namespace fap
@@ -86,7 +49,9 @@ using namespace fap;
 extern "C" size_t fa_paged_decode_workspace_size(const fa_paged_cache* cache, int H) {
   Cache c;
   if (check_cache(cache, &c) != FA_OK || H < 1 || H % c.Hkv) return 0;
-  return 256;
+  int nsm = 0, *err = nullptr;
+  if (fab_device(&nsm, &err) != FA_OK) nsm = 152;
+  return plan_decode(c, H, nsm).bytes;
 }
 
 extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,
@@ -99,22 +64,27 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
   if (!act_type(act)) return FA_ERR_TYPE;
   if (H < 1 || H % a.c.Hkv != 0 || q_row < 0 || q_head < 0) return FA_ERR_SHAPE;
   if (!(softcap >= 0.f) || !std::isfinite(softcap)) return FA_ERR_SHAPE;
-  if (H > 65535 || a.c.B > 65535) return FA_ERR_UNSUPPORTED;
+  if (H > 65535 || (long long)a.c.num_pages * a.c.page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (a.c.B > 0 && (!q || !O || !seq_lens)) return FA_ERR_NULL;
   if (!aligned(q, act_bytes(act)) || !aligned(O, 16) || !aligned(lse, 4) || !aligned(seq_lens, 4) ||
       !aligned(alibi_slopes, 4) || !aligned(sinks, 4))
     return FA_ERR_ALIGN;
   int nsm = 0;
   if ((rc = fab_device(&nsm, &a.c.err)) != FA_OK) return rc;
-  if (!workspace || workspace_bytes < fa_paged_decode_workspace_size(cache, H)) return FA_ERR_WORKSPACE;
+  const DecodePlan p = plan_decode(a.c, H, nsm);
+  if (!workspace || workspace_bytes < p.bytes) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
   if (a.c.B == 0) return FA_OK;
-  a.q = q, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens, a.H = H, a.G = H / a.c.Hkv;
+  a.q = q, a.act = act, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens;
+  a.H = H, a.G = H / a.c.Hkv, a.HG = p.HG, a.chunks = p.chunks;
   a.scale = scale, a.softcap = softcap, a.alibi = alibi_slopes, a.sinks = sinks, a.O = O, a.lse = lse;
-  const dim3 grid(H, a.c.B);
+  a.part = static_cast<float*>(workspace);
+  a.jobs = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_jobs);
+  a.R = p.R, a.pk = p.pk, a.pv = p.pv, a.slots = p.slots;
+  a.csk = copy_size(a.c.rbk), a.csv = copy_size(a.c.rbv);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (act == FA_ACT_F32) k_decode_simple<float><<<grid, 256, 0, s>>>(a);
-  else if (act == FA_ACT_F16) k_decode_simple<__half><<<grid, 256, 0, s>>>(a);
-  else k_decode_simple<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const cudaError_t e = a.c.D == 64    ? run_decode_d64(a, p.nw, p.smem, s)
+                        : a.c.D == 128 ? run_decode_d128(a, p.nw, p.smem, s)
+                                       : run_decode_d256(a, p.nw, p.smem, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
