@@ -439,6 +439,11 @@ extern "C" fa_status fa_back_test_wait_limit(unsigned long long limit_ns) {
   return FA_OK;
 }
 
+extern "C" unsigned long long fab_take_wait_ns(void) {
+  const unsigned long long hook = g_next_wait_ns.exchange(0);
+  return hook ? hook - 1 : kWaitLimitNs;
+}
+
 extern "C" fa_status fab_device(int* nsm, int** err) {
   int major = 0, minor = 0;
   *nsm = device_sms(&major, &minor);

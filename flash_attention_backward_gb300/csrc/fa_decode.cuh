@@ -44,6 +44,25 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the first product of a sum: C is zero
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (x & m) | v and (x & m) ^ v in one instruction (with two constants the compiler was seen to take two)
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t v) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(m), "r"(v));
+  return y;
+}
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t m, uint32_t v) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(x), "r"(m), "r"(v));
+  return y;
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
@@ -114,8 +133,8 @@ __device__ __forceinline__ int v_comp(int type, int n, int g, int half) {
 // scores: s[i] of keys g, g, g + 8, g + 8 and heads 2t, 2t + 1, 2t, 2t + 1 (the C fragment)
 
 template <int D>
-__device__ __forceinline__ void scores_f16(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
-  const uint32_t at = tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * pitch + (lane >> 4) * 16;
+__device__ __forceinline__ void scores_f16(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
+  const uint32_t at = rows[lane & 15] + (lane >> 4) * 16;
   float c2[4] = {};
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
@@ -132,14 +151,14 @@ __device__ __forceinline__ void scores_f16(float (&s)[4], uint32_t tile, int pit
 // the word's bytes 0, 2 and 1, 3 as binary16 pairs of signed codes: 1024 + (c + 128) - 1152
 __device__ __forceinline__ void q8_h2(uint32_t w, uint32_t& x0, uint32_t& x1) {
   constexpr uint32_t kBias = 0x64806480u;  // 1152, 1152; xor with it sets the exponent and flips the sign bit
-  x0 = hsub2((w & 0x00ff00ffu) ^ kBias, kBias);
-  x1 = hsub2(((w >> 8) & 0x00ff00ffu) ^ kBias, kBias);
+  x0 = hsub2(and_xor(w, 0x00ff00ffu, kBias), kBias);
+  x1 = hsub2(and_xor(w >> 8, 0x00ff00ffu, kBias), kBias);
 }
 
 template <int D>
-__device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+__device__ __forceinline__ void scores_q8(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = tile + g * pitch, r1 = r0 + 8 * pitch;
+  const uint32_t r0 = rows[g], r1 = rows[g + 8];
 #pragma unroll
   for (int pr = 0; pr < D / 64; ++pr) {
     const uint32_t p0 = r0 + pr * 68, p1 = r1 + pr * 68;
@@ -147,10 +166,10 @@ __device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t tile, int pitc
     uint32_t u0 = lds_u32(p0 + 4 * t), u1 = lds_u32(p1 + 4 * t);
     if (t == 0) u0 = __byte_perm(u0, m0, 0x5432), u1 = __byte_perm(u1, m1, 0x5432);
     uint32_t a0, a1, a2, a3;
-    float c[4] = {};
+    float c[4];
     uint4 b = lds_v4(qf + (pr * 4 + 0) * 512);
     q8_h2(u0, a0, a2), q8_h2(u1, a1, a3);
-    mma_f16(c, a0, a1, a2, a3, b.x, b.y);
+    mma_f16_first(c, a0, a1, a2, a3, b.x, b.y);
     mma_f16(c, a0, a1, a2, a3, b.z, b.w);
     b = lds_v4(qf + (pr * 4 + 1) * 512);
     q8_h2(lds_u32(p0 + 16 + 4 * t), a0, a2), q8_h2(lds_u32(p1 + 16 + 4 * t), a1, a3);
@@ -158,10 +177,10 @@ __device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t tile, int pitc
     mma_f16(c, a0, a1, a2, a3, b.z, b.w);
     float d0 = lo_h(h0), d1 = lo_h(h1);
     s[0] = fmaf(d0, c[0], s[0]), s[1] = fmaf(d0, c[1], s[1]), s[2] = fmaf(d1, c[2], s[2]), s[3] = fmaf(d1, c[3], s[3]);
-    float e[4] = {};
+    float e[4];
     b = lds_v4(qf + (pr * 4 + 2) * 512);
     q8_h2(lds_u32(p0 + 36 + 4 * t), a0, a2), q8_h2(lds_u32(p1 + 36 + 4 * t), a1, a3);
-    mma_f16(e, a0, a1, a2, a3, b.x, b.y);
+    mma_f16_first(e, a0, a1, a2, a3, b.x, b.y);
     mma_f16(e, a0, a1, a2, a3, b.z, b.w);
     b = lds_v4(qf + (pr * 4 + 3) * 512);
     q8_h2(lds_u32(p0 + 52 + 4 * t), a0, a2), q8_h2(lds_u32(p1 + 52 + 4 * t), a1, a3);
@@ -175,14 +194,14 @@ __device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t tile, int pitc
 // bytes 0, 2 of the word: low and high nibbles as binary16 pairs, minus 8
 __device__ __forceinline__ void q4_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   constexpr uint32_t kExp = 0x64006400u, kBias = 0x64086408u;  // 1024, 1032
-  lo = hsub2((w & 0x000f000fu) | kExp, kBias);
-  hi = hsub2(((w >> 4) & 0x000f000fu) | kExp, kBias);
+  lo = hsub2(and_or(w, 0x000f000fu, kExp), kBias);
+  hi = hsub2(and_or(w >> 4, 0x000f000fu, kExp), kBias);
 }
 
 template <int D>
-__device__ __forceinline__ void scores_q4(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+__device__ __forceinline__ void scores_q4(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = tile + g * pitch, r1 = r0 + 8 * pitch;
+  const uint32_t r0 = rows[g], r1 = rows[g + 8];
 #pragma unroll
   for (int pr = 0; pr < D / 64; ++pr) {
     const uint32_t p0 = r0 + pr * 36, p1 = r1 + pr * 36;
@@ -192,10 +211,10 @@ __device__ __forceinline__ void scores_q4(float (&s)[4], uint32_t tile, int pitc
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       uint32_t a0, a1, a2, a3;
-      float c[4] = {};
+      float c[4];
       uint4 b = lds_v4(qf + (pr * 4 + 2 * o) * 512);
       q4_h2(u0, a0, a2), q4_h2(u1, a1, a3);
-      mma_f16(c, a0, a1, a2, a3, b.x, b.y);
+      mma_f16_first(c, a0, a1, a2, a3, b.x, b.y);
       mma_f16(c, a0, a1, a2, a3, b.z, b.w);
       b = lds_v4(qf + (pr * 4 + 2 * o + 1) * 512);
       q4_h2(u0 >> 8, a0, a2), q4_h2(u1 >> 8, a1, a3);
@@ -214,9 +233,9 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& l
 }
 
 template <int D>
-__device__ __forceinline__ void scores_f32(float (&s)[4], uint32_t tile, int pitch, uint32_t qf, int lane) {
+__device__ __forceinline__ void scores_f32(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = tile + g * pitch + 4 * t, r1 = r0 + 8 * pitch;
+  const uint32_t r0 = rows[g] + 4 * t, r1 = rows[g + 8] + 4 * t;
   float c2[4] = {}, c3[4] = {};
 #pragma unroll 8
   for (int ks = 0; ks < D / 8; ++ks) {
@@ -249,8 +268,8 @@ __device__ __forceinline__ void transpose_scores(float (&s)[4]) {
 // values: o[n] += V^T P for the DV / 16 tiles of 16 components; p: head g, keys 2t, 2t+1, 2t+8, 2t+9
 
 template <int DV>
-__device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
-  const uint32_t at = tile + ((lane & 7) + (lane >> 4) * 8) * pitch + ((lane >> 3) & 1) * 16;
+__device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
+  const uint32_t at = rows[(lane & 7) + (lane >> 4) * 8] + ((lane >> 3) & 1) * 16;
   const uint32_t h0 = pack_h2(p[0], p[1]), h1 = pack_h2(p[2], p[3]);
   const uint32_t l0 = pack_h2(p[0] - lo_h(h0), p[1] - hi_h(h0)), l1 = pack_h2(p[2] - lo_h(h1), p[3] - hi_h(h1));
 #pragma unroll
@@ -263,14 +282,14 @@ __device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (
 }
 
 template <int DV>
-__device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+__device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
   uint32_t ph[4], pl[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) split_tf32(__float_as_uint(p[i]), ph[i], pl[i]);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t r0 = tile + (8 * k + 2 * t) * pitch + 4 * g, r1 = r0 + pitch;
+    const uint32_t r0 = rows[8 * k + 2 * t] + 4 * g, r1 = rows[8 * k + 2 * t + 1] + 4 * g;
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) {
       uint32_t h[4], l[4];
@@ -300,14 +319,13 @@ struct Scaled {
 template <int B>
 __device__ __forceinline__ uint32_t q8_b2(uint32_t k0, uint32_t k1) {
   const uint32_t v = __byte_perm(k0, k1, B * 0x11 + (4 + B) * 0x1100);  // to bytes 0 and 2
-  return bsub2((v & 0x007f007fu) | 0x43004300u, (v & 0x00800080u) | 0x43004300u);
+  return bsub2(and_or(v, 0x007f007fu, 0x43004300u), and_or(v, 0x00800080u, 0x43004300u));
 }
 
 template <int DV>
-__device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+__device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r[4] = {tile + (2 * t) * pitch, tile + (2 * t + 1) * pitch, tile + (2 * t + 8) * pitch,
-                         tile + (2 * t + 9) * pitch};
+  const uint32_t r[4] = {rows[2 * t], rows[2 * t + 1], rows[2 * t + 8], rows[2 * t + 9]};
 #pragma unroll
   for (int pr = 0; pr < DV / 64; ++pr) {
     uint32_t w[4], x[4];
@@ -344,14 +362,13 @@ __device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&
 // nibble at bit SH of bytes 0 and 2 as a bf16 pair, minus 8
 template <int SH>
 __device__ __forceinline__ uint32_t q4_b2(uint32_t w) {
-  return bsub2(((w >> SH) & 0x000f000fu) | 0x43004300u, 0x43084308u);
+  return bsub2(and_or(w >> SH, 0x000f000fu, 0x43004300u), 0x43084308u);
 }
 
 template <int DV>
-__device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&p)[4], uint32_t tile, int pitch, int lane) {
+__device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r[4] = {tile + (2 * t) * pitch, tile + (2 * t + 1) * pitch, tile + (2 * t + 8) * pitch,
-                         tile + (2 * t + 9) * pitch};
+  const uint32_t r[4] = {rows[2 * t], rows[2 * t + 1], rows[2 * t + 8], rows[2 * t + 9]};
 #pragma unroll
   for (int blk = 0; blk < DV / 32; ++blk) {
     uint32_t w[4];
@@ -379,6 +396,10 @@ __device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&
 // ------------------------------------------------------------------------------------------------
 // the kernel
 
+#ifndef FA_NW
+#define FA_NW 16
+#endif
+constexpr int kNW = FA_NW;
 constexpr int kUnit = 128;      // keys that a range of work is counted in
 constexpr int kMinUnits = 2;    // a range has at least this many units (where the work is that much)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -400,8 +421,13 @@ struct DecodeArgs {
   float* part;  // [R][HG][2]: partial O [8][DV], then maxima [8] and sums [8]
   int4* jobs;   // [R]: the sequence that range r begins and a later one ends: {b, last range, slot, 0}, or b = -1
   int R;        // ranges of the grid
-  int pk, pv, slots;  // bytes of a key / value row in shared memory, slots of each ring
-  int csk, csv;       // bytes of one asynchronous copy
+  int pk, pv, slots;  // bytes from one key / value row to the next in shared memory, slots of each ring
+  int tiled;          // 1: a tile's rows are one box of the tensor maps; 0: one bulk copy a row
+  int nbk, nbv;       // bytes of a row's bulk copy: it and what pads its ends to 16 bytes
+  int esk, esv;       // log2 of the tensor maps' element size
+  uint32_t page_mul;  // j / page_size = j * page_mul >> page_shift for j < 2^30
+  int page_shift;
+  uint64_t wait_ns;   // a wait for a copy gives up after this long (0, the failure-detection hook: at once)
 };
 
 __device__ __forceinline__ float act_load(const void* p, int act, long long i) {
@@ -425,35 +451,24 @@ __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / 
 __device__ __forceinline__ long long range_begin(long long r, long long U, int Re) { return r * U / Re; }
 __device__ __forceinline__ int range_of(long long u, long long U, int Re) { return (int)(((u + 1) * Re - 1) / U); }
 
-__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src, int size, bool on) {
-  const int n = on ? size : 0;  // the rest is filled with zeros
-  if (size == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else if (size == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the newest 2 slots - 1 groups have arrived
-__device__ __forceinline__ void cp_wait(int slots) {
-  if (slots == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (slots == 2) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (slots == 3) asm volatile("cp.async.wait_group 5;" ::: "memory");
-  else asm volatile("cp.async.wait_group 7;" ::: "memory");
+// Sixteen rows of one KV head by TMA: x (elements, a multiple of 16 bytes) is where the head's rows start
+// in a cell, y the first row of the pool.
+__device__ __forceinline__ void tile_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 
-template <int CS>
-__device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, const uint8_t* pool, int rb, int Hkv, int hk, int row,
-                                          int lane) {
-  const int per = rb / CS, n = 16 * per;
-  const uint32_t inv = (65536 + per - 1) / per;  // i / per for i < 16 per <= 4096
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane;
-    const int k = min((int)(((uint32_t)i * inv) >> 16), 15);
-    const int src_row = __shfl_sync(kFull, row, k);
-    const int off = (i - k * per) * CS;
-    if (i < n)
-      cp_async(dst + k * pitch + off, pool + ((long long)max(src_row, 0) * Hkv + hk) * rb + off, CS, src_row >= 0);
-  }
+// An untiled bulk copy of a cache row and the bytes up to the 16-byte boundaries around it: those lie
+// in the same page, whose size is a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_row(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
+
+constexpr uint64_t kDrainNs = 2000000000ull;
 
 // One range of keys (blockIdx.x / HG) of one (KV head, chunk of eight query heads) (blockIdx.x % HG).
 //
@@ -462,18 +477,25 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, const uint8_t
 // rows are read at the same time.  Within a range each warp takes every NW-th tile of 16 keys with a
 // ring, a running maximum and sums of its own: no barrier until the range or the sequence ends.
 template <int D, int DV, int NW>
-__global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
+__global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k,
+                                                        const __grid_constant__ CUtensorMap map_v) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_scan[NW];
   __shared__ int s_seq, s_off;
   __shared__ float s_qs[8], s_ml[NW][16];
-  __shared__ uint32_t s_valid[NW][4];
+  __shared__ uint64_t s_bar[NW][2][4];               // a slot's key rows, value rows have arrived
+  __shared__ uint32_t s_valid[NW][4];                // keys of the slot's tile
+  __shared__ uint32_t s_rows[NW][2][4][16];          // where the slot's rows start
+  __shared__ __align__(16) uint32_t s_zero[DV + 4];  // the value row of a key that is not there
   constexpr int QF = (D / 8) * 512;  // operand fragments of q: f32 keys take one per 8 components, others per 16
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hg = blockIdx.x % a.HG, r = blockIdx.x / a.HG, hk = hg / a.chunks;
   const int head0 = hk * a.G + (hg - hk * a.chunks) * 8, nh = min(8, a.G - (hg - hk * a.chunks) * 8);
   const int B = a.c.B;
   const uint32_t qf = smem_u32(smem), ring = qf + QF;
+  if (lane < 8) fab::mbar_init(&s_bar[warp][lane >> 2][lane & 3], 1);
+  for (int i = threadIdx.x; i < DV + 4; i += NW * 32) s_zero[i] = 0;
+  fab::fence_mbar_init();  // ordered before the first copy by the barriers below
 
   // ---- the range: U units in all, of which this CTA takes [u0, u1)
   long long U = 0;
@@ -531,57 +553,91 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
   const int slot_k = 16 * a.pk, slot_v = 16 * a.pv;
   const uint32_t ring_k = ring + warp * a.slots * (slot_k + slot_v), ring_v = ring_k + a.slots * slot_k;
   const float lnscale = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
-  int b = s_seq, off = s_off, seg = 0;
+  int b = s_seq, off = s_off, seg = 0, slot = 0;
+  uint32_t phases = 0, armed = 0;  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way
+  bool dead = false;    // a wait ran out: no more work is issued
   int4 job = make_int4(-1, 0, 0, 0);
+  __syncthreads();
   for (long long u = u0; u < u1; ++seg) {
     int keys = seq_keys(a, b);
     while (keys == 0 && b + 1 < B) keys = seq_keys(a, ++b), off = 0;
     if (keys == 0) break;  // (the lengths changed while the kernel ran)
     const int nu = units_of(keys), take = (int)min((long long)(nu - off), u1 - u);
-    const int j0 = off * kUnit, j1 = min(keys, (off + take) * kUnit), ntile = (j1 - j0 + 15) >> 4;
+    const int j0 = off * kUnit, j1 = min(keys, (off + take) * kUnit), ntile = dead ? 0 : (j1 - j0 + 15) >> 4;
     const bool whole = take == nu;
     const long long ub = u - off;  // the sequence's first unit
     if (off == 0 && !whole) job = make_int4(b, range_of(ub + nu - 1, U, Re), seg == 0 ? 0 : 1, 0);
 
-    // ---- rows of a tile, one key a lane; page numbers are fetched a tile ahead of their copies
+    // ---- rows of a tile.  Tiled copies (whole tiles in a page): the tile's first row, the same in every
+    // lane.  Otherwise one key a lane, lanes 16 .. 31 as 0 .. 15.  Page numbers are fetched a tile ahead of
+    // the copies that they are for.
     const int32_t* table = a.c.table + (long long)b * a.c.max_pages;
-    auto page_of = [&](int tile) {
-      const int j = j0 + tile * 16 + (lane & 15);
-      return tile < ntile && j < j1 ? __ldg(table + j / a.c.page_size) : -1;
+    struct Where {
+      int page, off;
     };
-    auto row_of = [&](int tile, int page) {
-      const int j = j0 + tile * 16 + (lane & 15);
-      const bool in = tile < ntile && j < j1;
-      const bool ok = in && page >= 0 && page < a.c.num_pages;
-      if (in && !ok) *a.c.err = FA_ERR_PAGE;
-      return ok ? page * a.c.page_size + j % a.c.page_size : -1;
-    };
-    auto fetch_k = [&](int slot, int row, bool on) {
-      if (on) {
-        const uint32_t ok = __ballot_sync(kFull, row >= 0) & 0xffffu;
-        if (lane == 0) s_valid[warp][slot] = ok;
-        const uint32_t dst = ring_k + slot * slot_k;
-        if (a.csk == 16) copy_rows<16>(dst, a.pk, a.c.k, a.c.rbk, a.c.Hkv, hk, row, lane);
-        else if (a.csk == 8) copy_rows<8>(dst, a.pk, a.c.k, a.c.rbk, a.c.Hkv, hk, row, lane);
-        else copy_rows<4>(dst, a.pk, a.c.k, a.c.rbk, a.c.Hkv, hk, row, lane);
+    const int key_lane = a.tiled ? 0 : lane & 15;
+    auto where = [&](int tile) {
+      const int j = j0 + tile * 16 + key_lane;
+      Where w = {-1, 0};
+      if (tile < ntile && j < j1) {
+        const int p = (int)((uint64_t)j * a.page_mul >> a.page_shift);
+        w.page = __ldg(table + p), w.off = j - p * a.c.page_size;
+        if (w.page < 0) w.page = 0x7fffffff;
       }
-      cp_commit();
+      return w;
     };
-    auto fetch_v = [&](int slot, int row, bool on) {
-      if (on) {
-        const uint32_t dst = ring_v + slot * slot_v;
-        if (a.csv == 16) copy_rows<16>(dst, a.pv, a.c.v, a.c.rbv, a.c.Hkv, hk, row, lane);
-        else if (a.csv == 8) copy_rows<8>(dst, a.pv, a.c.v, a.c.rbv, a.c.Hkv, hk, row, lane);
-        else copy_rows<4>(dst, a.pv, a.c.v, a.c.rbv, a.c.Hkv, hk, row, lane);
+    auto row_of = [&](const Where& w) {
+      const bool ok = w.page >= 0 && w.page < a.c.num_pages;
+      if (w.page >= 0 && !ok) *a.c.err = FA_ERR_PAGE;
+      return ok ? w.page * a.c.page_size + w.off : -1;
+    };
+    auto fetch = [&](int kv, int slot, int row, int tile) {
+      uint64_t* bar = &s_bar[warp][kv][slot];
+      const int rb = kv ? a.c.rbv : a.c.rbk, pitch = kv ? a.pv : a.pk;
+      const uint32_t dst = kv ? ring_v + slot * slot_v : ring_k + slot * slot_k;
+      armed |= 1u << (4 * kv + slot);
+      if (a.tiled) {
+        const int n = row >= 0 ? min(16, j1 - (j0 + tile * 16)) : 0;  // the rows behind them are not used
+        if (lane == 0) {
+          if (kv == 0) s_valid[warp][slot] = (1u << n) - 1;
+          fab::mbar_arrive_expect_tx(bar, n ? 16 * pitch : 0);
+          if (n) tile_rows(dst, kv ? &map_v : &map_k, (hk * rb & ~15) >> (kv ? a.esv : a.esk), row, smem_u32(bar));
+        }
+        if (lane < 16)
+          s_rows[warp][kv][slot][lane] = kv && lane >= n ? smem_u32(s_zero) : dst + lane * pitch + (hk * rb & 15);
+        return;
       }
-      cp_commit();
+      const uint32_t ok = __ballot_sync(kFull, row >= 0) & 0xffffu;
+      const int nb = kv ? a.nbv : a.nbk;
+      if (lane == 0) {
+        if (kv == 0) s_valid[warp][slot] = ok;
+        fab::mbar_arrive_expect_tx(bar, __popc(ok) * nb);
+      }
+      __syncwarp();
+      if (lane < 16) {
+        const long long at = ((long long)max(row, 0) * a.c.Hkv + hk) * rb;
+        s_rows[warp][kv][slot][lane] = kv && row < 0 ? smem_u32(s_zero) : dst + lane * pitch + ((uint32_t)at & 15);
+        if (row >= 0) bulk_row(dst + lane * pitch, (kv ? a.c.v : a.c.k) + (at & ~15LL), nb, smem_u32(bar));
+      }
     };
-    for (int s = 0; s < a.slots; ++s) {
-      const int tile = warp + s * NW, row = row_of(tile, page_of(tile));
-      fetch_k(s, row, tile < ntile);
-      fetch_v(s, row, tile < ntile);
+    for (int i = 0, sl = slot; i < a.slots; ++i) {
+      const int tile = warp + i * NW;
+      if (tile < ntile) {
+        const int row = row_of(where(tile));
+        fetch(0, sl, row, tile), fetch(1, sl, row, tile);
+      }
+      if (++sl == a.slots) sl = 0;
     }
-    int next = warp + a.slots * NW, page = page_of(next);
+    // the slot's copies have arrived (all lanes agree)
+    auto arrived = [&](int kv, int slot) {
+      const uint32_t bit = 1u << (4 * kv + slot);
+      const bool came = a.wait_ns > 0 && fab::mbar_wait_bounded(&s_bar[warp][kv][slot], (phases & bit) != 0, a.wait_ns);
+      if (!__all_sync(kFull, came)) return false;
+      phases ^= bit, armed &= ~bit;
+      return true;
+    };
+    int next = warp + a.slots * NW;
+    Where ahead = where(next);
 
     // ---- q of the chunk's heads: scaled by a power of two into range, split into parts
     for (int h = warp; h < 8; h += NW) {
@@ -628,22 +684,22 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
-    int slot = 0;
     for (int tile = warp; tile < ntile; tile += NW, next += NW) {
-      const int row = row_of(next, page);
-      page = page_of(next + NW);
-      cp_wait(a.slots);
-      __syncwarp();
+      const int row = row_of(ahead);
+      ahead = where(next + NW);
+      dead = !arrived(0, slot);
+      if (dead) break;
       float s[4] = {};
-      const uint32_t tk = ring_k + slot * slot_k, tv = ring_v + slot * slot_v, qa = qf + lane * 16;
-      if (a.c.k_type == FA_Q8_0) scores_q8<D>(s, tk, a.pk, qa, lane);
-      else if (a.c.k_type == FA_F16) scores_f16<D>(s, tk, a.pk, qa, lane);
-      else if (a.c.k_type == FA_Q4_0) scores_q4<D>(s, tk, a.pk, qa, lane);
-      else scores_f32<D>(s, tk, a.pk, qa, lane);
+      const uint32_t* kr = s_rows[warp][0][slot];
+      const uint32_t qa = qf + lane * 16;
+      if (a.c.k_type == FA_Q8_0) scores_q8<D>(s, kr, qa, lane);
+      else if (a.c.k_type == FA_F16) scores_f16<D>(s, kr, qa, lane);
+      else if (a.c.k_type == FA_Q4_0) scores_q4<D>(s, kr, qa, lane);
+      else scores_f32<D>(s, kr, qa, lane);
       transpose_scores(s);
       const uint32_t ok = s_valid[warp][slot];
       __syncwarp();
-      fetch_k(slot, row, next < ntile);
+      if (next < ntile) fetch(0, slot, row, next);
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -658,7 +714,7 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
       const bool move = mx > m + kRescale || (m == -INFINITY && mx > m);
       if (__any_sync(kFull, move)) {
-        const float f = move ? (m == -INFINITY ? 0.f : exp2f(m - mx)) : 1.f;
+        const float f = move ? (m == -INFINITY ? 0.f : fab::ex2(m - mx)) : 1.f;
         if (move) m = mx;
         l *= f;
         const float f0 = __shfl_sync(kFull, f, 8 * t), f1 = __shfl_sync(kFull, f, 8 * t + 4);
@@ -668,18 +724,26 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
       const float ref = m == -INFINITY ? 0.f : m - kLift;
       float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = exp2f(s[i] - ref), l += p[i];
-      cp_wait(a.slots);
+      for (int i = 0; i < 4; ++i) p[i] = fab::ex2(s[i] - ref), l += p[i];
+      dead = !arrived(1, slot);
+      if (dead) break;
+      const uint32_t* vr = s_rows[warp][1][slot];
+      if (a.c.v_type == FA_Q8_0) values_q8<DV>(o, p, vr, lane);
+      else if (a.c.v_type == FA_F16) values_f16<DV>(o, p, vr, lane);
+      else if (a.c.v_type == FA_Q4_0) values_q4<DV>(o, p, vr, lane);
+      else values_f32<DV>(o, p, vr, lane);
       __syncwarp();
-      if (a.c.v_type == FA_Q8_0) values_q8<DV>(o, p, tv, a.pv, lane);
-      else if (a.c.v_type == FA_F16) values_f16<DV>(o, p, tv, a.pv, lane);
-      else if (a.c.v_type == FA_Q4_0) values_q4<DV>(o, p, tv, a.pv, lane);
-      else values_f32<DV>(o, p, tv, a.pv, lane);
-      __syncwarp();
-      fetch_v(slot, row, next < ntile);
+      if (next < ntile) fetch(1, slot, row, next);
       if (++slot == a.slots) slot = 0;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (dead && ntile > 0) {  // let the copies in flight land before their memory gets another use
+      if (lane == 0) {
+        atomicExch(a.c.err, FA_ERR_TIMEOUT);
+        for (int i = 0; i < 8; ++i)
+          if ((armed >> i) & 1) fab::mbar_wait_bounded(&s_bar[warp][i >> 2][i & 3], (phases >> i) & 1, kDrainNs);
+      }
+      __syncwarp();
+    }
     l += __shfl_xor_sync(kFull, l, 1);
     l += __shfl_xor_sync(kFull, l, 2);
     if (t == 0) s_ml[warp][g] = m, s_ml[warp][8 + g] = l;
@@ -737,6 +801,7 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a) {
         if (!whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
       }
     }
+    fab::fence_proxy_async_smem();  // the sums' memory takes copies again
     __syncthreads();
     u += take, ++b, off = 0;
   }
@@ -778,25 +843,28 @@ __global__ void __launch_bounds__(256) k_decode_join(const DecodeArgs a) {
   if (threadIdx.x == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
 }
 
-cudaError_t run_decode_d64(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s);
-cudaError_t run_decode_d128(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s);
-cudaError_t run_decode_d256(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s);
+struct DecodeMaps {
+  CUtensorMap k, v;
+};
+cudaError_t run_decode_d64(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s);
+cudaError_t run_decode_d128(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s);
+cudaError_t run_decode_d256(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s);
 
 template <int D, int DV, int NW>
-cudaError_t run_decode(const DecodeArgs& a, size_t smem, cudaStream_t s) {
+cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, size_t smem, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_decode<D, DV, NW><<<a.R * a.HG, NW * 32, smem, s>>>(a);
+  k_decode<D, DV, NW><<<a.R * a.HG, NW * 32, smem, s>>>(a, m.k, m.v);
   if (a.R > 1) k_decode_join<DV><<<dim3(a.R, a.H), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <int D>
-cudaError_t pick_decode(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s) {
+cudaError_t pick_decode(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s) {
   switch (a.c.Dv) {
-    case 64: return nw == 8 ? run_decode<D, 64, 8>(a, smem, s) : run_decode<D, 64, 4>(a, smem, s);
-    case 128: return nw == 8 ? run_decode<D, 128, 8>(a, smem, s) : run_decode<D, 128, 4>(a, smem, s);
+    case 64: return nw == kNW ? run_decode<D, 64, kNW>(a, m, smem, s) : run_decode<D, 64, 4>(a, m, smem, s);
+    case 128: return nw == kNW ? run_decode<D, 128, kNW>(a, m, smem, s) : run_decode<D, 128, 4>(a, m, smem, s);
   }
-  return nw == 8 ? run_decode<D, 256, 8>(a, smem, s) : run_decode<D, 256, 4>(a, smem, s);
+  return nw == kNW ? run_decode<D, 256, kNW>(a, m, smem, s) : run_decode<D, 256, 4>(a, m, smem, s);
 }
 
 }  // namespace fap

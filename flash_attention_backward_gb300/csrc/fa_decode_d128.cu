@@ -3,7 +3,7 @@
 #include "fa_decode.cuh"
 
 namespace fap {
-cudaError_t run_decode_d128(const DecodeArgs& a, int nw, size_t smem, cudaStream_t s) {
-  return pick_decode<128>(a, nw, smem, s);
+cudaError_t run_decode_d128(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s) {
+  return pick_decode<128>(a, m, nw, smem, s);
 }
 }  // namespace fap

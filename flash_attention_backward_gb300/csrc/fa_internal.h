@@ -39,6 +39,10 @@ __attribute__((visibility("hidden"))) fa_status fab_back_capped(
 // the entry points report them.
 __attribute__((visibility("hidden"))) fa_status fab_device(int* nsm, int** err);
 
+// The wait limit of a call's kernels in nanoseconds: the normal one, or the pending limit of
+// fa_back_test_wait_limit(), which this call takes.
+__attribute__((visibility("hidden"))) unsigned long long fab_take_wait_ns(void);
+
 #ifdef __cplusplus
 }
 #endif

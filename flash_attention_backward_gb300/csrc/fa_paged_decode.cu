@@ -1,6 +1,9 @@
 // Host side of fa_paged_decode(): checks, the plan and the launch (kernels: fa_decode.cuh).
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "fa_decode.cuh"
 
@@ -13,7 +16,31 @@ static int smem_pitch(int rb) {
   while (p % 128 % 32 != 16) p += 16;
   return p;
 }
-static int copy_size(int rb) { return rb % 16 == 0 ? 16 : rb % 8 == 0 ? 8 : 4; }
+static int copy_bytes(int rb) { return (rb + 15) / 16 * 16; }
+
+// The pool as a matrix of cells [rows][Hkv * rb bytes], read in boxes of 16 rows x `pitch` bytes: the row,
+// what lies before it back to a 16-byte boundary, and padding that spaces the rows in shared memory.
+// Elements are as wide as keeps a box within 256 of them.
+static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, int rb, int pitch, int* es_log2) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  if (!fn) return false;
+  const int lg = pitch <= 512 ? 1 : pitch <= 1024 ? 2 : 3;
+  *es_log2 = lg;
+  const cuuint64_t dims[2] = {(cuuint64_t)Hkv * rb >> lg, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)Hkv * rb};
+  const cuuint32_t box[2] = {(cuuint32_t)(pitch >> lg), 16}, es[2] = {1, 1};
+  return fn(m, lg == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : lg == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT64,
+            2, const_cast<void*>(pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 struct DecodePlan {
   int nw, slots, R, HG, chunks, pk, pv;
@@ -27,9 +54,9 @@ static DecodePlan plan_decode(const Cache& c, int H, int nsm) {
   const int G = H / c.Hkv;
   p.chunks = (G + 7) / 8;
   p.HG = c.Hkv * p.chunks;
-  p.pk = smem_pitch(c.rbk), p.pv = smem_pitch(c.rbv);
+  p.pk = smem_pitch(copy_bytes(c.rbk)), p.pv = smem_pitch(copy_bytes(c.rbv));
   const size_t qf = (size_t)(c.D / 8) * 512, room = 200 * 1024, stage = 16 * (size_t)(p.pk + p.pv);
-  p.nw = 8 * stage + qf <= room ? 8 : 4;
+  p.nw = kNW * stage + qf <= room ? kNW : 4;
   p.slots = (int)std::max<size_t>(1, std::min<size_t>(4, (room - qf) / (p.nw * stage)));
   const size_t ring = p.nw * p.slots * stage, sums = (size_t)p.nw * c.Dv * 8 * sizeof(float);
   p.smem = qf + std::max(ring, sums);
@@ -81,10 +108,22 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
   a.part = static_cast<float*>(workspace);
   a.jobs = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_jobs);
   a.R = p.R, a.pk = p.pk, a.pv = p.pv, a.slots = p.slots;
-  a.csk = copy_size(a.c.rbk), a.csv = copy_size(a.c.rbv);
+  a.nbk = copy_bytes(a.c.rbk), a.nbv = copy_bytes(a.c.rbv);
+  int lg = 0;
+  while ((1LL << lg) < a.c.page_size) ++lg;
+  a.page_shift = 30 + lg;
+  a.page_mul = (uint32_t)(((1ULL << a.page_shift) + a.c.page_size - 1) / a.c.page_size);
+  a.wait_ns = fab_take_wait_ns();
+  // tiled copies where a tile of 16 keys never spans pages and cells are spaced by multiples of 16 bytes
+  DecodeMaps m = {};
+  const long long rows = (long long)a.c.num_pages * a.c.page_size;
+  a.tiled = a.c.page_size % 16 == 0 && (a.c.Hkv * a.c.rbk) % 16 == 0 && (a.c.Hkv * a.c.rbv) % 16 == 0 && rows > 0;
+  if (a.tiled && (!map_pool(&m.k, a.c.k, rows, a.c.Hkv, a.c.rbk, p.pk, &a.esk) ||
+                  !map_pool(&m.v, a.c.v, rows, a.c.Hkv, a.c.rbv, p.pv, &a.esv)))
+    return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a.c.D == 64    ? run_decode_d64(a, p.nw, p.smem, s)
-                        : a.c.D == 128 ? run_decode_d128(a, p.nw, p.smem, s)
-                                       : run_decode_d256(a, p.nw, p.smem, s);
+  const cudaError_t e = a.c.D == 64    ? run_decode_d64(a, m, p.nw, p.smem, s)
+                        : a.c.D == 128 ? run_decode_d128(a, m, p.nw, p.smem, s)
+                                       : run_decode_d256(a, m, p.nw, p.smem, s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

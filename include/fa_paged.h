@@ -158,6 +158,9 @@ fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* seq, const i
  * same type and lse [B][H] f32 (NULL: not wanted) are contiguous.  H % Hkv == 0.  Alignment: q to
  * its element, O 16 bytes, lse, seq_lens, alibi_slopes, sinks 4 bytes, workspace 256 bytes.
  * The workspace holds the split partials; its size does not depend on the lengths.
+ * The kernel's waits for its own copies are bounded: one that runs out is reported as FA_ERR_TIMEOUT
+ * by fa_back_get_error() and leaves the outputs undefined.  fa_back_test_wait_limit() applies to the
+ * next call here too; a limit of 0 counts every wait as run out.
  */
 size_t fa_paged_decode_workspace_size(const fa_paged_cache* cache, int H);
 fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,

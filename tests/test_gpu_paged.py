@@ -451,6 +451,18 @@ def test_decode_equal_calls_and_streams(fb):
     assert torch.equal(c["O"], out["O"])
 
 
+def test_decode_gives_up_on_a_wait(fb):
+    """With a wait limit of zero the kernel records a timeout, drains its copies and returns; the next call
+    is right again."""
+    p = R.Paged(8, [3000, 500, 1000], 2, 256, 256, Q8, Q8, 64)
+    q, cache, out = check_decode(fb, p, 8)
+    assert fb.fa_back_test_wait_limit(0) == 0
+    fb.paged_decode(q, cache, cuda(np.array(p.lens, np.int32)), scale=256 ** -0.5)
+    assert fb.STATUS[fb.fa_back_get_error()] == "FA_ERR_TIMEOUT"
+    again = fb.paged_decode(q, cache, cuda(np.array(p.lens, np.int32)), scale=256 ** -0.5)
+    assert torch.equal(again["O"], out["O"]) and fb.fa_back_get_error() == 0
+
+
 def test_decode_in_a_graph_follows_lengths_and_rows(fb):
     """A captured append + decode step: replays take the lengths, positions and rows of the moment."""
     p = R.Paged(6, [90, 300], 2, 64, 64, Q8, Q8, 16)
