@@ -133,8 +133,8 @@ __device__ __forceinline__ int v_comp(int type, int n, int g, int half) {
 // scores: s[i] of keys g, g, g + 8, g + 8 and heads 2t, 2t + 1, 2t, 2t + 1 (the C fragment)
 
 template <int D>
-__device__ __forceinline__ void scores_f16(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
-  const uint32_t at = rows[lane & 15] + (lane >> 4) * 16;
+__device__ __forceinline__ void scores_f16(float (&s)[4], uint32_t rows, uint32_t qf, int lane) {
+  const uint32_t at = lds_u32(rows + 4 * (lane & 15)) + (lane >> 4) * 16;
   float c2[4] = {};
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
@@ -156,10 +156,10 @@ __device__ __forceinline__ void q8_h2(uint32_t w, uint32_t& x0, uint32_t& x1) {
 }
 
 template <int D>
-__device__ __forceinline__ void scores_q8(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
+__device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = rows[g], r1 = rows[g + 8];
-#pragma unroll
+  const uint32_t r0 = lds_u32(rows + 4 * g), r1 = lds_u32(rows + 4 * g + 32);
+#pragma unroll 2
   for (int pr = 0; pr < D / 64; ++pr) {
     const uint32_t p0 = r0 + pr * 68, p1 = r1 + pr * 68;
     const uint32_t h0 = lds_u32(p0), h1 = lds_u32(p1), m0 = lds_u32(p0 + 32), m1 = lds_u32(p1 + 32);
@@ -199,9 +199,9 @@ __device__ __forceinline__ void q4_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 template <int D>
-__device__ __forceinline__ void scores_q4(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
+__device__ __forceinline__ void scores_q4(float (&s)[4], uint32_t rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = rows[g], r1 = rows[g + 8];
+  const uint32_t r0 = lds_u32(rows + 4 * g), r1 = lds_u32(rows + 4 * g + 32);
 #pragma unroll
   for (int pr = 0; pr < D / 64; ++pr) {
     const uint32_t p0 = r0 + pr * 36, p1 = r1 + pr * 36;
@@ -233,9 +233,9 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& l
 }
 
 template <int D>
-__device__ __forceinline__ void scores_f32(float (&s)[4], const uint32_t* rows, uint32_t qf, int lane) {
+__device__ __forceinline__ void scores_f32(float (&s)[4], uint32_t rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = rows[g] + 4 * t, r1 = rows[g + 8] + 4 * t;
+  const uint32_t r0 = lds_u32(rows + 4 * g) + 4 * t, r1 = lds_u32(rows + 4 * g + 32) + 4 * t;
   float c2[4] = {}, c3[4] = {};
 #pragma unroll 8
   for (int ks = 0; ks < D / 8; ++ks) {
@@ -268,8 +268,8 @@ __device__ __forceinline__ void transpose_scores(float (&s)[4]) {
 // values: o[n] += V^T P for the DV / 16 tiles of 16 components; p: head g, keys 2t, 2t+1, 2t+8, 2t+9
 
 template <int DV>
-__device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
-  const uint32_t at = rows[(lane & 7) + (lane >> 4) * 8] + ((lane >> 3) & 1) * 16;
+__device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (&p)[4], uint32_t rows, int lane) {
+  const uint32_t at = lds_u32(rows + 4 * ((lane & 7) + (lane >> 4) * 8)) + ((lane >> 3) & 1) * 16;
   const uint32_t h0 = pack_h2(p[0], p[1]), h1 = pack_h2(p[2], p[3]);
   const uint32_t l0 = pack_h2(p[0] - lo_h(h0), p[1] - hi_h(h0)), l1 = pack_h2(p[2] - lo_h(h1), p[3] - hi_h(h1));
 #pragma unroll
@@ -282,14 +282,14 @@ __device__ __forceinline__ void values_f16(float (&o)[DV / 16][4], const float (
 }
 
 template <int DV>
-__device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
+__device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (&p)[4], uint32_t rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
   uint32_t ph[4], pl[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) split_tf32(__float_as_uint(p[i]), ph[i], pl[i]);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t r0 = rows[8 * k + 2 * t] + 4 * g, r1 = rows[8 * k + 2 * t + 1] + 4 * g;
+    const uint32_t r0 = lds_u32(rows + 4 * (8 * k + 2 * t)) + 4 * g, r1 = lds_u32(rows + 4 * (8 * k + 2 * t + 1)) + 4 * g;
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) {
       uint32_t h[4], l[4];
@@ -323,9 +323,9 @@ __device__ __forceinline__ uint32_t q8_b2(uint32_t k0, uint32_t k1) {
 }
 
 template <int DV>
-__device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
+__device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&p)[4], uint32_t rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r[4] = {rows[2 * t], rows[2 * t + 1], rows[2 * t + 8], rows[2 * t + 9]};
+  const uint32_t r[4] = {lds_u32(rows + 8 * t), lds_u32(rows + 8 * t + 4), lds_u32(rows + 8 * t + 32), lds_u32(rows + 8 * t + 36)};
 #pragma unroll
   for (int pr = 0; pr < DV / 64; ++pr) {
     uint32_t w[4], x[4];
@@ -366,9 +366,9 @@ __device__ __forceinline__ uint32_t q4_b2(uint32_t w) {
 }
 
 template <int DV>
-__device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&p)[4], const uint32_t* rows, int lane) {
+__device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&p)[4], uint32_t rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t r[4] = {rows[2 * t], rows[2 * t + 1], rows[2 * t + 8], rows[2 * t + 9]};
+  const uint32_t r[4] = {lds_u32(rows + 8 * t), lds_u32(rows + 8 * t + 4), lds_u32(rows + 8 * t + 32), lds_u32(rows + 8 * t + 36)};
 #pragma unroll
   for (int blk = 0; blk < DV / 32; ++blk) {
     uint32_t w[4];
@@ -396,16 +396,13 @@ __device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&
 // ------------------------------------------------------------------------------------------------
 // the kernel
 
-#ifndef FA_NW
-#define FA_NW 16
-#endif
-constexpr int kNW = FA_NW;
-constexpr int kUnit = 128;      // keys that a range of work is counted in
-constexpr int kMinUnits = 2;    // a range has at least this many units (where the work is that much)
+constexpr int kUnit = 128;       // keys that a range of work is counted in
+constexpr int kMinUnits = 2;     // a range has at least this many units (where the work is that much)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLift = 7.f;    // weights are exp2(x - max + 7): the parts' small end moves out of the way
-constexpr float kRescale = 8.f; // the running maximum moves when a score exceeds it by this (weights <= 2^15)
+constexpr float kLift = 7.f;     // weights are exp2(x - max + 7): the parts' small end moves out of the way
+constexpr float kRescale = 8.f;  // the running maximum moves when a score exceeds it by this (weights <= 2^15)
+constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct DecodeArgs {
   Cache c;
@@ -421,14 +418,49 @@ struct DecodeArgs {
   float* part;  // [R][HG][2]: partial O [8][DV], then maxima [8] and sums [8]
   int4* jobs;   // [R]: the sequence that range r begins and a later one ends: {b, last range, slot, 0}, or b = -1
   int R;        // ranges of the grid
-  int pk, pv, slots;  // bytes from one key / value row to the next in shared memory, slots of each ring
-  int tiled;          // 1: a tile's rows are one box of the tensor maps; 0: one bulk copy a row
-  int nbk, nbv;       // bytes of a row's bulk copy: it and what pads its ends to 16 bytes
-  int esk, esv;       // log2 of the tensor maps' element size
+  int tiled;    // 1: a tile's rows are one box of the tensor maps; 0: one bulk copy a row
   uint32_t page_mul;  // j / page_size = j * page_mul >> page_shift for j < 2^30
   int page_shift;
   uint64_t wait_ns;   // a wait for a copy gives up after this long (0, the failure-detection hook: at once)
 };
+
+struct DecodeMaps {
+  CUtensorMap k, v;
+};
+
+// ---- what a kernel's shape fixes, for the host too
+__host__ __device__ constexpr int cache_row_bytes(int type, int D) {
+  return type == FA_F32 ? 4 * D : type == FA_F16 ? 2 * D : type == FA_Q8_0 ? D / 32 * 34 : D / 32 * 18;
+}
+// bytes of a row's bulk copy: it and what pads its ends to 16-byte boundaries (the row starts up to 16 bytes,
+// less its own excess over a multiple of 16, behind one)
+__host__ __device__ constexpr int copy_bytes(int rb) { return (rb + 15) / 16 * 16; }
+// Rows in shared memory start an odd multiple of 16 bytes after one another: the eight rows that a
+// fragment load touches then lie in different banks.
+__host__ __device__ constexpr int smem_pitch(int rb) { return copy_bytes(rb) % 32 == 16 ? copy_bytes(rb) : copy_bytes(rb) + 16; }
+// log2 of the tensor map's element size: a box is at most 256 elements wide
+__host__ __device__ constexpr int map_es(int pitch) { return pitch <= 512 ? 1 : pitch <= 1024 ? 2 : 3; }
+
+// One CTA an SM.  As many warps (16, 12, 8 or 4) as registers and shared memory hold with one slot each
+// (a tile's key rows, its value rows, and the warp's sums), then as many slots as fit.
+constexpr int kSmem = 222 * 1024;  // of the 227 KB: what the fixed-size arrays leave
+constexpr int kSlotCtl = 160;      // a slot's row addresses, barriers and mask (struct Slot of the kernel)
+struct DecodeShape {
+  int nw, slots, smem, pk, pv, qf, stage;
+};
+__host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, int vt) {
+  DecodeShape c{};
+  c.pk = smem_pitch(cache_row_bytes(kt, D)), c.pv = smem_pitch(cache_row_bytes(vt, DV));
+  c.qf = (kt == FA_F32 ? D / 8 : D / 16) * 512;
+  c.stage = 16 * (c.pk + c.pv);
+  const int sums = DV * 32, slot = c.stage + kSlotCtl;
+  c.nw = DV == 256 ? 12 : 16;
+  while (c.nw > 4 && c.qf + c.nw * (slot + sums) > kSmem) c.nw -= 4;
+  c.slots = (kSmem - c.qf - c.nw * sums) / (c.nw * slot);
+  if (c.slots > 4) c.slots = 4;
+  c.smem = c.qf + c.nw * (c.slots * c.stage + sums);
+  return c;
+}
 
 __device__ __forceinline__ float act_load(const void* p, int act, long long i) {
   if (act == FA_ACT_F32) return static_cast<const float*>(p)[i];
@@ -451,6 +483,32 @@ __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / 
 __device__ __forceinline__ long long range_begin(long long r, long long U, int Re) { return r * U / Re; }
 __device__ __forceinline__ int range_of(long long u, long long U, int Re) { return (int)(((u + 1) * Re - 1) / U); }
 
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// (out of line: it is rarely entered)
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = fab::globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (bar_try(bar, parity)) return true;
+    if ((it & 255u) == 0 && fab::globaltimer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // Sixteen rows of one KV head by TMA: x (elements, a multiple of 16 bytes) is where the head's rows start
 // in a cell, y the first row of the pool.
 __device__ __forceinline__ void tile_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -468,32 +526,50 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const uint8_t* src, uint3
                : "memory");
 }
 
-constexpr uint64_t kDrainNs = 2000000000ull;
+// Soft cap and distance bias of a lane's four scores (keys at distances d, d + 1, d + 8, d + 9; out of line)
+static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float slope, int d) {
+  if (cap > 0.f) {
+    const float inv = 1.f / cap;
+    x = make_float4(cap * tanhf(x.x * inv), cap * tanhf(x.y * inv), cap * tanhf(x.z * inv), cap * tanhf(x.w * inv));
+  }
+  return make_float4(fmaf(slope, (float)d, x.x), fmaf(slope, (float)(d + 1), x.y), fmaf(slope, (float)(d + 8), x.z),
+                     fmaf(slope, (float)(d + 9), x.w));
+}
 
 // One range of keys (blockIdx.x / HG) of one (KV head, chunk of eight query heads) (blockIdx.x % HG).
 //
 // The work is the list of all sequences' keys in units of 128, cut into equal ranges whatever the
 // lengths are; consecutive CTAs take the same keys of the different heads, so a page's neighbouring
 // rows are read at the same time.  Within a range each warp takes every NW-th tile of 16 keys with a
-// ring, a running maximum and sums of its own: no barrier until the range or the sequence ends.
-template <int D, int DV, int NW>
-__global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k,
-                                                        const __grid_constant__ CUtensorMap map_v) {
+// ring, a running maximum and sums of its own: no barrier until the range or the sequence ends, and the
+// next sequence's first tiles are under way before this one's sums are joined.
+template <int D, int DV, int KT, int VT>
+__global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
+    k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
+  constexpr int NW = C.nw, SLOTS = C.slots, PK = C.pk, PV = C.pv;
+  constexpr int RBK = cache_row_bytes(KT, D), RBV = cache_row_bytes(VT, DV);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_scan[NW];
   __shared__ int s_seq, s_off;
   __shared__ float s_qs[8], s_ml[NW][16];
-  __shared__ uint64_t s_bar[NW][2][4];               // a slot's key rows, value rows have arrived
-  __shared__ uint32_t s_valid[NW][4];                // keys of the slot's tile
-  __shared__ uint32_t s_rows[NW][2][4][16];          // where the slot's rows start
+  // a slot: where its 16 key rows and its 16 value rows start, the barriers of either, the tile's key mask
+  struct Slot {
+    uint32_t rows[2][16];
+    uint64_t bar[2];
+    uint32_t valid, pad[3];
+  };
+  static_assert(sizeof(Slot) == kSlotCtl && SLOTS >= 1, "shared memory plan");
+  __shared__ __align__(16) Slot s_slot[NW][SLOTS];
   __shared__ __align__(16) uint32_t s_zero[DV + 4];  // the value row of a key that is not there
-  constexpr int QF = (D / 8) * 512;  // operand fragments of q: f32 keys take one per 8 components, others per 16
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hg = blockIdx.x % a.HG, r = blockIdx.x / a.HG, hk = hg / a.chunks;
   const int head0 = hk * a.G + (hg - hk * a.chunks) * 8, nh = min(8, a.G - (hg - hk * a.chunks) * 8);
   const int B = a.c.B;
-  const uint32_t qf = smem_u32(smem), ring = qf + QF;
-  if (lane < 8) fab::mbar_init(&s_bar[warp][lane >> 2][lane & 3], 1);
+  const uint32_t qf = smem_u32(smem), ring = qf + C.qf + warp * (SLOTS * C.stage), ctl = smem_u32(&s_slot[warp][0]);
+  float* acc = reinterpret_cast<float*>(smem + C.qf + NW * SLOTS * C.stage);
+  const int shift_k = hk * RBK & 15, shift_v = hk * RBV & 15;
+  if (lane < 2 * SLOTS) fab::mbar_init(&s_slot[warp][lane >> 1].bar[lane & 1], 1);
   for (int i = threadIdx.x; i < DV + 4; i += NW * 32) s_zero[i] = 0;
   fab::fence_mbar_init();  // ordered before the first copy by the barriers below
 
@@ -506,7 +582,6 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a, const __
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
     if (lane == 0) s_scan[warp] = n;
     __syncthreads();
-#pragma unroll
     for (int w = 0; w < NW; ++w) U += s_scan[w];
     __syncthreads();
   }
@@ -550,245 +625,272 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a, const __
     if (base > u0) break;
   }
 
-  const int slot_k = 16 * a.pk, slot_v = 16 * a.pv;
-  const uint32_t ring_k = ring + warp * a.slots * (slot_k + slot_v), ring_v = ring_k + a.slots * slot_k;
-  const float lnscale = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
-  int b = s_seq, off = s_off, seg = 0, slot = 0;
-  uint32_t phases = 0, armed = 0;  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way
-  bool dead = false;    // a wait ran out: no more work is issued
+  // ---- a segment: the part of one sequence that lies in the range
+  struct Segment {
+    int b, keys, j0, j1, ntile;  // sequence, its keys, the segment's keys [j0, j1) and tiles
+    bool whole;                  // the sequence lies in the range
+  };
   int4 job = make_int4(-1, 0, 0, 0);
-  __syncthreads();
-  for (long long u = u0; u < u1; ++seg) {
-    int keys = seq_keys(a, b);
-    while (keys == 0 && b + 1 < B) keys = seq_keys(a, ++b), off = 0;
-    if (keys == 0) break;  // (the lengths changed while the kernel ran)
-    const int nu = units_of(keys), take = (int)min((long long)(nu - off), u1 - u);
-    const int j0 = off * kUnit, j1 = min(keys, (off + take) * kUnit), ntile = dead ? 0 : (j1 - j0 + 15) >> 4;
-    const bool whole = take == nu;
-    const long long ub = u - off;  // the sequence's first unit
-    if (off == 0 && !whole) job = make_int4(b, range_of(ub + nu - 1, U, Re), seg == 0 ? 0 : 1, 0);
+  auto segment = [&](int b, int off, long long u, int seg) {
+    Segment s = {b, 0, 0, 0, 0, false};
+    if (u >= u1) return s;
+    s.keys = seq_keys(a, b);
+    while (s.keys == 0 && s.b + 1 < B) s.keys = seq_keys(a, ++s.b), off = 0;
+    const int nu = units_of(s.keys), take = (int)min((long long)(nu - off), u1 - u);
+    s.j0 = off * kUnit, s.j1 = min(s.keys, (off + take) * kUnit);
+    s.ntile = (s.j1 - s.j0 + 15) >> 4;  // (0 if the lengths changed while the kernel ran)
+    s.whole = take == nu;
+    if (off == 0 && !s.whole) job = make_int4(s.b, range_of(u + nu - 1, U, Re), seg == 0 ? 0 : 1, 0);
+    return s;
+  };
 
-    // ---- rows of a tile.  Tiled copies (whole tiles in a page): the tile's first row, the same in every
-    // lane.  Otherwise one key a lane, lanes 16 .. 31 as 0 .. 15.  Page numbers are fetched a tile ahead of
-    // the copies that they are for.
-    const int32_t* table = a.c.table + (long long)b * a.c.max_pages;
-    struct Where {
-      int page, off;
-    };
-    const int key_lane = a.tiled ? 0 : lane & 15;
-    auto where = [&](int tile) {
-      const int j = j0 + tile * 16 + key_lane;
-      Where w = {-1, 0};
-      if (tile < ntile && j < j1) {
-        const int p = (int)((uint64_t)j * a.page_mul >> a.page_shift);
-        w.page = __ldg(table + p), w.off = j - p * a.c.page_size;
-        if (w.page < 0) w.page = 0x7fffffff;
-      }
-      return w;
-    };
-    auto row_of = [&](const Where& w) {
-      const bool ok = w.page >= 0 && w.page < a.c.num_pages;
-      if (w.page >= 0 && !ok) *a.c.err = FA_ERR_PAGE;
-      return ok ? w.page * a.c.page_size + w.off : -1;
-    };
-    auto fetch = [&](int kv, int slot, int row, int tile) {
-      uint64_t* bar = &s_bar[warp][kv][slot];
-      const int rb = kv ? a.c.rbv : a.c.rbk, pitch = kv ? a.pv : a.pk;
-      const uint32_t dst = kv ? ring_v + slot * slot_v : ring_k + slot * slot_k;
-      armed |= 1u << (4 * kv + slot);
-      if (a.tiled) {
-        const int n = row >= 0 ? min(16, j1 - (j0 + tile * 16)) : 0;  // the rows behind them are not used
-        if (lane == 0) {
-          if (kv == 0) s_valid[warp][slot] = (1u << n) - 1;
-          fab::mbar_arrive_expect_tx(bar, n ? 16 * pitch : 0);
-          if (n) tile_rows(dst, kv ? &map_v : &map_k, (hk * rb & ~15) >> (kv ? a.esv : a.esk), row, smem_u32(bar));
-        }
-        if (lane < 16)
-          s_rows[warp][kv][slot][lane] = kv && lane >= n ? smem_u32(s_zero) : dst + lane * pitch + (hk * rb & 15);
-        return;
-      }
-      const uint32_t ok = __ballot_sync(kFull, row >= 0) & 0xffffu;
-      const int nb = kv ? a.nbv : a.nbk;
-      if (lane == 0) {
-        if (kv == 0) s_valid[warp][slot] = ok;
-        fab::mbar_arrive_expect_tx(bar, __popc(ok) * nb);
-      }
-      __syncwarp();
-      if (lane < 16) {
-        const long long at = ((long long)max(row, 0) * a.c.Hkv + hk) * rb;
-        s_rows[warp][kv][slot][lane] = kv && row < 0 ? smem_u32(s_zero) : dst + lane * pitch + ((uint32_t)at & 15);
-        if (row >= 0) bulk_row(dst + lane * pitch, (kv ? a.c.v : a.c.k) + (at & ~15LL), nb, smem_u32(bar));
-      }
-    };
-    for (int i = 0, sl = slot; i < a.slots; ++i) {
-      const int tile = warp + i * NW;
-      if (tile < ntile) {
-        const int row = row_of(where(tile));
-        fetch(0, sl, row, tile), fetch(1, sl, row, tile);
-      }
-      if (++sl == a.slots) sl = 0;
+  // ---- rows of a tile.  Tiled copies (whole tiles in a page): the tile's first row, the same in every
+  // lane.  Otherwise one key a lane, lanes 16 .. 31 as 0 .. 15.  Page numbers are fetched a tile ahead of
+  // the copies that they are for.
+  struct Where {
+    int page, off;
+  };
+  const int key_lane = a.tiled ? 0 : lane & 15;
+  auto where = [&](const Segment& s, int tile) {
+    const int j = s.j0 + tile * 16 + key_lane;
+    Where w = {-1, 0};
+    if (tile < s.ntile && j < s.j1) {
+      const int p = (int)((uint64_t)j * a.page_mul >> a.page_shift);
+      w.page = __ldg(a.c.table + (long long)s.b * a.c.max_pages + p), w.off = j - p * a.c.page_size;
+      if (w.page < 0) w.page = 0x7fffffff;
     }
-    // the slot's copies have arrived (all lanes agree)
-    auto arrived = [&](int kv, int slot) {
-      const uint32_t bit = 1u << (4 * kv + slot);
-      const bool came = a.wait_ns > 0 && fab::mbar_wait_bounded(&s_bar[warp][kv][slot], (phases & bit) != 0, a.wait_ns);
+    return w;
+  };
+  auto row_of = [&](const Where& w) {
+    const bool ok = w.page >= 0 && w.page < a.c.num_pages;
+    if (w.page >= 0 && !ok) *a.c.err = FA_ERR_PAGE;
+    return ok ? w.page * a.c.page_size + w.off : -1;
+  };
+  uint32_t phases = 0, armed = 0;  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way
+  auto fetch = [&](const Segment& s, int kv, int slot, int row, int tile) {
+    const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), bar = sl + 128 + 8 * kv;
+    const uint32_t dst = ring + slot * C.stage + (kv ? 16 * PK : 0);
+    const int pitch = kv ? PV : PK;
+    armed |= 1u << (4 * kv + slot);
+    if (a.tiled) {
+      const int n = row >= 0 ? min(16, s.j1 - (s.j0 + tile * 16)) : 0;  // the rows behind them are not used
+      if (lane == 0) {
+        if (kv == 0) sts_u32(sl + 144, (1u << n) - 1);
+        bar_expect(bar, n ? 16 * pitch : 0);
+        if (n) tile_rows(dst, kv ? &map_v : &map_k, kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK), row, bar);
+      }
+      if (lane < 16)
+        sts_u32(sl + 64 * kv + 4 * lane, kv && lane >= n ? smem_u32(s_zero) : dst + lane * pitch + (kv ? shift_v : shift_k));
+      return;
+    }
+    const uint32_t ok = __ballot_sync(kFull, row >= 0) & 0xffffu;
+    const uint32_t nb = kv ? copy_bytes(RBV) : copy_bytes(RBK);
+    if (lane == 0) {
+      if (kv == 0) sts_u32(sl + 144, ok);
+      bar_expect(bar, __popc(ok) * nb);
+    }
+    __syncwarp();
+    if (lane < 16) {
+      const long long at = ((long long)max(row, 0) * a.c.Hkv + hk) * (kv ? RBV : RBK);
+      sts_u32(sl + 64 * kv + 4 * lane, kv && row < 0 ? smem_u32(s_zero) : dst + lane * pitch + ((uint32_t)at & 15));
+      if (row >= 0) bulk_row(dst + lane * pitch, (kv ? a.c.v : a.c.k) + (at & ~15LL), nb, bar);
+    }
+  };
+  // the slot's copies have arrived (all lanes agree)
+  auto arrived = [&](int kv, int slot) {
+    const uint32_t bit = 1u << (4 * kv + slot), bar = ctl + slot * (uint32_t)sizeof(Slot) + 128 + 8 * kv;
+    const uint32_t parity = (phases & bit) != 0;
+    bool came = a.wait_ns > 0 && bar_try(bar, parity);
+    if (!__all_sync(kFull, came)) {
+      came = a.wait_ns > 0 && bar_wait_slow(bar, parity, a.wait_ns);
       if (!__all_sync(kFull, came)) return false;
-      phases ^= bit, armed &= ~bit;
-      return true;
-    };
-    int next = warp + a.slots * NW;
-    Where ahead = where(next);
-
-    // ---- q of the chunk's heads: scaled by a power of two into range, split into parts
+    }
+    phases ^= bit, armed &= ~bit;
+    return true;
+  };
+  int slot = 0;
+  auto prefetch = [&](const Segment& s) {
+    for (int i = 0, sl = slot; i < SLOTS; ++i) {
+      const int tile = warp + i * NW;
+      if (tile < s.ntile) {
+        const int row = row_of(where(s, tile));
+        fetch(s, 0, sl, row, tile), fetch(s, 1, sl, row, tile);
+      }
+      if (++sl == SLOTS) sl = 0;
+    }
+  };
+  // q of the chunk's heads, a head a warp: scaled by a power of two into range, split into parts
+  auto load_q = [&](const Segment& s) {
     for (int h = warp; h < 8; h += NW) {
+      const long long at = s.b * a.q_row + (head0 + h) * a.q_head;
       float m = 0.f;
-      const long long at = b * a.q_row + (head0 + h) * a.q_head;
       if (h < nh)
         for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(act_load(a.q, a.act, at + d)));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      if (lane == 0) s_qs[h] = m > 0.f && m < INFINITY ? ldexpf(1.f, (a.c.k_type == FA_F32 ? 0 : 8) - ilogbf(m)) : 1.f;
-    }
-    __syncthreads();
-    {
-      const int steps = a.c.k_type == FA_F32 ? D / 8 : D / 16;
-      const long long at = b * a.q_row + (long long)(head0 + g) * a.q_head;
-      const float qs = s_qs[g];
-      for (int ks = warp; ks < steps; ks += NW) {
+      const float qs = m > 0.f && m < INFINITY ? ldexpf(1.f, (KT == FA_F32 ? 0 : 8) - ilogbf(m)) : 1.f;
+      if (lane == 0) s_qs[h] = qs;
+      constexpr int steps = KT == FA_F32 ? D / 8 : D / 16;
+      for (int ks = g; ks < steps; ks += 8) {
         uint32_t w[4];
-        if (a.c.k_type == FA_F32) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float x = g < nh ? act_load(a.q, a.act, at + ks * 8 + t + 4 * i) * qs : 0.f;
-            split_tf32(__float_as_uint(x), w[i], w[2 + i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float x = g < nh ? act_load(a.q, a.act, at + k_comp16(a.c.k_type, ks, t, i, 0)) * qs : 0.f;
-            const float y = g < nh ? act_load(a.q, a.act, at + k_comp16(a.c.k_type, ks, t, i, 1)) * qs : 0.f;
+        for (int i = 0; i < 2; ++i) {
+          if (KT == FA_F32) {
+            split_tf32(__float_as_uint(h < nh ? act_load(a.q, a.act, at + ks * 8 + t + 4 * i) * qs : 0.f), w[i], w[2 + i]);
+          } else {
+            const float x = h < nh ? act_load(a.q, a.act, at + k_comp16(KT, ks, t, i, 0)) * qs : 0.f;
+            const float y = h < nh ? act_load(a.q, a.act, at + k_comp16(KT, ks, t, i, 1)) * qs : 0.f;
             w[i] = pack_h2(x, y);
             w[2 + i] = pack_h2(x - lo_h(w[i]), y - hi_h(w[i]));
           }
         }
-        fab::sts_v4(qf + ks * 512 + lane * 16, w[0], w[1], w[2], w[3]);
+        fab::sts_v4(qf + ks * 512 + (h * 4 + t) * 16, w[0], w[1], w[2], w[3]);
       }
     }
-    __syncthreads();
+  };
+
+  long long u = u0;
+  int off = s_off;
+  bool dead = false;  // a wait ran out: no more work is issued
+  Segment sg = segment(s_seq, off, u, 0);
+  prefetch(sg);
+  load_q(sg);
+  __syncthreads();
+  for (int seg = 0; u < u1; ++seg) {
     // ---- the warp's tiles
     const float qscale = a.scale / s_qs[g];
     const float slope = a.alibi && g < nh ? a.alibi[head0 + g] : 0.f;
+    const bool ext = a.softcap > 0.f || a.alibi;
     float o[DV / 16][4];
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
+    const int ntile = dead ? 0 : sg.ntile;
+    int next = warp + SLOTS * NW;
+    Where ahead = where(sg, next);
     for (int tile = warp; tile < ntile; tile += NW, next += NW) {
       const int row = row_of(ahead);
-      ahead = where(next + NW);
+      ahead = where(sg, next + NW);
+      const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), qa = qf + lane * 16;
       dead = !arrived(0, slot);
       if (dead) break;
       float s[4] = {};
-      const uint32_t* kr = s_rows[warp][0][slot];
-      const uint32_t qa = qf + lane * 16;
-      if (a.c.k_type == FA_Q8_0) scores_q8<D>(s, kr, qa, lane);
-      else if (a.c.k_type == FA_F16) scores_f16<D>(s, kr, qa, lane);
-      else if (a.c.k_type == FA_Q4_0) scores_q4<D>(s, kr, qa, lane);
-      else scores_f32<D>(s, kr, qa, lane);
+      if (KT == FA_Q8_0) scores_q8<D>(s, sl, qa, lane);
+      else if (KT == FA_F16) scores_f16<D>(s, sl, qa, lane);
+      else if (KT == FA_Q4_0) scores_q4<D>(s, sl, qa, lane);
+      else scores_f32<D>(s, sl, qa, lane);
       transpose_scores(s);
-      const uint32_t ok = s_valid[warp][slot];
+      const uint32_t ok = lds_u32(sl + 144);
       __syncwarp();
-      if (next < ntile) fetch(0, slot, row, next);
-      float mx = -INFINITY;
+      if (next < ntile) fetch(sg, 0, slot, row, next);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-        float x = s[i] * qscale;
-        if (a.softcap > 0.f) x = a.softcap * tanhf(x * lnscale);
-        if (a.alibi) x = fmaf(slope, (float)(j0 + tile * 16 + key - (keys - 1)), x);
-        s[i] = (ok >> key) & 1 ? x * kLog2e : -INFINITY;
-        mx = fmaxf(mx, s[i]);
+      for (int i = 0; i < 4; ++i) s[i] *= qscale;
+      if (ext) {
+        const float4 x = cap_and_bias(make_float4(s[0], s[1], s[2], s[3]), a.softcap, slope,
+                                      sg.j0 + tile * 16 + 2 * t - (sg.keys - 1));
+        s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] *= kLog2e;
+      if (ok != 0xffffu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((ok >> (2 * t + (i & 1) + 8 * (i >> 1))) & 1)) s[i] = -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      const bool move = mx > m + kRescale || (m == -INFINITY && mx > m);
+      const bool first = m == -INFINITY, move = first ? mx > m : mx > m + kRescale;
       if (__any_sync(kFull, move)) {
-        const float f = move ? (m == -INFINITY ? 0.f : fab::ex2(m - mx)) : 1.f;
+        const float f = move && !first ? fab::ex2(m - mx) : 1.f;  // (nothing has been summed up to the first)
         if (move) m = mx;
-        l *= f;
-        const float f0 = __shfl_sync(kFull, f, 8 * t), f1 = __shfl_sync(kFull, f, 8 * t + 4);
+        if (__any_sync(kFull, f != 1.f)) {
+          l *= f;
+          const float f0 = __shfl_sync(kFull, f, 8 * t), f1 = __shfl_sync(kFull, f, 8 * t + 4);
 #pragma unroll
-        for (int n = 0; n < DV / 16; ++n) o[n][0] *= f0, o[n][1] *= f1, o[n][2] *= f0, o[n][3] *= f1;
+          for (int n = 0; n < DV / 16; ++n) o[n][0] *= f0, o[n][1] *= f1, o[n][2] *= f0, o[n][3] *= f1;
+        }
       }
       const float ref = m == -INFINITY ? 0.f : m - kLift;
       float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = fab::ex2(s[i] - ref), l += p[i];
+      for (int i = 0; i < 4; ++i) p[i] = fab::ex2(s[i] - ref);
+      l += (p[0] + p[1]) + (p[2] + p[3]);
       dead = !arrived(1, slot);
       if (dead) break;
-      const uint32_t* vr = s_rows[warp][1][slot];
-      if (a.c.v_type == FA_Q8_0) values_q8<DV>(o, p, vr, lane);
-      else if (a.c.v_type == FA_F16) values_f16<DV>(o, p, vr, lane);
-      else if (a.c.v_type == FA_Q4_0) values_q4<DV>(o, p, vr, lane);
-      else values_f32<DV>(o, p, vr, lane);
+      if (VT == FA_Q8_0) values_q8<DV>(o, p, sl + 64, lane);
+      else if (VT == FA_F16) values_f16<DV>(o, p, sl + 64, lane);
+      else if (VT == FA_Q4_0) values_q4<DV>(o, p, sl + 64, lane);
+      else values_f32<DV>(o, p, sl + 64, lane);
       __syncwarp();
-      if (next < ntile) fetch(1, slot, row, next);
-      if (++slot == a.slots) slot = 0;
+      if (next < ntile) fetch(sg, 1, slot, row, next);
+      if (++slot == SLOTS) slot = 0;
     }
-    if (dead && ntile > 0) {  // let the copies in flight land before their memory gets another use
+    if (dead && ntile > 0) {  // let the copies in flight land: nothing more is issued
       if (lane == 0) {
         atomicExch(a.c.err, FA_ERR_TIMEOUT);
         for (int i = 0; i < 8; ++i)
-          if ((armed >> i) & 1) fab::mbar_wait_bounded(&s_bar[warp][i >> 2][i & 3], (phases >> i) & 1, kDrainNs);
+          if ((armed >> i) & 1) bar_wait_slow(ctl + (i & 3) * (uint32_t)sizeof(Slot) + 128 + 8 * (i >> 2), (phases >> i) & 1, kDrainNs);
       }
       __syncwarp();
     }
+    // ---- the next segment's first copies
+    const Segment cur = sg;
+    const int take = units_of(cur.j1 - cur.j0);
+    u += max(take, 1);
+    sg = segment(cur.b + 1 < B ? cur.b + 1 : cur.b, 0, u, seg + 1);
+    if (!dead) prefetch(sg);
+    // ---- the warps' sums, joined in the warps' order
     l += __shfl_xor_sync(kFull, l, 1);
     l += __shfl_xor_sync(kFull, l, 2);
     if (t == 0) s_ml[warp][g] = m, s_ml[warp][8 + g] = l;
-    __syncthreads();  // the rings are free: they take the warps' sums
-    float* acc = reinterpret_cast<float*>(smem + QF);
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[((warp * (DV / 16) + n) * 4 + i) * 32 + lane] = o[n][i];
-    // heads 2t, 2t + 1 of the columns that this lane joins
-    float M[2] = {-INFINITY, -INFINITY}, S[2] = {0.f, 0.f};
+    __syncthreads();
+    if (u < u1) load_q(sg);
+    float M[2] = {-INFINITY, -INFINITY}, S[2] = {0.f, 0.f}, fw[2][NW];  // heads 2t, 2t + 1
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+#pragma unroll
       for (int w = 0; w < NW; ++w) M[i] = fmaxf(M[i], s_ml[w][2 * t + i]);
       const float ref = M[i] == -INFINITY ? 0.f : M[i];
-      for (int w = 0; w < NW; ++w) S[i] += s_ml[w][8 + 2 * t + i] * exp2f(s_ml[w][2 * t + i] - ref);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        fw[i][w] = fab::ex2(s_ml[w][2 * t + i] - ref);
+        S[i] = fmaf(s_ml[w][8 + 2 * t + i], fw[i][w], S[i]);
+      }
     }
-    __syncthreads();
     float* part = a.part + ((long long)(r * a.HG + hg) * 2 + (seg == 0 ? 0 : 1)) * (8 * DV + 16);
     float fin[2], lse[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float total = S[i], top = M[i], f = 1.f;
-      if (whole && a.sinks && 2 * t + i < nh) {  // one more term of the sum, without a value
+      if (cur.whole && a.sinks && 2 * t + i < nh) {  // one more term of the sum, without a value
         const float sk = a.sinks[head0 + 2 * t + i] * kLog2e;
         top = fmaxf(M[i], sk);
         f = M[i] == -INFINITY ? 0.f : exp2f(M[i] - top);
         total = S[i] * f + exp2f(sk - top + kLift);
       }
-      fin[i] = whole ? (total > 0.f ? f / total : 0.f) : 1.f;
+      fin[i] = cur.whole ? (total > 0.f ? f / total : 0.f) : 1.f;
       lse[i] = total > 0.f ? (top - kLift + log2f(total)) * kLn2 : -INFINITY;
     }
     for (int n = warp; n < DV / 16; n += NW) {
       float x[4] = {};
+#pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float f0 = s_ml[w][2 * t] == -INFINITY ? 0.f : exp2f(s_ml[w][2 * t] - M[0]);
-        const float f1 = s_ml[w][2 * t + 1] == -INFINITY ? 0.f : exp2f(s_ml[w][2 * t + 1] - M[1]);
         const float* p = acc + (w * (DV / 16) + n) * 128 + lane;
-        x[0] = fmaf(p[0], f0, x[0]), x[1] = fmaf(p[32], f1, x[1]), x[2] = fmaf(p[64], f0, x[2]), x[3] = fmaf(p[96], f1, x[3]);
+        x[0] = fmaf(p[0], fw[0][w], x[0]), x[1] = fmaf(p[32], fw[1][w], x[1]);
+        x[2] = fmaf(p[64], fw[0][w], x[2]), x[3] = fmaf(p[96], fw[1][w], x[3]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int h = 2 * t + (i & 1), d = v_comp(a.c.v_type, n, g, i >> 1);
+        const int h = 2 * t + (i & 1), d = v_comp(VT, n, g, i >> 1);
         if (h < nh) {
-          if (whole) act_store(a.O, a.act, ((long long)b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
+          if (cur.whole) act_store(a.O, a.act, ((long long)cur.b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
           else part[h * DV + d] = x[i];
         }
       }
@@ -797,13 +899,11 @@ __global__ void __launch_bounds__(NW * 32) k_decode(const DecodeArgs a, const __
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = 2 * t + i;
-        if (h < nh && whole && a.lse) a.lse[(long long)b * a.H + head0 + h] = lse[i];
-        if (!whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
+        if (h < nh && cur.whole && a.lse) a.lse[(long long)cur.b * a.H + head0 + h] = lse[i];
+        if (!cur.whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
       }
     }
-    fab::fence_proxy_async_smem();  // the sums' memory takes copies again
     __syncthreads();
-    u += take, ++b, off = 0;
   }
   if (hg == 0 && threadIdx.x == 0) a.jobs[r] = job;
 }
@@ -843,28 +943,47 @@ __global__ void __launch_bounds__(256) k_decode_join(const DecodeArgs a) {
   if (threadIdx.x == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
 }
 
-struct DecodeMaps {
-  CUtensorMap k, v;
-};
-cudaError_t run_decode_d64(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s);
-cudaError_t run_decode_d128(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s);
-cudaError_t run_decode_d256(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s);
+typedef cudaError_t (*DecodeFn)(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s);
 
-template <int D, int DV, int NW>
-cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int D, int DV, int KT, int VT>
+cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s) {
+  constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
+  cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, KT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C.smem);
   if (e != cudaSuccess) return e;
-  k_decode<D, DV, NW><<<a.R * a.HG, NW * 32, smem, s>>>(a, m.k, m.v);
+  k_decode<D, DV, KT, VT><<<a.R * a.HG, C.nw * 32, C.smem, s>>>(a, m.k, m.v);
   if (a.R > 1) k_decode_join<DV><<<dim3(a.R, a.H), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
-template <int D>
-cudaError_t pick_decode(const DecodeArgs& a, const DecodeMaps& m, int nw, size_t smem, cudaStream_t s) {
-  switch (a.c.Dv) {
-    case 64: return nw == kNW ? run_decode<D, 64, kNW>(a, m, smem, s) : run_decode<D, 64, 4>(a, m, smem, s);
-    case 128: return nw == kNW ? run_decode<D, 128, kNW>(a, m, smem, s) : run_decode<D, 128, 4>(a, m, smem, s);
+template <int D, int DV, int KT>
+DecodeFn pick_decode_v(int vt) {
+  switch (vt) {
+    case FA_F32: return run_decode<D, DV, KT, FA_F32>;
+    case FA_F16: return run_decode<D, DV, KT, FA_F16>;
+    case FA_Q8_0: return run_decode<D, DV, KT, FA_Q8_0>;
   }
-  return nw == kNW ? run_decode<D, 256, kNW>(a, m, smem, s) : run_decode<D, 256, 4>(a, m, smem, s);
+  return run_decode<D, DV, KT, FA_Q4_0>;
 }
+// The kernel for D and the key type KT; a translation unit each, so that they compile in parallel.
+template <int D, int KT>
+DecodeFn pick_decode(int Dv, int vt);
+template <> DecodeFn pick_decode<64, FA_F32>(int, int);
+template <> DecodeFn pick_decode<64, FA_F16>(int, int);
+template <> DecodeFn pick_decode<64, FA_Q8_0>(int, int);
+template <> DecodeFn pick_decode<64, FA_Q4_0>(int, int);
+template <> DecodeFn pick_decode<128, FA_F32>(int, int);
+template <> DecodeFn pick_decode<128, FA_F16>(int, int);
+template <> DecodeFn pick_decode<128, FA_Q8_0>(int, int);
+template <> DecodeFn pick_decode<128, FA_Q4_0>(int, int);
+template <> DecodeFn pick_decode<256, FA_F32>(int, int);
+template <> DecodeFn pick_decode<256, FA_F16>(int, int);
+template <> DecodeFn pick_decode<256, FA_Q8_0>(int, int);
+template <> DecodeFn pick_decode<256, FA_Q4_0>(int, int);
+#define FAP_INSTANTIATE_DECODE(D, KT)                              \
+  template <>                                                      \
+  DecodeFn pick_decode<D, KT>(int Dv, int vt) {                    \
+    return Dv == 64    ? pick_decode_v<D, 64, KT>(vt)              \
+           : Dv == 128 ? pick_decode_v<D, 128, KT>(vt)             \
+                       : pick_decode_v<D, 256, KT>(vt);            \
+  }
 
 }  // namespace fap

@@ -9,19 +9,10 @@
 
 namespace fap {
 
-// Rows in shared memory start 16 bytes (mod 128) after one another: the eight rows that a fragment
-// load touches then lie in different banks.
-static int smem_pitch(int rb) {
-  int p = (rb + 15) / 16 * 16;
-  while (p % 128 % 32 != 16) p += 16;
-  return p;
-}
-static int copy_bytes(int rb) { return (rb + 15) / 16 * 16; }
-
 // The pool as a matrix of cells [rows][Hkv * rb bytes], read in boxes of 16 rows x `pitch` bytes: the row,
 // what lies before it back to a 16-byte boundary, and padding that spaces the rows in shared memory.
 // Elements are as wide as keeps a box within 256 of them.
-static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, int rb, int pitch, int* es_log2) {
+static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, int rb, int pitch) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -32,8 +23,7 @@ static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, 
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   if (!fn) return false;
-  const int lg = pitch <= 512 ? 1 : pitch <= 1024 ? 2 : 3;
-  *es_log2 = lg;
+  const int lg = map_es(pitch);
   const cuuint64_t dims[2] = {(cuuint64_t)Hkv * rb >> lg, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)Hkv * rb};
   const cuuint32_t box[2] = {(cuuint32_t)(pitch >> lg), 16}, es[2] = {1, 1};
@@ -43,30 +33,32 @@ static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, 
 }
 
 struct DecodePlan {
-  int nw, slots, R, HG, chunks, pk, pv;
-  size_t smem, off_jobs, bytes;
+  int R, HG, chunks;
+  size_t off_jobs, bytes;
 };
 
-// One CTA an SM: eight warps with up to four slots of 16 keys each in what shared memory holds beside
-// q's fragments, or four warps where a tile of wide rows leaves no room for eight.
 static DecodePlan plan_decode(const Cache& c, int H, int nsm) {
   DecodePlan p;
   const int G = H / c.Hkv;
   p.chunks = (G + 7) / 8;
   p.HG = c.Hkv * p.chunks;
-  p.pk = smem_pitch(copy_bytes(c.rbk)), p.pv = smem_pitch(copy_bytes(c.rbv));
-  const size_t qf = (size_t)(c.D / 8) * 512, room = 200 * 1024, stage = 16 * (size_t)(p.pk + p.pv);
-  p.nw = kNW * stage + qf <= room ? kNW : 4;
-  p.slots = (int)std::max<size_t>(1, std::min<size_t>(4, (room - qf) / (p.nw * stage)));
-  const size_t ring = p.nw * p.slots * stage, sums = (size_t)p.nw * c.Dv * 8 * sizeof(float);
-  p.smem = qf + std::max(ring, sums);
-  // ranges: what the SMs hold at a time, but no more than units of work can exist
+  // ranges: one CTA an SM, but no more than units of work can exist
   const long long units = (long long)c.B * (((long long)c.max_pages * c.page_size + kUnit - 1) / kUnit);
-  long long R = std::max(1, nsm / p.HG);
+  const long long R = std::max(1, nsm / p.HG);
   p.R = (int)std::max(1LL, std::min(R, units / kMinUnits));
   p.off_jobs = (size_t)p.R * p.HG * 2 * (8 * c.Dv + 16) * sizeof(float);
   p.bytes = (p.off_jobs + p.R * sizeof(int4) + 255) / 256 * 256;
   return p;
+}
+
+template <int D>
+static DecodeFn pick_decode_k(const Cache& c) {
+  switch (c.k_type) {
+    case FA_F32: return pick_decode<D, FA_F32>(c.Dv, c.v_type);
+    case FA_F16: return pick_decode<D, FA_F16>(c.Dv, c.v_type);
+    case FA_Q8_0: return pick_decode<D, FA_Q8_0>(c.Dv, c.v_type);
+  }
+  return pick_decode<D, FA_Q4_0>(c.Dv, c.v_type);
 }
 
 }  // namespace fap
@@ -107,8 +99,7 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
   a.scale = scale, a.softcap = softcap, a.alibi = alibi_slopes, a.sinks = sinks, a.O = O, a.lse = lse;
   a.part = static_cast<float*>(workspace);
   a.jobs = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_jobs);
-  a.R = p.R, a.pk = p.pk, a.pv = p.pv, a.slots = p.slots;
-  a.nbk = copy_bytes(a.c.rbk), a.nbv = copy_bytes(a.c.rbv);
+  a.R = p.R;
   int lg = 0;
   while ((1LL << lg) < a.c.page_size) ++lg;
   a.page_shift = 30 + lg;
@@ -118,12 +109,9 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
   DecodeMaps m = {};
   const long long rows = (long long)a.c.num_pages * a.c.page_size;
   a.tiled = a.c.page_size % 16 == 0 && (a.c.Hkv * a.c.rbk) % 16 == 0 && (a.c.Hkv * a.c.rbv) % 16 == 0 && rows > 0;
-  if (a.tiled && (!map_pool(&m.k, a.c.k, rows, a.c.Hkv, a.c.rbk, p.pk, &a.esk) ||
-                  !map_pool(&m.v, a.c.v, rows, a.c.Hkv, a.c.rbv, p.pv, &a.esv)))
+  if (a.tiled && (!map_pool(&m.k, a.c.k, rows, a.c.Hkv, a.c.rbk, smem_pitch(a.c.rbk)) ||
+                  !map_pool(&m.v, a.c.v, rows, a.c.Hkv, a.c.rbv, smem_pitch(a.c.rbv))))
     return FA_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a.c.D == 64    ? run_decode_d64(a, m, p.nw, p.smem, s)
-                        : a.c.D == 128 ? run_decode_d128(a, m, p.nw, p.smem, s)
-                                       : run_decode_d256(a, m, p.nw, p.smem, s);
-  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const DecodeFn run = a.c.D == 64 ? pick_decode_k<64>(a.c) : a.c.D == 128 ? pick_decode_k<128>(a.c) : pick_decode_k<256>(a.c);
+  return run(a, m, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
