@@ -159,7 +159,7 @@ template <int D>
 __device__ __forceinline__ void scores_q8(float (&s)[4], uint32_t rows, uint32_t qf, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const uint32_t r0 = lds_u32(rows + 4 * g), r1 = lds_u32(rows + 4 * g + 32);
-#pragma unroll 2
+#pragma unroll
   for (int pr = 0; pr < D / 64; ++pr) {
     const uint32_t p0 = r0 + pr * 68, p1 = r1 + pr * 68;
     const uint32_t h0 = lds_u32(p0), h1 = lds_u32(p1), m0 = lds_u32(p0 + 32), m1 = lds_u32(p1 + 32);
@@ -526,6 +526,25 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const uint8_t* src, uint3
                : "memory");
 }
 
+// A tile's rows one by one: key `lane` & 15 is row `row` of the pool (-1: none), `first` the head's row of
+// cell 0 (out of line: only caches whose tiles are not boxes of a tensor map come here).
+static __device__ __noinline__ void fetch_rows(uint32_t sl, int kv, uint32_t dst, int pitch, const uint8_t* first, int row,
+                                               long long cell, int rb, uint32_t zero) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t bar = sl + 128 + 8 * kv, ok = __ballot_sync(kFull, row >= 0) & 0xffffu, nb = copy_bytes(rb);
+  if (lane == 0) {
+    if (kv == 0) sts_u32(sl + 144, ok);
+    bar_expect(bar, __popc(ok) * nb);
+  }
+  __syncwarp();
+  if (lane < 16) {
+    const uint8_t* src = first + max(row, 0) * cell;
+    const uint32_t in = (uint32_t)reinterpret_cast<uintptr_t>(src) & 15;
+    sts_u32(sl + 64 * kv + 4 * lane, kv && row < 0 ? zero : dst + lane * pitch + in);
+    if (row >= 0) bulk_row(dst + lane * pitch, src - in, nb, bar);
+  }
+}
+
 // Soft cap and distance bias of a lane's four scores (keys at distances d, d + 1, d + 8, d + 9; out of line)
 static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float slope, int d) {
   if (cap > 0.f) {
@@ -574,16 +593,30 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
   fab::fence_mbar_init();  // ordered before the first copy by the barriers below
 
   // ---- the range: U units in all, of which this CTA takes [u0, u1)
+  int n_own = 0, s_before = 0, n_all = 0;  // units of this thread's sequence, of those before it, of all in a batch
+  auto scan = [&](int c0) {
+    const int b = c0 + threadIdx.x;
+    n_own = b < B ? units_of(seq_keys(a, b)) : 0;
+    int x = n_own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    s_before = x - n_own, n_all = 0;
+    for (int w = 0; w < NW; ++w) {
+      const int v = s_scan[w];
+      if (w < warp) s_before += v;
+      n_all += v;
+    }
+  };
   long long U = 0;
   for (int c0 = 0; c0 < B; c0 += NW * 32) {
-    const int b = c0 + threadIdx.x;
-    int n = b < B ? units_of(seq_keys(a, b)) : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
-    if (lane == 0) s_scan[warp] = n;
-    __syncthreads();
-    for (int w = 0; w < NW; ++w) U += s_scan[w];
-    __syncthreads();
+    scan(c0);
+    U += n_all;
   }
   // sequences without keys: their rows, by the CTA whose turn it is
   for (int b = r + a.R * threadIdx.x; b < B; b += a.R * NW * 32) {
@@ -602,28 +635,15 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
     if (hg == 0 && threadIdx.x == 0) a.jobs[r] = make_int4(-1, 0, 0, 0);
     return;
   }
-  // the sequence that u0 lies in
-  long long base = 0;
-  for (int c0 = 0; c0 < B; c0 += NW * 32) {
-    const int b = c0 + threadIdx.x;
-    const int n = b < B ? units_of(seq_keys(a, b)) : 0;
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    long long before = base + x - n;
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += s_scan[w];
-      base += s_scan[w];
-    }
-    if (before <= u0 && u0 < before + n) s_seq = b, s_off = (int)(u0 - before);
-    __syncthreads();
+  // the sequence that u0 lies in: the batch of sequences, then the sequence
+  for (long long base = 0, c0 = 0; c0 < B; c0 += NW * 32) {
+    if (B > NW * 32) scan((int)c0);
+    const long long before = base + s_before;
+    if (before <= u0 && u0 < before + n_own) s_seq = (int)c0 + threadIdx.x, s_off = (int)(u0 - before);
+    base += n_all;
     if (base > u0) break;
   }
+  __syncthreads();
 
   // ---- a segment: the part of one sequence that lies in the range
   struct Segment {
@@ -683,18 +703,9 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
         sts_u32(sl + 64 * kv + 4 * lane, kv && lane >= n ? smem_u32(s_zero) : dst + lane * pitch + (kv ? shift_v : shift_k));
       return;
     }
-    const uint32_t ok = __ballot_sync(kFull, row >= 0) & 0xffffu;
-    const uint32_t nb = kv ? copy_bytes(RBV) : copy_bytes(RBK);
-    if (lane == 0) {
-      if (kv == 0) sts_u32(sl + 144, ok);
-      bar_expect(bar, __popc(ok) * nb);
-    }
-    __syncwarp();
-    if (lane < 16) {
-      const long long at = ((long long)max(row, 0) * a.c.Hkv + hk) * (kv ? RBV : RBK);
-      sts_u32(sl + 64 * kv + 4 * lane, kv && row < 0 ? smem_u32(s_zero) : dst + lane * pitch + ((uint32_t)at & 15));
-      if (row >= 0) bulk_row(dst + lane * pitch, (kv ? a.c.v : a.c.k) + (at & ~15LL), nb, bar);
-    }
+    const uint8_t* pool = kv ? a.c.v : a.c.k;
+    const int rb = kv ? RBV : RBK;
+    fetch_rows(sl, kv, dst, pitch, pool + (long long)hk * rb, row, (long long)a.c.Hkv * rb, rb, smem_u32(s_zero));
   };
   // the slot's copies have arrived (all lanes agree)
   auto arrived = [&](int kv, int slot) {
@@ -840,6 +851,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
     const Segment cur = sg;
     const int take = units_of(cur.j1 - cur.j0);
     u += max(take, 1);
+    if (u >= u1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     sg = segment(cur.b + 1 < B ? cur.b + 1 : cur.b, 0, u, seg + 1);
     if (!dead) prefetch(sg);
     // ---- the warps' sums, joined in the warps' order
@@ -909,38 +921,72 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
 }
 
 // Joins the partial sums of a sequence that several ranges took, in the ranges' order.  blockIdx.x: the
-// range that begins it, blockIdx.y: query head.
+// range that begins it, blockIdx.y: query head.  The grid starts while the ranges' last CTAs run.
 template <int DV>
 __global__ void __launch_bounds__(256) k_decode_join(const DecodeArgs a) {
+  constexpr int LN = DV / 4, GR = 256 / LN;  // threads of a row (four components each), rows read at a time
+  __shared__ float s_f[256], s_red[8];
+  __shared__ float4 s_x[256];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = a.jobs[blockIdx.x];
   if (job.x < 0) return;
   const int h = blockIdx.y, hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
-  constexpr int GR = 256 / DV;  // 4, 2 or 1 groups of threads take parts in turn
-  const int d = threadIdx.x % DV, gr = threadIdx.x / DV, r0 = blockIdx.x, np = job.y - r0 + 1;
+  const int tid = threadIdx.x, ln = tid % LN, gr = tid / LN, r0 = blockIdx.x, np = job.y - r0 + 1;
   auto part = [&](int i) {
     return a.part + ((long long)((r0 + i) * a.HG + hg) * 2 + (i == 0 ? job.z : 0)) * (8 * DV + 16);
   };
-  float M = -INFINITY;
-  for (int i = 0; i < np; ++i) M = fmaxf(M, part(i)[8 * DV + c]);
-  float S = 0.f, x = 0.f, top = M;
-  if (a.sinks) top = fmaxf(M, a.sinks[h] * kLog2e);
-  const float ref = top == -INFINITY ? 0.f : top;
-  for (int i = 0; i < np; ++i) {
-    const float* p = part(i);
-    const float f = exp2f(p[8 * DV + c] - ref);
-    S = fmaf(p[8 * DV + 8 + c], f, S);
-    if (i % GR == gr) x = fmaf(p[c * DV + d], f, x);
-  }
-  if (a.sinks) S += exp2f(a.sinks[h] * kLog2e - ref + kLift);
-  __shared__ float red[256];
-  if (GR > 1) {
-    red[threadIdx.x] = x;
+  auto block = [&](float v, bool mx) {  // the block's maximum or sum, in a fixed order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float w = __shfl_xor_sync(kFull, v, o);
+      v = mx ? fmaxf(v, w) : v + w;
+    }
     __syncthreads();
-    if (gr == 0)
-      for (int i = 1; i < GR; ++i) x += red[i * DV + d];
+    if ((tid & 31) == 0) s_red[tid >> 5] = v;
+    __syncthreads();
+    v = s_red[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v = mx ? fmaxf(v, s_red[w]) : v + s_red[w];
+    return v;
+  };
+  float M = -INFINITY;
+  for (int i = tid; i < np; i += 256) M = fmaxf(M, part(i)[8 * DV + c]);
+  M = block(M, true);
+  const float sk = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
+  const float top = fmaxf(M, sk), ref = top == -INFINITY ? 0.f : top;
+  float S = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < np; i0 += 256) {
+    __syncthreads();
+    if (i0 + tid < np) {
+      const float* p = part(i0 + tid) + 8 * DV + c;
+      s_f[tid] = exp2f(p[0] - ref);
+      S = fmaf(p[8], s_f[tid], S);
+    }
+    __syncthreads();
+    const int n = min(256, np - i0);
+#pragma unroll 4
+    for (int i = gr; i < n; i += GR) {
+      const float4 v = *reinterpret_cast<const float4*>(part(i0 + i) + c * DV + 4 * ln);
+      const float f = s_f[i];
+      x.x = fmaf(v.x, f, x.x), x.y = fmaf(v.y, f, x.y), x.z = fmaf(v.z, f, x.z), x.w = fmaf(v.w, f, x.w);
+    }
   }
-  if (gr == 0) act_store(a.O, a.act, ((long long)job.x * a.H + h) * DV + d, S > 0.f ? x / S : 0.f);
-  if (threadIdx.x == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
+  S = block(S, false);
+  if (a.sinks) S += exp2f(sk - ref + kLift);
+  s_x[tid] = x;
+  __syncthreads();
+  if (gr == 0) {
+    for (int i = 1; i < GR; ++i) {
+      const float4 v = s_x[i * LN + ln];
+      x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+    }
+    const float inv = S > 0.f ? 1.f / S : 0.f;
+    const long long at = ((long long)job.x * a.H + h) * DV + 4 * ln;
+    act_store(a.O, a.act, at, x.x * inv), act_store(a.O, a.act, at + 1, x.y * inv);
+    act_store(a.O, a.act, at + 2, x.z * inv), act_store(a.O, a.act, at + 3, x.w * inv);
+  }
+  if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
 }
 
 typedef cudaError_t (*DecodeFn)(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s);
@@ -951,7 +997,14 @@ cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s)
   cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, KT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C.smem);
   if (e != cudaSuccess) return e;
   k_decode<D, DV, KT, VT><<<a.R * a.HG, C.nw * 32, C.smem, s>>>(a, m.k, m.v);
-  if (a.R > 1) k_decode_join<DV><<<dim3(a.R, a.H), 256, 0, s>>>(a);
+  if (a.R > 1) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.R, a.H), cfg.blockDim = dim3(256), cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, k_decode_join<DV>, a)) != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 template <int D, int DV, int KT>
