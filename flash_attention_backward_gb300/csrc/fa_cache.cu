@@ -144,50 +144,54 @@ __device__ __forceinline__ void store_row8(uint8_t* row, int type, int e0, const
   }
 }
 
-// K (IS_K) or V rows of the CTA's lane groups: HC heads of one token each.
+// K (IS_K) or V rows: a warp takes HC heads of one token, D / 8 lanes a head.
 template <int D, typename TX, bool IS_K>
 __device__ __forceinline__ void append_rows(const RowArgs& a) {
-  constexpr int LG = D / 8, GW = 32 / LG;
-  const int lane = threadIdx.x & 31, e0 = (lane & (LG - 1)) * 8;
-  const long long item = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * GW + lane / LG;
-  const int t = item < (long long)a.T * a.nchunk ? (int)(item / a.nchunk) : -1;
-  const int h0 = t >= 0 ? (int)(item - (long long)t * a.nchunk) * a.HC : 0;
-  long long cell = -1;
-  int pos = 0;
-  if (t >= 0) {
-    const int b = a.seq[t];
-    pos = a.pos[t];
-    if (b >= 0 && pos >= 0) cell = cache_row(a.c, b, pos);
-  }
-  if (!__any_sync(kFull, cell >= 0)) return;
-  Turn8 turn;
-  if (IS_K) turn.set(a.rope, pos, e0);
+  constexpr int LG = D / 8, GW = 32 / LG, U = sizeof(TX) == 2 ? 4 : 2;
+  const int lane = threadIdx.x & 31, grp = lane / LG, e0 = (lane & (LG - 1)) * 8;
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int t = (int)(item / a.nchunk), h0 = (int)(item - (long long)t * a.nchunk) * a.HC;
+  if (t >= a.T) return;
+  const int h1 = min(a.c.Hkv, h0 + a.HC), b = a.seq[t], pos = a.pos[t];
+  const bool vec = IS_K ? a.veck : a.vecv;
+  const TX* x0 = (IS_K ? static_cast<const TX*>(a.xk) + t * a.k_row : static_cast<const TX*>(a.xv) + t * a.v_row) + e0;
+  const long long head = IS_K ? a.k_head : a.v_head;
+  float w[8];
+  if (IS_K && a.wk) load8(a.wk + e0, false, w);
+  if (b < 0 || pos < 0) return;
   const int rb = IS_K ? a.c.rbk : a.c.rbv, type = IS_K ? a.c.k_type : a.c.v_type;
-  for (int i = 0; i < a.HC; ++i) {
-    const int h = h0 + i;
-    const bool on = cell >= 0 && h < a.c.Hkv;
-    float x[8] = {};
-    if (on) {
-      const TX* p = IS_K ? static_cast<const TX*>(a.xk) + t * a.k_row + h * a.k_head
-                         : static_cast<const TX*>(a.xv) + t * a.v_row + h * a.v_head;
-      load8(p + e0, IS_K ? a.veck : a.vecv, x);
+  Turn8<D> turn;
+  uint8_t* cell = nullptr;
+  for (int h = h0 + grp, first = 1; h - grp < h1; h += U * GW, first = 0) {
+    Oct<TX> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * GW < h1) load8_raw(x0 + (h + u * GW) * head, vec, raw[u]);
+    if (first) {
+      const long long row = cache_row(a.c, b, pos);
+      if (row < 0) return;
+      cell = (IS_K ? a.c.k : a.c.v) + row * a.c.Hkv * (long long)rb;
+      if (IS_K) turn.set(a.rope, pos, e0);
     }
-    if (IS_K) {
-      float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-      ss = group_sum<LG>(ss);
-      if (on && a.wk) {
-        const float r = inv_rms(ss, 1.f / D, a.eps);
-        float wv[8];
-        load8(a.wk + e0, false, wv);
+    for (int u = 0; u < U; ++u) {
+      if (h - grp + u * GW >= h1) break;  // (the same in all lanes)
+      const bool on = h + u * GW < h1;
+      float x[8] = {};
+      if (on) unpack8(raw[u], x);
+      if (IS_K) {
+        if (a.wk) {
+          float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wv[j];
+          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+          const float r = inv_rms(group_sum<LG>(ss), 1.f / D, a.eps);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+        }
+        if (a.rope.n_rot) turn.apply(x, a.rope.style, 1.f);
       }
-      if (a.rope.n_rot) turn.apply(x, a.rope.style, 1.f);
+      store_row8(cell + (on ? h + u * GW : 0) * (long long)rb, type, e0, x, on);
     }
-    uint8_t* row = (IS_K ? a.c.k : a.c.v) + ((on ? cell : 0) * a.c.Hkv + (on ? h : 0)) * (long long)rb;
-    store_row8(row, type, e0, x, on);
   }
 }
 
@@ -322,12 +326,12 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
   a.veck = aligned(k, 16) && (w.k_row * es) % 16 == 0 && (w.k_head * es) % 16 == 0;
   a.vecv = aligned(v, 16) && (w.v_row * es) % 16 == 0 && (w.v_head * es) % 16 == 0;
   a.wk = k_norm, a.eps = eps;
-  const long long hc = (long long)T * a.c.Hkv / (16LL * nsm * (256 / std::min(a.c.D, a.c.Dv)));
-  a.HC = (int)std::max(1LL, std::min<long long>(hc, a.c.Hkv));
+  // heads that a warp takes: at least those that lie side by side, more where there are tokens enough
+  const int side = 256 / std::min(a.c.D, a.c.Dv);
+  const long long hc = (long long)T * a.c.Hkv / (16LL * nsm * side) * side;
+  a.HC = (int)std::max<long long>(side, std::min<long long>(hc, 16));
   a.nchunk = (a.c.Hkv + a.HC - 1) / a.HC;
-  // lane groups of a CTA differ between K and V where D != Dv: the grid covers the larger head
-  const int perm = 8 * (256 / std::max(a.c.D, a.c.Dv));
-  const long long blocks = ((long long)T * a.nchunk + perm - 1) / perm;
+  const long long blocks = ((long long)T * a.nchunk + 7) / 8;
   if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks, 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -23,137 +23,160 @@ fa_status check_rope(const fa_rope* r, int D, const int32_t* pos, int N, Rope* o
   return FA_OK;
 }
 
+// Queries or keys: one of them a CTA.
+struct NormSide {
+  const void* x;
+  const void* gy;      // backward: gradient of the output
+  long long row, head; // strides of x
+  const float* w;
+  void* y;             // y, or dx
+  int H;               // heads
+  int HC, nchunk;      // heads of one token that a warp takes, chunks of a token
+  bool vec;            // x starts every head on 16 bytes
+};
 struct NormArgs {
-  const void *q, *k;            // x
-  const void *gq, *gk;          // backward: gradients of the outputs
-  long long q_row, q_head, k_row, k_head;
-  const float *wq, *wk;
+  NormSide side[2];
+  int ctas_q;          // CTAs 0 .. ctas_q - 1 take queries, the rest keys
   float eps;
   const int32_t* pos;
   Rope rope;
-  int N, H, HT;                 // HT = H + Hkv
-  void *qo, *ko;                // y, or dx
-  int HC, nchunk;               // heads of one token that a lane group takes, chunks of a token
-  bool vecq, veck;              // rows of q / k start on 16 bytes
-  float* part;                  // backward: [CTA][2][D] sums of dw
+  int N;
+  float* part;         // backward: [CTA][D] sums of dw
 };
 
-// One lane group (D / 8 lanes) takes HC heads of one token: the rotation's factors are computed once
-// for them.
+// Rows that a lane group has under way at a time: 32 or 64 bytes a lane of x (and as much of gy).
+template <typename T>
+constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+
+// A warp takes HC heads of one token, D / 8 lanes a head: the rotation's factors are computed once for
+// them, and the loads of the next kRows heads are issued together.
 template <int D, typename TX, typename TY>
 __global__ void __launch_bounds__(256) k_norm_rope(const NormArgs a) {
-  constexpr int LG = D / 8, GW = 32 / LG;
-  const int lane = threadIdx.x & 31, lg = lane & (LG - 1), e0 = lg * 8;
-  const long long item = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * GW + lane / LG;
-  const bool live = item < (long long)a.N * a.nchunk;
-  const int n = live ? (int)(item / a.nchunk) : 0;
-  const int h0 = live ? (int)(item - (long long)n * a.nchunk) * a.HC : 0;
-  Turn8 t;
-  t.set(a.rope, live && a.rope.n_rot ? a.pos[n] : 0, e0);
-  for (int i = 0; i < a.HC; ++i) {
-    const int h = h0 + i;
-    const bool on = live && h < a.HT, isq = h < a.H;
-    float x[8] = {};
-    if (on) {
-      if (isq) load8(static_cast<const TX*>(a.q) + n * a.q_row + h * a.q_head + e0, a.vecq, x);
-      else load8(static_cast<const TX*>(a.k) + n * a.k_row + (h - a.H) * a.k_head + e0, a.veck, x);
-    }
-    float ss = 0.f;
+  constexpr int LG = D / 8, GW = 32 / LG, U = kRows<TX>;
+  const bool isq = blockIdx.x < a.ctas_q;
+  const NormSide& sd = a.side[isq ? 0 : 1];
+  const int lane = threadIdx.x & 31, grp = lane / LG, e0 = (lane & (LG - 1)) * 8;
+  const long long item = (long long)(blockIdx.x - (isq ? 0 : a.ctas_q)) * 8 + (threadIdx.x >> 5);
+  if (item >= (long long)a.N * sd.nchunk) return;
+  const int n = (int)(item / sd.nchunk), h0 = (int)(item - (long long)n * sd.nchunk) * sd.HC;
+  const int h1 = min(sd.H, h0 + sd.HC);
+  const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + e0;
+  TY* y0 = static_cast<TY*>(sd.y) + (long long)n * sd.H * D + e0;
+  float w[8];
+  if (sd.w) load8(sd.w + e0, false, w);
+  Turn8<D> t;
+  for (int h = h0 + grp, first = 1; h - grp < h1; h += U * GW, first = 0) {
+    Oct<TX> raw[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    ss = group_sum<LG>(ss);
-    const float* w = isq ? a.wq : a.wk;
-    if (on && w) {
-      const float r = inv_rms(ss, 1.f / D, a.eps);
-      float wv[8];
-      load8(w + e0, false, wv);
+    for (int u = 0; u < U; ++u)
+      if (h + u * GW < h1) load8_raw(x0 + (h + u * GW) * sd.head, sd.vec, raw[u]);
+    if (first) t.set(a.rope, a.rope.n_rot ? a.pos[n] : 0, e0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wv[j];
-    }
-    if (a.rope.n_rot) t.apply(x, a.rope.style, 1.f);
-    if (on) {
-      TY* y = isq ? static_cast<TY*>(a.qo) + ((long long)n * a.H + h) * D
-                  : static_cast<TY*>(a.ko) + ((long long)n * (a.HT - a.H) + (h - a.H)) * D;
-      store8(y + e0, x);
+    for (int u = 0; u < U; ++u) {
+      if (h - grp + u * GW >= h1) break;  // (the same in all lanes)
+      const bool on = h + u * GW < h1;
+      float x[8] = {};
+      if (on) unpack8(raw[u], x);
+      if (sd.w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+        const float r = inv_rms(group_sum<LG>(ss), 1.f / D, a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
+      }
+      if (a.rope.n_rot) t.apply(x, a.rope.style, 1.f);
+      if (on) store8(y0 + (h + u * GW) * D, x);
     }
   }
 }
 
+// The same shape, in a loop over the items; dw is summed by lane over all of them, then over the CTA's
+// lane groups in order.
 template <int D, typename TX, typename TY>
-__global__ void __launch_bounds__(256) k_norm_rope_back(const NormArgs a) {
-  constexpr int LG = D / 8, GW = 32 / LG, GC = 8 * GW;  // lane groups of a CTA
-  __shared__ float red[GC][2 * D];
-  const int lane = threadIdx.x & 31, lg = lane & (LG - 1), e0 = lg * 8;
-  const int grp = (threadIdx.x >> 5) * GW + lane / LG;
-  float dw[2][8] = {};
-  const long long items = (long long)a.N * a.nchunk, step = (long long)gridDim.x * GC;
-  const long long rounds = (items + step - 1) / step;
-  for (long long rd = 0; rd < rounds; ++rd) {
-    const long long item = rd * step + (long long)blockIdx.x * GC + grp;
-    const bool live = item < items;
-    const int n = live ? (int)(item / a.nchunk) : 0;
-    const int h0 = live ? (int)(item - (long long)n * a.nchunk) * a.HC : 0;
-    Turn8 t;
-    t.set(a.rope, live && a.rope.n_rot ? a.pos[n] : 0, e0);
-    for (int i = 0; i < a.HC; ++i) {
-      const int h = h0 + i;
-      const bool on = live && h < a.HT, isq = h < a.H;
-      const float* w = isq ? a.wq : a.wk;
-      float x[8] = {}, g[8] = {}, wv[8] = {};
-      const long long at = isq ? ((long long)n * a.H + h) * D : ((long long)n * (a.HT - a.H) + (h - a.H)) * D;
-      if (on) {
-        load8((isq ? static_cast<const TY*>(a.gq) : static_cast<const TY*>(a.gk)) + at + e0, true, g);
-        if (w) {
-          if (isq) load8(static_cast<const TX*>(a.q) + n * a.q_row + h * a.q_head + e0, a.vecq, x);
-          else load8(static_cast<const TX*>(a.k) + n * a.k_row + (h - a.H) * a.k_head + e0, a.veck, x);
-          load8(w + e0, false, wv);
-        }
-      }
-      if (a.rope.n_rot) t.apply(g, a.rope.style, -1.f);
-      float ss = 0.f, hx = 0.f;
+__global__ void __launch_bounds__(256, 2) k_norm_rope_back(const NormArgs a) {
+  constexpr int LG = D / 8, GW = 32 / LG, U = kRows<TX> < kRows<TY> ? kRows<TX> : kRows<TY>;
+  __shared__ float red[8 * GW][D];
+  const bool isq = blockIdx.x < a.ctas_q;
+  const NormSide& sd = a.side[isq ? 0 : 1];
+  const int lane = threadIdx.x & 31, grp = lane / LG, e0 = (lane & (LG - 1)) * 8, warp = threadIdx.x >> 5;
+  const long long items = (long long)a.N * sd.nchunk;
+  const int ctas = isq ? a.ctas_q : gridDim.x - a.ctas_q, cta = blockIdx.x - (isq ? 0 : a.ctas_q);
+  float w[8], dw[8] = {};
+  if (sd.w) load8(sd.w + e0, false, w);
+  for (long long item = (long long)cta * 8 + warp; item < items; item += (long long)ctas * 8) {
+    const int n = (int)(item / sd.nchunk), h0 = (int)(item - (long long)n * sd.nchunk) * sd.HC;
+    const int h1 = min(sd.H, h0 + sd.HC);
+    const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + e0;
+    const TY* g0 = static_cast<const TY*>(sd.gy) + (long long)n * sd.H * D + e0;
+    TX* d0 = static_cast<TX*>(sd.y) + (long long)n * sd.H * D + e0;
+    Turn8<D> t;
+    for (int h = h0 + grp, first = 1; h - grp < h1; h += U * GW, first = 0) {
+      Oct<TX> rx[U];
+      Oct<TY> rg[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss), hx = fmaf(g[j] * wv[j], x[j], hx);
-      ss = group_sum<LG>(ss);
-      hx = group_sum<LG>(hx);
-      if (on && w) {
-        const float r = inv_rms(ss, 1.f / D, a.eps);
-        const float m = hx * (1.f / D) * r * r;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = g[j] * x[j] * r;
-          if (isq) dw[0][j] += d;
-          else dw[1][j] += d;
-          g[j] = r * fmaf(-x[j], m, g[j] * wv[j]);
+      for (int u = 0; u < U; ++u)
+        if (h + u * GW < h1) {
+          load8_raw(g0 + (h + u * GW) * D, true, rg[u]);
+          if (sd.w) load8_raw(x0 + (h + u * GW) * sd.head, sd.vec, rx[u]);
         }
+      if (first) t.set(a.rope, a.rope.n_rot ? a.pos[n] : 0, e0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (h - grp + u * GW >= h1) break;  // (the same in all lanes)
+        const bool on = h + u * GW < h1;
+        float x[8] = {}, g[8] = {};
+        if (on) unpack8(rg[u], g);
+        if (a.rope.n_rot) t.apply(g, a.rope.style, -1.f);
+        if (sd.w) {
+          if (on) unpack8(rx[u], x);
+          float ss = 0.f, hx = 0.f, gx[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            gx[j] = g[j] * x[j];
+            ss = fmaf(x[j], x[j], ss), hx = fmaf(gx[j], w[j], hx);
+          }
+          ss = group_sum<LG>(ss);
+          hx = group_sum<LG>(hx);
+          const float r = inv_rms(ss, 1.f / D, a.eps), m = -hx * (1.f / D) * r * r * r;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (on) dw[j] = fmaf(gx[j], r, dw[j]);
+            g[j] = fmaf(g[j] * w[j], r, x[j] * m);
+          }
+        }
+        if (on) store8(d0 + (h + u * GW) * D, g);
       }
-      if (on) store8((isq ? static_cast<TX*>(a.qo) : static_cast<TX*>(a.ko)) + at + e0, g);
     }
   }
-  // the CTA's groups in order, one column a thread
+  if (!sd.w) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) red[grp][e0 + j] = dw[0][j], red[grp][D + e0 + j] = dw[1][j];
+  for (int j = 0; j < 8; ++j) red[warp * GW + grp][e0 + j] = dw[j];
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += 256) {
+  for (int c = threadIdx.x; c < D; c += 256) {
     float s = 0.f;
-    for (int g = 0; g < GC; ++g) s += red[g][c];
-    a.part[(long long)blockIdx.x * 2 * D + c] = s;
+#pragma unroll
+    for (int g = 0; g < 8 * GW; ++g) s += red[g][c];
+    a.part[(long long)blockIdx.x * D + c] = s;
   }
 }
 
-// dw[c] = the CTAs' sums in a fixed order: 32 columns a CTA, each split over 32 rows of threads.
-__global__ void __launch_bounds__(1024) k_dw_reduce(const float* part, int nblk, int D, float* dwq, float* dwk) {
+// dw = the CTAs' sums in a fixed order: 32 columns a CTA, each split over 32 rows of threads.  blockIdx.y 0:
+// queries, 1: keys.
+__global__ void __launch_bounds__(1024) k_dw_reduce(const float* part, int ctas_q, int ctas, int D, float* dwq, float* dwk) {
   __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int c = blockIdx.x * 32 + threadIdx.x, b0 = blockIdx.y ? ctas_q : 0, b1 = blockIdx.y ? ctas : ctas_q;
+  float* out = blockIdx.y ? dwk : dwq;
+  if (!out) return;
   float s = 0.f;
-  for (int b = threadIdx.y; b < nblk; b += 32) s += part[(long long)b * 2 * D + c];
+  for (int b = b0 + threadIdx.y; b < b1; b += 32) s += part[(long long)b * D + c];
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0) {
     s = 0.f;
 #pragma unroll
     for (int y = 0; y < 32; ++y) s += red[y][threadIdx.x];
-    float* out = c < D ? dwq : dwk;
-    if (out) out[c < D ? c : c - D] = s;
+    out[c] = s;
   }
 }
 
@@ -202,21 +225,29 @@ static fa_status norm_args(const void* q, const void* k, int x_type, const fa_qk
   *a = z;
   const fa_status rc = check_rope(rope, D, pos, N, &a->rope);
   if (rc != FA_OK) return rc;
-  a->q = q, a->k = k, a->q_row = v.q_row, a->q_head = v.q_head, a->k_row = v.k_row, a->k_head = v.k_head;
-  a->wq = wq, a->wk = wk, a->eps = eps, a->pos = pos, a->N = N, a->H = H, a->HT = H + Hkv;
-  a->vecq = rows_on_16(q, v.q_row, v.q_head, es), a->veck = rows_on_16(k, v.k_row, v.k_head, es);
+  NormSide& sq = a->side[0];
+  NormSide& sk = a->side[1];
+  sq.x = q, sq.row = v.q_row, sq.head = v.q_head, sq.w = wq, sq.H = H, sq.vec = rows_on_16(q, v.q_row, v.q_head, es);
+  sk.x = k, sk.row = v.k_row, sk.head = v.k_head, sk.w = wk, sk.H = Hkv, sk.vec = rows_on_16(k, v.k_row, v.k_head, es);
+  a->eps = eps, a->pos = pos, a->N = N;
   return FA_OK;
 }
 
-// Heads of a token that one lane group takes: enough to share the rotation's factors, few enough
-// that every SM has warps.
-static void chunk_heads(NormArgs* a, int D, int nsm) {
-  const long long want = 16LL * nsm * (256 / D);  // lane groups: two CTAs' worth of warps an SM
-  long long hc = (long long)a->N * a->HT / want;
-  hc = std::max(1LL, std::min<long long>(hc, a->HT));
-  a->nchunk = (int)((a->HT + hc - 1) / hc);
-  a->HC = (a->HT + a->nchunk - 1) / a->nchunk;
-  a->nchunk = (a->HT + a->HC - 1) / a->HC;
+// Heads of a token that one warp takes: `most` where there are tokens enough to fill the card with warps
+// of that, else fewer, down to the heads that lie side by side in a warp.
+static void chunk_heads(NormArgs* a, int D, int nsm, int most) {
+  const int side = 256 / D;  // heads side by side
+  const long long rows = (long long)a->N * (a->side[0].H + a->side[1].H) / (16LL * nsm * side);
+  for (NormSide& s : a->side) {
+    if (s.H == 0) {
+      s.HC = 1, s.nchunk = 0;
+      continue;
+    }
+    const int hc = (int)std::max(1LL, std::min<long long>(rows, most / side)) * side;
+    s.nchunk = (s.H + hc - 1) / hc;
+    s.HC = ((s.H + s.nchunk - 1) / s.nchunk + side - 1) / side * side;
+    s.nchunk = (s.H + s.HC - 1) / s.HC;
+  }
 }
 
 static int back_ctas(int nsm) { return 2 * nsm; }
@@ -253,11 +284,12 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, c
   int nsm = 0, *err = nullptr;
   if ((rc = fab_device(&nsm, &err)) != FA_OK) return rc;
   if (N == 0) return FA_OK;
-  a.qo = q_out, a.ko = k_out;
-  chunk_heads(&a, D, nsm);
-  const long long per = 8 * (256 / D), blocks = ((long long)N * a.nchunk + per - 1) / per;
-  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  pick_norm(false, D, x_type, y_type)<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.side[0].y = q_out, a.side[1].y = k_out;
+  chunk_heads(&a, D, nsm, 16);
+  const long long bq = ((long long)N * a.side[0].nchunk + 7) / 8, bk = ((long long)N * a.side[1].nchunk + 7) / 8;
+  if (bq + bk > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  a.ctas_q = (int)bq;
+  pick_norm(false, D, x_type, y_type)<<<(unsigned)(bq + bk), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -265,7 +297,7 @@ extern "C" size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv,
   if (N < 0 || H < 1 || Hkv < 0 || !head_size(D)) return 0;
   int nsm = 0, *err = nullptr;
   if (fab_device(&nsm, &err) != FA_OK) nsm = 152;
-  return (size_t)back_ctas(nsm) * 2 * D * sizeof(float);
+  return (size_t)back_ctas(nsm) * D * sizeof(float);
 }
 
 extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, int y_type, const void* q, const void* k,
@@ -281,17 +313,22 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
     return FA_ERR_ALIGN;
   int nsm = 0, *err = nullptr;
   if ((rc = fab_device(&nsm, &err)) != FA_OK) return rc;
-  if (!workspace || workspace_bytes < (size_t)back_ctas(nsm) * 2 * D * sizeof(float)) return FA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < (size_t)back_ctas(nsm) * D * sizeof(float)) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
-  a.gq = gq, a.gk = gk, a.qo = dq, a.ko = dk;
+  a.side[0].gy = gq, a.side[1].gy = gk, a.side[0].y = dq, a.side[1].y = dk;
   a.part = static_cast<float*>(workspace);
-  chunk_heads(&a, D, nsm);
-  const long long per = 8 * (256 / D), want = ((long long)N * a.nchunk + per - 1) / per;
-  const int blocks = (int)std::max(1LL, std::min<long long>(want, back_ctas(nsm)));
+  chunk_heads(&a, D, nsm, 8);
+  // CTAs shared out by the heads of either side; every side that has heads gets one
+  const long long iq = (long long)N * a.side[0].nchunk, ik = (long long)N * a.side[1].nchunk;
+  const int all = back_ctas(nsm);
+  int ck = Hkv ? (int)std::min<long long>(std::max(1LL, (long long)all * Hkv / (H + Hkv)), std::max(1LL, (ik + 7) / 8)) : 0;
+  const int cq = (int)std::min<long long>(all - ck, std::max(1LL, (iq + 7) / 8));
+  a.ctas_q = cq;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  pick_norm(true, D, x_type, y_type)<<<blocks, 256, 0, s>>>(a);
+  pick_norm(true, D, x_type, y_type)<<<cq + ck, 256, 0, s>>>(a);
   float* oq = wq ? dwq : nullptr;
-  float* ok = wk ? dwk : nullptr;
-  if (oq || ok) k_dw_reduce<<<2 * D / 32, dim3(32, 32), 0, s>>>(a.part, blocks, D, oq, ok);
+  float* ok = wk && Hkv ? dwk : nullptr;
+  if (oq || ok) k_dw_reduce<<<dim3(D / 32, 2), dim3(32, 32), 0, s>>>(a.part, cq, cq + ck, D, oq, ok);
+  if (wk && !Hkv && dwk) cudaMemsetAsync(dwk, 0, D * sizeof(float), s);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -37,18 +37,26 @@ struct alignas(16) Oct {
 
 // vec: p is 16-byte aligned (warp-uniform); otherwise element by element
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
+__device__ __forceinline__ void load8_raw(const T* p, bool vec, Oct<T>& o) {
   if (vec) {
-    Oct<T> o;
     constexpr int n = sizeof(Oct<T>) / 16;
 #pragma unroll
     for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(&o)[i] = reinterpret_cast<const uint4*>(p)[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(o.v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(p[i]);
+    for (int i = 0; i < 8; ++i) o.v[i] = p[i];
   }
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Oct<T>& o, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = to_f32(o.v[i]);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
+  Oct<T> o;
+  load8_raw(p, vec, o);
+  unpack8(o, x);
 }
 
 template <typename T>
@@ -69,50 +77,58 @@ struct Rope {
   int n_rot, style;
 };
 
-// Factors of a lane's eight elements e0 .. e0+7: y[i] = x[i] c[i] + partner[i] s[i], the sign of the
-// pair's first / second member in s.  The angle is pos * freq modulo 2^64 in units of 2^-64 turns:
-// the wrap of the integer product is the reduction modulo one turn, with no rounding, so the
-// error is that of the 32 bits kept (1.5e-9 rad) and of sincospi, at every position.
+// A warp that holds heads of one token: D / 8 lanes a head, so 256 / D heads side by side.  Factors of a
+// lane's eight elements e0 .. e0+7: y[i] = x[i] c[i] + partner[i] s[i], the sign of the pair's first /
+// second member in s.  The angle is pos * freq modulo 2^64 in units of 2^-64 turns: the wrap of the
+// integer product is the reduction modulo one turn, with no rounding, so the error is that of the 32
+// bits kept (1.5e-9 rad) and of sincospi, at every position.  The token's n_rot / 2 <= D / 2 angles are
+// shared out over the lanes, D / 64 neighbouring ones each, and handed round by shuffles.
+template <int D>
 struct Turn8 {
   float c[8], s[8];
-  int lane_off;  // partner lane (FA_ROPE_HALVES), relative
+  int src;  // partner lane (FA_ROPE_HALVES)
 
+  // All lanes of the warp take part; pos is the same in all.
   __device__ __forceinline__ void set(const Rope& r, int pos, int e0) {
+    constexpr int P = D / 64;
+    const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
+    src = lane;
+    if (half == 0) return;
+    float cs[P], sn[P];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-    lane_off = 0;
-    if (e0 >= r.n_rot) return;
-    const int half = r.n_rot >> 1;
+    for (int i = 0; i < P; ++i) {
+      cs[i] = 1.f, sn[i] = 0.f;
+      const int p = lane * P + i;
+      if (p < half) {
+        const uint64_t a = (uint64_t)(int64_t)pos * r.freqs[p];
+        sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+      }
+    }
+    const bool in = e0 < r.n_rot;
     if (r.style == FA_ROPE_HALVES) {  // n_rot % 16 == 0: a lane lies in one half
       const bool second = e0 >= half;
-      const int p0 = second ? e0 - half : e0;
-      lane_off = second ? -(half >> 3) : half >> 3;
+      const int p0 = !in ? 0 : second ? e0 - half : e0;
+      if (in) src = lane + (second ? -(half >> 3) : half >> 3);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float sn;
-        angle(r.freqs[p0 + i], pos, sn, c[i]);
-        s[i] = second ? sn : -sn;
+        const float ci = __shfl_sync(kFull, cs[i % P], (p0 + i) / P), si = __shfl_sync(kFull, sn[i % P], (p0 + i) / P);
+        c[i] = in ? ci : 1.f;
+        s[i] = !in ? 0.f : second ? si : -si;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        if (e0 + i >= r.n_rot) break;  // n_rot is even, not always a multiple of 8
-        float sn, cs;
-        angle(r.freqs[(e0 + i) >> 1], pos, sn, cs);
-        c[i] = c[i + 1] = cs;
-        s[i] = -sn, s[i + 1] = sn;
+      for (int i = 0; i < 4; ++i) {
+        const int p = (e0 >> 1) + i;
+        const float ci = __shfl_sync(kFull, cs[i % P], p / P), si = __shfl_sync(kFull, sn[i % P], p / P);
+        c[2 * i] = c[2 * i + 1] = p < half ? ci : 1.f;
+        s[2 * i] = p < half ? -si : 0.f, s[2 * i + 1] = -s[2 * i];
       }
     }
-  }
-  static __device__ __forceinline__ void angle(uint64_t f, int pos, float& sn, float& cs) {
-    const uint64_t a = (uint64_t)(int64_t)pos * f;
-    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
   }
   // sign +1: rotate; -1: rotate back (the transpose).  All lanes of the warp take part.
   __device__ __forceinline__ void apply(float (&x)[8], int style, float sign) const {
     float p[8];
     if (style == FA_ROPE_HALVES) {
-      const int src = (threadIdx.x & 31) + lane_off;
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(kFull, x[i], src);
     } else {
