@@ -149,8 +149,8 @@ template <int D, typename TX, bool IS_K>
 __device__ __forceinline__ void append_rows(const RowArgs& a) {
   constexpr int LG = D / 8, GW = 32 / LG, U = sizeof(TX) == 2 ? 4 : 2;
   const int lane = threadIdx.x & 31, grp = lane / LG, e0 = (lane & (LG - 1)) * 8;
-  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(item / a.nchunk), h0 = (int)(item - (long long)t * a.nchunk) * a.HC;
+  const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const int t = item / (unsigned)a.nchunk, h0 = (int)(item - (unsigned)t * a.nchunk) * a.HC;
   if (t >= a.T) return;
   const int h1 = min(a.c.Hkv, h0 + a.HC), b = a.seq[t], pos = a.pos[t];
   const bool vec = IS_K ? a.veck : a.vecv;
@@ -171,7 +171,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
       const long long row = cache_row(a.c, b, pos);
       if (row < 0) return;
       cell = (IS_K ? a.c.k : a.c.v) + row * a.c.Hkv * (long long)rb;
-      if (IS_K) turn.set(a.rope, pos, e0);
+      if (IS_K) turn.set(a.rope, pos, e0, 1.f);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -188,7 +188,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
         }
-        if (a.rope.n_rot) turn.apply(x, a.rope.style, 1.f);
+        if (a.rope.n_rot) turn.apply(x, a.rope.style);
       }
       store_row8(cell + (on ? h + u * GW : 0) * (long long)rb, type, e0, x, on);
     }
@@ -332,7 +332,7 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
   a.HC = (int)std::max<long long>(side, std::min<long long>(hc, 16));
   a.nchunk = (a.c.Hkv + a.HC - 1) / a.HC;
   const long long blocks = ((long long)T * a.nchunk + 7) / 8;
-  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if (blocks > 0x0fffffffLL) return FA_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks, 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (x_type == FA_ACT_F32) k_cache_append<float><<<grid, 256, 0, s>>>(a);

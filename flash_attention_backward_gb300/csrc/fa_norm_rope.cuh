@@ -1,0 +1,311 @@
+// Queries and keys of a layer, head by head: RMS norm and position rotation in one pass, and the
+// gradient.
+//
+//   y = R (w o x r),  r = rsqrt(mean(x^2) + eps)
+//   g = R^T gy,  dw = sum g o x r,  h = g o w,  dx = r (h - x r^2 mean(h o x))
+//
+// Both are bound by memory: a head is read once and written once (backward: x and gy read, dx written),
+// everything between stays in registers.  The arithmetic has to stay out of the way, though: a head of
+// 128 bf16 components is 256 bytes, so an SM takes one every ten cycles at the card's bandwidth.  Hence
+// the layout: D / 8 lanes a head, and a lane holds both members of its four rotation pairs, which makes
+// the rotation free of shuffles; packed pairs of f32 (fma.rn.f32x2) halve the instructions; the angles of a
+// token are computed once for all heads of it that a warp takes.
+#pragma once
+#include "fa_paged.cuh"
+
+namespace fap {
+
+struct NormSide {  // queries or keys
+  const void* x;
+  const void* gy;      // backward: gradient of the output
+  long long row, head; // strides of x
+  const float* w;
+  void* y;             // y, or dx
+  int H;               // heads
+  int HC, nchunk;      // backward: heads of one token that a warp takes, chunks of a token
+};
+struct NormArgs {
+  NormSide side[2];
+  int HC, nchunk;      // forward: heads (queries', then keys') of one token that a warp takes, chunks of a token
+  int ctas_q;          // backward: CTAs 0 .. ctas_q - 1 take queries, the rest keys
+  float eps;
+  const int32_t* pos;
+  Rope rope;
+  int N;
+  bool vec;            // both start every head of x on 16 bytes (or have none)
+  float* part;         // backward: [CTA][D] sums of dw
+};
+
+// Rows that a lane group has under way at a time: 32 or 64 bytes a lane of x (and as much of gy).
+template <typename T>
+constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+#ifndef FA_BC
+#define FA_BC 2
+#define FA_BR 2
+#define FA_BM 16
+#endif
+constexpr int kBackRows = FA_BR, kBackCtas = FA_BC, kBackHeads = FA_BM;
+
+// A lane's four rotation pairs: components [ea, ea + 4) and [eb, eb + 4) of the head.
+//   FA_ROPE_HALVES  pair i is (x[ea + i], x[eb + i]).  The rotated components are pairs 0 .. n_rot / 2 - 1
+//                   (i, i + n_rot / 2); the others pair up likewise and turn by nothing (n_rot % 16 == 0:
+//                   a lane's pairs are all of one kind).
+//   FA_ROPE_PAIRS   eight neighbouring components, pair i is (x[ea + 2i], x[ea + 2i + 1]).
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T v[4];
+};
+template <typename T>
+struct Eight {
+  Four<T> a, b;
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_eight(const T* p, int ea, int eb, Eight<T>& o) {
+  if (VEC) {
+    o.a = *reinterpret_cast<const Four<T>*>(p + ea);
+    o.b = *reinterpret_cast<const Four<T>*>(p + eb);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.a.v[i] = p[ea + i], o.b.v[i] = p[eb + i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack_eight(const Eight<T>& o, float2 (&x)[4]) {
+  x[0] = make_float2(to_f32(o.a.v[0]), to_f32(o.a.v[1])), x[1] = make_float2(to_f32(o.a.v[2]), to_f32(o.a.v[3]));
+  x[2] = make_float2(to_f32(o.b.v[0]), to_f32(o.b.v[1])), x[3] = make_float2(to_f32(o.b.v[2]), to_f32(o.b.v[3]));
+}
+template <typename T>
+__device__ __forceinline__ void store_eight(T* p, int ea, int eb, const float2 (&x)[4]) {
+  Four<T> a, b;
+  a.v[0] = from_f32<T>(x[0].x), a.v[1] = from_f32<T>(x[0].y), a.v[2] = from_f32<T>(x[1].x), a.v[3] = from_f32<T>(x[1].y);
+  b.v[0] = from_f32<T>(x[2].x), b.v[1] = from_f32<T>(x[2].y), b.v[2] = from_f32<T>(x[3].x), b.v[3] = from_f32<T>(x[3].y);
+  *reinterpret_cast<Four<T>*>(p + ea) = a;
+  *reinterpret_cast<Four<T>*>(p + eb) = b;
+}
+
+// What a lane keeps for a token: its components, the norm's weights, the factors of its pairs.
+template <int D, int STYLE>
+struct Lane {
+  int ea, eb;
+  bool norm;
+  float2 w[4];
+  float2 c[2], s[2], ns[2];  // cos, sin, -sin of pairs (0, 1) and (2, 3)
+
+  __device__ __forceinline__ void place(const Rope& r) {
+    const int p = (threadIdx.x & (D / 8 - 1)) * 4, half = r.n_rot >> 1;
+    if (STYLE == FA_ROPE_PAIRS) ea = 2 * p, eb = ea + 4;
+    else if (p < half) ea = p, eb = p + half;
+    else ea = r.n_rot + (p - half), eb = ea + (D - r.n_rot) / 2;
+  }
+  __device__ __forceinline__ void weights(const float* weight) {
+    norm = weight != nullptr;
+    if (norm) {
+      Eight<float> o;
+      load_eight<float, false>(weight, ea, eb, o);
+      unpack_eight(o, w);
+    }
+  }
+  // The factors at a position; sign -1 turns back (the transpose).  The angle is pos * freq modulo 2^64
+  // in units of 2^-64 turns: the wrap of the integer product is the reduction modulo one turn, with no
+  // rounding, so the error is that of the 32 bits kept (1.5e-9 rad) and of sincospi, at every position.
+  // The token's D / 2 pairs are shared out over the warp's lanes, D / 64 neighbouring ones each.
+  __device__ __forceinline__ void turn(const Rope& r, int pos, float sign) {
+    constexpr int P = D / 64;
+    const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
+    float cs[P], sn[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      cs[i] = 1.f, sn[i] = 0.f;
+      if (lane * P + i < half) {
+        const uint64_t a = (uint64_t)(int64_t)pos * r.freqs[lane * P + i];
+        sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+        sn[i] *= sign;
+      }
+    }
+    const int p = (lane & (D / 8 - 1)) * 4;
+    float cc[4], ss[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cc[i] = P == 4 ? cs[i % P] : __shfl_sync(kFull, cs[i % P], (p + i) / P);  // (D = 256: the lane's own)
+      ss[i] = P == 4 ? sn[i % P] : __shfl_sync(kFull, sn[i % P], (p + i) / P);
+    }
+    c[0] = make_float2(cc[0], cc[1]), c[1] = make_float2(cc[2], cc[3]);
+    s[0] = make_float2(ss[0], ss[1]), s[1] = make_float2(ss[2], ss[3]);
+    ns[0] = make_float2(-ss[0], -ss[1]), ns[1] = make_float2(-ss[2], -ss[3]);
+  }
+  __device__ __forceinline__ void rotate(float2 (&x)[4]) const {
+    if (STYLE == FA_ROPE_HALVES) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = x[i], b = x[2 + i];
+        x[i] = __ffma2_rn(b, ns[i], __fmul2_rn(a, c[i]));
+        x[2 + i] = __ffma2_rn(a, s[i], __fmul2_rn(b, c[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ci = i & 1 ? c[i >> 1].y : c[i >> 1].x, si = i & 1 ? s[i >> 1].y : s[i >> 1].x, ni = i & 1 ? ns[i >> 1].y : ns[i >> 1].x;
+        const float a = x[i].x, b = x[i].y;
+        x[i].x = fmaf(b, ni, a * ci);
+        x[i].y = fmaf(a, si, b * ci);
+      }
+    }
+  }
+  __device__ __forceinline__ void forward(float2 (&x)[4], float eps) const {
+    if (norm) {
+      float2 q = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) q = __ffma2_rn(x[i], x[i], q);
+      const float r = inv_rms(group_sum<D / 8>(q.x + q.y), 1.f / D, eps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __fmul2_rn(__fmul2_rn(x[i], make_float2(r, r)), w[i]);
+    }
+    rotate(x);
+  }
+  // g: gradient of the output, becomes dx.  on: the lane's head counts
+  __device__ __forceinline__ void backward(const float2 (&x)[4], float2 (&g)[4], float2 (&dw)[4], float eps, bool on) const {
+    rotate(g);
+    if (!norm) return;
+    float2 gx[4], q = make_float2(0.f, 0.f), z = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      gx[i] = __fmul2_rn(g[i], x[i]);
+      q = __ffma2_rn(x[i], x[i], q);
+      z = __ffma2_rn(gx[i], w[i], z);
+    }
+    const float ss = group_sum<D / 8>(q.x + q.y), hx = group_sum<D / 8>(z.x + z.y);
+    const float r = inv_rms(ss, 1.f / D, eps), m = -hx * (1.f / D) * r * r;
+    const float rd = on ? r : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dw[i] = __ffma2_rn(gx[i], make_float2(rd, rd), dw[i]);
+      g[i] = __fmul2_rn(make_float2(r, r), __ffma2_rn(x[i], make_float2(m, m), __fmul2_rn(g[i], w[i])));
+    }
+  }
+};
+
+// A warp takes HC heads of one token, 256 / D side by side, and loads the next kRows of each together.
+// VEC: every head of x starts on 16 bytes (else it is loaded element by element).  Lanes without a head
+// of their own (the last ones of a token) work on the last head and store nothing.
+template <int D, typename TX, typename TY, bool VEC, int STYLE>
+__global__ void __launch_bounds__(256) k_norm_rope(const NormArgs a) {
+  constexpr int GW = 256 / D, U = kRows<TX>;
+  const int grp = (threadIdx.x & 31) / (D / 8);
+  const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const int n = item / (unsigned)a.nchunk, c0 = (int)(item - (unsigned)n * a.nchunk) * a.HC;
+  if (n >= a.N) return;
+  Lane<D, STYLE> ln;
+  ln.place(a.rope);
+  bool turned = false;
+  for (int k = 0; k < 2; ++k) {
+    const NormSide& sd = a.side[k];
+    const int first = k ? a.side[0].H : 0;  // the side's first head among all
+    const int h0 = max(c0 - first, 0);
+    int left = min(sd.H, c0 + a.HC - first) - h0;  // heads that the warp still has
+    if (left <= 0) continue;
+    const long long head = sd.head;
+    const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + h0 * head;
+    TY* y0 = static_cast<TY*>(sd.y) + ((long long)n * sd.H + h0 + grp) * D;
+    Eight<TX> raw[U];
+    auto fetch = [&] {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * GW < left) load_eight<TX, VEC>(x0 + min(grp + u * GW, left - 1) * head, ln.ea, ln.eb, raw[u]);
+    };
+    fetch();
+    ln.weights(sd.w);
+    if (!turned) ln.turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, 1.f);
+    turned = true;
+    for (;;) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * GW >= left) break;  // (the same in all lanes)
+        float2 x[4];
+        unpack_eight(raw[u], x);
+        ln.forward(x, a.eps);
+        if (grp + u * GW < left) store_eight(y0 + u * GW * D, ln.ea, ln.eb, x);
+      }
+      left -= U * GW;
+      if (left <= 0) break;
+      x0 += U * GW * head, y0 += U * GW * D;
+      fetch();
+    }
+  }
+}
+
+// The same shape, in a loop over the items; dw is summed by lane over all of them, then over the CTA's
+// lane groups in order.
+template <int D, typename TX, typename TY, bool VEC, int STYLE>
+__global__ void __launch_bounds__(256, kBackCtas) k_norm_rope_back(const NormArgs a) {
+  constexpr int GW = 256 / D, U = kBackRows;
+  __shared__ float red[8 * GW][D];
+  const bool isq = blockIdx.x < a.ctas_q;
+  const NormSide sd = a.side[isq ? 0 : 1];
+  const int grp = (threadIdx.x & 31) / (D / 8), warp = threadIdx.x >> 5;
+  const unsigned items = (unsigned)a.N * sd.nchunk;
+  const int ctas = isq ? a.ctas_q : gridDim.x - a.ctas_q, cta = blockIdx.x - (isq ? 0 : a.ctas_q);
+  float2 dw[4] = {};
+  Lane<D, STYLE> ln;
+  ln.place(a.rope);
+  ln.weights(sd.w);
+  for (unsigned item = cta * 8 + warp; item < items; item += ctas * 8) {
+    const int n = item / (unsigned)sd.nchunk, h0 = (int)(item - (unsigned)n * sd.nchunk) * sd.HC;
+    int left = min(sd.H - h0, sd.HC);
+    const long long at = ((long long)n * sd.H + h0) * D;
+    const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + h0 * sd.head;
+    const TY* g0 = static_cast<const TY*>(sd.gy) + at;
+    TX* d0 = static_cast<TX*>(sd.y) + at + grp * D;
+    Eight<TX> rx[U];
+    Eight<TY> rg[U];
+    auto fetch = [&] {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * GW < left) {
+          const int h = min(grp + u * GW, left - 1);
+          load_eight<TY, true>(g0 + h * D, ln.ea, ln.eb, rg[u]);
+          if (ln.norm) load_eight<TX, VEC>(x0 + h * sd.head, ln.ea, ln.eb, rx[u]);
+        }
+    };
+    fetch();
+    ln.turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, -1.f);
+    for (;;) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * GW >= left) break;  // (the same in all lanes)
+        const bool on = grp + u * GW < left;
+        float2 x[4], g[4];
+        unpack_eight(rg[u], g);
+        unpack_eight(rx[u], x);
+        ln.backward(x, g, dw, a.eps, on);
+        if (on) store_eight(d0 + u * GW * D, ln.ea, ln.eb, g);
+      }
+      left -= U * GW;
+      if (left <= 0) break;
+      x0 += U * GW * sd.head, g0 += U * GW * D, d0 += U * GW * D;
+      fetch();
+    }
+  }
+  if (!ln.norm) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float* ra = &red[warp * GW + grp][ln.ea + 2 * i];
+    float* rb = &red[warp * GW + grp][ln.eb + 2 * i];
+    ra[0] = dw[i].x, ra[1] = dw[i].y, rb[0] = dw[2 + i].x, rb[1] = dw[2 + i].y;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < D; c += 256) {
+    float s = 0.f;
+#pragma unroll
+    for (int g = 0; g < 8 * GW; ++g) s += red[g][c];
+    a.part[(long long)blockIdx.x * D + c] = s;
+  }
+}
+
+typedef void (*NormKernel)(const NormArgs);
+
+// The kernel for these types (fa_norm_rope_fwd.cu, fa_norm_rope_back.cu)
+NormKernel pick_norm_fwd(int D, int tx, int ty, bool vec, int style);
+NormKernel pick_norm_back(int D, int tx, int ty, bool vec, int style);
+
+}  // namespace fap

@@ -88,8 +88,8 @@ struct Turn8 {
   float c[8], s[8];
   int src;  // partner lane (FA_ROPE_HALVES)
 
-  // All lanes of the warp take part; pos is the same in all.
-  __device__ __forceinline__ void set(const Rope& r, int pos, int e0) {
+  // All lanes of the warp take part; pos is the same in all.  sign +1: rotate; -1: back (the transpose).
+  __device__ __forceinline__ void set(const Rope& r, int pos, int e0, float sign) {
     constexpr int P = D / 64;
     const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
     src = lane;
@@ -102,6 +102,7 @@ struct Turn8 {
       if (p < half) {
         const uint64_t a = (uint64_t)(int64_t)pos * r.freqs[p];
         sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+        sn[i] *= sign;
       }
     }
     const bool in = e0 < r.n_rot;
@@ -125,8 +126,8 @@ struct Turn8 {
       }
     }
   }
-  // sign +1: rotate; -1: rotate back (the transpose).  All lanes of the warp take part.
-  __device__ __forceinline__ void apply(float (&x)[8], int style, float sign) const {
+  // All lanes of the warp take part.
+  __device__ __forceinline__ void apply(float (&x)[8], int style) const {
     float p[8];
     if (style == FA_ROPE_HALVES) {
 #pragma unroll
@@ -136,7 +137,7 @@ struct Turn8 {
       for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(p[i], sign * s[i], x[i] * c[i]);
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(p[i], s[i], x[i] * c[i]);
   }
 };
 
