@@ -258,45 +258,42 @@ def fa_back_test_wait_limit(limit_ns: int) -> int:
     return int(lib().fa_back_test_wait_limit(limit_ns))
 
 
-# ---- fa_paged.h: structures are passed by reference (None: a NULL pointer)
-
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
-
+# ---- fa_paged.h.  Structures (or None for a NULL pointer) go where the header takes pointers to them:
+# ctypes passes their address.
 
 def fa_rope_frequencies(n_rot: int, base: float, scale: float, factors, out) -> int:
     """factors, out: host addresses (float32 and uint64 arrays of n_rot / 2) or None."""
-    return int(lib().fa_rope_frequencies(n_rot, base, scale, factors, out))
+    return lib().fa_rope_frequencies(n_rot, base, scale, factors, out)
 
 
 def fa_qk_norm_rope(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, q_out, k_out, y_type, stream) -> int:
-    return lib().fa_qk_norm_rope(q, k, x_type, _ref(views), wq, wk, eps, pos, _ref(rope), N, H, Hkv, D, q_out, k_out,
-                                 y_type, stream)
+    return (_lib or lib()).fa_qk_norm_rope(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, q_out, k_out,
+                                           y_type, stream)
 
 
 def fa_qk_norm_rope_backward_workspace_size(N: int, H: int, Hkv: int, D: int) -> int:
-    return lib().fa_qk_norm_rope_backward_workspace_size(N, H, Hkv, D)
+    return (_lib or lib()).fa_qk_norm_rope_backward_workspace_size(N, H, Hkv, D)
 
 
 def fa_qk_norm_rope_backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, dq, dk, dwq,
                              dwk, workspace, workspace_bytes, stream) -> int:
-    return lib().fa_qk_norm_rope_backward(gq, gk, y_type, q, k, x_type, _ref(views), wq, wk, eps, pos, _ref(rope), N, H,
-                                          Hkv, D, dq, dk, dwq, dwk, workspace, workspace_bytes, stream)
+    return (_lib or lib()).fa_qk_norm_rope_backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, rope, N, H,
+                                                    Hkv, D, dq, dk, dwq, dwk, workspace, workspace_bytes, stream)
 
 
 def fa_cache_append(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, rope, stream) -> int:
-    return lib().fa_cache_append(k, v, x_type, _ref(views), _ref(cache), seq, pos, T, k_norm, eps, _ref(rope), stream)
+    return (_lib or lib()).fa_cache_append(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, rope, stream)
 
 
 def fa_cache_read(cache, seq, pos, T, y_type, k_out, v_out, stream) -> int:
-    return lib().fa_cache_read(_ref(cache), seq, pos, T, y_type, k_out, v_out, stream)
+    return (_lib or lib()).fa_cache_read(cache, seq, pos, T, y_type, k_out, v_out, stream)
 
 
 def fa_paged_decode_workspace_size(cache, H: int) -> int:
-    return lib().fa_paged_decode_workspace_size(_ref(cache), H)
+    return (_lib or lib()).fa_paged_decode_workspace_size(cache, H)
 
 
 def fa_paged_decode(q, act, q_row, q_head, cache, seq_lens, H, scale, alibi_slopes, softcap, sinks, O, lse, workspace,
                     workspace_bytes, stream) -> int:
-    return lib().fa_paged_decode(q, act, q_row, q_head, _ref(cache), seq_lens, H, scale, alibi_slopes, softcap, sinks, O,
-                                 lse, workspace, workspace_bytes, stream)
+    return (_lib or lib()).fa_paged_decode(q, act, q_row, q_head, cache, seq_lens, H, scale, alibi_slopes, softcap,
+                                           sinks, O, lse, workspace, workspace_bytes, stream)

@@ -39,45 +39,57 @@ struct RowArgs {
 // ------------------------------------------------------------------------------------------------
 // block quantisers: four neighbouring lanes hold a block of 32, eight elements each.
 //
-// A code is the nearest integer to x / d (q8_0: d = amax / 127, ties away from zero; q4_0: d = m / -8,
-// ties up).  x * (1 / d) is off by about 2^-23 of itself, so where it falls within 2^-12 of a border
-// between two codes the decision is taken again on exact products: 127 |x| against (n + 1/2) amax,
-// or -8 x against (k - 1/2) m, each product as the f32 pair that fma gives.
+// A code is the nearest integer to y = x / d (q8_0: d = amax / 127, ties away from zero; q4_0: d = m / -8,
+// ties up).  Adding 1.5 * 2^23 to x * (1 / d) rounds it to the nearest integer, which is then in the
+// sum's low bits; the remainder x * (1 / d) - n says how near a border it was.  The product is off by
+// about 2^-23 of itself, so within 2^-12 of a border between two codes the decision is taken again, out
+// of line, on exact products: 127 |x| against (n + 1/2) amax, or -8 x against (k - 1/2) m, each product
+// as the f32 pair that fma gives.
+
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+constexpr float kNearBorder = 0.5f - 0x1p-12f;
+constexpr float kTiny = 1e-30f;       // below this the binary16 scale is zero, whatever the codes
 
 __device__ __forceinline__ float prod_diff(float a, float b, float c, float d) {  // a b - c d
   const float p = a * b, q = c * d;
   return (p - q) + (fmaf(a, b, -p) - fmaf(c, d, -q));
 }
-
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
-  return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+// The code of x near a border, plus kMagic
+static __device__ __noinline__ float q8_border(float x, float inv, float am) {
+  const float n = floorf(fabsf(x) * inv);
+  return kMagic + copysignf(prod_diff(127.f, fabsf(x), n + 0.5f, am) >= 0.f ? n + 1.f : n, x);
 }
-
-constexpr float kNearBorder = 0x1p-12f;
-constexpr float kTiny = 1e-30f;  // below this the binary16 scale is zero, whatever the codes
+static __device__ __noinline__ float q4_border(float x, float inv, float m) {
+  const float k = rintf(fmaf(x, inv, 0.5f)), df = prod_diff(-8.f, x, k - 0.5f, m);
+  return kMagic + 8.f + ((m > 0.f ? df >= 0.f : df <= 0.f) ? k : k - 1.f);
+}
+__device__ __forceinline__ uint32_t low_bytes(const float* t) {  // the low bytes of four sums
+  const uint32_t a = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040);
+  const uint32_t b = __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
 
 // Eight codes as bytes in lo, hi; the block's scale in d.
 __device__ __forceinline__ void quant_q8(const float (&x)[8], uint32_t& lo, uint32_t& hi, __half& d) {
   float am = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
-  am = quad_max(am);
+  am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
+  am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
   d = __float2half_rn(am / 127.f);
   const float inv = am > kTiny ? 127.f / am : 0.f;
-  uint32_t w[2] = {0, 0};
+  float t[8], near = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = fabsf(x[i]) * inv;
-    float n = floorf(y);
-    const float f = y - n;
-    bool up = f >= 0.5f;
-    if (fabsf(f - 0.5f) < kNearBorder && inv > 0.f) up = prod_diff(127.f, fabsf(x[i]), n + 0.5f, am) >= 0.f;
-    n = fminf(n + (up ? 1.f : 0.f), 127.f);
-    const int c = (int)copysignf(n, x[i]);
-    w[i >> 2] |= (uint32_t)(c & 255) << (8 * (i & 3));
+    t[i] = fmaf(x[i], inv, kMagic);
+    near = fmaxf(near, fabsf(fmaf(x[i], inv, kMagic - t[i])));
   }
-  lo = w[0], hi = w[1];
+  if (near > kNearBorder) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(fmaf(x[i], inv, kMagic - t[i])) > kNearBorder) t[i] = q8_border(x[i], inv, am);
+  }
+  lo = low_bytes(t), hi = low_bytes(t + 4);
 }
 
 // Eight codes 0..15 as bytes.
@@ -88,26 +100,26 @@ __device__ __forceinline__ void quant_q4(const float (&x)[8], uint32_t& lo, uint
     if (fabsf(x[i]) > am) am = fabsf(x[i]), m = x[i];
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {  // the first of equal magnitudes: the lower lane's
-    const float am2 = __shfl_xor_sync(kFull, am, o), m2 = __shfl_xor_sync(kFull, m, o);
+    const float m2 = __shfl_xor_sync(kFull, m, o);
     const bool lower = (threadIdx.x & o) != 0;  // the partner is the lower lane
-    if (am2 > am || (am2 == am && lower)) am = am2, m = m2;
+    if (fabsf(m2) > fabsf(m) || (fabsf(m2) == fabsf(m) && lower)) m = m2;
   }
   d = __float2half_rn(m * -0.125f);
-  const float inv = am > kTiny ? -8.f / m : 0.f;
-  uint32_t w[2] = {0, 0};
+  const float inv = fabsf(m) > kTiny ? -8.f / m : 0.f;
+  float t[8], near = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = fmaf(x[i], inv, 0.5f);
-    float n = floorf(t);
-    const float k = rintf(t);
-    if (fabsf(t - k) < kNearBorder && inv != 0.f) {
-      const float df = prod_diff(-8.f, x[i], k - 0.5f, m);
-      n = (m > 0.f ? df >= 0.f : df <= 0.f) ? k : k - 1.f;
-    }
-    const int c = (int)fminf(fmaxf(n + 8.f, 0.f), 15.f);
-    w[i >> 2] |= (uint32_t)c << (8 * (i & 3));
+    t[i] = fmaf(x[i], inv, kMagic + 8.f);
+    near = fmaxf(near, fabsf(fmaf(x[i], inv, kMagic + 8.f - t[i])));
   }
-  lo = w[0], hi = w[1];
+  if (near > kNearBorder) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(fmaf(x[i], inv, kMagic + 8.f - t[i])) > kNearBorder) t[i] = q4_border(x[i], inv, m);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = fminf(t[i], kMagic + 15.f);
+  lo = low_bytes(t), hi = low_bytes(t + 4);
 }
 
 __device__ __forceinline__ void put16(uint8_t* p, uint32_t v) { *reinterpret_cast<uint16_t*>(p) = (uint16_t)v; }
@@ -122,97 +134,101 @@ __device__ __forceinline__ void store_row8(uint8_t* row, int type, int e0, const
   } else {
     uint32_t lo, hi;
     __half d;
+    uint8_t* p;
     if (type == FA_Q8_0) {
       quant_q8(x, lo, hi, d);
-      uint8_t* blk = row + (e0 >> 5) * 34;
-      if (on) {
-        if (j == 0) put16(blk, __half_as_ushort(d));
-        uint8_t* p = blk + 2 + 8 * j;
-        put16(p, lo), put16(p + 2, lo >> 16), put16(p + 4, hi), put16(p + 6, hi >> 16);
-      }
+      p = row + (e0 >> 5) * 34;
     } else {
       quant_q4(x, lo, hi, d);
       const uint32_t lo2 = __shfl_xor_sync(kFull, lo, 2), hi2 = __shfl_xor_sync(kFull, hi, 2);
-      if (on && j < 2) {  // byte b: element b low, element b + 16 high
-        lo |= lo2 << 4, hi |= hi2 << 4;
-        uint8_t* blk = row + (e0 >> 5) * 18;
-        if (j == 0) put16(blk, __half_as_ushort(d));
-        uint8_t* p = blk + 2 + 8 * j;
-        put16(p, lo), put16(p + 2, lo >> 16), put16(p + 4, hi), put16(p + 6, hi >> 16);
-      }
+      lo |= lo2 << 4, hi |= hi2 << 4;  // byte b: element b low, element b + 16 high
+      p = row + (e0 >> 5) * 18;
+      on = on && j < 2;
+    }
+    if (on) {
+      if (j == 0) put16(p, __half_as_ushort(d));
+      p += 2 + 8 * j;
+      put16(p, lo), put16(p + 2, lo >> 16), put16(p + 4, hi), put16(p + 6, hi >> 16);
     }
   }
 }
 
-// K (IS_K) or V rows: a warp takes HC heads of one token, D / 8 lanes a head.
+// K (IS_K) or V rows: a warp takes HC heads of a token, D / 8 lanes a head, and goes on to another token.
 template <int D, typename TX, bool IS_K>
 __device__ __forceinline__ void append_rows(const RowArgs& a) {
-  constexpr int LG = D / 8, GW = 32 / LG, U = sizeof(TX) == 2 ? 4 : 2;
+  constexpr int LG = D / 8, GW = 32 / LG;
   const int lane = threadIdx.x & 31, grp = lane / LG, e0 = (lane & (LG - 1)) * 8;
-  const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5);
-  const int t = item / (unsigned)a.nchunk, h0 = (int)(item - (unsigned)t * a.nchunk) * a.HC;
-  if (t >= a.T) return;
-  const int h1 = min(a.c.Hkv, h0 + a.HC), b = a.seq[t], pos = a.pos[t];
   const bool vec = IS_K ? a.veck : a.vecv;
-  const TX* x0 = (IS_K ? static_cast<const TX*>(a.xk) + t * a.k_row : static_cast<const TX*>(a.xv) + t * a.v_row) + e0;
   const long long head = IS_K ? a.k_head : a.v_head;
-  float w[8];
-  if (IS_K && a.wk) load8(a.wk + e0, false, w);
-  if (b < 0 || pos < 0) return;
   const int rb = IS_K ? a.c.rbk : a.c.rbv, type = IS_K ? a.c.k_type : a.c.v_type;
-  Turn8<D> turn;
-  uint8_t* cell = nullptr;
-  for (int h = h0 + grp, first = 1; h - grp < h1; h += U * GW, first = 0) {
-    Oct<TX> raw[U];
+  const bool norm = IS_K && a.wk, turns = IS_K && a.rope.n_rot;
+  float w[8];
+  if (norm) load8(a.wk + e0, false, w);
+  const unsigned items = (unsigned)a.T * a.nchunk, step = gridDim.x * 8;
+  for (unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5); item < items; item += step) {
+    const int t = item / (unsigned)a.nchunk, h0 = (int)(item - (unsigned)t * a.nchunk) * a.HC;
+    const int b = a.seq[t], pos = a.pos[t];
+    const TX* x0 = (IS_K ? static_cast<const TX*>(a.xk) + t * a.k_row : static_cast<const TX*>(a.xv) + t * a.v_row) + e0;
+    int left = min(a.c.Hkv - h0, a.HC);
+    if (b < 0 || pos < 0) continue;
+    x0 += h0 * head;
+    Oct<TX> raw;
+    load8_raw(x0 + min(grp, left - 1) * head, vec, raw);
+    const long long cell = cache_row(a.c, b, pos);
+    if (cell < 0) continue;
+    uint8_t* row = (IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h0 + grp) * rb;
+    Turn8<D> turn;
+    if (turns) turn.set(a.rope, pos, e0, 1.f);
+#pragma unroll 1
+    for (;;) {
+      float x[8];
+      unpack8(raw, x);
+      const bool on = grp < left, more = left > GW;
+      left -= GW;
+      x0 += GW * head;
+      if (more) load8_raw(x0 + min(grp, left - 1) * head, vec, raw);  // the next heads, ahead of this one's work
+      if (norm) {
+        float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (h + u * GW < h1) load8_raw(x0 + (h + u * GW) * head, vec, raw[u]);
-    if (first) {
-      const long long row = cache_row(a.c, b, pos);
-      if (row < 0) return;
-      cell = (IS_K ? a.c.k : a.c.v) + row * a.c.Hkv * (long long)rb;
-      if (IS_K) turn.set(a.rope, pos, e0, 1.f);
-    }
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+        const float r = inv_rms(group_sum<LG>(ss), 1.f / D, a.eps);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (h - grp + u * GW >= h1) break;  // (the same in all lanes)
-      const bool on = h + u * GW < h1;
-      float x[8] = {};
-      if (on) unpack8(raw[u], x);
-      if (IS_K) {
-        if (a.wk) {
-          float ss = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-          const float r = inv_rms(group_sum<LG>(ss), 1.f / D, a.eps);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-        }
-        if (a.rope.n_rot) turn.apply(x, a.rope.style);
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
       }
-      store_row8(cell + (on ? h + u * GW : 0) * (long long)rb, type, e0, x, on);
+      if (turns) turn.apply(x, a.rope.style);
+      store_row8(row, type, e0, x, on);
+      if (!more) break;
+      row += GW * rb;
     }
   }
 }
 
 // blockIdx.y 0: keys, 1: values
-template <typename TX>
+template <int D, int DV, typename TX>
 __global__ void __launch_bounds__(256) k_cache_append(const RowArgs a) {
-  if (blockIdx.y == 0) {
-    if (a.c.D == 64) append_rows<64, TX, true>(a);
-    else if (a.c.D == 128) append_rows<128, TX, true>(a);
-    else append_rows<256, TX, true>(a);
-  } else {
-    if (a.c.Dv == 64) append_rows<64, TX, false>(a);
-    else if (a.c.Dv == 128) append_rows<128, TX, false>(a);
-    else append_rows<256, TX, false>(a);
-  }
+  if (blockIdx.y == 0) append_rows<D, TX, true>(a);
+  else append_rows<DV, TX, false>(a);
+}
+
+typedef void (*RowKernel)(const RowArgs);
+template <int D, typename TX>
+static RowKernel pick_append_v(int Dv) {
+  return Dv == 64 ? k_cache_append<D, 64, TX> : Dv == 128 ? k_cache_append<D, 128, TX> : k_cache_append<D, 256, TX>;
+}
+template <typename TX>
+static RowKernel pick_append(int D, int Dv) {
+  return D == 64 ? pick_append_v<64, TX>(Dv) : D == 128 ? pick_append_v<128, TX>(Dv) : pick_append_v<256, TX>(Dv);
 }
 
 // ------------------------------------------------------------------------------------------------
 // read
 
 __device__ __forceinline__ uint32_t get16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+
+// byte b (0, 1) of w as a number, less `bias`: as the low byte of 2^23
+__device__ __forceinline__ float byte_minus(uint32_t w, int b, float bias) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, b ? 0x7441 : 0x7440)) - (8388608.f + bias);
+}
 
 __device__ __forceinline__ void load_row8(const uint8_t* row, int type, int e0, float (&x)[8]) {
   const int j = (e0 >> 3) & 3;
@@ -223,19 +239,19 @@ __device__ __forceinline__ void load_row8(const uint8_t* row, int type, int e0, 
   } else if (type == FA_Q8_0) {
     const uint8_t* blk = row + (e0 >> 5) * 34;
     const float d = __half2float(__ushort_as_half((unsigned short)get16(blk)));
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const uint32_t w = get16(blk + 2 + 8 * j + i);
-      x[i] = d * (float)(int8_t)(w & 255), x[i + 1] = d * (float)(int8_t)(w >> 8);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = get16(blk + 2 + 8 * j + 2 * i) ^ 0x8080u;  // code + 128
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = d * byte_minus(w[i >> 1], i & 1, 128.f);
   } else {
     const uint8_t* blk = row + (e0 >> 5) * 18;
     const float d = __half2float(__ushort_as_half((unsigned short)get16(blk)));
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const uint32_t w = get16(blk + 2 + 8 * (j & 1) + i) >> (j < 2 ? 0 : 4);
-      x[i] = d * (float)((int)(w & 15) - 8), x[i + 1] = d * (float)((int)((w >> 8) & 15) - 8);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = (get16(blk + 2 + 8 * (j & 1) + 2 * i) >> (j < 2 ? 0 : 4)) & 0x0f0fu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = d * byte_minus(w[i >> 1], i & 1, 8.f);
   }
 }
 
@@ -243,10 +259,9 @@ template <int D, typename TY, bool IS_K>
 __device__ __forceinline__ void read_rows(const RowArgs& a) {
   constexpr int LG = D / 8, GW = 32 / LG;
   const int lane = threadIdx.x & 31, e0 = (lane & (LG - 1)) * 8;
-  const long long item = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * GW + lane / LG;
-  const long long t = item / a.c.Hkv;
+  const unsigned item = (blockIdx.x * 8u + (threadIdx.x >> 5)) * GW + lane / LG, t = item / (unsigned)a.c.Hkv;
   const int h = (int)(item - t * a.c.Hkv);
-  if (t >= a.T) return;
+  if (t >= (unsigned)a.T) return;
   const int b = a.seq[t], pos = a.pos[t];
   if (b < 0 || pos < 0) return;
   const long long cell = cache_row(a.c, b, pos);
@@ -254,7 +269,7 @@ __device__ __forceinline__ void read_rows(const RowArgs& a) {
   const int rb = IS_K ? a.c.rbk : a.c.rbv, type = IS_K ? a.c.k_type : a.c.v_type;
   float x[8];
   load_row8((IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h) * (long long)rb, type, e0, x);
-  store8(static_cast<TY*>(IS_K ? a.ko : a.vo) + item * D + e0, x);
+  store8(static_cast<TY*>(IS_K ? a.ko : a.vo) + (long long)item * D + e0, x);
 }
 
 template <typename TY>
@@ -332,12 +347,13 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
   a.HC = (int)std::max<long long>(side, std::min<long long>(hc, 16));
   a.nchunk = (a.c.Hkv + a.HC - 1) / a.HC;
   const long long blocks = ((long long)T * a.nchunk + 7) / 8;
-  if (blocks > 0x0fffffffLL) return FA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks, 2);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (x_type == FA_ACT_F32) k_cache_append<float><<<grid, 256, 0, s>>>(a);
-  else if (x_type == FA_ACT_F16) k_cache_append<__half><<<grid, 256, 0, s>>>(a);
-  else k_cache_append<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+  if ((long long)T * a.nchunk > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  // at most the warps that the SMs hold: each goes on to further tokens with its code at hand
+  const dim3 grid((unsigned)std::min<long long>(blocks, 2 * nsm), 2);
+  const RowKernel k_append = x_type == FA_ACT_F32   ? pick_append<float>(a.c.D, a.c.Dv)
+                             : x_type == FA_ACT_F16 ? pick_append<__half>(a.c.D, a.c.Dv)
+                                                    : pick_append<__nv_bfloat16>(a.c.D, a.c.Dv);
+  k_append<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -358,7 +374,7 @@ extern "C" fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* s
   } else {
     const int per = 8 * (256 / std::max(a.c.D, a.c.Dv));
     const long long blocks = ((long long)T * a.c.Hkv + per - 1) / per;
-    if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    if ((long long)T * a.c.Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks, 2);
     if (y_type == FA_ACT_F32) k_cache_read<float><<<grid, 256, 0, s>>>(a);
     else if (y_type == FA_ACT_F16) k_cache_read<__half><<<grid, 256, 0, s>>>(a);

@@ -13,57 +13,65 @@ from . import _native as nat
 from .api import FaBackError, Workspace, _check, _ptr
 
 _ACT = {torch.float32: nat.FA_ACT_F32, torch.float16: nat.FA_ACT_F16, torch.bfloat16: nat.FA_ACT_BF16}
+_F32, _I32, _empty = torch.float32, torch.int32, torch.empty
+
+# These calls are made once a layer and step, on small tensors, so what they cost on the host counts:
+# each argument is looked at once, and what a refusal says is put together only when there is one.
 
 
 def _act(t: torch.dtype) -> int:
-    try:
-        return _ACT[t]
-    except KeyError:
-        raise FaBackError(f"activations are float32, float16 or bfloat16, not {t}") from None
+    act = _ACT.get(t)
+    if act is None:
+        raise FaBackError(f"activations are float32, float16 or bfloat16, not {t}")
+    return act
 
 
-def _expect(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> None:
-    """t (or None) is contiguous, of this type, shape and device."""
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise FaBackError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got {t.dtype} "
-                          f"{tuple(t.shape)} on {t.device}")
+def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """The address of t, which is contiguous, of this type, shape (a tuple) and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise FaBackError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got {t.dtype} "
+                      f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
-def _heads(name: str, t: torch.Tensor, N: int, D: int, dtype, device) -> torch.Tensor:
-    """t [N][heads][D], possibly a view whose components are contiguous."""
-    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != D or t.dtype != dtype or t.device != device:
-        raise FaBackError(f"{name}: {dtype} [{N}][heads][{D}] on {device} expected, got {t.dtype} {tuple(t.shape)} on "
-                          f"{t.device}")
-    if t.numel() and (t.stride(2) != 1 or t.stride(0) < 0 or t.stride(1) < 0):
-        raise FaBackError(f"{name}: components must be contiguous")
-    return t
+def _heads(name: str, t: torch.Tensor, N: int, D: int, dtype, device):
+    """Heads and strides (token, head) of t [N][heads][D], possibly a view whose components are contiguous."""
+    if t.dim() == 3 and t.dtype is dtype and t.device == device:
+        n, heads, d = t.shape
+        row, head, comp = t.stride()
+        if n == N and d == D and ((comp == 1 and row >= 0 and head >= 0) or not t.numel()):
+            return heads, row, head
+    raise FaBackError(f"{name}: {dtype} [{N}][heads][{D}] with contiguous components on {device} expected, got "
+                      f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
 class _On:
-    """The stream that a call enqueues on, with the tensors' device current.  With `stream` given, what
-    the call allocates belongs to that stream."""
+    """Around a call: its stream's device is current, and with `stream` given, what it allocates belongs
+    to that stream.  Only made where that is not so already."""
 
     def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        if device.type != "cuda":
-            raise FaBackError(f"CUDA tensors expected, got {device}")
-        if stream is not None:
-            self._guard = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-        else:
-            self._guard = None
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        self._guard = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
+        self._guard.__enter__()
 
     def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+        self._guard.__exit__(*exc)
+
+
+def _index(device: torch.device) -> int:
+    if device.type != "cuda":
+        raise FaBackError(f"CUDA tensors expected, got {device}")
+    return device.index
+
+
+def _call(fn, device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """fn(stream handle) on the current stream of the device, or on `stream`."""
+    index = _index(device)
+    if stream is None and index == torch._C._cuda_getDevice():
+        return fn(torch._C._cuda_getCurrentRawStream(index))
+    with _On(device, stream):
+        return fn(torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream)
 
 
 def rope_frequencies(n_rot: int, base: float = 10000.0, *, scale: float = 1.0, factors=None,
@@ -79,12 +87,11 @@ def rope_frequencies(n_rot: int, base: float = 10000.0, *, scale: float = 1.0, f
     return out.to(device)
 
 
-def _rope(rope: Optional[torch.Tensor], style: int, pos: torch.Tensor, N: int, device) -> Optional[nat.fa_rope]:
+def _rope(rope: Optional[torch.Tensor], style: int, device) -> Optional[nat.fa_rope]:
     if rope is None:
         return None
-    if rope.dtype != torch.int64 or rope.dim() != 1 or rope.device != device or not rope.is_contiguous():
+    if rope.dtype is not torch.int64 or rope.dim() != 1 or rope.device != device or not rope.is_contiguous():
         raise FaBackError("rope: the contiguous int64 frequencies of rope_frequencies() on the tensors' device expected")
-    _expect("pos", pos, torch.int32, (N,), device)
     return nat.fa_rope(rope.data_ptr(), 2 * rope.numel(), style)
 
 
@@ -130,18 +137,17 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, seq: torch
     frequencies rope (rope_frequencies(), or None) on the way."""
     dev, T = cache.device, k.shape[0]
     act = _act(k.dtype)
-    _heads("k", k, T, cache.D, k.dtype, dev)
-    _heads("v", v, T, cache.Dv, k.dtype, dev)
-    if k.shape[1] != cache.Hkv or v.shape[1] != cache.Hkv:
+    hk, k_row, k_head = _heads("k", k, T, cache.D, k.dtype, dev)
+    hv, v_row, v_head = _heads("v", v, T, cache.Dv, k.dtype, dev)
+    if hk != cache.Hkv or hv != hk:
         raise FaBackError(f"k, v: {cache.Hkv} heads expected")
-    _expect("seq", seq, torch.int32, (T,), dev)
-    _expect("pos", pos, torch.int32, (T,), dev)
-    _expect("k_norm", k_norm, torch.float32, (cache.D,), dev)
-    r = _rope(rope, rope_style, pos, T, dev)
-    views = nat.fa_kv_views(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-    with _On(dev, stream) as on:
-        _check(nat.fa_cache_append(k.data_ptr(), v.data_ptr(), act, views, cache.c, seq.data_ptr(), pos.data_ptr(), T,
-                                   _ptr(k_norm), eps, r, on.handle))
+    p_seq = _expect("seq", seq, _I32, (T,), dev)
+    p_pos = _expect("pos", pos, _I32, (T,), dev)
+    p_norm = None if k_norm is None else _expect("k_norm", k_norm, _F32, (cache.D,), dev)
+    r = _rope(rope, rope_style, dev)
+    views = nat.fa_kv_views(k_row, k_head, v_row, v_head)
+    _check(_call(lambda s: nat.fa_cache_append(k.data_ptr(), v.data_ptr(), act, views, cache.c, p_seq, p_pos, T, p_norm,
+                                               eps, r, s), dev, stream))
 
 
 def cache_read(cache: PagedCache, seq: torch.Tensor, pos: torch.Tensor, *, dtype=torch.float32,
@@ -150,21 +156,25 @@ def cache_read(cache: PagedCache, seq: torch.Tensor, pos: torch.Tensor, *, dtype
     dtype, or with dtype=torch.uint8 the raw rows [T][Hkv][row], the contiguous cache that backward()
     and forward() take.  Rows of skipped tokens (negative seq or pos) are not written."""
     dev, T = cache.device, seq.shape[0]
-    raw = dtype == torch.uint8
-    act = nat.FA_ACT_RAW if raw else _act(dtype)
-    _expect("seq", seq, torch.int32, (T,), dev)
-    _expect("pos", pos, torch.int32, (T,), dev)
-    nk, nv = (cache.k.shape[3], cache.v.shape[3]) if raw else (cache.D, cache.Dv)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = {"k": torch.empty((T, cache.Hkv, nk), dtype=dtype, device=dev),
-                   "v": torch.empty((T, cache.Hkv, nv), dtype=dtype, device=dev)}
+    if dtype is torch.uint8:
+        act, nk, nv = nat.FA_ACT_RAW, cache.k.shape[3], cache.v.shape[3]
+    else:
+        act, nk, nv = _act(dtype), cache.D, cache.Dv
+    p_seq = _expect("seq", seq, _I32, (T,), dev)
+    p_pos = _expect("pos", pos, _I32, (T,), dev)
+
+    def run(s):
+        o = out
+        if o is None:
+            o = {"k": _empty((T, cache.Hkv, nk), dtype=dtype, device=dev), "v": _empty((T, cache.Hkv, nv), dtype=dtype, device=dev)}
+            p_k, p_v = o["k"].data_ptr(), o["v"].data_ptr()
         else:
-            _expect("out k", out["k"], dtype, (T, cache.Hkv, nk), dev)
-            _expect("out v", out["v"], dtype, (T, cache.Hkv, nv), dev)
-        _check(nat.fa_cache_read(cache.c, seq.data_ptr(), pos.data_ptr(), T, act, out["k"].data_ptr(),
-                                 out["v"].data_ptr(), on.handle))
-    return out
+            p_k = _expect("out k", o["k"], dtype, (T, cache.Hkv, nk), dev)
+            p_v = _expect("out v", o["v"], dtype, (T, cache.Hkv, nv), dev)
+        _check(nat.fa_cache_read(cache.c, p_seq, p_pos, T, act, p_k, p_v, s))
+        return o
+
+    return _call(run, dev, stream)
 
 
 def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, scale: float,
@@ -175,33 +185,39 @@ def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, 
     seq_lens [B] (int32) positions of the cache's sequences: {"O": [B][H][Dv] of q's type, "lse": [B][H] f32}.
     ALiBi slopes and sinks (f32 [H]) and the soft cap are those of backward().  A negative length marks a
     padding slot, whose rows are not written."""
-    B, H = q.shape[0], q.shape[1]
-    dev = cache.device
-    act = _act(q.dtype)
-    _heads("q", q, cache.B, cache.D, q.dtype, dev)
-    _expect("seq_lens", seq_lens, torch.int32, (B,), dev)
-    _expect("alibi_slopes", alibi_slopes, torch.float32, (H,), dev)
-    _expect("sinks", sinks, torch.float32, (H,), dev)
-    with _On(dev, stream) as on:
-        ws = (workspace or Workspace(dev)).get(cache.decode_workspace_size(H))
-        if out is None:
-            out = {"O": torch.empty((B, H, cache.Dv), dtype=q.dtype, device=dev),
-                   "lse": torch.empty((B, H), dtype=torch.float32, device=dev)}
+    dev, B, dtype = cache.device, cache.B, q.dtype
+    act = _act(dtype)
+    H, q_row, q_head = _heads("q", q, B, cache.D, dtype, dev)
+    p_len = _expect("seq_lens", seq_lens, _I32, (B,), dev)
+    p_alibi = None if alibi_slopes is None else _expect("alibi_slopes", alibi_slopes, _F32, (H,), dev)
+    p_sinks = None if sinks is None else _expect("sinks", sinks, _F32, (H,), dev)
+    _index(dev)
+
+    def run(s):
+        o = out
+        need = cache._ws.get(H) or cache.decode_workspace_size(H)
+        if o is None:
+            o = {"O": _empty((B, H, cache.Dv), dtype=dtype, device=dev), "lse": _empty((B, H), dtype=_F32, device=dev)}
+            p_o, p_lse = o["O"].data_ptr(), o["lse"].data_ptr()
         else:
-            _expect("out O", out["O"], q.dtype, (B, H, cache.Dv), dev)
-            _expect("out lse", out["lse"], torch.float32, (B, H), dev)
-        _check(nat.fa_paged_decode(q.data_ptr(), act, q.stride(0), q.stride(1), cache.c, seq_lens.data_ptr(), H, scale,
-                                   _ptr(alibi_slopes), softcap, _ptr(sinks), out["O"].data_ptr(), out["lse"].data_ptr(),
-                                   ws.data_ptr(), ws.numel(), on.handle))
-    return out
+            p_o = _expect("out O", o["O"], dtype, (B, H, cache.Dv), dev)
+            p_lse = _expect("out lse", o["lse"], _F32, (B, H), dev)
+        ws = _empty((need,), dtype=torch.uint8, device=dev) if workspace is None else workspace.get(need)
+        _check(nat.fa_paged_decode(q.data_ptr(), act, q_row, q_head, cache.c, p_len, H, scale, p_alibi, softcap, p_sinks,
+                                   p_o, p_lse, ws.data_ptr(), need, s))
+        return o
+
+    return _call(run, dev, stream)
 
 
-def _qk(q, k, N, D, dtype, dev):
-    _heads("q", q, N, D, dtype, dev)
-    if k is None:
-        return 0, nat.fa_qk_views(q.stride(0), q.stride(1), 0, 0)
-    _heads("k", k, N, D, dtype, dev)
-    return k.shape[1], nat.fa_qk_views(q.stride(0), q.stride(1), k.stride(0), k.stride(1))
+def _qk(q, k):
+    """Shape, device, dtype of q and the head counts and views of q and k (k may be None)."""
+    if q.dim() != 3:
+        raise FaBackError(f"q: [N][H][D] expected, got {tuple(q.shape)}")
+    (N, H, D), dev, dtype = q.shape, q.device, q.dtype
+    _, q_row, q_head = _heads("q", q, N, D, dtype, dev)
+    Hkv, k_row, k_head = (0, 0, 0) if k is None else _heads("k", k, N, D, dtype, dev)
+    return N, H, D, dev, dtype, Hkv, nat.fa_qk_views(q_row, q_head, k_row, k_head)
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch.Tensor], *,
@@ -211,25 +227,27 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch
     """RMS norm of every head (weights wq, wk f32 [D]; None: not normalised) and rotation by pos [N]
     (int32) of queries q [N][H][D] and keys k [N][Hkv][D] (f32, f16 or bf16, possibly views of one
     projection; k may be None): {"q", "k"}, contiguous, of dtype (default q's)."""
-    N, H, D = q.shape
-    dev = q.device
-    Hkv, views = _qk(q, k, N, D, q.dtype, dev)
-    dtype = q.dtype if dtype is None else dtype
-    x_type, y_type = _act(q.dtype), _act(dtype)
-    _expect("wq", wq, torch.float32, (D,), dev)
-    _expect("wk", wk, torch.float32, (D,), dev)
-    r = _rope(rope, rope_style, pos, N, dev)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = {"q": torch.empty((N, H, D), dtype=dtype, device=dev),
-                   "k": None if k is None else torch.empty((N, Hkv, D), dtype=dtype, device=dev)}
+    N, H, D, dev, x_dtype, Hkv, views = _qk(q, k)
+    dtype = x_dtype if dtype is None else dtype
+    x_type, y_type = _act(x_dtype), _act(dtype)
+    p_wq = None if wq is None else _expect("wq", wq, _F32, (D,), dev)
+    p_wk = None if wk is None else _expect("wk", wk, _F32, (D,), dev)
+    r = _rope(rope, rope_style, dev)
+    p_pos = None if r is None else _expect("pos", pos, _I32, (N,), dev)
+
+    def run(s):
+        o = out
+        if o is None:
+            o = {"q": _empty((N, H, D), dtype=dtype, device=dev), "k": None if k is None else _empty((N, Hkv, D), dtype=dtype, device=dev)}
+            p_q, p_k = o["q"].data_ptr(), None if k is None else o["k"].data_ptr()
         else:
-            _expect("out q", out["q"], dtype, (N, H, D), dev)
-            _expect("out k", out["k"], dtype, (N, Hkv, D), dev)
-        _check(nat.fa_qk_norm_rope(q.data_ptr(), _ptr(k), x_type, views, _ptr(wq), _ptr(wk), eps,
-                                   None if r is None else pos.data_ptr(), r, N, H, Hkv, D, out["q"].data_ptr(),
-                                   _ptr(out["k"]), y_type, on.handle))
-    return out
+            p_q = _expect("out q", o["q"], dtype, (N, H, D), dev)
+            p_k = None if k is None else _expect("out k", o["k"], dtype, (N, Hkv, D), dev)
+        _check(nat.fa_qk_norm_rope(q.data_ptr(), _ptr(k), x_type, views, p_wq, p_wk, eps, p_pos, r, N, H, Hkv, D, p_q, p_k,
+                                   y_type, s))
+        return o
+
+    return _call(run, dev, stream)
 
 
 def qk_norm_rope_backward(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
@@ -240,34 +258,36 @@ def qk_norm_rope_backward(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch
                           stream: Optional[torch.cuda.Stream] = None) -> dict:
     """The gradient of qk_norm_rope(): given gq [N][H][D] and gk [N][Hkv][D] (contiguous, e.g. backward()'s dQ
     and dK) and the forward's inputs, {"dq", "dk" of q's type, "dwq", "dwk" f32 [D] (with the weights)}."""
-    N, H, D = q.shape
-    dev = q.device
-    Hkv, views = _qk(q, k, N, D, q.dtype, dev)
+    N, H, D, dev, dtype, Hkv, views = _qk(q, k)
     if (gk is None) != (k is None):
         raise FaBackError("gk and k are given together")
-    x_type, y_type = _act(q.dtype), _act(gq.dtype)
-    _expect("gq", gq, gq.dtype, (N, H, D), dev)
-    _expect("gk", gk, gq.dtype, (N, Hkv, D), dev)
-    _expect("wq", wq, torch.float32, (D,), dev)
-    _expect("wk", wk, torch.float32, (D,), dev)
-    r = _rope(rope, rope_style, pos, N, dev)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = {"dq": torch.empty((N, H, D), dtype=q.dtype, device=dev)}
+    x_type, y_type = _act(dtype), _act(gq.dtype)
+    p_gq = _expect("gq", gq, gq.dtype, (N, H, D), dev)
+    p_gk = None if gk is None else _expect("gk", gk, gq.dtype, (N, Hkv, D), dev)
+    p_wq = None if wq is None else _expect("wq", wq, _F32, (D,), dev)
+    p_wk = None if wk is None else _expect("wk", wk, _F32, (D,), dev)
+    r = _rope(rope, rope_style, dev)
+    p_pos = None if r is None else _expect("pos", pos, _I32, (N,), dev)
+
+    def run(s):
+        o = out
+        if o is None:
+            o = {"dq": _empty((N, H, D), dtype=dtype, device=dev)}
             if k is not None:
-                out["dk"] = torch.empty((N, Hkv, D), dtype=q.dtype, device=dev)
+                o["dk"] = _empty((N, Hkv, D), dtype=dtype, device=dev)
             if wq is not None:
-                out["dwq"] = torch.empty((D,), dtype=torch.float32, device=dev)
+                o["dwq"] = _empty((D,), dtype=_F32, device=dev)
             if wk is not None and k is not None:
-                out["dwk"] = torch.empty((D,), dtype=torch.float32, device=dev)
+                o["dwk"] = _empty((D,), dtype=_F32, device=dev)
         else:
-            _expect("out dq", out["dq"], q.dtype, (N, H, D), dev)
-            _expect("out dk", out.get("dk"), q.dtype, (N, Hkv, D), dev)
-            _expect("out dwq", out.get("dwq"), torch.float32, (D,), dev)
-            _expect("out dwk", out.get("dwk"), torch.float32, (D,), dev)
-        ws = (workspace or Workspace(dev)).get(nat.fa_qk_norm_rope_backward_workspace_size(N, H, Hkv, D))
+            for name, t, shape in (("dq", dtype, (N, H, D)), ("dk", dtype, (N, Hkv, D)), ("dwq", _F32, (D,)), ("dwk", _F32, (D,))):
+                if o.get(name) is not None:
+                    _expect("out " + name, o[name], t, shape, dev)
+        need = nat.fa_qk_norm_rope_backward_workspace_size(N, H, Hkv, D)
+        ws = _empty((need,), dtype=torch.uint8, device=dev) if workspace is None else workspace.get(need)
         _check(nat.fa_qk_norm_rope_backward(
-            gq.data_ptr(), _ptr(gk), y_type, q.data_ptr(), _ptr(k), x_type, views, _ptr(wq), _ptr(wk), eps,
-            None if r is None else pos.data_ptr(), r, N, H, Hkv, D, out["dq"].data_ptr(), _ptr(out.get("dk")),
-            _ptr(out.get("dwq")), _ptr(out.get("dwk")), ws.data_ptr(), ws.numel(), on.handle))
-    return out
+            p_gq, p_gk, y_type, q.data_ptr(), _ptr(k), x_type, views, p_wq, p_wk, eps, p_pos, r, N, H, Hkv, D,
+            o["dq"].data_ptr(), _ptr(o.get("dk")), _ptr(o.get("dwq")), _ptr(o.get("dwk")), ws.data_ptr(), need, s))
+        return o
+
+    return _call(run, dev, stream)
