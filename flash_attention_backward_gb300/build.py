@@ -10,6 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libfa_back.so")
+FAST_SRC = os.path.join(CSRC, "py_fast.cpp")
+FAST = os.path.join(HERE, "_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -23,11 +25,31 @@ def _deps():
     return out
 
 
+def _newer(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB, _deps()) and _newer(FAST, _fast_deps())
+
+
+def _fast_deps():
+    return [FAST_SRC] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+
+
+def _fast_command(out: str):
+    """Compile and link the marshalling module of paged.py against this interpreter's PyTorch."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    inc = [a for p in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                       sysconfig.get_paths()["include"], "/usr/local/cuda/include") for a in ("-isystem", p)]
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", abi, *inc, FAST_SRC, "-o", out, "-L", lib,
+            "-Wl,--no-as-needed", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
 
 
 def nvcc() -> str:
@@ -38,10 +60,27 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libfa_back.so next to this file; returns its path.  The translation units compile in
-    parallel (one nvcc per file, objects in a temporary folder), then one link."""
+    """Build libfa_back.so and the marshalling module _fast.so next to this file; returns the library's
+    path.  The translation units compile in parallel (one compiler per file, objects in a temporary
+    folder), then one link."""
     if not force and up_to_date():
         return LIB
+    fast = None
+    if force or not _newer(FAST, _fast_deps()):
+        fast = subprocess.Popen(_fast_command(FAST + ".tmp%d" % os.getpid()), stdout=subprocess.PIPE,
+                                stderr=subprocess.STDOUT, text=True)
+    if force or not _newer(LIB, _deps()):
+        _build_library(verbose)
+    if fast is not None:
+        out, _ = fast.communicate()
+        if fast.returncode != 0:
+            sys.stderr.write(out)
+            raise RuntimeError("g++ failed building _fast.so")
+        os.replace(FAST + ".tmp%d" % os.getpid(), FAST)
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
     tmp = LIB + ".tmp%d" % os.getpid()
     flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
     if verbose:
@@ -68,7 +107,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout)
             raise RuntimeError("nvcc failed linking libfa_back.so")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

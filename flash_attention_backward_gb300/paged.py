@@ -5,6 +5,7 @@ tensors' device (or on `stream`).
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -12,8 +13,30 @@ import torch
 from . import _native as nat
 from .api import FaBackError, Workspace, _check, _ptr
 
+try:
+    from . import _fast  # the plain form of the calls below, in C++ (csrc/py_fast.cpp)
+except ImportError:  # not built: the same calls from here, at a few microseconds more each
+    _fast = None
+
 _ACT = {torch.float32: nat.FA_ACT_F32, torch.float16: nat.FA_ACT_F16, torch.bfloat16: nat.FA_ACT_BF16}
 _F32, _I32, _empty = torch.float32, torch.int32, torch.empty
+
+
+
+def _bind():
+    """Hand the library's entry points to _fast, once; False without it."""
+    global _plain
+    if _fast is None:
+        return False
+    L = nat.lib()
+    _fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.fa_qk_norm_rope, L.fa_qk_norm_rope_backward, L.fa_qk_norm_rope_backward_workspace_size, L.fa_cache_append,
+        L.fa_cache_read, L.fa_paged_decode, L.fa_paged_decode_workspace_size)))
+    _plain = True
+    return True
+
+
+_plain = False  # _fast is bound
 
 # These calls are made once a layer and step, on small tensors, so what they cost on the host counts:
 # each argument is looked at once, and what a refusal says is put together only when there is one.
@@ -117,6 +140,7 @@ class PagedCache:
         self.device = k.device
         self.c = nat.fa_paged_cache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), k_type, v_type, self.num_pages,
                                     self.page_size, self.B, self.max_pages, self.Hkv, D, Dv)
+        self._at, self._index = ctypes.addressof(self.c), self.device.index
         self._ws = {}  # decode workspace bytes by query head count
 
     def decode_workspace_size(self, H: int) -> int:
@@ -135,6 +159,9 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, seq: torch
     pos [T] of sequences seq [T] (int32; negative: a padding token, skipped) of the cache, quantised to
     its types.  Keys are normalised by k_norm (f32 [D], or None) and rotated by pos with the
     frequencies rope (rope_frequencies(), or None) on the way."""
+    if stream is None and cache._index is not None and (_plain or _bind()) and _fast.append(
+            k, v, cache._at, cache._index, seq, pos, k_norm, eps, rope, rope_style):
+        return
     dev, T = cache.device, k.shape[0]
     act = _act(k.dtype)
     hk, k_row, k_head = _heads("k", k, T, cache.D, k.dtype, dev)
@@ -155,6 +182,10 @@ def cache_read(cache: PagedCache, seq: torch.Tensor, pos: torch.Tensor, *, dtype
     """The cache's rows at positions pos [T] of sequences seq [T]: {"k": [T][Hkv][D], "v": [T][Hkv][Dv]} of
     dtype, or with dtype=torch.uint8 the raw rows [T][Hkv][row], the contiguous cache that backward()
     and forward() take.  Rows of skipped tokens (negative seq or pos) are not written."""
+    if stream is None and out is None and cache._index is not None and (_plain or _bind()):
+        got = _fast.read(cache._at, cache._index, seq, pos, dtype)
+        if got is not None:
+            return got
     dev, T = cache.device, seq.shape[0]
     if dtype is torch.uint8:
         act, nk, nv = nat.FA_ACT_RAW, cache.k.shape[3], cache.v.shape[3]
@@ -185,6 +216,10 @@ def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, 
     seq_lens [B] (int32) positions of the cache's sequences: {"O": [B][H][Dv] of q's type, "lse": [B][H] f32}.
     ALiBi slopes and sinks (f32 [H]) and the soft cap are those of backward().  A negative length marks a
     padding slot, whose rows are not written."""
+    if stream is None and out is None and workspace is None and cache._index is not None and (_plain or _bind()):
+        got = _fast.decode(q, cache._at, cache._index, seq_lens, scale, alibi_slopes, softcap, sinks)
+        if got is not None:
+            return got
     dev, B, dtype = cache.device, cache.B, q.dtype
     act = _act(dtype)
     H, q_row, q_head = _heads("q", q, B, cache.D, dtype, dev)
@@ -227,6 +262,10 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch
     """RMS norm of every head (weights wq, wk f32 [D]; None: not normalised) and rotation by pos [N]
     (int32) of queries q [N][H][D] and keys k [N][Hkv][D] (f32, f16 or bf16, possibly views of one
     projection; k may be None): {"q", "k"}, contiguous, of dtype (default q's)."""
+    if stream is None and out is None and (_plain or _bind()):
+        got = _fast.norm(q, k, pos, wq, wk, eps, rope, rope_style, dtype)
+        if got is not None:
+            return got
     N, H, D, dev, x_dtype, Hkv, views = _qk(q, k)
     dtype = x_dtype if dtype is None else dtype
     x_type, y_type = _act(x_dtype), _act(dtype)
@@ -258,6 +297,10 @@ def qk_norm_rope_backward(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch
                           stream: Optional[torch.cuda.Stream] = None) -> dict:
     """The gradient of qk_norm_rope(): given gq [N][H][D] and gk [N][Hkv][D] (contiguous, e.g. backward()'s dQ
     and dK) and the forward's inputs, {"dq", "dk" of q's type, "dwq", "dwk" f32 [D] (with the weights)}."""
+    if stream is None and out is None and workspace is None and (_plain or _bind()):
+        got = _fast.norm_back(gq, gk, q, k, pos, wq, wk, eps, rope, rope_style)
+        if got is not None:
+            return got
     N, H, D, dev, dtype, Hkv, views = _qk(q, k)
     if (gk is None) != (k is None):
         raise FaBackError("gk and k are given together")

@@ -536,6 +536,44 @@ def test_decode_beyond_two_gigabytes(fb):
     assert fb.fa_back_get_error() == 0
 
 
+def test_both_forms_of_the_wrappers_agree(fb, monkeypatch):
+    """The calls with and without the marshalling module: the same results, keys and types."""
+    from flash_attention_backward_gb300 import paged
+    assert paged._fast is not None
+    rng = np.random.default_rng(31)
+    p = R.Paged(31, [70, 0, 200], 2, 128, 64, Q8, F16, 16)
+    cache = p.on_gpu(fb, torch)
+    (q, _), (k, _), (v, _) = (act_array(rng, (3, h, d), "bf16") for h, d in ((6, 128), (2, 128), (2, 64)))
+    w, rope = torch.rand(128, device="cuda") + 0.5, fb.rope_frequencies(128)
+    seq, pos = cuda(np.array([0, 2, 2], np.int32)), cuda(np.array([5, 17, 180], np.int32))
+    lens = cuda(np.array(p.lens, np.int32))
+    calls = [
+        lambda: fb.paged_decode(q, cache, lens, scale=0.1, softcap=20.0, sinks=w[:6].contiguous()),
+        lambda: fb.cache_read(cache, seq, pos, dtype=torch.bfloat16),
+        lambda: fb.qk_norm_rope(q, k, pos, wq=w, wk=w, rope=rope, rope_style=fb.FA_ROPE_PAIRS, dtype=torch.float32),
+        lambda: fb.qk_norm_rope(q, None, None, wq=w),
+        lambda: fb.qk_norm_rope_backward(q, k, q, k, pos, wq=w, wk=w, rope=rope),
+        lambda: fb.qk_norm_rope_backward(q.float(), None, q, None, pos, rope=rope),
+    ]
+    was = paged._fast
+    for name in ("norm", "norm_back", "append", "read", "decode"):
+        assert callable(getattr(was, name))
+    fast = [c() for c in calls]
+    fb.cache_append(k, v, cache, seq, pos, k_norm=w, rope=rope)
+    after = cache.k.clone(), cache.v.clone()
+    cache.k.copy_(torch.from_numpy(p.k)), cache.v.copy_(torch.from_numpy(p.v))
+    monkeypatch.setattr(paged, "_fast", None)
+    monkeypatch.setattr(paged, "_plain", False)
+    for c, f in zip(calls, fast):
+        g = c()
+        assert list(g) == list(f)
+        for n in g:
+            assert (g[n] is None) == (f[n] is None)
+            assert g[n] is None or (g[n].dtype == f[n].dtype and torch.equal(g[n], f[n])), n
+    fb.cache_append(k, v, cache, seq, pos, k_norm=w, rope=rope)
+    assert torch.equal(cache.k, after[0]) and torch.equal(cache.v, after[1])
+
+
 # ------------------------------------------------------------------------------------------------
 # together with the attention of fa_back.h
 
