@@ -396,8 +396,8 @@ __device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&
 // ------------------------------------------------------------------------------------------------
 // the kernel
 
-constexpr int kUnit = 128;       // keys that a range of work is counted in
-constexpr int kMinUnits = 2;     // a range has at least this many units (where the work is that much)
+constexpr int kMinTiles = 4;     // an item has at least this many tiles of 16 keys (where its sequence has)
+constexpr int kPlanBatch = 256;  // with more sequences than this, a kernel of its own lays out the items
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLift = 7.f;     // weights are exp2(x - max + 7): the parts' small end moves out of the way
@@ -415,10 +415,11 @@ struct DecodeArgs {
   const float *alibi, *sinks;
   void* O;
   float* lse;
-  float* part;  // [R][HG][2]: partial O [8][DV], then maxima [8] and sums [8]
-  int4* jobs;   // [R]: the sequence that range r begins and a later one ends: {b, last range, slot, 0}, or b = -1
-  int R;        // ranges of the grid
-  int tiled;    // 1: a tile's rows are one box of the tensor maps; 0: one bulk copy a row
+  float* part;  // [slots][HG]: partial O [8][DV], then maxima [8] and sums [8] of an item of a split sequence
+  int4* jobs;   // [njobs]: the split sequences: {b, first slot, slots, 0}; b = -1 behind the last one
+  int4* items;  // [nitems] laid out beforehand: {b, splits, split, slot}, b = -1 behind the last one; or NULL
+  int R, nitems, njobs;  // items that the card holds at a time, that can be at most, split sequences at most
+  int box;      // rows of the tensor maps' boxes, 16 or 8: a tile is one or two; 0: one bulk copy a row
   uint32_t page_mul;  // j / page_size = j * page_mul >> page_shift for j < 2^30
   int page_shift;
   uint64_t wait_ns;   // a wait for a copy gives up after this long (0, the failure-detection hook: at once)
@@ -441,24 +442,32 @@ __host__ __device__ constexpr int smem_pitch(int rb) { return copy_bytes(rb) % 3
 // log2 of the tensor map's element size: a box is at most 256 elements wide
 __host__ __device__ constexpr int map_es(int pitch) { return pitch <= 512 ? 1 : pitch <= 1024 ? 2 : 3; }
 
-// One CTA an SM.  As many warps (16, 12, 8 or 4) as registers and shared memory hold with one slot each
-// (a tile's key rows, its value rows, and the warp's sums), then as many slots as fit.
-constexpr int kSmem = 222 * 1024;  // of the 227 KB: what the fixed-size arrays leave
-constexpr int kSlotCtl = 160;      // a slot's row addresses, barriers and mask (struct Slot of the kernel)
+// CTAs of few warps, several to an SM: a short sequence is a few tiles, and while one CTA starts, joins its
+// warps or waits for its first rows, the others work.  Registers (about 168 a thread for Dv = 256, else
+// 128) allow 12 or 16 warps an SM; shared memory may allow fewer.  What it has left goes to slots (a
+// tile's key rows and value rows) of each warp's ring, which also takes the warp's sums in the end.
+#ifndef FA_NW
+#define FA_NW 4
+#endif
+constexpr int kSmemSm = 227 * 1024;  // of an SM, for dynamic and static arrays and 1 KB a CTA
+constexpr int kSlotCtl = 160;        // a slot's row addresses, barriers and mask (struct Slot of the kernel)
 struct DecodeShape {
-  int nw, slots, smem, pk, pv, qf, stage;
+  int nw, ctas, slots, smem, pk, pv, qf, stage, ring;
 };
 __host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, int vt) {
   DecodeShape c{};
   c.pk = smem_pitch(cache_row_bytes(kt, D)), c.pv = smem_pitch(cache_row_bytes(vt, DV));
   c.qf = (kt == FA_F32 ? D / 8 : D / 16) * 512;
   c.stage = 16 * (c.pk + c.pv);
-  const int sums = DV * 32, slot = c.stage + kSlotCtl;
-  c.nw = DV == 256 ? 12 : 16;
-  while (c.nw > 4 && c.qf + c.nw * (slot + sums) > kSmem) c.nw -= 4;
-  c.slots = (kSmem - c.qf - c.nw * sums) / (c.nw * slot);
+  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 2048;
+  c.nw = FA_NW;
+  c.ctas = (DV == 256 ? 12 : 16) / c.nw;
+  while (c.ctas > 1 && fixed + c.nw * (slot > sums ? slot : sums) > kSmemSm / c.ctas) --c.ctas;
+  while (c.nw > 4 && fixed + c.nw * slot > kSmemSm / c.ctas) c.nw -= 4;
+  c.slots = (kSmemSm / c.ctas - fixed) / (c.nw * slot);
   if (c.slots > 4) c.slots = 4;
-  c.smem = c.qf + c.nw * (c.slots * c.stage + sums);
+  c.ring = c.slots * c.stage > sums ? c.slots * c.stage : (sums + 127) / 128 * 128;
+  c.smem = c.qf + c.nw * c.ring;
   return c;
 }
 
@@ -478,10 +487,74 @@ __device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
   const int L = __ldg(a.lens + b);
   return min(max(L, 0), a.c.max_pages * a.c.page_size);
 }
-__device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
 
-__device__ __forceinline__ long long range_begin(long long r, long long U, int Re) { return r * U / Re; }
-__device__ __forceinline__ int range_of(long long u, long long U, int Re) { return (int)(((u + 1) * Re - 1) / U); }
+// ---- the items of work: a sequence of n tiles is cut into ceil(n / chunk) of nearly equal size.  The chunk
+// is what makes all items of U tiles fit the card at once (an item a sequence more than U / chunk at
+// most), but not so small that joining the parts costs more than it gains: with w tiles an item a
+// sequence of n takes about w / 4 tile times and n / w parts, least near w = 0.37 sqrt(n) as measured.
+__device__ __forceinline__ int chunk_tiles(long long U, int B, int R) {
+  const long long room = max(R - B, (R + 1) / 2);
+  return (int)max((long long)max(kMinTiles, (int)(0.37f * sqrtf((float)U))), (U + room - 1) / room);
+}
+// What a sequence adds to the running counts: items, and for one that is split its slots and itself
+struct Counts {
+  int items, slots, split;
+};
+// slots and split sequences stay below 2 R and R (each split one has over a chunk of the at most R chunks)
+__device__ __forceinline__ uint64_t pack_counts(int n, int chunk) {
+  const uint32_t s = (n + chunk - 1) / chunk;
+  return (uint64_t)s | (s > 1 ? ((uint64_t)s << 32) + (1ull << 48) : 0ull);
+}
+__device__ __forceinline__ Counts unpack_counts(uint64_t x) {
+  return Counts{(int)(uint32_t)x, (int)((x >> 32) & 0xffff), (int)(x >> 48)};
+}
+// Sum of v over the block, and over the threads before this one (the warps' sums in `smem`, a word each)
+template <int NW, typename T>
+__device__ __forceinline__ T block_scan(T v, T* smem, T* before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) smem[warp] = x;
+  __syncthreads();
+  T all = 0;
+  *before = x - v;
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) *before += smem[w];
+    all += smem[w];
+  }
+  return all;
+}
+
+// Lays out the items of a large batch: one CTA.
+static __global__ void __launch_bounds__(1024) k_decode_plan(const DecodeArgs a) {
+  __shared__ uint64_t s_scan[32];
+  const int B = a.c.B;
+  uint64_t U = 0, before;
+  for (int c0 = 0; c0 < B; c0 += 1024) {
+    const int b = c0 + threadIdx.x;
+    U += block_scan<32, uint64_t>(b < B ? tiles_of(seq_keys(a, b)) : 0, s_scan, &before);
+  }
+  const int chunk = chunk_tiles((long long)U, B, a.R);
+  uint64_t base = 0;
+  for (int c0 = 0; c0 < B; c0 += 1024) {
+    const int b = c0 + threadIdx.x;
+    const uint64_t v = b < B ? pack_counts(tiles_of(seq_keys(a, b)), chunk) : 0;
+    const uint64_t all = block_scan<32, uint64_t>(v, s_scan, &before);
+    const Counts at = unpack_counts(base + before), own = unpack_counts(v);
+    for (int i = 0; i < own.items; ++i) a.items[at.items + i] = make_int4(b, own.items, i, at.slots + i);
+    if (own.split) a.jobs[at.split] = make_int4(b, at.slots, own.items, 0);
+    base += all;
+  }
+  const Counts total = unpack_counts(base);
+  for (int i = total.items + threadIdx.x; i < a.nitems; i += 1024) a.items[i] = make_int4(-1, 0, 0, 0);
+  for (int i = total.split + threadIdx.x; i < a.njobs; i += 1024) a.jobs[i] = make_int4(-1, 0, 0, 0);
+}
 
 __device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -509,7 +582,7 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
   }
 }
 
-// Sixteen rows of one KV head by TMA: x (elements, a multiple of 16 bytes) is where the head's rows start
+// A box of rows of one KV head by TMA: x (elements, a multiple of 16 bytes) is where the head's rows start
 // in a cell, y the first row of the pool.
 __device__ __forceinline__ void tile_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
@@ -555,22 +628,19 @@ static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float sl
                      fmaf(slope, (float)(d + 9), x.w));
 }
 
-// One range of keys (blockIdx.x / HG) of one (KV head, chunk of eight query heads) (blockIdx.x % HG).
-//
-// The work is the list of all sequences' keys in units of 128, cut into equal ranges whatever the
-// lengths are; consecutive CTAs take the same keys of the different heads, so a page's neighbouring
-// rows are read at the same time.  Within a range each warp takes every NW-th tile of 16 keys with a
-// ring, a running maximum and sums of its own: no barrier until the range or the sequence ends, and the
-// next sequence's first tiles are under way before this one's sums are joined.
+// One item (blockIdx.x / HG): a sequence, or a part of a long one, for one (KV head, chunk of eight query
+// heads) (blockIdx.x % HG).  Consecutive CTAs take the same keys of the different heads, so a page's
+// neighbouring rows are read at the same time.  Each warp takes every NW-th tile of 16 keys with a ring, a
+// running maximum and sums of its own: no barrier until the item's last tile.
 template <int D, int DV, int KT, int VT>
-__global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
+__global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_shape(D, DV, KT, VT).ctas)
     k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
   constexpr int NW = C.nw, SLOTS = C.slots, PK = C.pk, PV = C.pv;
   constexpr int RBK = cache_row_bytes(KT, D), RBV = cache_row_bytes(VT, DV);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_scan[NW];
-  __shared__ int s_seq, s_off;
+  __shared__ uint64_t s_scan[NW];
+  __shared__ int4 s_item;
   __shared__ float s_qs[8], s_ml[NW][16];
   // a slot: where its 16 key rows and its 16 value rows start, the barriers of either, the tile's key mask
   struct Slot {
@@ -585,41 +655,43 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
   const int hg = blockIdx.x % a.HG, r = blockIdx.x / a.HG, hk = hg / a.chunks;
   const int head0 = hk * a.G + (hg - hk * a.chunks) * 8, nh = min(8, a.G - (hg - hk * a.chunks) * 8);
   const int B = a.c.B;
-  const uint32_t qf = smem_u32(smem), ring = qf + C.qf + warp * (SLOTS * C.stage), ctl = smem_u32(&s_slot[warp][0]);
-  float* acc = reinterpret_cast<float*>(smem + C.qf + NW * SLOTS * C.stage);
+  const uint32_t qf = smem_u32(smem), ring = qf + C.qf + warp * C.ring, ctl = smem_u32(&s_slot[warp][0]);
+  constexpr int kSums = C.ring / 4;  // floats from one warp's sums (in its ring) to the next's
+  float* acc = reinterpret_cast<float*>(smem + C.qf);
   const int shift_k = hk * RBK & 15, shift_v = hk * RBV & 15;
   if (lane < 2 * SLOTS) fab::mbar_init(&s_slot[warp][lane >> 1].bar[lane & 1], 1);
   for (int i = threadIdx.x; i < DV + 4; i += NW * 32) s_zero[i] = 0;
   fab::fence_mbar_init();  // ordered before the first copy by the barriers below
 
-  // ---- the range: U units in all, of which this CTA takes [u0, u1)
-  int n_own = 0, s_before = 0, n_all = 0;  // units of this thread's sequence, of those before it, of all in a batch
-  auto scan = [&](int c0) {
-    const int b = c0 + threadIdx.x;
-    n_own = b < B ? units_of(seq_keys(a, b)) : 0;
-    int x = n_own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, x, o);
-      if (lane >= o) x += y;
+  // ---- the item: {sequence, its splits, this split, slot}
+  if (a.items) {
+    if (threadIdx.x == 0) s_item = a.items[r];
+  } else {  // from the lengths
+    if (threadIdx.x == 0) s_item = make_int4(-1, 0, 0, 0);
+    uint64_t U = 0, base = 0, before;
+    int n_own = 0;
+    for (int c0 = 0; c0 < B; c0 += NW * 32) {
+      const int b = c0 + threadIdx.x;
+      n_own = b < B ? tiles_of(seq_keys(a, b)) : 0;
+      U += block_scan<NW, uint64_t>(n_own, s_scan, &before);
     }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    s_before = x - n_own, n_all = 0;
-    for (int w = 0; w < NW; ++w) {
-      const int v = s_scan[w];
-      if (w < warp) s_before += v;
-      n_all += v;
+    const int chunk = chunk_tiles((long long)U, B, a.R);
+    const bool lists = r == 0 && hg == 0;  // this CTA lists the split sequences
+    for (int c0 = 0; c0 < B; c0 += NW * 32) {
+      const int b = c0 + threadIdx.x;
+      if (B > NW * 32) n_own = b < B ? tiles_of(seq_keys(a, b)) : 0;
+      const uint64_t v = pack_counts(n_own, chunk), all = block_scan<NW, uint64_t>(v, s_scan, &before);
+      const Counts at = unpack_counts(base + before), own = unpack_counts(v);
+      if (at.items <= r && r < at.items + own.items) s_item = make_int4(b, own.items, r - at.items, at.slots + r - at.items);
+      if (lists && own.split) a.jobs[at.split] = make_int4(b, at.slots, own.items, 0);
+      base += all;
+      if (!lists && unpack_counts(base).items > r) break;
     }
-  };
-  long long U = 0;
-  for (int c0 = 0; c0 < B; c0 += NW * 32) {
-    scan(c0);
-    U += n_all;
+    if (lists)
+      for (int i = unpack_counts(base).split + threadIdx.x; i < a.njobs; i += NW * 32) a.jobs[i] = make_int4(-1, 0, 0, 0);
   }
   // sequences without keys: their rows, by the CTA whose turn it is
-  for (int b = r + a.R * threadIdx.x; b < B; b += a.R * NW * 32) {
+  for (int b = r + a.nitems * threadIdx.x; b < B; b += a.nitems * NW * 32) {
     const int L = __ldg(a.lens + b);
     if (L > a.c.max_pages * a.c.page_size && hg == 0) *a.c.err = FA_ERR_PAGE;
     if (L < 0 || seq_keys(a, b) > 0) continue;
@@ -629,48 +701,28 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
       if (a.lse) a.lse[at] = a.sinks ? a.sinks[h] : -INFINITY;
     }
   }
-  const int Re = (int)max(1LL, min((long long)a.R, U / kMinUnits));
-  const long long u0 = r < Re ? range_begin(r, U, Re) : 0, u1 = r < Re ? range_begin(r + 1, U, Re) : 0;
-  if (u0 >= u1) {
-    if (hg == 0 && threadIdx.x == 0) a.jobs[r] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  // the sequence that u0 lies in: the batch of sequences, then the sequence
-  for (long long base = 0, c0 = 0; c0 < B; c0 += NW * 32) {
-    if (B > NW * 32) scan((int)c0);
-    const long long before = base + s_before;
-    if (before <= u0 && u0 < before + n_own) s_seq = (int)c0 + threadIdx.x, s_off = (int)(u0 - before);
-    base += n_all;
-    if (base > u0) break;
-  }
   __syncthreads();
-
-  // ---- a segment: the part of one sequence that lies in the range
   struct Segment {
-    int b, keys, j0, j1, ntile;  // sequence, its keys, the segment's keys [j0, j1) and tiles
-    bool whole;                  // the sequence lies in the range
+    int b, keys, j0, j1, ntile;  // sequence, its keys, the item's keys [j0, j1) and tiles
   };
-  int4 job = make_int4(-1, 0, 0, 0);
-  auto segment = [&](int b, int off, long long u, int seg) {
-    Segment s = {b, 0, 0, 0, 0, false};
-    if (u >= u1) return s;
-    s.keys = seq_keys(a, b);
-    while (s.keys == 0 && s.b + 1 < B) s.keys = seq_keys(a, ++s.b), off = 0;
-    const int nu = units_of(s.keys), take = (int)min((long long)(nu - off), u1 - u);
-    s.j0 = off * kUnit, s.j1 = min(s.keys, (off + take) * kUnit);
-    s.ntile = (s.j1 - s.j0 + 15) >> 4;  // (0 if the lengths changed while the kernel ran)
-    s.whole = take == nu;
-    if (off == 0 && !s.whole) job = make_int4(s.b, range_of(u + nu - 1, U, Re), seg == 0 ? 0 : 1, 0);
-    return s;
-  };
+  const int4 item = s_item;
+  if (item.x < 0) return;
+  Segment sg;
+  sg.b = item.x, sg.keys = seq_keys(a, item.x);
+  {
+    const long long n = tiles_of(sg.keys);
+    sg.j0 = 16 * (int)(n * item.z / item.y), sg.j1 = min(sg.keys, 16 * (int)(n * (item.z + 1) / item.y));
+    sg.ntile = tiles_of(sg.j1 - sg.j0);
+  }
+  const bool whole = item.y == 1;
 
-  // ---- rows of a tile.  Tiled copies (whole tiles in a page): the tile's first row, the same in every
-  // lane.  Otherwise one key a lane, lanes 16 .. 31 as 0 .. 15.  Page numbers are fetched a tile ahead of
-  // the copies that they are for.
+  // ---- rows of a tile: key `lane` & 15 a lane.  Boxes of rows (16 or 8 in one page) go by the tensor maps,
+  // else each row is copied by itself.  Page numbers are fetched a tile ahead of the copies that they are
+  // for.
   struct Where {
     int page, off;
   };
-  const int key_lane = a.tiled ? 0 : lane & 15;
+  const int key_lane = a.box == 16 ? 0 : a.box == 8 ? lane & 8 : lane & 15;  // the first key of the lane's box
   auto where = [&](const Segment& s, int tile) {
     const int j = s.j0 + tile * 16 + key_lane;
     Where w = {-1, 0};
@@ -692,15 +744,20 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
     const uint32_t dst = ring + slot * C.stage + (kv ? 16 * PK : 0);
     const int pitch = kv ? PV : PK;
     armed |= 1u << (4 * kv + slot);
-    if (a.tiled) {
-      const int n = row >= 0 ? min(16, s.j1 - (s.j0 + tile * 16)) : 0;  // the rows behind them are not used
+    if (a.box) {
+      const int n = min(16, s.j1 - (s.j0 + tile * 16));  // the rows behind them are not used
+      const bool in = (lane & 15) < n && row >= 0;
+      const uint32_t ok = a.box == 16 ? (row >= 0 ? (1u << n) - 1 : 0) : __ballot_sync(kFull, in) & 0xffffu;
       if (lane == 0) {
-        if (kv == 0) sts_u32(sl + 144, (1u << n) - 1);
-        bar_expect(bar, n ? 16 * pitch : 0);
-        if (n) tile_rows(dst, kv ? &map_v : &map_k, kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK), row, bar);
+        if (kv == 0) sts_u32(sl + 144, ok);
+        const int boxes = a.box == 16 ? (ok ? 2 : 0) : ((ok & 0xff) ? 1 : 0) + ((ok >> 8) ? 1 : 0);
+        bar_expect(bar, boxes * 8 * pitch);
       }
+      __syncwarp();
+      if (lane == 0 ? ok & 0xff : lane == 8 && a.box == 8 && (ok >> 8))
+        tile_rows(dst + lane * pitch, kv ? &map_v : &map_k, kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK), row, bar);
       if (lane < 16)
-        sts_u32(sl + 64 * kv + 4 * lane, kv && lane >= n ? smem_u32(s_zero) : dst + lane * pitch + (kv ? shift_v : shift_k));
+        sts_u32(sl + 64 * kv + 4 * lane, kv && !in ? smem_u32(s_zero) : dst + lane * pitch + (kv ? shift_v : shift_k));
       return;
     }
     const uint8_t* pool = kv ? a.c.v : a.c.k;
@@ -760,14 +817,11 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
     }
   };
 
-  long long u = u0;
-  int off = s_off;
-  bool dead = false;  // a wait ran out: no more work is issued
-  Segment sg = segment(s_seq, off, u, 0);
   prefetch(sg);
   load_q(sg);
   __syncthreads();
-  for (int seg = 0; u < u1; ++seg) {
+  bool dead = false;  // a wait ran out: no more work is issued
+  {
     // ---- the warp's tiles
     const float qscale = a.scale / s_qs[g];
     const float slope = a.alibi && g < nh ? a.alibi[head0 + g] : 0.f;
@@ -778,7 +832,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
-    const int ntile = dead ? 0 : sg.ntile;
+    const int ntile = sg.ntile;
     int next = warp + SLOTS * NW;
     Where ahead = where(sg, next);
     for (int tile = warp; tile < ntile; tile += NW, next += NW) {
@@ -839,7 +893,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
       if (next < ntile) fetch(sg, 1, slot, row, next);
       if (++slot == SLOTS) slot = 0;
     }
-    if (dead && ntile > 0) {  // let the copies in flight land: nothing more is issued
+    if (dead) {  // let the copies in flight land: nothing more is issued
       if (lane == 0) {
         atomicExch(a.c.err, FA_ERR_TIMEOUT);
         for (int i = 0; i < 8; ++i)
@@ -847,23 +901,16 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
       }
       __syncwarp();
     }
-    // ---- the next segment's first copies
-    const Segment cur = sg;
-    const int take = units_of(cur.j1 - cur.j0);
-    u += max(take, 1);
-    if (u >= u1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    sg = segment(cur.b + 1 < B ? cur.b + 1 : cur.b, 0, u, seg + 1);
-    if (!dead) prefetch(sg);
-    // ---- the warps' sums, joined in the warps' order
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ---- the warps' sums (in their rings), joined in the warps' order
     l += __shfl_xor_sync(kFull, l, 1);
     l += __shfl_xor_sync(kFull, l, 2);
     if (t == 0) s_ml[warp][g] = m, s_ml[warp][8 + g] = l;
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[((warp * (DV / 16) + n) * 4 + i) * 32 + lane] = o[n][i];
+      for (int i = 0; i < 4; ++i) acc[warp * kSums + (n * 4 + i) * 32 + lane] = o[n][i];
     __syncthreads();
-    if (u < u1) load_q(sg);
     float M[2] = {-INFINITY, -INFINITY}, S[2] = {0.f, 0.f}, fw[2][NW];  // heads 2t, 2t + 1
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -876,25 +923,25 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
         S[i] = fmaf(s_ml[w][8 + 2 * t + i], fw[i][w], S[i]);
       }
     }
-    float* part = a.part + ((long long)(r * a.HG + hg) * 2 + (seg == 0 ? 0 : 1)) * (8 * DV + 16);
+    float* part = a.part + ((long long)item.w * a.HG + hg) * (8 * DV + 16);  // (a split sequence's)
     float fin[2], lse[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float total = S[i], top = M[i], f = 1.f;
-      if (cur.whole && a.sinks && 2 * t + i < nh) {  // one more term of the sum, without a value
+      if (whole && a.sinks && 2 * t + i < nh) {  // one more term of the sum, without a value
         const float sk = a.sinks[head0 + 2 * t + i] * kLog2e;
         top = fmaxf(M[i], sk);
         f = M[i] == -INFINITY ? 0.f : exp2f(M[i] - top);
         total = S[i] * f + exp2f(sk - top + kLift);
       }
-      fin[i] = cur.whole ? (total > 0.f ? f / total : 0.f) : 1.f;
+      fin[i] = whole ? (total > 0.f ? f / total : 0.f) : 1.f;
       lse[i] = total > 0.f ? (top - kLift + log2f(total)) * kLn2 : -INFINITY;
     }
     for (int n = warp; n < DV / 16; n += NW) {
       float x[4] = {};
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float* p = acc + (w * (DV / 16) + n) * 128 + lane;
+        const float* p = acc + w * kSums + n * 128 + lane;
         x[0] = fmaf(p[0], fw[0][w], x[0]), x[1] = fmaf(p[32], fw[1][w], x[1]);
         x[2] = fmaf(p[64], fw[0][w], x[2]), x[3] = fmaf(p[96], fw[1][w], x[3]);
       }
@@ -902,7 +949,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
       for (int i = 0; i < 4; ++i) {
         const int h = 2 * t + (i & 1), d = v_comp(VT, n, g, i >> 1);
         if (h < nh) {
-          if (cur.whole) act_store(a.O, a.act, ((long long)cur.b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
+          if (whole) act_store(a.O, a.act, ((long long)sg.b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
           else part[h * DV + d] = x[i];
         }
       }
@@ -911,81 +958,77 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = 2 * t + i;
-        if (h < nh && cur.whole && a.lse) a.lse[(long long)cur.b * a.H + head0 + h] = lse[i];
-        if (!cur.whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
+        if (h < nh && whole && a.lse) a.lse[(long long)sg.b * a.H + head0 + h] = lse[i];
+        if (!whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
       }
     }
-    __syncthreads();
   }
-  if (hg == 0 && threadIdx.x == 0) a.jobs[r] = job;
 }
 
-// Joins the partial sums of a sequence that several ranges took, in the ranges' order.  blockIdx.x: the
-// range that begins it, blockIdx.y: query head.  The grid starts while the ranges' last CTAs run.
+// Joins the parts of a split sequence (blockIdx.x), in their order, for a query head (blockIdx.y).  The grid
+// starts while the items' last CTAs run.  Each group of threads takes every GR-th part with a running
+// maximum, then the groups are joined.
 template <int DV>
-__global__ void __launch_bounds__(256) k_decode_join(const DecodeArgs a) {
-  constexpr int LN = DV / 4, GR = 256 / LN;  // threads of a row (four components each), rows read at a time
-  __shared__ float s_f[256], s_red[8];
-  __shared__ float4 s_x[256];
+__global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
+  constexpr int LN = DV / 4, GR = 512 / LN;  // threads of a row (four components each), rows read at a time
+  __shared__ float s_m[GR], s_l[GR];
+  __shared__ float4 s_x[512];
+  const int h = blockIdx.y, hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
+  const int tid = threadIdx.x, ln = tid % LN, gr = tid / LN;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = a.jobs[blockIdx.x];
   if (job.x < 0) return;
-  const int h = blockIdx.y, hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
-  const int tid = threadIdx.x, ln = tid % LN, gr = tid / LN, r0 = blockIdx.x, np = job.y - r0 + 1;
-  auto part = [&](int i) {
-    return a.part + ((long long)((r0 + i) * a.HG + hg) * 2 + (i == 0 ? job.z : 0)) * (8 * DV + 16);
-  };
-  auto block = [&](float v, bool mx) {  // the block's maximum or sum, in a fixed order
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float w = __shfl_xor_sync(kFull, v, o);
-      v = mx ? fmaxf(v, w) : v + w;
-    }
-    __syncthreads();
-    if ((tid & 31) == 0) s_red[tid >> 5] = v;
-    __syncthreads();
-    v = s_red[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) v = mx ? fmaxf(v, s_red[w]) : v + s_red[w];
-    return v;
-  };
-  float M = -INFINITY;
-  for (int i = tid; i < np; i += 256) M = fmaxf(M, part(i)[8 * DV + c]);
-  M = block(M, true);
-  const float sk = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
-  const float top = fmaxf(M, sk), ref = top == -INFINITY ? 0.f : top;
-  float S = 0.f;
+  const int np = job.z;
+  float M = -INFINITY, S = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < np; i0 += 256) {
-    __syncthreads();
-    if (i0 + tid < np) {
-      const float* p = part(i0 + tid) + 8 * DV + c;
-      s_f[tid] = exp2f(p[0] - ref);
-      S = fmaf(p[8], s_f[tid], S);
+  constexpr int Q = 4;  // parts under way at a time
+  for (int i0 = gr; i0 < np; i0 += Q * GR) {
+    float m[Q], l[Q];
+    float4 v[Q];
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      const int i = i0 + k * GR;
+      m[k] = -INFINITY, l[k] = 0.f, v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < np) {
+        const float* p = a.part + ((long long)(job.y + i) * a.HG + hg) * (8 * DV + 16);
+        m[k] = p[8 * DV + c], l[k] = p[8 * DV + 8 + c], v[k] = *reinterpret_cast<const float4*>(p + c * DV + 4 * ln);
+      }
     }
-    __syncthreads();
-    const int n = min(256, np - i0);
-#pragma unroll 4
-    for (int i = gr; i < n; i += GR) {
-      const float4 v = *reinterpret_cast<const float4*>(part(i0 + i) + c * DV + 4 * ln);
-      const float f = s_f[i];
-      x.x = fmaf(v.x, f, x.x), x.y = fmaf(v.y, f, x.y), x.z = fmaf(v.z, f, x.z), x.w = fmaf(v.w, f, x.w);
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < Q; ++k) top = fmaxf(top, m[k]);
+    const float ref = top == -INFINITY ? 0.f : top, f0 = fab::ex2(M - ref);
+    M = top, S *= f0;
+    x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      const float f = fab::ex2(m[k] - ref);
+      S = fmaf(l[k], f, S);
+      x.x = fmaf(v[k].x, f, x.x), x.y = fmaf(v[k].y, f, x.y), x.z = fmaf(v[k].z, f, x.z), x.w = fmaf(v[k].w, f, x.w);
     }
   }
-  S = block(S, false);
-  if (a.sinks) S += exp2f(sk - ref + kLift);
+  if (ln == 0) s_m[gr] = M, s_l[gr] = S;
   s_x[tid] = x;
   __syncthreads();
-  if (gr == 0) {
-    for (int i = 1; i < GR; ++i) {
-      const float4 v = s_x[i * LN + ln];
-      x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
-    }
-    const float inv = S > 0.f ? 1.f / S : 0.f;
-    const long long at = ((long long)job.x * a.H + h) * DV + 4 * ln;
-    act_store(a.O, a.act, at, x.x * inv), act_store(a.O, a.act, at + 1, x.y * inv);
-    act_store(a.O, a.act, at + 2, x.z * inv), act_store(a.O, a.act, at + 3, x.w * inv);
+  if (gr > 0) return;
+  const float sk = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
+  float top = sk;
+#pragma unroll
+  for (int i = 0; i < GR; ++i) top = fmaxf(top, s_m[i]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  S = 0.f, x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < GR; ++i) {
+    const float f = fab::ex2(s_m[i] - ref);
+    const float4 v = s_x[i * LN + ln];
+    S = fmaf(s_l[i], f, S);
+    x.x = fmaf(v.x, f, x.x), x.y = fmaf(v.y, f, x.y), x.z = fmaf(v.z, f, x.z), x.w = fmaf(v.w, f, x.w);
   }
+  if (a.sinks) S += fab::ex2(sk - ref + kLift);
+  const float inv = S > 0.f ? 1.f / S : 0.f;
+  const long long at = ((long long)job.x * a.H + h) * DV + 4 * ln;
+  act_store(a.O, a.act, at, x.x * inv), act_store(a.O, a.act, at + 1, x.y * inv);
+  act_store(a.O, a.act, at + 2, x.z * inv), act_store(a.O, a.act, at + 3, x.w * inv);
   if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
 }
 
@@ -996,13 +1039,14 @@ cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s)
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
   cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, KT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C.smem);
   if (e != cudaSuccess) return e;
-  k_decode<D, DV, KT, VT><<<a.R * a.HG, C.nw * 32, C.smem, s>>>(a, m.k, m.v);
-  if (a.R > 1) {
+  if (a.items) k_decode_plan<<<1, 1024, 0, s>>>(a);
+  k_decode<D, DV, KT, VT><<<(unsigned)(a.nitems * a.HG), C.nw * 32, C.smem, s>>>(a, m.k, m.v);
+  if (a.njobs > 0) {
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.R, a.H), cfg.blockDim = dim3(256), cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    cfg.gridDim = dim3(a.njobs, a.H), cfg.blockDim = dim3(512), cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, k_decode_join<DV>, a)) != cudaSuccess) return e;
   }
   return cudaGetLastError();
