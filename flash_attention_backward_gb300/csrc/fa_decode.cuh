@@ -459,7 +459,7 @@ __host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, in
   c.pk = smem_pitch(cache_row_bytes(kt, D)), c.pv = smem_pitch(cache_row_bytes(vt, DV));
   c.qf = (kt == FA_F32 ? D / 8 : D / 16) * 512;
   c.stage = 16 * (c.pk + c.pv);
-  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 2048;
+  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 3072;
   c.nw = FA_NW;
   c.ctas = (DV == 256 ? 12 : 16) / c.nw;
   while (c.ctas > 1 && fixed + c.nw * (slot > sums ? slot : sums) > kSmemSm / c.ctas) --c.ctas;
@@ -490,18 +490,42 @@ __device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
 
 // ---- the items of work: a sequence of n tiles is cut into ceil(n / chunk) of nearly equal size.  The chunk
-// is what makes all items of U tiles fit the card at once (an item a sequence more than U / chunk at
-// most), but not so small that joining the parts costs more than it gains: with w tiles an item a
-// sequence of n takes about w / 4 tile times and n / w parts, least near w = 0.37 sqrt(n) as measured.
-__device__ __forceinline__ int chunk_tiles(long long U, int B, int R) {
+// is what makes the items of all U tiles fit the card at once (R items), but not so small that joining the
+// parts costs more than it gains: with w tiles an item a sequence of n takes about w / 4 tile times and
+// n / w parts, least near w = 0.37 sqrt(n) as measured.  A chunk of U / (R - B) always fits, U / R never
+// unless all divide; chunks between the two are tried where the batch is small (fit_chunk).  Whatever
+// chunk is taken is at least U / R, so there are at most R + B items, R split sequences and 2 R parts.
+__device__ __forceinline__ int least_chunk(long long U, int R) {
+  return (int)max((long long)max(kMinTiles, (int)(0.37f * sqrtf((float)U))), (U + R - 1) / R);
+}
+__device__ __forceinline__ int safe_chunk(long long U, int B, int R) {
   const long long room = max(R - B, (R + 1) / 2);
-  return (int)max((long long)max(kMinTiles, (int)(0.37f * sqrtf((float)U))), (U + room - 1) / room);
+  return (int)max((long long)least_chunk(U, R), (U + room - 1) / room);
+}
+// The least of the block's candidates between the two whose items fit (tiles: the B sequences'), if that
+// saves more than joining further parts costs (about six tile times of a warp); all threads get it.  (A
+// rounding here costs a wave, not correctness.)
+template <int NW>
+__device__ __forceinline__ int fit_chunk(const int* tiles, int B, int R, int lo, int hi, int* smem) {
+  constexpr int kWorth = 6 * NW;
+  if (hi - lo <= kWorth) return hi;
+  const int c = lo + (int)((long long)(hi - lo) * threadIdx.x / (NW * 32 - 1));
+  const uint32_t inv = (uint32_t)((0x100000000ull + c - 1) / c);
+  int items = 0;
+  for (int b = 0; b < B; ++b) items += (int)((uint64_t)(uint32_t)(tiles[b] + c - 1) * inv >> 32);
+  int best = items <= R ? c : hi;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(kFull, best, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = best;
+  __syncthreads();
+  for (int w = 0; w < NW; ++w) best = min(best, smem[w]);
+  return hi - best > kWorth ? best : hi;
 }
 // What a sequence adds to the running counts: items, and for one that is split its slots and itself
 struct Counts {
   int items, slots, split;
 };
-// slots and split sequences stay below 2 R and R (each split one has over a chunk of the at most R chunks)
 __device__ __forceinline__ uint64_t pack_counts(int n, int chunk) {
   const uint32_t s = (n + chunk - 1) / chunk;
   return (uint64_t)s | (s > 1 ? ((uint64_t)s << 32) + (1ull << 48) : 0ull);
@@ -540,7 +564,7 @@ static __global__ void __launch_bounds__(1024) k_decode_plan(const DecodeArgs a)
     const int b = c0 + threadIdx.x;
     U += block_scan<32, uint64_t>(b < B ? tiles_of(seq_keys(a, b)) : 0, s_scan, &before);
   }
-  const int chunk = chunk_tiles((long long)U, B, a.R);
+  const int chunk = safe_chunk((long long)U, B, a.R);
   uint64_t base = 0;
   for (int c0 = 0; c0 < B; c0 += 1024) {
     const int b = c0 + threadIdx.x;
@@ -641,6 +665,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_scan[NW];
   __shared__ int4 s_item;
+  __shared__ int s_tiles[kPlanBatch];
   __shared__ float s_qs[8], s_ml[NW][16];
   // a slot: where its 16 key rows and its 16 value rows start, the barriers of either, the tile's key mask
   struct Slot {
@@ -673,13 +698,15 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
     for (int c0 = 0; c0 < B; c0 += NW * 32) {
       const int b = c0 + threadIdx.x;
       n_own = b < B ? tiles_of(seq_keys(a, b)) : 0;
+      if (b < B) s_tiles[b] = n_own;
       U += block_scan<NW, uint64_t>(n_own, s_scan, &before);
     }
-    const int chunk = chunk_tiles((long long)U, B, a.R);
+    const int chunk = fit_chunk<NW>(s_tiles, B, a.R, least_chunk((long long)U, a.R), safe_chunk((long long)U, B, a.R),
+                                    reinterpret_cast<int*>(s_scan));
     const bool lists = r == 0 && hg == 0;  // this CTA lists the split sequences
     for (int c0 = 0; c0 < B; c0 += NW * 32) {
       const int b = c0 + threadIdx.x;
-      if (B > NW * 32) n_own = b < B ? tiles_of(seq_keys(a, b)) : 0;
+      if (B > NW * 32) n_own = b < B ? s_tiles[b] : 0;
       const uint64_t v = pack_counts(n_own, chunk), all = block_scan<NW, uint64_t>(v, s_scan, &before);
       const Counts at = unpack_counts(base + before), own = unpack_counts(v);
       if (at.items <= r && r < at.items + own.items) s_item = make_int4(b, own.items, r - at.items, at.slots + r - at.items);
@@ -717,26 +744,26 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
   const bool whole = item.y == 1;
 
   // ---- rows of a tile: key `lane` & 15 a lane.  Boxes of rows (16 or 8 in one page) go by the tensor maps,
-  // else each row is copied by itself.  Page numbers are fetched a tile ahead of the copies that they are
-  // for.
-  struct Where {
-    int page, off;
+  // else each row is copied by itself.  The first rows of the warp's next 32 boxes are looked up at once, a
+  // box a lane; single rows a tile at a time.
+  const int boxes = a.box == 8 ? 2 : 1, per_batch = 32 / boxes;  // boxes of a tile, tiles of a lookup
+  auto lookup = [&](int j) {  // row of the pool of key j, -1 where there is none
+    if (j >= sg.j1) return -1;
+    const int p = (int)((uint64_t)j * a.page_mul >> a.page_shift);
+    const int page = __ldg(a.c.table + (long long)sg.b * a.c.max_pages + p);
+    if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + (j - p * a.c.page_size);
+    *a.c.err = FA_ERR_PAGE;
+    return -1;
   };
-  const int key_lane = a.box == 16 ? 0 : a.box == 8 ? lane & 8 : lane & 15;  // the first key of the lane's box
-  auto where = [&](const Segment& s, int tile) {
-    const int j = s.j0 + tile * 16 + key_lane;
-    Where w = {-1, 0};
-    if (tile < s.ntile && j < s.j1) {
-      const int p = (int)((uint64_t)j * a.page_mul >> a.page_shift);
-      w.page = __ldg(a.c.table + (long long)s.b * a.c.max_pages + p), w.off = j - p * a.c.page_size;
-      if (w.page < 0) w.page = 0x7fffffff;
+  int found = -1, found_at = -1000;  // the lookup's rows, and the warp's turn that it starts with
+  auto row_of = [&](int turn) {  // of the warp's turn-th tile
+    if (!a.box) return lookup(sg.j0 + 16 * (warp + NW * turn) + (lane & 15));
+    if (turn - found_at >= per_batch) {
+      const int l = a.box == 8 ? lane >> 1 : lane;
+      found = lookup(sg.j0 + 16 * (warp + NW * (turn + l)) + (a.box == 8 ? 8 * (lane & 1) : 0));
+      found_at = turn;
     }
-    return w;
-  };
-  auto row_of = [&](const Where& w) {
-    const bool ok = w.page >= 0 && w.page < a.c.num_pages;
-    if (w.page >= 0 && !ok) *a.c.err = FA_ERR_PAGE;
-    return ok ? w.page * a.c.page_size + w.off : -1;
+    return __shfl_sync(kFull, found, (turn - found_at) * boxes + (a.box == 8 ? (lane >> 3) & 1 : 0));
   };
   uint32_t phases = 0, armed = 0;  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way
   auto fetch = [&](const Segment& s, int kv, int slot, int row, int tile) {
@@ -781,7 +808,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
     for (int i = 0, sl = slot; i < SLOTS; ++i) {
       const int tile = warp + i * NW;
       if (tile < s.ntile) {
-        const int row = row_of(where(s, tile));
+        const int row = row_of(i);
         fetch(s, 0, sl, row, tile), fetch(s, 1, sl, row, tile);
       }
       if (++sl == SLOTS) sl = 0;
@@ -833,11 +860,9 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
     const int ntile = sg.ntile;
-    int next = warp + SLOTS * NW;
-    Where ahead = where(sg, next);
-    for (int tile = warp; tile < ntile; tile += NW, next += NW) {
-      const int row = row_of(ahead);
-      ahead = where(sg, next + NW);
+    int next = warp + SLOTS * NW, turn = SLOTS;
+    for (int tile = warp; tile < ntile; tile += NW, next += NW, ++turn) {
+      const int row = next < ntile ? row_of(turn) : -1;
       const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), qa = qf + lane * 16;
       dead = !arrived(0, slot);
       if (dead) break;

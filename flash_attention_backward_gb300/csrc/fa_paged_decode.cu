@@ -45,12 +45,11 @@ static DecodePlan plan_decode(const Cache& c, int H, int nsm) {
   p.HG = c.Hkv * p.chunks;
   const int ctas = decode_shape(c.D, c.Dv, c.k_type, c.v_type).ctas;
   p.R = std::max(1, ctas * nsm / p.HG);  // items that run at a time
-  // at most so many: one a sequence, and one for each chunk of at least a share of the room, or kMinTiles
+  // at most R + B (see fa_decode.cuh), and no more than tables of this width can ask for
   const long long cap = ((long long)c.max_pages * c.page_size + 15) / 16, per = (cap + kMinTiles - 1) / kMinTiles;
-  const long long room = std::max(p.R - c.B, (p.R + 1) / 2);
-  p.nitems = (int)std::max(1LL, std::min(c.B * std::max(per, 1LL), room + c.B));
+  p.nitems = (int)std::max(1LL, std::min<long long>(c.B * std::max(per, 1LL), (long long)p.R + c.B));
   p.njobs = per > 1 ? std::min(c.B, p.R) : 0;  // split sequences: none if no sequence can be
-  const size_t slots = p.njobs ? std::min<long long>(2LL * p.R, p.nitems) : 0;
+  const size_t slots = p.njobs ? std::min(2 * p.R, p.nitems) : 0;
   p.planned = c.B > kPlanBatch;
   p.off_jobs = slots * p.HG * (8 * c.Dv + 16) * sizeof(float);
   p.off_items = p.off_jobs + (size_t)std::max(p.njobs, 1) * sizeof(int4);
