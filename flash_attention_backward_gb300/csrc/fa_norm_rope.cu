@@ -150,7 +150,9 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
   a.side[0].gy = gq, a.side[1].gy = gk, a.side[0].y = dq, a.side[1].y = dk;
   a.part = static_cast<float*>(workspace);
-  for (NormSide& sd : a.side) chunk_heads(sd.H, rows_a_warp(a, D, nsm), 256 / D, kBackHeads, &sd.HC, &sd.nchunk);
+  a.err = err;
+  const BackKernel k_back = pick_norm_back(D, x_type, y_type, a.vec, a.rope.style);
+  for (NormSide& sd : a.side) sd.nchunk = (sd.H + k_back.heads - 1) / k_back.heads;
   // CTAs shared out by the heads of either side; every side that has heads gets one
   const long long iq = (long long)N * a.side[0].nchunk, ik = (long long)N * a.side[1].nchunk;
   if (iq > 0x7fffffffLL || ik > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -159,7 +161,10 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
   const int cq = (int)std::min<long long>(all - ck, std::max(1LL, (iq + 7) / 8));
   a.ctas_q = cq;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  pick_norm_back(D, x_type, y_type, a.vec, a.rope.style)<<<cq + ck, 256, 0, s>>>(a);
+  if (k_back.smem > 48 * 1024 &&
+      cudaFuncSetAttribute(k_back.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k_back.smem) != cudaSuccess)
+    return FA_ERR_CUDA;
+  k_back.fn<<<cq + ck, kBackWarps * 32, k_back.smem, s>>>(a);
   float* oq = wq ? dwq : nullptr;
   float* ok = wk && Hkv ? dwk : nullptr;
   if (oq || ok) k_dw_reduce<<<dim3(D / 32, 2), dim3(32, 32), 0, s>>>(a.part, cq, cq + ck, D, oq, ok);

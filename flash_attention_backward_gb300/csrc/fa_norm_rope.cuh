@@ -12,6 +12,7 @@
 // token are computed once for all heads of it that a warp takes.
 #pragma once
 #include "fa_paged.cuh"
+#include "sm100.cuh"
 
 namespace fap {
 
@@ -22,7 +23,7 @@ struct NormSide {  // queries or keys
   const float* w;
   void* y;             // y, or dx
   int H;               // heads
-  int HC, nchunk;      // backward: heads of one token that a warp takes, chunks of a token
+  int nchunk;          // backward: chunks of a token's heads
 };
 struct NormArgs {
   NormSide side[2];
@@ -34,17 +35,13 @@ struct NormArgs {
   int N;
   bool vec;            // both start every head of x on 16 bytes (or have none)
   float* part;         // backward: [CTA][D] sums of dw
+  int* err;
 };
 
 // Rows that a lane group has under way at a time: 32 or 64 bytes a lane of x (and as much of gy).
 template <typename T>
 constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
-#ifndef FA_BC
-#define FA_BC 2
-#define FA_BR 2
-#define FA_BM 16
-#endif
-constexpr int kBackRows = FA_BR, kBackCtas = FA_BC, kBackHeads = FA_BM;
+constexpr uint64_t kCopyLimitNs = 2000000000ull;  // a wait for a copy gives up after this long
 
 // A lane's four rotation pairs: components [ea, ea + 4) and [eb, eb + 4) of the head.
 //   FA_ROPE_HALVES  pair i is (x[ea + i], x[eb + i]).  The rotated components are pairs 0 .. n_rot / 2 - 1
@@ -234,12 +231,132 @@ __global__ void __launch_bounds__(256) k_norm_rope(const NormArgs a) {
   }
 }
 
-// The same shape, in a loop over the items; dw is summed by lane over all of them, then over the CTA's
-// lane groups in order.
-template <int D, typename TX, typename TY, bool VEC, int STYLE>
-__global__ void __launch_bounds__(256, kBackCtas) k_norm_rope_back(const NormArgs a) {
-  constexpr int GW = 256 / D, U = kBackRows;
-  __shared__ float red[8 * GW][D];
+// The gradient.  Each warp takes a run of items (HC heads of a token), which pass through a ring of its own
+// in shared memory: bulk copies bring x and gy of the items to come while one is worked on, which takes
+// the loads off the registers and the issue slots.  A token's factors are computed when the run comes to
+// it.  dw is summed by lane over the run, then over the CTA's lane groups in order.
+constexpr int kBackCtas = 2, kBackSlots = 3, kBackWarps = 8;
+// Heads of an item: what a slot of 4 KB holds, in multiples of those side by side in a warp
+template <int D, typename TX, typename TY>
+constexpr int kBackHeads = 4096 / (256 * (int)(sizeof(TX) + sizeof(TY))) * (256 / D);
+
+__device__ __forceinline__ void bulk_run(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+template <int D, typename TX, typename TY, int GROUPS>
+__device__ __forceinline__ void sum_dw(const NormArgs& a, const float2 (&dw)[4], int ea, int eb, int group, float (*red)[D]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float* ra = &red[group][ea + 2 * i];
+    float* rb = &red[group][eb + 2 * i];
+    ra[0] = dw[i].x, ra[1] = dw[i].y, rb[0] = dw[2 + i].x, rb[1] = dw[2 + i].y;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < D; c += kBackWarps * 32) {
+    float s = 0.f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) s += red[g][c];
+    a.part[(long long)blockIdx.x * D + c] = s;
+  }
+}
+
+template <int D, typename TX, typename TY, int STYLE>
+__global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(const NormArgs a) {
+  constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>, GB = HC * D * sizeof(TY), XB = HC * D * sizeof(TX), S = kBackSlots;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[kBackWarps * GW][D];
+  __shared__ uint64_t s_bar[kBackWarps][S];
+  const bool isq = blockIdx.x < a.ctas_q;
+  const NormSide sd = a.side[isq ? 0 : 1];
+  const int lane = threadIdx.x & 31, grp = lane / (D / 8), warp = threadIdx.x >> 5;
+  const int ctas = isq ? a.ctas_q : gridDim.x - a.ctas_q, me = (blockIdx.x - (isq ? 0 : a.ctas_q)) * kBackWarps + warp;
+  const unsigned items = (unsigned)a.N * sd.nchunk;
+  const unsigned first = (unsigned)((unsigned long long)items * me / (ctas * kBackWarps));
+  const unsigned last = (unsigned)((unsigned long long)items * (me + 1) / (ctas * kBackWarps));
+  const uint32_t slots = fab::smem_u32(ring) + warp * S * (GB + XB);
+  if (lane < S) fab::mbar_init(&s_bar[warp][lane], 1);
+  fab::fence_mbar_init();
+  __syncwarp();
+
+  float2 dw[4] = {};
+  Lane<D, STYLE> ln;
+  ln.place(a.rope);
+  ln.weights(sd.w);
+  // token and first head of the next item to fetch, and of the one to work on
+  int fn = first / (unsigned)sd.nchunk, fh = (int)(first - (unsigned)fn * sd.nchunk) * HC, n = fn, h = fh;
+  unsigned fetched = first;
+  auto fetch = [&](int slot) {
+    const int cnt = min(HC, sd.H - fh);
+    const uint32_t at = slots + slot * (GB + XB), bar = fab::smem_u32(&s_bar[warp][slot]);
+    const TX* x = static_cast<const TX*>(sd.x) + fn * sd.row + fh * sd.head;
+    if (lane == 0) {
+      fab::mbar_arrive_expect_tx(&s_bar[warp][slot], cnt * D * (sizeof(TY) + (ln.norm ? sizeof(TX) : 0)));
+      bulk_run(at, static_cast<const TY*>(sd.gy) + ((long long)fn * sd.H + fh) * D, cnt * D * sizeof(TY), bar);
+      if (ln.norm && sd.head == D) bulk_run(at + GB, x, cnt * D * sizeof(TX), bar);
+    }
+    if (ln.norm && sd.head != D) {
+      __syncwarp();
+      if (lane < cnt) bulk_run(at + GB + lane * D * (int)sizeof(TX), x + lane * sd.head, D * sizeof(TX), bar);
+    }
+    ++fetched;
+    if ((fh += HC) >= sd.H) fh = 0, ++fn;
+  };
+  for (int i = 0; i < S; ++i)
+    if (fetched < last) fetch(i);
+  int slot = 0, token = -1;
+  uint32_t phase = 0;
+  auto pos_of = [&](int t) { return a.rope.n_rot && t < a.N ? a.pos[t] : 0; };
+  int pos = pos_of(n);
+  for (unsigned item = first; item < last; ++item) {
+    if (n != token) {
+      ln.turn(a.rope, pos, -1.f);
+      token = n, pos = pos_of(n + 1);  // the next token's, in time
+    }
+    const bool came = fab::mbar_wait_bounded(&s_bar[warp][slot], phase, kCopyLimitNs);
+    if (!__all_sync(kFull, came)) {  // wait once more for the other slots' copies, then give up
+      if (lane == 0) {
+        atomicExch(a.err, FA_ERR_TIMEOUT);
+        for (unsigned k = item; k < fetched; ++k) {
+          fab::mbar_wait_bounded(&s_bar[warp][slot], phase, kCopyLimitNs);
+          if (++slot == S) slot = 0, phase ^= 1;
+        }
+      }
+      break;
+    }
+    const int cnt = min(HC, sd.H - h);
+    const TY* gs = reinterpret_cast<const TY*>(ring + warp * S * (GB + XB) + slot * (GB + XB));
+    const TX* xs = reinterpret_cast<const TX*>(reinterpret_cast<const uint8_t*>(gs) + GB);
+    TX* d0 = static_cast<TX*>(sd.y) + ((long long)n * sd.H + h + grp) * D;
+#pragma unroll 2
+    for (int k = 0; k < cnt; k += GW) {
+      const int hh = min(k + grp, cnt - 1);  // lanes without a head of their own work on the last, unheeded
+      Eight<TX> rx;
+      Eight<TY> rg;
+      float2 x[4], g[4];
+      load_eight<TY, true>(gs + hh * D, ln.ea, ln.eb, rg);
+      if (ln.norm) load_eight<TX, true>(xs + hh * D, ln.ea, ln.eb, rx);
+      unpack_eight(rg, g);
+      unpack_eight(rx, x);
+      const bool on = k + grp < cnt;
+      ln.backward(x, g, dw, a.eps, on);
+      if (on) store_eight(d0 + k * D, ln.ea, ln.eb, g);
+    }
+    __syncwarp();
+    if (fetched < last) fetch(slot);
+    if (++slot == S) slot = 0, phase ^= 1;
+    if ((h += HC) >= sd.H) h = 0, ++n;
+  }
+  if (ln.norm) sum_dw<D, TX, TY, kBackWarps * GW>(a, dw, ln.ea, ln.eb, warp * GW + grp, red);
+}
+
+// The gradient where heads of x do not start on 16 bytes: element by element.
+template <int D, typename TX, typename TY, int STYLE>
+__global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_any(const NormArgs a) {
+  constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>;
+  __shared__ float red[kBackWarps * GW][D];
   const bool isq = blockIdx.x < a.ctas_q;
   const NormSide sd = a.side[isq ? 0 : 1];
   const int grp = (threadIdx.x & 31) / (D / 8), warp = threadIdx.x >> 5;
@@ -249,63 +366,37 @@ __global__ void __launch_bounds__(256, kBackCtas) k_norm_rope_back(const NormArg
   Lane<D, STYLE> ln;
   ln.place(a.rope);
   ln.weights(sd.w);
-  for (unsigned item = cta * 8 + warp; item < items; item += ctas * 8) {
-    const int n = item / (unsigned)sd.nchunk, h0 = (int)(item - (unsigned)n * sd.nchunk) * sd.HC;
-    int left = min(sd.H - h0, sd.HC);
+  for (unsigned item = cta * kBackWarps + warp; item < items; item += ctas * kBackWarps) {
+    const int n = item / (unsigned)sd.nchunk, h0 = (int)(item - (unsigned)n * sd.nchunk) * HC, cnt = min(sd.H - h0, HC);
     const long long at = ((long long)n * sd.H + h0) * D;
-    const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + h0 * sd.head;
-    const TY* g0 = static_cast<const TY*>(sd.gy) + at;
-    TX* d0 = static_cast<TX*>(sd.y) + at + grp * D;
-    Eight<TX> rx[U];
-    Eight<TY> rg[U];
-    auto fetch = [&] {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u * GW < left) {
-          const int h = min(grp + u * GW, left - 1);
-          load_eight<TY, true>(g0 + h * D, ln.ea, ln.eb, rg[u]);
-          if (ln.norm) load_eight<TX, VEC>(x0 + h * sd.head, ln.ea, ln.eb, rx[u]);
-        }
-    };
-    fetch();
     ln.turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, -1.f);
-    for (;;) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u * GW >= left) break;  // (the same in all lanes)
-        const bool on = grp + u * GW < left;
-        float2 x[4], g[4];
-        unpack_eight(rg[u], g);
-        unpack_eight(rx[u], x);
-        ln.backward(x, g, dw, a.eps, on);
-        if (on) store_eight(d0 + u * GW * D, ln.ea, ln.eb, g);
-      }
-      left -= U * GW;
-      if (left <= 0) break;
-      x0 += U * GW * sd.head, g0 += U * GW * D, d0 += U * GW * D;
-      fetch();
+#pragma unroll 1
+    for (int k = 0; k < cnt; k += GW) {
+      const int hh = min(k + grp, cnt - 1);
+      Eight<TX> rx;
+      Eight<TY> rg;
+      float2 x[4], g[4];
+      load_eight<TY, true>(static_cast<const TY*>(sd.gy) + at + hh * D, ln.ea, ln.eb, rg);
+      if (ln.norm) load_eight<TX, false>(static_cast<const TX*>(sd.x) + n * sd.row + (h0 + hh) * sd.head, ln.ea, ln.eb, rx);
+      unpack_eight(rg, g);
+      unpack_eight(rx, x);
+      const bool on = k + grp < cnt;
+      ln.backward(x, g, dw, a.eps, on);
+      if (on) store_eight(static_cast<TX*>(sd.y) + at + (k + grp) * D, ln.ea, ln.eb, g);
     }
   }
-  if (!ln.norm) return;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float* ra = &red[warp * GW + grp][ln.ea + 2 * i];
-    float* rb = &red[warp * GW + grp][ln.eb + 2 * i];
-    ra[0] = dw[i].x, ra[1] = dw[i].y, rb[0] = dw[2 + i].x, rb[1] = dw[2 + i].y;
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < D; c += 256) {
-    float s = 0.f;
-#pragma unroll
-    for (int g = 0; g < 8 * GW; ++g) s += red[g][c];
-    a.part[(long long)blockIdx.x * D + c] = s;
-  }
+  if (ln.norm) sum_dw<D, TX, TY, kBackWarps * GW>(a, dw, ln.ea, ln.eb, warp * GW + grp, red);
 }
 
 typedef void (*NormKernel)(const NormArgs);
 
-// The kernel for these types (fa_norm_rope_fwd.cu, fa_norm_rope_back.cu)
+// The kernels for these types (fa_norm_rope_fwd.cu, fa_norm_rope_back.cu); of the gradient's, the heads of an
+// item and the bytes of dynamic shared memory too.
 NormKernel pick_norm_fwd(int D, int tx, int ty, bool vec, int style);
-NormKernel pick_norm_back(int D, int tx, int ty, bool vec, int style);
+struct BackKernel {
+  NormKernel fn;
+  int heads, smem;
+};
+BackKernel pick_norm_back(int D, int tx, int ty, bool vec, int style);
 
 }  // namespace fap
