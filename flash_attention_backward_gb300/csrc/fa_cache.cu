@@ -17,8 +17,11 @@ fa_status check_cache(const fa_paged_cache* c, Cache* out) {
   if (((long long)c->page_size * c->Hkv * rbk) % 16 || ((long long)c->page_size * c->Hkv * rbv) % 16) return FA_ERR_ALIGN;
   if ((c->num_pages > 0 && (!c->k || !c->v)) || (c->B > 0 && c->max_pages > 0 && !c->page_table)) return FA_ERR_NULL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4)) return FA_ERR_ALIGN;
+  int lg = 0;
+  while ((1LL << lg) < c->page_size) ++lg;
+  const uint32_t mul = (uint32_t)(((1ULL << (30 + lg)) + c->page_size - 1) / c->page_size);
   *out = Cache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->page_table, c->k_type, c->v_type,
-               c->num_pages, c->page_size, c->B, c->max_pages, c->Hkv, c->D, c->Dv, (int)rbk, (int)rbv, nullptr};
+               c->num_pages, c->page_size, c->B, c->max_pages, c->Hkv, c->D, c->Dv, (int)rbk, (int)rbv, nullptr, mul, 30 + lg};
   return FA_OK;
 }
 
@@ -77,7 +80,7 @@ __device__ __forceinline__ void quant_q8(const float (&x)[8], uint32_t& lo, uint
   am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
   am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
   d = __float2half_rn(am / 127.f);
-  const float inv = am > kTiny ? 127.f / am : 0.f;
+  const float inv = am > kTiny ? 127.f * __frcp_rn(am) : 0.f;
   float t[8], near = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -105,7 +108,7 @@ __device__ __forceinline__ void quant_q4(const float (&x)[8], uint32_t& lo, uint
     if (fabsf(m2) > fabsf(m) || (fabsf(m2) == fabsf(m) && lower)) m = m2;
   }
   d = __float2half_rn(m * -0.125f);
-  const float inv = fabsf(m) > kTiny ? -8.f / m : 0.f;
+  const float inv = fabsf(m) > kTiny ? -8.f * __frcp_rn(m) : 0.f;
   float t[8], near = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -153,6 +156,8 @@ __device__ __forceinline__ void store_row8(uint8_t* row, int type, int e0, const
   }
 }
 
+constexpr int kAppendCtas = 3;  // CTAs an SM
+
 // K (IS_K) or V rows: a warp takes HC heads of a token, D / 8 lanes a head, and goes on to another token.
 template <int D, typename TX, bool IS_K>
 __device__ __forceinline__ void append_rows(const RowArgs& a) {
@@ -173,7 +178,12 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
     if (b < 0 || pos < 0) continue;
     x0 += h0 * head;
     Oct<TX> raw;
-    load8_raw(x0 + min(grp, left - 1) * head, vec, raw);
+    auto load = [&] {  // (lanes without a head of their own: the last head's elements, unheeded)
+      const TX* p = x0 + min(grp, left - 1) * head;
+      if (vec) load8_raw(p, true, raw);
+      else raw = load8_any(p);
+    };
+    load();
     const long long cell = cache_row(a.c, b, pos);
     if (cell < 0) continue;
     uint8_t* row = (IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h0 + grp) * rb;
@@ -186,7 +196,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
       const bool on = grp < left, more = left > GW;
       left -= GW;
       x0 += GW * head;
-      if (more) load8_raw(x0 + min(grp, left - 1) * head, vec, raw);  // the next heads, ahead of this one's work
+      if (more) load();  // the next heads, ahead of this one's work
       if (norm) {
         float ss = 0.f;
 #pragma unroll
@@ -205,7 +215,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
 
 // blockIdx.y 0: keys, 1: values
 template <int D, int DV, typename TX>
-__global__ void __launch_bounds__(256) k_cache_append(const RowArgs a) {
+__global__ void __launch_bounds__(256, kAppendCtas) k_cache_append(const RowArgs a) {
   if (blockIdx.y == 0) append_rows<D, TX, true>(a);
   else append_rows<DV, TX, false>(a);
 }
@@ -230,13 +240,14 @@ __device__ __forceinline__ float byte_minus(uint32_t w, int b, float bias) {
   return __uint_as_float(__byte_perm(w, 0x4b000000u, b ? 0x7441 : 0x7440)) - (8388608.f + bias);
 }
 
-__device__ __forceinline__ void load_row8(const uint8_t* row, int type, int e0, float (&x)[8]) {
+template <int TYPE>
+__device__ __forceinline__ void load_row8(const uint8_t* row, int e0, float (&x)[8]) {
   const int j = (e0 >> 3) & 3;
-  if (type == FA_F32) {
+  if (TYPE == FA_F32) {
     load8(reinterpret_cast<const float*>(row) + e0, true, x);
-  } else if (type == FA_F16) {
+  } else if (TYPE == FA_F16) {
     load8(reinterpret_cast<const __half*>(row) + e0, true, x);
-  } else if (type == FA_Q8_0) {
+  } else if (TYPE == FA_Q8_0) {
     const uint8_t* blk = row + (e0 >> 5) * 34;
     const float d = __half2float(__ushort_as_half((unsigned short)get16(blk)));
     uint32_t w[4];
@@ -255,35 +266,49 @@ __device__ __forceinline__ void load_row8(const uint8_t* row, int type, int e0, 
   }
 }
 
-template <int D, typename TY, bool IS_K>
+// K (IS_K) or V rows: a warp takes HC heads of a token.
+template <int D, typename TY, bool IS_K, int TYPE>
 __device__ __forceinline__ void read_rows(const RowArgs& a) {
-  constexpr int LG = D / 8, GW = 32 / LG;
+  constexpr int LG = D / 8, GW = 32 / LG, RB = TYPE == FA_F32 ? 4 * D : TYPE == FA_F16 ? 2 * D : TYPE == FA_Q8_0 ? D / 32 * 34 : D / 32 * 18;
   const int lane = threadIdx.x & 31, e0 = (lane & (LG - 1)) * 8;
-  const unsigned item = (blockIdx.x * 8u + (threadIdx.x >> 5)) * GW + lane / LG, t = item / (unsigned)a.c.Hkv;
-  const int h = (int)(item - t * a.c.Hkv);
+  const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5), t = item / (unsigned)a.nchunk;
   if (t >= (unsigned)a.T) return;
-  const int b = a.seq[t], pos = a.pos[t];
+  const int b = a.seq[t], pos = a.pos[t], h0 = (int)(item - t * a.nchunk) * a.HC, h1 = min(a.c.Hkv, h0 + a.HC);
   if (b < 0 || pos < 0) return;
   const long long cell = cache_row(a.c, b, pos);
   if (cell < 0) return;
-  const int rb = IS_K ? a.c.rbk : a.c.rbv, type = IS_K ? a.c.k_type : a.c.v_type;
-  float x[8];
-  load_row8((IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h) * (long long)rb, type, e0, x);
-  store8(static_cast<TY*>(IS_K ? a.ko : a.vo) + (long long)item * D + e0, x);
+  int h = h0 + lane / LG;
+  const uint8_t* row = (IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h) * RB;
+  TY* y = static_cast<TY*>(IS_K ? a.ko : a.vo) + ((long long)t * a.c.Hkv + h) * D + e0;
+#pragma unroll 4
+  for (; h < h1; h += GW, row += GW * RB, y += GW * D) {
+    float x[8];
+    load_row8<TYPE>(row, e0, x);
+    store8(y, x);
+  }
+}
+template <int D, typename TY, bool IS_K>
+__device__ __forceinline__ void read_type(const RowArgs& a) {
+  switch (IS_K ? a.c.k_type : a.c.v_type) {
+    case FA_F32: return read_rows<D, TY, IS_K, FA_F32>(a);
+    case FA_F16: return read_rows<D, TY, IS_K, FA_F16>(a);
+    case FA_Q8_0: return read_rows<D, TY, IS_K, FA_Q8_0>(a);
+    default: return read_rows<D, TY, IS_K, FA_Q4_0>(a);
+  }
 }
 
 template <typename TY>
 __global__ void __launch_bounds__(256) k_cache_read(const RowArgs a) {
   if (blockIdx.y == 0) {
     if (!a.ko) return;
-    if (a.c.D == 64) read_rows<64, TY, true>(a);
-    else if (a.c.D == 128) read_rows<128, TY, true>(a);
-    else read_rows<256, TY, true>(a);
+    if (a.c.D == 64) read_type<64, TY, true>(a);
+    else if (a.c.D == 128) read_type<128, TY, true>(a);
+    else read_type<256, TY, true>(a);
   } else {
     if (!a.vo) return;
-    if (a.c.Dv == 64) read_rows<64, TY, false>(a);
-    else if (a.c.Dv == 128) read_rows<128, TY, false>(a);
-    else read_rows<256, TY, false>(a);
+    if (a.c.Dv == 64) read_type<64, TY, false>(a);
+    else if (a.c.Dv == 128) read_type<128, TY, false>(a);
+    else read_type<256, TY, false>(a);
   }
 }
 
@@ -341,15 +366,21 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
   a.veck = aligned(k, 16) && (w.k_row * es) % 16 == 0 && (w.k_head * es) % 16 == 0;
   a.vecv = aligned(v, 16) && (w.v_row * es) % 16 == 0 && (w.v_head * es) % 16 == 0;
   a.wk = k_norm, a.eps = eps;
-  // heads that a warp takes: at least those that lie side by side, more where there are tokens enough
-  const int side = 256 / std::min(a.c.D, a.c.Dv);
-  const long long hc = (long long)T * a.c.Hkv / (16LL * nsm * side) * side;
-  a.HC = (int)std::max<long long>(side, std::min<long long>(hc, 16));
+  // Heads that a warp takes of a token: one row (the heads that lie side by side), two, four, up to all,
+  // whichever is done first by the warps that the SMs hold.  A token costs a warp about as much as two
+  // rows before its first one (its page and the rotation's factors).
+  const int side = 256 / std::min(a.c.D, a.c.Dv), all = (a.c.Hkv + side - 1) / side;
+  const long long warps = 8LL * kAppendCtas * nsm;
+  long long best = -1;
+  for (int rows = 1;; rows = std::min(2 * rows, all)) {
+    const long long items = (long long)T * ((all + rows - 1) / rows), cost = (2 * items + warps - 1) / warps * (2 + rows);
+    if (best < 0 || cost <= best) best = cost, a.HC = rows * side;
+    if (rows == all) break;
+  }
   a.nchunk = (a.c.Hkv + a.HC - 1) / a.HC;
-  const long long blocks = ((long long)T * a.nchunk + 7) / 8;
   if ((long long)T * a.nchunk > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  // at most the warps that the SMs hold: each goes on to further tokens with its code at hand
-  const dim3 grid((unsigned)std::min<long long>(blocks, 2 * nsm), 2);
+  const long long blocks = ((long long)T * a.nchunk + 7) / 8;
+  const dim3 grid((unsigned)std::min<long long>(blocks, kAppendCtas * nsm), 2);
   const RowKernel k_append = x_type == FA_ACT_F32   ? pick_append<float>(a.c.D, a.c.Dv)
                              : x_type == FA_ACT_F16 ? pick_append<__half>(a.c.D, a.c.Dv)
                                                     : pick_append<__nv_bfloat16>(a.c.D, a.c.Dv);
@@ -372,9 +403,13 @@ extern "C" fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* s
   if (y_type == FA_ACT_RAW) {
     k_cache_read_raw<<<dim3((unsigned)(((long long)T + 7) / 8), 2), 256, 0, s>>>(a);
   } else {
-    const int per = 8 * (256 / std::max(a.c.D, a.c.Dv));
-    const long long blocks = ((long long)T * a.c.Hkv + per - 1) / per;
-    if ((long long)T * a.c.Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    // heads that a warp takes of a token: one row of them, up to four where the card is full without
+    const int side = 256 / std::min(a.c.D, a.c.Dv), all = (a.c.Hkv + side - 1) / side;
+    const long long rows = std::max(1LL, std::min({4LL, (long long)all, (long long)T * all / (64LL * nsm)}));
+    a.HC = (int)rows * side;
+    a.nchunk = (a.c.Hkv + a.HC - 1) / a.HC;
+    const long long blocks = ((long long)T * a.nchunk + 7) / 8;
+    if ((long long)T * a.nchunk > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks, 2);
     if (y_type == FA_ACT_F32) k_cache_read<float><<<grid, 256, 0, s>>>(a);
     else if (y_type == FA_ACT_F16) k_cache_read<__half><<<grid, 256, 0, s>>>(a);

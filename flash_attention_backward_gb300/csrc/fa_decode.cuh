@@ -420,8 +420,6 @@ struct DecodeArgs {
   int4* items;  // [nitems] laid out beforehand: {b, splits, split, slot}, b = -1 behind the last one; or NULL
   int R, nitems, njobs;  // items that the card holds at a time, that can be at most, split sequences at most
   int box;      // rows of the tensor maps' boxes, 16 or 8: a tile is one or two; 0: one bulk copy a row
-  uint32_t page_mul;  // j / page_size = j * page_mul >> page_shift for j < 2^30
-  int page_shift;
   uint64_t wait_ns;   // a wait for a copy gives up after this long (0, the failure-detection hook: at once)
 };
 
@@ -749,7 +747,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
   const int boxes = a.box == 8 ? 2 : 1, per_batch = 32 / boxes;  // boxes of a tile, tiles of a lookup
   auto lookup = [&](int j) {  // row of the pool of key j, -1 where there is none
     if (j >= sg.j1) return -1;
-    const int p = (int)((uint64_t)j * a.page_mul >> a.page_shift);
+    const int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
     const int page = __ldg(a.c.table + (long long)sg.b * a.c.max_pages + p);
     if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + (j - p * a.c.page_size);
     *a.c.err = FA_ERR_PAGE;

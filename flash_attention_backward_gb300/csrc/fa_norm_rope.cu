@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(1024) k_dw_reduce(const float* part, int ctas_
   const int c = blockIdx.x * 32 + threadIdx.x, b0 = blockIdx.y ? ctas_q : 0, b1 = blockIdx.y ? ctas : ctas_q;
   float* out = blockIdx.y ? dwk : dwq;
   if (!out) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the grid starts while the gradient's last CTAs run)
   float s = 0.f;
   for (int b = b0 + threadIdx.y; b < b1; b += 32) s += part[(long long)b * D + c];
   red[threadIdx.y][threadIdx.x] = s;
@@ -167,7 +168,14 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
   k_back.fn<<<cq + ck, kBackWarps * 32, k_back.smem, s>>>(a);
   float* oq = wq ? dwq : nullptr;
   float* ok = wk && Hkv ? dwk : nullptr;
-  if (oq || ok) k_dw_reduce<<<dim3(D / 32, 2), dim3(32, 32), 0, s>>>(a.part, cq, cq + ck, D, oq, ok);
+  if (oq || ok) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / 32, 2), cfg.blockDim = dim3(32, 32), cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_dw_reduce, (const float*)a.part, cq, cq + ck, D, oq, ok) != cudaSuccess) return FA_ERR_CUDA;
+  }
   if (wk && !Hkv && dwk) cudaMemsetAsync(dwk, 0, D * sizeof(float), s);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -235,10 +235,17 @@ __global__ void __launch_bounds__(256) k_norm_rope(const NormArgs a) {
 // in shared memory: bulk copies bring x and gy of the items to come while one is worked on, which takes
 // the loads off the registers and the issue slots.  A token's factors are computed when the run comes to
 // it.  dw is summed by lane over the run, then over the CTA's lane groups in order.
-constexpr int kBackCtas = 2, kBackSlots = 3, kBackWarps = 8;
-// Heads of an item: what a slot of 4 KB holds, in multiples of those side by side in a warp
+constexpr int kBackCtas = 2, kBackWarps = 8;
+// Slots of a warp's ring and their bytes: a head of f32 takes up to 2 KB, and an item of one or two would
+// cost more in its handling than in its work (2048 tokens of 28 heads of 256: 33.8 us with 2 slots of
+// 6 KB, 34.9 with 3 of 4).
+template <typename TX, typename TY>
+constexpr int kBackSlots = sizeof(TX) + sizeof(TY) == 8 ? 2 : 3;
+template <typename TX, typename TY>
+constexpr int kBackBytes = sizeof(TX) + sizeof(TY) == 8 ? 6144 : 4096;
+// Heads of an item: what a slot holds, in multiples of those side by side in a warp
 template <int D, typename TX, typename TY>
-constexpr int kBackHeads = 4096 / (256 * (int)(sizeof(TX) + sizeof(TY))) * (256 / D);
+constexpr int kBackHeads = kBackBytes<TX, TY> / (256 * (int)(sizeof(TX) + sizeof(TY))) * (256 / D);
 
 __device__ __forceinline__ void bulk_run(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -265,7 +272,7 @@ __device__ __forceinline__ void sum_dw(const NormArgs& a, const float2 (&dw)[4],
 
 template <int D, typename TX, typename TY, int STYLE>
 __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(const NormArgs a) {
-  constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>, GB = HC * D * sizeof(TY), XB = HC * D * sizeof(TX), S = kBackSlots;
+  constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>, GB = HC * D * sizeof(TY), XB = HC * D * sizeof(TX), S = kBackSlots<TX, TY>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float red[kBackWarps * GW][D];
   __shared__ uint64_t s_bar[kBackWarps][S];
@@ -349,6 +356,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
     if (++slot == S) slot = 0, phase ^= 1;
     if ((h += HC) >= sd.H) h = 0, ++n;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (ln.norm) sum_dw<D, TX, TY, kBackWarps * GW>(a, dw, ln.ea, ln.eb, warp * GW + grp, red);
 }
 

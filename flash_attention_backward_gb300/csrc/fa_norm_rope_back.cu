@@ -6,7 +6,7 @@ namespace fap {
 
 template <int D, typename TX, typename TY>
 static BackKernel pick_style(bool vec, int style) {
-  constexpr int heads = kBackHeads<D, TX, TY>, ring = kBackWarps * kBackSlots * heads * D * (int)(sizeof(TX) + sizeof(TY));
+  constexpr int heads = kBackHeads<D, TX, TY>, ring = kBackWarps * kBackSlots<TX, TY> * heads * D * (int)(sizeof(TX) + sizeof(TY));
   const bool pairs = style == FA_ROPE_PAIRS;
   if (!vec) return BackKernel{pairs ? k_norm_rope_back_any<D, TX, TY, FA_ROPE_PAIRS> : k_norm_rope_back_any<D, TX, TY, FA_ROPE_HALVES>, heads, 0};
   return BackKernel{pairs ? k_norm_rope_back<D, TX, TY, FA_ROPE_PAIRS> : k_norm_rope_back<D, TX, TY, FA_ROPE_HALVES>, heads, ring};

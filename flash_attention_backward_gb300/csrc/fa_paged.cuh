@@ -47,6 +47,14 @@ __device__ __forceinline__ void load8_raw(const T* p, bool vec, Oct<T>& o) {
     for (int i = 0; i < 8; ++i) o.v[i] = p[i];
   }
 }
+// (out of line, so that the 16-byte path is not left with eight predicated loads)
+template <typename T>
+__device__ __noinline__ Oct<T> load8_any(const T* p) {
+  Oct<T> o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o.v[i] = p[i];
+  return o;
+}
 template <typename T>
 __device__ __forceinline__ void unpack8(const Oct<T>& o, float (&x)[8]) {
 #pragma unroll
@@ -168,12 +176,14 @@ struct Cache {
   int k_type, v_type, num_pages, page_size, B, max_pages, Hkv, D, Dv;
   int rbk, rbv;  // bytes of a row
   int* err;
+  uint32_t page_mul;  // j / page_size = j * page_mul >> page_shift for 0 <= j < 2^30
+  int page_shift;
 };
 
 // Row (page * page_size + offset) of position j of sequence b, or -1 (and FA_ERR_PAGE recorded)
 __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
-  const int p = j / c.page_size;
-  if (b < c.B && p < c.max_pages) {
+  if (b < c.B && j < c.max_pages * c.page_size) {
+    const int p = (int)((uint64_t)j * c.page_mul >> c.page_shift);
     const int page = __ldg(c.table + (long long)b * c.max_pages + p);
     if (page >= 0 && page < c.num_pages) return (long long)page * c.page_size + (j - p * c.page_size);
   }

@@ -108,10 +108,6 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
   a.jobs = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_jobs);
   a.items = p.planned ? reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_items) : nullptr;
   a.R = p.R, a.nitems = p.nitems, a.njobs = p.njobs;
-  int lg = 0;
-  while ((1LL << lg) < a.c.page_size) ++lg;
-  a.page_shift = 30 + lg;
-  a.page_mul = (uint32_t)(((1ULL << a.page_shift) + a.c.page_size - 1) / a.c.page_size);
   a.wait_ns = fab_take_wait_ns();
   // boxes of 16 or 8 rows where these never span pages and cells are spaced by multiples of 16 bytes
   DecodeMaps m = {};
