@@ -121,12 +121,21 @@ static Plan make_plan(int N, int M, int H, int Hkv, int D, int Dv, int nsm, size
 static int plan_level(const Plan& P) { return P.dsq ? (P.pre ? 2 : 3) : P.pre ? 1 : 0; }
 
 static int device_sms(int* major, int* minor) {
-  int dev = 0, nsm = 0;
+  static std::atomic<int> known[64];  // a device's SM count and compute capability, which do not change
+  int dev = 0, nsm = 0, ma = 0, mi = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  if (cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  if (major) cudaDeviceGetAttribute(major, cudaDevAttrComputeCapabilityMajor, dev);
-  if (minor) cudaDeviceGetAttribute(minor, cudaDevAttrComputeCapabilityMinor, dev);
-  return nsm;
+  int v = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (!v) {
+    if (cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&ma, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&mi, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+      return -1;
+    v = nsm << 12 | ma << 6 | mi;
+    if (dev < 64) known[dev].store(v, std::memory_order_relaxed);
+  }
+  if (major) *major = v >> 6 & 63;
+  if (minor) *minor = v & 63;
+  return v >> 12;
 }
 
 

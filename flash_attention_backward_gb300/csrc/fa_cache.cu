@@ -216,6 +216,8 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
 // blockIdx.y 0: keys, 1: values
 template <int D, int DV, typename TX>
 __global__ void __launch_bounds__(256, kAppendCtas) k_cache_append(const RowArgs a) {
+  after_last();
+  lets_next();
   if (blockIdx.y == 0) append_rows<D, TX, true>(a);
   else append_rows<DV, TX, false>(a);
 }
@@ -299,6 +301,8 @@ __device__ __forceinline__ void read_type(const RowArgs& a) {
 
 template <typename TY>
 __global__ void __launch_bounds__(256) k_cache_read(const RowArgs a) {
+  after_last();
+  lets_next();
   if (blockIdx.y == 0) {
     if (!a.ko) return;
     if (a.c.D == 64) read_type<64, TY, true>(a);
@@ -314,6 +318,8 @@ __global__ void __launch_bounds__(256) k_cache_read(const RowArgs a) {
 
 // A token's cell (all KV heads' rows) is contiguous: one warp copies it in 4-byte words.
 __global__ void __launch_bounds__(256) k_cache_read_raw(const RowArgs a) {
+  after_last();
+  lets_next();
   const long long t = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const bool is_k = blockIdx.y == 0;
   void* out = is_k ? a.ko : a.vo;
@@ -384,8 +390,7 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
   const RowKernel k_append = x_type == FA_ACT_F32   ? pick_append<float>(a.c.D, a.c.Dv)
                              : x_type == FA_ACT_F16 ? pick_append<__half>(a.c.D, a.c.Dv)
                                                     : pick_append<__nv_bfloat16>(a.c.D, a.c.Dv);
-  k_append<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_next(k_append, grid, dim3(256), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 extern "C" fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* seq, const int32_t* pos, int T,
@@ -401,7 +406,7 @@ extern "C" fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* s
   a.ko = k_out, a.vo = v_out;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (y_type == FA_ACT_RAW) {
-    k_cache_read_raw<<<dim3((unsigned)(((long long)T + 7) / 8), 2), 256, 0, s>>>(a);
+    return launch_next(k_cache_read_raw, dim3((unsigned)(((long long)T + 7) / 8), 2), dim3(256), 0, s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   } else {
     // heads that a warp takes of a token: one row of them, up to four where the card is full without
     const int side = 256 / std::min(a.c.D, a.c.Dv), all = (a.c.Hkv + side - 1) / side;
@@ -411,9 +416,7 @@ extern "C" fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* s
     const long long blocks = ((long long)T * a.nchunk + 7) / 8;
     if ((long long)T * a.nchunk > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks, 2);
-    if (y_type == FA_ACT_F32) k_cache_read<float><<<grid, 256, 0, s>>>(a);
-    else if (y_type == FA_ACT_F16) k_cache_read<__half><<<grid, 256, 0, s>>>(a);
-    else k_cache_read<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    const RowKernel k_read = y_type == FA_ACT_F32 ? k_cache_read<float> : y_type == FA_ACT_F16 ? k_cache_read<__half> : k_cache_read<__nv_bfloat16>;
+    return launch_next(k_read, grid, dim3(256), 0, s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

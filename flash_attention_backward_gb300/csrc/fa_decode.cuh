@@ -13,6 +13,8 @@
 // block scale into two bf16 parts (16 bits, with f32's range), a weight alone into two binary16
 // parts (22 bits), and for f32 rows all operands into two tf32 parts (three products).
 #pragma once
+#include <atomic>
+
 #include "fa_paged.cuh"
 #include "sm100.cuh"
 
@@ -556,6 +558,7 @@ __device__ __forceinline__ T block_scan(T v, T* smem, T* before) {
 // Lays out the items of a large batch: one CTA.
 static __global__ void __launch_bounds__(1024) k_decode_plan(const DecodeArgs a) {
   __shared__ uint64_t s_scan[32];
+  after_last();
   const int B = a.c.B;
   uint64_t U = 0, before;
   for (int c0 = 0; c0 < B; c0 += 1024) {
@@ -685,6 +688,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
   if (lane < 2 * SLOTS) fab::mbar_init(&s_slot[warp][lane >> 1].bar[lane & 1], 1);
   for (int i = threadIdx.x; i < DV + 4; i += NW * 32) s_zero[i] = 0;
   fab::fence_mbar_init();  // ordered before the first copy by the barriers below
+  after_last();
 
   // ---- the item: {sequence, its splits, this split, slot}
   if (a.items) {
@@ -924,7 +928,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
       }
       __syncwarp();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    lets_next();  // (the join, whose CTAs are large: not before the tiles are done)
     // ---- the warps' sums (in their rings), joined in the warps' order
     l += __shfl_xor_sync(kFull, l, 1);
     l += __shfl_xor_sync(kFull, l, 2);
@@ -998,7 +1002,7 @@ __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
   __shared__ float4 s_x[512];
   const int h = blockIdx.y, hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
   const int tid = threadIdx.x, ln = tid % LN, gr = tid / LN;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_last();
   const int4 job = a.jobs[blockIdx.x];
   if (job.x < 0) return;
   const int np = job.z;
@@ -1060,19 +1064,21 @@ typedef cudaError_t (*DecodeFn)(const DecodeArgs& a, const DecodeMaps& m, cudaSt
 template <int D, int DV, int KT, int VT>
 cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
-  cudaError_t e = cudaFuncSetAttribute(k_decode<D, DV, KT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C.smem);
+  static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (a.items) k_decode_plan<<<1, 1024, 0, s>>>(a);
-  k_decode<D, DV, KT, VT><<<(unsigned)(a.nitems * a.HG), C.nw * 32, C.smem, s>>>(a, m.k, m.v);
-  if (a.njobs > 0) {
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.njobs, a.H), cfg.blockDim = dim3(512), cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, k_decode_join<DV>, a)) != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(k_decode<D, DV, KT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C.smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
   }
-  return cudaGetLastError();
+  if (a.items && (e = launch_next(k_decode_plan, dim3(1), dim3(1024), 0, s, a)) != cudaSuccess) return e;
+  e = launch_next(k_decode<D, DV, KT, VT>, dim3((unsigned)(a.nitems * a.HG)), dim3(C.nw * 32), C.smem, s, a, m.k, m.v);
+  if (e != cudaSuccess) return e;
+  if (a.njobs > 0) return launch_next(k_decode_join<DV>, dim3(a.njobs, a.H), dim3(512), 0, s, a);
+  return cudaSuccess;
 }
 template <int D, int DV, int KT>
 DecodeFn pick_decode_v(int vt) {

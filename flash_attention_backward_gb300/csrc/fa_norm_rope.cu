@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(1024) k_dw_reduce(const float* part, int ctas_
   const int c = blockIdx.x * 32 + threadIdx.x, b0 = blockIdx.y ? ctas_q : 0, b1 = blockIdx.y ? ctas : ctas_q;
   float* out = blockIdx.y ? dwk : dwq;
   if (!out) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the grid starts while the gradient's last CTAs run)
+  after_last();
   float s = 0.f;
   for (int b = b0 + threadIdx.y; b < b1; b += 32) s += part[(long long)b * D + c];
   red[threadIdx.y][threadIdx.x] = s;
@@ -123,8 +123,10 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, c
   chunk_heads(H + Hkv, rows_a_warp(a, D, nsm), 256 / D, 32, &a.HC, &a.nchunk);
   const long long items = (long long)N * a.nchunk;  // (that many heads would not fit in memory)
   if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  pick_norm_fwd(D, x_type, y_type, a.vec, a.rope.style)<<<(unsigned)((items + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_next(pick_norm_fwd(D, x_type, y_type, a.vec, a.rope.style), dim3((unsigned)((items + 7) / 8)), dim3(256), 0,
+                     static_cast<cudaStream_t>(stream), a) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 extern "C" size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv, int D) {
@@ -165,17 +167,12 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
   if (k_back.smem > 48 * 1024 &&
       cudaFuncSetAttribute(k_back.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k_back.smem) != cudaSuccess)
     return FA_ERR_CUDA;
-  k_back.fn<<<cq + ck, kBackWarps * 32, k_back.smem, s>>>(a);
+  if (launch_next(k_back.fn, dim3(cq + ck), dim3(kBackWarps * 32), k_back.smem, s, a) != cudaSuccess) return FA_ERR_CUDA;
   float* oq = wq ? dwq : nullptr;
   float* ok = wk && Hkv ? dwk : nullptr;
-  if (oq || ok) {
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(D / 32, 2), cfg.blockDim = dim3(32, 32), cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_dw_reduce, (const float*)a.part, cq, cq + ck, D, oq, ok) != cudaSuccess) return FA_ERR_CUDA;
-  }
+  if ((oq || ok) &&
+      launch_next(k_dw_reduce, dim3(D / 32, 2), dim3(32, 32), 0, s, a.part, cq, cq + ck, D, oq, ok) != cudaSuccess)
+    return FA_ERR_CUDA;
   if (wk && !Hkv && dwk) cudaMemsetAsync(dwk, 0, D * sizeof(float), s);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -188,6 +188,8 @@ struct Lane {
 template <int D, typename TX, typename TY, bool VEC, int STYLE>
 __global__ void __launch_bounds__(256) k_norm_rope(const NormArgs a) {
   constexpr int GW = 256 / D, U = kRows<TX>;
+  after_last();
+  lets_next();
   const int grp = (threadIdx.x & 31) / (D / 8);
   const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5);
   const int n = item / (unsigned)a.nchunk, c0 = (int)(item - (unsigned)n * a.nchunk) * a.HC;
@@ -276,6 +278,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float red[kBackWarps * GW][D];
   __shared__ uint64_t s_bar[kBackWarps][S];
+  after_last();
   const bool isq = blockIdx.x < a.ctas_q;
   const NormSide sd = a.side[isq ? 0 : 1];
   const int lane = threadIdx.x & 31, grp = lane / (D / 8), warp = threadIdx.x >> 5;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
     if (++slot == S) slot = 0, phase ^= 1;
     if ((h += HC) >= sd.H) h = 0, ++n;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  lets_next();
   if (ln.norm) sum_dw<D, TX, TY, kBackWarps * GW>(a, dw, ln.ea, ln.eb, warp * GW + grp, red);
 }
 
@@ -365,6 +368,7 @@ template <int D, typename TX, typename TY, int STYLE>
 __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_any(const NormArgs a) {
   constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>;
   __shared__ float red[kBackWarps * GW][D];
+  after_last();
   const bool isq = blockIdx.x < a.ctas_q;
   const NormSide sd = a.side[isq ? 0 : 1];
   const int grp = (threadIdx.x & 31) / (D / 8), warp = threadIdx.x >> 5;

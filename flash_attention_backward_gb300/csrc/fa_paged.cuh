@@ -191,7 +191,23 @@ __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
   return -1;
 }
 
+// ---- launches that overlap.  A kernel launched by launch_next() may start while the one before it on the
+// stream still runs its last CTAs; it begins with after_last(), which waits for all of that one's work.
+// lets_next() says that the next one's CTAs may take what is free from here on.  (Without such a launch
+// before or behind them both do nothing.)
+__device__ __forceinline__ void after_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void lets_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- host
+template <typename... P, typename... A>
+inline cudaError_t launch_next(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool head_size(int d) { return d == 64 || d == 128 || d == 256; }
 inline int act_bytes(int t) { return t == FA_ACT_F32 ? 4 : 2; }
