@@ -41,8 +41,9 @@ def within(got, ref, tol, what=""):
     got = np.asarray(got, np.float64)
     fin = np.isfinite(ref)
     assert np.array_equal(np.isneginf(got), np.isneginf(ref)), what
-    bad = ~(np.abs(got - ref)[fin] <= np.broadcast_to(tol, ref.shape)[fin])
-    assert not bad.any(), (what, int(bad.sum()), np.abs(got - ref)[fin][bad][:4], np.broadcast_to(tol, ref.shape)[fin][bad][:4])
+    off, tol = np.abs(got[fin] - ref[fin]), np.broadcast_to(tol, ref.shape)[fin]
+    bad = ~(off <= tol)
+    assert not bad.any(), (what, int(bad.sum()), off[bad][:4], tol[bad][:4])
 
 
 # ------------------------------------------------------------------------------------------------
@@ -174,6 +175,56 @@ def test_norm_rope_in_place_and_same_input_twice(fb):
     k = q.clone()
     got = fb.qk_norm_rope(q, k, pos, wq=w, wk=w, rope=rope, out={"q": q, "k": k})
     assert got["q"] is q and torch.equal(q, ref["q"]) and torch.equal(k, ref["k"])
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "odd_rows", "broadcast"])
+def test_norm_rope_layouts(fb, layout):
+    """Heads apart from each other, rows that start off 16 bytes, one token's heads for every token: the same
+    results as from contiguous copies, both ways."""
+    rng = np.random.default_rng(12)
+    N, H, Hkv, D = 53, 13, 3, 128
+    if layout == "interleaved":  # [N][Hkv][q .. q, k, v] as some projections have them
+        x, _ = act_array(rng, (N, Hkv, 6, D), "bf16")
+        q, k = x[:, :, 0], x[:, :, 4]
+    elif layout == "odd_rows":
+        flat, _ = act_array(rng, (N * (H + Hkv) * D + 3,), "bf16")
+        x = flat[3:].view(N, H + Hkv, D)
+        q, k = x[:, :H], x[:, H:]
+    else:
+        (q, _), (k, _) = act_array(rng, (1, H, D), "bf16"), act_array(rng, (N, 1, D), "bf16")
+        q, k = q.expand(N, H, D), k.expand(N, Hkv, D)
+    w, rope = torch.rand(D, device="cuda") + 0.5, fb.rope_frequencies(D)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda") * 7
+    gq, gk = torch.randn(q.shape, device="cuda"), torch.randn(k.shape, device="cuda")
+    for style in (fb.FA_ROPE_HALVES, fb.FA_ROPE_PAIRS):
+        kw = dict(wq=w, wk=w, rope=rope, rope_style=style)
+        a, b = (fb.qk_norm_rope(x, y, pos, **kw) for x, y in ((q, k), (q.contiguous(), k.contiguous())))
+        for n in ("q", "k"):
+            assert torch.equal(a[n], b[n])
+        a, b = (fb.qk_norm_rope_backward(gq, gk, x, y, pos, **kw) for x, y in ((q, k), (q.contiguous(), k.contiguous())))
+        for n in ("dq", "dk"):
+            assert torch.equal(a[n], b[n])
+        for n in ("dwq", "dwk"):  # (other runs of rows: another order of the sum)
+            assert float((a[n] - b[n]).abs().max()) <= 1e-4 * float(b[n].abs().max())
+
+
+def test_norm_rope_many_heads_and_rows(fb):
+    """More heads than a warp takes at a time, and tokens that do not divide into the warps' runs."""
+    rng = np.random.default_rng(13)
+    for N, H, Hkv, D, act in ((3, 131, 67, 64, "f16"), (2501, 5, 1, 256, "bf16"), (1, 40, 8, 128, "f32"), (9000, 1, 1, 64, "f32")):
+        (q, qa), (k, ka), (gq, gqa), (gk, gka) = (act_array(rng, (N, h, D), act) for h in (H, Hkv, H, Hkv))
+        pos = rng.integers(0, 1 << 20, N).astype(np.int32)
+        w = [(1.0 + 0.2 * rng.standard_normal(D)).astype(np.float32) for _ in range(2)]
+        kw = dict(wq=cuda(w[0]), wk=cuda(w[1]), rope=fb.rope_frequencies(D // 2))
+        y = fb.qk_norm_rope(q, k, cuda(pos), dtype=torch.float32, **kw)
+        g = fb.qk_norm_rope_backward(gq, gk, q, k, cuda(pos), **kw)
+        for n, x, wt, gy in (("q", qa, w[0], gqa), ("k", ka, w[1], gka)):
+            ref = R.rotate(R.norm(x, wt, 1e-6), pos, D // 2, 10000.0, True)
+            dx, dw, *_ = back_reference(x, wt, gy, pos, D // 2, True)
+            for got, want, tol in ((y[n], ref, 1e-6), (g["d" + n], dx, 1e-6 if act == "f32" else 3e-3), (g["dw" + n], dw, 1e-5)):
+                e = got.double().cpu().numpy() - want  # (rms: 2^-8.5 / sqrt 3 of bf16's own rounding, some 2^-24 otherwise)
+                assert (e ** 2).sum() <= tol ** 2 * (want ** 2).sum(), (N, n)
+    assert fb.fa_back_get_error() == 0
 
 
 def test_norm_rope_backward_is_deterministic_and_empty(fb):
@@ -310,6 +361,33 @@ def test_quantisers_on_borders_and_extremes(fb):
                 assert np.array_equal(got[n].cpu().numpy().astype(np.float64), ref.astype(np.float32).astype(np.float64)), (act, ty, n)
 
 
+@pytest.mark.parametrize("seed", range(10))
+def test_append_random(fb, seed):
+    """Seeded random shapes: values bit for bit, keys without norm and rotation too, unwritten rows untouched."""
+    r = np.random.default_rng(7000 + seed)
+    pick = lambda *a: a[int(r.integers(len(a)))]  # noqa: E731
+    D, Dv, Hkv = pick(64, 128, 256), pick(64, 128, 256), pick(1, 2, 3, 5, 8, 16)
+    kt, vt, act, page = pick(F32, F16, Q8, Q4), pick(F32, F16, Q8, Q4), pick("f32", "f16", "bf16"), pick(16, 20, 64)
+    T, B = int(np.exp(r.uniform(0, np.log(900)))), int(r.integers(1, 6))
+    cache, table = empty_cache(fb, B, -(-T // page) + 1, page, Hkv, D, Dv, kt, vt, seed=seed)
+    seq = r.integers(0, B, T).astype(np.int32)
+    pos = np.array([(seq[:t] == seq[t]).sum() for t in range(T)], np.int32)
+    (k, ka), (v, va) = act_array(r, (T, Hkv, D), act), act_array(r, (T, Hkv, Dv), act)
+    fb.cache_append(k, v, cache, cuda(seq), cuda(pos))
+    raw = fb.cache_read(cache, cuda(seq), cuda(pos), dtype=torch.uint8)
+    dec = fb.cache_read(cache, cuda(seq), cuda(pos))
+    for n, x, ty, d in (("k", ka, kt, D), ("v", va, vt, Dv)):
+        ref = R.stored(x.astype(np.float64), ty)[1]
+        got = R.oracle.dequant(raw[n].cpu().numpy(), ty, d).reshape(ref.shape)
+        assert np.array_equal(got, ref), n
+        assert np.array_equal(dec[n].cpu().numpy().astype(np.float64), ref.astype(np.float32).astype(np.float64)), n
+        pool = cache.k if n == "k" else cache.v
+        untouched = np.ones(pool.shape[:2], bool)
+        untouched[rows_of(table, seq, pos, page)] = False
+        assert bool((pool.cpu()[torch.from_numpy(untouched)] == 0xA5).all())
+    assert fb.fa_back_get_error() == 0
+
+
 def test_append_strided_views_match_contiguous(fb):
     rng = np.random.default_rng(11)
     T, H, Hkv, D = 45, 4, 2, 128
@@ -414,6 +492,10 @@ SHAPES = {  # lens, H, Hkv, D, Dv, kt, vt, act, page, opts
     "large_q": ([1500, 64], 6, 2, 64, 64, F16, F32, "f32", 64, dict(q_amp=1e18, scale=1e-19)),
     "many_sequences": (list(range(0, 300)), 4, 1, 64, 64, Q8, Q8, "bf16", 16, {}),
     "long_one": ([40000], 8, 2, 128, 128, Q8, Q8, "f32", 64, {}),
+    "large_batch_one_long": ([9000] + [0, 1, 17, 40] * 75, 6, 2, 64, 64, Q8, Q8, "f32", 16, {}),
+    "large_batch_split": ([700] * 260, 8, 8, 64, 64, F16, Q4, "bf16", 40, {}),
+    "fits_less_than_a_chunk": ([3000, 2900] + [10] * 60, 16, 8, 64, 64, Q8, F16, "bf16", 8, {}),
+    "hkv_3_page_8": ([333, 8, 9, 1000], 6, 3, 128, 128, Q8, Q8, "f32", 8 * 3, {}),
     "long_and_short": ([20011, 1, 3, 0, 9001, 17] + [5] * 30, 12, 2, 128, 128, Q8, Q4, "f32", 64, {}),
 }
 
@@ -423,6 +505,23 @@ def test_decode_shapes(fb, name):
     lens, H, Hkv, D, Dv, kt, vt, act, page, opts = SHAPES[name]
     p = R.Paged(sorted(SHAPES).index(name) + 900, lens, Hkv, D, Dv, kt, vt, page)
     check_decode(fb, p, H, act, seed=1, **opts)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_decode_random(fb, seed):
+    """Seeded random shapes, types, pages, lengths and score extensions."""
+    r = np.random.default_rng(4000 + seed)
+    pick = lambda *a: a[int(r.integers(len(a)))]  # noqa: E731
+    D, Dv = pick(64, 128, 256), pick(64, 128, 256)
+    kt, vt = pick(F32, F16, Q8, Q4), pick(F32, F16, Q8, Q4)
+    Hkv, G, B = pick(1, 2, 3, 4, 5), pick(1, 2, 3, 5, 8, 9, 13), int(r.integers(1, 12))
+    page = pick(8, 16, 24, 32, 40, 48, 64, 100, 256)
+    if page * Hkv * synth.row_bytes(kt, D) % 16 or page * Hkv * synth.row_bytes(vt, Dv) % 16:
+        page = 16
+    lens = [int(x) for x in np.exp(r.uniform(-0.5, np.log(3000), B))]
+    p = R.Paged(seed, lens, Hkv, D, Dv, kt, vt, page)
+    check_decode(fb, p, G * Hkv, pick("f32", "f16", "bf16"), softcap=pick(0.0, 0.0, 20.0), alibi=pick(True, False),
+                 sinks=pick(True, False), seed=seed)
 
 
 @pytest.mark.parametrize("amp", [1e-4, 1e4])
