@@ -123,7 +123,10 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, c
   chunk_heads(H + Hkv, rows_a_warp(a, D, nsm), 256 / D, 32, &a.HC, &a.nchunk);
   const long long items = (long long)N * a.nchunk;  // (that many heads would not fit in memory)
   if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  return launch_next(pick_norm_fwd(D, x_type, y_type, a.vec, a.rope.style), dim3((unsigned)((items + 7) / 8)), dim3(256), 0,
+  long long grid = (items + 7) / 8;
+  const int ctas = x_type == FA_ACT_F32 ? kForwardCtas<float> : kForwardCtas<__half>;
+  if (ctas) grid = std::min<long long>(grid, (long long)ctas * nsm);
+  return launch_next(pick_norm_fwd(D, x_type, y_type, a.vec, a.rope.style), dim3((unsigned)grid), dim3(256), 0,
                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;

@@ -131,6 +131,11 @@ struct Lane {
     s[0] = make_float2(ss[0], ss[1]), s[1] = make_float2(ss[2], ss[3]);
     ns[0] = make_float2(-ss[0], -ss[1]), ns[1] = make_float2(-ss[2], -ss[3]);
   }
+  // Takes over the factors of another lane's, of the same token.
+  __device__ __forceinline__ void turned_as(const Lane& o) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = o.c[i], s[i] = o.s[i], ns[i] = o.ns[i];
+  }
   __device__ __forceinline__ void rotate(float2 (&x)[4]) const {
     if (STYLE == FA_ROPE_HALVES) {
 #pragma unroll
@@ -183,53 +188,67 @@ struct Lane {
 };
 
 // A warp takes HC heads of one token, 256 / D side by side, and loads the next kRows of each together.
-// VEC: every head of x starts on 16 bytes (else it is loaded element by element).  Lanes without a head
-// of their own (the last ones of a token) work on the last head and store nothing.
+// VEC: every head of x starts on 16 bytes (else it is loaded element by element).  Lanes without a head of
+// their own (the last ones of a token) work on the last head and store nothing.
+// With 16-bit x, whose time is its instructions, a warp goes on to further tokens with both weights at hand;
+// with f32 x, whose time is its bytes, many short warps keep more loads in flight.
+template <typename TX>
+constexpr int kForwardCtas = sizeof(TX) == 2 ? 3 : 0;  // CTAs an SM, or 0: a warp takes one item
 template <int D, typename TX, typename TY, bool VEC, int STYLE>
-__global__ void __launch_bounds__(256) k_norm_rope(const NormArgs a) {
+__global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormArgs a) {
   constexpr int GW = 256 / D, U = kRows<TX>;
   after_last();
   lets_next();
   const int grp = (threadIdx.x & 31) / (D / 8);
-  const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5);
-  const int n = item / (unsigned)a.nchunk, c0 = (int)(item - (unsigned)n * a.nchunk) * a.HC;
-  if (n >= a.N) return;
-  Lane<D, STYLE> ln;
-  ln.place(a.rope);
-  bool turned = false;
-  for (int k = 0; k < 2; ++k) {
-    const NormSide& sd = a.side[k];
-    const int first = k ? a.side[0].H : 0;  // the side's first head among all
-    const int h0 = max(c0 - first, 0);
-    int left = min(sd.H, c0 + a.HC - first) - h0;  // heads that the warp still has
-    if (left <= 0) continue;
-    const long long head = sd.head;
-    const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + h0 * head;
-    TY* y0 = static_cast<TY*>(sd.y) + ((long long)n * sd.H + h0 + grp) * D;
-    Eight<TX> raw[U];
-    auto fetch = [&] {
+  const unsigned items = (unsigned)a.N * a.nchunk;
+  constexpr bool ON = kForwardCtas<TX> > 0;
+  Lane<D, STYLE> lanes[1 + ON];  // queries' (and keys'); one for both where each item is another warp's
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u * GW < left) load_eight<TX, VEC>(x0 + min(grp + u * GW, left - 1) * head, ln.ea, ln.eb, raw[u]);
-    };
-    fetch();
-    ln.weights(sd.w);
-    if (!turned) ln.turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, 1.f);
-    turned = true;
-    for (;;) {
+  for (int k = 0; k <= ON; ++k) {
+    lanes[k].place(a.rope);
+    if (ON) lanes[k].weights(a.side[k].w);
+  }
+  for (unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5); item < items; item += gridDim.x * 8u) {
+    const int n = item / (unsigned)a.nchunk, c0 = (int)(item - (unsigned)n * a.nchunk) * a.HC;
+    bool turned = false;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u * GW >= left) break;  // (the same in all lanes)
-        float2 x[4];
-        unpack_eight(raw[u], x);
-        ln.forward(x, a.eps);
-        if (grp + u * GW < left) store_eight(y0 + u * GW * D, ln.ea, ln.eb, x);
-      }
-      left -= U * GW;
-      if (left <= 0) break;
-      x0 += U * GW * head, y0 += U * GW * D;
+    for (int k = 0; k < 2; ++k) {
+      const NormSide& sd = a.side[k];
+      const int first = k ? a.side[0].H : 0;  // the side's first head among all
+      const int h0 = max(c0 - first, 0);
+      int left = min(sd.H, c0 + a.HC - first) - h0;  // heads that the warp still has
+      if (left <= 0) continue;
+      Lane<D, STYLE>& ln = lanes[ON ? k : 0];
+      const long long head = sd.head;
+      const TX* x0 = static_cast<const TX*>(sd.x) + n * sd.row + h0 * head;
+      TY* y0 = static_cast<TY*>(sd.y) + ((long long)n * sd.H + h0 + grp) * D;
+      Eight<TX> raw[U];
+      auto fetch = [&] {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u * GW < left) load_eight<TX, VEC>(x0 + min(grp + u * GW, left - 1) * head, ln.ea, ln.eb, raw[u]);
+      };
       fetch();
+      if (!ON) ln.weights(sd.w);
+      if (!turned) lanes[0].turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, 1.f);
+      turned = true;
+      if (ON && k) ln.turned_as(lanes[0]);
+      for (;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u * GW >= left) break;  // (the same in all lanes)
+          float2 x[4];
+          unpack_eight(raw[u], x);
+          ln.forward(x, a.eps);
+          if (grp + u * GW < left) store_eight(y0 + u * GW * D, ln.ea, ln.eb, x);
+        }
+        left -= U * GW;
+        if (left <= 0) break;
+        x0 += U * GW * head, y0 += U * GW * D;
+        fetch();
+      }
     }
+    if (!ON) break;
   }
 }
 
