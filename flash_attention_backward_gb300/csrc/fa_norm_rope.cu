@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(1024) k_dw_reduce(const float* part, int ctas_
   __shared__ float red[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x, b0 = blockIdx.y ? ctas_q : 0, b1 = blockIdx.y ? ctas : ctas_q;
   float* out = blockIdx.y ? dwk : dwq;
-  if (!out) return;
   after_last();
+  if (!out) return;
   float s = 0.f;
   for (int b = b0 + threadIdx.y; b < b1; b += 32) s += part[(long long)b * D + c];
   red[threadIdx.y][threadIdx.x] = s;

@@ -49,7 +49,7 @@ struct Args {
   const at::Tensor* heads(int i, at::ScalarType t, int64_t n, int64_t D) {
     const at::Tensor* x = tensor(i);
     if (!ok) return nullptr;
-    if (x->dim() != 3 || x->scalar_type() != t || x->size(0) != n || x->size(2) != D || x->stride(2) != 1 || x->numel() == 0)
+    if (x->dim() != 3 || x->scalar_type() != t || x->size(0) != n || n > INT32_MAX || x->size(2) != D || x->stride(2) != 1 || x->numel() == 0)
       ok = false;
     return x;
   }

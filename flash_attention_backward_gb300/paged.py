@@ -22,7 +22,6 @@ _ACT = {torch.float32: nat.FA_ACT_F32, torch.float16: nat.FA_ACT_F16, torch.bflo
 _F32, _I32, _empty = torch.float32, torch.int32, torch.empty
 
 
-
 def _bind():
     """Hand the library's entry points to _fast, once; False without it."""
     global _plain
@@ -51,6 +50,8 @@ def _act(t: torch.dtype) -> int:
 
 def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> int:
     """The address of t, which is contiguous, of this type, shape (a tuple) and device."""
+    if t is None:
+        raise FaBackError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got None")
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return t.data_ptr()
     raise FaBackError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got {t.dtype} "
@@ -62,7 +63,7 @@ def _heads(name: str, t: torch.Tensor, N: int, D: int, dtype, device):
     if t.dim() == 3 and t.dtype is dtype and t.device == device:
         n, heads, d = t.shape
         row, head, comp = t.stride()
-        if n == N and d == D and ((comp == 1 and row >= 0 and head >= 0) or not t.numel()):
+        if n == N < 2 ** 31 and d == D and ((comp == 1 and row >= 0 and head >= 0) or not t.numel()):
             return heads, row, head
     raise FaBackError(f"{name}: {dtype} [{N}][heads][{D}] with contiguous components on {device} expected, got "
                       f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")

@@ -254,6 +254,8 @@ def test_wrappers_refuse_what_the_kernels_do_not_take():
     raises(fb.qk_norm_rope, q, x.half(), i2)
     raises(fb.qk_norm_rope, q, x, i2.long(), rope=torch.zeros(64, dtype=torch.int64))
     raises(fb.qk_norm_rope, q, x, i2, dtype=torch.int32)
+    raises(fb.qk_norm_rope, q, x, None, rope=torch.zeros(64, dtype=torch.int64))
+    raises(fb.qk_norm_rope, q[:1, :1].expand(2 ** 32 + 2, 1, 128), None, i2)  # more rows than 31 bits hold
     raises(fb.qk_norm_rope_backward, q, None, q, x, i2)
     raises(fb.qk_norm_rope_backward, q[:1], x, q, x, i2)
     # tensors that are in order but live on the CPU: there is no fallback
