@@ -66,6 +66,17 @@ static __device__ __noinline__ float q4_border(float x, float inv, float m) {
   const float k = rintf(fmaf(x, inv, 0.5f)), df = prod_diff(-8.f, x, k - 0.5f, m);
   return kMagic + 8.f + ((m > 0.f ? df >= 0.f : df <= 0.f) ? k : k - 1.f);
 }
+// The largest and the smallest of three; a NaN wins, so that a block that holds one gets a NaN for its scale.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float smallest(float a, float b, float c) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint32_t low_bytes(const float* t) {  // the low bytes of four sums
   const uint32_t a = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040);
   const uint32_t b = __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040);
@@ -74,11 +85,10 @@ __device__ __forceinline__ uint32_t low_bytes(const float* t) {  // the low byte
 
 // Eight codes as bytes in lo, hi; the block's scale in d.
 __device__ __forceinline__ void quant_q8(const float (&x)[8], uint32_t& lo, uint32_t& hi, __half& d) {
-  float am = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
-  am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
-  am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
+  float am = largest(largest(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), largest(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])),
+                     largest(fabsf(x[6]), fabsf(x[7]), 0.f));
+  am = largest(am, __shfl_xor_sync(kFull, am, 1), 0.f);
+  am = largest(am, __shfl_xor_sync(kFull, am, 2), 0.f);
   d = __float2half_rn(am / 127.f);
   const float inv = am > kTiny ? 127.f * __frcp_rn(am) : 0.f;
   float t[8], near = 0.f;
@@ -95,17 +105,36 @@ __device__ __forceinline__ void quant_q8(const float (&x)[8], uint32_t& lo, uint
   lo = low_bytes(t), hi = low_bytes(t + 4);
 }
 
-// Eight codes 0..15 as bytes.
-__device__ __forceinline__ void quant_q4(const float (&x)[8], uint32_t& lo, uint32_t& hi, __half& d) {
-  float am = 0.f, m = 0.f;
+// The first of the block's values of largest magnitude, where two signs share it (all lanes of the warp)
+static __device__ __noinline__ float first_largest(float4 a, float4 b) {
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float m = x[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (fabsf(x[i]) > am) am = fabsf(x[i]), m = x[i];
+  for (int i = 1; i < 8; ++i)
+    if (fabsf(x[i]) > fabsf(m)) m = x[i];
 #pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {  // the first of equal magnitudes: the lower lane's
+  for (int o = 1; o <= 2; o <<= 1) {  // of equal ones the lower lane's
     const float m2 = __shfl_xor_sync(kFull, m, o);
     const bool lower = (threadIdx.x & o) != 0;  // the partner is the lower lane
     if (fabsf(m2) > fabsf(m) || (fabsf(m2) == fabsf(m) && lower)) m = m2;
+  }
+  return m;
+}
+
+// Eight codes 0..15 as bytes.
+__device__ __forceinline__ void quant_q4(const float (&x)[8], uint32_t& lo, uint32_t& hi, __half& d) {
+  float top = largest(largest(x[0], x[1], x[2]), largest(x[3], x[4], x[5]), largest(x[6], x[7], x[7]));
+  float low = smallest(smallest(x[0], x[1], x[2]), smallest(x[3], x[4], x[5]), smallest(x[6], x[7], x[7]));
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const float t2 = __shfl_xor_sync(kFull, top, o), l2 = __shfl_xor_sync(kFull, low, o);
+    top = largest(top, t2, t2), low = smallest(low, l2, l2);
+  }
+  float m = (top > -low ? top : low) + 0.f;  // (+0 for a block of zeros, whatever their signs)
+  const bool both = top == -low;
+  if (__any_sync(kFull, both && top > 0.f)) {
+    const float f = first_largest(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]));
+    if (both) m = f;
   }
   d = __float2half_rn(m * -0.125f);
   const float inv = fabsf(m) > kTiny ? -8.f * __frcp_rn(m) : 0.f;

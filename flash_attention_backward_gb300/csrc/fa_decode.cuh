@@ -446,13 +446,11 @@ __host__ __device__ constexpr int map_es(int pitch) { return pitch <= 512 ? 1 : 
 // warps or waits for its first rows, the others work.  Registers (about 168 a thread for Dv = 256, else
 // 128) allow 12 or 16 warps an SM; shared memory may allow fewer.  What it has left goes to slots (a
 // tile's key rows and value rows) of each warp's ring, which also takes the warp's sums in the end.
-#ifndef FA_NW
-#define FA_NW 4
-#endif
+constexpr int kWarps = 4;
 constexpr int kSmemSm = 227 * 1024;  // of an SM, for dynamic and static arrays and 1 KB a CTA
 constexpr int kSlotCtl = 160;        // a slot's row addresses, barriers and mask (struct Slot of the kernel)
 struct DecodeShape {
-  int nw, ctas, slots, smem, pk, pv, qf, stage, ring;
+  int ctas, slots, smem, pk, pv, qf, stage, ring;
 };
 __host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, int vt) {
   DecodeShape c{};
@@ -460,14 +458,12 @@ __host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, in
   c.qf = (kt == FA_F32 ? D / 8 : D / 16) * 512;
   c.stage = 16 * (c.pk + c.pv);
   const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 3072;
-  c.nw = FA_NW;
-  c.ctas = (DV == 256 ? 12 : 16) / c.nw;
-  while (c.ctas > 1 && fixed + c.nw * (slot > sums ? slot : sums) > kSmemSm / c.ctas) --c.ctas;
-  while (c.nw > 4 && fixed + c.nw * slot > kSmemSm / c.ctas) c.nw -= 4;
-  c.slots = (kSmemSm / c.ctas - fixed) / (c.nw * slot);
+  c.ctas = (DV == 256 ? 12 : 16) / kWarps;
+  while (c.ctas > 1 && fixed + kWarps * (slot > sums ? slot : sums) > kSmemSm / c.ctas) --c.ctas;
+  c.slots = (kSmemSm / c.ctas - fixed) / (kWarps * slot);
   if (c.slots > 4) c.slots = 4;
   c.ring = c.slots * c.stage > sums ? c.slots * c.stage : (sums + 127) / 128 * 128;
-  c.smem = c.qf + c.nw * c.ring;
+  c.smem = c.qf + kWarps * c.ring;
   return c;
 }
 
@@ -658,10 +654,10 @@ static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float sl
 // neighbouring rows are read at the same time.  Each warp takes every NW-th tile of 16 keys with a ring, a
 // running maximum and sums of its own: no barrier until the item's last tile.
 template <int D, int DV, int KT, int VT>
-__global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_shape(D, DV, KT, VT).ctas)
+__global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
-  constexpr int NW = C.nw, SLOTS = C.slots, PK = C.pk, PV = C.pv;
+  constexpr int NW = kWarps, SLOTS = C.slots, PK = C.pk, PV = C.pv;
   constexpr int RBK = cache_row_bytes(KT, D), RBV = cache_row_bytes(VT, DV);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_scan[NW];
@@ -731,18 +727,12 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
     }
   }
   __syncthreads();
-  struct Segment {
-    int b, keys, j0, j1, ntile;  // sequence, its keys, the item's keys [j0, j1) and tiles
-  };
   const int4 item = s_item;
   if (item.x < 0) return;
-  Segment sg;
-  sg.b = item.x, sg.keys = seq_keys(a, item.x);
-  {
-    const long long n = tiles_of(sg.keys);
-    sg.j0 = 16 * (int)(n * item.z / item.y), sg.j1 = min(sg.keys, 16 * (int)(n * (item.z + 1) / item.y));
-    sg.ntile = tiles_of(sg.j1 - sg.j0);
-  }
+  const int b = item.x, keys = seq_keys(a, b);
+  const long long n_all = tiles_of(keys);
+  const int j0 = 16 * (int)(n_all * item.z / item.y);  // the item's keys [j0, j1) and tiles
+  const int j1 = min(keys, 16 * (int)(n_all * (item.z + 1) / item.y)), ntile = tiles_of(j1 - j0);
   const bool whole = item.y == 1;
 
   // ---- rows of a tile: key `lane` & 15 a lane.  Boxes of rows (16 or 8 in one page) go by the tensor maps,
@@ -750,31 +740,31 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
   // box a lane; single rows a tile at a time.
   const int boxes = a.box == 8 ? 2 : 1, per_batch = 32 / boxes;  // boxes of a tile, tiles of a lookup
   auto lookup = [&](int j) {  // row of the pool of key j, -1 where there is none
-    if (j >= sg.j1) return -1;
+    if (j >= j1) return -1;
     const int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
-    const int page = __ldg(a.c.table + (long long)sg.b * a.c.max_pages + p);
+    const int page = __ldg(a.c.table + (long long)b * a.c.max_pages + p);
     if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + (j - p * a.c.page_size);
     *a.c.err = FA_ERR_PAGE;
     return -1;
   };
   int found = -1, found_at = -1000;  // the lookup's rows, and the warp's turn that it starts with
   auto row_of = [&](int turn) {  // of the warp's turn-th tile
-    if (!a.box) return lookup(sg.j0 + 16 * (warp + NW * turn) + (lane & 15));
+    if (!a.box) return lookup(j0 + 16 * (warp + NW * turn) + (lane & 15));
     if (turn - found_at >= per_batch) {
       const int l = a.box == 8 ? lane >> 1 : lane;
-      found = lookup(sg.j0 + 16 * (warp + NW * (turn + l)) + (a.box == 8 ? 8 * (lane & 1) : 0));
+      found = lookup(j0 + 16 * (warp + NW * (turn + l)) + (a.box == 8 ? 8 * (lane & 1) : 0));
       found_at = turn;
     }
     return __shfl_sync(kFull, found, (turn - found_at) * boxes + (a.box == 8 ? (lane >> 3) & 1 : 0));
   };
   uint32_t phases = 0, armed = 0;  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way
-  auto fetch = [&](const Segment& s, int kv, int slot, int row, int tile) {
+  auto fetch = [&](int kv, int slot, int row, int tile) {
     const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), bar = sl + 128 + 8 * kv;
     const uint32_t dst = ring + slot * C.stage + (kv ? 16 * PK : 0);
     const int pitch = kv ? PV : PK;
     armed |= 1u << (4 * kv + slot);
     if (a.box) {
-      const int n = min(16, s.j1 - (s.j0 + tile * 16));  // the rows behind them are not used
+      const int n = min(16, j1 - (j0 + tile * 16));  // the rows behind them are not used
       const bool in = (lane & 15) < n && row >= 0;
       const uint32_t ok = a.box == 16 ? (row >= 0 ? (1u << n) - 1 : 0) : __ballot_sync(kFull, in) & 0xffffu;
       if (lane == 0) {
@@ -806,26 +796,30 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
     return true;
   };
   int slot = 0;
-  auto prefetch = [&](const Segment& s) {
+  auto prefetch = [&] {
     for (int i = 0, sl = slot; i < SLOTS; ++i) {
       const int tile = warp + i * NW;
-      if (tile < s.ntile) {
+      if (tile < ntile) {
         const int row = row_of(i);
-        fetch(s, 0, sl, row, tile), fetch(s, 1, sl, row, tile);
+        fetch(0, sl, row, tile), fetch(1, sl, row, tile);
       }
       if (++sl == SLOTS) sl = 0;
     }
   };
   // q of the chunk's heads, a head a warp: scaled by a power of two into range, split into parts
-  auto load_q = [&](const Segment& s) {
+  auto load_q = [&] {
     for (int h = warp; h < 8; h += NW) {
-      const long long at = s.b * a.q_row + (head0 + h) * a.q_head;
+      const long long at = b * a.q_row + (head0 + h) * a.q_head;
       float m = 0.f;
       if (h < nh)
         for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(act_load(a.q, a.act, at + d)));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      const float qs = m > 0.f && m < INFINITY ? ldexpf(1.f, (KT == FA_F32 ? 0 : 8) - ilogbf(m)) : 1.f;
+      // the largest magnitude goes to 2^8 (binary16 parts), or with f32 keys into 2^-80 .. 2^60 (whose tf32
+      // parts are not denormal, and whose products with keys have room)
+      const int e = m > 0.f && m < INFINITY ? ilogbf(m) : 8;
+      const int up = KT == FA_F32 ? min(max(e, -80), 60) - e : min(8 - e, 126);
+      const float qs = ldexpf(1.f, up);
       if (lane == 0) s_qs[h] = qs;
       constexpr int steps = KT == FA_F32 ? D / 8 : D / 16;
       for (int ks = g; ks < steps; ks += 8) {
@@ -846,8 +840,8 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
     }
   };
 
-  prefetch(sg);
-  load_q(sg);
+  prefetch();
+  load_q();
   __syncthreads();
   bool dead = false;  // a wait ran out: no more work is issued
   {
@@ -861,7 +855,6 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
-    const int ntile = sg.ntile;
     int next = warp + SLOTS * NW, turn = SLOTS;
     for (int tile = warp; tile < ntile; tile += NW, next += NW, ++turn) {
       const int row = next < ntile ? row_of(turn) : -1;
@@ -876,12 +869,12 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
       transpose_scores(s);
       const uint32_t ok = lds_u32(sl + 144);
       __syncwarp();
-      if (next < ntile) fetch(sg, 0, slot, row, next);
+      if (next < ntile) fetch(0, slot, row, next);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] *= qscale;
       if (ext) {
         const float4 x = cap_and_bias(make_float4(s[0], s[1], s[2], s[3]), a.softcap, slope,
-                                      sg.j0 + tile * 16 + 2 * t - (sg.keys - 1));
+                                      j0 + tile * 16 + 2 * t - (keys - 1));
         s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
       }
 #pragma unroll
@@ -917,7 +910,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
       else if (VT == FA_Q4_0) values_q4<DV>(o, p, sl + 64, lane);
       else values_f32<DV>(o, p, sl + 64, lane);
       __syncwarp();
-      if (next < ntile) fetch(sg, 1, slot, row, next);
+      if (next < ntile) fetch(1, slot, row, next);
       if (++slot == SLOTS) slot = 0;
     }
     if (dead) {  // let the copies in flight land: nothing more is issued
@@ -958,11 +951,13 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
       if (whole && a.sinks && 2 * t + i < nh) {  // one more term of the sum, without a value
         const float sk = a.sinks[head0 + 2 * t + i] * kLog2e;
         top = fmaxf(M[i], sk);
-        f = M[i] == -INFINITY ? 0.f : exp2f(M[i] - top);
-        total = S[i] * f + exp2f(sk - top + kLift);
+        if (top > -INFINITY) {
+          f = exp2f(M[i] - top);
+          total = S[i] * f + exp2f(sk - top + kLift);
+        }
       }
-      fin[i] = whole ? (total > 0.f ? f / total : 0.f) : 1.f;
-      lse[i] = total > 0.f ? (top - kLift + log2f(total)) * kLn2 : -INFINITY;
+      fin[i] = whole ? (total == 0.f ? 0.f : f / total) : 1.f;
+      lse[i] = total == 0.f ? -INFINITY : (top - kLift + log2f(total)) * kLn2;
     }
     for (int n = warp; n < DV / 16; n += NW) {
       float x[4] = {};
@@ -976,7 +971,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
       for (int i = 0; i < 4; ++i) {
         const int h = 2 * t + (i & 1), d = v_comp(VT, n, g, i >> 1);
         if (h < nh) {
-          if (whole) act_store(a.O, a.act, ((long long)sg.b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
+          if (whole) act_store(a.O, a.act, ((long long)b * a.H + head0 + h) * DV + d, x[i] * fin[i & 1]);
           else part[h * DV + d] = x[i];
         }
       }
@@ -985,7 +980,7 @@ __global__ void __launch_bounds__(decode_shape(D, DV, KT, VT).nw * 32, decode_sh
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = 2 * t + i;
-        if (h < nh && whole && a.lse) a.lse[(long long)sg.b * a.H + head0 + h] = lse[i];
+        if (h < nh && whole && a.lse) a.lse[(long long)b * a.H + head0 + h] = lse[i];
         if (!whole) part[8 * DV + h] = M[i], part[8 * DV + 8 + h] = S[i];
       }
     }
@@ -1052,11 +1047,11 @@ __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
     x.x = fmaf(v.x, f, x.x), x.y = fmaf(v.y, f, x.y), x.z = fmaf(v.z, f, x.z), x.w = fmaf(v.w, f, x.w);
   }
   if (a.sinks) S += fab::ex2(sk - ref + kLift);
-  const float inv = S > 0.f ? 1.f / S : 0.f;
+  const float inv = S == 0.f ? 0.f : 1.f / S;
   const long long at = ((long long)job.x * a.H + h) * DV + 4 * ln;
   act_store(a.O, a.act, at, x.x * inv), act_store(a.O, a.act, at + 1, x.y * inv);
   act_store(a.O, a.act, at + 2, x.z * inv), act_store(a.O, a.act, at + 3, x.w * inv);
-  if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S > 0.f ? (ref - kLift + log2f(S)) * kLn2 : -INFINITY;
+  if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S == 0.f ? -INFINITY : (ref - kLift + log2f(S)) * kLn2;
 }
 
 typedef cudaError_t (*DecodeFn)(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s);
@@ -1075,7 +1070,7 @@ cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s)
     ready.fetch_or(bit);
   }
   if (a.items && (e = launch_next(k_decode_plan, dim3(1), dim3(1024), 0, s, a)) != cudaSuccess) return e;
-  e = launch_next(k_decode<D, DV, KT, VT>, dim3((unsigned)(a.nitems * a.HG)), dim3(C.nw * 32), C.smem, s, a, m.k, m.v);
+  e = launch_next(k_decode<D, DV, KT, VT>, dim3((unsigned)(a.nitems * a.HG)), dim3(kWarps * 32), C.smem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
   if (a.njobs > 0) return launch_next(k_decode_join<DV>, dim3(a.njobs, a.H), dim3(512), 0, s, a);
   return cudaSuccess;

@@ -64,7 +64,9 @@ fa_status fa_rope_frequencies(int n_rot, double base, double scale, const float*
  * views: token n, head h starts at element n*row + h*head of its tensor (components contiguous),
  * so both may lie in one fused projection.  Outputs are contiguous, [N][H][D] and [N][Hkv][D], of
  * y_type; q_out may be q itself (and k_out k) when q is contiguous and y_type is x_type.  Hkv may
- * be 0 (k and k_out unused).  wq, wk f32 [D]; eps >= 0; pos [N] (unused without rotation).
+ * be 0 (k and k_out unused).  wq, wk f32 [D]; eps >= 0; pos [N] (unused without rotation).  The sum
+ * of squares is f32: it overflows for components beyond about 1e18, and below 1e-19 it vanishes
+ * beside any eps that is not 0.
  * D in {64, 128, 256}.  Alignment: q and k to their element; the outputs 16 bytes.
  */
 typedef struct fa_qk_views {
@@ -81,8 +83,10 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, const fa_qk_
  * r = rsqrt(mean(x^2) + eps), g = R(pos)^T gy and h = w o g:
  *   dx = r (h - x r^2 mean(h o x)),   dw = sum over tokens and heads of g o x r
  * (without a weight dx = g, and x is not read: q, k may then be NULL).  dq, dk: contiguous, of
- * x_type.  dwq, dwk: f32 [D], written where wq / wk is given (NULL: not wanted).  N = 0 writes
- * zeros to dwq and dwk.  Alignment: as for the forward; gq, gk, dq, dk 16 bytes.
+ * x_type, not overlapping the inputs.  dwq, dwk: f32 [D], written where wq / wk is given (NULL: not
+ * wanted).  N = 0 writes zeros to dwq and dwk.  Alignment: as for the forward; gq, gk, dq, dk 16
+ * bytes, workspace 256 bytes.  The kernel's waits for its own copies are bounded: one that runs out
+ * is reported as FA_ERR_TIMEOUT by fa_back_get_error() and leaves the outputs undefined.
  */
 size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv, int D);
 fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, int y_type, const void* q, const void* k, int x_type,
@@ -121,9 +125,10 @@ typedef struct fa_paged_cache {
  *   FA_Q8_0  d = amax / 127; code = x / d to the nearest, ties away from zero.
  *   FA_Q4_0  d = m / -8 with m the first of the values of largest magnitude; code = min(15,
  *            floor(x / d + 8.5)).
- * The scale is stored as binary16(d), the codes use d itself; a block whose scale is zero in f32
- * gets zero codes (q4_0: 8).  Blocks with a value above 8.3e6 (q8_0) or 5.2e5 (q4_0), or one that
- * is not finite, leave binary16's range and do not decode to finite values.
+ * The scale is stored as binary16(d), the codes use d itself; a block of no value above 1e-30, whose
+ * stored scale is zero, gets zero codes (q4_0: 8).  Blocks with a value above 8.3e6 (q8_0) or 5.2e5
+ * (q4_0), or one that is not finite, leave binary16's range: none of their values decodes to a
+ * finite one.
  */
 typedef struct fa_kv_views {
   int64_t k_row, k_head, v_row, v_head; /* in elements, >= 0 */
@@ -153,10 +158,12 @@ fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* seq, const i
  * that is fa_forward() of a single query (N = 1) with the score extensions of fa_back_ext().
  * L = 0 gives O = 0 and lse = -inf (sinks[h] with sinks).  L < 0 marks a padding slot: its O and
  * lse are left as they were.  L above max_pages * page_size counts as that many (FA_ERR_PAGE);
- * keys on an invalid page count as masked (FA_ERR_PAGE).
+ * keys on an invalid page count as masked (FA_ERR_PAGE).  What rows behind seq_lens[b] hold does
+ * not matter.  An infinity or a NaN in q or in a row that counts may turn what it enters into NaN.
  * q [B][H][D] of act type may be a view (q_row, q_head strides in elements); O [B][H][Dv] of the
- * same type and lse [B][H] f32 (NULL: not wanted) are contiguous.  H % Hkv == 0.  Alignment: q to
- * its element, O 16 bytes, lse, seq_lens, alibi_slopes, sinks 4 bytes, workspace 256 bytes.
+ * same type and lse [B][H] f32 (NULL: not wanted) are contiguous.  H % Hkv == 0; H at most 65535, B
+ * at most 2^20, num_pages * page_size below 2^31 (else FA_ERR_UNSUPPORTED).  Alignment: q to its
+ * element, O 16 bytes, lse, seq_lens, alibi_slopes, sinks 4 bytes, workspace 256 bytes.
  * The workspace holds the split partials; its size does not depend on the lengths.
  * The kernel's waits for its own copies are bounded: one that runs out is reported as FA_ERR_TIMEOUT
  * by fa_back_get_error() and leaves the outputs undefined.  fa_back_test_wait_limit() applies to the

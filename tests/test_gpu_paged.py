@@ -388,6 +388,28 @@ def test_append_random(fb, seed):
     assert fb.fa_back_get_error() == 0
 
 
+@pytest.mark.parametrize("ty", [Q8, Q4])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf, 1e9])
+@pytest.mark.parametrize("at", [0, 13, 31])
+def test_append_block_without_a_finite_scale(fb, ty, bad, at):
+    """A block that holds a NaN, an infinity or a value beyond binary16's scale decodes to no finite value;
+    the blocks beside it are as they would be."""
+    rng = np.random.default_rng(at)
+    x = rng.standard_normal((2, 1, 64)).astype(np.float32)
+    x[1, 0, 32 + at] = bad
+    cache, _ = empty_cache(fb, 1, 1, 16, 1, 64, 64, ty, ty)
+    seq, pos = cuda(np.zeros(2, np.int32)), cuda(np.arange(2, dtype=np.int32))
+    fb.cache_append(cuda(x), cuda(x), cache, seq, pos)
+    got = fb.cache_read(cache, seq, pos)
+    clean = x.copy()
+    clean[1, 0, 32:] = 0.0
+    ref = R.stored(clean.astype(np.float64), ty)[1].astype(np.float32)
+    for n in ("k", "v"):
+        g = got[n].cpu().numpy()
+        assert not np.isfinite(g[1, 0, 32:]).any()
+        assert np.array_equal(g[0], ref[0]) and np.array_equal(g[1, 0, :32], ref[1, 0, :32])
+
+
 def test_append_strided_views_match_contiguous(fb):
     rng = np.random.default_rng(11)
     T, H, Hkv, D = 45, 4, 2, 128
@@ -530,6 +552,37 @@ def test_decode_value_range(fb, vt, amp):
     """Values far from one: block scales and products leave neither end of the working types' range."""
     p = R.Paged(vt + 40, [500, 30], 2, 128, 128, Q8, vt, 16, v_amp=amp)
     check_decode(fb, p, 8)
+
+
+@pytest.mark.parametrize("kt", [F32, F16, Q8, Q4])
+@pytest.mark.parametrize("q_amp, k_amp, scale", [(1e-39, 1.0, 1.0), (1e-36, 1.0, 1e36), (1e37, 1.0, 1e-37), (1e-30, 1e3, 1e27)])
+def test_decode_query_range(fb, kt, q_amp, k_amp, scale):
+    """Queries near both ends of f32's range (denormal ones too), with keys and a scale that bring the scores back."""
+    p = R.Paged(60 + kt, [900, 30], 2, 128, 128, kt, Q8, 16, k_amp=k_amp)
+    check_decode(fb, p, 8, q_amp=q_amp, scale=scale / 11.3)
+
+
+def test_decode_f32_keys_beyond_other_types(fb):
+    """f32 keys of 1e30: the products are those of q and k themselves."""
+    p = R.Paged(71, [900, 30], 2, 64, 64, F32, F32, 16, k_amp=1e30)
+    check_decode(fb, p, 4, q_amp=1e-30)
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+def test_decode_nan_stays_with_its_head(fb, sinks):
+    p = R.Paged(72, [30, 2500, 0], 2, 64, 64, Q8, F16, 16)
+    q, qa = act_array(np.random.default_rng(3), (3, 6, 64), "f32")
+    sk = np.zeros(6, np.float32) if sinks else None
+    O, lse, mag, smag = R.decode(p, qa, 0.125, sinks=sk)
+    tol_O, tol_lse = R.decode_tolerance(p, mag, smag, "f32")
+    q[:, 4, 7] = float("nan")
+    got = fb.paged_decode(q, p.on_gpu(fb, torch), cuda(np.array(p.lens, np.int32)), scale=0.125, sinks=cuda(sk))
+    gO, gl = got["O"].cpu().numpy(), got["lse"].cpu().numpy()
+    assert np.isnan(gO[:2, 4]).all() and np.isnan(gl[:2, 4]).all()
+    rest = [0, 1, 2, 3, 5]
+    within(gO[:, rest], O[:, rest], tol_O[:, rest], "O")
+    within(gl[:, rest], lse[:, rest], tol_lse[:, rest], "lse")
+    assert not gO[2].any() and np.array_equal(gl[2], lse[2])
 
 
 def test_decode_equal_calls_and_streams(fb):
