@@ -683,6 +683,12 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   const int shift_k = hk * RBK & 15, shift_v = hk * RBV & 15;
   if (lane < 2 * SLOTS) fab::mbar_init(&s_slot[warp][lane >> 1].bar[lane & 1], 1);
   for (int i = threadIdx.x; i < DV + 4; i += NW * 32) s_zero[i] = 0;
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {  // the rows of a whole tile
+    const int kv = lane >> 4, r16 = lane & 15;
+    s_slot[warp][i].rows[kv][r16] = ring + i * C.stage + (kv ? 16 * PK + shift_v + r16 * PV : shift_k + r16 * PK);
+    if (lane == 0) s_slot[warp][i].valid = 0xffffu;
+  }
   fab::fence_mbar_init();  // ordered before the first copy by the barriers below
   after_last();
 
@@ -757,26 +763,47 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     }
     return __shfl_sync(kFull, found, (turn - found_at) * boxes + (a.box == 8 ? (lane >> 3) & 1 : 0));
   };
-  uint32_t phases = 0, armed = 0;  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way
+  // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way, mask or places not the usual ones
+  uint32_t phases = 0, armed = 0, patched = 0;
   auto fetch = [&](int kv, int slot, int row, int tile) {
     const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), bar = sl + 128 + 8 * kv;
     const uint32_t dst = ring + slot * C.stage + (kv ? 16 * PK : 0);
     const int pitch = kv ? PV : PK;
     armed |= 1u << (4 * kv + slot);
-    if (a.box) {
-      const int n = min(16, j1 - (j0 + tile * 16));  // the rows behind them are not used
-      const bool in = (lane & 15) < n && row >= 0;
-      const uint32_t ok = a.box == 16 ? (row >= 0 ? (1u << n) - 1 : 0) : __ballot_sync(kFull, in) & 0xffffu;
+    const int n = min(16, j1 - (j0 + tile * 16));  // the rows behind them are not used
+    const CUtensorMap* map = kv ? &map_v : &map_k;
+    const int x = kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK);
+    // A slot's mask and its value rows' places are rewritten for a tile with rows missing, and after one.
+    const uint32_t bit = 1u << (4 * kv + slot);
+    if (a.box == 16) {
       if (lane == 0) {
-        if (kv == 0) sts_u32(sl + 144, ok);
-        const int boxes = a.box == 16 ? (ok ? 2 : 0) : ((ok & 0xff) ? 1 : 0) + ((ok >> 8) ? 1 : 0);
-        bar_expect(bar, boxes * 8 * pitch);
+        bar_expect(bar, row >= 0 ? 16 * pitch : 0);
+        if (row >= 0) tile_rows(dst, map, x, row, bar);
       }
+      const bool part = n < 16 || row < 0;
+      if (part || (patched & bit)) {
+        patched = part ? patched | bit : patched & ~bit;
+        if (kv == 0) {
+          if (lane == 0) sts_u32(sl + 144, row >= 0 ? (1u << n) - 1 : 0);
+        } else if (lane < 16) {
+          sts_u32(sl + 64 + 4 * lane, lane < n && row >= 0 ? dst + lane * pitch + shift_v : smem_u32(s_zero));
+        }
+      }
+      return;
+    }
+    if (a.box) {
+      const uint32_t ok = __ballot_sync(kFull, (lane & 15) < n && row >= 0) & 0xffffu;
+      if (lane == 0) bar_expect(bar, (((ok & 0xff) ? 1 : 0) + ((ok >> 8) ? 1 : 0)) * 8 * pitch);
       __syncwarp();
-      if (lane == 0 ? ok & 0xff : lane == 8 && a.box == 8 && (ok >> 8))
-        tile_rows(dst + lane * pitch, kv ? &map_v : &map_k, kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK), row, bar);
-      if (lane < 16)
-        sts_u32(sl + 64 * kv + 4 * lane, kv && !in ? smem_u32(s_zero) : dst + lane * pitch + (kv ? shift_v : shift_k));
+      if (lane == 0 ? ok & 0xff : lane == 8 && (ok >> 8)) tile_rows(dst + lane * pitch, map, x, row, bar);
+      if (ok != 0xffffu || (patched & bit)) {
+        patched = ok != 0xffffu ? patched | bit : patched & ~bit;
+        if (kv == 0) {
+          if (lane == 0) sts_u32(sl + 144, ok);
+        } else if (lane < 16) {
+          sts_u32(sl + 64 + 4 * lane, ok >> lane & 1 ? dst + lane * pitch + shift_v : smem_u32(s_zero));
+        }
+      }
       return;
     }
     const uint8_t* pool = kv ? a.c.v : a.c.k;
