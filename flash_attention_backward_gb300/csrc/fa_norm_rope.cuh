@@ -10,6 +10,12 @@
 // the layout: D / 8 lanes a head, and a lane holds both members of its four rotation pairs, which makes
 // the rotation free of shuffles; packed pairs of f32 (fma.rn.f32x2) halve the instructions; the angles of a
 // token are computed once for all heads of it that a warp takes.
+//
+// Measured on a GB300 (6787 GB/s copy rate): forward, 2048 tokens of 28 heads of 256, f32: 117 MB in 17.7 us,
+// 98 % of the copy rate; 16411 tokens of 10 heads of 64, bf16 to f32: 63 MB in 15.5 us, 60 % (instructions: a
+// head of 64 has half the bytes, and the 16 angles of its token are shared by ten heads only).  Gradient, 8191
+// tokens of 40 heads of 128, bf16: 252 MB in 51 us, 73 %; 2048 tokens of 28 heads of 256, f32: 176 MB in
+// 33 us, 78 %.  A decode step's call (64 tokens) is 2.4 us, a launch and two latencies.
 #pragma once
 #include "fa_paged.cuh"
 #include "sm100.cuh"
@@ -190,8 +196,9 @@ struct Lane {
 // A warp takes HC heads of one token, 256 / D side by side, and loads the next kRows of each together.
 // VEC: every head of x starts on 16 bytes (else it is loaded element by element).  Lanes without a head of
 // their own (the last ones of a token) work on the last head and store nothing.
-// With 16-bit x, whose time is its instructions, a warp goes on to further tokens with both weights at hand;
-// with f32 x, whose time is its bytes, many short warps keep more loads in flight.
+// With 16-bit x, whose time is its instructions, a warp goes on to further tokens with both weights at hand
+// (16411 tokens of 10 heads of 64: 18.5 -> 15.5 us); with f32 x, whose time is its bytes, many short warps
+// keep more loads in flight (2048 tokens of 28 heads of 256: 17.7 us, and 23.9 the other way).
 template <typename TX>
 constexpr int kForwardCtas = sizeof(TX) == 2 ? 3 : 0;  // CTAs an SM, or 0: a warp takes one item
 template <int D, typename TX, typename TY, bool VEC, int STYLE>
@@ -255,7 +262,8 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
 // The gradient.  Each warp takes a run of items (HC heads of a token), which pass through a ring of its own
 // in shared memory: bulk copies bring x and gy of the items to come while one is worked on, which takes
 // the loads off the registers and the issue slots.  A token's factors are computed when the run comes to
-// it.  dw is summed by lane over the run, then over the CTA's lane groups in order.
+// it.  dw is summed by lane over the run, then over the CTA's lane groups in order.  (Loads into registers
+// instead of the ring: 79 us for 8191 tokens of 40 heads of 128, bf16, against 51.)
 constexpr int kBackCtas = 2, kBackWarps = 8;
 // Slots of a warp's ring and their bytes: a head of f32 takes up to 2 KB, and an item of one or two would
 // cost more in its handling than in its work (2048 tokens of 28 heads of 256: 33.8 us with 2 slots of
