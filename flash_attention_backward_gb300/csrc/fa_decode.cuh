@@ -1027,8 +1027,8 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
 
 // Joins the parts of a split sequence (blockIdx.x), in their order, for a query head (blockIdx.y).  The grid
 // starts while the items' last CTAs run.  Each group of threads takes every GR-th part with a running
-// maximum, then the groups are joined: bound by the latency of two rounds of loads, about 3 us behind the
-// items' end (75520 keys: 114 parts of 24 heads, 2.8 MB).
+// maximum, then the groups are joined: bound by the latency of a launch and two rounds of loads (75520 keys:
+// about 114 parts of 24 heads, 2.8 MB, read from L2).
 template <int DV>
 __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
   constexpr int LN = DV / 4, GR = 512 / LN;  // threads of a row (four components each), rows read at a time

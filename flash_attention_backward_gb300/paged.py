@@ -1,7 +1,8 @@
 """PyTorch-facing wrappers of fa_paged.h: the paged raw cache, and the per-head norm and rotation.
 
 Each call allocates its outputs and workspace with PyTorch and enqueues on the current stream of the
-tensors' device (or on `stream`).
+tensors' device (or on `stream`).  No autograd graph is recorded: qk_norm_rope_backward() is called as
+backward() is.
 """
 from __future__ import annotations
 
