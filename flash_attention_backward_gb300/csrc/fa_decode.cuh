@@ -468,7 +468,7 @@ __host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, in
   c.pk = smem_pitch(cache_row_bytes(kt, D)), c.pv = smem_pitch(cache_row_bytes(vt, DV));
   c.qf = (kt == FA_F32 ? D / 8 : D / 16) * 512;
   c.stage = 16 * (c.pk + c.pv);
-  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 3072;
+  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 3 * 1024;
   c.ctas = (DV == 256 ? 12 : 16) / kWarps;
   while (c.ctas > 1 && fixed + kWarps * (slot > sums ? slot : sums) > kSmemSm / c.ctas) --c.ctas;
   c.slots = (kSmemSm / c.ctas - fixed) / (kWarps * slot);
