@@ -554,6 +554,46 @@ def test_decode_value_range(fb, vt, amp):
     check_decode(fb, p, 8)
 
 
+@pytest.mark.parametrize("page", [16, 64, 40, 20])
+@pytest.mark.parametrize("kt, vt", [(Q8, Q8), (F16, F16)])
+def test_decode_around_invalid_pages(fb, kt, vt, page):
+    """Pages without a valid number in the middle of long sequences: their keys are masked, those behind them count."""
+    p = R.Paged(page + kt, [4000, 700, 33], 2, 128, 128, kt, vt, page)
+    rng = np.random.default_rng(page)
+    bad = rng.random(p.table.shape) < 0.2
+    bad[:, 0] = [False, True, False]
+    p.table[bad] = np.where(rng.random(bad.sum()) < 0.5, -1, 10 ** 6)
+    q, qa = act_array(rng, (3, 8, 128), "f32")
+    got = fb.paged_decode(q, p.on_gpu(fb, torch), cuda(np.array(p.lens, np.int32)), scale=0.1)
+    torch.cuda.synchronize()
+    assert fb.STATUS[fb.fa_back_get_error()] == "FA_ERR_PAGE"
+    for b, n in enumerate(p.lens):
+        keep = ~bad[b, np.arange(n) // page]
+        p.kd[b], p.vd[b], p.lens[b] = p.kd[b][keep], p.vd[b][keep], int(keep.sum())
+    O, lse, mag, smag = R.decode(p, qa, 0.1)
+    tol_O, tol_lse = R.decode_tolerance(p, mag, smag, "f32")
+    within(got["O"].cpu().numpy(), O, tol_O, "O")
+    within(got["lse"].cpu().numpy(), lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("pair", [(16, 64), (40, 20)])
+def test_decode_calls_that_overlap(fb, pair):
+    """Calls on two streams at once, each with a workspace of its own."""
+    ps = [R.Paged(90 + i, [6000, 50, 900], 2, 128, 128, Q8, Q8, page) for i, page in enumerate(pair)]
+    want = [check_decode(fb, p, 8, seed=i) for i, p in enumerate(ps)]
+    lens = [cuda(np.array(p.lens, np.int32)) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for (q, cache, _), n, s in zip(want, lens, streams):
+            got.append(fb.paged_decode(q, cache, n, scale=128 ** -0.5, stream=s))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        out = want[i % 2][2]
+        assert torch.equal(g["O"], out["O"]) and torch.equal(g["lse"], out["lse"])
+
+
 @pytest.mark.parametrize("kt", [F32, F16, Q8, Q4])
 @pytest.mark.parametrize("q_amp, k_amp, scale", [(1e-39, 1.0, 1.0), (1e-36, 1.0, 1e36), (1e37, 1.0, 1e-37), (1e-30, 1e3, 1e27)])
 def test_decode_query_range(fb, kt, q_amp, k_amp, scale):
