@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -84,8 +85,9 @@ struct Args {
   bool here() { return ok && c10::cuda::current_device() == device; }
 };
 
+// (straight from the allocator: at::empty's dispatch is most of what it costs)
 at::Tensor make(at::IntArrayRef shape, at::ScalarType t, int device) {
-  return at::empty(shape, at::TensorOptions().dtype(t).device(at::Device(at::kCUDA, device)));
+  return at::Tensor(at::detail::empty_cuda(shape, t, at::Device(at::kCUDA, device), std::nullopt));
 }
 void put(PyObject* d, PyObject* key, const at::Tensor& t) {
   PyObject* o = THPVariable_Wrap(t);
