@@ -458,6 +458,7 @@ extern "C" fa_status fab_device(int* nsm, int** err) {
   *nsm = device_sms(&major, &minor);
   if (*nsm <= 0) return FA_ERR_CUDA;
   if (major != 10 || minor != 3) return FA_ERR_DEVICE;
+  if (!err) return FA_OK;
   return cudaGetSymbolAddress(reinterpret_cast<void**>(err), g_err) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

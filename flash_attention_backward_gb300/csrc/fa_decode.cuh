@@ -22,8 +22,6 @@
 // registers) do not raise that (45.4 us); rolling the key loop up does not either.  A short call is a chain
 // of latencies: launch, lengths, first rows, four tiles, the join (512 keys, 2 KV heads of 128: 9 us).
 #pragma once
-#include <atomic>
-
 #include "fa_paged.cuh"
 #include "sm100.cuh"
 
@@ -1099,15 +1097,8 @@ template <int D, int DV, int KT, int VT>
 cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
   static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev > 63 || !(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(k_decode<D, DV, KT, VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C.smem);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit);
-  }
+  cudaError_t e = cudaSuccess;
+  if (!allow_smem(reinterpret_cast<const void*>(k_decode<D, DV, KT, VT>), C.smem, &ready)) return cudaErrorInvalidValue;
   if (a.items && (e = launch_next(k_decode_plan, dim3(1), dim3(1024), 0, s, a)) != cudaSuccess) return e;
   e = launch_next(k_decode<D, DV, KT, VT>, dim3((unsigned)(a.nitems * a.HG)), dim3(kWarps * 32), C.smem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;

@@ -35,8 +35,8 @@ __attribute__((visibility("hidden"))) fa_status fab_back_capped(
     float* dV, float* lse, float* delta, void* workspace, size_t workspace_bytes, void* stream, size_t ws_cap,
     const float* lse_in, const float* delta_in, float* O, const fab_opts* ext);
 
-// The current device's SM count and the address of its error word; FA_ERR_DEVICE / FA_ERR_CUDA as
-// the entry points report them.
+// The current device's SM count and the address of its error word (err NULL: not wanted);
+// FA_ERR_DEVICE / FA_ERR_CUDA as the entry points report them.
 __attribute__((visibility("hidden"))) fa_status fab_device(int* nsm, int** err);
 
 // The wait limit of a call's kernels in nanoseconds: the normal one, or the pending limit of

@@ -116,8 +116,8 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, c
   if (rc != FA_OK) return rc;
   if (N > 0 && (!q_out || (Hkv > 0 && !k_out))) return FA_ERR_NULL;
   if (!aligned(q_out, 16) || !aligned(k_out, 16)) return FA_ERR_ALIGN;
-  int nsm = 0, *err = nullptr;
-  if ((rc = fab_device(&nsm, &err)) != FA_OK) return rc;
+  int nsm = 0;
+  if ((rc = fab_device(&nsm, nullptr)) != FA_OK) return rc;
   if (N == 0) return FA_OK;
   a.side[0].y = q_out, a.side[1].y = k_out;
   chunk_heads(H + Hkv, rows_a_warp(a, D, nsm), 256 / D, 32, &a.HC, &a.nchunk);
@@ -134,8 +134,8 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, c
 
 extern "C" size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv, int D) {
   if (N < 0 || H < 1 || Hkv < 0 || !head_size(D)) return 0;
-  int nsm = 0, *err = nullptr;
-  if (fab_device(&nsm, &err) != FA_OK) nsm = 152;
+  int nsm = 0;
+  if (fab_device(&nsm, nullptr) != FA_OK) nsm = 152;
   return (size_t)back_ctas(nsm) * D * sizeof(float);
 }
 
@@ -167,9 +167,7 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
   const int cq = (int)std::min<long long>(all - ck, std::max(1LL, (iq + 7) / 8));
   a.ctas_q = cq;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (k_back.smem > 48 * 1024 &&
-      cudaFuncSetAttribute(k_back.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k_back.smem) != cudaSuccess)
-    return FA_ERR_CUDA;
+  if (k_back.smem > 48 * 1024 && !allow_smem(reinterpret_cast<const void*>(k_back.fn), k_back.smem, k_back.ready)) return FA_ERR_CUDA;
   if (launch_next(k_back.fn, dim3(cq + ck), dim3(kBackWarps * 32), k_back.smem, s, a) != cudaSuccess) return FA_ERR_CUDA;
   float* oq = wq ? dwq : nullptr;
   float* ok = wk && Hkv ? dwk : nullptr;

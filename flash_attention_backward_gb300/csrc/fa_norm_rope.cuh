@@ -430,11 +430,12 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_a
 typedef void (*NormKernel)(const NormArgs);
 
 // The kernels for these types (fa_norm_rope_fwd.cu, fa_norm_rope_back.cu); of the gradient's, the heads of an
-// item and the bytes of dynamic shared memory too.
+// item and what there is to know of its dynamic shared memory too.
 NormKernel pick_norm_fwd(int D, int tx, int ty, bool vec, int style);
 struct BackKernel {
   NormKernel fn;
   int heads, smem;
+  std::atomic<uint64_t>* ready;  // devices that `smem` bytes have been allowed on
 };
 BackKernel pick_norm_back(int D, int tx, int ty, bool vec, int style);
 

@@ -8,8 +8,12 @@ template <int D, typename TX, typename TY>
 static BackKernel pick_style(bool vec, int style) {
   constexpr int heads = kBackHeads<D, TX, TY>, ring = kBackWarps * kBackSlots<TX, TY> * heads * D * (int)(sizeof(TX) + sizeof(TY));
   const bool pairs = style == FA_ROPE_PAIRS;
-  if (!vec) return BackKernel{pairs ? k_norm_rope_back_any<D, TX, TY, FA_ROPE_PAIRS> : k_norm_rope_back_any<D, TX, TY, FA_ROPE_HALVES>, heads, 0};
-  return BackKernel{pairs ? k_norm_rope_back<D, TX, TY, FA_ROPE_PAIRS> : k_norm_rope_back<D, TX, TY, FA_ROPE_HALVES>, heads, ring};
+  static std::atomic<uint64_t> ready[2];
+  if (!vec)
+    return BackKernel{pairs ? k_norm_rope_back_any<D, TX, TY, FA_ROPE_PAIRS> : k_norm_rope_back_any<D, TX, TY, FA_ROPE_HALVES>, heads, 0,
+                      nullptr};
+  return BackKernel{pairs ? k_norm_rope_back<D, TX, TY, FA_ROPE_PAIRS> : k_norm_rope_back<D, TX, TY, FA_ROPE_HALVES>, heads, ring,
+                    &ready[pairs]};
 }
 template <int D, typename TX>
 static BackKernel pick_y(int ty, bool vec, int style) {

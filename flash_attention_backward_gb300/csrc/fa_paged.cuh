@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/fa_paged.h"
 #include "fa_internal.h"
 
@@ -207,6 +209,15 @@ inline cudaError_t launch_next(void (*k)(P...), dim3 grid, dim3 block, size_t sm
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+// Allows a kernel's dynamic shared memory on the current device, once for each (ready: the devices so far).
+inline bool allow_smem(const void* k, int bytes, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && (ready->load() >> dev & 1)) return true;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev < 64) ready->fetch_or(1ull << dev);
+  return true;
 }
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool head_size(int d) { return d == 64 || d == 128 || d == 256; }

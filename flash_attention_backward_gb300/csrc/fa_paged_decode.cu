@@ -74,8 +74,8 @@ using namespace fap;
 extern "C" size_t fa_paged_decode_workspace_size(const fa_paged_cache* cache, int H) {
   Cache c;
   if (check_cache(cache, &c) != FA_OK || H < 1 || H % c.Hkv) return 0;
-  int nsm = 0, *err = nullptr;
-  if (fab_device(&nsm, &err) != FA_OK) nsm = 152;
+  int nsm = 0;
+  if (fab_device(&nsm, nullptr) != FA_OK) nsm = 152;
   return plan_decode(c, H, nsm).bytes;
 }
 
