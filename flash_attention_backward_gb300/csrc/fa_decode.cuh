@@ -15,7 +15,7 @@
 //
 // Bounds, on a GB300 (6787 GB/s measured copy rate).  The cache rows are read once; binary16 and f32 rows
 // are bound by that: 48 ragged sequences of up to 8192 keys (32 heads, 8 KV heads of 128, 602 MB) take
-// 108 us, 82 % of the copy rate.  Quantised rows are bound by instructions: a tile of q8_0 keys and values
+// 106 us, 84 % of the copy rate.  Quantised rows are bound by instructions: a tile of q8_0 keys and values
 // of 256 is about 1250 a warp, of which the decoding of 8192 codes is some 420 and the 64 products 64; one
 // sequence of 75520 keys (24 heads, 4 KV heads of 256, 164 MB) takes 43 us, 56 % of the copy rate, at 1.9
 // instructions a cycle and SM, with the tensor pipe 19 % busy.  Sixteen warps an SM instead of twelve (128
