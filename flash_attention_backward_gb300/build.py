@@ -2,9 +2,11 @@
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import tempfile
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -13,6 +15,7 @@ LIB = os.path.join(HERE, "libfa_back.so")
 FAST_SRC = os.path.join(CSRC, "py_fast.cpp")
 FAST = os.path.join(HERE, "_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+_fast_given_up = False  # the marshalling module could not be built in this process
 
 
 def sources():
@@ -30,7 +33,7 @@ def _newer(target: str, deps) -> bool:
 
 
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and _newer(FAST, _fast_deps())
+    return _newer(LIB, _deps()) and (_fast_given_up or _newer(FAST, _fast_deps()))
 
 
 def _fast_deps():
@@ -46,7 +49,7 @@ def _fast_command(out: str):
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     inc = [a for p in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-                       sysconfig.get_paths()["include"], "/usr/local/cuda/include") for a in ("-isystem", p)]
+                       sysconfig.get_paths()["include"], os.path.join(_cuda_home(), "include")) for a in ("-isystem", p)]
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", abi, *inc, FAST_SRC, "-o", out, "-L", lib,
             "-Wl,--no-as-needed", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-Wl,-rpath,{lib}"]
@@ -59,25 +62,64 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def _cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc()) or "/usr/local/cuda/bin/nvcc")))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libfa_back.so and the marshalling module _fast.so next to this file; returns the library's
+    """Build libfa_back.so and the marshalling module of paged.py next to this file; returns the library's
     path.  The translation units compile in parallel (one compiler per file, objects in a temporary
-    folder), then one link."""
+    folder), then one link.  The module is optional: without g++ or PyTorch's headers a warning says so,
+    and the wrappers make their calls from Python."""
     if not force and up_to_date():
         return LIB
-    fast = None
-    if force or not _newer(FAST, _fast_deps()):
-        fast = subprocess.Popen(_fast_command(FAST + ".tmp%d" % os.getpid()), stdout=subprocess.PIPE,
-                                stderr=subprocess.STDOUT, text=True)
-    if force or not _newer(LIB, _deps()):
-        _build_library(verbose)
+    fast = _FastBuild() if force or not (_fast_given_up or _newer(FAST, _fast_deps())) else None
+    try:
+        if force or not _newer(LIB, _deps()):
+            _build_library(verbose)
+    except BaseException:
+        if fast is not None:
+            fast.stop()
+        raise
     if fast is not None:
-        out, _ = fast.communicate()
-        if fast.returncode != 0:
-            sys.stderr.write(out)
-            raise RuntimeError("g++ failed building _fast.so")
-        os.replace(FAST + ".tmp%d" % os.getpid(), FAST)
+        fast.finish()
     return LIB
+
+
+class _FastBuild:
+    """The marshalling module's compiler, beside the library's.  What it was made of before goes first: a
+    module of older headers would not do for the library that is built now."""
+
+    def __init__(self):
+        self.tmp = FAST + ".tmp%d" % os.getpid()
+        self.proc, self.why = None, ""
+        if os.path.exists(FAST):
+            os.remove(FAST)
+        try:
+            self.proc = subprocess.Popen(_fast_command(self.tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        except (OSError, ImportError, AttributeError) as e:  # no g++, no PyTorch
+            self.why = "%s: %s" % (type(e).__name__, e)
+
+    def finish(self) -> None:
+        global _fast_given_up
+        if self.proc is not None:
+            out, _ = self.proc.communicate()
+            if self.proc.returncode == 0:
+                os.replace(self.tmp, FAST)
+                _fast_given_up = False
+                return
+            self.why = "g++ ended with %d: %s" % (self.proc.returncode, out.strip()[-500:])
+        _fast_given_up = True
+        self.stop()
+        warnings.warn("%s was not built, the wrappers make their calls from Python (%s)" % (os.path.basename(FAST), self.why),
+                      RuntimeWarning, stacklevel=3)
+
+    def stop(self) -> None:
+        if self.proc is not None and self.proc.poll() is None:
+            self.proc.kill()
+            self.proc.communicate()
+        if os.path.exists(self.tmp):
+            os.remove(self.tmp)
 
 
 def _build_library(verbose: bool) -> None:

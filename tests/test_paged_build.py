@@ -1,0 +1,69 @@
+"""The marshalling module of the paged wrappers is optional: the library builds and the wrappers work without it."""
+import os
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from flash_attention_backward_gb300 import build as B  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    B.build()
+
+
+@pytest.fixture
+def elsewhere(monkeypatch, tmp_path):
+    """The module goes to a folder of its own; an older one lies there."""
+    target = tmp_path / "_fast.so"
+    target.write_bytes(b"of an older build")
+    os.utime(target, (0, 0))
+    monkeypatch.setattr(B, "FAST", str(target))
+    monkeypatch.setattr(B, "_fast_given_up", False, raising=False)
+    return target
+
+
+def compiler(monkeypatch, folder, text):
+    folder.mkdir()
+    (folder / "g++").write_text(text)
+    (folder / "g++").chmod(0o755)
+    monkeypatch.setenv("PATH", str(folder) + os.pathsep + os.environ["PATH"])
+
+
+def test_a_compiler_that_fails_leaves_the_library_and_a_warning(monkeypatch, tmp_path, elsewhere):
+    log = tmp_path / "calls"
+    compiler(monkeypatch, tmp_path / "bin", "#!/bin/sh\necho called >> %s\n"
+             "while [ $# -gt 0 ]; do [ \"$1\" = -o ] && echo partial > \"$2\"; shift; done\necho no such header; exit 1\n" % log)
+    with pytest.warns(RuntimeWarning, match="no such header"):
+        assert B.build() == B.LIB
+    assert os.path.exists(B.LIB)
+    assert os.listdir(elsewhere.parent) in (["calls", "bin"], ["bin", "calls"])  # neither the older module nor half of a new one
+    B.build()  # not tried again in this process
+    assert log.read_text().count("called") == 1
+
+
+def test_no_compiler_and_no_torch(monkeypatch, tmp_path, elsewhere):
+    (tmp_path / "empty").mkdir()
+    monkeypatch.setenv("PATH", str(tmp_path / "empty"))
+    with pytest.warns(RuntimeWarning, match="FileNotFoundError"):
+        assert B.build() == B.LIB
+    monkeypatch.setattr(B, "_fast_given_up", False, raising=False)
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    with pytest.warns(RuntimeWarning, match="_fast"):
+        assert B.build() == B.LIB
+    assert not elsewhere.exists()
+
+
+def test_a_library_that_fails_stops_the_modules_compiler(monkeypatch, tmp_path, elsewhere):
+    compiler(monkeypatch, tmp_path / "bin", "#!/bin/sh\nexec sleep 600\n")
+    monkeypatch.setattr(B, "LIB", str(tmp_path / "lib.so"))
+
+    def fails(verbose):
+        raise RuntimeError("nvcc failed")
+
+    monkeypatch.setattr(B, "_build_library", fails)
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        B.build()
+    assert sorted(os.listdir(tmp_path)) == ["bin"]
