@@ -5,15 +5,20 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 import warnings
+
+try:
+    from ._fast_path import fast_path
+except ImportError:  # run as a file, without the package (and PyTorch)
+    from _fast_path import fast_path
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libfa_back.so")
 FAST_SRC = os.path.join(CSRC, "py_fast.cpp")
-FAST = os.path.join(HERE, "_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _fast_given_up = False  # the marshalling module could not be built in this process
 
@@ -28,12 +33,12 @@ def _deps():
     return out
 
 
-def _newer(target: str, deps) -> bool:
-    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+def _newer(target, deps) -> bool:
+    return target is not None and os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
 
 
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and (_fast_given_up or _newer(FAST, _fast_deps()))
+    return _newer(LIB, _deps()) and (_fast_given_up or _newer(fast_path(), _fast_deps()))
 
 
 def _fast_deps():
@@ -42,8 +47,6 @@ def _fast_deps():
 
 def _fast_command(out: str):
     """Compile and link the marshalling module of paged.py against this interpreter's PyTorch."""
-    import sysconfig
-
     import torch
 
     root = os.path.dirname(torch.__file__)
@@ -73,7 +76,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     and the wrappers make their calls from Python."""
     if not force and up_to_date():
         return LIB
-    fast = _FastBuild() if force or not (_fast_given_up or _newer(FAST, _fast_deps())) else None
+    fast = _FastBuild() if force or not (_fast_given_up or _newer(fast_path(), _fast_deps())) else None
     try:
         if force or not _newer(LIB, _deps()):
             _build_library(verbose)
@@ -91,13 +94,15 @@ class _FastBuild:
     module of older headers would not do for the library that is built now."""
 
     def __init__(self):
-        self.tmp = FAST + ".tmp%d" % os.getpid()
-        self.proc, self.why = None, ""
-        if os.path.exists(FAST):
-            os.remove(FAST)
+        self.target = fast_path()
+        self.tmp, self.proc, self.why = "%s.tmp%d" % (self.target, os.getpid()), None, "no PyTorch"
+        if self.target is None:
+            return
+        if os.path.exists(self.target):
+            os.remove(self.target)
         try:
             self.proc = subprocess.Popen(_fast_command(self.tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-        except (OSError, ImportError, AttributeError) as e:  # no g++, no PyTorch
+        except (OSError, AttributeError) as e:  # no g++, no PyTorch as expected
             self.why = "%s: %s" % (type(e).__name__, e)
 
     def finish(self) -> None:
@@ -105,13 +110,13 @@ class _FastBuild:
         if self.proc is not None:
             out, _ = self.proc.communicate()
             if self.proc.returncode == 0:
-                os.replace(self.tmp, FAST)
+                os.replace(self.tmp, self.target)
                 _fast_given_up = False
                 return
             self.why = "g++ ended with %d: %s" % (self.proc.returncode, out.strip()[-500:])
         _fast_given_up = True
         self.stop()
-        warnings.warn("%s was not built, the wrappers make their calls from Python (%s)" % (os.path.basename(FAST), self.why),
+        warnings.warn("the marshalling module _fast was not built, the wrappers make their calls from Python (%s)" % self.why,
                       RuntimeWarning, stacklevel=3)
 
     def stop(self) -> None:

@@ -7,17 +7,33 @@ backward() is.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from typing import Optional
 
 import torch
 
 from . import _native as nat
+from ._fast_path import fast_path
 from .api import FaBackError, Workspace, _check, _ptr
 
-try:
-    from . import _fast  # the plain form of the calls below, in C++ (csrc/py_fast.cpp)
-except ImportError:  # not built: the same calls from here, at a few microseconds more each
-    _fast = None
+
+def _load_fast():
+    """The plain form of the calls below, in C++ (csrc/py_fast.cpp), or None where it is not built for this
+    PyTorch and interpreter: the same calls are then made from here, at a few microseconds more each."""
+    path = fast_path()
+    if path is None or not os.path.exists(path):
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location(__package__ + "._fast", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError:
+        return None
+
+
+_fast = _load_fast()
 
 _ACT = {torch.float32: nat.FA_ACT_F32, torch.float16: nat.FA_ACT_F16, torch.bfloat16: nat.FA_ACT_BF16}
 _F32, _I32, _empty = torch.float32, torch.int32, torch.empty

@@ -20,7 +20,7 @@ def elsewhere(monkeypatch, tmp_path):
     target = tmp_path / "_fast.so"
     target.write_bytes(b"of an older build")
     os.utime(target, (0, 0))
-    monkeypatch.setattr(B, "FAST", str(target))
+    monkeypatch.setattr(B, "fast_path", lambda: str(target))
     monkeypatch.setattr(B, "_fast_given_up", False, raising=False)
     return target
 
@@ -50,10 +50,15 @@ def test_no_compiler_and_no_torch(monkeypatch, tmp_path, elsewhere):
     with pytest.warns(RuntimeWarning, match="FileNotFoundError"):
         assert B.build() == B.LIB
     monkeypatch.setattr(B, "_fast_given_up", False, raising=False)
-    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
-    with pytest.warns(RuntimeWarning, match="_fast"):
-        assert B.build() == B.LIB
     assert not elsewhere.exists()
+
+
+def test_without_torch_the_library_is_built(monkeypatch):
+    monkeypatch.setattr(B, "_fast_given_up", False)
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    assert B.fast_path() is None
+    with pytest.warns(RuntimeWarning, match="no PyTorch"):
+        assert B.build() == B.LIB
 
 
 def test_a_library_that_fails_stops_the_modules_compiler(monkeypatch, tmp_path, elsewhere):
@@ -67,3 +72,12 @@ def test_a_library_that_fails_stops_the_modules_compiler(monkeypatch, tmp_path, 
     with pytest.raises(RuntimeError, match="nvcc failed"):
         B.build()
     assert sorted(os.listdir(tmp_path)) == ["bin"]
+
+
+def test_a_module_of_another_torch_or_interpreter_is_not_taken(monkeypatch):
+    from flash_attention_backward_gb300 import paged
+    here = B.fast_path()
+    assert os.path.exists(here) and paged._load_fast() is not None
+    assert torch.__version__ in here and here.endswith(B.sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    assert B.fast_path() != here and not B.up_to_date() and paged._load_fast() is None
