@@ -112,6 +112,9 @@ class _FastBuild:
             if self.proc.returncode == 0:
                 os.replace(self.tmp, self.target)
                 _fast_given_up = False
+                paged = sys.modules.get((__package__ or "-") + ".paged")
+                if paged is not None:  # imported before there was a module
+                    paged.look_for_fast()
                 return
             self.why = "g++ ended with %d: %s" % (self.proc.returncode, out.strip()[-500:])
         _fast_given_up = True

@@ -35,6 +35,14 @@ def _load_fast():
 
 _fast = _load_fast()
 
+
+def look_for_fast() -> None:
+    """Take the marshalling module that has been built since this one was imported; the one that it has stays."""
+    global _fast
+    if _fast is None:
+        _fast = _load_fast()
+
+
 _ACT = {torch.float32: nat.FA_ACT_F32, torch.float16: nat.FA_ACT_F16, torch.bfloat16: nat.FA_ACT_BF16}
 _F32, _I32, _empty = torch.float32, torch.int32, torch.empty
 

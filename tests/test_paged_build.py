@@ -81,3 +81,24 @@ def test_a_module_of_another_torch_or_interpreter_is_not_taken(monkeypatch):
     assert torch.__version__ in here and here.endswith(B.sysconfig.get_config_var("EXT_SUFFIX"))
     monkeypatch.setattr(torch, "__version__", "0.0.0")
     assert B.fast_path() != here and not B.up_to_date() and paged._load_fast() is None
+
+
+def test_a_module_built_after_the_import_is_taken(monkeypatch, tmp_path):
+    """Import, then build in the same process, as from a fresh tree."""
+    import shutil
+
+    from flash_attention_backward_gb300 import paged
+    fresh = str(tmp_path / os.path.basename(B.fast_path()))
+    old = B.fast_path()
+    for m in (B, paged):
+        monkeypatch.setattr(m, "fast_path", lambda: fresh)
+    monkeypatch.setattr(paged, "_fast", None)
+    monkeypatch.setattr(paged, "_plain", False)
+    assert paged._load_fast() is None
+    monkeypatch.setattr(B, "_fast_command", lambda out: ["cp", old, out])  # (its compiler takes a while)
+    B.build()
+    assert paged._fast is not None and callable(paged._fast.decode) and not paged._plain
+    was = paged._fast
+    shutil.copy(old, fresh)
+    paged.look_for_fast()
+    assert paged._fast is was
