@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   // sequences without keys: their rows, by the CTA whose turn it is
   for (int b = r + a.nitems * threadIdx.x; b < B; b += a.nitems * NW * 32) {
     const int L = __ldg(a.lens + b);
-    if (L > a.c.max_pages * a.c.page_size && hg == 0) *a.c.err = FA_ERR_PAGE;
+    if (L > a.c.max_pages * a.c.page_size && hg == 0) report_page(a.c.err);
     if (L < 0 || seq_keys(a, b) > 0) continue;
     for (int h = head0; h < head0 + nh; ++h) {
       const long long at = (long long)b * a.H + h;
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     const int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
     const int page = __ldg(a.c.table + (long long)b * a.c.max_pages + p);
     if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + (j - p * a.c.page_size);
-    *a.c.err = FA_ERR_PAGE;
+    report_page(a.c.err);
     return -1;
   };
   int found = -1, found_at = -1000;  // the lookup's rows, and the warp's turn that it starts with

@@ -182,6 +182,9 @@ struct Cache {
   int page_shift;
 };
 
+// FA_ERR_PAGE, unless something is recorded already: outputs are defined after it, and not after a timeout.
+__device__ __forceinline__ void report_page(int* err) { atomicCAS(err, FA_OK, FA_ERR_PAGE); }
+
 // Row (page * page_size + offset) of position j of sequence b, or -1 (and FA_ERR_PAGE recorded)
 __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
   if (b < c.B && j < c.max_pages * c.page_size) {
@@ -189,7 +192,7 @@ __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
     const int page = __ldg(c.table + (long long)b * c.max_pages + p);
     if (page >= 0 && page < c.num_pages) return (long long)page * c.page_size + (j - p * c.page_size);
   }
-  *c.err = FA_ERR_PAGE;
+  report_page(c.err);
   return -1;
 }
 

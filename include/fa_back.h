@@ -262,8 +262,8 @@ fa_status fa_back_strided(const float* q, const void* k, int k_type, const void*
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Sticky device-side status of the kernels enqueued so far on the current device (FA_OK,
- * FA_ERR_TIMEOUT or, from the operators of fa_paged.h, FA_ERR_PAGE; the last recorded where there
- * were several).  Synchronises the device, then clears the word. */
+ * FA_ERR_TIMEOUT or, from the operators of fa_paged.h, FA_ERR_PAGE; FA_ERR_TIMEOUT where there were
+ * both, in either order).  Synchronises the device, then clears the word. */
 fa_status fa_back_get_error(void);
 
 /* Human-readable name of a status code. */
