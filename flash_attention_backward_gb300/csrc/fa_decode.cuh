@@ -489,7 +489,7 @@ __device__ __forceinline__ void act_store(void* p, int act, long long i, float x
 
 // Keys of sequence b: its length, 0 for padding, at most the table's capacity
 __device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
-  const int L = __ldg(a.lens + b);
+  const int L = a.lens[b];
   return min(max(L, 0), a.c.max_pages * a.c.page_size);
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   }
   // sequences without keys: their rows, by the CTA whose turn it is
   for (int b = r + a.nitems * threadIdx.x; b < B; b += a.nitems * NW * 32) {
-    const int L = __ldg(a.lens + b);
+    const int L = a.lens[b];
     if (L > a.c.max_pages * a.c.page_size && hg == 0) report_page(a.c.err);
     if (L < 0 || seq_keys(a, b) > 0) continue;
     for (int h = head0; h < head0 + nh; ++h) {
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   auto lookup = [&](int j) {  // row of the pool of key j, -1 where there is none
     if (j >= j1) return -1;
     const int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
-    const int page = __ldg(a.c.table + (long long)b * a.c.max_pages + p);
+    const int page = a.c.table[(long long)b * a.c.max_pages + p];
     if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + (j - p * a.c.page_size);
     report_page(a.c.err);
     return -1;

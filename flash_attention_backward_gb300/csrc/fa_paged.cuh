@@ -189,7 +189,7 @@ __device__ __forceinline__ void report_page(int* err) { atomicCAS(err, FA_OK, FA
 __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
   if (b < c.B && j < c.max_pages * c.page_size) {
     const int p = (int)((uint64_t)j * c.page_mul >> c.page_shift);
-    const int page = __ldg(c.table + (long long)b * c.max_pages + p);
+    const int page = c.table[(long long)b * c.max_pages + p];
     if (page >= 0 && page < c.num_pages) return (long long)page * c.page_size + (j - p * c.page_size);
   }
   report_page(c.err);
@@ -199,7 +199,9 @@ __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
 // ---- launches that overlap.  A kernel launched by launch_next() may start while the one before it on the
 // stream still runs its last CTAs; it begins with after_last(), which waits for all of that one's work.
 // lets_next() says that the next one's CTAs may take what is free from here on.  (Without such a launch
-// before or behind them both do nothing.)
+// before or behind them both do nothing.)  What that one writes (lengths, positions, page tables) is not
+// read-only while this kernel runs: it is read by ordinary loads, which after_last() orders, and not by the
+// non-coherent ones of __ldg and const __restrict__.
 __device__ __forceinline__ void after_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void lets_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

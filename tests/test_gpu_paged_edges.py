@@ -34,3 +34,38 @@ def test_a_page_report_does_not_hide_a_timeout(fb):
             c()
         assert fb.STATUS[fb.fa_back_get_error()] == want
         assert fb.fa_back_get_error() == 0
+
+
+def test_lengths_and_pages_written_just_before(fb):
+    """Each call sees the lengths, positions and page numbers that the kernel before it on the stream has written."""
+    p = R.Paged(9, [3000, 40, 900], 2, 64, 64, Q8, F16, 16)
+    q, cache, _ = check_decode(fb, p, 4)
+    full, table = cuda(np.array(p.lens, np.int32)), cache.page_table.clone()
+    steps = [full - 30 * i for i in range(1, 30)]
+    kw = dict(scale=0.125)
+    want = []
+    for n in steps:
+        cache.page_table.copy_(table if len(want) % 2 else table.flip(1))
+        n = n.clamp(min=1)
+        torch.cuda.synchronize()
+        want.append(fb.paged_decode(q, cache, n, **kw))
+        torch.cuda.synchronize()
+    lens, got = torch.zeros_like(full), []
+    pos, seq = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    rows = torch.cat([fb.cache_read(cache, seq, seq + j, dtype=torch.uint8)["k"] for j in range(40)])
+    for _ in range(5):
+        for i, n in enumerate(steps):
+            torch.clamp(n, min=1, out=lens)
+            cache.page_table.copy_(table if i % 2 else table.flip(1))
+            got.append(fb.paged_decode(q, cache, lens, **kw))
+    for i, g in enumerate(got):
+        w = want[i % len(steps)]
+        for n in ("O", "lse"):  # bits: with the flipped table short sequences' pages have rows of NaN
+            assert torch.equal(g[n].view(torch.int32), w[n].view(torch.int32))
+            assert i % len(steps) % 2 == 0 or bool(torch.isfinite(g[n]).all())
+    cache.page_table.copy_(table if (len(steps) - 1) % 2 else table.flip(1))
+    for j in range(40):  # reads that follow a position counted up on the device
+        g = fb.cache_read(cache, seq, pos, dtype=torch.uint8)["k"]
+        pos.add_(1)
+        assert torch.equal(g[0], rows[j])
+    fb.fa_back_get_error()  # (the flipped table's unused pages)

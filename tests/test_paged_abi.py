@@ -262,3 +262,14 @@ def test_wrappers_refuse_what_the_kernels_do_not_take():
     raises(fb.cache_append, x, x, c, i2, i2)
     raises(fb.paged_decode, q, c, i2, scale=1.0)
     raises(fb.qk_norm_rope, q, x, i2)
+
+
+def test_kernels_that_start_early_read_with_ordinary_loads():
+    """A kernel that may begin before the one before it on the stream has ended reads what that one writes:
+    non-coherent loads are for data that nobody writes while the kernel runs."""
+    folder = os.path.join(ROOT, "flash_attention_backward_gb300", "csrc")
+    files = [f for f in sorted(os.listdir(folder)) if re.match(r"fa_(paged|decode|cache|norm_rope)", f)]
+    assert {"fa_paged.cuh", "fa_decode.cuh", "fa_cache.cu", "fa_norm_rope.cuh"} <= set(files)
+    for f in files:
+        code = re.sub(r"//.*", "", open(os.path.join(folder, f)).read())
+        assert not re.search(r"__ldg|ld\.global\.nc|__restrict__|__ldcv?a?\b", code), f
