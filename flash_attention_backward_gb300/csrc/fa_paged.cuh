@@ -89,7 +89,8 @@ struct Rope {
 
 // A warp that holds heads of one token: D / 8 lanes a head, so 256 / D heads side by side.  Factors of a
 // lane's eight elements e0 .. e0+7: y[i] = x[i] c[i] + partner[i] s[i], the sign of the pair's first /
-// second member in s.  The angle is pos * freq modulo 2^64 in units of 2^-64 turns: the wrap of the
+// second member in s, for its first n elements; the others are not rotated and not touched (turned by nothing,
+// an infinity would become NaN and a NaN would enter its partner).  The angle is pos * freq modulo 2^64 in units of 2^-64 turns: the wrap of the
 // integer product is the reduction modulo one turn, with no rounding, so the error is that of the 32
 // bits kept (1.5e-9 rad) and of sincospi, at every position.  The token's n_rot / 2 <= D / 2 angles are
 // shared out over the lanes, D / 64 neighbouring ones each, and handed round by shuffles.
@@ -97,12 +98,14 @@ template <int D>
 struct Turn8 {
   float c[8], s[8];
   int src;  // partner lane (FA_ROPE_HALVES)
+  int n;    // the lane's elements that are rotated, its first ones (FA_ROPE_HALVES: all or none)
 
   // All lanes of the warp take part; pos is the same in all.  sign +1: rotate; -1: back (the transpose).
   __device__ __forceinline__ void set(const Rope& r, int pos, int e0, float sign) {
     constexpr int P = D / 64;
     const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
     src = lane;
+    n = min(max(r.n_rot - e0, 0), 8);
     if (half == 0) return;
     float cs[P], sn[P];
 #pragma unroll
@@ -123,16 +126,16 @@ struct Turn8 {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float ci = __shfl_sync(kFull, cs[i % P], (p0 + i) / P), si = __shfl_sync(kFull, sn[i % P], (p0 + i) / P);
-        c[i] = in ? ci : 1.f;
-        s[i] = !in ? 0.f : second ? si : -si;
+        c[i] = ci;
+        s[i] = second ? si : -si;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int p = (e0 >> 1) + i;
         const float ci = __shfl_sync(kFull, cs[i % P], p / P), si = __shfl_sync(kFull, sn[i % P], p / P);
-        c[2 * i] = c[2 * i + 1] = p < half ? ci : 1.f;
-        s[2 * i] = p < half ? -si : 0.f, s[2 * i + 1] = -s[2 * i];
+        c[2 * i] = c[2 * i + 1] = ci;
+        s[2 * i] = -si, s[2 * i + 1] = si;
       }
     }
   }
@@ -147,7 +150,7 @@ struct Turn8 {
       for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(p[i], s[i], x[i] * c[i]);
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? fmaf(p[i], s[i], x[i] * c[i]) : x[i];
   }
 };
 

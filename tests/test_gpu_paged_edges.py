@@ -69,3 +69,61 @@ def test_lengths_and_pages_written_just_before(fb):
         pos.add_(1)
         assert torch.equal(g[0], rows[j])
     fb.fa_back_get_error()  # (the flipped table's unused pages)
+
+
+ROTATIONS = [(64, 0, True), (64, 0, False), (64, 16, True), (64, 64, True), (128, 32, True), (128, 34, False), (128, 128, False),
+             (256, 96, True), (256, 2, False), (256, 256, True)]
+
+
+def not_finite(N, H, D, seed):
+    """Ordinary heads with one infinity or NaN each, every component in turn."""
+    x = np.random.default_rng(seed).standard_normal((N, H, D)).astype(np.float32)
+    n = np.arange(N * H)
+    x.reshape(N * H, D)[n, n % D] = np.array([np.inf, np.nan, -np.inf], np.float32)[n // D % 3]
+    return x
+
+
+def turned(x, pos, n_rot, halves, sign=1.0):
+    """The definition: (a cos - b sin, a sin + b cos) for the pairs, nothing for the rest."""
+    y = x.astype(np.float64)
+    if n_rot:
+        with np.errstate(invalid="ignore"):
+            y = R.rotate(y, pos, n_rot, 10000.0, halves, sign)
+    return y
+
+
+def same_kinds(got, ref, tol, what):
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), (what, int(np.isnan(got).sum()), int(np.isnan(ref).sum()))
+    inf = np.isinf(ref)
+    assert np.array_equal(got[inf], ref[inf]) and np.array_equal(np.isinf(got), inf), what
+    fin = np.isfinite(ref)
+    assert np.abs(got[fin] - ref[fin]).max() <= tol, what
+
+
+@pytest.mark.parametrize("D, n_rot, halves", ROTATIONS)
+def test_a_value_that_is_not_finite_touches_its_pair_alone(fb, D, n_rot, halves):
+    """Rotation without a norm, its gradient and an append to F32 and F16 rows: an infinity or a NaN enters the two
+    components of its pair, as in the definition, and an unrotated one is kept as it is."""
+    H, Hkv = 6, 2
+    N = 3 * D // Hkv  # every component with every kind, in the keys too
+    q, k = not_finite(N, H, D, D), not_finite(N, Hkv, D, D + 1)
+    # positions whose angles are off the axes: cos and sin are not 0 (inf * 0)
+    pos = np.random.default_rng(n_rot).integers(1, 5000, N).astype(np.int32)
+    rope = fb.rope_frequencies(n_rot, 10000.0) if n_rot else None
+    kw = dict(rope=rope, rope_style=int(halves))
+    tol = 20 * U * 12  # 20 u of the pair's magnitude, which is below 12 for these normals
+    got = fb.qk_norm_rope(cuda(q), cuda(k), cuda(pos), **kw)
+    back = fb.qk_norm_rope_backward(cuda(q), cuda(k), cuda(q), cuda(k), cuda(pos), **kw)
+    for n, x in (("q", q), ("k", k)):
+        same_kinds(got[n].cpu().numpy().astype(np.float64), turned(x, pos, n_rot, halves), tol, n)
+        same_kinds(back["d" + n].cpu().numpy().astype(np.float64), turned(x, pos, n_rot, halves, -1.0), tol, "d" + n)
+    for ty in (F32, F16):
+        cache, _ = empty_cache(fb, 1, -(-5000 // 64), 64, Hkv, D, D, ty, ty)
+        at = np.random.default_rng(1).permutation(np.arange(1, 5000))[:N].astype(np.int32)
+        seq = cuda(np.zeros(N, np.int32))
+        fb.cache_append(cuda(k), cuda(k), cache, seq, cuda(at), **kw)
+        rows = fb.cache_read(cache, seq, cuda(at))
+        half = 0.0 if ty == F32 else 2.0 ** -11 * 12
+        same_kinds(rows["k"].cpu().numpy().astype(np.float64), turned(k, at, n_rot, halves), tol + half, "rows k")
+        same_kinds(rows["v"].cpu().numpy().astype(np.float64), k.astype(np.float64), half, "rows v")
+    assert fb.fa_back_get_error() == 0
