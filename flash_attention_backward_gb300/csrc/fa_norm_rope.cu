@@ -166,6 +166,7 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
   int ck = Hkv ? (int)std::min<long long>(std::max(1LL, (long long)all * Hkv / (H + Hkv)), std::max(1LL, (ik + 7) / 8)) : 0;
   const int cq = (int)std::min<long long>(all - ck, std::max(1LL, (iq + 7) / 8));
   a.ctas_q = cq;
+  a.wait_ns = fab_take_wait_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (k_back.smem > 48 * 1024 && !allow_smem(reinterpret_cast<const void*>(k_back.fn), k_back.smem, k_back.ready)) return FA_ERR_CUDA;
   if (launch_next(k_back.fn, dim3(cq + ck), dim3(kBackWarps * 32), k_back.smem, s, a) != cudaSuccess) return FA_ERR_CUDA;

@@ -42,12 +42,13 @@ struct NormArgs {
   bool vec;            // both start every head of x on 16 bytes (or have none)
   float* part;         // backward: [CTA][D] sums of dw
   int* err;
+  uint64_t wait_ns;    // backward: a wait for a copy gives up after this long (0, the failure-detection hook: at once)
 };
 
 // Rows that a lane group has under way at a time: 32 or 64 bytes a lane of x (and as much of gy).
 template <typename T>
 constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
-constexpr uint64_t kCopyLimitNs = 2000000000ull;  // a wait for a copy gives up after this long
+constexpr uint64_t kCopyDrainNs = 2000000000ull;  // after a wait that ran out: for the copies in flight to land
 
 // A lane's four rotation pairs: components [ea, ea + 4) and [eb, eb + 4) of the head.
 //   FA_ROPE_HALVES  pair i is (x[ea + i], x[eb + i]).  The rotated components are pairs 0 .. n_rot / 2 - 1
@@ -360,12 +361,12 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
       ln.turn(a.rope, pos, -1.f);
       token = n, pos = pos_of(n + 1);  // the next token's, in time
     }
-    const bool came = fab::mbar_wait_bounded(&s_bar[warp][slot], phase, kCopyLimitNs);
-    if (!__all_sync(kFull, came)) {  // wait once more for the other slots' copies, then give up
+    const bool came = a.wait_ns > 0 && fab::mbar_wait_bounded(&s_bar[warp][slot], phase, a.wait_ns);
+    if (!__all_sync(kFull, came)) {  // let the copies in flight land, then give up
       if (lane == 0) {
         atomicExch(a.err, FA_ERR_TIMEOUT);
         for (unsigned k = item; k < fetched; ++k) {
-          fab::mbar_wait_bounded(&s_bar[warp][slot], phase, kCopyLimitNs);
+          fab::mbar_wait_bounded(&s_bar[warp][slot], phase, kCopyDrainNs);
           if (++slot == S) slot = 0, phase ^= 1;
         }
       }

@@ -87,6 +87,8 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, const fa_qk_
  * wanted).  N = 0 writes zeros to dwq and dwk.  Alignment: as for the forward; gq, gk, dq, dk 16
  * bytes, workspace 256 bytes.  The kernel's waits for its own copies are bounded: one that runs out
  * is reported as FA_ERR_TIMEOUT by fa_back_get_error() and leaves the outputs undefined.
+ * fa_back_test_wait_limit() applies to the next call here too; a limit of 0 counts every wait as run
+ * out (heads of x that do not start on 16 bytes are loaded without copies to wait for).
  */
 size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv, int D);
 fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, int y_type, const void* q, const void* k, int x_type,

@@ -127,3 +127,22 @@ def test_a_value_that_is_not_finite_touches_its_pair_alone(fb, D, n_rot, halves)
         same_kinds(rows["k"].cpu().numpy().astype(np.float64), turned(k, at, n_rot, halves), tol + half, "rows k")
         same_kinds(rows["v"].cpu().numpy().astype(np.float64), k.astype(np.float64), half, "rows v")
     assert fb.fa_back_get_error() == 0
+
+
+@pytest.mark.parametrize("N, H, Hkv, D, act", [(3000, 6, 2, 128, "bf16"), (500, 3, 1, 256, "f32"), (2, 1, 1, 64, "f32")])
+def test_gradient_gives_up_on_a_wait(fb, N, H, Hkv, D, act):
+    """With a wait limit of zero the gradient's kernel records a timeout, drains its copies and returns; the next
+    call is right again, bit for bit."""
+    rng = np.random.default_rng(N)
+    (q, _), (k, _), (gq, _), (gk, _) = (act_array(rng, (N, h, D), act) for h in (H, Hkv, H, Hkv))
+    w, pos = torch.rand(D, device="cuda") + 0.5, torch.arange(N, dtype=torch.int32, device="cuda")
+    kw = dict(wq=w, wk=w, rope=fb.rope_frequencies(D))
+    want = fb.qk_norm_rope_backward(gq, gk, q, k, pos, **kw)
+    assert fb.fa_back_get_error() == 0
+    assert fb.fa_back_test_wait_limit(0) == 0
+    fb.qk_norm_rope_backward(gq, gk, q, k, pos, **kw)
+    assert fb.STATUS[fb.fa_back_get_error()] == "FA_ERR_TIMEOUT"
+    again = fb.qk_norm_rope_backward(gq, gk, q, k, pos, **kw)
+    assert fb.fa_back_get_error() == 0
+    for n in want:
+        assert torch.equal(again[n], want[n]), n
