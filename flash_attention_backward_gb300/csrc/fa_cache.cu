@@ -221,7 +221,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
     if (cell < 0) continue;
     uint8_t* row = (IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h0 + grp) * rb;
     Turn8<D> turn;
-    if (turns) turn.set(a.rope, pos, e0, 1.f);
+    if (turns) turn.set(a.rope, pos, e0);
 #pragma unroll 1
     for (;;) {
       float x[8];

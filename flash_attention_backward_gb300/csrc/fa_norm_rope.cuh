@@ -113,9 +113,7 @@ struct Lane {
       unpack_eight(o, w);
     }
   }
-  // The factors at a position; sign -1 turns back (the transpose).  The angle is pos * freq modulo 2^64
-  // in units of 2^-64 turns: the wrap of the integer product is the reduction modulo one turn, with no
-  // rounding, so the error is that of the 32 bits kept (1.5e-9 rad) and of sincospi, at every position.
+  // The factors at a position (sin_cos_turn); sign -1 turns back (the transpose).
   // The token's D / 2 pairs are shared out over the warp's lanes, D / 64 neighbouring ones each.
   __device__ __forceinline__ void turn(const Rope& r, int pos, float sign) {
     constexpr int P = D / 64;
@@ -125,8 +123,7 @@ struct Lane {
     for (int i = 0; i < P; ++i) {
       cs[i] = 1.f, sn[i] = 0.f;
       if (lane * P + i < half) {
-        const uint64_t a = (uint64_t)(int64_t)pos * r.freqs[lane * P + i];
-        sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+        sin_cos_turn(r.freqs[lane * P + i], pos, &sn[i], &cs[i]);
         sn[i] *= sign;
       }
     }

@@ -87,21 +87,31 @@ struct Rope {
   int n_rot, style;
 };
 
+// sin and cos of pos * freq, modulo 2^64 in units of 2^-64 turns: the wrap of the integer product is the
+// reduction modulo one turn, with no rounding.  Of the 32 bits that are kept (1.5e-9 rad) f32 holds 24: the
+// others, below 4e-7 rad, are added to first order, so that what is left is the error of sincospif, of one
+// rounding and those 1.5e-9 rad, at every position.  (All 32 at once in f32 would be up to 9.4e-8 rad off.)
+__device__ __forceinline__ void sin_cos_turn(uint64_t freq, int pos, float* sn, float* cs) {
+  const int a = (int)(((uint64_t)(int64_t)pos * freq) >> 32);
+  float s, c;
+  sincospif((float)(a & ~0xff) * 0x1p-31f, &s, &c);
+  const float rest = (float)(a & 0xff) * (float)(3.14159265358979323846 * 0x1p-31);
+  *sn = fmaf(c, rest, s), *cs = fmaf(-s, rest, c);
+}
+
 // A warp that holds heads of one token: D / 8 lanes a head, so 256 / D heads side by side.  Factors of a
 // lane's eight elements e0 .. e0+7: y[i] = x[i] c[i] + partner[i] s[i], the sign of the pair's first /
 // second member in s, for its first n elements; the others are not rotated and not touched (turned by nothing,
-// an infinity would become NaN and a NaN would enter its partner).  The angle is pos * freq modulo 2^64 in units of 2^-64 turns: the wrap of the
-// integer product is the reduction modulo one turn, with no rounding, so the error is that of the 32
-// bits kept (1.5e-9 rad) and of sincospi, at every position.  The token's n_rot / 2 <= D / 2 angles are
-// shared out over the lanes, D / 64 neighbouring ones each, and handed round by shuffles.
+// an infinity would become NaN and a NaN would enter its partner).  The token's n_rot / 2 <= D / 2 angles
+// are shared out over the lanes, D / 64 neighbouring ones each, and handed round by shuffles.
 template <int D>
 struct Turn8 {
   float c[8], s[8];
   int src;  // partner lane (FA_ROPE_HALVES)
   int n;    // the lane's elements that are rotated, its first ones (FA_ROPE_HALVES: all or none)
 
-  // All lanes of the warp take part; pos is the same in all.  sign +1: rotate; -1: back (the transpose).
-  __device__ __forceinline__ void set(const Rope& r, int pos, int e0, float sign) {
+  // All lanes of the warp take part; pos is the same in all.
+  __device__ __forceinline__ void set(const Rope& r, int pos, int e0) {
     constexpr int P = D / 64;
     const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
     src = lane;
@@ -112,11 +122,7 @@ struct Turn8 {
     for (int i = 0; i < P; ++i) {
       cs[i] = 1.f, sn[i] = 0.f;
       const int p = lane * P + i;
-      if (p < half) {
-        const uint64_t a = (uint64_t)(int64_t)pos * r.freqs[p];
-        sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-        sn[i] *= sign;
-      }
+      if (p < half) sin_cos_turn(r.freqs[p], pos, &sn[i], &cs[i]);
     }
     const bool in = e0 < r.n_rot;
     if (r.style == FA_ROPE_HALVES) {  // n_rot % 16 == 0: a lane lies in one half

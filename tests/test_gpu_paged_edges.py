@@ -146,3 +146,34 @@ def test_gradient_gives_up_on_a_wait(fb, N, H, Hkv, D, act):
     assert fb.fa_back_get_error() == 0
     for n in want:
         assert torch.equal(again[n], want[n]), n
+
+
+def test_rotation_angles_to_32_bits(fb):
+    """cos and sin themselves (the rotation of (1, 0)), at any frequency and position: within 1.5 units of the result
+    (one of sincospi's, half of the rounding behind it; a unit is at most 2^-23 of the value) and the 1.5e-9 rad
+    that an angle of 32 bits is off.  Both ways, and on the way into a cache."""
+    rng = np.random.default_rng(41)
+    N, D = 4000, 64
+    freq = rng.integers(-2 ** 63, 2 ** 63, 32)
+    rope = cuda(freq)
+    x = np.zeros((N, 1, D), np.float32)
+    for halves in (True, False):
+        first, second = (np.arange(32), np.arange(32) + 32) if halves else (2 * np.arange(32), 2 * np.arange(32) + 1)
+        x[:] = 0.0
+        x[:, 0, first] = 1.0
+
+        def check(got, pos, sign, what):
+            turns = np.array([[(int(p) * int(f)) % 2 ** 64 for f in freq] for p in pos], dtype=object)
+            t = (turns / 2 ** 64).astype(np.float64)  # (2^-53 turns: nothing here)
+            for at, ref in ((first, np.cos(2 * np.pi * t)), (second, sign * np.sin(2 * np.pi * t))):
+                off = np.abs(got[:, 0, at] - ref)
+                assert (off <= 1.5 * 2.0 ** -23 * np.abs(ref) + 1.5e-9).all(), (what, off.max())
+
+        pos = rng.integers(-2 ** 31, 2 ** 31, N).astype(np.int32)
+        kw = dict(rope=rope, rope_style=int(halves))
+        check(fb.qk_norm_rope(cuda(x), None, cuda(pos), **kw)["q"].double().cpu().numpy(), pos, 1.0, "forward")
+        check(fb.qk_norm_rope_backward(cuda(x), None, cuda(x), None, cuda(pos), **kw)["dq"].double().cpu().numpy(), pos, -1.0, "back")
+        cache, _ = empty_cache(fb, 1, -(-N // 64), 64, 1, D, D, F32, F32)
+        at, seq = np.arange(N, dtype=np.int32), cuda(np.zeros(N, np.int32))
+        fb.cache_append(cuda(x), cuda(x), cache, seq, cuda(at), **kw)
+        check(fb.cache_read(cache, seq, cuda(at))["k"].double().cpu().numpy(), at, 1.0, "append")
