@@ -10,7 +10,7 @@
 // Precision.  Codes are exact in binary16 (q8_0, q4_0 keys) and in bf16 (values), and block scales
 // are applied in f32, to the product (keys) or to the weight (values).  q is split into two binary16
 // parts (22 bits of the head's largest magnitude, after an exact power-of-two scale), a weight times
-// block scale into two bf16 parts (16 bits, with f32's range), a weight alone into two binary16
+// block scale into three bf16 parts (all 24 bits, with f32's range), a weight alone into two binary16
 // parts (22 bits), and for f32 rows all operands into two tf32 parts (three products).
 //
 // Bounds, on a GB300 (6787 GB/s measured copy rate).  The cache rows are read once; binary16 and f32 rows
@@ -313,14 +313,20 @@ __device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (
   }
 }
 
-// weights times block scales as two bf16 parts
+// Weights times block scales as three bf16 parts of eight bits each, which hold all 24 of an f32: the parts
+// are cut off, so the high halves of two values and of what they leave are pairs already.
 struct Scaled {
-  uint32_t h0, h1, l0, l1;
+  uint32_t h0, h1, m0, m1, l0, l1;
+  static __device__ __forceinline__ uint32_t take(float& x, float& y) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    x -= __uint_as_float(a & 0xffff0000u), y -= __uint_as_float(b & 0xffff0000u);
+    return __byte_perm(a, b, 0x7632);
+  }
   __device__ __forceinline__ Scaled(const float (&p)[4], float d0, float d1, float d2, float d3) {
-    const float x0 = p[0] * d0, x1 = p[1] * d1, x2 = p[2] * d2, x3 = p[3] * d3;
-    h0 = pack_b2(x0, x1), h1 = pack_b2(x2, x3);
-    l0 = pack_b2(x0 - __uint_as_float(h0 << 16), x1 - __uint_as_float(h0 & 0xffff0000u));
-    l1 = pack_b2(x2 - __uint_as_float(h1 << 16), x3 - __uint_as_float(h1 & 0xffff0000u));
+    float x0 = p[0] * d0, x1 = p[1] * d1, x2 = p[2] * d2, x3 = p[3] * d3;
+    h0 = take(x0, x1), h1 = take(x2, x3);
+    m0 = take(x0, x1), m1 = take(x2, x3);
+    l0 = take(x0, x1), l1 = take(x2, x3);
   }
 };
 
@@ -351,18 +357,22 @@ __device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&
       const Scaled b(p, d[0], d[1], d[2], d[3]);
       const uint32_t a0 = q8_b2<0>(w[0], w[1]), a1 = q8_b2<1>(w[0], w[1]), a2 = q8_b2<0>(w[2], w[3]), a3 = q8_b2<1>(w[2], w[3]);
       mma_bf16(o[4 * pr], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[4 * pr], a0, a1, a2, a3, b.m0, b.m1);
       mma_bf16(o[4 * pr], a0, a1, a2, a3, b.l0, b.l1);
       const uint32_t c0 = q8_b2<2>(w[0], w[1]), c1 = q8_b2<3>(w[0], w[1]), c2 = q8_b2<2>(w[2], w[3]), c3 = q8_b2<3>(w[2], w[3]);
       mma_bf16(o[4 * pr + 1], c0, c1, c2, c3, b.h0, b.h1);
+      mma_bf16(o[4 * pr + 1], c0, c1, c2, c3, b.m0, b.m1);
       mma_bf16(o[4 * pr + 1], c0, c1, c2, c3, b.l0, b.l1);
     }
     {
       const Scaled b(p, e[0], e[1], e[2], e[3]);
       const uint32_t a0 = q8_b2<0>(x[0], x[1]), a1 = q8_b2<1>(x[0], x[1]), a2 = q8_b2<0>(x[2], x[3]), a3 = q8_b2<1>(x[2], x[3]);
       mma_bf16(o[4 * pr + 2], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[4 * pr + 2], a0, a1, a2, a3, b.m0, b.m1);
       mma_bf16(o[4 * pr + 2], a0, a1, a2, a3, b.l0, b.l1);
       const uint32_t c0 = q8_b2<2>(x[0], x[1]), c1 = q8_b2<3>(x[0], x[1]), c2 = q8_b2<2>(x[2], x[3]), c3 = q8_b2<3>(x[2], x[3]);
       mma_bf16(o[4 * pr + 3], c0, c1, c2, c3, b.h0, b.h1);
+      mma_bf16(o[4 * pr + 3], c0, c1, c2, c3, b.m0, b.m1);
       mma_bf16(o[4 * pr + 3], c0, c1, c2, c3, b.l0, b.l1);
     }
   }
@@ -392,11 +402,13 @@ __device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&
     {
       const uint32_t a0 = q4_b2<0>(u), a1 = q4_b2<4>(u), a2 = q4_b2<0>(v), a3 = q4_b2<4>(v);
       mma_bf16(o[2 * blk], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[2 * blk], a0, a1, a2, a3, b.m0, b.m1);
       mma_bf16(o[2 * blk], a0, a1, a2, a3, b.l0, b.l1);
     }
     {
       const uint32_t a0 = q4_b2<8>(u), a1 = q4_b2<12>(u), a2 = q4_b2<8>(v), a3 = q4_b2<12>(v);
       mma_bf16(o[2 * blk + 1], a0, a1, a2, a3, b.h0, b.h1);
+      mma_bf16(o[2 * blk + 1], a0, a1, a2, a3, b.m0, b.m1);
       mma_bf16(o[2 * blk + 1], a0, a1, a2, a3, b.l0, b.l1);
     }
   }

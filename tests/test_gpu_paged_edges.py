@@ -177,3 +177,30 @@ def test_rotation_angles_to_32_bits(fb):
         at, seq = np.arange(N, dtype=np.int32), cuda(np.zeros(N, np.int32))
         fb.cache_append(cuda(x), cuda(x), cache, seq, cuda(at), **kw)
         check(fb.cache_read(cache, seq, cuda(at))["k"].double().cpu().numpy(), at, 1.0, "append")
+
+
+@pytest.mark.parametrize("vt", [Q8, Q4])
+def test_weights_of_quantised_values_keep_their_bits(fb, vt):
+    """Two keys, of which one has values: O is that key's weight, 1 / (1 + exp(-a)), times whole numbers.
+
+    Per output, in u = 2^-24 of it: the score a is exact (11 bits, a key of one 1), its product with log2 e two
+    roundings, 1.5 a <= 1.5; either exponential 4 (2^-22), which enter by 1 - weight < 0.74: 6; the parts of
+    the weight are exact, their three products are summed with up to 2 lost each: 6; the sum of weights, the
+    factors of the join, the division and its product: 6.  Together under 24.  (Two bf16 parts alone: up to 128.)"""
+    B, H, D = 64, 8, 64
+    rng = np.random.default_rng(51)
+    p = R.Paged(51, [2] * B, 1, D, D, F16, vt, 16)
+    a = rng.integers(1, 1024, (B, H)) / 1024.0 * rng.choice([-1.0, 1.0], (B, H))
+    q = np.zeros((B, H, D), np.float32)
+    q[..., 0] = a
+    k, v = np.zeros((B, 2, D), np.float16), np.zeros((B, 2, 1, D), np.float32)
+    k[:, 0, 0] = 1.0
+    v[:, 0, 0] = rng.integers(-126, 127, (B, D)) if vt == Q8 else rng.integers(-7, 8, (B, D))
+    v[:, 0, 0, ::32] = 127 if vt == Q8 else -8  # the block scale is 1
+    p.k[p.table[:, 0], :2, 0] = k.view(np.uint8)
+    p.v[p.table[:, 0], :2] = R.synth.quantize_rows(v, vt)
+    got = fb.paged_decode(cuda(q), p.on_gpu(fb, torch), cuda(np.array(p.lens, np.int32)), scale=1.0)
+    ref = (1.0 / (1.0 + np.exp(-a)))[..., None] * v[:, 0].astype(np.float64)
+    off = np.abs(got["O"].double().cpu().numpy() - ref)
+    assert (off <= 24 * U * np.abs(ref)).all(), (off / np.maximum(np.abs(ref), 1e-30)).max() / U
+    assert fb.fa_back_get_error() == 0
