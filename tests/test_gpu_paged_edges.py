@@ -204,3 +204,33 @@ def test_weights_of_quantised_values_keep_their_bits(fb, vt):
     off = np.abs(got["O"].double().cpu().numpy() - ref)
     assert (off <= 24 * U * np.abs(ref)).all(), (off / np.maximum(np.abs(ref), 1e-30)).max() / U
     assert fb.fa_back_get_error() == 0
+
+
+@pytest.mark.parametrize("ty", [F32, F16, Q8, Q4])
+def test_f32_outputs_of_long_sequences(fb, ty):
+    """A batch that fills the card with whole sequences: each warp sums 188 tiles of 16 keys.
+
+    The 2-norm of the error over that of O, in u = 2^-24.  O is a sum of terms of random sign, so what is off
+    by d in each term is off by d in O: score (22 bits of q, 4 rounded steps), exponential and parts of a weight,
+    each at random, below 6 in the root mean square; products and sum of a tile, cut off up to 3 times, 6 of a sum
+    that is 1 / sqrt(750) of the whole: nothing; 188 rounded additions of at most 1 at random, whose sizes grow to
+    the final one's: sqrt(188 / 3 / 2) = 6; the sum of weights 188 of one sign, at random: sqrt(188 / 3) = 8.
+    Together 12; 32 are allowed.  (In one chain through the tensor core, two or six cuts a tile of one unit on
+    average, all towards zero: 75 to 375.)"""
+    B, L, H, D, page = 80, 12000, 64, 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(61 + ty)
+    table = torch.arange(B * 188, dtype=torch.int32, device="cuda").view(B, 188)
+    pools = [torch.zeros(B * 188, page, 1, R.synth.row_bytes(ty, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache = fb.PagedCache(pools[0], ty, pools[1], ty, table, D=D, Dv=D)
+    q = torch.randn(B, H, D, generator=gen, device="cuda")
+    pos, ref = torch.arange(L, dtype=torch.int32, device="cuda"), torch.empty(B, H, D, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        x = torch.randn(2, L, 1, D, generator=gen, device="cuda")
+        fb.cache_append(x[0], x[1], cache, torch.full_like(pos, b), pos)
+        raw = fb.cache_read(cache, torch.full_like(pos, b), pos, dtype=torch.uint8)
+        k, v = (cuda(R.oracle.dequant(raw[n][:, 0].cpu().numpy(), ty, D).reshape(L, D)).double() for n in ("k", "v"))
+        ref[b] = torch.softmax(q[b].double() @ k.T * D ** -0.5, -1) @ v
+    got = fb.paged_decode(q, cache, torch.full((B,), L, dtype=torch.int32, device="cuda"), scale=D ** -0.5)
+    off = float((got["O"].double() - ref).norm() / ref.norm())
+    assert off <= 32 * U, off / U
+    assert fb.fa_back_get_error() == 0
