@@ -252,9 +252,11 @@ __device__ __forceinline__ void scores_q4(float (&s)[4], uint32_t rows, uint32_t
   }
 }
 
+// An f32 as two tf32 parts, of 11 bits each; the second one is rounded to them (the tensor core cuts off the
+// bits below, which are the last two of 13 here; an infinity or NaN is in the first part already)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
   hi = x & 0xffffe000u;
-  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u;
 }
 
 template <int D>

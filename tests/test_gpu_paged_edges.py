@@ -234,3 +234,21 @@ def test_f32_outputs_of_long_sequences(fb, ty):
     off = float((got["O"].double() - ref).norm() / ref.norm())
     assert off <= 32 * U, off / U
     assert fb.fa_back_get_error() == 0
+
+
+def test_f32_values_are_rounded_to_their_parts(fb):
+    """One key: O is its f32 value p v / p, with v and the weight p (2^7 but for the rounding of its exponent) each in
+    parts of 11 and 11 bits.  In u: rounded, v and p are off by at most 4 (two of 13 lower bits go; a granule is 2) and
+    on average by nothing; the product of the second parts, 2^-12 of 2^-12, is left out: 1; the sum of the three
+    products is cut twice, the first time beside a sum of 2^-11 (nothing), the second by less than 2, 0.7 on average
+    over a binade; division and its product 2.  Together 13 at most, and in the mean of 512 weights and 131072 values
+    0.7 (+ 0.1 left out) with a deviation of 1 / sqrt(512) + 4 / sqrt(131072) = 0.06: under 1.2.  (Parts that are cut
+    off: 1.3 more in the mean for v, 1.3 for p.)"""
+    B, Hkv, D = 64, 8, 256
+    p = R.Paged(71, [1] * B, Hkv, 64, D, F16, F32, 16)
+    q, _ = act_array(np.random.default_rng(71), (B, Hkv, 64), "f32")
+    got = fb.paged_decode(q, p.on_gpu(fb, torch), cuda(np.ones(B, np.int32)), scale=0.1)
+    v = np.stack([x[0] for x in p.vd])
+    rel = (got["O"].double().cpu().numpy() - v) / np.abs(v) * np.sign(v) / U
+    assert np.abs(rel).max() <= 13.0, np.abs(rel).max()
+    assert abs(rel.mean()) <= 1.2, rel.mean()
