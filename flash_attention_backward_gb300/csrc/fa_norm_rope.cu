@@ -22,20 +22,20 @@ fa_status check_rope(const fa_rope* r, int D, const int32_t* pos, int N, Rope* o
 // dw = the CTAs' sums in a fixed order: 32 columns a CTA, each split over 32 rows of threads.  blockIdx.y 0:
 // queries, 1: keys.
 __global__ void __launch_bounds__(1024) k_dw_reduce(const float* part, int ctas_q, int ctas, int D, float* dwq, float* dwk) {
-  __shared__ float red[32][33];
+  __shared__ float red[32][33], lost[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x, b0 = blockIdx.y ? ctas_q : 0, b1 = blockIdx.y ? ctas : ctas_q;
   float* out = blockIdx.y ? dwk : dwq;
   after_last();
   if (!out) return;
-  float s = 0.f;
-  for (int b = b0 + threadIdx.y; b < b1; b += 32) s += part[(long long)b * D + c];
-  red[threadIdx.y][threadIdx.x] = s;
+  ExactSum s;
+  for (int b = b0 + threadIdx.y; b < b1; b += 32) s.add(part[(long long)b * D + c]);
+  red[threadIdx.y][threadIdx.x] = s.s, lost[threadIdx.y][threadIdx.x] = s.lost;
   __syncthreads();
   if (threadIdx.y == 0) {
-    s = 0.f;
+    s = ExactSum();
 #pragma unroll
-    for (int y = 0; y < 32; ++y) s += red[y][threadIdx.x];
-    out[c] = s;
+    for (int y = 0; y < 32; ++y) s.add(red[y][threadIdx.x]), s.lost += lost[y][threadIdx.x];
+    out[c] = s.value();
   }
 }
 

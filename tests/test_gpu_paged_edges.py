@@ -252,3 +252,35 @@ def test_f32_values_are_rounded_to_their_parts(fb):
     rel = (got["O"].double().cpu().numpy() - v) / np.abs(v) * np.sign(v) / U
     assert np.abs(rel).max() <= 13.0, np.abs(rel).max()
     assert abs(rel.mean()) <= 1.2, rel.mean()
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_weights_gradient_over_many_rows(fb, off):
+    """dw of 4 million rows of one head, 1724 a lane, from aligned rows and from rows off 16 bytes; the 2-norm of the error
+    over that of dw, in u = 2^-24.  Terms have random signs: an error d of each is one of d in the sum: two rounded
+    products and r, 1.2 in the root mean square.  A sum of n terms: each addition rounds by 0.3 (a half at most, evenly)
+    of a unit of the sum so far, of up to 2: 0.3 sqrt(n / 2) of the last one; 41 terms and 42 of those sums: 1.4 and
+    1.4; the rest keeps what its roundings lose, but for the last two, 0.4.  Together 2.4, and 3.2 are allowed (all in one f32 sum: 8.8)."""
+    N, D = 4193000, 64
+    gen = torch.Generator(device="cuda").manual_seed(81)
+    x, gy = (torch.randn(N * D + 8, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    x, gy = x[off:off + N * D].view(N, 1, D), gy[:N * D].view(N, 1, D)
+    w = torch.rand(D, generator=gen, device="cuda") + 0.5
+    got = fb.qk_norm_rope_backward(gy, None, x, None, None, wq=w)["dwq"].double()
+    ref = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for a, g in zip(x.split(1 << 19), gy.split(1 << 19)):
+        a = a.double()
+        ref += (g.double() * a / torch.sqrt((a * a).mean(-1, keepdim=True) + 1e-6)).sum((0, 1))
+    e = float((got - ref).norm() / ref.norm()) / U
+    assert e <= 3.2, e
+    assert fb.fa_back_get_error() == 0
+
+
+def test_weights_gradient_of_an_infinity(fb):
+    """An infinite gradient component makes that of its weight infinite, of the definition's sign, and no other."""
+    N, H, D = 3000, 2, 128
+    rng = np.random.default_rng(91)
+    (x, xa), (g, _) = act_array(rng, (N, H, D), "f32"), act_array(rng, (N, H, D), "f32")
+    g[1234, 1, 17] = float("inf")
+    got = fb.qk_norm_rope_backward(g, None, x, None, None, wq=torch.ones(D, device="cuda"))["dwq"].cpu().numpy()
+    assert got[17] == np.sign(xa[1234, 1, 17]) * np.inf and np.isfinite(np.delete(got, 17)).all()
