@@ -445,8 +445,10 @@ constexpr int kMinTiles = 4;     // an item has at least this many tiles of 16 k
 constexpr int kPlanBatch = 256;  // with more sequences than this, a kernel of its own lays out the items
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLift = 7.f;     // weights are exp2(x - max + 7): the parts' small end moves out of the way
-constexpr float kRescale = 8.f;  // the running maximum moves when a score exceeds it by this (weights <= 2^15)
+constexpr float kRescale = 8.f;  // the running maximum moves when a score exceeds it by this
+// Weights are exp2(x - max + lift).  Lifted by 7 (weights <= 2^15) the binary16 parts' small end is out of the way;
+// of f32 values, whose weights need no such room, they stay <= 1, so that no product leaves f32's range.
+__host__ __device__ constexpr float weight_lift(int vt) { return vt == FA_F32 ? -kRescale : 7.f; }
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct DecodeArgs {
@@ -457,6 +459,7 @@ struct DecodeArgs {
   const int32_t* lens;
   int H, G, HG, chunks;  // query heads, heads of a group, (KV head, chunk of 8 heads) pairs, chunks of a group
   float scale, softcap;
+  float lift;   // weight_lift() of the value type
   const float *alibi, *sinks;
   void* O;
   float* lse;
@@ -703,6 +706,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
   constexpr int NW = kWarps, SLOTS = C.slots, PK = C.pk, PV = C.pv;
+  constexpr float kLift = weight_lift(VT);
   constexpr int RBK = cache_row_bytes(KT, D), RBV = cache_row_bytes(VT, DV);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_scan[NW];
@@ -1119,19 +1123,20 @@ __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
     S = fmaf(s_l[i], f, S);
     x.x = fmaf(v.x, f, x.x), x.y = fmaf(v.y, f, x.y), x.z = fmaf(v.z, f, x.z), x.w = fmaf(v.w, f, x.w);
   }
-  if (a.sinks) S += fab::ex2(sk - ref + kLift);
+  if (a.sinks) S += fab::ex2(sk - ref + a.lift);
   const float inv = S == 0.f ? 0.f : 1.f / S;
   const long long at = ((long long)job.x * a.H + h) * DV + 4 * ln;
   act_store(a.O, a.act, at, x.x * inv), act_store(a.O, a.act, at + 1, x.y * inv);
   act_store(a.O, a.act, at + 2, x.z * inv), act_store(a.O, a.act, at + 3, x.w * inv);
-  if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S == 0.f ? -INFINITY : (ref - kLift + log2f(S)) * kLn2;
+  if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S == 0.f ? -INFINITY : (ref - a.lift + log2f(S)) * kLn2;
 }
 
-typedef cudaError_t (*DecodeFn)(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s);
+typedef cudaError_t (*DecodeFn)(DecodeArgs a, const DecodeMaps& m, cudaStream_t s);
 
 template <int D, int DV, int KT, int VT>
-cudaError_t run_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t s) {
+cudaError_t run_decode(DecodeArgs a, const DecodeMaps& m, cudaStream_t s) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
+  a.lift = weight_lift(VT);
   static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
   cudaError_t e = cudaSuccess;
   if (!allow_smem(reinterpret_cast<const void*>(k_decode<D, DV, KT, VT>), C.smem, &ready)) return cudaErrorInvalidValue;

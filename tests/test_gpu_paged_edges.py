@@ -284,3 +284,11 @@ def test_weights_gradient_of_an_infinity(fb):
     g[1234, 1, 17] = float("inf")
     got = fb.qk_norm_rope_backward(g, None, x, None, None, wq=torch.ones(D, device="cuda"))["dwq"].cpu().numpy()
     assert got[17] == np.sign(xa[1234, 1, 17]) * np.inf and np.isfinite(np.delete(got, 17)).all()
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("lens", [[500, 30], [9000, 1, 2]])
+def test_f32_values_near_the_top_of_their_range(fb, lens, sinks):
+    """O lies between the values, so finite values give a finite O: no weight on the way is above one."""
+    p = R.Paged(101, lens, 2, 128, 128, F16, F32, 16, v_amp=1e36)
+    check_decode(fb, p, 8, sinks=sinks)
