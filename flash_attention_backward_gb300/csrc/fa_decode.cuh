@@ -690,7 +690,7 @@ static __device__ __noinline__ void fetch_rows(uint32_t sl, int kv, uint32_t dst
 // Soft cap and distance bias of a lane's four scores (keys at distances d, d + 1, d + 8, d + 9; out of line)
 static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float slope, int d) {
   if (cap > 0.f) {
-    const float inv = 1.f / cap;
+    const float inv = fminf(1.f / cap, 3.4028234e38f);  // (a denormal cap: not infinity, which 0 times is NaN)
     x = make_float4(cap * tanhf(x.x * inv), cap * tanhf(x.y * inv), cap * tanhf(x.z * inv), cap * tanhf(x.w * inv));
   }
   return make_float4(fmaf(slope, (float)d, x.x), fmaf(slope, (float)(d + 1), x.y), fmaf(slope, (float)(d + 8), x.z),

@@ -292,3 +292,14 @@ def test_f32_values_near_the_top_of_their_range(fb, lens, sinks):
     """O lies between the values, so finite values give a finite O: no weight on the way is above one."""
     p = R.Paged(101, lens, 2, 128, 128, F16, F32, 16, v_amp=1e36)
     check_decode(fb, p, 8, sinks=sinks)
+
+
+@pytest.mark.parametrize("cap", [1e-45, 1e-40, 1e-38, 3e38])
+def test_soft_cap_at_the_ends_of_its_range(fb, cap):
+    """Caps whose reciprocal leaves f32's range, with scores that are zero (of keys of zeros) and others."""
+    p = R.Paged(111, [40, 300], 2, 64, 64, F16, F16, 16)
+    for b in range(2):
+        j = np.arange(0, p.lens[b], 3)
+        p.k[p.table[b, j // 16], j % 16] = 0
+        p.kd[b][j] = 0.0
+    check_decode(fb, p, 4, softcap=cap)
