@@ -117,6 +117,8 @@ def _index(device: torch.device) -> int:
 def _call(fn, device: torch.device, stream: Optional[torch.cuda.Stream]):
     """fn(stream handle) on the current stream of the device, or on `stream`."""
     index = _index(device)
+    if stream is not None and stream.device != device:
+        raise FaBackError(f"stream: one of {device} expected, where the tensors are, got one of {stream.device}")
     if stream is None and index == torch._C._cuda_getDevice():
         return fn(torch._C._cuda_getCurrentRawStream(index))
     with _On(device, stream):
