@@ -538,13 +538,17 @@ __device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
 // parts costs more than it gains: with w tiles an item a sequence of n takes about w / 4 tile times and
 // n / w parts, least near w = 0.37 sqrt(n) as measured.  A chunk of U / (R - B) always fits, U / R never
 // unless all divide; chunks between the two are tried where the batch is small (fit_chunk).  Whatever
-// chunk is taken is at least U / R, so there are at most R + B items, R split sequences and 2 R parts.
-__device__ __forceinline__ int least_chunk(long long U, int R) {
-  return (int)max((long long)max(kMinTiles, (int)(0.37f * sqrtf((float)U))), (U + R - 1) / R);
+// chunk is taken is at least U / R, or no sequence's n is above it, so there are at most R + B items, R split
+// sequences and 2 R parts.
+constexpr long long kMaxTiles = 1 << 26;  // of a sequence (2^30 positions)
+__host__ __device__ __forceinline__ int least_chunk(long long U, int R) {
+  const long long fits = (U + R - 1) / R, joins = (long long)(0.37f * sqrtf((float)U)), c = fits > joins ? fits : joins;
+  return (int)(c < kMinTiles ? kMinTiles : c < kMaxTiles ? c : kMaxTiles);
 }
-__device__ __forceinline__ int safe_chunk(long long U, int B, int R) {
-  const long long room = max(R - B, (R + 1) / 2);
-  return (int)max((long long)least_chunk(U, R), (U + room - 1) / room);
+__host__ __device__ __forceinline__ int safe_chunk(long long U, int B, int R) {
+  const long long room = R - B > (R + 1) / 2 ? R - B : (R + 1) / 2, c = (U + room - 1) / room;
+  const int least = least_chunk(U, R);
+  return (int)(c < least ? least : c < kMaxTiles ? c : kMaxTiles);
 }
 // The least of the block's candidates between the two whose items fit (tiles: the B sequences'), if that
 // saves more than joining further parts costs (about six tile times of a warp); all threads get it.  (A
@@ -570,11 +574,11 @@ __device__ __forceinline__ int fit_chunk(const int* tiles, int B, int R, int lo,
 struct Counts {
   int items, slots, split;
 };
-__device__ __forceinline__ uint64_t pack_counts(int n, int chunk) {
+__host__ __device__ __forceinline__ uint64_t pack_counts(int n, int chunk) {
   const uint32_t s = (n + chunk - 1) / chunk;
   return (uint64_t)s | (s > 1 ? ((uint64_t)s << 32) + (1ull << 48) : 0ull);
 }
-__device__ __forceinline__ Counts unpack_counts(uint64_t x) {
+__host__ __device__ __forceinline__ Counts unpack_counts(uint64_t x) {
   return Counts{(int)(uint32_t)x, (int)((x >> 32) & 0xffff), (int)(x >> 48)};
 }
 // Sum of v over the block, and over the threads before this one (the warps' sums in `smem`, a word each)
