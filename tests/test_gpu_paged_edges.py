@@ -303,3 +303,39 @@ def test_soft_cap_at_the_ends_of_its_range(fb, cap):
         p.k[p.table[b, j // 16], j % 16] = 0
         p.kd[b][j] = 0.0
     check_decode(fb, p, 4, softcap=cap)
+
+
+def test_the_marshalling_module_serves_the_plain_calls(fb, monkeypatch):
+    """What test_both_forms_of_the_wrappers_agree compares is served by the module: with the Python form's entry points
+    out of reach the same calls still return, and called directly none of the module's functions declines."""
+    from flash_attention_backward_gb300 import _native, paged
+    rng = np.random.default_rng(31)
+    p = R.Paged(31, [70, 0, 200], 2, 128, 64, Q8, F16, 16)
+    cache = p.on_gpu(fb, torch)
+    (q, _), (k, _), (v, _) = (act_array(rng, (3, h, d), "bf16") for h, d in ((6, 128), (2, 128), (2, 64)))
+    w, rope = torch.rand(128, device="cuda") + 0.5, fb.rope_frequencies(128)
+    seq, pos = cuda(np.array([0, 2, 2], np.int32)), cuda(np.array([5, 17, 180], np.int32))
+    lens, sinks = cuda(np.array(p.lens, np.int32)), torch.zeros(6, device="cuda")
+    fb.paged_decode(q, cache, lens, scale=0.1)  # binds it
+
+    def out_of_reach(*a):
+        raise AssertionError("the Python form")
+
+    for n in ("fa_qk_norm_rope", "fa_qk_norm_rope_backward", "fa_cache_append", "fa_cache_read", "fa_paged_decode"):
+        monkeypatch.setattr(_native, n, out_of_reach)
+    fb.paged_decode(q, cache, lens, scale=0.1, softcap=20.0, sinks=sinks, alibi_slopes=sinks)
+    fb.cache_read(cache, seq, pos, dtype=torch.bfloat16)
+    fb.cache_append(k, v, cache, seq, pos, k_norm=w, rope=rope)
+    fb.qk_norm_rope(q, k, pos, wq=w, wk=w, rope=rope, rope_style=fb.FA_ROPE_PAIRS, dtype=torch.float32)
+    fb.qk_norm_rope(q, None, None, wq=w)
+    fb.qk_norm_rope_backward(q, k, q, k, pos, wq=w, wk=w, rope=rope)
+    fb.qk_norm_rope_backward(q.float(), None, q, None, pos, rope=rope)
+    f, style = paged._fast, fb.FA_ROPE_HALVES
+    assert f.norm(q, k, pos, w, w, 1e-6, rope, style, None) is not None
+    assert f.norm_back(q, k, q, k, pos, w, w, 1e-6, rope, style) is not None
+    assert f.append(k, v, cache._at, cache._index, seq, pos, w, 1e-6, rope, style) is True
+    assert f.read(cache._at, cache._index, seq, pos, torch.float16) is not None
+    assert f.decode(q, cache._at, cache._index, lens, 0.1, None, 0.0, None) is not None
+    with pytest.raises(AssertionError, match="the Python form"):  # (and what it declines goes there)
+        fb.paged_decode(q, cache, lens, scale=0.1, workspace=fb.Workspace("cuda"))
+    assert fb.fa_back_get_error() == 0
