@@ -148,8 +148,9 @@ def _rope(rope: Optional[torch.Tensor], style: int, device) -> Optional[nat.fa_r
 
 class PagedCache:
     """A paged raw K/V cache: pools k and v (uint8 [num_pages][page_size][Hkv][row]) of cache types k_type
-    and v_type, and page_table (int32 [B][max_pages]).  Holds the tensors; nothing is copied, so the
-    table may be edited in place between calls."""
+    and v_type, and page_table (int32 [B][max_pages]).  Holds the tensors; nothing is copied, so pools and
+    table may be edited in place between calls.  It is of the tensors that it was made with: for others (a pool
+    that has grown) make another one."""
 
     def __init__(self, k: torch.Tensor, k_type: int, v: torch.Tensor, v_type: int, page_table: torch.Tensor, *, D: int,
                  Dv: int):
@@ -170,6 +171,11 @@ class PagedCache:
                                     self.page_size, self.B, self.max_pages, self.Hkv, D, Dv)
         self._at, self._index = ctypes.addressof(self.c), self.device.index
         self._ws = {}  # decode workspace bytes by query head count
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:  # the kernels would go on with the old tensor's address
+            raise FaBackError(f"{name}: a PagedCache keeps what it was made with; make another one")
+        super().__setattr__(name, value)
 
     def decode_workspace_size(self, H: int) -> int:
         """fa_paged_decode_workspace_size() of this cache (0: the arguments are invalid)."""
