@@ -83,6 +83,13 @@ def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> int:
                       f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
+def _count(name: str, t: torch.Tensor) -> int:
+    """The tokens of t [T]..."""
+    if t.dim() == 0:
+        raise FaBackError(f"{name}: a tensor of tokens expected, got one value")
+    return t.shape[0]
+
+
 def _heads(name: str, t: torch.Tensor, N: int, D: int, dtype, device):
     """Heads and strides (token, head) of t [N][heads][D], possibly a view whose components are contiguous."""
     if t.dim() == 3 and t.dtype is dtype and t.device == device:
@@ -196,7 +203,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, seq: torch
     if stream is None and cache._index is not None and (_plain or _bind()) and _fast.append(
             k, v, cache._at, cache._index, seq, pos, k_norm, eps, rope, rope_style):
         return
-    dev, T = cache.device, k.shape[0]
+    dev, T = cache.device, _count("k", k)
     act = _act(k.dtype)
     hk, k_row, k_head = _heads("k", k, T, cache.D, k.dtype, dev)
     hv, v_row, v_head = _heads("v", v, T, cache.Dv, k.dtype, dev)
@@ -220,7 +227,7 @@ def cache_read(cache: PagedCache, seq: torch.Tensor, pos: torch.Tensor, *, dtype
         got = _fast.read(cache._at, cache._index, seq, pos, dtype)
         if got is not None:
             return got
-    dev, T = cache.device, seq.shape[0]
+    dev, T = cache.device, _count("seq", seq)
     if dtype is torch.uint8:
         act, nk, nv = nat.FA_ACT_RAW, cache.k.shape[3], cache.v.shape[3]
     else:

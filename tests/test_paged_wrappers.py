@@ -35,3 +35,12 @@ def test_a_cache_keeps_what_it_was_made_with(name):
     assert getattr(c, name) is was
     c.page_table.fill_(1)  # in place
     assert c.decode_workspace_size.__self__ is c
+
+
+def test_single_values_in_the_place_of_tokens_are_refused():
+    c, one = paged_cache(), torch.zeros((), dtype=torch.int32)
+    for call in (lambda: fb.cache_read(c, one, one), lambda: fb.cache_append(one.float(), one.float(), c, one, one),
+                 lambda: fb.paged_decode(one.float(), c, one, scale=1.0), lambda: fb.qk_norm_rope(one.float(), None, None),
+                 lambda: fb.qk_norm_rope_backward(one.float(), None, one.float(), None, None)):
+        with pytest.raises(fb.FaBackError):
+            call()
