@@ -10,8 +10,8 @@
 // Precision.  Codes are exact in binary16 (q8_0, q4_0 keys) and in bf16 (values), and block scales
 // are applied in f32, to the product (keys) or to the weight (values).  q is split into two binary16
 // parts (22 bits of the head's largest magnitude, after an exact power-of-two scale), a weight times
-// block scale into three bf16 parts (all 24 bits, with f32's range), a weight alone into two binary16
-// parts (22 bits), and for f32 rows all operands into two tf32 parts (three products).
+// block scale into three bf16 parts (all 24 bits, with f32's range; two parts, 16 bits, for 16-bit outputs),
+// a weight alone into two binary16 parts (22 bits), and for f32 rows all operands into two tf32 parts (three products).
 //
 // Bounds, on a GB300 (6787 GB/s measured copy rate).  The cache rows are read once; binary16 and f32 rows
 // are bound by that: 48 ragged sequences of up to 8192 keys (32 heads, 8 KV heads of 128, 602 MB) take
@@ -342,7 +342,10 @@ __device__ __forceinline__ void values_f32(float (&o)[DV / 16][4], const float (
 }
 
 // Weights times block scales as three bf16 parts of eight bits each, which hold all 24 of an f32: the parts
-// are cut off, so the high halves of two values and of what they leave are pairs already.
+// are cut off, so the high halves of two values and of what they leave are pairs already.  Two parts, the second one
+// rounded, hold 16 bits, of which a 16-bit output keeps 11 or 8: they do for those (24 ragged sequences of mixed
+// types, f16 outputs: 43.7 us, 45.5 with three; f32 outputs, 512 q8_0 keys: 1.6e-6 off 64 bits with two, 2.4e-7).
+template <int PARTS>
 struct Scaled {
   uint32_t h0, h1, m0, m1, l0, l1;
   static __device__ __forceinline__ uint32_t take(float& x, float& y) {
@@ -353,15 +356,24 @@ struct Scaled {
   __device__ __forceinline__ Scaled(const float (&p)[4], float d0, float d1, float d2, float d3) {
     float x0 = p[0] * d0, x1 = p[1] * d1, x2 = p[2] * d2, x3 = p[3] * d3;
     h0 = take(x0, x1), h1 = take(x2, x3);
-    m0 = take(x0, x1), m1 = take(x2, x3);
-    l0 = take(x0, x1), l1 = take(x2, x3);
+    if (PARTS == 2) {
+      m0 = pack_b2(x0, x1), m1 = pack_b2(x2, x3), l0 = l1 = 0;
+    } else {
+      m0 = take(x0, x1), m1 = take(x2, x3);
+      l0 = take(x0, x1), l1 = take(x2, x3);
+    }
   }
 };
 
-__device__ __forceinline__ void add_scaled(float (&o)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const Scaled& b) {
+template <int PARTS>
+__device__ __forceinline__ void add_scaled(float (&o)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const Scaled<PARTS>& b) {
   float c[4];
-  mma_bf16_first(c, a0, a1, a2, a3, b.l0, b.l1);
-  mma_bf16(c, a0, a1, a2, a3, b.m0, b.m1);
+  if (PARTS == 2) {
+    mma_bf16_first(c, a0, a1, a2, a3, b.m0, b.m1);
+  } else {
+    mma_bf16_first(c, a0, a1, a2, a3, b.l0, b.l1);
+    mma_bf16(c, a0, a1, a2, a3, b.m0, b.m1);
+  }
   mma_bf16(c, a0, a1, a2, a3, b.h0, b.h1);
   add_tile(o, c);
 }
@@ -373,7 +385,7 @@ __device__ __forceinline__ uint32_t q8_b2(uint32_t k0, uint32_t k1) {
   return bsub2(and_or(v, 0x007f007fu, 0x43004300u), and_or(v, 0x00800080u, 0x43004300u));
 }
 
-template <int DV>
+template <int DV, int PARTS>
 __device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&p)[4], uint32_t rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const uint32_t r[4] = {lds_u32(rows + 8 * t), lds_u32(rows + 8 * t + 4), lds_u32(rows + 8 * t + 32), lds_u32(rows + 8 * t + 36)};
@@ -390,14 +402,14 @@ __device__ __forceinline__ void values_q8(float (&o)[DV / 16][4], const float (&
       d[i] = lo_h(h), e[i] = hi_h(m);
     }
     {
-      const Scaled b(p, d[0], d[1], d[2], d[3]);
+      const Scaled<PARTS> b(p, d[0], d[1], d[2], d[3]);
       const uint32_t a0 = q8_b2<0>(w[0], w[1]), a1 = q8_b2<1>(w[0], w[1]), a2 = q8_b2<0>(w[2], w[3]), a3 = q8_b2<1>(w[2], w[3]);
       add_scaled(o[4 * pr], a0, a1, a2, a3, b);
       const uint32_t c0 = q8_b2<2>(w[0], w[1]), c1 = q8_b2<3>(w[0], w[1]), c2 = q8_b2<2>(w[2], w[3]), c3 = q8_b2<3>(w[2], w[3]);
       add_scaled(o[4 * pr + 1], c0, c1, c2, c3, b);
     }
     {
-      const Scaled b(p, e[0], e[1], e[2], e[3]);
+      const Scaled<PARTS> b(p, e[0], e[1], e[2], e[3]);
       const uint32_t a0 = q8_b2<0>(x[0], x[1]), a1 = q8_b2<1>(x[0], x[1]), a2 = q8_b2<0>(x[2], x[3]), a3 = q8_b2<1>(x[2], x[3]);
       add_scaled(o[4 * pr + 2], a0, a1, a2, a3, b);
       const uint32_t c0 = q8_b2<2>(x[0], x[1]), c1 = q8_b2<3>(x[0], x[1]), c2 = q8_b2<2>(x[2], x[3]), c3 = q8_b2<3>(x[2], x[3]);
@@ -412,7 +424,7 @@ __device__ __forceinline__ uint32_t q4_b2(uint32_t w) {
   return bsub2(and_or(w >> SH, 0x000f000fu, 0x43004300u), 0x43084308u);
 }
 
-template <int DV>
+template <int DV, int PARTS>
 __device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&p)[4], uint32_t rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const uint32_t r[4] = {lds_u32(rows + 8 * t), lds_u32(rows + 8 * t + 4), lds_u32(rows + 8 * t + 32), lds_u32(rows + 8 * t + 36)};
@@ -425,7 +437,7 @@ __device__ __forceinline__ void values_q4(float (&o)[DV / 16][4], const float (&
       w[i] = lds_u16(r[i] + blk * 18 + 2 + 2 * g);  // components 2g, 2g + 1 and 2g + 16, 2g + 17
       d[i] = lo_h(lds_u16(r[i] + blk * 18));
     }
-    const Scaled b(p, d[0], d[1], d[2], d[3]);
+    const Scaled<PARTS> b(p, d[0], d[1], d[2], d[3]);
     const uint32_t u = w[0] | w[1] << 16, v = w[2] | w[3] << 16;
     {
       const uint32_t a0 = q4_b2<0>(u), a1 = q4_b2<4>(u), a2 = q4_b2<0>(v), a3 = q4_b2<4>(v);
@@ -985,9 +997,11 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       l += (p[0] + p[1]) + (p[2] + p[3]);
       dead = !arrived(1, slot);
       if (dead) break;
-      if (VT == FA_Q8_0) values_q8<DV>(o, p, sl + 64, lane);
+      if (VT == FA_Q8_0 && a.act == FA_ACT_F32) values_q8<DV, 3>(o, p, sl + 64, lane);
+      else if (VT == FA_Q8_0) values_q8<DV, 2>(o, p, sl + 64, lane);
       else if (VT == FA_F16) values_f16<DV>(o, p, sl + 64, lane);
-      else if (VT == FA_Q4_0) values_q4<DV>(o, p, sl + 64, lane);
+      else if (VT == FA_Q4_0 && a.act == FA_ACT_F32) values_q4<DV, 3>(o, p, sl + 64, lane);
+      else if (VT == FA_Q4_0) values_q4<DV, 2>(o, p, sl + 64, lane);
       else values_f32<DV>(o, p, sl + 64, lane);
       __syncwarp();
       if (next < ntile) fetch(1, slot, row, next);
