@@ -1,9 +1,12 @@
 // Rows into and out of a paged raw K/V cache.  A token's activations are read once and its cache rows
-// written once (append), or the other way (read).  Rows are quantised at the rate that instructions
-// allow, not memory: norm, rotation, largest magnitude, codes, border test and packing are 25 to 33
-// instructions a value and lane (counted), so 2048 tokens of 4 KV heads of 256 (f32 to q8_0, keys normalised and rotated) and their
-// read-back in binary16 take 12.3 us where the 34 MB would take 5.0 (of GPU time on a GB300; 5003 tokens
-// of 8 heads of 128, bf16 to f16 and q4_0: 21.7 us against 9.9).  64 tokens take 5.2 us, two launches.
+// written once (append), or the other way (read).  On a GB300, of GPU time: 2048 tokens of 4 KV heads of
+// 256 (f32 to q8_0, keys normalised and rotated) 8.0 us where their bytes would take 3.1 at the copy rate, 5003 tokens
+// of 8 heads of 128 (bf16 to f16 and q4_0) 14.7 for 4.9; reading those back in binary16 4.3 for 1.9 and 6.3 for 4.9,
+// raw 3.4 for 1.3 and 7.8 for 3.9; 64 tokens 3.4 and 1.9, a launch and its latencies.  Norm, rotation, largest
+// magnitude, codes, border test and packing are 25 to 33 instructions a value and lane (counted), but fewer than half
+// of the issue slots are used (1.9 and 2.1 of 4 a cycle and SM): an append's warps, 30 % of an SM's, wait for their
+// loads and for the shuffles of one row at a time.  The decoded read waits for loads and, since one kernel
+// holds every type of K and V, for instructions.
 #include <algorithm>
 #include <cmath>
 

@@ -13,14 +13,19 @@
 // block scale into three bf16 parts (all 24 bits, with f32's range; two parts, 16 bits, for 16-bit outputs),
 // a weight alone into two binary16 parts (22 bits), and for f32 rows all operands into two tf32 parts (three products).
 //
-// Bounds, on a GB300 (6787 GB/s measured copy rate).  The cache rows are read once; binary16 and f32 rows
-// are bound by that: 48 ragged sequences of up to 8192 keys (32 heads, 8 KV heads of 128, 602 MB) take
-// 106 us, 84 % of the copy rate.  Quantised rows are bound by instructions: a tile of q8_0 keys and values
-// of 256 is about 1250 a warp, of which the decoding of 8192 codes is some 420 and the 64 products 64; one
-// sequence of 75520 keys (24 heads, 4 KV heads of 256, 164 MB) takes 43 us, 56 % of the copy rate, at 1.9
-// instructions a cycle and SM, with the tensor pipe 19 % busy.  Sixteen warps an SM instead of twelve (128
-// registers) do not raise that (45.4 us); rolling the key loop up does not either.  A short call is a chain
-// of latencies: launch, lengths, first rows, four tiles, the join (512 keys, 2 KV heads of 128: 9 us).
+// Bounds, on a GB300 (6787 GB/s measured copy rate; the floor is the rows, read once).  binary16 and f32 rows
+// wait for DRAM: 48 ragged sequences of up to 8192 keys (32 heads, 8 KV heads of 128) in 109 us, 82 % of that rate,
+// f32 rows 240 us, 74 %; one sequence of 75520 f32 keys (24 heads, 4 KV heads of 256) 97 us, 94 %.  Quantised rows
+// wait for latencies: the same sequence in q8_0 (164 MB) takes 47 us, 51 %, a ragged batch of q4_0 keys and q8_0
+// values with every extension 44 us, 29 %.  A tile of q8_0 keys and values of 256 is about 1365 instructions a warp,
+// some 420 of them for the decoding of 8192 codes and 80 products; the 26 million of the sequence would be issued in
+// 22 us, but at 1.8 of 4 a cycle and SM, no pipe above 37 %, what is short is work to switch to: three warps a
+// scheduler (168 registers: 64 sums a lane), in phases of their own on some 20 KB of straight-line code ("wait" and "no
+// instruction" lead the stalls), and a single slot of copies a warp.  Sixteen warps an SM at 128 registers did not
+// help (45.4 us for 43.2 before the sums of tiles were kept apart), nor did rolling the key loop up.  A short call is
+// a chain of latencies: launch, lengths, first rows, four tiles, the join's launch (512 keys, 2 KV heads of 128: 9 us).
+// More than eight query heads to a KV head read and decode its rows once for each eight (24 heads, 2 KV heads,
+// f16: 46 us where 12 heads take 36); more than 256 sequences take a launch more (300: 155 us, 83 %).
 #pragma once
 #include "fa_paged.cuh"
 #include "sm100.cuh"
@@ -503,7 +508,9 @@ __host__ __device__ constexpr int map_es(int pitch) { return pitch <= 512 ? 1 : 
 // CTAs of few warps, several to an SM: a short sequence is a few tiles, and while one CTA starts, joins its
 // warps or waits for its first rows, the others work.  Registers (about 168 a thread for Dv = 256, else
 // 128) allow 12 or 16 warps an SM; shared memory may allow fewer.  What it has left goes to slots (a
-// tile's key rows and value rows) of each warp's ring, which also takes the warp's sums in the end.
+// tile's key rows and value rows) of each warp's ring, which also takes the warp's sums in the end: one for
+// q8_0 and f16 rows of 256 (a key row's copy is then asked for as soon as its scores are done, a value row's behind
+// the products), two for q8_0 of 128, up to four for smaller rows.
 // (Against CTAs that fill an SM with 8, 12 or 16 warps: 9.0 us for 11.8 with 512 keys, 41 for 58 with a
 // ragged batch of mixed types.)
 constexpr int kWarps = 4;

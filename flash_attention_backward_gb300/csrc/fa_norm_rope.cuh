@@ -4,18 +4,21 @@
 //   y = R (w o x r),  r = rsqrt(mean(x^2) + eps)
 //   g = R^T gy,  dw = sum g o x r,  h = g o w,  dx = r (h - x r^2 mean(h o x))
 //
-// Both are bound by memory: a head is read once and written once (backward: x and gy read, dx written),
-// everything between stays in registers.  The arithmetic has to stay out of the way, though: a head of
-// 128 bf16 components is 256 bytes, so an SM takes one every ten cycles at the card's bandwidth.  Hence
-// the layout: D / 8 lanes a head, and a lane holds both members of its four rotation pairs, which makes
-// the rotation free of shuffles; packed pairs of f32 (fma.rn.f32x2) halve the instructions; the angles of a
-// token are computed once for all heads of it that a warp takes.
+// A head is read once and written once (backward: x and gy read, dx written), everything between stays in
+// registers.  The arithmetic has to stay out of the way: a head of 128 bf16 components is 256 bytes, so an SM
+// takes one every ten cycles at the card's bandwidth.  Hence the layout: D / 8 lanes a head, and a lane holds both
+// members of its four rotation pairs, which makes the rotation free of shuffles; packed pairs of f32
+// (fma.rn.f32x2) halve the instructions; the angles of a token are computed once for all heads of it that a warp
+// takes.
 //
-// Measured on a GB300 (6787 GB/s copy rate): forward, 2048 tokens of 28 heads of 256, f32: 117 MB in 17.7 us,
-// 98 % of the copy rate; 16411 tokens of 10 heads of 64, bf16 to f32: 63 MB in 15.5 us, 60 % (instructions: a
-// head of 64 has half the bytes, and the 16 angles of its token are shared by ten heads only).  Gradient, 8191
-// tokens of 40 heads of 128, bf16: 252 MB in 51 us, 73 %; 2048 tokens of 28 heads of 256, f32: 176 MB in
-// 33 us, 78 %.  A decode step's call (64 tokens) is 2.4 us, a launch and two latencies.
+// Measured on a GB300 (6787 GB/s copy rate).  Forward, 2048 tokens of 28 heads of 256, f32, 117 MB: 21.1 us a call
+// over changing inputs, 82 % of the copy rate (17.7 us of GPU time over the same inputs, part of which L2 then
+// holds).  16411 tokens of 10 heads of 64, bf16 to f32, 63 MB: 16.1 us, 58 %, at 2.4 of 4 instructions a cycle and SM: a
+// head of 64 has a quarter of those bytes, the 16 angles of its token (half of the warp's lanes) are shared by ten
+// heads only, and ten heads are two and a half rounds of four.  Gradient, 8191 tokens of 40 heads of 128, bf16, 252
+// MB: 52 us, 71 %, at 2.4 instructions a cycle beside 52 % of DRAM; 2048 tokens of 28 heads of 256, f32, 176 MB:
+// 34.4 us, 75 %.  Heads off 16 bytes: forward 20.1 us for 17.7, gradient 49.7 for 33.5.  64 tokens: 2.4 us, a launch
+// and two latencies.
 #pragma once
 #include "fa_paged.cuh"
 #include "sm100.cuh"
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
 // in shared memory: bulk copies bring x and gy of the items to come while one is worked on, which takes
 // the loads off the registers and the issue slots.  A token's factors are computed when the run comes to
 // it.  dw is summed by lane over the run (put_dw), then over the CTA's lane groups in order.  (Loads into registers
-// instead of the ring: 79 us for 8191 tokens of 40 heads of 128, bf16, against 51.)
+// instead of the ring: 79 us for 8191 tokens of 40 heads of 128, bf16, against 52.)
 constexpr int kBackCtas = 2, kBackWarps = 8;
 // Slots of a warp's ring and their bytes: a head of f32 takes up to 2 KB, and an item of one or two would
 // cost more in its handling than in its work (2048 tokens of 28 heads of 256: 33.8 us with 2 slots of
