@@ -13,9 +13,9 @@
 //
 // Measured on a GB300 (6787 GB/s copy rate).  Forward, 2048 tokens of 28 heads of 256, f32, 117 MB: 21.1 us a call
 // over changing inputs, 82 % of the copy rate (17.7 us of GPU time over the same inputs, part of which L2 then
-// holds).  16411 tokens of 10 heads of 64, bf16 to f32, 63 MB: 16.1 us, 58 %, at 2.4 of 4 instructions a cycle and SM: a
-// head of 64 has a quarter of those bytes, the 16 angles of its token (half of the warp's lanes) are shared by ten
-// heads only, and ten heads are two and a half rounds of four.  Gradient, 8191 tokens of 40 heads of 128, bf16, 252
+// holds).  16411 tokens of 10 heads of 64, bf16 to f32, 63 MB: 16.1 us, 58 %, at 2.4 of 4 instructions a cycle and SM: the
+// 16 angles of a token (half of the warp's lanes) are shared by ten heads only, and those are two and a half rounds
+// of four.  Gradient, 8191 tokens of 40 heads of 128, bf16, 252
 // MB: 52 us, 71 %, at 2.4 instructions a cycle beside 52 % of DRAM; 2048 tokens of 28 heads of 256, f32, 176 MB:
 // 34.4 us, 75 %.  Heads off 16 bytes: forward 20.1 us for 17.7, gradient 49.7 for 33.5.  64 tokens: 2.4 us, a launch
 // and two latencies.
