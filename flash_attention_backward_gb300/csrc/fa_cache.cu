@@ -203,6 +203,12 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
   const long long head = IS_K ? a.k_head : a.v_head;
   const int rb = IS_K ? a.c.rbk : a.c.rbv, type = IS_K ? a.c.k_type : a.c.v_type;
   const bool norm = IS_K && a.wk, turns = IS_K && a.rope.n_rot;
+  // A key's squares are summed up as fa_qk_norm_rope() does it, so that a key stored through either is the
+  // same: with FA_ROPE_HALVES from other components than the lane's eight, which it loads beside them (they are
+  // in the cache then).
+  const bool apart = norm && a.rope.style == FA_ROPE_HALVES;
+  int ea = 0, eb = 0;
+  if (apart) place_eight<D>(FA_ROPE_HALVES, a.rope.n_rot, ea, eb);
   float w[8];
   if (norm) load8(a.wk + e0, false, w);
   const unsigned items = (unsigned)a.T * a.nchunk, step = gridDim.x * 8;
@@ -227,17 +233,27 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
     if (turns) turn.set(a.rope, pos, e0);
 #pragma unroll 1
     for (;;) {
-      float x[8];
+      float x[8], r = 1.f;
       unpack8(raw, x);
+      if (norm) {
+        float2 sq[4];
+        if (apart) {
+          const TX* p = x0 - e0 + min(grp, left - 1) * head;
+          Eight<TX> other;
+          if (vec) load_eight<TX, true>(p, ea, eb, other);
+          else load_eight<TX, false>(p, ea, eb, other);
+          unpack_eight(other, sq);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sq[j] = make_float2(x[2 * j], x[2 * j + 1]);
+        }
+        r = inv_rms(square_sum<D>(sq), 1.f / D, a.eps);
+      }
       const bool on = grp < left, more = left > GW;
       left -= GW;
       x0 += GW * head;
       if (more) load();  // the next heads, ahead of this one's work
       if (norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float r = inv_rms(group_sum<LG>(ss), 1.f / D, a.eps);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
       }

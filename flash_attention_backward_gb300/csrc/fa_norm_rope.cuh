@@ -53,35 +53,6 @@ template <typename T>
 constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
 constexpr uint64_t kCopyDrainNs = 2000000000ull;  // after a wait that ran out: for the copies in flight to land
 
-// A lane's four rotation pairs: components [ea, ea + 4) and [eb, eb + 4) of the head.
-//   FA_ROPE_HALVES  pair i is (x[ea + i], x[eb + i]).  The rotated components are pairs 0 .. n_rot / 2 - 1
-//                   (i, i + n_rot / 2); the others pair up likewise and are not turned (n_rot % 16 == 0:
-//                   a lane's pairs are all of one kind).
-//   FA_ROPE_PAIRS   eight neighbouring components, pair i is (x[ea + 2i], x[ea + 2i + 1]).
-template <typename T>
-struct alignas(4 * sizeof(T)) Four {
-  T v[4];
-};
-template <typename T>
-struct Eight {
-  Four<T> a, b;
-};
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_eight(const T* p, int ea, int eb, Eight<T>& o) {
-  if (VEC) {
-    o.a = *reinterpret_cast<const Four<T>*>(p + ea);
-    o.b = *reinterpret_cast<const Four<T>*>(p + eb);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.a.v[i] = p[ea + i], o.b.v[i] = p[eb + i];
-  }
-}
-template <typename T>
-__device__ __forceinline__ void unpack_eight(const Eight<T>& o, float2 (&x)[4]) {
-  x[0] = make_float2(to_f32(o.a.v[0]), to_f32(o.a.v[1])), x[1] = make_float2(to_f32(o.a.v[2]), to_f32(o.a.v[3]));
-  x[2] = make_float2(to_f32(o.b.v[0]), to_f32(o.b.v[1])), x[3] = make_float2(to_f32(o.b.v[2]), to_f32(o.b.v[3]));
-}
 template <typename T>
 __device__ __forceinline__ void store_eight(T* p, int ea, int eb, const float2 (&x)[4]) {
   Four<T> a, b;
@@ -102,11 +73,9 @@ struct Lane {
   float2 c[2], s[2], ns[2];  // cos, sin, -sin of pairs (0, 1) and (2, 3)
 
   __device__ __forceinline__ void place(const Rope& r) {
-    const int p = (threadIdx.x & (D / 8 - 1)) * 4, half = r.n_rot >> 1;
-    n = min(max(half - p, 0), 4);
-    if (STYLE == FA_ROPE_PAIRS) ea = 2 * p, eb = ea + 4;
-    else if (p < half) ea = p, eb = p + half;
-    else ea = r.n_rot + (p - half), eb = ea + (D - r.n_rot) / 2;
+    const int p = (threadIdx.x & (D / 8 - 1)) * 4;
+    n = min(max((r.n_rot >> 1) - p, 0), 4);
+    place_eight<D>(STYLE, r.n_rot, ea, eb);
   }
   __device__ __forceinline__ void weights(const float* weight) {
     norm = weight != nullptr;
@@ -171,10 +140,7 @@ struct Lane {
   }
   __device__ __forceinline__ void forward(float2 (&x)[4], float eps) const {
     if (norm) {
-      float2 q = __fmul2_rn(x[0], x[0]);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) q = __ffma2_rn(x[i], x[i], q);
-      const float r = inv_rms(group_sum<D / 8>(q.x + q.y), 1.f / D, eps);
+      const float r = inv_rms(square_sum<D>(x), 1.f / D, eps);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = __fmul2_rn(__fmul2_rn(x[i], make_float2(r, r)), w[i]);
     }

@@ -168,6 +168,54 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+// A lane's four rotation pairs: components [ea, ea + 4) and [eb, eb + 4) of the head.
+//   FA_ROPE_HALVES  pair i is (x[ea + i], x[eb + i]).  The rotated components are pairs 0 .. n_rot / 2 - 1
+//                   (i, i + n_rot / 2); the others pair up likewise and are not turned (n_rot % 16 == 0:
+//                   a lane's pairs are all of one kind).
+//   FA_ROPE_PAIRS   eight neighbouring components, pair i is (x[ea + 2i], x[ea + 2i + 1]).
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T v[4];
+};
+template <typename T>
+struct Eight {
+  Four<T> a, b;
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_eight(const T* p, int ea, int eb, Eight<T>& o) {
+  if (VEC) {
+    o.a = *reinterpret_cast<const Four<T>*>(p + ea);
+    o.b = *reinterpret_cast<const Four<T>*>(p + eb);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.a.v[i] = p[ea + i], o.b.v[i] = p[eb + i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack_eight(const Eight<T>& o, float2 (&x)[4]) {
+  x[0] = make_float2(to_f32(o.a.v[0]), to_f32(o.a.v[1])), x[1] = make_float2(to_f32(o.a.v[2]), to_f32(o.a.v[3]));
+  x[2] = make_float2(to_f32(o.b.v[0]), to_f32(o.b.v[1])), x[3] = make_float2(to_f32(o.b.v[2]), to_f32(o.b.v[3]));
+}
+
+// Where the lane's four pairs lie.
+template <int D>
+__device__ __forceinline__ void place_eight(int style, int n_rot, int& ea, int& eb) {
+  const int p = (threadIdx.x & (D / 8 - 1)) * 4, half = n_rot >> 1;
+  if (style == FA_ROPE_PAIRS) ea = 2 * p, eb = ea + 4;
+  else if (p < half) ea = p, eb = p + half;
+  else ea = n_rot + (p - half), eb = ea + (D - n_rot) / 2;
+}
+// Sum of squares of a head that D / 8 lanes hold so.  The order of the sum is part of the result: whoever
+// normalises a head takes it from here, so that equal heads give equal bits.
+template <int D>
+__device__ __forceinline__ float square_sum(const float2 (&x)[4]) {
+  float2 q = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) q = __ffma2_rn(x[i], x[i], q);
+  return group_sum<D / 8>(q.x + q.y);
+}
+
 // 1 / sqrt(v): the hardware approximation and one Newton step (it alone is off by up to two units,
 // and the whole head is scaled by it)
 __device__ __forceinline__ float inv_rms(float sum, float inv_n, float eps) {
