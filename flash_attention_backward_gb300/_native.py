@@ -49,6 +49,23 @@ class fa_paged_cache(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("k_type", "v_type", "num_pages", "page_size", "B", "max_pages", "Hkv", "D", "Dv")]
 
 
+class fa_rope_axes(ctypes.Structure):
+    """struct fa_rope_axes of fa_paged_ext.h."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("pos_stride", ctypes.c_int64), ("n_rot", ctypes.c_int32),
+                ("style", ctypes.c_int32), ("n_axes", ctypes.c_int32)]
+
+
+class fa_page_lists(ctypes.Structure):
+    """struct fa_page_lists of fa_paged_ext.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("page_table", "seq_lens", "free_pages", "num_free")] + [
+        (n, ctypes.c_int32) for n in ("num_pages", "page_size", "B", "max_pages")]
+
+
+class fa_page_bounds_pool(ctypes.Structure):
+    """struct fa_page_bounds_pool of fa_paged_ext.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 class NativeLibraryMissing(RuntimeError):
     """libfa_back.so is not built or cannot be loaded; there is no fallback path."""
 
@@ -129,6 +146,25 @@ def lib():
     L.fa_paged_decode_workspace_size.argtypes = [P(fa_paged_cache), i]
     L.fa_paged_decode.restype = i
     L.fa_paged_decode.argtypes = [vp, i, i64, i64, P(fa_paged_cache), vp, i, f, vp, f, vp, vp, vp, vp, sz, vp]
+    L.fa_qk_norm_rope_axes.restype = i
+    L.fa_qk_norm_rope_axes.argtypes = [vp, vp, i, P(fa_qk_views), vp, vp, f, vp, P(fa_rope_axes), i, i, i, i, vp, vp, i, vp]
+    L.fa_qk_norm_rope_axes_backward.restype = i
+    L.fa_qk_norm_rope_axes_backward.argtypes = [vp, vp, i, vp, vp, i, P(fa_qk_views), vp, vp, f, vp, P(fa_rope_axes), i, i, i,
+                                                i, vp, vp, vp, vp, vp, sz, vp]
+    L.fa_cache_append_axes.restype = i
+    L.fa_cache_append_axes.argtypes = [vp, vp, i, P(fa_kv_views), P(fa_paged_cache), vp, vp, i, vp, f, vp, P(fa_rope_axes), vp]
+    L.fa_pages_extend.restype = i
+    L.fa_pages_extend.argtypes = [P(fa_page_lists), vp, i, vp, vp, vp, vp, vp, vp]
+    L.fa_pages_trim.restype = i
+    L.fa_pages_trim.argtypes = [P(fa_page_lists), vp, vp]
+    L.fa_page_bounds.restype = i
+    L.fa_page_bounds.argtypes = [P(fa_paged_cache), P(fa_page_bounds_pool), vp, vp, vp]
+    L.fa_page_select_workspace_size.restype = sz
+    L.fa_page_select_workspace_size.argtypes = [P(fa_paged_cache), i, i]
+    L.fa_page_select.restype = i
+    L.fa_page_select.argtypes = [vp, i, i64, i64, P(fa_paged_cache), P(fa_page_bounds_pool), vp, i, f, vp, i, i, i, vp, vp, sz, vp]
+    L.fa_paged_decode_pages.restype = i
+    L.fa_paged_decode_pages.argtypes = [vp, i, i64, i64, P(fa_paged_cache), vp, vp, i, i, f, vp, f, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -297,3 +333,48 @@ def fa_paged_decode(q, act, q_row, q_head, cache, seq_lens, H, scale, alibi_slop
                     workspace_bytes, stream) -> int:
     return (_lib or lib()).fa_paged_decode(q, act, q_row, q_head, cache, seq_lens, H, scale, alibi_slopes, softcap,
                                            sinks, O, lse, workspace, workspace_bytes, stream)
+
+
+# ---- fa_paged_ext.h
+
+def fa_qk_norm_rope_axes(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, q_out, k_out, y_type, stream) -> int:
+    return (_lib or lib()).fa_qk_norm_rope_axes(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, q_out, k_out,
+                                                y_type, stream)
+
+
+def fa_qk_norm_rope_axes_backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, dq, dk, dwq,
+                                  dwk, workspace, workspace_bytes, stream) -> int:
+    return (_lib or lib()).fa_qk_norm_rope_axes_backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, rope, N, H,
+                                                         Hkv, D, dq, dk, dwq, dwk, workspace, workspace_bytes, stream)
+
+
+def fa_cache_append_axes(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, rope_pos, rope, stream) -> int:
+    return (_lib or lib()).fa_cache_append_axes(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, rope_pos, rope, stream)
+
+
+def fa_pages_extend(lists, new_tokens, T, starts, first, seq, pos, row, stream) -> int:
+    return (_lib or lib()).fa_pages_extend(lists, new_tokens, T, starts, first, seq, pos, row, stream)
+
+
+def fa_pages_trim(lists, keep, stream) -> int:
+    return (_lib or lib()).fa_pages_trim(lists, keep, stream)
+
+
+def fa_page_bounds(cache, bounds, first, seq_lens, stream) -> int:
+    return (_lib or lib()).fa_page_bounds(cache, bounds, first, seq_lens, stream)
+
+
+def fa_page_select_workspace_size(cache, H: int, K: int) -> int:
+    return (_lib or lib()).fa_page_select_workspace_size(cache, H, K)
+
+
+def fa_page_select(q, act, q_row, q_head, cache, bounds, seq_lens, H, scale, alibi_slopes, K, first, last, pages, workspace,
+                   workspace_bytes, stream) -> int:
+    return (_lib or lib()).fa_page_select(q, act, q_row, q_head, cache, bounds, seq_lens, H, scale, alibi_slopes, K, first,
+                                          last, pages, workspace, workspace_bytes, stream)
+
+
+def fa_paged_decode_pages(q, act, q_row, q_head, cache, seq_lens, pages, K, H, scale, alibi_slopes, softcap, sinks, O, lse,
+                          workspace, workspace_bytes, stream) -> int:
+    return (_lib or lib()).fa_paged_decode_pages(q, act, q_row, q_head, cache, seq_lens, pages, K, H, scale, alibi_slopes,
+                                                 softcap, sinks, O, lse, workspace, workspace_bytes, stream)

@@ -24,11 +24,11 @@ fa_status check_cache(const fa_paged_cache* c, Cache* out) {
   if (((long long)c->page_size * c->Hkv * rbk) % 16 || ((long long)c->page_size * c->Hkv * rbv) % 16) return FA_ERR_ALIGN;
   if ((c->num_pages > 0 && (!c->k || !c->v)) || (c->B > 0 && c->max_pages > 0 && !c->page_table)) return FA_ERR_NULL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4)) return FA_ERR_ALIGN;
-  int lg = 0;
-  while ((1LL << lg) < c->page_size) ++lg;
-  const uint32_t mul = (uint32_t)(((1ULL << (30 + lg)) + c->page_size - 1) / c->page_size);
+  uint32_t mul;
+  int shift;
+  page_divisor(c->page_size, &mul, &shift);
   *out = Cache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->page_table, c->k_type, c->v_type,
-               c->num_pages, c->page_size, c->B, c->max_pages, c->Hkv, c->D, c->Dv, (int)rbk, (int)rbv, nullptr, mul, 30 + lg};
+               c->num_pages, c->page_size, c->B, c->max_pages, c->Hkv, c->D, c->Dv, (int)rbk, (int)rbv, nullptr, mul, shift};
   return FA_OK;
 }
 
@@ -211,6 +211,8 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
   if (apart) place_eight<D>(FA_ROPE_HALVES, a.rope.n_rot, ea, eb);
   float w[8];
   if (norm) load8(a.wk + e0, false, w);
+  PairPos<D> axes;
+  if (turns) axes.look_up(a.rope);
   const unsigned items = (unsigned)a.T * a.nchunk, step = gridDim.x * 8;
   for (unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5); item < items; item += step) {
     const int t = item / (unsigned)a.nchunk, h0 = (int)(item - (unsigned)t * a.nchunk) * a.HC;
@@ -230,7 +232,11 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
     if (cell < 0) continue;
     uint8_t* row = (IS_K ? a.c.k : a.c.v) + (cell * a.c.Hkv + h0 + grp) * rb;
     Turn8<D> turn;
-    if (turns) turn.set(a.rope, pos, e0);
+    if (turns) {
+      int at[D / 64];
+      axes.at(a.rope, t, pos, at);
+      turn.set(a.rope, at, e0);
+    }
 #pragma unroll 1
     for (;;) {
       float x[8], r = 1.f;
@@ -402,9 +408,10 @@ static fa_status row_args(const fa_paged_cache* cache, const int32_t* seq, const
   return FA_OK;
 }
 
-extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, const fa_kv_views* views,
-                                     const fa_paged_cache* cache, const int32_t* seq, const int32_t* pos, int T,
-                                     const float* k_norm, float eps, const fa_rope* rope, void* stream) {
+// rope: by the rows' positions; axes: by rope_pos
+static fa_status append(const void* k, const void* v, int x_type, const fa_kv_views* views, const fa_paged_cache* cache,
+                        const int32_t* seq, const int32_t* pos, int T, const float* k_norm, float eps, const fa_rope* rope,
+                        const int32_t* rope_pos, const fa_rope_axes* axes, void* stream) {
   RowArgs a;
   fa_status rc = row_args(cache, seq, pos, T, &a);
   if (rc != FA_OK) return rc;
@@ -416,7 +423,7 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
   if (T > 0 && (!k || !v)) return FA_ERR_NULL;
   const int es = act_bytes(x_type);
   if (!aligned(k, es) || !aligned(v, es) || !aligned(k_norm, 4)) return FA_ERR_ALIGN;
-  if ((rc = check_rope(rope, a.c.D, pos, T, &a.rope)) != FA_OK) return rc;
+  if ((rc = check_rope(rope, axes, a.c.D, axes ? rope_pos : pos, T, &a.rope)) != FA_OK) return rc;
   int nsm = 0;
   if ((rc = fab_device(&nsm, &a.c.err)) != FA_OK) return rc;
   if (T == 0) return FA_OK;
@@ -443,6 +450,18 @@ extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, c
                              : x_type == FA_ACT_F16 ? pick_append<__half>(a.c.D, a.c.Dv)
                                                     : pick_append<__nv_bfloat16>(a.c.D, a.c.Dv);
   return launch_next(k_append, grid, dim3(256), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" fa_status fa_cache_append(const void* k, const void* v, int x_type, const fa_kv_views* views,
+                                     const fa_paged_cache* cache, const int32_t* seq, const int32_t* pos, int T,
+                                     const float* k_norm, float eps, const fa_rope* rope, void* stream) {
+  return append(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, rope, nullptr, nullptr, stream);
+}
+extern "C" fa_status fa_cache_append_axes(const void* k, const void* v, int x_type, const fa_kv_views* views,
+                                          const fa_paged_cache* cache, const int32_t* seq, const int32_t* pos, int T,
+                                          const float* k_norm, float eps, const int32_t* rope_pos,
+                                          const fa_rope_axes* rope, void* stream) {
+  return append(k, v, x_type, views, cache, seq, pos, T, k_norm, eps, nullptr, rope_pos, rope, stream);
 }
 
 extern "C" fa_status fa_cache_read(const fa_paged_cache* cache, const int32_t* seq, const int32_t* pos, int T,

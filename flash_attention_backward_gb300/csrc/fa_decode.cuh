@@ -474,6 +474,8 @@ struct DecodeArgs {
   int act;
   long long q_row, q_head;
   const int32_t* lens;
+  const int32_t* sel;  // [B][Hkv][K]: the pages that count (fa_paged_decode_pages()), or NULL: all
+  int K;
   int H, G, HG, chunks;  // query heads, heads of a group, (KV head, chunk of 8 heads) pairs, chunks of a group
   float scale, softcap;
   float lift;   // weight_lift() of the value type
@@ -545,10 +547,19 @@ __device__ __forceinline__ void act_store(void* p, int act, long long i, float x
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
 }
 
-// Keys of sequence b: its length, 0 for padding, at most the table's capacity
-__device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
+// Length of sequence b: 0 for padding, at most the table's capacity
+__device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) {
   const int L = a.lens[b];
   return min(max(L, 0), a.c.max_pages * a.c.page_size);
+}
+__device__ __forceinline__ int pages_of(const Cache& c, int len) {
+  return len > 0 ? (int)((uint64_t)(len - 1) * c.page_mul >> c.page_shift) + 1 : 0;
+}
+// Keys of sequence b: its length; with selected pages the keys of as many of them as there can be, the places of
+// keys that are not there among them (they are masked)
+__device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
+  const int L = seq_len(a, b);
+  return a.sel ? min(a.K, pages_of(a.c, L)) * a.c.page_size : L;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
 
@@ -720,6 +731,20 @@ static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float sl
                      fmaf(slope, (float)(d + 9), x.w));
 }
 
+// The same where the keys are those of selected pages, whose positions the list says (places j, j + 1, j + 8, j + 9 of
+// its keys; those behind its end are masked, whatever they get).
+static __device__ __noinline__ float4 cap_and_bias_sel(float4 x, float cap, float slope, const Cache& c, const int32_t* sel, int K, int j, int L) {
+  float4 y = cap_and_bias(x, cap, 0.f, 0);
+  float far[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = j + (i & 1) + 8 * (i >> 1), p = (int)((uint64_t)at * c.page_mul >> c.page_shift);
+    far[i] = (float)(sel[min(p, K - 1)] * c.page_size + (at - p * c.page_size) - (L - 1));
+  }
+  y.x = fmaf(slope, far[0], y.x), y.y = fmaf(slope, far[1], y.y), y.z = fmaf(slope, far[2], y.z), y.w = fmaf(slope, far[3], y.w);
+  return y;
+}
+
 // One item (blockIdx.x / HG): a sequence, or a part of a long one, for one (KV head, chunk of eight query
 // heads) (blockIdx.x % HG).  Consecutive CTAs take the same keys of the different heads, so a page's
 // neighbouring rows are read at the same time.  Each warp takes every NW-th tile of 16 keys with a ring, a
@@ -812,37 +837,50 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   const int j0 = 16 * (int)(n_all * item.z / item.y);  // the item's keys [j0, j1) and tiles
   const int j1 = min(keys, 16 * (int)(n_all * (item.z + 1) / item.y)), ntile = tiles_of(j1 - j0);
   const bool whole = item.y == 1;
+  const int len = a.sel ? seq_len(a, b) : keys;
+  const int32_t* sel = a.sel ? a.sel + ((long long)b * a.c.Hkv + hk) * a.K : nullptr;
 
   // ---- rows of a tile: key `lane` & 15 a lane.  Boxes of rows (16 or 8 in one page) go by the tensor maps,
   // else each row is copied by itself.  The first rows of the warp's next 32 boxes are looked up at once, a
   // box a lane; single rows a tile at a time.
   const int boxes = a.box == 8 ? 2 : 1, per_batch = 32 / boxes;  // boxes of a tile, tiles of a lookup
-  auto lookup = [&](int j) {  // row of the pool of key j, -1 where there is none
+  auto lookup = [&](int j, int& there) {  // row of the pool of key j, -1 where there is none; keys from it on in its page
     if (j >= j1) return -1;
-    const int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
+    int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
+    const int in = j - p * a.c.page_size;
+    if (sel) {
+      p = sel[p];
+      if (p < 0 || p >= pages_of(a.c, len)) return -1;
+      there = len - (p * a.c.page_size + in);
+      if (there <= 0) return -1;
+    }
     const int page = a.c.table[(long long)b * a.c.max_pages + p];
-    if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + (j - p * a.c.page_size);
+    if (page >= 0 && page < a.c.num_pages) return page * a.c.page_size + in;
     report_page(a.c.err);
     return -1;
   };
   int found = -1, found_at = -1000;  // the lookup's rows, and the warp's turn that it starts with
-  auto row_of = [&](int turn) {  // of the warp's turn-th tile
-    if (!a.box) return lookup(j0 + 16 * (warp + NW * turn) + (lane & 15));
+  int found_there = 0;               // of selected pages
+  auto row_of = [&](int turn, int& there) {  // of the warp's turn-th tile
+    if (!a.box) return lookup(j0 + 16 * (warp + NW * turn) + (lane & 15), there);
     if (turn - found_at >= per_batch) {
       const int l = a.box == 8 ? lane >> 1 : lane;
-      found = lookup(j0 + 16 * (warp + NW * (turn + l)) + (a.box == 8 ? 8 * (lane & 1) : 0));
+      found = lookup(j0 + 16 * (warp + NW * (turn + l)) + (a.box == 8 ? 8 * (lane & 1) : 0), found_there);
       found_at = turn;
     }
-    return __shfl_sync(kFull, found, (turn - found_at) * boxes + (a.box == 8 ? (lane >> 3) & 1 : 0));
+    const int from = (turn - found_at) * boxes + (a.box == 8 ? (lane >> 3) & 1 : 0);
+    if (sel) there = __shfl_sync(kFull, found_there, from);
+    return __shfl_sync(kFull, found, from);
   };
   // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way, mask or places not the usual ones
   uint32_t phases = 0, armed = 0, patched = 0;
-  auto fetch = [&](int kv, int slot, int row, int tile) {
+  auto fetch = [&](int kv, int slot, int row, int there, int tile) {
     const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), bar = sl + 128 + 8 * kv;
     const uint32_t dst = ring + slot * C.stage + (kv ? 16 * PK : 0);
     const int pitch = kv ? PV : PK;
     armed |= 1u << (4 * kv + slot);
-    const int n = min(16, j1 - (j0 + tile * 16));  // the rows behind them are not used
+    int n = min(16, j1 - (j0 + tile * 16));  // the rows behind them are not used
+    if (sel) n = a.box == 16 ? min(16, there) : min(8, there) + (lane & 8);  // (a.box == 8: of the lane's box)
     const CUtensorMap* map = kv ? &map_v : &map_k;
     const int x = kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK);
     // A slot's mask and its value rows' places are rewritten for a tile with rows missing, and after one.
@@ -899,8 +937,9 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     for (int i = 0, sl = slot; i < SLOTS; ++i) {
       const int tile = warp + i * NW;
       if (tile < ntile) {
-        const int row = row_of(i);
-        fetch(0, sl, row, tile), fetch(1, sl, row, tile);
+        int there = 0;
+        const int row = row_of(i, there);
+        fetch(0, sl, row, there, tile), fetch(1, sl, row, there, tile);
       }
       if (++sl == SLOTS) sl = 0;
     }
@@ -956,7 +995,8 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     float m = -INFINITY, l = 0.f;  // head g: the maximum that weights refer to (log2), this lane's sum
     int next = warp + SLOTS * NW, turn = SLOTS;
     for (int tile = warp; tile < ntile; tile += NW, next += NW, ++turn) {
-      const int row = next < ntile ? row_of(turn) : -1;
+      int there = 0;
+      const int row = next < ntile ? row_of(turn, there) : -1;
       const uint32_t sl = ctl + slot * (uint32_t)sizeof(Slot), qa = qf + lane * 16;
       dead = !arrived(0, slot);
       if (dead) break;
@@ -968,12 +1008,13 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       transpose_scores(s);
       const uint32_t ok = lds_u32(sl + 144);
       __syncwarp();
-      if (next < ntile) fetch(0, slot, row, next);
+      if (next < ntile) fetch(0, slot, row, there, next);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] *= qscale;
       if (ext) {
-        const float4 x = cap_and_bias(make_float4(s[0], s[1], s[2], s[3]), a.softcap, slope,
-                                      j0 + tile * 16 + 2 * t - (keys - 1));
+        const float4 y = make_float4(s[0], s[1], s[2], s[3]);
+        const float4 x = sel && a.alibi ? cap_and_bias_sel(y, a.softcap, slope, a.c, sel, a.K, j0 + tile * 16 + 2 * t, len)
+                                        : cap_and_bias(y, a.softcap, slope, j0 + tile * 16 + 2 * t - (keys - 1));
         s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
       }
 #pragma unroll
@@ -1011,7 +1052,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       else if (VT == FA_Q4_0) values_q4<DV, 2>(o, p, sl + 64, lane);
       else values_f32<DV>(o, p, sl + 64, lane);
       __syncwarp();
-      if (next < ntile) fetch(1, slot, row, next);
+      if (next < ntile) fetch(1, slot, row, there, next);
       if (++slot == SLOTS) slot = 0;
     }
     if (dead) {  // let the copies in flight land: nothing more is issued

@@ -7,15 +7,20 @@
 
 namespace fap {
 
-fa_status check_rope(const fa_rope* r, int D, const int32_t* pos, int N, Rope* out) {
-  *out = Rope{nullptr, 0, FA_ROPE_HALVES};
-  if (!r || !r->freqs || r->n_rot == 0) return FA_OK;
-  if (r->style != FA_ROPE_PAIRS && r->style != FA_ROPE_HALVES) return FA_ERR_SHAPE;
-  if (r->n_rot < 0 || (r->n_rot & 1) || r->n_rot > D) return FA_ERR_SHAPE;
-  if (r->style == FA_ROPE_HALVES && r->n_rot % 16) return FA_ERR_UNSUPPORTED;
-  if (N > 0 && !pos) return FA_ERR_NULL;
-  if (!aligned(r->freqs, 8) || !aligned(pos, 4)) return FA_ERR_ALIGN;
-  *out = Rope{r->freqs, r->n_rot, r->style};
+fa_status check_rope(const fa_rope* r, const fa_rope_axes* axes, int D, const int32_t* pos, int N, Rope* out) {
+  *out = Rope{nullptr, 0, FA_ROPE_HALVES, nullptr, nullptr, 0, 1};
+  fa_rope one = {};
+  if (axes) one.freqs = axes->freqs, one.n_rot = axes->n_rot, one.style = axes->style;
+  else if (r) one = *r;
+  if (!one.freqs || one.n_rot == 0) return FA_OK;
+  if (one.style != FA_ROPE_PAIRS && one.style != FA_ROPE_HALVES) return FA_ERR_SHAPE;
+  if (one.n_rot < 0 || (one.n_rot & 1) || one.n_rot > D) return FA_ERR_SHAPE;
+  if (axes && (axes->n_axes < 1 || axes->n_axes > 8 || axes->pos_stride < 0)) return FA_ERR_SHAPE;
+  if (one.style == FA_ROPE_HALVES && one.n_rot % 16) return FA_ERR_UNSUPPORTED;
+  if ((N > 0 && !pos) || (axes && !axes->axis)) return FA_ERR_NULL;
+  if (!aligned(one.freqs, 8) || !aligned(pos, 4)) return FA_ERR_ALIGN;
+  *out = Rope{one.freqs, one.n_rot, one.style, pos, nullptr, 0, 1};
+  if (axes) out->axis = axes->axis, out->stride = axes->pos_stride, out->n_axes = axes->n_axes;
   return FA_OK;
 }
 
@@ -45,8 +50,8 @@ static bool rows_on_16(const void* p, long long row, long long head, int es) {
 
 // Checks what both directions take; fills everything but the outputs and the gradients.
 static fa_status norm_args(const void* q, const void* k, int x_type, const fa_qk_views* vw, const float* wq,
-                           const float* wk, float eps, const int32_t* pos, const fa_rope* rope, int N, int H, int Hkv,
-                           int D, int y_type, bool back, NormArgs* a) {
+                           const float* wk, float eps, const int32_t* pos, const fa_rope* rope, const fa_rope_axes* axes,
+                           int N, int H, int Hkv, int D, int y_type, bool back, NormArgs* a) {
   if (!act_type(x_type) || !act_type(y_type)) return FA_ERR_TYPE;
   if (N < 0 || H < 1 || Hkv < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return FA_ERR_SHAPE;
   if (!head_size(D)) return FA_ERR_UNSUPPORTED;
@@ -60,13 +65,13 @@ static fa_status norm_args(const void* q, const void* k, int x_type, const fa_qk
   if (!aligned(q, es) || !aligned(k, es) || !aligned(wq, 4) || !aligned(wk, 4)) return FA_ERR_ALIGN;
   NormArgs z = {};
   *a = z;
-  const fa_status rc = check_rope(rope, D, pos, N, &a->rope);
+  const fa_status rc = check_rope(rope, axes, D, pos, N, &a->rope);
   if (rc != FA_OK) return rc;
   NormSide& sq = a->side[0];
   NormSide& sk = a->side[1];
   sq.x = q, sq.row = v.q_row, sq.head = v.q_head, sq.w = wq, sq.H = H;
   sk.x = k, sk.row = v.k_row, sk.head = v.k_head, sk.w = wk, sk.H = Hkv;
-  a->eps = eps, a->pos = pos, a->N = N;
+  a->eps = eps, a->N = N;
   a->vec = rows_on_16(q, v.q_row, v.q_head, es) && (Hkv == 0 || rows_on_16(k, v.k_row, v.k_head, es));
   return FA_OK;
 }
@@ -107,12 +112,12 @@ extern "C" fa_status fa_rope_frequencies(int n_rot, double base, double scale, c
   return FA_OK;
 }
 
-extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, const fa_qk_views* views,
-                                     const float* wq, const float* wk, float eps, const int32_t* pos,
-                                     const fa_rope* rope, int N, int H, int Hkv, int D, void* q_out, void* k_out,
-                                     int y_type, void* stream) {
+// (rope or axes, or neither)
+static fa_status forward(const void* q, const void* k, int x_type, const fa_qk_views* views, const float* wq, const float* wk,
+                         float eps, const int32_t* pos, const fa_rope* rope, const fa_rope_axes* axes, int N, int H, int Hkv,
+                         int D, void* q_out, void* k_out, int y_type, void* stream) {
   NormArgs a;
-  fa_status rc = norm_args(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, y_type, false, &a);
+  fa_status rc = norm_args(q, k, x_type, views, wq, wk, eps, pos, rope, axes, N, H, Hkv, D, y_type, false, &a);
   if (rc != FA_OK) return rc;
   if (N > 0 && (!q_out || (Hkv > 0 && !k_out))) return FA_ERR_NULL;
   if (!aligned(q_out, 16) || !aligned(k_out, 16)) return FA_ERR_ALIGN;
@@ -132,6 +137,19 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, c
              : FA_ERR_CUDA;
 }
 
+extern "C" fa_status fa_qk_norm_rope(const void* q, const void* k, int x_type, const fa_qk_views* views,
+                                     const float* wq, const float* wk, float eps, const int32_t* pos,
+                                     const fa_rope* rope, int N, int H, int Hkv, int D, void* q_out, void* k_out,
+                                     int y_type, void* stream) {
+  return forward(q, k, x_type, views, wq, wk, eps, pos, rope, nullptr, N, H, Hkv, D, q_out, k_out, y_type, stream);
+}
+extern "C" fa_status fa_qk_norm_rope_axes(const void* q, const void* k, int x_type, const fa_qk_views* views,
+                                          const float* wq, const float* wk, float eps, const int32_t* pos,
+                                          const fa_rope_axes* rope, int N, int H, int Hkv, int D, void* q_out,
+                                          void* k_out, int y_type, void* stream) {
+  return forward(q, k, x_type, views, wq, wk, eps, pos, nullptr, rope, N, H, Hkv, D, q_out, k_out, y_type, stream);
+}
+
 extern "C" size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv, int D) {
   if (N < 0 || H < 1 || Hkv < 0 || !head_size(D)) return 0;
   int nsm = 0;
@@ -139,13 +157,12 @@ extern "C" size_t fa_qk_norm_rope_backward_workspace_size(int N, int H, int Hkv,
   return (size_t)back_ctas(nsm) * D * sizeof(float);
 }
 
-extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, int y_type, const void* q, const void* k,
-                                              int x_type, const fa_qk_views* views, const float* wq, const float* wk,
-                                              float eps, const int32_t* pos, const fa_rope* rope, int N, int H,
-                                              int Hkv, int D, void* dq, void* dk, float* dwq, float* dwk,
-                                              void* workspace, size_t workspace_bytes, void* stream) {
+static fa_status backward(const void* gq, const void* gk, int y_type, const void* q, const void* k, int x_type,
+                          const fa_qk_views* views, const float* wq, const float* wk, float eps, const int32_t* pos,
+                          const fa_rope* rope, const fa_rope_axes* axes, int N, int H, int Hkv, int D, void* dq, void* dk,
+                          float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream) {
   NormArgs a;
-  fa_status rc = norm_args(q, k, x_type, views, wq, wk, eps, pos, rope, N, H, Hkv, D, y_type, true, &a);
+  fa_status rc = norm_args(q, k, x_type, views, wq, wk, eps, pos, rope, axes, N, H, Hkv, D, y_type, true, &a);
   if (rc != FA_OK) return rc;
   if (N > 0 && (!gq || !dq || (Hkv > 0 && (!gk || !dk)))) return FA_ERR_NULL;
   if (!aligned(gq, 16) || !aligned(gk, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dwq, 4) || !aligned(dwk, 4))
@@ -177,4 +194,22 @@ extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, in
     return FA_ERR_CUDA;
   if (wk && !Hkv && dwk) cudaMemsetAsync(dwk, 0, D * sizeof(float), s);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" fa_status fa_qk_norm_rope_backward(const void* gq, const void* gk, int y_type, const void* q, const void* k,
+                                              int x_type, const fa_qk_views* views, const float* wq, const float* wk,
+                                              float eps, const int32_t* pos, const fa_rope* rope, int N, int H,
+                                              int Hkv, int D, void* dq, void* dk, float* dwq, float* dwk,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+  return backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, rope, nullptr, N, H, Hkv, D, dq, dk, dwq, dwk, workspace,
+                  workspace_bytes, stream);
+}
+extern "C" fa_status fa_qk_norm_rope_axes_backward(const void* gq, const void* gk, int y_type, const void* q,
+                                                   const void* k, int x_type, const fa_qk_views* views,
+                                                   const float* wq, const float* wk, float eps, const int32_t* pos,
+                                                   const fa_rope_axes* rope, int N, int H, int Hkv, int D, void* dq,
+                                                   void* dk, float* dwq, float* dwk, void* workspace,
+                                                   size_t workspace_bytes, void* stream) {
+  return backward(gq, gk, y_type, q, k, x_type, views, wq, wk, eps, pos, nullptr, rope, N, H, Hkv, D, dq, dk, dwq, dwk, workspace,
+                  workspace_bytes, stream);
 }

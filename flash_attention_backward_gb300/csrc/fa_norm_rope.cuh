@@ -39,7 +39,6 @@ struct NormArgs {
   int HC, nchunk;      // forward: heads (queries', then keys') of one token that a warp takes, chunks of a token
   int ctas_q;          // backward: CTAs 0 .. ctas_q - 1 take queries, the rest keys
   float eps;
-  const int32_t* pos;
   Rope rope;
   int N;
   bool vec;            // both start every head of x on 16 bytes (or have none)
@@ -71,6 +70,7 @@ struct Lane {
   bool norm;
   float2 w[4];
   float2 c[2], s[2], ns[2];  // cos, sin, -sin of pairs (0, 1) and (2, 3)
+  static constexpr int P = D / 64;
 
   __device__ __forceinline__ void place(const Rope& r) {
     const int p = (threadIdx.x & (D / 8 - 1)) * 4;
@@ -85,17 +85,16 @@ struct Lane {
       unpack_eight(o, w);
     }
   }
-  // The factors at a position (sin_cos_turn); sign -1 turns back (the transpose).
-  // The token's D / 2 pairs are shared out over the warp's lanes, D / 64 neighbouring ones each.
-  __device__ __forceinline__ void turn(const Rope& r, int pos, float sign) {
-    constexpr int P = D / 64;
+  // The factors (sin_cos_turn) at the positions of the lane's share of the token's pairs (PairPos); sign -1 turns
+  // back (the transpose).
+  __device__ __forceinline__ void turn(const Rope& r, const int (&pos)[P], float sign) {
     const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
     float cs[P], sn[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       cs[i] = 1.f, sn[i] = 0.f;
       if (lane * P + i < half) {
-        sin_cos_turn(r.freqs[lane * P + i], pos, &sn[i], &cs[i]);
+        sin_cos_turn(r.freqs[lane * P + i], pos[i], &sn[i], &cs[i]);
         sn[i] *= sign;
       }
     }
@@ -190,6 +189,8 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
     lanes[k].place(a.rope);
     if (ON) lanes[k].weights(a.side[k].w);
   }
+  PairPos<D> axes;
+  axes.look_up(a.rope);
   for (unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5); item < items; item += gridDim.x * 8u) {
     const int n = item / (unsigned)a.nchunk, c0 = (int)(item - (unsigned)n * a.nchunk) * a.HC;
     bool turned = false;
@@ -212,7 +213,11 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
       };
       fetch();
       if (!ON) ln.weights(sd.w);
-      if (!turned) lanes[0].turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, 1.f);
+      if (!turned) {
+        int pos[D / 64];
+        axes.at(a.rope, n, a.rope.n_rot ? a.rope.pos[n] : 0, pos);
+        lanes[0].turn(a.rope, pos, 1.f);
+      }
       turned = true;
       if (ON && k) ln.turned_as(lanes[0]);
       for (;;) {
@@ -342,14 +347,20 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
     if (fetched < last) fetch(i);
   int slot = 0, token = -1;
   uint32_t phase = 0;
-  auto pos_of = [&](int t) { return a.rope.n_rot && t < a.N ? a.pos[t] : 0; };
-  int pos = pos_of(n);
+  PairPos<D> axes;
+  axes.look_up(a.rope);
+  int pos[D / 64] = {};
+  auto pos_of = [&](int t) {
+    if (a.rope.n_rot && t < a.N) axes.at(a.rope, t, a.rope.pos[t], pos);
+  };
+  pos_of(n);
   unsigned run = dw_run(last - first);
   bool put = false;  // sums lie in `red` already
   for (unsigned item = first; item < last; ++item) {
     if (n != token) {
       ln.turn(a.rope, pos, -1.f);
-      token = n, pos = pos_of(n + 1);  // the next token's, in time
+      token = n;
+      pos_of(n + 1);  // the next token's, in time
     }
     const bool came = a.wait_ns > 0 && fab::mbar_wait_bounded(&s_bar[warp][slot], phase, a.wait_ns);
     if (!__all_sync(kFull, came)) {  // let the copies in flight land, then give up
@@ -413,10 +424,14 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_a
   ln.weights(sd.w);
   unsigned run = dw_run(items / (ctas * kBackWarps));
   bool put = false;
+  PairPos<D> axes;
+  axes.look_up(a.rope);
   for (unsigned item = cta * kBackWarps + warp; item < items; item += ctas * kBackWarps) {
     const int n = item / (unsigned)sd.nchunk, h0 = (int)(item - (unsigned)n * sd.nchunk) * HC, cnt = min(sd.H - h0, HC);
     const long long at = ((long long)n * sd.H + h0) * D;
-    ln.turn(a.rope, a.rope.n_rot ? a.pos[n] : 0, -1.f);
+    int pos[D / 64];
+    axes.at(a.rope, n, a.rope.n_rot ? a.rope.pos[n] : 0, pos);
+    ln.turn(a.rope, pos, -1.f);
 #pragma unroll 1
     for (int k = 0; k < cnt; k += GW) {
       const int hh = min(k + grp, cnt - 1);

@@ -8,7 +8,7 @@
 
 #include <atomic>
 
-#include "../../include/fa_paged.h"
+#include "../../include/fa_paged_ext.h"
 #include "fa_internal.h"
 
 namespace fap {
@@ -85,6 +85,33 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 struct Rope {
   const uint64_t* freqs;
   int n_rot, style;
+  const int32_t* pos;   // [n_axes][tokens], an axis every `stride`
+  const uint8_t* axis;  // [n_rot / 2], or NULL: one axis
+  long long stride;
+  int n_axes;
+};
+
+// A warp's lanes share out a token's D / 2 pairs, D / 64 neighbouring ones each: the axes of a lane's pairs, a byte
+// each (looked up once; a token then costs a load a pair beside the one that all pairs share without axes), and
+// their positions.
+template <int D>
+struct PairPos {
+  static constexpr int P = D / 64;
+  uint32_t axes = 0;
+
+  __device__ __forceinline__ void look_up(const Rope& r) {
+    if (!r.axis) return;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int pair = (int)(threadIdx.x & 31) * P + i;
+      if (pair < r.n_rot >> 1) axes |= (uint32_t)min((int)r.axis[pair], r.n_axes - 1) << (8 * i);
+    }
+  }
+  // Of token n; p where there is one axis.
+  __device__ __forceinline__ void at(const Rope& r, long long n, int p, int (&pos)[P]) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) pos[i] = r.axis ? r.pos[(axes >> (8 * i) & 255) * r.stride + n] : p;
+  }
 };
 
 // sin and cos of pos * freq, modulo 2^64 in units of 2^-64 turns: the wrap of the integer product is the
@@ -110,8 +137,8 @@ struct Turn8 {
   int src;  // partner lane (FA_ROPE_HALVES)
   int n;    // the lane's elements that are rotated, its first ones (FA_ROPE_HALVES: all or none)
 
-  // All lanes of the warp take part; pos is the same in all.
-  __device__ __forceinline__ void set(const Rope& r, int pos, int e0) {
+  // All lanes of the warp take part; pos: of the lane's pairs (PairPos).
+  __device__ __forceinline__ void set(const Rope& r, const int (&pos)[D / 64], int e0) {
     constexpr int P = D / 64;
     const int lane = threadIdx.x & 31, half = r.n_rot >> 1;
     src = lane;
@@ -122,7 +149,7 @@ struct Turn8 {
     for (int i = 0; i < P; ++i) {
       cs[i] = 1.f, sn[i] = 0.f;
       const int p = lane * P + i;
-      if (p < half) sin_cos_turn(r.freqs[p], pos, &sn[i], &cs[i]);
+      if (p < half) sin_cos_turn(r.freqs[p], pos[i], &sn[i], &cs[i]);
     }
     const bool in = e0 < r.n_rot;
     if (r.style == FA_ROPE_HALVES) {  // n_rot % 16 == 0: a lane lies in one half
@@ -281,6 +308,12 @@ inline bool allow_smem(const void* k, int bytes, std::atomic<uint64_t>* ready) {
   if (dev < 64) ready->fetch_or(1ull << dev);
   return true;
 }
+// j / page_size = j * mul >> shift for 0 <= j < 2^30
+inline void page_divisor(int page_size, uint32_t* mul, int* shift) {
+  int lg = 0;
+  while ((1LL << lg) < page_size) ++lg;
+  *mul = (uint32_t)(((1ULL << (30 + lg)) + page_size - 1) / page_size), *shift = 30 + lg;
+}
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool head_size(int d) { return d == 64 || d == 128 || d == 256; }
 inline int act_bytes(int t) { return t == FA_ACT_F32 ? 4 : 2; }
@@ -288,6 +321,7 @@ inline bool act_type(int t) { return t >= FA_ACT_F32 && t <= FA_ACT_BF16; }
 
 // The argument checks of a paged cache, and its device form but for `err`.
 fa_status check_cache(const fa_paged_cache* c, Cache* out);
-fa_status check_rope(const fa_rope* r, int D, const int32_t* pos, int N, Rope* out);
+// The checks of a rotation by pos; axes: of several axes (r is not looked at then).
+fa_status check_rope(const fa_rope* r, const fa_rope_axes* axes, int D, const int32_t* pos, int N, Rope* out);
 
 }  // namespace fap

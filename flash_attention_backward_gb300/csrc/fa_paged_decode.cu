@@ -38,7 +38,8 @@ struct DecodePlan {
   bool planned;
 };
 
-static DecodePlan plan_decode(const Cache& c, int H, int nsm) {
+// K: pages of a sequence that count at most
+static DecodePlan plan_decode(const Cache& c, int H, int K, int nsm) {
   DecodePlan p;
   const int G = H / c.Hkv;
   p.chunks = (G + 7) / 8;
@@ -46,7 +47,7 @@ static DecodePlan plan_decode(const Cache& c, int H, int nsm) {
   const int ctas = decode_shape(c.D, c.Dv, c.k_type, c.v_type).ctas;
   p.R = std::max(1, ctas * nsm / p.HG);  // items that run at a time
   // at most R + B (see fa_decode.cuh), and no more than tables of this width can ask for
-  const long long cap = ((long long)c.max_pages * c.page_size + 15) / 16, per = (cap + kMinTiles - 1) / kMinTiles;
+  const long long cap = ((long long)std::min(K, c.max_pages) * c.page_size + 15) / 16, per = (cap + kMinTiles - 1) / kMinTiles;
   p.nitems = (int)std::max(1LL, std::min<long long>(c.B * std::max(per, 1LL), (long long)p.R + c.B));
   p.njobs = per > 1 ? std::min(c.B, p.R) : 0;  // split sequences: none if no sequence can be
   const size_t slots = p.njobs ? std::min(2 * p.R, p.nitems) : 0;
@@ -76,13 +77,13 @@ extern "C" size_t fa_paged_decode_workspace_size(const fa_paged_cache* cache, in
   if (check_cache(cache, &c) != FA_OK || H < 1 || H % c.Hkv) return 0;
   int nsm = 0;
   if (fab_device(&nsm, nullptr) != FA_OK) nsm = 152;
-  return plan_decode(c, H, nsm).bytes;
+  return plan_decode(c, H, c.max_pages, nsm).bytes;
 }
 
-extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,
-                                     const int32_t* seq_lens, int H, float scale, const float* alibi_slopes,
-                                     float softcap, const float* sinks, void* O, float* lse, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
+// pages [B][Hkv][K], or NULL: all of them (K is max_pages then)
+static fa_status decode(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache, const int32_t* seq_lens,
+                        const int32_t* pages, int K, int H, float scale, const float* alibi_slopes, float softcap,
+                        const float* sinks, void* O, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   DecodeArgs a = {};
   fa_status rc = check_cache(cache, &a.c);
   if (rc != FA_OK) return rc;
@@ -96,12 +97,12 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
     return FA_ERR_ALIGN;
   int nsm = 0;
   if ((rc = fab_device(&nsm, &a.c.err)) != FA_OK) return rc;
-  const DecodePlan p = plan_decode(a.c, H, nsm);
+  const DecodePlan p = plan_decode(a.c, H, K, nsm);
   if ((long long)p.nitems * p.HG > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
   if (a.c.B == 0) return FA_OK;
-  a.q = q, a.act = act, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens;
+  a.q = q, a.act = act, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens, a.sel = pages, a.K = K;
   a.H = H, a.G = H / a.c.Hkv, a.HG = p.HG, a.chunks = p.chunks;
   a.scale = scale, a.softcap = softcap, a.alibi = alibi_slopes, a.sinks = sinks, a.O = O, a.lse = lse;
   a.part = static_cast<float*>(workspace);
@@ -119,4 +120,23 @@ extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int6
     return FA_ERR_CUDA;
   const DecodeFn run = a.c.D == 64 ? pick_decode_k<64>(a.c) : a.c.D == 128 ? pick_decode_k<128>(a.c) : pick_decode_k<256>(a.c);
   return run(a, m, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" fa_status fa_paged_decode(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,
+                                     const int32_t* seq_lens, int H, float scale, const float* alibi_slopes,
+                                     float softcap, const float* sinks, void* O, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return decode(q, act, q_row, q_head, cache, seq_lens, nullptr, cache ? cache->max_pages : 0, H, scale, alibi_slopes, softcap, sinks, O,
+                lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" fa_status fa_paged_decode_pages(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,
+                                           const int32_t* seq_lens, const int32_t* pages, int K, int H, float scale,
+                                           const float* alibi_slopes, float softcap, const float* sinks, void* O,
+                                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (K < 1) return FA_ERR_SHAPE;
+  if (!pages && (!cache || cache->B > 0)) return FA_ERR_NULL;
+  if (!aligned(pages, 4)) return FA_ERR_ALIGN;
+  return decode(q, act, q_row, q_head, cache, seq_lens, pages, K, H, scale, alibi_slopes, softcap, sinks, O, lse, workspace,
+                workspace_bytes, stream);
 }

@@ -1,0 +1,492 @@
+// Which pages of a long cache a query should attend over: bounds of each page's keys in 8 bits, a score from
+// them, and the pages with the largest scores.
+//
+// max over a page's keys of q . k is at most sum max(q_i hi_i, q_i lo_i).  In 8 bits that sum is whole
+// numbers, exact in any order, and each block of 32 adds two f32 products and one sum in a fixed tree: the score is
+// the same bits wherever and however it is computed, and so are the pages chosen by it.
+#include <algorithm>
+#include <cmath>
+
+#include "fa_paged.cuh"
+
+namespace fap {
+
+constexpr float kTinyAmax = 1e-30f;
+
+struct BoundArgs {
+  Cache c;
+  int8_t* codes;
+  float* scales;
+  const int32_t *first, *lens;
+  int Z;  // CTAs that share a sequence's pages (of one KV head)
+};
+
+__device__ __forceinline__ int len_of(const Cache& c, const int32_t* lens, int b) {
+  return min(lens[b], c.max_pages * c.page_size);
+}
+__device__ __forceinline__ int page_of(const Cache& c, int j) { return (int)((uint64_t)(uint32_t)j * c.page_mul >> c.page_shift); }
+__device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 0 ? page_of(c, len - 1) + 1 : 0; }
+
+// ------------------------------------------------------------------------------------------------
+// bounds: a lane holds eight components, D / 8 lanes a row; the CTA's lane groups take the page's rows in turn and
+// join their largest and smallest values in the end.
+
+constexpr int kBoundWarps = 4;
+
+__device__ __forceinline__ uint32_t load_u32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+
+// value (u - bias) * d of byte b of w: 32768 + u as f32 by placing the byte, and (32768 + bias) d is exact
+__device__ __forceinline__ float byte_times(uint32_t w, int b, float d, float off) {
+  return fmaf(__uint_as_float(__byte_perm(w, 0x47000000u, 0x7404 | b << 4)), d, off);
+}
+
+template <int TYPE>
+struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
+  uint4 a, b;
+  __device__ __forceinline__ void load(const uint8_t* row, int e0) {
+    if (TYPE == FA_F32) {
+      a = reinterpret_cast<const uint4*>(row)[e0 >> 2], b = reinterpret_cast<const uint4*>(row)[(e0 >> 2) + 1];
+    } else if (TYPE == FA_F16) {
+      a = reinterpret_cast<const uint4*>(row)[e0 >> 3];
+    } else if (TYPE == FA_Q8_0) {  // pairs of blocks are 17 words: the first one's codes start in the middle of one
+      const int blk = e0 >> 5, j = (e0 >> 3) & 3, odd = blk & 1;
+      const uint8_t* p = row + (blk >> 1) * 68 + (odd ? 36 : 0) + 8 * j;
+      const uint32_t w0 = load_u32(p), w1 = load_u32(p + 4), w2 = odd ? 0 : load_u32(p + 8);
+      a.x = odd ? w0 : __byte_perm(w0, w1, 0x5432), a.y = odd ? w1 : __byte_perm(w1, w2, 0x5432);
+      a.z = *reinterpret_cast<const uint16_t*>(row + blk * 34);
+    } else {
+      const int blk = e0 >> 5, j = (e0 >> 3) & 3;
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row + blk * 18);
+      a.x = p[1 + 4 * (j & 1)] | (uint32_t)p[2 + 4 * (j & 1)] << 16, a.y = p[3 + 4 * (j & 1)] | (uint32_t)p[4 + 4 * (j & 1)] << 16;
+      if (j >= 2) a.x >>= 4, a.y >>= 4;
+      a.z = p[0];
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    if (TYPE == FA_F32) {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    } else if (TYPE == FA_F16) {
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+      }
+    } else {
+      const float d = __half2float(__ushort_as_half((unsigned short)a.z));
+      constexpr uint32_t kMask = TYPE == FA_Q8_0 ? 0xffffffffu : 0x0f0f0f0fu, kFlip = TYPE == FA_Q8_0 ? 0x80808080u : 0;
+      // (an infinite scale makes infinities of its block, whose bounds are infinite then)
+      const float off = fabsf(d) < INFINITY ? -(32768.f + (TYPE == FA_Q8_0 ? 128.f : 8.f)) * d : 0.f;
+      const uint32_t w0 = (a.x & kMask) ^ kFlip, w1 = (a.y & kMask) ^ kFlip;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = byte_times(w0, i, d, off), x[4 + i] = byte_times(w1, i, d, off);
+    }
+  }
+};
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kBoundWarps * 32) k_page_bounds(const BoundArgs a) {
+  constexpr int LG = D / 8, GROUPS = kBoundWarps * 32 / LG, U = TYPE == FA_F32 ? 4 : 8;
+  constexpr int RB = TYPE == FA_F32 ? 4 * D : TYPE == FA_F16 ? 2 * D : TYPE == FA_Q8_0 ? D / 32 * 34 : D / 32 * 18;
+  __shared__ float s_hi[kBoundWarps][D], s_lo[kBoundWarps][D];
+  after_last();
+  lets_next();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = (lane & (LG - 1)) * 8, grp = threadIdx.x / LG;
+  const unsigned hk = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv, z = rest % a.Z;
+  const int b = rest / a.Z, L = len_of(a.c, a.lens, b), f = a.first ? a.first[b] : 0;
+  if (f < 0 || f >= L) return;
+  const int n = pages_of(a.c, L);
+  const long long cell = (long long)a.c.Hkv * RB;
+  for (int p = page_of(a.c, f) + z; p < n; p += a.Z) {
+    const int page = a.c.table[(long long)b * a.c.max_pages + p];
+    if (page < 0 || page >= a.c.num_pages) {
+      if (threadIdx.x == 0) report_page(a.c.err);
+      continue;
+    }
+    const int rows = min(a.c.page_size, L - p * a.c.page_size);
+    const uint8_t* row = a.c.k + (long long)page * a.c.page_size * cell + hk * RB;
+    float hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
+    for (int r0 = grp; r0 < rows; r0 += U * GROUPS) {
+      Raw8<TYPE> raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u].load(row + min(r0 + u * GROUPS, rows - 1) * cell, e0);  // (the last row again does nothing)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[8];
+        raw[u].values(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hi[i] = fmaxf(hi[i], x[i]), lo[i] = fminf(lo[i], x[i]);
+      }
+    }
+#pragma unroll
+    for (int o = LG; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], o)), lo[i] = fminf(lo[i], __shfl_xor_sync(kFull, lo[i], o));
+    __syncthreads();  // (the arrays are the last page's until here)
+    if (lane < LG) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_hi[warp][e0 + i] = hi[i], s_lo[warp][e0 + i] = lo[i];
+    }
+    __syncthreads();
+    // a warp a block of 32 components, a lane a component
+    for (int blk = warp; blk < D / 32; blk += kBoundWarps) {
+      const int e = blk * 32 + lane;
+      float top = s_hi[0][e], low = s_lo[0][e];
+#pragma unroll
+      for (int w = 1; w < kBoundWarps; ++w) top = fmaxf(top, s_hi[w][e]), low = fminf(low, s_lo[w][e]);
+      const float m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(fabsf(top), fabsf(low)))));
+      float d = 0.f;
+      int up = 0, down = 0;
+      if (!(m < INFINITY)) {
+        d = INFINITY, up = 127, down = -127;
+      } else if (m > kTinyAmax) {
+        d = __fdiv_rn(m, 127.f);
+        up = max(-127, min(127, __float2int_ru(__fdiv_rn(top, d)))), down = max(-127, min(127, __float2int_rd(__fdiv_rn(low, d))));
+      }
+      const long long rec = (long long)page * a.c.Hkv + hk;
+      a.codes[rec * 2 * D + e] = (int8_t)up, a.codes[rec * 2 * D + D + e] = (int8_t)down;
+      if (lane == 0) a.scales[rec * (D / 32) + blk] = d;
+    }
+  }
+}
+
+typedef void (*BoundKernel)(const BoundArgs);
+template <int D>
+static BoundKernel pick_bounds(int t) {
+  return t == FA_F32 ? k_page_bounds<D, FA_F32> : t == FA_F16 ? k_page_bounds<D, FA_F16> : t == FA_Q8_0 ? k_page_bounds<D, FA_Q8_0> : k_page_bounds<D, FA_Q4_0>;
+}
+
+// ------------------------------------------------------------------------------------------------
+// scores, as whole numbers in their order
+
+struct SelectArgs {
+  Cache c;
+  const int8_t* codes;
+  const float* scales;
+  const void* q;
+  int act;
+  long long q_row, q_head;
+  const int32_t* lens;
+  int H, G, K, first, last;
+  float scale;
+  const float* alibi;
+  uint32_t* keys;  // [B][Hkv][max_pages]
+  int32_t* pages;
+  int chunk, chunks;  // pages that a CTA scores, CTAs of a sequence and KV head
+};
+
+constexpr uint32_t kForced = 0xffffffffu, kNoPage = 0;  // above and below every score
+__device__ __forceinline__ uint32_t key_of(float s) {
+  s = s != s ? INFINITY : s + 0.f;  // (one zero)
+  const uint32_t u = __float_as_uint(s);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float act_at(const void* p, int act, long long i) {
+  if (act == FA_ACT_F32) return static_cast<const float*>(p)[i];
+  if (act == FA_ACT_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+constexpr int kScoreWarps = 4, kScoreHeads = 16;  // query heads whose codes lie in shared memory at a time
+
+// A lane takes a block of 32 components of a page's bounds, D / 32 lanes a page; a CTA `chunk` pages of one sequence
+// and KV head for all its query heads.
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) k_page_scores(const SelectArgs a) {
+  constexpr int NB = D / 32, PW = 32 / NB;  // blocks; pages that a warp takes at a time
+  __shared__ __align__(16) uint32_t s_q[kScoreHeads][D / 4];
+  __shared__ float s_e[kScoreHeads][NB];
+  after_last();
+  lets_next();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane & (NB - 1);
+  const unsigned hk = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv;
+  const int b = rest / a.chunks, c0 = (rest % a.chunks) * a.chunk;
+  const int L = len_of(a.c, a.lens, b), n = pages_of(a.c, L);
+  if (c0 >= n || n <= a.K) return;  // (all pages are taken then)
+  const int c1 = min(n, c0 + a.chunk);
+  uint32_t* keys = a.keys + ((long long)b * a.c.Hkv + hk) * a.c.max_pages;
+  for (int g0 = 0; g0 < a.G; g0 += kScoreHeads) {
+    const int ng = min(kScoreHeads, a.G - g0), h0 = (int)hk * a.G + g0;
+    if (g0) __syncthreads();
+    // q in 8 bits: a warp a block, a lane a component
+    for (int i = warp; i < ng * NB; i += kScoreWarps) {
+      const int g = i / NB, k = i % NB;
+      const float x = act_at(a.q, a.act, b * a.q_row + (h0 + g) * a.q_head + k * 32 + lane);
+      const float m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(x))));
+      const bool some = m > kTinyAmax;
+      const int c = some ? max(-127, min(127, __float2int_rn(__fmul_rn(x, __fdiv_rn(127.f, m))))) : 0;
+      reinterpret_cast<int8_t*>(s_q[g])[k * 32 + lane] = (int8_t)c;
+      if (lane == 0) s_e[g][k] = some ? __fdiv_rn(m, 127.f) : 0.f;
+    }
+    __syncthreads();
+    for (int p0 = c0 + warp * PW; p0 < c1; p0 += kScoreWarps * PW) {
+      const int p = p0 + lane / NB;
+      const bool on = p < c1;
+      const int page = a.c.table[(long long)b * a.c.max_pages + min(p, c1 - 1)];
+      const bool there = page >= 0 && page < a.c.num_pages;
+      if (!there && on && blk == 0 && g0 == 0) report_page(a.c.err);
+      const long long rec = (long long)(there ? page : 0) * a.c.Hkv + hk;
+      const uint4* bounds = reinterpret_cast<const uint4*>(a.codes + rec * 2 * D) + 2 * blk;
+      uint4 h4[2], l4[2];
+      float d = 0.f;
+      if (there) {  // (no page: nothing to read, and none may exist)
+        h4[0] = bounds[0], h4[1] = bounds[1], l4[0] = bounds[D / 16], l4[1] = bounds[D / 16 + 1];
+        d = a.scales[rec * NB + blk];
+      } else {
+        h4[0] = h4[1] = l4[0] = l4[1] = make_uint4(0, 0, 0, 0);
+      }
+      const uint32_t hi[8] = {h4[0].x, h4[0].y, h4[0].z, h4[0].w, h4[1].x, h4[1].y, h4[1].z, h4[1].w};
+      const uint32_t lo[8] = {l4[0].x, l4[0].y, l4[0].z, l4[0].w, l4[1].x, l4[1].y, l4[1].z, l4[1].w};
+      const float far = (float)(min((long long)(p + 1) * a.c.page_size, (long long)L) - L);
+      float best = -INFINITY;
+      for (int g = 0; g < ng; ++g) {
+        const uint4* qv = reinterpret_cast<const uint4*>(s_q[g]) + 2 * blk;
+        const uint4 q0 = qv[0], q1 = qv[1];
+        const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        int I = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t neg;  // 0xff in the bytes of negative codes
+          asm("prmt.b32 %0, %1, %1, 0xba98;" : "=r"(neg) : "r"(qw[i]));
+          I = __dp4a((int)((hi[i] & ~neg) | (lo[i] & neg)), (int)qw[i], I);
+        }
+        float s = __fmul_rn(__fmul_rn((float)I, d), s_e[g][blk]);
+#pragma unroll
+        for (int o = 1; o < NB; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, o));
+        s = __fmul_rn(s, a.scale);
+        if (a.alibi) s = __fadd_rn(s, __fmul_rn(a.alibi[h0 + g], far));
+        s = s != s ? INFINITY : s;
+        best = fmaxf(best, s);
+      }
+      if (on && blk == 0) {
+        uint32_t key = !there ? kNoPage : key_of(best);
+        if (g0 && there) key = max(key, keys[p]);
+        if (p < a.first || p >= n - a.last) key = kForced;
+        keys[p] = key;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// the K largest: a CTA a sequence and KV head.  Its warps own neighbouring stretches of the pages, so that what
+// they choose is in ascending order; the keys lie in registers where there are at most kPickKeys a lane.  The K-th
+// largest is found by bisection between the smallest and the largest: a count a step, and as a rule it ends when
+// exactly K are above, after little more than log2(pages) steps.
+
+constexpr int kPickWarps = 16, kPickKeys = 16;
+
+struct Count16 {  // a word from each warp, double-buffered: one barrier a sum
+  uint32_t s[2][kPickWarps];
+};
+// Sum over the CTA; every thread gets it.
+__device__ __forceinline__ uint32_t cta_sum(uint32_t v, Count16& c, int& turn) {
+  const uint32_t w = __reduce_add_sync(kFull, v);
+  if ((threadIdx.x & 31) == 0) c.s[turn][threadIdx.x >> 5] = w;
+  __syncthreads();
+  const uint32_t x = (threadIdx.x & 31) < kPickWarps ? c.s[turn][threadIdx.x & 31] : 0;
+  turn ^= 1;
+  return __reduce_add_sync(kFull, x);
+}
+
+template <bool REGS>
+__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Count16& cnt, uint32_t (&ends)[2][kPickWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rounds = (n + kPickWarps * 32 - 1) / (kPickWarps * 32), base = warp * rounds * 32 + lane;
+  uint32_t r[REGS ? kPickKeys : 1];
+  auto key = [&](int i) {
+    const int p = base + i * 32;
+    return p < n ? keys[p] : 0u;
+  };
+  // the range of the scores that are not forced
+  uint32_t least = 0xffffffffu, most = 0;
+  auto see = [&](uint32_t k, int i) {
+    if (base + i * 32 < n && k != kForced) least = min(least, k), most = max(most, k);
+  };
+  if (REGS) {
+#pragma unroll
+    for (int i = 0; i < kPickKeys; ++i)
+      if (i < rounds) r[i] = key(i);
+#pragma unroll
+    for (int i = 0; i < kPickKeys; ++i)
+      if (i < rounds) see(r[i], i);
+  } else {
+    for (int i = 0; i < rounds; ++i) see(key(i), i);
+  }
+  least = __reduce_min_sync(kFull, least), most = __reduce_max_sync(kFull, most);
+  if (lane == 0) ends[0][warp] = least, ends[1][warp] = most;
+  __syncthreads();
+  uint32_t lo = __reduce_min_sync(kFull, ends[0][lane & (kPickWarps - 1)]), hi = __reduce_max_sync(kFull, ends[1][lane & (kPickWarps - 1)]);
+  int turn = 0;
+  auto count = [&](uint32_t t) {  // keys of at least t > 0
+    uint32_t c = 0;
+    if (REGS) {
+#pragma unroll
+      for (int i = 0; i < kPickKeys; ++i)
+        if (i < rounds) c += r[i] >= t;
+    } else {
+      for (int i = 0; i < rounds; ++i) c += key(i) >= t;
+    }
+    return cta_sum(c, cnt, turn);
+  };
+  const uint32_t K = (uint32_t)a.K;
+  uint32_t above = 0;     // keys above T
+  bool ties = false;      // T is shared by more keys than there is room for
+  uint32_t T;
+  if (a.first + a.last == a.K) {
+    T = kForced;
+  } else {  // count(lo) >= K and count(hi + 1) < K
+    uint32_t c_hi = (uint32_t)(a.first + a.last);
+    T = 0;
+    while (lo < hi) {
+      const uint32_t mid = lo + ((hi - lo) >> 1) + 1, c = count(mid);
+      if (c == K) {
+        T = mid;
+        break;
+      }
+      if (c > K) lo = mid;
+      else hi = mid - 1, c_hi = c;
+    }
+    if (lo == hi) T = lo, above = c_hi, ties = true;
+  }
+  // who is chosen, in order: those above T (or at it), and the first K - above of those at T
+  const uint32_t room = ties ? K - above : 0;
+  uint32_t chosen = 0, equal = 0;  // of this warp's
+  auto tell = [&](uint32_t k, int i) {
+    const bool in = base + i * 32 < n;
+    chosen += __popc(__ballot_sync(kFull, in && (ties ? k > T : k >= T)));
+    equal += __popc(__ballot_sync(kFull, in && ties && k == T));
+  };
+  if (REGS) {
+#pragma unroll
+    for (int i = 0; i < kPickKeys; ++i)
+      if (i < rounds) tell(r[i], i);
+  } else {
+    for (int i = 0; i < rounds; ++i) tell(key(i), i);
+  }
+  __syncthreads();  // (`ends` has been read)
+  if (lane == 0) ends[0][warp] = chosen, ends[1][warp] = equal;
+  __syncthreads();
+  uint32_t before = 0, eq_before = 0;
+  for (int w = 0; w < warp; ++w) before += ends[0][w], eq_before += ends[1][w];
+  before += min(eq_before, room);
+  auto put = [&](uint32_t k, int i) {
+    const int p = base + i * 32;
+    const bool in = p < n, over = in && (ties ? k > T : k >= T), same = in && ties && k == T;
+    const uint32_t below = (1u << lane) - 1, eq = __ballot_sync(kFull, same);
+    const bool take = over || (same && eq_before + __popc(eq & below) < room);
+    const uint32_t all = __ballot_sync(kFull, take);
+    if (take) out[before + __popc(all & below)] = p;
+    before += __popc(all), eq_before += __popc(eq);
+  };
+  if (REGS) {
+#pragma unroll
+    for (int i = 0; i < kPickKeys; ++i)
+      if (i < rounds) put(r[i], i);
+  } else {
+    for (int i = 0; i < rounds; ++i) put(key(i), i);
+  }
+}
+
+__global__ void __launch_bounds__(kPickWarps * 32) k_page_pick(const SelectArgs a) {
+  __shared__ Count16 s_cnt;
+  __shared__ uint32_t s_ends[2][kPickWarps];
+  after_last();
+  lets_next();
+  const int b = blockIdx.x / a.c.Hkv;
+  const int len = a.lens[b];
+  if (len < 0) return;
+  const int n = pages_of(a.c, len_of(a.c, a.lens, b));
+  int32_t* out = a.pages + (long long)blockIdx.x * a.K;
+  if (n <= a.K) {
+    for (int i = threadIdx.x; i < a.K; i += kPickWarps * 32) out[i] = i < n ? i : -1;
+    return;
+  }
+  const uint32_t* keys = a.keys + (long long)blockIdx.x * a.c.max_pages;
+  if (n <= kPickWarps * 32 * kPickKeys) pick<true>(a, keys, out, n, s_cnt, s_ends);
+  else pick<false>(a, keys, out, n, s_cnt, s_ends);
+}
+
+static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
+  if (!p) return FA_ERR_NULL;
+  if (c.num_pages > 0 && (!p->codes || !p->scales)) return FA_ERR_NULL;
+  return aligned(p->codes, 16) && aligned(p->scales, 16) ? FA_OK : FA_ERR_ALIGN;
+}
+static size_t key_bytes(const Cache& c) {
+  return std::max<size_t>(256, ((size_t)c.B * c.Hkv * c.max_pages * sizeof(uint32_t) + 255) / 256 * 256);
+}
+static bool select_range(const Cache& c, int H) {
+  return c.max_pages <= (1 << 22) && H <= 65535 && (long long)c.B * c.Hkv < (1 << 22);
+}
+
+}  // namespace fap
+
+using namespace fap;
+
+extern "C" fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_bounds_pool* bounds, const int32_t* first,
+                                    const int32_t* seq_lens, void* stream) {
+  BoundArgs a = {};
+  fa_status rc = check_cache(cache, &a.c);
+  if (rc != FA_OK) return rc;
+  if ((rc = check_bounds(a.c, bounds)) != FA_OK) return rc;
+  if (a.c.B > 0 && !seq_lens) return FA_ERR_NULL;
+  if (!aligned(first, 4) || !aligned(seq_lens, 4)) return FA_ERR_ALIGN;
+  int nsm = 0;
+  if ((rc = fab_device(&nsm, &a.c.err)) != FA_OK) return rc;
+  if (a.c.B == 0 || a.c.max_pages == 0) return FA_OK;
+  a.codes = bounds->codes, a.scales = bounds->scales, a.first = first, a.lens = seq_lens;
+  const long long rows = (long long)a.c.B * a.c.Hkv;
+  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, 12LL * nsm / rows));
+  if (rows * a.Z > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const BoundKernel k = a.c.D == 64 ? pick_bounds<64>(a.c.k_type) : a.c.D == 128 ? pick_bounds<128>(a.c.k_type) : pick_bounds<256>(a.c.k_type);
+  return launch_next(k, dim3((unsigned)(rows * a.Z)), dim3(kBoundWarps * 32), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+extern "C" size_t fa_page_select_workspace_size(const fa_paged_cache* cache, int H, int K) {
+  Cache c;
+  if (check_cache(cache, &c) != FA_OK || H < 1 || H % c.Hkv || K < 1 || !select_range(c, H)) return 0;
+  return key_bytes(c);
+}
+
+extern "C" fa_status fa_page_select(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,
+                                    const fa_page_bounds_pool* bounds, const int32_t* seq_lens, int H, float scale,
+                                    const float* alibi_slopes, int K, int first, int last, int32_t* pages,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  SelectArgs a = {};
+  fa_status rc = check_cache(cache, &a.c);
+  if (rc != FA_OK) return rc;
+  if ((rc = check_bounds(a.c, bounds)) != FA_OK) return rc;
+  if (!act_type(act)) return FA_ERR_TYPE;
+  if (H < 1 || H % a.c.Hkv != 0 || q_row < 0 || q_head < 0) return FA_ERR_SHAPE;
+  if (K < 1 || first < 0 || last < 0 || (long long)first + last > K) return FA_ERR_SHAPE;
+  if (!select_range(a.c, H) || (long long)a.c.B * a.c.Hkv * K > (1LL << 40)) return FA_ERR_UNSUPPORTED;
+  if (a.c.B > 0 && (!q || !seq_lens || !pages)) return FA_ERR_NULL;
+  if (!aligned(q, act_bytes(act)) || !aligned(seq_lens, 4) || !aligned(alibi_slopes, 4) || !aligned(pages, 4)) return FA_ERR_ALIGN;
+  int nsm = 0;
+  if ((rc = fab_device(&nsm, &a.c.err)) != FA_OK) return rc;
+  if (!workspace || workspace_bytes < key_bytes(a.c)) return FA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
+  if (a.c.B == 0) return FA_OK;
+  a.codes = bounds->codes, a.scales = bounds->scales, a.q = q, a.act = act, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens;
+  a.H = H, a.G = H / a.c.Hkv, a.K = K, a.first = first, a.last = last, a.scale = scale, a.alibi = alibi_slopes;
+  a.keys = static_cast<uint32_t*>(workspace), a.pages = pages;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.c.max_pages > K) {
+    const long long rows = (long long)a.c.B * a.c.Hkv;
+    const int at_once = kScoreWarps * 32 / (a.c.D / 32);  // pages that a CTA takes at a time
+    const long long want = std::max(1LL, 16LL * nsm / rows), most = (a.c.max_pages + at_once - 1) / at_once;
+    a.chunk = (int)((most + std::min(want, most) - 1) / std::min(want, most)) * at_once;
+    a.chunks = (a.c.max_pages + a.chunk - 1) / a.chunk;
+    if (rows * a.chunks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    void (*k)(const SelectArgs) = a.c.D == 64 ? k_page_scores<64> : a.c.D == 128 ? k_page_scores<128> : k_page_scores<256>;
+    if (launch_next(k, dim3((unsigned)(rows * a.chunks)), dim3(kScoreWarps * 32), 0, s, a) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return launch_next(k_page_pick, dim3((unsigned)(a.c.B * a.c.Hkv)), dim3(kPickWarps * 32), 0, s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}

@@ -1,4 +1,4 @@
-// The plain form of paged.py's calls, without Python between their arguments and the C entry points: a
+// The plain form of paged.py's and pages.py's calls, without Python between their arguments and the C entry points: a
 // layer's step makes several of them on a few kilobytes each, and there the wrappers cost more than the
 // kernels (a call's wall time on 64 tokens: 20 us from Python, 5 us from here).  What is handled here: outputs and workspace allocated by the call, on the current stream of
 // the tensors' device, which is the current one.  Anything else, and any argument that is not as it
@@ -12,7 +12,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "../../include/fa_paged.h"
+#include "../../include/fa_paged_ext.h"
 
 namespace {
 
@@ -24,9 +24,19 @@ struct Entry {
   decltype(&fa_cache_read) read;
   decltype(&fa_paged_decode) decode;
   decltype(&fa_paged_decode_workspace_size) decode_ws;
+  decltype(&fa_qk_norm_rope_axes) norm_axes;
+  decltype(&fa_qk_norm_rope_axes_backward) norm_axes_back;
+  decltype(&fa_cache_append_axes) append_axes;
+  decltype(&fa_paged_decode_pages) decode_pages;
+  decltype(&fa_pages_extend) extend;
+  decltype(&fa_pages_trim) trim;
+  decltype(&fa_page_bounds) bounds;
+  decltype(&fa_page_select) select;
+  decltype(&fa_page_select_workspace_size) select_ws;
 } fn;
+constexpr int kEntries = sizeof(Entry) / sizeof(void*);
 
-PyObject *s_q, *s_k, *s_v, *s_O, *s_lse, *s_dq, *s_dk, *s_dwq, *s_dwk;
+PyObject *s_q, *s_k, *s_v, *s_O, *s_lse, *s_dq, *s_dk, *s_dwq, *s_dwk, *s_seq, *s_pos, *s_row, *s_starts, *s_first;
 
 int act_of(at::ScalarType t) {
   return t == at::kFloat ? FA_ACT_F32 : t == at::kHalf ? FA_ACT_F16 : t == at::kBFloat16 ? FA_ACT_BF16 : -1;
@@ -72,6 +82,15 @@ struct Args {
     *p = r;
     return true;
   }
+  // axes i (uint8 [pairs]) of the rotation r, and positions j (int32 [axes][n], rows of neighbouring elements) or None
+  const int32_t* axes(int i, int j, const fa_rope& r, int64_t n, fa_rope_axes* out) {
+    const uint8_t* axis = flat<uint8_t>(i, at::kByte, r.n_rot / 2, false);
+    const at::Tensor* x = ok ? tensor(j) : nullptr;
+    if (!ok) return nullptr;
+    if (x->dim() != 2 || x->scalar_type() != at::kInt || x->size(1) != n || (n > 1 && x->stride(1) != 1)) return ok = false, nullptr;
+    *out = fa_rope_axes{r.freqs, axis, x->stride(0), r.n_rot, r.style, (int32_t)x->size(0)};
+    return static_cast<const int32_t*>(x->data_ptr());
+  }
   long long integer(int i) {
     const long long v = PyLong_AsLongLong(a[i]);
     if (v == -1 && PyErr_Occurred()) PyErr_Clear(), ok = false;
@@ -108,7 +127,7 @@ PyObject* guarded(F f) {
   Py_RETURN_NONE;
 }
 
-// (q, k, pos, wq, wk, eps, rope, style, dtype)
+// (q, k, pos, wq, wk, eps, rope, style, dtype, rope_axes)
 PyObject* norm(PyObject*, PyObject* const* argv, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     Args a{argv};
@@ -124,16 +143,21 @@ PyObject* norm(PyObject*, PyObject* const* argv, Py_ssize_t) {
     if (!a.ok) return nullptr;
     fa_rope r;
     const fa_rope* rp;
-    const int32_t* pos = a.rope(6, (int)a.integer(7), &r, &rp) ? a.flat<int32_t>(2, at::kInt, N, false) : nullptr;
+    fa_rope_axes ra;
+    const bool turns = a.rope(6, (int)a.integer(7), &r, &rp), several = argv[9] != Py_None;
+    if (several && !turns) return nullptr;
+    const int32_t* pos = several ? a.axes(9, 2, r, N, &ra) : turns ? a.flat<int32_t>(2, at::kInt, N, false) : nullptr;
     const double eps = a.number(5);
     if (argv[8] != Py_None && !THPDtype_Check(argv[8])) return nullptr;
     const at::ScalarType yt = argv[8] == Py_None ? xt : reinterpret_cast<THPDtype*>(argv[8])->scalar_type;
     if (!a.here() || act_of(xt) < 0 || act_of(yt) < 0) return nullptr;
     const at::Tensor oq = make({N, H, D}, yt, a.device), ok = k ? make({N, Hkv, D}, yt, a.device) : at::Tensor();
     const fa_qk_views views = {q->stride(0), q->stride(1), k ? k->stride(0) : 0, k ? k->stride(1) : 0};
-    if (fn.norm(at_of(q), k ? at_of(k) : nullptr, act_of(xt), &views, wq, wk, (float)eps, pos, rp, N, H, Hkv, D, oq.data_ptr(),
-                k ? ok.data_ptr() : nullptr, act_of(yt), c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
-      return nullptr;
+    auto call = [&](auto entry, auto* turn) {
+      return entry(at_of(q), k ? at_of(k) : nullptr, act_of(xt), &views, wq, wk, (float)eps, pos, turn, N, H, Hkv, D, oq.data_ptr(),
+                   k ? ok.data_ptr() : nullptr, act_of(yt), c10::cuda::getCurrentCUDAStream(a.device).stream());
+    };
+    if ((several ? call(fn.norm_axes, &ra) : call(fn.norm, rp)) != FA_OK) return nullptr;
     PyObject* d = PyDict_New();
     put(d, s_q, oq);
     if (k) put(d, s_k, ok);
@@ -142,7 +166,7 @@ PyObject* norm(PyObject*, PyObject* const* argv, Py_ssize_t) {
   });
 }
 
-// (gq, gk, q, k, pos, wq, wk, eps, rope, style)
+// (gq, gk, q, k, pos, wq, wk, eps, rope, style, rope_axes)
 PyObject* norm_back(PyObject*, PyObject* const* argv, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     Args a{argv};
@@ -164,7 +188,10 @@ PyObject* norm_back(PyObject*, PyObject* const* argv, Py_ssize_t) {
     if (!a.ok) return nullptr;
     fa_rope r;
     const fa_rope* rp;
-    const int32_t* pos = a.rope(8, (int)a.integer(9), &r, &rp) ? a.flat<int32_t>(4, at::kInt, N, false) : nullptr;
+    fa_rope_axes ra;
+    const bool turns = a.rope(8, (int)a.integer(9), &r, &rp), several = argv[10] != Py_None;
+    if (several && !turns) return nullptr;
+    const int32_t* pos = several ? a.axes(10, 4, r, N, &ra) : turns ? a.flat<int32_t>(4, at::kInt, N, false) : nullptr;
     const double eps = a.number(7);
     if (!a.here() || act_of(xt) < 0 || act_of(yt) < 0) return nullptr;
     const size_t need = fn.norm_back_ws(N, H, Hkv, D);
@@ -174,10 +201,12 @@ PyObject* norm_back(PyObject*, PyObject* const* argv, Py_ssize_t) {
     const at::Tensor ws = make({(int64_t)need}, at::kByte, a.device);
     const fa_qk_views views = {q->stride(0), q->stride(1), k ? k->stride(0) : 0, k ? k->stride(1) : 0};
     auto at_or_null = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-    if (fn.norm_back(at_of(gq), gk ? at_of(gk) : nullptr, act_of(yt), at_of(q), k ? at_of(k) : nullptr, act_of(xt), &views, wq, wk,
-                     (float)eps, pos, rp, N, H, Hkv, D, dq.data_ptr(), at_or_null(dk), static_cast<float*>(at_or_null(dwq)),
-                     static_cast<float*>(at_or_null(dwk)), ws.data_ptr(), need,
-                     c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
+    auto call = [&](auto entry, auto* turn) {
+      return entry(at_of(gq), gk ? at_of(gk) : nullptr, act_of(yt), at_of(q), k ? at_of(k) : nullptr, act_of(xt), &views, wq, wk,
+                   (float)eps, pos, turn, N, H, Hkv, D, dq.data_ptr(), at_or_null(dk), static_cast<float*>(at_or_null(dwq)),
+                   static_cast<float*>(at_or_null(dwk)), ws.data_ptr(), need, c10::cuda::getCurrentCUDAStream(a.device).stream());
+    };
+    if ((several ? call(fn.norm_axes_back, &ra) : call(fn.norm_back, rp)) != FA_OK)
       return nullptr;
     PyObject* d = PyDict_New();
     put(d, s_dq, dq);
@@ -188,14 +217,16 @@ PyObject* norm_back(PyObject*, PyObject* const* argv, Py_ssize_t) {
   });
 }
 
-// The cache: the address of its fa_paged_cache and its device, as PagedCache keeps them
-const fa_paged_cache* cache_of(Args& a, int i) {
-  const fa_paged_cache* c = reinterpret_cast<const fa_paged_cache*>(a.integer(i));
+// A structure whose address and device a Python object keeps (PagedCache, PageLists)
+template <typename T>
+const T* held(Args& a, int i) {
+  const T* c = reinterpret_cast<const T*>(a.integer(i));
   a.device = (int)a.integer(i + 1);
   return a.ok && c ? c : (a.ok = false, nullptr);
 }
+const fa_paged_cache* cache_of(Args& a, int i) { return held<fa_paged_cache>(a, i); }
 
-// (k, v, cache, device, seq, pos, k_norm, eps, rope, style)
+// (k, v, cache, device, seq, pos, k_norm, eps, rope, style, rope_axes, rope_pos)
 PyObject* append(PyObject*, PyObject* const* argv, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     Args a{argv};
@@ -215,11 +246,15 @@ PyObject* append(PyObject*, PyObject* const* argv, Py_ssize_t) {
     if (!a.ok) return nullptr;
     fa_rope r;
     const fa_rope* rp;
-    a.rope(8, (int)a.integer(9), &r, &rp);
+    fa_rope_axes ra;
+    const bool turns = a.rope(8, (int)a.integer(9), &r, &rp), several = argv[10] != Py_None;
+    if (several != (argv[11] != Py_None) || (several && !turns)) return nullptr;
+    const int32_t* rope_pos = several ? a.axes(10, 11, r, T, &ra) : nullptr;
     if (!a.here() || act_of(xt) < 0) return nullptr;
     const fa_kv_views views = {k->stride(0), k->stride(1), v->stride(0), v->stride(1)};
-    if (fn.append(at_of(k), at_of(v), act_of(xt), &views, c, seq, pos, T, w, (float)eps, rp,
-                  c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream(a.device).stream();
+    if ((several ? fn.append_axes(at_of(k), at_of(v), act_of(xt), &views, c, seq, pos, T, w, (float)eps, rope_pos, &ra, st)
+                 : fn.append(at_of(k), at_of(v), act_of(xt), &views, c, seq, pos, T, w, (float)eps, rp, st)) != FA_OK)
       return nullptr;
     Py_RETURN_TRUE;
   });
@@ -247,7 +282,7 @@ PyObject* read(PyObject*, PyObject* const* argv, Py_ssize_t) {
   });
 }
 
-// (q, cache, device, seq_lens, scale, alibi_slopes, softcap, sinks)
+// (q, cache, device, seq_lens, scale, alibi_slopes, softcap, sinks, pages)
 PyObject* decode(PyObject*, PyObject* const* argv, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     Args a{argv};
@@ -262,13 +297,20 @@ PyObject* decode(PyObject*, PyObject* const* argv, Py_ssize_t) {
     const float* alibi = a.ok ? a.flat<float>(5, at::kFloat, H, true) : nullptr;
     const float* sinks = a.ok ? a.flat<float>(7, at::kFloat, H, true) : nullptr;
     const double scale = a.number(4), softcap = a.number(6);
+    const at::Tensor* pages = a.ok && argv[8] != Py_None ? a.tensor(8) : nullptr;
+    if (pages && (pages->dim() != 3 || pages->scalar_type() != at::kInt || pages->size(0) != B || pages->size(1) != c->Hkv ||
+                  pages->size(2) > INT32_MAX || !pages->is_contiguous()))
+      return nullptr;
     if (!a.here() || act_of(xt) < 0) return nullptr;
     const size_t need = fn.decode_ws(c, H);
     const at::Tensor O = make({B, H, c->Dv}, xt, a.device), lse = make({B, H}, at::kFloat, a.device);
     const at::Tensor ws = make({(int64_t)need}, at::kByte, a.device);
-    if (fn.decode(at_of(q), act_of(xt), q->stride(0), q->stride(1), c, lens, H, (float)scale, alibi, (float)softcap, sinks,
-                  O.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), need,
-                  c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream(a.device).stream();
+    float* out_lse = static_cast<float*>(lse.data_ptr());
+    if ((pages ? fn.decode_pages(at_of(q), act_of(xt), q->stride(0), q->stride(1), c, lens, static_cast<const int32_t*>(at_of(pages)),
+                                 pages->size(2), H, (float)scale, alibi, (float)softcap, sinks, O.data_ptr(), out_lse, ws.data_ptr(), need, st)
+               : fn.decode(at_of(q), act_of(xt), q->stride(0), q->stride(1), c, lens, H, (float)scale, alibi, (float)softcap, sinks,
+                           O.data_ptr(), out_lse, ws.data_ptr(), need, st)) != FA_OK)
       return nullptr;
     PyObject* d = PyDict_New();
     put(d, s_O, O), put(d, s_lse, lse);
@@ -276,19 +318,90 @@ PyObject* decode(PyObject*, PyObject* const* argv, Py_ssize_t) {
   });
 }
 
+// (lists, device, new_tokens, T)
+PyObject* extend(PyObject*, PyObject* const* argv, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    Args a{argv};
+    const fa_page_lists* l = held<fa_page_lists>(a, 0);
+    if (!a.ok) return nullptr;
+    const int32_t* news = a.flat<int32_t>(2, at::kInt, l->B, false);
+    const long long T = a.integer(3);
+    if (!a.here() || T < 0 || T > INT32_MAX) return nullptr;
+    const at::Tensor seq = make({T}, at::kInt, a.device), pos = make({T}, at::kInt, a.device), row = make({T}, at::kInt, a.device);
+    const at::Tensor starts = make({(int64_t)l->B + 1}, at::kInt, a.device), first = make({l->B}, at::kInt, a.device);
+    auto p = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+    if (fn.extend(l, news, (int)T, p(starts), p(first), p(seq), p(pos), p(row), c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
+      return nullptr;
+    PyObject* d = PyDict_New();
+    put(d, s_seq, seq), put(d, s_pos, pos), put(d, s_row, row), put(d, s_starts, starts), put(d, s_first, first);
+    return d;
+  });
+}
+
+// (lists, device, keep)
+PyObject* trim(PyObject*, PyObject* const* argv, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    Args a{argv};
+    const fa_page_lists* l = held<fa_page_lists>(a, 0);
+    if (!a.ok) return nullptr;
+    const int32_t* keep = a.flat<int32_t>(2, at::kInt, l->B, false);
+    if (!a.here() || fn.trim(l, keep, c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK) return nullptr;
+    Py_RETURN_TRUE;
+  });
+}
+
+// (cache, device, bounds, seq_lens, first)
+PyObject* bounds(PyObject*, PyObject* const* argv, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    Args a{argv};
+    const fa_paged_cache* c = cache_of(a, 0);
+    const fa_page_bounds_pool* pool = reinterpret_cast<const fa_page_bounds_pool*>(a.integer(2));
+    if (!a.ok) return nullptr;
+    const int32_t* lens = a.flat<int32_t>(3, at::kInt, c->B, false);
+    const int32_t* first = a.ok ? a.flat<int32_t>(4, at::kInt, c->B, true) : nullptr;
+    if (!a.here() || fn.bounds(c, pool, first, lens, c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK) return nullptr;
+    Py_RETURN_TRUE;
+  });
+}
+
+// (q, cache, device, bounds, seq_lens, K, scale, first, last, alibi_slopes)
+PyObject* select_pages(PyObject*, PyObject* const* argv, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    Args a{argv};
+    const fa_paged_cache* c = cache_of(a, 1);
+    const fa_page_bounds_pool* pool = reinterpret_cast<const fa_page_bounds_pool*>(a.integer(3));
+    if (!a.ok) return nullptr;
+    const at::Tensor* q = a.tensor(0);
+    if (!a.ok || q->dim() != 3) return nullptr;
+    const at::ScalarType xt = q->scalar_type();
+    const int64_t B = c->B, H = q->size(1);
+    a.heads(0, xt, B, c->D);
+    const int32_t* lens = a.ok ? a.flat<int32_t>(4, at::kInt, B, false) : nullptr;
+    const float* alibi = a.ok ? a.flat<float>(9, at::kFloat, H, true) : nullptr;
+    const long long K = a.integer(5), first = a.integer(7), last = a.integer(8);
+    const double scale = a.number(6);
+    if (!a.here() || act_of(xt) < 0 || K < 1 || K > INT32_MAX || first < 0 || first > K || last < 0 || last > K) return nullptr;
+    const size_t need = fn.select_ws(c, H, (int)K);
+    if (!need) return nullptr;
+    const at::Tensor pages = make({B, c->Hkv, (int64_t)K}, at::kInt, a.device), ws = make({(int64_t)need}, at::kByte, a.device);
+    if (fn.select(at_of(q), act_of(xt), q->stride(0), q->stride(1), c, pool, lens, H, (float)scale, alibi, (int)K, (int)first, (int)last,
+                  static_cast<int32_t*>(pages.data_ptr()), ws.data_ptr(), need, c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
+      return nullptr;
+    return THPVariable_Wrap(pages);
+  });
+}
+
 // The addresses of libfa_back.so's entry points, in Entry's order
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t n) {
-  if (n != 7) return PyErr_Format(PyExc_TypeError, "seven addresses expected");
-  void* p[7];
-  for (int i = 0; i < 7; ++i)
+  if (n != kEntries) return PyErr_Format(PyExc_TypeError, "%d addresses expected", kEntries);
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i)
     if (!(p[i] = PyLong_AsVoidPtr(argv[i]))) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "address 0");
-  fn.norm = reinterpret_cast<decltype(fn.norm)>(p[0]);
-  fn.norm_back = reinterpret_cast<decltype(fn.norm_back)>(p[1]);
-  fn.norm_back_ws = reinterpret_cast<decltype(fn.norm_back_ws)>(p[2]);
-  fn.append = reinterpret_cast<decltype(fn.append)>(p[3]);
-  fn.read = reinterpret_cast<decltype(fn.read)>(p[4]);
-  fn.decode = reinterpret_cast<decltype(fn.decode)>(p[5]);
-  fn.decode_ws = reinterpret_cast<decltype(fn.decode_ws)>(p[6]);
+  int i = 0;
+  auto take = [&](auto& entry) { entry = reinterpret_cast<std::decay_t<decltype(entry)>>(p[i++]); };
+  take(fn.norm), take(fn.norm_back), take(fn.norm_back_ws), take(fn.append), take(fn.read), take(fn.decode), take(fn.decode_ws);
+  take(fn.norm_axes), take(fn.norm_axes_back), take(fn.append_axes), take(fn.decode_pages), take(fn.extend), take(fn.trim);
+  take(fn.bounds), take(fn.select), take(fn.select_ws);
   Py_RETURN_NONE;
 }
 
@@ -297,11 +410,15 @@ PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     if (argc != n || !fn.norm) return PyErr_Format(PyExc_TypeError, #name ": %d arguments, after bind()", n); \
     return name(self, argv, argc);                                                                         \
   }
-FAST(norm, 9)
-FAST(norm_back, 10)
-FAST(append, 10)
+FAST(norm, 10)
+FAST(norm_back, 11)
+FAST(append, 12)
 FAST(read, 5)
-FAST(decode, 8)
+FAST(decode, 9)
+FAST(extend, 4)
+FAST(trim, 3)
+FAST(bounds, 5)
+FAST(select_pages, 10)
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
@@ -310,14 +427,18 @@ PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_append)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_read)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_decode)), METH_FASTCALL, nullptr},
+    {"extend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_extend)), METH_FASTCALL, nullptr},
+    {"trim", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_trim)), METH_FASTCALL, nullptr},
+    {"bounds", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_bounds)), METH_FASTCALL, nullptr},
+    {"select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_select_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "plain calls of paged.py", -1, methods, nullptr, nullptr, nullptr, nullptr};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "plain calls of paged.py and pages.py", -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
 PyMODINIT_FUNC PyInit__fast(void) {
-  PyObject** names[] = {&s_q, &s_k, &s_v, &s_O, &s_lse, &s_dq, &s_dk, &s_dwq, &s_dwk};
-  const char* text[] = {"q", "k", "v", "O", "lse", "dq", "dk", "dwq", "dwk"};
-  for (int i = 0; i < 9; ++i) *names[i] = PyUnicode_InternFromString(text[i]);
+  PyObject** names[] = {&s_q, &s_k, &s_v, &s_O, &s_lse, &s_dq, &s_dk, &s_dwq, &s_dwk, &s_seq, &s_pos, &s_row, &s_starts, &s_first};
+  const char* text[] = {"q", "k", "v", "O", "lse", "dq", "dk", "dwq", "dwk", "seq", "pos", "row", "starts", "first"};
+  for (int i = 0; i < 14; ++i) *names[i] = PyUnicode_InternFromString(text[i]);
   return PyModule_Create(&module);
 }

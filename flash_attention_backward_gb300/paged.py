@@ -55,7 +55,9 @@ def _bind():
     L = nat.lib()
     _fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.fa_qk_norm_rope, L.fa_qk_norm_rope_backward, L.fa_qk_norm_rope_backward_workspace_size, L.fa_cache_append,
-        L.fa_cache_read, L.fa_paged_decode, L.fa_paged_decode_workspace_size)))
+        L.fa_cache_read, L.fa_paged_decode, L.fa_paged_decode_workspace_size, L.fa_qk_norm_rope_axes,
+        L.fa_qk_norm_rope_axes_backward, L.fa_cache_append_axes, L.fa_paged_decode_pages, L.fa_pages_extend, L.fa_pages_trim,
+        L.fa_page_bounds, L.fa_page_select, L.fa_page_select_workspace_size)))
     _plain = True
     return True
 
@@ -153,6 +155,20 @@ def _rope(rope: Optional[torch.Tensor], style: int, device) -> Optional[nat.fa_r
     return nat.fa_rope(rope.data_ptr(), 2 * rope.numel(), style)
 
 
+def _axes(rope: Optional[torch.Tensor], axes: Optional[torch.Tensor], style: int, name: str, pos: Optional[torch.Tensor],
+          N: int, device):
+    """fa_rope_axes and the address of the positions pos [axes][N], whose rows may lie apart."""
+    if rope is None:
+        raise FaBackError("rope_axes: the axes of the frequencies rope, which are missing")
+    r = _rope(rope, style, device)
+    p_axes = _expect("rope_axes", axes, torch.uint8, (rope.numel(),), device)
+    if pos is None or pos.dtype is not _I32 or pos.dim() != 2 or pos.shape[1] != N or pos.device != device or (
+            N > 1 and pos.stride(1) != 1):
+        raise FaBackError(f"{name}: int32 [axes][{N}] with rows of neighbouring elements on {device} expected, got " + (
+            "None" if pos is None else f"{pos.dtype} {tuple(pos.shape)}, strides {pos.stride()}, on {pos.device}"))
+    return nat.fa_rope_axes(r.freqs, p_axes, pos.stride(0), r.n_rot, style, pos.shape[0]), pos.data_ptr()
+
+
 class PagedCache:
     """A paged raw K/V cache: pools k and v (uint8 [num_pages][page_size][Hkv][row]) of cache types k_type
     and v_type, and page_table (int32 [B][max_pages]).  Holds the tensors; nothing is copied, so pools and
@@ -177,6 +193,7 @@ class PagedCache:
         self.c = nat.fa_paged_cache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), k_type, v_type, self.num_pages,
                                     self.page_size, self.B, self.max_pages, self.Hkv, D, Dv)
         self._at, self._index = ctypes.addressof(self.c), self.device.index
+        self._dims = (self.num_pages, self.Hkv, D, self.device)  # what a PageBounds has in common with it
         self._ws = {}  # decode workspace bytes by query head count
 
     def __setattr__(self, name, value):
@@ -195,13 +212,15 @@ class PagedCache:
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, seq: torch.Tensor, pos: torch.Tensor, *,
                  k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, rope: Optional[torch.Tensor] = None,
-                 rope_style: int = nat.FA_ROPE_HALVES, stream: Optional[torch.cuda.Stream] = None) -> None:
+                 rope_style: int = nat.FA_ROPE_HALVES, rope_axes: Optional[torch.Tensor] = None,
+                 rope_pos: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Store keys k [T][Hkv][D] and values v [T][Hkv][Dv] (f32, f16 or bf16; may be views) as positions
     pos [T] of sequences seq [T] (int32; negative: a padding token, skipped) of the cache, quantised to
     its types.  Keys are normalised by k_norm (f32 [D], or None) and rotated by pos with the
-    frequencies rope (rope_frequencies(), or None) on the way."""
+    frequencies rope (rope_frequencies(), or None) on the way; with rope_axes (rope_sections()) by positions
+    rope_pos [axes][T] (int32) of several axes instead."""
     if stream is None and cache._index is not None and (_plain or _bind()) and _fast.append(
-            k, v, cache._at, cache._index, seq, pos, k_norm, eps, rope, rope_style):
+            k, v, cache._at, cache._index, seq, pos, k_norm, eps, rope, rope_style, rope_axes, rope_pos):
         return
     dev, T = cache.device, _count("k", k)
     act = _act(k.dtype)
@@ -212,8 +231,15 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, seq: torch
     p_seq = _expect("seq", seq, _I32, (T,), dev)
     p_pos = _expect("pos", pos, _I32, (T,), dev)
     p_norm = None if k_norm is None else _expect("k_norm", k_norm, _F32, (cache.D,), dev)
-    r = _rope(rope, rope_style, dev)
     views = nat.fa_kv_views(k_row, k_head, v_row, v_head)
+    if rope_axes is not None:
+        r, p_rope = _axes(rope, rope_axes, rope_style, "rope_pos", rope_pos, T, dev)
+        _check(_call(lambda s: nat.fa_cache_append_axes(k.data_ptr(), v.data_ptr(), act, views, cache.c, p_seq, p_pos, T, p_norm,
+                                                        eps, p_rope, r, s), dev, stream))
+        return
+    if rope_pos is not None:
+        raise FaBackError("rope_pos: positions of the axes rope_axes, which are missing")
+    r = _rope(rope, rope_style, dev)
     _check(_call(lambda s: nat.fa_cache_append(k.data_ptr(), v.data_ptr(), act, views, cache.c, p_seq, p_pos, T, p_norm,
                                                eps, r, s), dev, stream))
 
@@ -251,14 +277,15 @@ def cache_read(cache: PagedCache, seq: torch.Tensor, pos: torch.Tensor, *, dtype
 
 def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, scale: float,
                  alibi_slopes: Optional[torch.Tensor] = None, softcap: float = 0.0,
-                 sinks: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                 sinks: Optional[torch.Tensor] = None, pages: Optional[torch.Tensor] = None, out: Optional[dict] = None,
                  workspace: Optional[Workspace] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
     """Attention of one new token per sequence: q [B][H][D] (f32, f16 or bf16; may be a view) over the first
     seq_lens [B] (int32) positions of the cache's sequences: {"O": [B][H][Dv] of q's type, "lse": [B][H] f32}.
     ALiBi slopes and sinks (f32 [H]) and the soft cap are those of backward().  A negative length marks a
-    padding slot, whose rows are not written."""
+    padding slot, whose rows are not written.  pages (int32 [B][Hkv][K], page_select()): of each KV head, the pages
+    of the sequence that count, distinct, -1 where there is none."""
     if stream is None and out is None and workspace is None and cache._index is not None and (_plain or _bind()):
-        got = _fast.decode(q, cache._at, cache._index, seq_lens, scale, alibi_slopes, softcap, sinks)
+        got = _fast.decode(q, cache._at, cache._index, seq_lens, scale, alibi_slopes, softcap, sinks, pages)
         if got is not None:
             return got
     dev, B, dtype = cache.device, cache.B, q.dtype
@@ -267,6 +294,9 @@ def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, 
     p_len = _expect("seq_lens", seq_lens, _I32, (B,), dev)
     p_alibi = None if alibi_slopes is None else _expect("alibi_slopes", alibi_slopes, _F32, (H,), dev)
     p_sinks = None if sinks is None else _expect("sinks", sinks, _F32, (H,), dev)
+    if pages is not None:
+        K = pages.shape[2] if pages.dim() == 3 else 0
+        p_pages = _expect("pages", pages, _I32, (B, cache.Hkv, K), dev)
     _index(dev)
 
     def run(s):
@@ -279,6 +309,10 @@ def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, 
             p_o = _expect("out O", o["O"], dtype, (B, H, cache.Dv), dev)
             p_lse = _expect("out lse", o["lse"], _F32, (B, H), dev)
         ws = _empty((need,), dtype=torch.uint8, device=dev) if workspace is None else workspace.get(need)
+        if pages is not None:
+            _check(nat.fa_paged_decode_pages(q.data_ptr(), act, q_row, q_head, cache.c, p_len, p_pages, K, H, scale, p_alibi,
+                                             softcap, p_sinks, p_o, p_lse, ws.data_ptr(), need, s))
+            return o
         _check(nat.fa_paged_decode(q.data_ptr(), act, q_row, q_head, cache.c, p_len, H, scale, p_alibi, softcap, p_sinks,
                                    p_o, p_lse, ws.data_ptr(), need, s))
         return o
@@ -296,15 +330,25 @@ def _qk(q, k):
     return N, H, D, dev, dtype, Hkv, nat.fa_qk_views(q_row, q_head, k_row, k_head)
 
 
+def _turn(rope, style, axes, pos, N, dev, one, several):
+    """Which of the two entry points a rotation asks for, and what it takes of it: the rotation and its positions."""
+    if axes is not None:
+        return several, *_axes(rope, axes, style, "pos", pos, N, dev)
+    r = _rope(rope, style, dev)
+    return one, r, None if r is None else _expect("pos", pos, _I32, (N,), dev)
+
+
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch.Tensor], *,
                  wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                 rope: Optional[torch.Tensor] = None, rope_style: int = nat.FA_ROPE_HALVES, dtype=None,
+                 rope: Optional[torch.Tensor] = None, rope_style: int = nat.FA_ROPE_HALVES,
+                 rope_axes: Optional[torch.Tensor] = None, dtype=None,
                  out: Optional[dict] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
     """RMS norm of every head (weights wq, wk f32 [D]; None: not normalised) and rotation by pos [N]
     (int32) of queries q [N][H][D] and keys k [N][Hkv][D] (f32, f16 or bf16, possibly views of one
-    projection; k may be None): {"q", "k"}, contiguous, of dtype (default q's)."""
+    projection; k may be None): {"q", "k"}, contiguous, of dtype (default q's).  With rope_axes (rope_sections()) the
+    positions are those of several axes, pos [axes][N]."""
     if stream is None and out is None and (_plain or _bind()):
-        got = _fast.norm(q, k, pos, wq, wk, eps, rope, rope_style, dtype)
+        got = _fast.norm(q, k, pos, wq, wk, eps, rope, rope_style, dtype, rope_axes)
         if got is not None:
             return got
     N, H, D, dev, x_dtype, Hkv, views = _qk(q, k)
@@ -312,8 +356,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch
     x_type, y_type = _act(x_dtype), _act(dtype)
     p_wq = None if wq is None else _expect("wq", wq, _F32, (D,), dev)
     p_wk = None if wk is None else _expect("wk", wk, _F32, (D,), dev)
-    r = _rope(rope, rope_style, dev)
-    p_pos = None if r is None else _expect("pos", pos, _I32, (N,), dev)
+    norm, r, p_pos = _turn(rope, rope_style, rope_axes, pos, N, dev, nat.fa_qk_norm_rope, nat.fa_qk_norm_rope_axes)
 
     def run(s):
         o = out
@@ -323,8 +366,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch
         else:
             p_q = _expect("out q", o["q"], dtype, (N, H, D), dev)
             p_k = None if k is None else _expect("out k", o["k"], dtype, (N, Hkv, D), dev)
-        _check(nat.fa_qk_norm_rope(q.data_ptr(), _ptr(k), x_type, views, p_wq, p_wk, eps, p_pos, r, N, H, Hkv, D, p_q, p_k,
-                                   y_type, s))
+        _check(norm(q.data_ptr(), _ptr(k), x_type, views, p_wq, p_wk, eps, p_pos, r, N, H, Hkv, D, p_q, p_k, y_type, s))
         return o
 
     return _call(run, dev, stream)
@@ -333,13 +375,13 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: Optional[torch
 def qk_norm_rope_backward(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
                           pos: Optional[torch.Tensor], *, wq: Optional[torch.Tensor] = None,
                           wk: Optional[torch.Tensor] = None, eps: float = 1e-6, rope: Optional[torch.Tensor] = None,
-                          rope_style: int = nat.FA_ROPE_HALVES, out: Optional[dict] = None,
-                          workspace: Optional[Workspace] = None,
+                          rope_style: int = nat.FA_ROPE_HALVES, rope_axes: Optional[torch.Tensor] = None,
+                          out: Optional[dict] = None, workspace: Optional[Workspace] = None,
                           stream: Optional[torch.cuda.Stream] = None) -> dict:
     """The gradient of qk_norm_rope(): given gq [N][H][D] and gk [N][Hkv][D] (contiguous, e.g. backward()'s dQ
     and dK) and the forward's inputs, {"dq", "dk" of q's type, "dwq", "dwk" f32 [D] (with the weights)}."""
     if stream is None and out is None and workspace is None and (_plain or _bind()):
-        got = _fast.norm_back(gq, gk, q, k, pos, wq, wk, eps, rope, rope_style)
+        got = _fast.norm_back(gq, gk, q, k, pos, wq, wk, eps, rope, rope_style, rope_axes)
         if got is not None:
             return got
     N, H, D, dev, dtype, Hkv, views = _qk(q, k)
@@ -350,8 +392,7 @@ def qk_norm_rope_backward(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch
     p_gk = None if gk is None else _expect("gk", gk, gq.dtype, (N, Hkv, D), dev)
     p_wq = None if wq is None else _expect("wq", wq, _F32, (D,), dev)
     p_wk = None if wk is None else _expect("wk", wk, _F32, (D,), dev)
-    r = _rope(rope, rope_style, dev)
-    p_pos = None if r is None else _expect("pos", pos, _I32, (N,), dev)
+    back, r, p_pos = _turn(rope, rope_style, rope_axes, pos, N, dev, nat.fa_qk_norm_rope_backward, nat.fa_qk_norm_rope_axes_backward)
 
     def run(s):
         o = out
@@ -369,7 +410,7 @@ def qk_norm_rope_backward(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch
                     _expect("out " + name, o[name], t, shape, dev)
         need = nat.fa_qk_norm_rope_backward_workspace_size(N, H, Hkv, D)
         ws = _empty((need,), dtype=torch.uint8, device=dev) if workspace is None else workspace.get(need)
-        _check(nat.fa_qk_norm_rope_backward(
+        _check(back(
             p_gq, p_gk, y_type, q.data_ptr(), _ptr(k), x_type, views, p_wq, p_wk, eps, p_pos, r, N, H, Hkv, D,
             o["dq"].data_ptr(), _ptr(o.get("dk")), _ptr(o.get("dwq")), _ptr(o.get("dwk")), ws.data_ptr(), need, s))
         return o
