@@ -195,7 +195,7 @@ __device__ __forceinline__ void store_row8(uint8_t* row, int type, int e0, const
 constexpr int kAppendCtas = 3;  // CTAs an SM (2048 tokens with read-back 12.8 us, 14.2 with two)
 
 // K (IS_K) or V rows: a warp takes HC heads of a token, D / 8 lanes a head, and goes on to another token.
-template <int D, typename TX, bool IS_K>
+template <int D, typename TX, bool IS_K, bool AXES>
 __device__ __forceinline__ void append_rows(const RowArgs& a) {
   constexpr int LG = D / 8, GW = 32 / LG;
   const int lane = threadIdx.x & 31, grp = lane / LG, e0 = (lane & (LG - 1)) * 8;
@@ -211,7 +211,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
   if (apart) place_eight<D>(FA_ROPE_HALVES, a.rope.n_rot, ea, eb);
   float w[8];
   if (norm) load8(a.wk + e0, false, w);
-  PairPos<D> axes;
+  PairPos<D, AXES> axes;
   if (turns) axes.look_up(a.rope);
   const unsigned items = (unsigned)a.T * a.nchunk, step = gridDim.x * 8;
   for (unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5); item < items; item += step) {
@@ -272,22 +272,28 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
 }
 
 // blockIdx.y 0: keys, 1: values
-template <int D, int DV, typename TX>
+template <int D, int DV, typename TX, bool AXES>
 __global__ void __launch_bounds__(256, kAppendCtas) k_cache_append(const RowArgs a) {
   after_last();
   lets_next();
-  if (blockIdx.y == 0) append_rows<D, TX, true>(a);
-  else append_rows<DV, TX, false>(a);
+  if (blockIdx.y == 0) append_rows<D, TX, true, AXES>(a);
+  else append_rows<DV, TX, false, AXES>(a);
 }
 
 typedef void (*RowKernel)(const RowArgs);
-template <int D, typename TX>
+template <int D, typename TX, bool AXES>
 static RowKernel pick_append_v(int Dv) {
-  return Dv == 64 ? k_cache_append<D, 64, TX> : Dv == 128 ? k_cache_append<D, 128, TX> : k_cache_append<D, 256, TX>;
+  return Dv == 64 ? k_cache_append<D, 64, TX, AXES> : Dv == 128 ? k_cache_append<D, 128, TX, AXES> : k_cache_append<D, 256, TX, AXES>;
 }
-template <typename TX>
-static RowKernel pick_append(int D, int Dv) {
-  return D == 64 ? pick_append_v<64, TX>(Dv) : D == 128 ? pick_append_v<128, TX>(Dv) : pick_append_v<256, TX>(Dv);
+template <typename TX, bool AXES>
+static RowKernel pick_append_d(int D, int Dv) {
+  return D == 64 ? pick_append_v<64, TX, AXES>(Dv) : D == 128 ? pick_append_v<128, TX, AXES>(Dv) : pick_append_v<256, TX, AXES>(Dv);
+}
+template <bool AXES>
+static RowKernel pick_append(int x_type, int D, int Dv) {
+  return x_type == FA_ACT_F32   ? pick_append_d<float, AXES>(D, Dv)
+         : x_type == FA_ACT_F16 ? pick_append_d<__half, AXES>(D, Dv)
+                                : pick_append_d<__nv_bfloat16, AXES>(D, Dv);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -446,9 +452,7 @@ static fa_status append(const void* k, const void* v, int x_type, const fa_kv_vi
   if ((long long)T * a.nchunk > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const long long blocks = ((long long)T * a.nchunk + 7) / 8;
   const dim3 grid((unsigned)std::min<long long>(blocks, kAppendCtas * nsm), 2);
-  const RowKernel k_append = x_type == FA_ACT_F32   ? pick_append<float>(a.c.D, a.c.Dv)
-                             : x_type == FA_ACT_F16 ? pick_append<__half>(a.c.D, a.c.Dv)
-                                                    : pick_append<__nv_bfloat16>(a.c.D, a.c.Dv);
+  const RowKernel k_append = a.rope.axis ? pick_append<true>(x_type, a.c.D, a.c.Dv) : pick_append<false>(x_type, a.c.D, a.c.Dv);
   return launch_next(k_append, grid, dim3(256), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -557,9 +557,10 @@ __device__ __forceinline__ int pages_of(const Cache& c, int len) {
 }
 // Keys of sequence b: its length; with selected pages the keys of as many of them as there can be, the places of
 // keys that are not there among them (they are masked)
+template <bool SEL>
 __device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
   const int L = seq_len(a, b);
-  return a.sel ? min(a.K, pages_of(a.c, L)) * a.c.page_size : L;
+  return SEL ? min(a.K, pages_of(a.c, L)) * a.c.page_size : L;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
 
@@ -634,20 +635,21 @@ __device__ __forceinline__ T block_scan(T v, T* smem, T* before) {
 }
 
 // Lays out the items of a large batch, whose lengths every CTA would otherwise read and scan: one CTA.
-static __global__ void __launch_bounds__(1024) k_decode_plan(const DecodeArgs a) {
+template <bool SEL>
+__global__ void __launch_bounds__(1024) k_decode_plan(const DecodeArgs a) {
   __shared__ uint64_t s_scan[32];
   after_last();
   const int B = a.c.B;
   uint64_t U = 0, before;
   for (int c0 = 0; c0 < B; c0 += 1024) {
     const int b = c0 + threadIdx.x;
-    U += block_scan<32, uint64_t>(b < B ? tiles_of(seq_keys(a, b)) : 0, s_scan, &before);
+    U += block_scan<32, uint64_t>(b < B ? tiles_of(seq_keys<SEL>(a, b)) : 0, s_scan, &before);
   }
   const int chunk = safe_chunk((long long)U, B, a.R);
   uint64_t base = 0;
   for (int c0 = 0; c0 < B; c0 += 1024) {
     const int b = c0 + threadIdx.x;
-    const uint64_t v = b < B ? pack_counts(tiles_of(seq_keys(a, b)), chunk) : 0;
+    const uint64_t v = b < B ? pack_counts(tiles_of(seq_keys<SEL>(a, b)), chunk) : 0;
     const uint64_t all = block_scan<32, uint64_t>(v, s_scan, &before);
     const Counts at = unpack_counts(base + before), own = unpack_counts(v);
     for (int i = 0; i < own.items; ++i) a.items[at.items + i] = make_int4(b, own.items, i, at.slots + i);
@@ -749,7 +751,8 @@ static __device__ __noinline__ float4 cap_and_bias_sel(float4 x, float cap, floa
 // heads) (blockIdx.x % HG).  Consecutive CTAs take the same keys of the different heads, so a page's
 // neighbouring rows are read at the same time.  Each warp takes every NW-th tile of 16 keys with a ring, a
 // running maximum and sums of its own: no barrier until the item's last tile.
-template <int D, int DV, int KT, int VT>
+// SEL: over selected pages (kernels of their own: the lookups of the plain ones took 1 to 2 % more with both in one).
+template <int D, int DV, int KT, int VT, bool SEL>
 __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
@@ -798,7 +801,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     int n_own = 0;
     for (int c0 = 0; c0 < B; c0 += NW * 32) {
       const int b = c0 + threadIdx.x;
-      n_own = b < B ? tiles_of(seq_keys(a, b)) : 0;
+      n_own = b < B ? tiles_of(seq_keys<SEL>(a, b)) : 0;
       if (b < B) s_tiles[b] = n_own;
       U += block_scan<NW, uint64_t>(n_own, s_scan, &before);
     }
@@ -822,7 +825,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   for (int b = r + a.nitems * threadIdx.x; b < B; b += a.nitems * NW * 32) {
     const int L = a.lens[b];
     if (L > a.c.max_pages * a.c.page_size && hg == 0) report_page(a.c.err);
-    if (L < 0 || seq_keys(a, b) > 0) continue;
+    if (L < 0 || seq_keys<SEL>(a, b) > 0) continue;
     for (int h = head0; h < head0 + nh; ++h) {
       const long long at = (long long)b * a.H + h;
       for (int d = 0; d < DV; ++d) act_store(a.O, a.act, at * DV + d, 0.f);
@@ -832,13 +835,13 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   __syncthreads();
   const int4 item = s_item;
   if (item.x < 0) return;
-  const int b = item.x, keys = seq_keys(a, b);
+  const int b = item.x, keys = seq_keys<SEL>(a, b);
   const long long n_all = tiles_of(keys);
   const int j0 = 16 * (int)(n_all * item.z / item.y);  // the item's keys [j0, j1) and tiles
   const int j1 = min(keys, 16 * (int)(n_all * (item.z + 1) / item.y)), ntile = tiles_of(j1 - j0);
   const bool whole = item.y == 1;
-  const int len = a.sel ? seq_len(a, b) : keys;
-  const int32_t* sel = a.sel ? a.sel + ((long long)b * a.c.Hkv + hk) * a.K : nullptr;
+  const int len = SEL ? seq_len(a, b) : keys;
+  const int32_t* sel = SEL ? a.sel + ((long long)b * a.c.Hkv + hk) * a.K : nullptr;
 
   // ---- rows of a tile: key `lane` & 15 a lane.  Boxes of rows (16 or 8 in one page) go by the tensor maps,
   // else each row is copied by itself.  The first rows of the warp's next 32 boxes are looked up at once, a
@@ -848,7 +851,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     if (j >= j1) return -1;
     int p = (int)((uint64_t)j * a.c.page_mul >> a.c.page_shift);
     const int in = j - p * a.c.page_size;
-    if (sel) {
+    if (SEL) {
       p = sel[p];
       if (p < 0 || p >= pages_of(a.c, len)) return -1;
       there = len - (p * a.c.page_size + in);
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       found_at = turn;
     }
     const int from = (turn - found_at) * boxes + (a.box == 8 ? (lane >> 3) & 1 : 0);
-    if (sel) there = __shfl_sync(kFull, found_there, from);
+    if (SEL) there = __shfl_sync(kFull, found_there, from);
     return __shfl_sync(kFull, found, from);
   };
   // by slot (keys: bits 0 .. 3, values: 4 .. 7): parity awaited, copies under way, mask or places not the usual ones
@@ -880,7 +883,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
     const int pitch = kv ? PV : PK;
     armed |= 1u << (4 * kv + slot);
     int n = min(16, j1 - (j0 + tile * 16));  // the rows behind them are not used
-    if (sel) n = a.box == 16 ? min(16, there) : min(8, there) + (lane & 8);  // (a.box == 8: of the lane's box)
+    if (SEL) n = a.box == 16 ? min(16, there) : min(8, there) + (lane & 8);  // (a.box == 8: of the lane's box)
     const CUtensorMap* map = kv ? &map_v : &map_k;
     const int x = kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK);
     // A slot's mask and its value rows' places are rewritten for a tile with rows missing, and after one.
@@ -1013,7 +1016,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       for (int i = 0; i < 4; ++i) s[i] *= qscale;
       if (ext) {
         const float4 y = make_float4(s[0], s[1], s[2], s[3]);
-        const float4 x = sel && a.alibi ? cap_and_bias_sel(y, a.softcap, slope, a.c, sel, a.K, j0 + tile * 16 + 2 * t, len)
+        const float4 x = SEL && a.alibi ? cap_and_bias_sel(y, a.softcap, slope, a.c, sel, a.K, j0 + tile * 16 + 2 * t, len)
                                         : cap_and_bias(y, a.softcap, slope, j0 + tile * 16 + 2 * t - (keys - 1));
         s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
       }
@@ -1199,49 +1202,49 @@ __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
 
 typedef cudaError_t (*DecodeFn)(DecodeArgs a, const DecodeMaps& m, cudaStream_t s);
 
-template <int D, int DV, int KT, int VT>
+template <int D, int DV, int KT, int VT, bool SEL>
 cudaError_t run_decode(DecodeArgs a, const DecodeMaps& m, cudaStream_t s) {
   constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
   a.lift = weight_lift(VT);
   static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
   cudaError_t e = cudaSuccess;
-  if (!allow_smem(reinterpret_cast<const void*>(k_decode<D, DV, KT, VT>), C.smem, &ready)) return cudaErrorInvalidValue;
-  if (a.items && (e = launch_next(k_decode_plan, dim3(1), dim3(1024), 0, s, a)) != cudaSuccess) return e;
-  e = launch_next(k_decode<D, DV, KT, VT>, dim3((unsigned)(a.nitems * a.HG)), dim3(kWarps * 32), C.smem, s, a, m.k, m.v);
+  if (!allow_smem(reinterpret_cast<const void*>(k_decode<D, DV, KT, VT, SEL>), C.smem, &ready)) return cudaErrorInvalidValue;
+  if (a.items && (e = launch_next(k_decode_plan<SEL>, dim3(1), dim3(1024), 0, s, a)) != cudaSuccess) return e;
+  e = launch_next(k_decode<D, DV, KT, VT, SEL>, dim3((unsigned)(a.nitems * a.HG)), dim3(kWarps * 32), C.smem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
   if (a.njobs > 0) return launch_next(k_decode_join<DV>, dim3(a.njobs, a.H), dim3(512), 0, s, a);
   return cudaSuccess;
 }
-template <int D, int DV, int KT>
+template <int D, int DV, int KT, bool SEL>
 DecodeFn pick_decode_v(int vt) {
   switch (vt) {
-    case FA_F32: return run_decode<D, DV, KT, FA_F32>;
-    case FA_F16: return run_decode<D, DV, KT, FA_F16>;
-    case FA_Q8_0: return run_decode<D, DV, KT, FA_Q8_0>;
+    case FA_F32: return run_decode<D, DV, KT, FA_F32, SEL>;
+    case FA_F16: return run_decode<D, DV, KT, FA_F16, SEL>;
+    case FA_Q8_0: return run_decode<D, DV, KT, FA_Q8_0, SEL>;
   }
-  return run_decode<D, DV, KT, FA_Q4_0>;
+  return run_decode<D, DV, KT, FA_Q4_0, SEL>;
 }
-// The kernel for D and the key type KT; a translation unit each, so that they compile in parallel.
-template <int D, int KT>
+// The kernel for D and the key type KT, over all pages or selected ones; a translation unit each, so that they
+// compile in parallel.
+template <int D, int KT, bool SEL>
 DecodeFn pick_decode(int Dv, int vt);
-template <> DecodeFn pick_decode<64, FA_F32>(int, int);
-template <> DecodeFn pick_decode<64, FA_F16>(int, int);
-template <> DecodeFn pick_decode<64, FA_Q8_0>(int, int);
-template <> DecodeFn pick_decode<64, FA_Q4_0>(int, int);
-template <> DecodeFn pick_decode<128, FA_F32>(int, int);
-template <> DecodeFn pick_decode<128, FA_F16>(int, int);
-template <> DecodeFn pick_decode<128, FA_Q8_0>(int, int);
-template <> DecodeFn pick_decode<128, FA_Q4_0>(int, int);
-template <> DecodeFn pick_decode<256, FA_F32>(int, int);
-template <> DecodeFn pick_decode<256, FA_F16>(int, int);
-template <> DecodeFn pick_decode<256, FA_Q8_0>(int, int);
-template <> DecodeFn pick_decode<256, FA_Q4_0>(int, int);
-#define FAP_INSTANTIATE_DECODE(D, KT)                              \
+#define FAP_DECLARE_DECODE(D, SEL)                                 \
+  template <> DecodeFn pick_decode<D, FA_F32, SEL>(int, int);      \
+  template <> DecodeFn pick_decode<D, FA_F16, SEL>(int, int);      \
+  template <> DecodeFn pick_decode<D, FA_Q8_0, SEL>(int, int);     \
+  template <> DecodeFn pick_decode<D, FA_Q4_0, SEL>(int, int);
+FAP_DECLARE_DECODE(64, false)
+FAP_DECLARE_DECODE(64, true)
+FAP_DECLARE_DECODE(128, false)
+FAP_DECLARE_DECODE(128, true)
+FAP_DECLARE_DECODE(256, false)
+FAP_DECLARE_DECODE(256, true)
+#define FAP_INSTANTIATE_DECODE(D, KT, SEL)                         \
   template <>                                                      \
-  DecodeFn pick_decode<D, KT>(int Dv, int vt) {                    \
-    return Dv == 64    ? pick_decode_v<D, 64, KT>(vt)              \
-           : Dv == 128 ? pick_decode_v<D, 128, KT>(vt)             \
-                       : pick_decode_v<D, 256, KT>(vt);            \
+  DecodeFn pick_decode<D, KT, SEL>(int Dv, int vt) {               \
+    return Dv == 64    ? pick_decode_v<D, 64, KT, SEL>(vt)         \
+           : Dv == 128 ? pick_decode_v<D, 128, KT, SEL>(vt)        \
+                       : pick_decode_v<D, 256, KT, SEL>(vt);       \
   }
 
 }  // namespace fap

@@ -2,5 +2,5 @@
 #include "fa_decode.cuh"
 
 namespace fap {
-FAP_INSTANTIATE_DECODE(128, FA_Q8_0)
+FAP_INSTANTIATE_DECODE(128, FA_Q8_0, false)
 }  // namespace fap

@@ -2,5 +2,5 @@
 #include "fa_decode.cuh"
 
 namespace fap {
-FAP_INSTANTIATE_DECODE(64, FA_Q4_0)
+FAP_INSTANTIATE_DECODE(64, FA_Q4_0, false)
 }  // namespace fap

@@ -1,0 +1,6 @@
+// Single-token attention over selected pages, D = 64, f16 keys: every Dv and value type.
+#include "fa_decode.cuh"
+
+namespace fap {
+FAP_INSTANTIATE_DECODE(64, FA_F16, true)
+}  // namespace fap

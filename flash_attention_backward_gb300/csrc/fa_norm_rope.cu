@@ -131,7 +131,9 @@ static fa_status forward(const void* q, const void* k, int x_type, const fa_qk_v
   long long grid = (items + 7) / 8;
   const int ctas = x_type == FA_ACT_F32 ? kForwardCtas<float> : kForwardCtas<__half>;
   if (ctas) grid = std::min<long long>(grid, (long long)ctas * nsm);
-  return launch_next(pick_norm_fwd(D, x_type, y_type, a.vec, a.rope.style), dim3((unsigned)grid), dim3(256), 0,
+  const NormKernel k_norm = a.rope.axis ? pick_norm_fwd<true>(D, x_type, y_type, a.vec, a.rope.style)
+                                        : pick_norm_fwd<false>(D, x_type, y_type, a.vec, a.rope.style);
+  return launch_next(k_norm, dim3((unsigned)grid), dim3(256), 0,
                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
@@ -174,7 +176,8 @@ static fa_status backward(const void* gq, const void* gk, int y_type, const void
   a.side[0].gy = gq, a.side[1].gy = gk, a.side[0].y = dq, a.side[1].y = dk;
   a.part = static_cast<float*>(workspace);
   a.err = err;
-  const BackKernel k_back = pick_norm_back(D, x_type, y_type, a.vec, a.rope.style);
+  const BackKernel k_back = a.rope.axis ? pick_norm_back<true>(D, x_type, y_type, a.vec, a.rope.style)
+                                        : pick_norm_back<false>(D, x_type, y_type, a.vec, a.rope.style);
   for (NormSide& sd : a.side) sd.nchunk = (sd.H + k_back.heads - 1) / k_back.heads;
   // CTAs shared out by the heads of either side; every side that has heads gets one
   const long long iq = (long long)N * a.side[0].nchunk, ik = (long long)N * a.side[1].nchunk;

@@ -175,7 +175,7 @@ struct Lane {
 // keep more loads in flight (2048 tokens of 28 heads of 256: 17.7 us, and 23.9 the other way).
 template <typename TX>
 constexpr int kForwardCtas = sizeof(TX) == 2 ? 3 : 0;  // CTAs an SM, or 0: a warp takes one item
-template <int D, typename TX, typename TY, bool VEC, int STYLE>
+template <int D, typename TX, typename TY, bool VEC, int STYLE, bool AXES>
 __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormArgs a) {
   constexpr int GW = 256 / D, U = kRows<TX>;
   after_last();
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
     lanes[k].place(a.rope);
     if (ON) lanes[k].weights(a.side[k].w);
   }
-  PairPos<D> axes;
+  PairPos<D, AXES> axes;
   axes.look_up(a.rope);
   for (unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5); item < items; item += gridDim.x * 8u) {
     const int n = item / (unsigned)a.nchunk, c0 = (int)(item - (unsigned)n * a.nchunk) * a.HC;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
       if (!ON) ln.weights(sd.w);
       if (!turned) {
         int pos[D / 64];
-        axes.at(a.rope, n, a.rope.n_rot ? a.rope.pos[n] : 0, pos);
+        axes.at(a.rope, n, !AXES && a.rope.n_rot ? a.rope.pos[n] : 0, pos);
         lanes[0].turn(a.rope, pos, 1.f);
       }
       turned = true;
@@ -301,7 +301,7 @@ __device__ __forceinline__ void sum_dw(const NormArgs& a, float (*red)[D]) {
   }
 }
 
-template <int D, typename TX, typename TY, int STYLE>
+template <int D, typename TX, typename TY, int STYLE, bool AXES>
 __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(const NormArgs a) {
   constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>, GB = HC * D * sizeof(TY), XB = HC * D * sizeof(TX), S = kBackSlots<TX, TY>;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
     if (fetched < last) fetch(i);
   int slot = 0, token = -1;
   uint32_t phase = 0;
-  PairPos<D> axes;
+  PairPos<D, AXES> axes;
   axes.look_up(a.rope);
   int pos[D / 64] = {};
   auto pos_of = [&](int t) {
-    if (a.rope.n_rot && t < a.N) axes.at(a.rope, t, a.rope.pos[t], pos);
+    if (a.rope.n_rot && t < a.N) axes.at(a.rope, t, AXES ? 0 : a.rope.pos[t], pos);
   };
   pos_of(n);
   unsigned run = dw_run(last - first);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
 }
 
 // The gradient where heads of x do not start on 16 bytes: element by element.
-template <int D, typename TX, typename TY, int STYLE>
+template <int D, typename TX, typename TY, int STYLE, bool AXES>
 __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_any(const NormArgs a) {
   constexpr int GW = 256 / D, HC = kBackHeads<D, TX, TY>;
   __shared__ __align__(16) float red[kBackWarps * GW][D];
@@ -424,13 +424,13 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_a
   ln.weights(sd.w);
   unsigned run = dw_run(items / (ctas * kBackWarps));
   bool put = false;
-  PairPos<D> axes;
+  PairPos<D, AXES> axes;
   axes.look_up(a.rope);
   for (unsigned item = cta * kBackWarps + warp; item < items; item += ctas * kBackWarps) {
     const int n = item / (unsigned)sd.nchunk, h0 = (int)(item - (unsigned)n * sd.nchunk) * HC, cnt = min(sd.H - h0, HC);
     const long long at = ((long long)n * sd.H + h0) * D;
     int pos[D / 64];
-    axes.at(a.rope, n, a.rope.n_rot ? a.rope.pos[n] : 0, pos);
+    axes.at(a.rope, n, !AXES && a.rope.n_rot ? a.rope.pos[n] : 0, pos);
     ln.turn(a.rope, pos, -1.f);
 #pragma unroll 1
     for (int k = 0; k < cnt; k += GW) {
@@ -459,14 +459,55 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_a
 
 typedef void (*NormKernel)(const NormArgs);
 
-// The kernels for these types (fa_norm_rope_fwd.cu, fa_norm_rope_back.cu); of the gradient's, the heads of an
-// item and what there is to know of its dynamic shared memory too.
+// The kernels for these types, with positions of one axis or of several; of the gradient's, the heads of an item and
+// what there is to know of its dynamic shared memory too.
+template <bool AXES>
 NormKernel pick_norm_fwd(int D, int tx, int ty, bool vec, int style);
+template <> NormKernel pick_norm_fwd<false>(int, int, int, bool, int);  // fa_norm_rope_fwd.cu
+template <> NormKernel pick_norm_fwd<true>(int, int, int, bool, int);   // fa_norm_axes_fwd.cu
 struct BackKernel {
   NormKernel fn;
   int heads, smem;
   std::atomic<uint64_t>* ready;  // devices that `smem` bytes have been allowed on
 };
+template <bool AXES>
 BackKernel pick_norm_back(int D, int tx, int ty, bool vec, int style);
+template <> BackKernel pick_norm_back<false>(int, int, int, bool, int);  // fa_norm_rope_back.cu
+template <> BackKernel pick_norm_back<true>(int, int, int, bool, int);   // fa_norm_axes_back.cu
+
+// How these files choose among what they instantiate
+template <int D, typename TX, typename TY, bool AXES>
+NormKernel norm_fwd_style(bool vec, int style) {
+  if (style == FA_ROPE_PAIRS) return vec ? k_norm_rope<D, TX, TY, true, FA_ROPE_PAIRS, AXES> : k_norm_rope<D, TX, TY, false, FA_ROPE_PAIRS, AXES>;
+  return vec ? k_norm_rope<D, TX, TY, true, FA_ROPE_HALVES, AXES> : k_norm_rope<D, TX, TY, false, FA_ROPE_HALVES, AXES>;
+}
+template <int D, typename TX, typename TY, bool AXES>
+BackKernel norm_back_style(bool vec, int style) {
+  constexpr int heads = kBackHeads<D, TX, TY>, ring = kBackWarps * kBackSlots<TX, TY> * heads * D * (int)(sizeof(TX) + sizeof(TY));
+  const bool pairs = style == FA_ROPE_PAIRS;
+  static std::atomic<uint64_t> ready[2];
+  if (!vec)
+    return BackKernel{pairs ? k_norm_rope_back_any<D, TX, TY, FA_ROPE_PAIRS, AXES> : k_norm_rope_back_any<D, TX, TY, FA_ROPE_HALVES, AXES>,
+                      heads, 0, nullptr};
+  return BackKernel{pairs ? k_norm_rope_back<D, TX, TY, FA_ROPE_PAIRS, AXES> : k_norm_rope_back<D, TX, TY, FA_ROPE_HALVES, AXES>, heads,
+                    ring, &ready[pairs]};
+}
+#define FAP_PICK_NORM(KIND, PICK, STYLE_OF, AXES)                                                   \
+  template <int D, typename TX>                                                                     \
+  static KIND PICK##_y(int ty, bool vec, int style) {                                               \
+    return ty == FA_ACT_F32   ? STYLE_OF<D, TX, float, AXES>(vec, style)                            \
+           : ty == FA_ACT_F16 ? STYLE_OF<D, TX, __half, AXES>(vec, style)                           \
+                              : STYLE_OF<D, TX, __nv_bfloat16, AXES>(vec, style);                   \
+  }                                                                                                 \
+  template <int D>                                                                                  \
+  static KIND PICK##_x(int tx, int ty, bool vec, int style) {                                       \
+    return tx == FA_ACT_F32   ? PICK##_y<D, float>(ty, vec, style)                                  \
+           : tx == FA_ACT_F16 ? PICK##_y<D, __half>(ty, vec, style)                                 \
+                              : PICK##_y<D, __nv_bfloat16>(ty, vec, style);                         \
+  }                                                                                                 \
+  template <>                                                                                       \
+  KIND PICK<AXES>(int D, int tx, int ty, bool vec, int style) {                                     \
+    return D == 64 ? PICK##_x<64>(tx, ty, vec, style) : D == 128 ? PICK##_x<128>(tx, ty, vec, style) : PICK##_x<256>(tx, ty, vec, style); \
+  }
 
 }  // namespace fap

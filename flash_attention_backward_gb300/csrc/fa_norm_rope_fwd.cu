@@ -4,31 +4,6 @@
 
 namespace fap {
 
-template <int D, typename TX, typename TY>
-static NormKernel pick_style(bool vec, int style) {
-  if (style == FA_ROPE_PAIRS) return vec ? k_norm_rope<D, TX, TY, true, FA_ROPE_PAIRS> : k_norm_rope<D, TX, TY, false, FA_ROPE_PAIRS>;
-  return vec ? k_norm_rope<D, TX, TY, true, FA_ROPE_HALVES> : k_norm_rope<D, TX, TY, false, FA_ROPE_HALVES>;
-}
-template <int D, typename TX>
-static NormKernel pick_y(int ty, bool vec, int style) {
-  switch (ty) {
-    case FA_ACT_F32: return pick_style<D, TX, float>(vec, style);
-    case FA_ACT_F16: return pick_style<D, TX, __half>(vec, style);
-  }
-  return pick_style<D, TX, __nv_bfloat16>(vec, style);
-}
-template <int D>
-static NormKernel pick_x(int tx, int ty, bool vec, int style) {
-  switch (tx) {
-    case FA_ACT_F32: return pick_y<D, float>(ty, vec, style);
-    case FA_ACT_F16: return pick_y<D, __half>(ty, vec, style);
-  }
-  return pick_y<D, __nv_bfloat16>(ty, vec, style);
-}
-NormKernel pick_norm_fwd(int D, int tx, int ty, bool vec, int style) {
-  return D == 64    ? pick_x<64>(tx, ty, vec, style)
-         : D == 128 ? pick_x<128>(tx, ty, vec, style)
-                    : pick_x<256>(tx, ty, vec, style);
-}
+FAP_PICK_NORM(NormKernel, pick_norm_fwd, norm_fwd_style, false)
 
 }  // namespace fap

@@ -58,14 +58,18 @@ static DecodePlan plan_decode(const Cache& c, int H, int K, int nsm) {
   return p;
 }
 
-template <int D>
+template <int D, bool SEL>
 static DecodeFn pick_decode_k(const Cache& c) {
   switch (c.k_type) {
-    case FA_F32: return pick_decode<D, FA_F32>(c.Dv, c.v_type);
-    case FA_F16: return pick_decode<D, FA_F16>(c.Dv, c.v_type);
-    case FA_Q8_0: return pick_decode<D, FA_Q8_0>(c.Dv, c.v_type);
+    case FA_F32: return pick_decode<D, FA_F32, SEL>(c.Dv, c.v_type);
+    case FA_F16: return pick_decode<D, FA_F16, SEL>(c.Dv, c.v_type);
+    case FA_Q8_0: return pick_decode<D, FA_Q8_0, SEL>(c.Dv, c.v_type);
   }
-  return pick_decode<D, FA_Q4_0>(c.Dv, c.v_type);
+  return pick_decode<D, FA_Q4_0, SEL>(c.Dv, c.v_type);
+}
+template <bool SEL>
+static DecodeFn pick_decode_d(const Cache& c) {
+  return c.D == 64 ? pick_decode_k<64, SEL>(c) : c.D == 128 ? pick_decode_k<128, SEL>(c) : pick_decode_k<256, SEL>(c);
 }
 
 }  // namespace fap
@@ -118,7 +122,7 @@ static fa_status decode(const void* q, int act, int64_t q_row, int64_t q_head, c
   if (a.box && (!map_pool(&m.k, a.c.k, rows, a.c.Hkv, a.c.rbk, smem_pitch(a.c.rbk), a.box) ||
                 !map_pool(&m.v, a.c.v, rows, a.c.Hkv, a.c.rbv, smem_pitch(a.c.rbv), a.box)))
     return FA_ERR_CUDA;
-  const DecodeFn run = a.c.D == 64 ? pick_decode_k<64>(a.c) : a.c.D == 128 ? pick_decode_k<128>(a.c) : pick_decode_k<256>(a.c);
+  const DecodeFn run = pages ? pick_decode_d<true>(a.c) : pick_decode_d<false>(a.c);
   return run(a, m, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
