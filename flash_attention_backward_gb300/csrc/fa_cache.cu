@@ -234,7 +234,7 @@ __device__ __forceinline__ void append_rows(const RowArgs& a) {
     Turn8<D> turn;
     if (turns) {
       int at[D / 64];
-      axes.at(a.rope, t, pos, at);
+      axes.hand_round(AXES ? axes.load(a.rope, t) : pos, at);
       turn.set(a.rope, at, e0);
     }
 #pragma unroll 1

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256, kForwardCtas<TX>) k_norm_rope(const NormA
       if (!ON) ln.weights(sd.w);
       if (!turned) {
         int pos[D / 64];
-        axes.at(a.rope, n, !AXES && a.rope.n_rot ? a.rope.pos[n] : 0, pos);
+        axes.hand_round(AXES || a.rope.n_rot ? axes.load(a.rope, n) : 0, pos);
         lanes[0].turn(a.rope, pos, 1.f);
       }
       turned = true;
@@ -349,18 +349,16 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back(c
   uint32_t phase = 0;
   PairPos<D, AXES> axes;
   axes.look_up(a.rope);
-  int pos[D / 64] = {};
-  auto pos_of = [&](int t) {
-    if (a.rope.n_rot && t < a.N) axes.at(a.rope, t, AXES ? 0 : a.rope.pos[t], pos);
-  };
-  pos_of(n);
+  auto pos_of = [&](int t) { return a.rope.n_rot && t < a.N ? axes.load(a.rope, t) : 0; };
+  int pos = pos_of(n);
   unsigned run = dw_run(last - first);
   bool put = false;  // sums lie in `red` already
   for (unsigned item = first; item < last; ++item) {
     if (n != token) {
-      ln.turn(a.rope, pos, -1.f);
-      token = n;
-      pos_of(n + 1);  // the next token's, in time
+      int at[D / 64];
+      axes.hand_round(pos, at);
+      ln.turn(a.rope, at, -1.f);
+      token = n, pos = pos_of(n + 1);  // the next token's, in time
     }
     const bool came = a.wait_ns > 0 && fab::mbar_wait_bounded(&s_bar[warp][slot], phase, a.wait_ns);
     if (!__all_sync(kFull, came)) {  // let the copies in flight land, then give up
@@ -430,7 +428,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, kBackCtas) k_norm_rope_back_a
     const int n = item / (unsigned)sd.nchunk, h0 = (int)(item - (unsigned)n * sd.nchunk) * HC, cnt = min(sd.H - h0, HC);
     const long long at = ((long long)n * sd.H + h0) * D;
     int pos[D / 64];
-    axes.at(a.rope, n, !AXES && a.rope.n_rot ? a.rope.pos[n] : 0, pos);
+    axes.hand_round(a.rope.n_rot ? axes.load(a.rope, n) : 0, pos);
     ln.turn(a.rope, pos, -1.f);
 #pragma unroll 1
     for (int k = 0; k < cnt; k += GW) {

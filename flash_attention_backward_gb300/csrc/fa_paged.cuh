@@ -92,25 +92,31 @@ struct Rope {
 };
 
 // A warp's lanes share out a token's D / 2 pairs, D / 64 neighbouring ones each: the positions of a lane's pairs.
-// With several axes a lane looks its pairs' axes up once, a byte each, and loads a position for each.  (In kernels of
-// their own: with both in one the plain rotation of 2048 tokens of 28 heads of 256, f32, took 25.7 us for 21.2.)
+// With several axes a lane looks its pairs' axes up once, a byte each, and of a token lane a loads axis a's position
+// and hands it round.  (In kernels of their own: with both in one the plain rotation of 2048 tokens of 28 heads of 256,
+// f32, took 25.7 us for 21.2.)
 template <int D, bool AXES>
 struct PairPos {
   static constexpr int P = D / 64;
   uint32_t axes = 0;
 
   __device__ __forceinline__ void look_up(const Rope& r) {
-    if (!AXES) return;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+    for (int i = 0; AXES && i < P; ++i) {
       const int pair = (int)(threadIdx.x & 31) * P + i;
       if (pair < r.n_rot >> 1) axes |= (uint32_t)min((int)r.axis[pair], r.n_axes - 1) << (8 * i);
     }
   }
-  // Of token n; p where there is one axis.
-  __device__ __forceinline__ void at(const Rope& r, long long n, int p, int (&pos)[P]) const {
+  // Of token n: what this lane loads...
+  __device__ __forceinline__ int load(const Rope& r, long long n) const {
+    if (!AXES) return r.pos[n];
+    const int lane = threadIdx.x & 31;
+    return lane < r.n_axes ? r.pos[lane * r.stride + n] : 0;
+  }
+  // ...and what its pairs get (all lanes of the warp take part)
+  __device__ __forceinline__ void hand_round(int mine, int (&pos)[P]) const {
 #pragma unroll
-    for (int i = 0; i < P; ++i) pos[i] = AXES ? r.pos[(axes >> (8 * i) & 255) * r.stride + n] : p;
+    for (int i = 0; i < P; ++i) pos[i] = AXES ? __shfl_sync(kFull, mine, axes >> (8 * i) & 255) : mine;
   }
 };
 
@@ -289,6 +295,22 @@ __device__ __forceinline__ long long cache_row(const Cache& c, int b, int j) {
 __device__ __forceinline__ void after_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void lets_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// ---- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// (arrive releases and wait acquires at cluster scope)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_barrier() { cluster_arrive(), cluster_wait(); }
+
 // ---- host
 template <typename... P, typename... A>
 inline cudaError_t launch_next(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
@@ -297,6 +319,18 @@ inline cudaError_t launch_next(void (*k)(P...), dim3 grid, dim3 block, size_t sm
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+// The same for clusters of `cluster` CTAs
+template <typename... P, typename... A>
+inline cudaError_t launch_clusters(void (*k)(P...), unsigned grid, unsigned cluster, unsigned block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(block), cfg.dynamicSmemBytes = smem, cfg.stream = s, cfg.attrs = at, cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
 }
 // Allows a kernel's dynamic shared memory on the current device, once for each (ready: the devices so far).

@@ -30,20 +30,6 @@ struct ListArgs {
   __device__ __forceinline__ int on_stack() const { return min(max(num_free[0], 0), num_pages); }
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_ctas() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// (arrive releases and wait acquires at cluster scope)
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t add_cap(uint32_t a, uint32_t b) { return min(a + b, kCap); }  // a, b <= kCap
 
 // Sums of (x, y) over the threads before this one, and over all of them, stopping at kCap (s: 33 words each).
@@ -218,14 +204,7 @@ static fa_status check_lists(const fa_page_lists* l, const int32_t* arg, ListArg
 static cudaError_t launch_lists(void (*k)(const ListArgs), long long work, const ListArgs& a, cudaStream_t s) {
   int ctas = 1;
   while (ctas < kMostCtas && work > 4LL * kThreads * ctas) ctas *= 2;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)ctas, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas), cfg.blockDim = dim3(kThreads), cfg.stream = s, cfg.attrs = at, cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, a);
+  return launch_clusters(k, (unsigned)ctas, (unsigned)ctas, kThreads, 0, s, a);
 }
 
 }  // namespace fap

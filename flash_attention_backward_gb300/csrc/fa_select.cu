@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "fa_paged.cuh"
+#include "sm100.cuh"
 
 namespace fap {
 
@@ -192,224 +193,279 @@ __device__ __forceinline__ float act_at(const void* p, int act, long long i) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-constexpr int kScoreWarps = 4, kScoreHeads = 16;  // query heads whose codes lie in shared memory at a time
-
-// A lane takes a block of 32 components of a page's bounds, D / 32 lanes a page; a CTA `chunk` pages of one sequence
-// and KV head for all its query heads.
+// q of `ng` query heads from h0 on in 8 bits: a warp a block, a lane a component (WARPS warps of the CTA).
+constexpr int kHeads = 16;  // query heads whose codes lie in shared memory at a time
 template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) k_page_scores(const SelectArgs a) {
-  constexpr int NB = D / 32, PW = 32 / NB;  // blocks; pages that a warp takes at a time
-  __shared__ __align__(16) uint32_t s_q[kScoreHeads][D / 4];
-  __shared__ float s_e[kScoreHeads][NB];
-  after_last();
-  lets_next();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane & (NB - 1);
-  const unsigned hk = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv;
-  const int b = rest / a.chunks, c0 = (rest % a.chunks) * a.chunk;
-  const int L = len_of(a.c, a.lens, b), n = pages_of(a.c, L);
-  if (c0 >= n || n <= a.K) return;  // (all pages are taken then)
-  const int c1 = min(n, c0 + a.chunk);
-  uint32_t* keys = a.keys + ((long long)b * a.c.Hkv + hk) * a.c.max_pages;
-  for (int g0 = 0; g0 < a.G; g0 += kScoreHeads) {
-    const int ng = min(kScoreHeads, a.G - g0), h0 = (int)hk * a.G + g0;
-    if (g0) __syncthreads();
-    // q in 8 bits: a warp a block, a lane a component
-    for (int i = warp; i < ng * NB; i += kScoreWarps) {
-      const int g = i / NB, k = i % NB;
-      const float x = act_at(a.q, a.act, b * a.q_row + (h0 + g) * a.q_head + k * 32 + lane);
-      const float m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(x))));
-      const bool some = m > kTinyAmax;
-      const int c = some ? max(-127, min(127, __float2int_rn(__fmul_rn(x, __fdiv_rn(127.f, m))))) : 0;
-      reinterpret_cast<int8_t*>(s_q[g])[k * 32 + lane] = (int8_t)c;
-      if (lane == 0) s_e[g][k] = some ? __fdiv_rn(m, 127.f) : 0.f;
+struct Codes {
+  uint32_t q[kHeads][D / 4];
+  float e[kHeads][D / 32];
+};
+template <int D, int WARPS>
+__device__ __forceinline__ void quantise_q(const SelectArgs& a, Codes<D>& s, int b, int h0, int ng) {
+  constexpr int NB = D / 32;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i = threadIdx.x >> 5; i < ng * NB; i += WARPS) {
+    const int g = i / NB, k = i % NB;
+    const float x = act_at(a.q, a.act, b * a.q_row + (h0 + g) * a.q_head + k * 32 + lane);
+    const float m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(x))));
+    const bool some = m > kTinyAmax;
+    const int c = some ? max(-127, min(127, __float2int_rn(__fmul_rn(x, __fdiv_rn(127.f, m))))) : 0;
+    reinterpret_cast<int8_t*>(s.q[g])[k * 32 + lane] = (int8_t)c;
+    if (lane == 0) s.e[g][k] = some ? __fdiv_rn(m, 127.f) : 0.f;
+  }
+}
+
+// A block of 32 components of a page's bounds
+struct Block {
+  uint4 hi[2], lo[2];
+  float d;
+};
+template <int D>
+__device__ __forceinline__ void load_block(const SelectArgs& a, int page, unsigned hk, int blk, Block& x) {
+  if (page >= 0) {
+    const long long rec = (long long)page * a.c.Hkv + hk;
+    const uint4* p = reinterpret_cast<const uint4*>(a.codes + rec * 2 * D) + 2 * blk;
+    x.hi[0] = p[0], x.hi[1] = p[1], x.lo[0] = p[D / 16], x.lo[1] = p[D / 16 + 1];
+    x.d = a.scales[rec * (D / 32) + blk];
+  } else {  // no page: nothing to read, and none may exist
+    x.hi[0] = x.hi[1] = x.lo[0] = x.lo[1] = make_uint4(0, 0, 0, 0);
+    x.d = 0.f;
+  }
+}
+// The largest score of `ng` query heads for the page whose blocks D / 32 neighbouring lanes hold; far: the
+// distance of its last key
+template <int D>
+__device__ __forceinline__ float best_score(const SelectArgs& a, const Codes<D>& s, const Block& x, int blk, int h0, int ng, float far) {
+  const uint32_t hi[8] = {x.hi[0].x, x.hi[0].y, x.hi[0].z, x.hi[0].w, x.hi[1].x, x.hi[1].y, x.hi[1].z, x.hi[1].w};
+  const uint32_t lo[8] = {x.lo[0].x, x.lo[0].y, x.lo[0].z, x.lo[0].w, x.lo[1].x, x.lo[1].y, x.lo[1].z, x.lo[1].w};
+  float best = -INFINITY;
+#pragma unroll 2
+  for (int g = 0; g < ng; ++g) {
+    const uint4* qv = reinterpret_cast<const uint4*>(s.q[g]) + 2 * blk;
+    const uint4 q0 = qv[0], q1 = qv[1];
+    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    int I = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t neg;  // 0xff in the bytes of negative codes
+      asm("prmt.b32 %0, %1, %1, 0xba98;" : "=r"(neg) : "r"(qw[i]));
+      I = __dp4a((int)((hi[i] & ~neg) | (lo[i] & neg)), (int)qw[i], I);
     }
+    float t = __fmul_rn(__fmul_rn((float)I, x.d), s.e[g][blk]);
+#pragma unroll
+    for (int o = 1; o < D / 32; o <<= 1) t = __fadd_rn(t, __shfl_xor_sync(kFull, t, o));
+    t = __fmul_rn(t, a.scale);
+    if (a.alibi) t = __fadd_rn(t, __fmul_rn(a.alibi[h0 + g], far));
+    best = fmaxf(best, t != t ? INFINITY : t);
+  }
+  return best;
+}
+
+// The scores of pages [c0, c1) of sequence b (length L, n pages) and KV head hk as keys, through put(page, key) and,
+// where the query heads do not lie in shared memory at once, get(page).  A lane takes a block of 32 components, D / 32
+// lanes a page; a warp looks 32 page numbers up at once and has the next pages' bounds under way while it works.
+template <int D, int WARPS, typename Put, typename Get>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, Codes<D>& s, int b, unsigned hk, int L, int n, int c0, int c1, Put put, Get get) {
+  constexpr int NB = D / 32, PW = 32 / NB, STEP = WARPS * PW;  // blocks; pages that a warp, and the CTA, takes at a time
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane & (NB - 1), mine = lane / NB;
+  for (int g0 = 0; g0 < a.G; g0 += kHeads) {
+    const int ng = min(kHeads, a.G - g0), h0 = (int)hk * a.G + g0;
+    int found = -1;
+    auto look_up = [&](int p0) {  // the warp's next NB turns, from page p0 on
+      const int p = p0 + (lane / PW) * STEP + lane % PW;
+      found = p < c1 ? a.c.table[(long long)b * a.c.max_pages + p] : -1;
+      if (found < 0 || found >= a.c.num_pages) {
+        if (p < c1) report_page(a.c.err);
+        found = -1;
+      }
+    };
+    const int first = c0 + warp * PW;
+    int turn = 0;  // of the look-up
+    Block x, y;
+    int page = -1;
+    look_up(first);
+    if (first < c1) page = __shfl_sync(kFull, found, mine), load_block<D>(a, page, hk, blk, x);
+    if (g0) __syncthreads();
+    quantise_q<D, WARPS>(a, s, b, h0, ng);
     __syncthreads();
-    for (int p0 = c0 + warp * PW; p0 < c1; p0 += kScoreWarps * PW) {
-      const int p = p0 + lane / NB;
-      const bool on = p < c1;
-      const int page = a.c.table[(long long)b * a.c.max_pages + min(p, c1 - 1)];
-      const bool there = page >= 0 && page < a.c.num_pages;
-      if (!there && on && blk == 0 && g0 == 0) report_page(a.c.err);
-      const long long rec = (long long)(there ? page : 0) * a.c.Hkv + hk;
-      const uint4* bounds = reinterpret_cast<const uint4*>(a.codes + rec * 2 * D) + 2 * blk;
-      uint4 h4[2], l4[2];
-      float d = 0.f;
-      if (there) {  // (no page: nothing to read, and none may exist)
-        h4[0] = bounds[0], h4[1] = bounds[1], l4[0] = bounds[D / 16], l4[1] = bounds[D / 16 + 1];
-        d = a.scales[rec * NB + blk];
-      } else {
-        h4[0] = h4[1] = l4[0] = l4[1] = make_uint4(0, 0, 0, 0);
+    for (int p0 = first; p0 < c1; p0 += STEP) {
+      int page2 = -1;
+      if (p0 + STEP < c1) {
+        if (++turn == NB) turn = 0, look_up(p0 + STEP);
+        page2 = __shfl_sync(kFull, found, turn * PW + mine);
+        load_block<D>(a, page2, hk, blk, y);
       }
-      const uint32_t hi[8] = {h4[0].x, h4[0].y, h4[0].z, h4[0].w, h4[1].x, h4[1].y, h4[1].z, h4[1].w};
-      const uint32_t lo[8] = {l4[0].x, l4[0].y, l4[0].z, l4[0].w, l4[1].x, l4[1].y, l4[1].z, l4[1].w};
+      const int p = p0 + mine;
       const float far = (float)(min((long long)(p + 1) * a.c.page_size, (long long)L) - L);
-      float best = -INFINITY;
-      for (int g = 0; g < ng; ++g) {
-        const uint4* qv = reinterpret_cast<const uint4*>(s_q[g]) + 2 * blk;
-        const uint4 q0 = qv[0], q1 = qv[1];
-        const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-        int I = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t neg;  // 0xff in the bytes of negative codes
-          asm("prmt.b32 %0, %1, %1, 0xba98;" : "=r"(neg) : "r"(qw[i]));
-          I = __dp4a((int)((hi[i] & ~neg) | (lo[i] & neg)), (int)qw[i], I);
-        }
-        float s = __fmul_rn(__fmul_rn((float)I, d), s_e[g][blk]);
-#pragma unroll
-        for (int o = 1; o < NB; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, o));
-        s = __fmul_rn(s, a.scale);
-        if (a.alibi) s = __fadd_rn(s, __fmul_rn(a.alibi[h0 + g], far));
-        s = s != s ? INFINITY : s;
-        best = fmaxf(best, s);
-      }
-      if (on && blk == 0) {
-        uint32_t key = !there ? kNoPage : key_of(best);
-        if (g0 && there) key = max(key, keys[p]);
+      const float best = best_score<D>(a, s, x, blk, h0, ng, far);
+      if (p < c1 && blk == 0) {
+        uint32_t key = page < 0 ? kNoPage : key_of(best);
+        if (g0 && page >= 0) key = max(key, get(p));
         if (p < a.first || p >= n - a.last) key = kForced;
-        keys[p] = key;
+        put(p, key);
       }
+      x = y, page = page2;
     }
   }
 }
 
 // ------------------------------------------------------------------------------------------------
-// the K largest: a CTA a sequence and KV head.  Its warps own neighbouring stretches of the pages, so that what
-// they choose is in ascending order; the keys lie in registers where there are at most kPickKeys a lane.  The K-th
-// largest is found by bisection between the smallest and the largest: a count a step, and as a rule it ends when
-// exactly K are above, after little more than log2(pages) steps.
+// the K largest of n keys, by a CTA.  Its warps own neighbouring stretches of the pages, so that what they choose is in
+// ascending order.  The K-th largest is found by bisection between the smallest and the largest: a count a step, and
+// as a rule it ends when exactly K are above, after little more than log2(n) steps.
 
-constexpr int kPickWarps = 16, kPickKeys = 16;
+constexpr int kPickWarps = 8;
 
-struct Count16 {  // a word from each warp, double-buffered: one barrier a sum
+struct Count {  // a word from each warp, double-buffered: one barrier a sum
   uint32_t s[2][kPickWarps];
+  uint32_t ends[2][kPickWarps];
 };
 // Sum over the CTA; every thread gets it.
-__device__ __forceinline__ uint32_t cta_sum(uint32_t v, Count16& c, int& turn) {
+__device__ __forceinline__ uint32_t cta_sum(uint32_t v, Count& c, int& turn) {
   const uint32_t w = __reduce_add_sync(kFull, v);
   if ((threadIdx.x & 31) == 0) c.s[turn][threadIdx.x >> 5] = w;
   __syncthreads();
-  const uint32_t x = (threadIdx.x & 31) < kPickWarps ? c.s[turn][threadIdx.x & 31] : 0;
+  const uint4* s = reinterpret_cast<const uint4*>(c.s[turn]);
   turn ^= 1;
-  return __reduce_add_sync(kFull, x);
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPickWarps / 4; ++i) {
+    const uint4 x = s[i];
+    sum += (x.x + x.y) + (x.z + x.w);
+  }
+  return sum;
 }
 
-template <bool REGS>
-__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Count16& cnt, uint32_t (&ends)[2][kPickWarps]) {
+__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Count& cnt) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rounds = (n + kPickWarps * 32 - 1) / (kPickWarps * 32), base = warp * rounds * 32 + lane;
-  uint32_t r[REGS ? kPickKeys : 1];
-  auto key = [&](int i) {
-    const int p = base + i * 32;
-    return p < n ? keys[p] : 0u;
-  };
   // the range of the scores that are not forced
   uint32_t least = 0xffffffffu, most = 0;
-  auto see = [&](uint32_t k, int i) {
-    if (base + i * 32 < n && k != kForced) least = min(least, k), most = max(most, k);
-  };
-  if (REGS) {
-#pragma unroll
-    for (int i = 0; i < kPickKeys; ++i)
-      if (i < rounds) r[i] = key(i);
-#pragma unroll
-    for (int i = 0; i < kPickKeys; ++i)
-      if (i < rounds) see(r[i], i);
-  } else {
-    for (int i = 0; i < rounds; ++i) see(key(i), i);
+  for (int i = 0, p = base; i < rounds; ++i, p += 32) {
+    const uint32_t k = p < n ? keys[p] : kForced;
+    if (k != kForced) least = min(least, k), most = max(most, k);
   }
   least = __reduce_min_sync(kFull, least), most = __reduce_max_sync(kFull, most);
-  if (lane == 0) ends[0][warp] = least, ends[1][warp] = most;
+  if (lane == 0) cnt.ends[0][warp] = least, cnt.ends[1][warp] = most;
   __syncthreads();
-  uint32_t lo = __reduce_min_sync(kFull, ends[0][lane & (kPickWarps - 1)]), hi = __reduce_max_sync(kFull, ends[1][lane & (kPickWarps - 1)]);
+  uint32_t lo = __reduce_min_sync(kFull, cnt.ends[0][lane & (kPickWarps - 1)]);
+  uint32_t hi = __reduce_max_sync(kFull, cnt.ends[1][lane & (kPickWarps - 1)]);
   int turn = 0;
-  auto count = [&](uint32_t t) {  // keys of at least t > 0
-    uint32_t c = 0;
-    if (REGS) {
-#pragma unroll
-      for (int i = 0; i < kPickKeys; ++i)
-        if (i < rounds) c += r[i] >= t;
-    } else {
-      for (int i = 0; i < rounds; ++i) c += key(i) >= t;
-    }
-    return cta_sum(c, cnt, turn);
-  };
   const uint32_t K = (uint32_t)a.K;
-  uint32_t above = 0;     // keys above T
-  bool ties = false;      // T is shared by more keys than there is room for
-  uint32_t T;
-  if (a.first + a.last == a.K) {
-    T = kForced;
-  } else {  // count(lo) >= K and count(hi + 1) < K
-    uint32_t c_hi = (uint32_t)(a.first + a.last);
-    T = 0;
+  uint32_t above = (uint32_t)(a.first + a.last);  // keys above hi
+  bool ties = false;                              // T is shared by more keys than there is room for
+  uint32_t T = kForced;
+  if (above < K) {  // at least K keys are at or above lo, and fewer above hi
     while (lo < hi) {
-      const uint32_t mid = lo + ((hi - lo) >> 1) + 1, c = count(mid);
+      const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
+      uint32_t c = 0;
+#pragma unroll 4
+      for (int i = 0, p = base; i < rounds; ++i, p += 32) c += p < n && keys[p] >= mid;
+      c = cta_sum(c, cnt, turn);
       if (c == K) {
         T = mid;
         break;
       }
       if (c > K) lo = mid;
-      else hi = mid - 1, c_hi = c;
+      else hi = mid - 1, above = c;
     }
-    if (lo == hi) T = lo, above = c_hi, ties = true;
+    if (lo == hi) T = lo, ties = true;
   }
   // who is chosen, in order: those above T (or at it), and the first K - above of those at T
   const uint32_t room = ties ? K - above : 0;
   uint32_t chosen = 0, equal = 0;  // of this warp's
-  auto tell = [&](uint32_t k, int i) {
-    const bool in = base + i * 32 < n;
-    chosen += __popc(__ballot_sync(kFull, in && (ties ? k > T : k >= T)));
-    equal += __popc(__ballot_sync(kFull, in && ties && k == T));
-  };
-  if (REGS) {
-#pragma unroll
-    for (int i = 0; i < kPickKeys; ++i)
-      if (i < rounds) tell(r[i], i);
-  } else {
-    for (int i = 0; i < rounds; ++i) tell(key(i), i);
+  for (int i = 0, p = base; i < rounds; ++i, p += 32) {
+    const uint32_t k = p < n ? keys[p] : 0;
+    const bool same = p < n && ties && k == T;
+    chosen += __popc(__ballot_sync(kFull, p < n && k >= T && !same));
+    equal += __popc(__ballot_sync(kFull, same));
   }
   __syncthreads();  // (`ends` has been read)
-  if (lane == 0) ends[0][warp] = chosen, ends[1][warp] = equal;
+  if (lane == 0) cnt.ends[0][warp] = chosen, cnt.ends[1][warp] = equal;
   __syncthreads();
   uint32_t before = 0, eq_before = 0;
-  for (int w = 0; w < warp; ++w) before += ends[0][w], eq_before += ends[1][w];
+  for (int w = 0; w < warp; ++w) before += cnt.ends[0][w], eq_before += cnt.ends[1][w];
   before += min(eq_before, room);
-  auto put = [&](uint32_t k, int i) {
-    const int p = base + i * 32;
-    const bool in = p < n, over = in && (ties ? k > T : k >= T), same = in && ties && k == T;
-    const uint32_t below = (1u << lane) - 1, eq = __ballot_sync(kFull, same);
-    const bool take = over || (same && eq_before + __popc(eq & below) < room);
+  const uint32_t below = (1u << lane) - 1;
+  for (int i = 0, p = base; i < rounds; ++i, p += 32) {
+    const uint32_t k = p < n ? keys[p] : 0;
+    const bool same = p < n && ties && k == T;
+    const uint32_t eq = __ballot_sync(kFull, same);
+    const bool take = same ? eq_before + __popc(eq & below) < room : p < n && k >= T;
     const uint32_t all = __ballot_sync(kFull, take);
     if (take) out[before + __popc(all & below)] = p;
     before += __popc(all), eq_before += __popc(eq);
-  };
-  if (REGS) {
-#pragma unroll
-    for (int i = 0; i < kPickKeys; ++i)
-      if (i < rounds) put(r[i], i);
-  } else {
-    for (int i = 0; i < rounds; ++i) put(key(i), i);
   }
 }
 
+// A sequence of at most K pages: all of them
+__device__ __forceinline__ void pick_all(const SelectArgs& a, int32_t* out, int n) {
+  for (int i = threadIdx.x; i < a.K; i += kPickWarps * 32) out[i] = i < n ? i : -1;
+}
+
+// ---- in one: a cluster a sequence and KV head, whose CTAs score a stretch of the pages each; the keys go to the first
+// one's shared memory, and it chooses.
+__device__ __forceinline__ uint32_t at_first_cta(const void* p) {
+  uint32_t a = fab::smem_u32(p), r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  return r;
+}
+template <int D>
+__global__ void __launch_bounds__(kPickWarps * 32, 3) k_page_select(const SelectArgs a) {
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  __shared__ __align__(16) Codes<D> s_codes;
+  __shared__ __align__(16) Count s_cnt;
+  cluster_arrive();
+  after_last();
+  lets_next();
+  const unsigned C = cluster_ctas(), rank = cluster_rank(), job = blockIdx.x / C, hk = job % a.c.Hkv;
+  const int b = job / a.c.Hkv;
+  if (a.lens[b] < 0) return;  // (the cluster's CTAs all leave, here and below)
+  const int L = len_of(a.c, a.lens, b), n = pages_of(a.c, L);
+  int32_t* out = a.pages + (long long)job * a.K;
+  if (n <= a.K) {
+    if (rank == 0) pick_all(a, out, n);
+    return;
+  }
+  const uint32_t keys = at_first_cta(s_keys);
+  auto put = [&](int p, uint32_t k) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys + 4 * p), "r"(k) : "memory"); };
+  auto get = [&](int p) {
+    uint32_t k;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(keys + 4 * p) : "memory");
+    return k;
+  };
+  cluster_wait();  // the first CTA's memory is there
+  score_pages<D, kPickWarps>(a, s_codes, b, hk, L, n, (int)((long long)n * rank / C), (int)((long long)n * (rank + 1) / C), put, get);
+  cluster_barrier();
+  if (rank == 0) pick(a, s_keys, out, n, s_cnt);
+}
+
+// ---- in two, where the keys of a sequence may not fit there: scores into the workspace, then the choice
+template <int D>
+__global__ void __launch_bounds__(kPickWarps * 32, 3) k_page_scores(const SelectArgs a) {
+  __shared__ __align__(16) Codes<D> s_codes;
+  after_last();
+  lets_next();
+  const unsigned hk = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv;
+  const int b = rest / a.chunks, c0 = (rest % a.chunks) * a.chunk;
+  const int L = len_of(a.c, a.lens, b), n = pages_of(a.c, L);
+  if (c0 >= n || n <= a.K) return;
+  uint32_t* keys = a.keys + ((long long)b * a.c.Hkv + hk) * a.c.max_pages;
+  auto put = [&](int p, uint32_t k) { keys[p] = k; };
+  auto get = [&](int p) { return keys[p]; };
+  score_pages<D, kPickWarps>(a, s_codes, b, hk, L, n, c0, min(n, c0 + a.chunk), put, get);
+}
 __global__ void __launch_bounds__(kPickWarps * 32) k_page_pick(const SelectArgs a) {
-  __shared__ Count16 s_cnt;
-  __shared__ uint32_t s_ends[2][kPickWarps];
+  __shared__ __align__(16) Count s_cnt;
   after_last();
   lets_next();
   const int b = blockIdx.x / a.c.Hkv;
-  const int len = a.lens[b];
-  if (len < 0) return;
+  if (a.lens[b] < 0) return;
   const int n = pages_of(a.c, len_of(a.c, a.lens, b));
   int32_t* out = a.pages + (long long)blockIdx.x * a.K;
-  if (n <= a.K) {
-    for (int i = threadIdx.x; i < a.K; i += kPickWarps * 32) out[i] = i < n ? i : -1;
-    return;
-  }
-  const uint32_t* keys = a.keys + (long long)blockIdx.x * a.c.max_pages;
-  if (n <= kPickWarps * 32 * kPickKeys) pick<true>(a, keys, out, n, s_cnt, s_ends);
-  else pick<false>(a, keys, out, n, s_cnt, s_ends);
+  if (n <= a.K) pick_all(a, out, n);
+  else pick(a, a.keys + (long long)blockIdx.x * a.c.max_pages, out, n, s_cnt);
 }
 
 static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
@@ -417,8 +473,31 @@ static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
   if (c.num_pages > 0 && (!p->codes || !p->scales)) return FA_ERR_NULL;
   return aligned(p->codes, 16) && aligned(p->scales, 16) ? FA_OK : FA_ERR_ALIGN;
 }
+constexpr int kOnePages = 49152;  // keys that fit shared memory beside the rest (192 KB)
 static size_t key_bytes(const Cache& c) {
+  if (c.max_pages <= kOnePages) return 256;
   return std::max<size_t>(256, ((size_t)c.B * c.Hkv * c.max_pages * sizeof(uint32_t) + 255) / 256 * 256);
+}
+template <int D>
+static cudaError_t run_select(SelectArgs a, int nsm, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
+  const long long rows = (long long)a.c.B * a.c.Hkv;
+  if (a.c.max_pages <= kOnePages) {
+    // CTAs of a cluster: as many as give each at least a turn of its warps, and all of them two to an SM
+    unsigned C = 1;
+    const int turn = kPickWarps * 32 / (D / 32);
+    while (C < 8 && a.c.max_pages > 2 * (int)C * turn && rows * C * 2 <= 2LL * nsm) C *= 2;
+    if (!allow_smem(reinterpret_cast<const void*>(k_page_select<D>), kOnePages * 4, &ready)) return cudaErrorInvalidValue;
+    return launch_clusters(k_page_select<D>, (unsigned)(rows * C), C, kPickWarps * 32, (size_t)a.c.max_pages * 4, s, a);
+  }
+  const long long turn = kPickWarps * 32 / (D / 32), most = (a.c.max_pages + turn - 1) / turn;
+  const long long want = std::min(most, std::max(1LL, 8LL * nsm / rows));
+  a.chunk = (int)((most + want - 1) / want * turn);
+  a.chunks = (a.c.max_pages + a.chunk - 1) / a.chunk;
+  if (rows * a.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_next(k_page_scores<D>, dim3((unsigned)(rows * a.chunks)), dim3(kPickWarps * 32), 0, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_next(k_page_pick, dim3((unsigned)rows), dim3(kPickWarps * 32), 0, s, a);
 }
 static bool select_range(const Cache& c, int H) {
   return c.max_pages <= (1 << 22) && H <= 65535 && (long long)c.B * c.Hkv < (1 << 22);
@@ -478,15 +557,6 @@ extern "C" fa_status fa_page_select(const void* q, int act, int64_t q_row, int64
   a.H = H, a.G = H / a.c.Hkv, a.K = K, a.first = first, a.last = last, a.scale = scale, a.alibi = alibi_slopes;
   a.keys = static_cast<uint32_t*>(workspace), a.pages = pages;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.c.max_pages > K) {
-    const long long rows = (long long)a.c.B * a.c.Hkv;
-    const int at_once = kScoreWarps * 32 / (a.c.D / 32);  // pages that a CTA takes at a time
-    const long long want = std::max(1LL, 16LL * nsm / rows), most = (a.c.max_pages + at_once - 1) / at_once;
-    a.chunk = (int)((most + std::min(want, most) - 1) / std::min(want, most)) * at_once;
-    a.chunks = (a.c.max_pages + a.chunk - 1) / a.chunk;
-    if (rows * a.chunks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    void (*k)(const SelectArgs) = a.c.D == 64 ? k_page_scores<64> : a.c.D == 128 ? k_page_scores<128> : k_page_scores<256>;
-    if (launch_next(k, dim3((unsigned)(rows * a.chunks)), dim3(kScoreWarps * 32), 0, s, a) != cudaSuccess) return FA_ERR_CUDA;
-  }
-  return launch_next(k_page_pick, dim3((unsigned)(a.c.B * a.c.Hkv)), dim3(kPickWarps * 32), 0, s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const cudaError_t e = a.c.D == 64 ? run_select<64>(a, nsm, s) : a.c.D == 128 ? run_select<128>(a, nsm, s) : run_select<256>(a, nsm, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
