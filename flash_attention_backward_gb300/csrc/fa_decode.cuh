@@ -27,6 +27,8 @@
 // More than eight query heads to a KV head read and decode its rows once for each eight (24 heads, 2 KV heads,
 // f16: 46 us where 12 heads take 36); more than 256 sequences take a launch more (300: 155 us, 83 %).
 #pragma once
+#include <algorithm>
+
 #include "fa_paged.cuh"
 #include "sm100.cuh"
 
@@ -485,6 +487,7 @@ struct DecodeArgs {
   float* part;  // [slots][HG]: partial O [8][DV], then maxima [8] and sums [8] of an item of a split sequence
   int4* jobs;   // [njobs]: the split sequences: {b, first slot, slots, 0}; b = -1 behind the last one
   int4* items;  // [nitems] laid out beforehand: {b, splits, split, slot}, b = -1 behind the last one; or NULL
+  int joins;             // CTAs of the join that the card holds at a time
   int R, nitems, njobs;  // items that the card holds at a time, that can be at most, split sequences at most
   int box;      // rows of the tensor maps' boxes, 16 or 8: a tile is one or two; 0: one bulk copy a row
   uint64_t wait_ns;   // a wait for a copy gives up after this long (0, the failure-detection hook: at once)
@@ -1132,21 +1135,20 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   }
 }
 
-// Joins the parts of a split sequence (blockIdx.x), in their order, for a query head (blockIdx.y).  The grid
-// starts while the items' last CTAs run.  Each group of threads takes every GR-th part with a running
-// maximum, then the groups are joined: bound by the latency of a launch and two rounds of loads (75520 keys:
-// about 114 parts of 24 heads, 2.8 MB, read from L2).
+// Joins the parts of a split sequence, in their order, for a query head.  Each group of threads takes every GR-th
+// part with a running maximum, then the groups are joined: bound by the latency of a launch and two rounds of loads
+// (75520 keys: about 114 parts of 24 heads, 2.8 MB, read from L2).
 template <int DV>
-__global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
-  constexpr int LN = DV / 4, GR = 512 / LN;  // threads of a row (four components each), rows read at a time
-  __shared__ float s_m[GR], s_l[GR];
-  __shared__ float4 s_x[512];
-  const int h = blockIdx.y, hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
-  const int tid = threadIdx.x, ln = tid % LN, gr = tid / LN;
-  after_last();
-  const int4 job = a.jobs[blockIdx.x];
-  if (job.x < 0) return;
-  const int np = job.z;
+struct JoinSums {
+  static constexpr int LN = DV / 4, GR = 512 / LN;  // threads of a row (four components each), rows read at a time
+  float m[GR], l[GR];
+  float4 x[512];
+};
+template <int DV>
+__device__ __forceinline__ void join_parts(const DecodeArgs& a, const int4 job, int h, JoinSums<DV>& s) {
+  constexpr int LN = JoinSums<DV>::LN, GR = JoinSums<DV>::GR;
+  const int hk = h / a.G, hc = (h - hk * a.G) >> 3, hg = hk * a.chunks + hc, c = (h - hk * a.G) & 7;
+  const int tid = threadIdx.x, ln = tid % LN, gr = tid / LN, np = job.z;
   float M = -INFINITY, S = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int Q = 4;  // parts under way at a time
@@ -1175,21 +1177,21 @@ __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
       x.x = fmaf(v[k].x, f, x.x), x.y = fmaf(v[k].y, f, x.y), x.z = fmaf(v[k].z, f, x.z), x.w = fmaf(v[k].w, f, x.w);
     }
   }
-  if (ln == 0) s_m[gr] = M, s_l[gr] = S;
-  s_x[tid] = x;
+  if (ln == 0) s.m[gr] = M, s.l[gr] = S;
+  s.x[tid] = x;
   __syncthreads();
   if (gr > 0) return;
   const float sk = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
   float top = sk;
 #pragma unroll
-  for (int i = 0; i < GR; ++i) top = fmaxf(top, s_m[i]);
+  for (int i = 0; i < GR; ++i) top = fmaxf(top, s.m[i]);
   const float ref = top == -INFINITY ? 0.f : top;
   S = 0.f, x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < GR; ++i) {
-    const float f = fab::ex2(s_m[i] - ref);
-    const float4 v = s_x[i * LN + ln];
-    S = fmaf(s_l[i], f, S);
+    const float f = fab::ex2(s.m[i] - ref);
+    const float4 v = s.x[i * LN + ln];
+    S = fmaf(s.l[i], f, S);
     x.x = fmaf(v.x, f, x.x), x.y = fmaf(v.y, f, x.y), x.z = fmaf(v.z, f, x.z), x.w = fmaf(v.w, f, x.w);
   }
   if (a.sinks) S += fab::ex2(sk - ref + a.lift);
@@ -1198,6 +1200,21 @@ __global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
   act_store(a.O, a.act, at, x.x * inv), act_store(a.O, a.act, at + 1, x.y * inv);
   act_store(a.O, a.act, at + 2, x.z * inv), act_store(a.O, a.act, at + 3, x.w * inv);
   if (tid == 0 && a.lse) a.lse[(long long)job.x * a.H + h] = S == 0.f ? -INFINITY : (ref - a.lift + log2f(S)) * kLn2;
+}
+
+// The split sequences blockIdx.x, blockIdx.x + gridDim.x, ..., query head blockIdx.y.  There are no more CTAs than run
+// at a time, however many sequences may be split: most batches split few.  The grid starts while the items' last CTAs
+// run.
+template <int DV>
+__global__ void __launch_bounds__(512) k_decode_join(const DecodeArgs a) {
+  __shared__ JoinSums<DV> s_sums;
+  after_last();
+  for (int j = blockIdx.x; j < a.njobs; j += gridDim.x) {
+    const int4 job = a.jobs[j];
+    if (job.x < 0) return;  // (and none behind it)
+    if (j != blockIdx.x) __syncthreads();  // the sums have been read
+    join_parts<DV>(a, job, blockIdx.y, s_sums);
+  }
 }
 
 typedef cudaError_t (*DecodeFn)(DecodeArgs a, const DecodeMaps& m, cudaStream_t s);
@@ -1212,7 +1229,7 @@ cudaError_t run_decode(DecodeArgs a, const DecodeMaps& m, cudaStream_t s) {
   if (a.items && (e = launch_next(k_decode_plan<SEL>, dim3(1), dim3(1024), 0, s, a)) != cudaSuccess) return e;
   e = launch_next(k_decode<D, DV, KT, VT, SEL>, dim3((unsigned)(a.nitems * a.HG)), dim3(kWarps * 32), C.smem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
-  if (a.njobs > 0) return launch_next(k_decode_join<DV>, dim3(a.njobs, a.H), dim3(512), 0, s, a);
+  if (a.njobs > 0) return launch_next(k_decode_join<DV>, dim3(std::max(1, std::min(a.njobs, a.joins / a.H)), a.H), dim3(512), 0, s, a);
   return cudaSuccess;
 }
 template <int D, int DV, int KT, bool SEL>

@@ -112,7 +112,7 @@ static fa_status decode(const void* q, int act, int64_t q_row, int64_t q_head, c
   a.part = static_cast<float*>(workspace);
   a.jobs = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_jobs);
   a.items = p.planned ? reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + p.off_items) : nullptr;
-  a.R = p.R, a.nitems = p.nitems, a.njobs = p.njobs;
+  a.R = p.R, a.nitems = p.nitems, a.njobs = p.njobs, a.joins = 4 * nsm;
   a.wait_ns = fab_take_wait_ns();
   // boxes of 16 or 8 rows where these never span pages and cells are spaced by multiples of 16 bytes
   DecodeMaps m = {};

@@ -29,130 +29,189 @@ __device__ __forceinline__ int page_of(const Cache& c, int j) { return (int)((ui
 __device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 0 ? page_of(c, len - 1) + 1 : 0; }
 
 // ------------------------------------------------------------------------------------------------
-// bounds: a lane holds eight components, D / 8 lanes a row; the CTA's lane groups take the page's rows in turn and
-// join their largest and smallest values in the end.
+// bounds: a lane holds eight components, D / 8 lanes a row.  A warp takes a page of its own, or where there are not as
+// many pages the CTA's warps share one.
 
 constexpr int kBoundWarps = 4;
 
 __device__ __forceinline__ uint32_t load_u32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
-
-// value (u - bias) * d of byte b of w: 32768 + u as f32 by placing the byte, and (32768 + bias) d is exact
-__device__ __forceinline__ float byte_times(uint32_t w, int b, float d, float off) {
-  return fmaf(__uint_as_float(__byte_perm(w, 0x47000000u, 0x7404 | b << 4)), d, off);
+// of three; a NaN gives way
+__device__ __forceinline__ float most3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
+__device__ __forceinline__ float least3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// 32768 + byte b of w
+__device__ __forceinline__ float place_byte(uint32_t w, int b) { return __uint_as_float(__byte_perm(w, 0x47000000u, 0x7404 | b << 4)); }
 
 template <int TYPE>
 struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
-  uint4 a, b;
-  __device__ __forceinline__ void load(const uint8_t* row, int e0) {
-    if (TYPE == FA_F32) {
-      a = reinterpret_cast<const uint4*>(row)[e0 >> 2], b = reinterpret_cast<const uint4*>(row)[(e0 >> 2) + 1];
-    } else if (TYPE == FA_F16) {
-      a = reinterpret_cast<const uint4*>(row)[e0 >> 3];
+  uint32_t w[TYPE == FA_F32 ? 8 : TYPE == FA_F16 ? 4 : 3];
+
+  // where in a row the lane's components start
+  static __device__ __forceinline__ int place(int e0) {
+    const int blk = e0 >> 5, j = (e0 >> 3) & 3;
+    if (TYPE == FA_F32) return 4 * e0;
+    if (TYPE == FA_F16) return 2 * e0;
+    if (TYPE == FA_Q8_0) return (blk >> 1) * 68 + (blk & 1 ? 36 : 0) + 8 * j;  // a word (see load)
+    return blk * 18 + 2 + 8 * (j & 1);
+  }
+  // p: there; e0 tells the lanes apart
+  __device__ __forceinline__ void load(const uint8_t* p, int e0) {
+    const int blk = e0 >> 5, j = (e0 >> 3) & 3;
+    if (TYPE == FA_F32 || TYPE == FA_F16) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+      if (TYPE == FA_F32) {
+        const uint4 b = *reinterpret_cast<const uint4*>(p + 16);
+        w[4 % (sizeof(w) / 4)] = b.x, w[5 % (sizeof(w) / 4)] = b.y, w[6 % (sizeof(w) / 4)] = b.z, w[7 % (sizeof(w) / 4)] = b.w;
+      }
     } else if (TYPE == FA_Q8_0) {  // pairs of blocks are 17 words: the first one's codes start in the middle of one
-      const int blk = e0 >> 5, j = (e0 >> 3) & 3, odd = blk & 1;
-      const uint8_t* p = row + (blk >> 1) * 68 + (odd ? 36 : 0) + 8 * j;
-      const uint32_t w0 = load_u32(p), w1 = load_u32(p + 4), w2 = odd ? 0 : load_u32(p + 8);
-      a.x = odd ? w0 : __byte_perm(w0, w1, 0x5432), a.y = odd ? w1 : __byte_perm(w1, w2, 0x5432);
-      a.z = *reinterpret_cast<const uint16_t*>(row + blk * 34);
+      const bool odd = blk & 1;
+      const uint32_t a = load_u32(p), b = load_u32(p + 4), c = odd ? 0 : load_u32(p + 8);
+      w[0] = __funnelshift_r(a, b, odd ? 0 : 16), w[1] = __funnelshift_r(b, c, odd ? 0 : 16);
+      w[2] = *reinterpret_cast<const uint16_t*>(p - 8 * j - (odd ? 2 : 0));
     } else {
-      const int blk = e0 >> 5, j = (e0 >> 3) & 3;
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(row + blk * 18);
-      a.x = p[1 + 4 * (j & 1)] | (uint32_t)p[2 + 4 * (j & 1)] << 16, a.y = p[3 + 4 * (j & 1)] | (uint32_t)p[4 + 4 * (j & 1)] << 16;
-      if (j >= 2) a.x >>= 4, a.y >>= 4;
-      a.z = p[0];
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      w[0] = h[0] | (uint32_t)h[1] << 16, w[1] = h[2] | (uint32_t)h[3] << 16;
+      if (j >= 2) w[0] >>= 4, w[1] >>= 4;
+      w[2] = *reinterpret_cast<const uint16_t*>(p - 2 - 8 * (j & 1));
     }
   }
   __device__ __forceinline__ void values(float (&x)[8]) const {
     if (TYPE == FA_F32) {
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i % (sizeof(w) / 4)]);
     } else if (TYPE == FA_F16) {
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i % (sizeof(w) / 4)]));
         x[2 * i] = f.x, x[2 * i + 1] = f.y;
       }
-    } else {
-      const float d = __half2float(__ushort_as_half((unsigned short)a.z));
+    } else {  // (32768 + code + bias) d - (32768 + bias) d: the second product is exact, and so is the sum
       constexpr uint32_t kMask = TYPE == FA_Q8_0 ? 0xffffffffu : 0x0f0f0f0fu, kFlip = TYPE == FA_Q8_0 ? 0x80808080u : 0;
+      const float d = __half2float(__ushort_as_half((unsigned short)w[2]));
       // (an infinite scale makes infinities of its block, whose bounds are infinite then)
       const float off = fabsf(d) < INFINITY ? -(32768.f + (TYPE == FA_Q8_0 ? 128.f : 8.f)) * d : 0.f;
-      const uint32_t w0 = (a.x & kMask) ^ kFlip, w1 = (a.y & kMask) ^ kFlip;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = byte_times(w0, i, d, off), x[4 + i] = byte_times(w1, i, d, off);
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t u = (w[k] & kMask) ^ kFlip;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 y = __ffma2_rn(make_float2(place_byte(u, i), place_byte(u, i + 1)), make_float2(d, d), make_float2(off, off));
+          x[4 * k + i] = y.x, x[4 * k + i + 1] = y.y;
+        }
+      }
     }
   }
 };
 
+// Largest and smallest values of rows r0, r0 + step, ... of a page's `rows` (at least one), the lane's components
+template <int TYPE>
+__device__ __forceinline__ void row_range(const uint8_t* page, unsigned cell, int e0, int r0, int step, int rows, float (&hi)[8], float (&lo)[8]) {
+  constexpr int U = TYPE == FA_F32 ? 4 : 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
+#pragma unroll 1
+  for (int r = r0; r < rows; r += U * step) {
+    Raw8<TYPE> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].load(page + (uint64_t)(unsigned)min(r + u * step, rows - 1) * cell, e0);  // (the last row again does nothing)
+#pragma unroll
+    for (int u = 0; u < U; u += 2) {
+      float x[8], y[8];
+      raw[u].values(x), raw[u + 1].values(y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[i] = most3(hi[i], x[i], y[i]), lo[i] = least3(lo[i], x[i], y[i]);
+    }
+  }
+}
+
+// Codes and scale of the lane's components: four neighbouring lanes hold a block of 32.
+template <int D>
+__device__ __forceinline__ void put_bounds(const BoundArgs& a, long long rec, int e0, const float (&hi)[8], const float (&lo)[8], bool on) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = most3(m, fabsf(hi[i]), fabsf(lo[i]));
+  m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+  float d = 0.f;
+  uint32_t up[2] = {}, down[2] = {};
+  if (!(m < INFINITY)) {
+    d = INFINITY, up[0] = up[1] = 0x7f7f7f7fu, down[0] = down[1] = 0x81818181u;
+  } else if (m > kTinyAmax) {
+    d = __fdiv_rn(m, 127.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int u = max(-127, min(127, __float2int_ru(__fdiv_rn(hi[i], d)))), l = max(-127, min(127, __float2int_rd(__fdiv_rn(lo[i], d))));
+      up[i >> 2] |= (uint32_t)(u & 255) << (8 * (i & 3)), down[i >> 2] |= (uint32_t)(l & 255) << (8 * (i & 3));
+    }
+  }
+  if (!on) return;
+  *reinterpret_cast<uint2*>(a.codes + rec * 2 * D + e0) = make_uint2(up[0], up[1]);
+  *reinterpret_cast<uint2*>(a.codes + rec * 2 * D + D + e0) = make_uint2(down[0], down[1]);
+  if ((e0 & 31) == 0) a.scales[rec * (D / 32) + (e0 >> 5)] = d;
+}
+
 template <int D, int TYPE>
 __global__ void __launch_bounds__(kBoundWarps * 32) k_page_bounds(const BoundArgs a) {
-  constexpr int LG = D / 8, GROUPS = kBoundWarps * 32 / LG, U = TYPE == FA_F32 ? 4 : 8;
+  constexpr int LG = D / 8, GW = 32 / LG;  // lanes of a row, rows side by side in a warp
   constexpr int RB = TYPE == FA_F32 ? 4 * D : TYPE == FA_F16 ? 2 * D : TYPE == FA_Q8_0 ? D / 32 * 34 : D / 32 * 18;
-  __shared__ float s_hi[kBoundWarps][D], s_lo[kBoundWarps][D];
+  __shared__ float4 s_part[kBoundWarps - 1][4][32];
   after_last();
   lets_next();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = (lane & (LG - 1)) * 8, grp = threadIdx.x / LG;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = (lane & (LG - 1)) * 8, grp = lane / LG;
   const unsigned hk = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv, z = rest % a.Z;
   const int b = rest / a.Z, L = len_of(a.c, a.lens, b), f = a.first ? a.first[b] : 0;
   if (f < 0 || f >= L) return;
-  const int n = pages_of(a.c, L);
-  const long long cell = (long long)a.c.Hkv * RB;
-  for (int p = page_of(a.c, f) + z; p < n; p += a.Z) {
+  const int n = pages_of(a.c, L), p0 = page_of(a.c, f);
+  const bool apart = n - p0 > a.Z;  // a warp a page
+  const unsigned cell = (unsigned)a.c.Hkv * RB;
+  const int all = apart ? a.Z * kBoundWarps : a.Z;
+  for (int p = p0 + (int)(apart ? z * kBoundWarps + warp : z); p < n; p += all) {
     const int page = a.c.table[(long long)b * a.c.max_pages + p];
     if (page < 0 || page >= a.c.num_pages) {
-      if (threadIdx.x == 0) report_page(a.c.err);
+      if (lane == 0) report_page(a.c.err);
       continue;
     }
     const int rows = min(a.c.page_size, L - p * a.c.page_size);
-    const uint8_t* row = a.c.k + (long long)page * a.c.page_size * cell + hk * RB;
+    const uint8_t* at = a.c.k + (long long)page * a.c.page_size * cell + hk * RB + Raw8<TYPE>::place(e0);
     float hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
-    for (int r0 = grp; r0 < rows; r0 += U * GROUPS) {
-      Raw8<TYPE> raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) raw[u].load(row + min(r0 + u * GROUPS, rows - 1) * cell, e0);  // (the last row again does nothing)
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[8];
-        raw[u].values(x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hi[i] = fmaxf(hi[i], x[i]), lo[i] = fminf(lo[i], x[i]);
-      }
-    }
+    row_range<TYPE>(at, cell, e0, apart ? grp : warp * GW + grp, apart ? GW : kBoundWarps * GW, rows, hi, lo);
 #pragma unroll
     for (int o = LG; o < 32; o <<= 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], o)), lo[i] = fminf(lo[i], __shfl_xor_sync(kFull, lo[i], o));
-    __syncthreads();  // (the arrays are the last page's until here)
-    if (lane < LG) {
+    if (!apart) {
+      if (warp) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s_hi[warp][e0 + i] = hi[i], s_lo[warp][e0 + i] = lo[i];
-    }
-    __syncthreads();
-    // a warp a block of 32 components, a lane a component
-    for (int blk = warp; blk < D / 32; blk += kBoundWarps) {
-      const int e = blk * 32 + lane;
-      float top = s_hi[0][e], low = s_lo[0][e];
-#pragma unroll
-      for (int w = 1; w < kBoundWarps; ++w) top = fmaxf(top, s_hi[w][e]), low = fminf(low, s_lo[w][e]);
-      const float m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(fabsf(top), fabsf(low)))));
-      float d = 0.f;
-      int up = 0, down = 0;
-      if (!(m < INFINITY)) {
-        d = INFINITY, up = 127, down = -127;
-      } else if (m > kTinyAmax) {
-        d = __fdiv_rn(m, 127.f);
-        up = max(-127, min(127, __float2int_ru(__fdiv_rn(top, d)))), down = max(-127, min(127, __float2int_rd(__fdiv_rn(low, d))));
+        for (int i = 0; i < 2; ++i) {
+          s_part[warp - 1][i][lane] = make_float4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+          s_part[warp - 1][2 + i][lane] = make_float4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+        }
       }
-      const long long rec = (long long)page * a.c.Hkv + hk;
-      a.codes[rec * 2 * D + e] = (int8_t)up, a.codes[rec * 2 * D + D + e] = (int8_t)down;
-      if (lane == 0) a.scales[rec * (D / 32) + blk] = d;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int w = 0; w < kBoundWarps - 1; ++w)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 x = s_part[w][i][lane], y = s_part[w][2 + i][lane];
+            hi[4 * i] = fmaxf(hi[4 * i], x.x), hi[4 * i + 1] = fmaxf(hi[4 * i + 1], x.y), hi[4 * i + 2] = fmaxf(hi[4 * i + 2], x.z),
+                   hi[4 * i + 3] = fmaxf(hi[4 * i + 3], x.w);
+            lo[4 * i] = fminf(lo[4 * i], y.x), lo[4 * i + 1] = fminf(lo[4 * i + 1], y.y), lo[4 * i + 2] = fminf(lo[4 * i + 2], y.z),
+                   lo[4 * i + 3] = fminf(lo[4 * i + 3], y.w);
+          }
+      }
     }
+    if (apart || warp == 0) put_bounds<D>(a, (long long)page * a.c.Hkv + hk, e0, hi, lo, grp == 0);
+    // (shared by the CTA, a page is its only one: there are no more than Z)
   }
 }
 
@@ -240,7 +299,7 @@ __device__ __forceinline__ float best_score(const SelectArgs& a, const Codes<D>&
   const uint32_t hi[8] = {x.hi[0].x, x.hi[0].y, x.hi[0].z, x.hi[0].w, x.hi[1].x, x.hi[1].y, x.hi[1].z, x.hi[1].w};
   const uint32_t lo[8] = {x.lo[0].x, x.lo[0].y, x.lo[0].z, x.lo[0].w, x.lo[1].x, x.lo[1].y, x.lo[1].z, x.lo[1].w};
   float best = -INFINITY;
-#pragma unroll 2
+#pragma unroll 4
   for (int g = 0; g < ng; ++g) {
     const uint4* qv = reinterpret_cast<const uint4*>(s.q[g]) + 2 * blk;
     const uint4 q0 = qv[0], q1 = qv[1];
@@ -520,7 +579,7 @@ extern "C" fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_b
   if (a.c.B == 0 || a.c.max_pages == 0) return FA_OK;
   a.codes = bounds->codes, a.scales = bounds->scales, a.first = first, a.lens = seq_lens;
   const long long rows = (long long)a.c.B * a.c.Hkv;
-  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, 12LL * nsm / rows));
+  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, 8LL * nsm / rows));
   if (rows * a.Z > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const BoundKernel k = a.c.D == 64 ? pick_bounds<64>(a.c.k_type) : a.c.D == 128 ? pick_bounds<128>(a.c.k_type) : pick_bounds<256>(a.c.k_type);
   return launch_next(k, dim3((unsigned)(rows * a.Z)), dim3(kBoundWarps * 32), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess
