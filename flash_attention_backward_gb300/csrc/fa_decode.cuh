@@ -29,6 +29,7 @@
 #pragma once
 #include <algorithm>
 
+#include "fa_mma.cuh"
 #include "fa_paged.cuh"
 #include "sm100.cuh"
 
@@ -38,87 +39,6 @@ using fab::lds_u16;
 using fab::lds_u32;
 using fab::lds_v4;
 using fab::smem_u32;
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// the first product of a sum: C is zero
-__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-// (x & m) | v and (x & m) ^ v in one instruction (with two constants the compiler was seen to take two)
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t v) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(m), "r"(v));
-  return y;
-}
-__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t m, uint32_t v) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(x), "r"(m), "r"(v));
-  return y;
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {  // a in the low half
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_b2(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float lo_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
-__device__ __forceinline__ float hi_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // ------------------------------------------------------------------------------------------------
 // Which component of a head each operand element is.  The order inside a product is free as long as
@@ -524,14 +444,17 @@ constexpr int kSlotCtl = 160;        // a slot's row addresses, barriers and mas
 struct DecodeShape {
   int ctas, slots, smem, pk, pv, qf, stage, ring;
 };
-__host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, int vt) {
+// sel: over selected pages.  A sequence is short then, its CTAs wait for the latency of their copies, and of rows that
+// need little decoding a second slot gains more than the CTA that it takes the place of.
+__host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, int vt, bool sel = false) {
   DecodeShape c{};
   c.pk = smem_pitch(cache_row_bytes(kt, D)), c.pv = smem_pitch(cache_row_bytes(vt, DV));
   c.qf = (kt == FA_F32 ? D / 8 : D / 16) * 512;
   c.stage = 16 * (c.pk + c.pv);
-  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + 3 * 1024;
+  const int sums = DV * 32, slot = c.stage + kSlotCtl, fixed = c.qf + DV * 4 + (sel ? 2 : 3) * 1024;
   c.ctas = (DV == 256 ? 12 : 16) / kWarps;
   while (c.ctas > 1 && fixed + kWarps * (slot > sums ? slot : sums) > kSmemSm / c.ctas) --c.ctas;
+  if (sel && kt <= FA_F16 && vt <= FA_F16 && c.ctas > 2 && (kSmemSm / c.ctas - fixed) / (kWarps * slot) < 2) --c.ctas;
   c.slots = (kSmemSm / c.ctas - fixed) / (kWarps * slot);
   if (c.slots > 4) c.slots = 4;
   c.ring = c.slots * c.stage > sums ? c.slots * c.stage : (sums + 127) / 128 * 128;
@@ -539,11 +462,6 @@ __host__ __device__ constexpr DecodeShape decode_shape(int D, int DV, int kt, in
   return c;
 }
 
-__device__ __forceinline__ float act_load(const void* p, int act, long long i) {
-  if (act == FA_ACT_F32) return static_cast<const float*>(p)[i];
-  if (act == FA_ACT_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
 __device__ __forceinline__ void act_store(void* p, int act, long long i, float x) {
   if (act == FA_ACT_F32) static_cast<float*>(p)[i] = x;
   else if (act == FA_ACT_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
@@ -575,12 +493,17 @@ __device__ __forceinline__ int tiles_of(int keys) { return (keys + 15) >> 4; }
 // chunk is taken is at least U / R, or no sequence's n is above it, so there are at most R + B items, R split
 // sequences and 2 R parts.
 constexpr long long kMaxTiles = 1 << 26;  // of a sequence (2^30 positions)
+// a / b for a >= 0, b > 0.  (What is divided is below 2^32 but for the largest batches, and a 64-bit division is some
+// hundred dependent instructions: the half dozen of them were most of 3 us before a CTA knew its item.)
+__host__ __device__ __forceinline__ long long divide(long long a, int b) {
+  return (unsigned long long)a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 __host__ __device__ __forceinline__ int least_chunk(long long U, int R) {
-  const long long fits = (U + R - 1) / R, joins = (long long)(0.37f * sqrtf((float)U)), c = fits > joins ? fits : joins;
+  const long long fits = divide(U + R - 1, R), joins = (long long)(0.37f * sqrtf((float)U)), c = fits > joins ? fits : joins;
   return (int)(c < kMinTiles ? kMinTiles : c < kMaxTiles ? c : kMaxTiles);
 }
 __host__ __device__ __forceinline__ int safe_chunk(long long U, int B, int R) {
-  const long long room = R - B > (R + 1) / 2 ? R - B : (R + 1) / 2, c = (U + room - 1) / room;
+  const long long room = R - B > (R + 1) / 2 ? R - B : (R + 1) / 2, c = divide(U + room - 1, (int)room);
   const int least = least_chunk(U, R);
   return (int)(c < least ? least : c < kMaxTiles ? c : kMaxTiles);
 }
@@ -592,7 +515,7 @@ __device__ __forceinline__ int fit_chunk(const int* tiles, int B, int R, int lo,
   constexpr int kWorth = 6 * NW;
   if (hi - lo <= kWorth) return hi;
   const int c = lo + (int)((long long)(hi - lo) * threadIdx.x / (NW * 32 - 1));
-  const uint32_t inv = (uint32_t)((0x100000000ull + c - 1) / c);
+  const uint32_t inv = 0xffffffffu / (uint32_t)c + 1;  // 2^32 / c, rounded up
   int items = 0;
   for (int b = 0; b < B; ++b) items += (int)((uint64_t)(uint32_t)(tiles[b] + c - 1) * inv >> 32);
   int best = items <= R ? c : hi;
@@ -756,16 +679,17 @@ static __device__ __noinline__ float4 cap_and_bias_sel(float4 x, float cap, floa
 // running maximum and sums of its own: no barrier until the item's last tile.
 // SEL: over selected pages (kernels of their own: the lookups of the plain ones took 1 to 2 % more with both in one).
 template <int D, int DV, int KT, int VT, bool SEL>
-__global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
+__global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT, SEL).ctas)
     k_decode(const DecodeArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
+  constexpr DecodeShape C = decode_shape(D, DV, KT, VT, SEL);
   constexpr int NW = kWarps, SLOTS = C.slots, PK = C.pk, PV = C.pv;
   constexpr float kLift = weight_lift(VT);
   constexpr int RBK = cache_row_bytes(KT, D), RBV = cache_row_bytes(VT, DV);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_scan[NW];
   __shared__ int4 s_item;
-  __shared__ int s_tiles[kPlanBatch];
+  __shared__ int s_all_tiles[SEL ? 1 : kPlanBatch];
+  int* s_tiles = SEL ? reinterpret_cast<int*>(smem) : s_all_tiles;  // (q and the rings are not there yet)
   __shared__ float s_qs[8], s_ml[NW][16];
   // a slot: where its 16 key rows and its 16 value rows start, the barriers of either, the tile's key mask
   struct Slot {
@@ -840,8 +764,8 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
   if (item.x < 0) return;
   const int b = item.x, keys = seq_keys<SEL>(a, b);
   const long long n_all = tiles_of(keys);
-  const int j0 = 16 * (int)(n_all * item.z / item.y);  // the item's keys [j0, j1) and tiles
-  const int j1 = min(keys, 16 * (int)(n_all * (item.z + 1) / item.y)), ntile = tiles_of(j1 - j0);
+  const int j0 = 16 * (int)divide(n_all * item.z, item.y);  // the item's keys [j0, j1) and tiles
+  const int j1 = min(keys, 16 * (int)divide(n_all * (item.z + 1), item.y)), ntile = tiles_of(j1 - j0);
   const bool whole = item.y == 1;
   const int len = SEL ? seq_len(a, b) : keys;
   const int32_t* sel = SEL ? a.sel + ((long long)b * a.c.Hkv + hk) * a.K : nullptr;
@@ -950,13 +874,34 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       if (++sl == SLOTS) sl = 0;
     }
   };
-  // q of the chunk's heads, a head a warp: scaled by a power of two into range, split into parts
-  auto load_q = [&] {
-    for (int h = warp; h < 8; h += NW) {
-      const long long at = b * a.q_row + (head0 + h) * a.q_head;
+  // q of the chunk's heads, a head a warp: a lane's elements of the operands are asked for ahead of the first rows'
+  // copies and looked at behind them
+  constexpr int QH = 8 / NW, STEPS = KT == FA_F32 ? D / 8 : D / 16, QS = (STEPS + 7) / 8, QE = KT == FA_F32 ? 2 : 4;
+  float qv[QH][QS][QE];
+  auto ask_q = [&](auto* q) {  // (the type is told apart outside, so that the loads are under way together)
+#pragma unroll
+    for (int i = 0; i < QH; ++i) {
+      const int h = warp + i * NW;
+      const auto* at = q + (b * a.q_row + (head0 + h) * a.q_head);
+#pragma unroll
+      for (int j = 0; j < QS; ++j)
+#pragma unroll
+        for (int e = 0; e < QE; ++e) {
+          const int ks = g + 8 * j;
+          qv[i][j][e] = h < nh && ks < STEPS ? to_f32(at[KT == FA_F32 ? ks * 8 + t + 4 * e : k_comp16(KT, ks, t, e >> 1, e & 1)]) : 0.f;
+        }
+    }
+  };
+  // scaled by a power of two into range, split into parts
+  auto put_q = [&] {
+#pragma unroll
+    for (int i = 0; i < QH; ++i) {
+      const int h = warp + i * NW;
       float m = 0.f;
-      if (h < nh)
-        for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(act_load(a.q, a.act, at + d)));
+#pragma unroll
+      for (int j = 0; j < QS; ++j)
+#pragma unroll
+        for (int e = 0; e < QE; ++e) m = fmaxf(m, fabsf(qv[i][j][e]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
       // the largest magnitude goes to 2^8 (binary16 parts), or with f32 keys into 2^-80 .. 2^60 (whose tf32
@@ -965,27 +910,29 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT).ctas)
       const int up = KT == FA_F32 ? min(max(e, -80), 60) - e : min(8 - e, 126);
       const float qs = ldexpf(1.f, up);
       if (lane == 0) s_qs[h] = qs;
-      constexpr int steps = KT == FA_F32 ? D / 8 : D / 16;
-      for (int ks = g; ks < steps; ks += 8) {
+#pragma unroll
+      for (int j = 0; j < QS; ++j) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int k = 0; k < 2; ++k) {
           if (KT == FA_F32) {
-            split_tf32(__float_as_uint(h < nh ? act_load(a.q, a.act, at + ks * 8 + t + 4 * i) * qs : 0.f), w[i], w[2 + i]);
+            split_tf32(__float_as_uint(qv[i][j][k] * qs), w[k], w[2 + k]);
           } else {
-            const float x = h < nh ? act_load(a.q, a.act, at + k_comp16(KT, ks, t, i, 0)) * qs : 0.f;
-            const float y = h < nh ? act_load(a.q, a.act, at + k_comp16(KT, ks, t, i, 1)) * qs : 0.f;
-            w[i] = pack_h2(x, y);
-            w[2 + i] = pack_h2(x - lo_h(w[i]), y - hi_h(w[i]));
+            const float x = qv[i][j][2 * k % QE] * qs, y = qv[i][j][(2 * k + 1) % QE] * qs;
+            w[k] = pack_h2(x, y);
+            w[2 + k] = pack_h2(x - lo_h(w[k]), y - hi_h(w[k]));
           }
         }
-        fab::sts_v4(qf + ks * 512 + (h * 4 + t) * 16, w[0], w[1], w[2], w[3]);
+        if (g + 8 * j < STEPS) fab::sts_v4(qf + (g + 8 * j) * 512 + (h * 4 + t) * 16, w[0], w[1], w[2], w[3]);
       }
     }
   };
 
+  if (a.act == FA_ACT_F32) ask_q(static_cast<const float*>(a.q));
+  else if (a.act == FA_ACT_F16) ask_q(static_cast<const __half*>(a.q));
+  else ask_q(static_cast<const __nv_bfloat16*>(a.q));
   prefetch();
-  load_q();
+  put_q();
   __syncthreads();
   bool dead = false;  // a wait ran out: no more work is issued
   {
@@ -1221,7 +1168,7 @@ typedef cudaError_t (*DecodeFn)(DecodeArgs a, const DecodeMaps& m, cudaStream_t 
 
 template <int D, int DV, int KT, int VT, bool SEL>
 cudaError_t run_decode(DecodeArgs a, const DecodeMaps& m, cudaStream_t s) {
-  constexpr DecodeShape C = decode_shape(D, DV, KT, VT);
+  constexpr DecodeShape C = decode_shape(D, DV, KT, VT, SEL);
   a.lift = weight_lift(VT);
   static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
   cudaError_t e = cudaSuccess;

@@ -39,12 +39,12 @@ struct DecodePlan {
 };
 
 // K: pages of a sequence that count at most
-static DecodePlan plan_decode(const Cache& c, int H, int K, int nsm) {
+static DecodePlan plan_decode(const Cache& c, int H, int K, bool sel, int nsm) {
   DecodePlan p;
   const int G = H / c.Hkv;
   p.chunks = (G + 7) / 8;
   p.HG = c.Hkv * p.chunks;
-  const int ctas = decode_shape(c.D, c.Dv, c.k_type, c.v_type).ctas;
+  const int ctas = decode_shape(c.D, c.Dv, c.k_type, c.v_type, sel).ctas;
   p.R = std::max(1, ctas * nsm / p.HG);  // items that run at a time
   // at most R + B (see fa_decode.cuh), and no more than tables of this width can ask for
   const long long cap = ((long long)std::min(K, c.max_pages) * c.page_size + 15) / 16, per = (cap + kMinTiles - 1) / kMinTiles;
@@ -81,7 +81,7 @@ extern "C" size_t fa_paged_decode_workspace_size(const fa_paged_cache* cache, in
   if (check_cache(cache, &c) != FA_OK || H < 1 || H % c.Hkv) return 0;
   int nsm = 0;
   if (fab_device(&nsm, nullptr) != FA_OK) nsm = 152;
-  return plan_decode(c, H, c.max_pages, nsm).bytes;
+  return plan_decode(c, H, c.max_pages, false, nsm).bytes;
 }
 
 // pages [B][Hkv][K], or NULL: all of them (K is max_pages then)
@@ -101,7 +101,7 @@ static fa_status decode(const void* q, int act, int64_t q_row, int64_t q_head, c
     return FA_ERR_ALIGN;
   int nsm = 0;
   if ((rc = fab_device(&nsm, &a.c.err)) != FA_OK) return rc;
-  const DecodePlan p = plan_decode(a.c, H, K, nsm);
+  const DecodePlan p = plan_decode(a.c, H, K, pages != nullptr, nsm);
   if ((long long)p.nitems * p.HG > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;

@@ -6,7 +6,9 @@
 // the same bits wherever and however it is computed, and so are the pages chosen by it.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
+#include "fa_mma.cuh"
 #include "fa_paged.cuh"
 #include "sm100.cuh"
 
@@ -32,7 +34,14 @@ __device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 
 // bounds: a lane holds eight components, D / 8 lanes a row.  A warp takes a page of its own, or where there are not as
 // many pages the CTA's warps share one.
 
-constexpr int kBoundWarps = 4;
+#ifndef KW
+#define KW 4
+#define KU 8
+#define KM 1
+#define KZ 8
+#define KA 1
+#endif
+constexpr int kBoundWarps = KW;
 
 __device__ __forceinline__ uint32_t load_u32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 // of three; a NaN gives way
@@ -114,7 +123,7 @@ struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
 // Largest and smallest values of rows r0, r0 + step, ... of a page's `rows` (at least one), the lane's components
 template <int TYPE>
 __device__ __forceinline__ void row_range(const uint8_t* page, unsigned cell, int e0, int r0, int step, int rows, float (&hi)[8], float (&lo)[8]) {
-  constexpr int U = TYPE == FA_F32 ? 4 : 8;
+  constexpr int U = TYPE == FA_F32 ? 4 : KU;
 #pragma unroll
   for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
 #pragma unroll 1
@@ -159,7 +168,7 @@ __device__ __forceinline__ void put_bounds(const BoundArgs& a, long long rec, in
 }
 
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kBoundWarps * 32) k_page_bounds(const BoundArgs a) {
+__global__ void __launch_bounds__(kBoundWarps * 32, KM) k_page_bounds(const BoundArgs a) {
   constexpr int LG = D / 8, GW = 32 / LG;  // lanes of a row, rows side by side in a warp
   constexpr int RB = TYPE == FA_F32 ? 4 * D : TYPE == FA_F16 ? 2 * D : TYPE == FA_Q8_0 ? D / 32 * 34 : D / 32 * 18;
   __shared__ float4 s_part[kBoundWarps - 1][4][32];
@@ -170,7 +179,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32) k_page_bounds(const BoundArg
   const int b = rest / a.Z, L = len_of(a.c, a.lens, b), f = a.first ? a.first[b] : 0;
   if (f < 0 || f >= L) return;
   const int n = pages_of(a.c, L), p0 = page_of(a.c, f);
-  const bool apart = n - p0 > a.Z;  // a warp a page
+  const bool apart = KA * (n - p0) > a.Z;  // a warp a page
   const unsigned cell = (unsigned)a.c.Hkv * RB;
   const int all = apart ? a.Z * kBoundWarps : a.Z;
   for (int p = p0 + (int)(apart ? z * kBoundWarps + warp : z); p < n; p += all) {
@@ -234,6 +243,7 @@ struct SelectArgs {
   const int32_t* lens;
   int H, G, K, first, last;
   float scale;
+  bool vec;        // every head of q starts on 16 bytes
   const float* alibi;
   uint32_t* keys;  // [B][Hkv][max_pages]
   int32_t* pages;
@@ -246,221 +256,313 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   const uint32_t u = __float_as_uint(s);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float act_at(const void* p, int act, long long i) {
-  if (act == FA_ACT_F32) return static_cast<const float*>(p)[i];
-  if (act == FA_ACT_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-// q of `ng` query heads from h0 on in 8 bits: a warp a block, a lane a component (WARPS warps of the CTA).
-constexpr int kHeads = 16;  // query heads whose codes lie in shared memory at a time
+// The whole numbers come from the tensor core: 16 pages by 8 query heads a product, the page's codes (largest ones,
+// then smallest) against q's positive and negative codes.  A code enters as the binary16 number 1152 + code, which is an
+// "and" and an "exclusive or" away from its byte, and 1152 times the sum of q's codes is taken off beforehand: all
+// sums stay whole numbers below 2^24, exact in f32.  (Products of four bytes on the plain units: 12.7 us for 1180 pages of
+// 4 KV heads of 256 with 6 query heads each, and 17.1 for 48 ragged sequences of up to 512 pages of 8 KV heads of 128.)
+//
+// Of a block of 32 components, lane t = lane & 3 holds components 8 t .. 8 t + 7 of pages g and g + 8, g = lane >> 2: a word
+// a k16 step, its bytes 0 and 2 the first pair of the operand, 1 and 3 the second.
+constexpr int kHeads = 8;  // query heads at a time
+constexpr float kCodeBias = 1152.f;
 template <int D>
-struct Codes {
-  uint32_t q[kHeads][D / 4];
-  float e[kHeads][D / 32];
+struct Queries {
+  float4 start[D / 32][4];   // of heads 2 t and 2 t + 1: what a block's sums start from, and the scales e
+  uint4 b[D / 32][2][32];    // a lane's operands of a block's four steps
 };
+// Query heads h0 .. h0 + ng - 1 in 8 bits: a thread takes the eight components that a lane holds of one head's block.
 template <int D, int WARPS>
-__device__ __forceinline__ void quantise_q(const SelectArgs& a, Codes<D>& s, int b, int h0, int ng) {
-  constexpr int NB = D / 32;
-  const int lane = threadIdx.x & 31;
-#pragma unroll 4
-  for (int i = threadIdx.x >> 5; i < ng * NB; i += WARPS) {
-    const int g = i / NB, k = i % NB;
-    const float x = act_at(a.q, a.act, b * a.q_row + (h0 + g) * a.q_head + k * 32 + lane);
-    const float m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(x))));
-    const bool some = m > kTinyAmax;
-    const int c = some ? max(-127, min(127, __float2int_rn(__fmul_rn(x, __fdiv_rn(127.f, m))))) : 0;
-    reinterpret_cast<int8_t*>(s.q[g])[k * 32 + lane] = (int8_t)c;
-    if (lane == 0) s.e[g][k] = some ? __fdiv_rn(m, 127.f) : 0.f;
+__device__ __forceinline__ void quantise_q(const SelectArgs& a, Queries<D>& s, int b, int h0, int ng) {
+  for (int i = threadIdx.x; i < D; i += WARPS * 32) {  // (D / 32 blocks of 8 heads by 4: whole warps)
+    const int k = i >> 5, g = (i >> 2) & 7, t = i & 3;
+    float x[8];
+    auto load = [&](auto* q) {  // (the type is told apart outside, so that the loads are under way together)
+      using T = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
+      const T* p = q + (b * a.q_row + (h0 + min(g, ng - 1)) * a.q_head + k * 32 + 8 * t);
+      Oct<T> o;
+      load8_raw(p, a.vec, o);
+      unpack8(o, x);
+    };
+    if (a.act == FA_ACT_F32) load(static_cast<const float*>(a.q));
+    else if (a.act == FA_ACT_F16) load(static_cast<const __half*>(a.q));
+    else load(static_cast<const __nv_bfloat16*>(a.q));
+    uint32_t top = 0;  // largest magnitude, as bits (a NaN is above infinity)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(fabsf(x[j])));
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    const float m = __uint_as_float(top);
+    const bool some = m > kTinyAmax && g < ng;
+    const float r = __fdiv_rn(127.f, m);
+    int c[8], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] = some ? max(-127, min(127, __float2int_rn(__fmul_rn(x[j], r)))) : 0;
+      sum += c[j];
+    }
+    sum += __shfl_xor_sync(kFull, sum, 1);
+    sum += __shfl_xor_sync(kFull, sum, 2);
+    uint32_t w[8];
+    auto pair = [&](int lo, int hi) { return pack_h2((float)lo, (float)hi); };
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const int c0 = c[4 * st], c1 = c[4 * st + 1], c2 = c[4 * st + 2], c3 = c[4 * st + 3];
+      w[2 * st] = pair(max(c0, 0), max(c2, 0)), w[2 * st + 1] = pair(max(c1, 0), max(c3, 0));
+      w[4 + 2 * st] = pair(min(c0, 0), min(c2, 0)), w[5 + 2 * st] = pair(min(c1, 0), min(c3, 0));
+    }
+    const int lane = i & 31;
+    s.b[k][0][lane] = make_uint4(w[0], w[1], w[2], w[3]), s.b[k][1][lane] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (t == 0) {
+      float* st = reinterpret_cast<float*>(&s.start[k][g >> 1]);
+      st[g & 1] = -kCodeBias * (float)sum, st[2 + (g & 1)] = some ? __fdiv_rn(m, 127.f) : 0.f;
+    }
   }
 }
 
-// A block of 32 components of a page's bounds
-struct Block {
-  uint4 hi[2], lo[2];
-  float d;
+// Bounds of pages g and g + 8, the lane's part of a block
+struct Bounds2 {
+  uint2 hi[2], lo[2];
+  float d[2];
 };
 template <int D>
-__device__ __forceinline__ void load_block(const SelectArgs& a, int page, unsigned hk, int blk, Block& x) {
-  if (page >= 0) {
-    const long long rec = (long long)page * a.c.Hkv + hk;
-    const uint4* p = reinterpret_cast<const uint4*>(a.codes + rec * 2 * D) + 2 * blk;
-    x.hi[0] = p[0], x.hi[1] = p[1], x.lo[0] = p[D / 16], x.lo[1] = p[D / 16 + 1];
-    x.d = a.scales[rec * (D / 32) + blk];
-  } else {  // no page: nothing to read, and none may exist
-    x.hi[0] = x.hi[1] = x.lo[0] = x.lo[1] = make_uint4(0, 0, 0, 0);
-    x.d = 0.f;
+__device__ __forceinline__ void load_bounds(const SelectArgs& a, const int (&page)[2], unsigned hk, int blk, int t, Bounds2& x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (page[i] >= 0) {
+      const long long rec = (long long)page[i] * a.c.Hkv + hk;
+      const uint2* p = reinterpret_cast<const uint2*>(a.codes + rec * 2 * D) + 4 * blk + t;
+      x.hi[i] = p[0], x.lo[i] = p[D / 8], x.d[i] = a.scales[rec * (D / 32) + blk];
+    } else {  // no page: nothing to read, and none may exist
+      x.hi[i] = x.lo[i] = make_uint2(0, 0), x.d[i] = 0.f;
+    }
   }
 }
-// The largest score of `ng` query heads for the page whose blocks D / 32 neighbouring lanes hold; far: the
-// distance of its last key
-template <int D>
-__device__ __forceinline__ float best_score(const SelectArgs& a, const Codes<D>& s, const Block& x, int blk, int h0, int ng, float far) {
-  const uint32_t hi[8] = {x.hi[0].x, x.hi[0].y, x.hi[0].z, x.hi[0].w, x.hi[1].x, x.hi[1].y, x.hi[1].z, x.hi[1].w};
-  const uint32_t lo[8] = {x.lo[0].x, x.lo[0].y, x.lo[0].z, x.lo[0].w, x.lo[1].x, x.lo[1].y, x.lo[1].z, x.lo[1].w};
-  float best = -INFINITY;
-#pragma unroll 4
-  for (int g = 0; g < ng; ++g) {
-    const uint4* qv = reinterpret_cast<const uint4*>(s.q[g]) + 2 * blk;
-    const uint4 q0 = qv[0], q1 = qv[1];
-    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-    int I = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t neg;  // 0xff in the bytes of negative codes
-      asm("prmt.b32 %0, %1, %1, 0xba98;" : "=r"(neg) : "r"(qw[i]));
-      I = __dp4a((int)((hi[i] & ~neg) | (lo[i] & neg)), (int)qw[i], I);
-    }
-    float t = __fmul_rn(__fmul_rn((float)I, x.d), s.e[g][blk]);
-#pragma unroll
-    for (int o = 1; o < D / 32; o <<= 1) t = __fadd_rn(t, __shfl_xor_sync(kFull, t, o));
-    t = __fmul_rn(t, a.scale);
-    if (a.alibi) t = __fadd_rn(t, __fmul_rn(a.alibi[h0 + g], far));
-    best = fmaxf(best, t != t ? INFINITY : t);
-  }
-  return best;
+__device__ __forceinline__ void step(float (&c)[4], uint32_t w0, uint32_t w1, uint32_t b0, uint32_t b1) {
+  constexpr uint32_t kMask = 0x00ff00ffu, kBias = 0x64806480u;  // 1152, 1152; the exclusive or flips the code's sign bit
+  mma_f16(c, and_xor(w0, kMask, kBias), and_xor(w1, kMask, kBias), and_xor(w0 >> 8, kMask, kBias), and_xor(w1 >> 8, kMask, kBias), b0, b1);
 }
 
 // The scores of pages [c0, c1) of sequence b (length L, n pages) and KV head hk as keys, through put(page, key) and,
-// where the query heads do not lie in shared memory at once, get(page).  A lane takes a block of 32 components, D / 32
-// lanes a page; a warp looks 32 page numbers up at once and has the next pages' bounds under way while it works.
-template <int D, int WARPS, typename Put, typename Get>
-__device__ __forceinline__ void score_pages(const SelectArgs& a, Codes<D>& s, int b, unsigned hk, int L, int n, int c0, int c1, Put put, Get get) {
-  constexpr int NB = D / 32, PW = 32 / NB, STEP = WARPS * PW;  // blocks; pages that a warp, and the CTA, takes at a time
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane & (NB - 1), mine = lane / NB;
+// where there are more than eight query heads, get(page); ready() is called before the first of them.
+template <int D, int WARPS, typename Ready, typename Put, typename Get>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, int b, unsigned hk, int L, int n, int c0, int c1, Ready ready, Put put,
+                                            Get get) {
+  constexpr int NB = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   for (int g0 = 0; g0 < a.G; g0 += kHeads) {
     const int ng = min(kHeads, a.G - g0), h0 = (int)hk * a.G + g0;
-    int found = -1;
-    auto look_up = [&](int p0) {  // the warp's next NB turns, from page p0 on
-      const int p = p0 + (lane / PW) * STEP + lane % PW;
-      found = p < c1 ? a.c.table[(long long)b * a.c.max_pages + p] : -1;
-      if (found < 0 || found >= a.c.num_pages) {
-        if (p < c1) report_page(a.c.err);
-        found = -1;
-      }
+    auto look_up = [&](int p0) {  // page number of page p0 + (lane & 15)
+      const int p = p0 + (lane & 15);
+      if (p >= c1) return -1;
+      const int page = a.c.table[(long long)b * a.c.max_pages + p];
+      if (page >= 0 && page < a.c.num_pages) return page;
+      report_page(a.c.err);
+      return -1;
     };
-    const int first = c0 + warp * PW;
-    int turn = 0;  // of the look-up
-    Block x, y;
-    int page = -1;
-    look_up(first);
-    if (first < c1) page = __shfl_sync(kFull, found, mine), load_block<D>(a, page, hk, blk, x);
+    // (small heads: the next pages' bounds are under way while these are scored)
+    constexpr bool AHEAD = NB <= 4;
+    int p0 = c0 + warp * 16, page[2];
+    Bounds2 x[NB], y[AHEAD ? NB : 1];
+    auto fetch = [&](int found, Bounds2* z) {
+      page[0] = __shfl_sync(kFull, found, g), page[1] = __shfl_sync(kFull, found, g + 8);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) load_bounds<D>(a, page, hk, k, t, z[k]);
+    };
+    int found = look_up(p0);
+    if (p0 < c1) fetch(found, x);
+    if (AHEAD) found = look_up(p0 + WARPS * 16);
+    int there[2];
     if (g0) __syncthreads();
     quantise_q<D, WARPS>(a, s, b, h0, ng);
     __syncthreads();
-    for (int p0 = first; p0 < c1; p0 += STEP) {
-      int page2 = -1;
-      if (p0 + STEP < c1) {
-        if (++turn == NB) turn = 0, look_up(p0 + STEP);
-        page2 = __shfl_sync(kFull, found, turn * PW + mine);
-        load_block<D>(a, page2, hk, blk, y);
+    ready();
+    const float slope[2] = {a.alibi && 2 * t < ng ? a.alibi[h0 + 2 * t] : 0.f, a.alibi && 2 * t + 1 < ng ? a.alibi[h0 + 2 * t + 1] : 0.f};
+    for (; p0 < c1; p0 += WARPS * 16) {
+      there[0] = page[0], there[1] = page[1];
+      const int next = AHEAD ? look_up(p0 + 2 * WARPS * 16) : look_up(p0 + WARPS * 16);
+      if (AHEAD && p0 + WARPS * 16 < c1) fetch(found, y);
+      float l0[4], l1[4], l2[4], sum[4];  // the tree over the blocks, a level each
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const float4 st = s.start[k][t];
+        const uint4 b0 = s.b[k][0][lane], b1 = s.b[k][1][lane];
+        float c[4] = {st.x, st.y, st.x, st.y};
+        step(c, x[k].hi[0].x, x[k].hi[1].x, b0.x, b0.y);
+        step(c, x[k].hi[0].y, x[k].hi[1].y, b0.z, b0.w);
+        step(c, x[k].lo[0].x, x[k].lo[1].x, b1.x, b1.y);
+        step(c, x[k].lo[0].y, x[k].lo[1].y, b1.z, b1.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = __fmul_rn(__fmul_rn(c[i], x[k].d[i >> 1]), i & 1 ? st.w : st.z);
+          if (!(k & 1)) {
+            l0[i] = v;
+            continue;
+          }
+          v = __fadd_rn(l0[i], v);
+          if (NB > 2 && !(k & 2)) {
+            l1[i] = v;
+            continue;
+          }
+          if (NB > 2) v = __fadd_rn(l1[i], v);
+          if (NB > 4 && !(k & 4)) {
+            l2[i] = v;
+            continue;
+          }
+          if (NB > 4) v = __fadd_rn(l2[i], v);
+          sum[i] = v;
+        }
       }
-      const int p = p0 + mine;
-      const float far = (float)(min((long long)(p + 1) * a.c.page_size, (long long)L) - L);
-      const float best = best_score<D>(a, s, x, blk, h0, ng, far);
-      if (p < c1 && blk == 0) {
-        uint32_t key = page < 0 ? kNoPage : key_of(best);
-        if (g0 && page >= 0) key = max(key, get(p));
+      float best[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = p0 + g + 8 * i;
+        const float far = (float)(min((long long)(p + 1) * a.c.page_size, (long long)L) - L);
+        best[i] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = __fmul_rn(sum[2 * i + j], a.scale);
+          if (a.alibi) v = __fadd_rn(v, __fmul_rn(slope[j], far));
+          v = v != v ? INFINITY : v;
+          if (2 * t + j < ng) best[i] = fmaxf(best[i], v);
+        }
+        best[i] = fmaxf(best[i], __shfl_xor_sync(kFull, best[i], 1));
+        best[i] = fmaxf(best[i], __shfl_xor_sync(kFull, best[i], 2));
+      }
+      const int p = p0 + g + 8 * t;
+      if (t < 2 && p < c1) {
+        uint32_t key = (t ? there[1] : there[0]) < 0 ? kNoPage : key_of(t ? best[1] : best[0]);
+        if (g0 && key != kNoPage) key = max(key, get(p));
         if (p < a.first || p >= n - a.last) key = kForced;
         put(p, key);
       }
-      x = y, page = page2;
+      found = next;
+      if (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) x[k] = y[AHEAD ? k : 0];
+      } else if (p0 + WARPS * 16 < c1) {
+        fetch(found, x);
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------------------------------------
 // the K largest of n keys, by a CTA.  Its warps own neighbouring stretches of the pages, so that what they choose is in
-// ascending order.  The K-th largest is found by bisection between the smallest and the largest: a count a step, and
-// as a rule it ends when exactly K are above, after little more than log2(n) steps.
+// ascending order.  The K-th largest is found by counting keys in 256 equal bins between the smallest and the largest,
+// then in 256 of the bin that it lies in, and so on: it ends when exactly K are above a bin's start, after two rounds
+// as a rule.  (Bisection, a count a step: 12 steps and 1.5 us more for 1180 pages.)
 
-constexpr int kPickWarps = 8;
+constexpr int kBins = 256, kHeld = 8;  // kHeld: keys that a thread holds in registers
 
-struct Count {  // a word from each warp, double-buffered: one barrier a sum
-  uint32_t s[2][kPickWarps];
-  uint32_t ends[2][kPickWarps];
+struct Bins {
+  uint32_t n[kBins];
+  uint32_t ends[2][16];      // a word a warp
+  uint32_t bin, above, all;  // where the K-th largest is: keys above the bin, and with those in it
 };
-// Sum over the CTA; every thread gets it.
-__device__ __forceinline__ uint32_t cta_sum(uint32_t v, Count& c, int& turn) {
-  const uint32_t w = __reduce_add_sync(kFull, v);
-  if ((threadIdx.x & 31) == 0) c.s[turn][threadIdx.x >> 5] = w;
-  __syncthreads();
-  const uint4* s = reinterpret_cast<const uint4*>(c.s[turn]);
-  turn ^= 1;
-  uint32_t sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPickWarps / 4; ++i) {
-    const uint4 x = s[i];
-    sum += (x.x + x.y) + (x.z + x.w);
-  }
-  return sum;
-}
 
-__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Count& cnt) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rounds = (n + kPickWarps * 32 - 1) / (kPickWarps * 32), base = warp * rounds * 32 + lane;
+template <int WARPS, bool HELD>
+__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Bins& s) {
+  static_assert(WARPS * 32 >= kBins && WARPS <= 16, "a thread a bin");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rounds = (n + WARPS * 32 - 1) / (WARPS * 32), base = warp * rounds * 32 + lane;
+  const uint32_t K = (uint32_t)a.K, forced = (uint32_t)(a.first + a.last);
+  uint32_t r[HELD ? kHeld : 1];
+  if (HELD) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < rounds) r[i] = base + i * 32 < n ? keys[base + i * 32] : 0;
+  }
+  auto each = [&](auto f) {  // f(key, page, there is one) for the thread's keys
+    if (HELD) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i < rounds) f(r[HELD ? i : 0], base + i * 32, base + i * 32 < n);
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < rounds; ++i) f(base + i * 32 < n ? keys[base + i * 32] : 0u, base + i * 32, base + i * 32 < n);
+    }
+  };
   // the range of the scores that are not forced
   uint32_t least = 0xffffffffu, most = 0;
-  for (int i = 0, p = base; i < rounds; ++i, p += 32) {
-    const uint32_t k = p < n ? keys[p] : kForced;
-    if (k != kForced) least = min(least, k), most = max(most, k);
-  }
+  each([&](uint32_t k, int, bool in) {
+    if (in && k != kForced) least = min(least, k), most = max(most, k);
+  });
   least = __reduce_min_sync(kFull, least), most = __reduce_max_sync(kFull, most);
-  if (lane == 0) cnt.ends[0][warp] = least, cnt.ends[1][warp] = most;
+  if (lane == 0) s.ends[0][warp] = least, s.ends[1][warp] = most;
+  if (tid < kBins) s.n[tid] = 0;
   __syncthreads();
-  uint32_t lo = __reduce_min_sync(kFull, cnt.ends[0][lane & (kPickWarps - 1)]);
-  uint32_t hi = __reduce_max_sync(kFull, cnt.ends[1][lane & (kPickWarps - 1)]);
-  int turn = 0;
-  const uint32_t K = (uint32_t)a.K;
-  uint32_t above = (uint32_t)(a.first + a.last);  // keys above hi
-  bool ties = false;                              // T is shared by more keys than there is room for
-  uint32_t T = kForced;
-  if (above < K) {  // at least K keys are at or above lo, and fewer above hi
-    while (lo < hi) {
-      const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
-      uint32_t c = 0;
-#pragma unroll 4
-      for (int i = 0, p = base; i < rounds; ++i, p += 32) c += p < n && keys[p] >= mid;
-      c = cta_sum(c, cnt, turn);
-      if (c == K) {
-        T = mid;
-        break;
-      }
-      if (c > K) lo = mid;
-      else hi = mid - 1, above = c;
+  uint32_t lo = __reduce_min_sync(kFull, s.ends[0][lane & (WARPS - 1)]);
+  uint32_t hi = __reduce_max_sync(kFull, s.ends[1][lane & (WARPS - 1)]);
+  uint32_t T = kForced, above = forced;
+  bool ties = false;  // T is shared by more keys than there is room for
+  while (above < K) {  // `above` keys are above hi, and at least K - above in [lo, hi]
+    const int shift = max(0, 24 - __clz(hi - lo | 1));  // (hi - lo) >> shift < 256
+    each([&](uint32_t k, int, bool in) {
+      if (in && k >= lo && k <= hi) atomicAdd(&s.n[(k - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // keys from a bin's start on: a thread a bin, from the highest down
+    const uint32_t own = tid < kBins ? s.n[kBins - 1 - tid] : 0;
+    uint32_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += x;
     }
-    if (lo == hi) T = lo, ties = true;
+    if (lane == 31) s.ends[0][warp] = sum;
+    __syncthreads();
+    sum += above;
+#pragma unroll
+    for (int w = 0; w < kBins / 32; ++w) sum += w < warp ? s.ends[0][w] : 0;
+    if (tid < kBins && sum - own < K && K <= sum) s.bin = kBins - 1 - tid, s.above = sum - own, s.all = sum;
+    if (tid < kBins) s.n[tid] = 0;
+    __syncthreads();
+    lo += s.bin << shift, above = s.above;
+    T = lo;
+    if (s.all == K) break;
+    if (shift == 0) {
+      ties = true;
+      break;
+    }
+    hi = min(hi, lo + (1u << shift) - 1);
+    __syncthreads();  // (the three words have been read)
   }
   // who is chosen, in order: those above T (or at it), and the first K - above of those at T
   const uint32_t room = ties ? K - above : 0;
   uint32_t chosen = 0, equal = 0;  // of this warp's
-  for (int i = 0, p = base; i < rounds; ++i, p += 32) {
-    const uint32_t k = p < n ? keys[p] : 0;
-    const bool same = p < n && ties && k == T;
-    chosen += __popc(__ballot_sync(kFull, p < n && k >= T && !same));
+  each([&](uint32_t k, int, bool in) {
+    const bool same = in && ties && k == T;
+    chosen += __popc(__ballot_sync(kFull, in && k >= T && !same));
     equal += __popc(__ballot_sync(kFull, same));
-  }
+  });
   __syncthreads();  // (`ends` has been read)
-  if (lane == 0) cnt.ends[0][warp] = chosen, cnt.ends[1][warp] = equal;
+  if (lane == 0) s.ends[0][warp] = chosen, s.ends[1][warp] = equal;
   __syncthreads();
   uint32_t before = 0, eq_before = 0;
-  for (int w = 0; w < warp; ++w) before += cnt.ends[0][w], eq_before += cnt.ends[1][w];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w)
+    if (w < warp) before += s.ends[0][w], eq_before += s.ends[1][w];
   before += min(eq_before, room);
   const uint32_t below = (1u << lane) - 1;
-  for (int i = 0, p = base; i < rounds; ++i, p += 32) {
-    const uint32_t k = p < n ? keys[p] : 0;
-    const bool same = p < n && ties && k == T;
+  each([&](uint32_t k, int p, bool in) {
+    const bool same = in && ties && k == T;
     const uint32_t eq = __ballot_sync(kFull, same);
-    const bool take = same ? eq_before + __popc(eq & below) < room : p < n && k >= T;
+    const bool take = same ? eq_before + __popc(eq & below) < room : in && k >= T;
     const uint32_t all = __ballot_sync(kFull, take);
     if (take) out[before + __popc(all & below)] = p;
     before += __popc(all), eq_before += __popc(eq);
-  }
+  });
+}
+template <int WARPS>
+__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Bins& s) {
+  if (n <= kHeld * WARPS * 32) pick<WARPS, true>(a, keys, out, n, s);
+  else pick<WARPS, false>(a, keys, out, n, s);
 }
 
 // A sequence of at most K pages: all of them
 __device__ __forceinline__ void pick_all(const SelectArgs& a, int32_t* out, int n) {
-  for (int i = threadIdx.x; i < a.K; i += kPickWarps * 32) out[i] = i < n ? i : -1;
+  for (int i = threadIdx.x; i < a.K; i += blockDim.x) out[i] = i < n ? i : -1;
 }
 
 // ---- in one: a cluster a sequence and KV head, whose CTAs score a stretch of the pages each; the keys go to the first
@@ -470,11 +572,11 @@ __device__ __forceinline__ uint32_t at_first_cta(const void* p) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
   return r;
 }
-template <int D>
-__global__ void __launch_bounds__(kPickWarps * 32, 3) k_page_select(const SelectArgs a) {
+template <int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const SelectArgs a) {
   extern __shared__ __align__(16) uint32_t s_keys[];
-  __shared__ __align__(16) Codes<D> s_codes;
-  __shared__ __align__(16) Count s_cnt;
+  __shared__ __align__(16) Queries<D> s_q;
+  __shared__ Bins s_bins;
   cluster_arrive();
   after_last();
   lets_next();
@@ -488,22 +590,27 @@ __global__ void __launch_bounds__(kPickWarps * 32, 3) k_page_select(const Select
     return;
   }
   const uint32_t keys = at_first_cta(s_keys);
+  bool there = false;
+  auto ready = [&] {  // the first CTA's memory is there
+    if (!there) cluster_wait();
+    there = true;
+  };
   auto put = [&](int p, uint32_t k) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys + 4 * p), "r"(k) : "memory"); };
   auto get = [&](int p) {
     uint32_t k;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(keys + 4 * p) : "memory");
     return k;
   };
-  cluster_wait();  // the first CTA's memory is there
-  score_pages<D, kPickWarps>(a, s_codes, b, hk, L, n, (int)((long long)n * rank / C), (int)((long long)n * (rank + 1) / C), put, get);
+  score_pages<D, WARPS>(a, s_q, b, hk, L, n, (int)((long long)n * rank / C), (int)((long long)n * (rank + 1) / C), ready, put, get);
   cluster_barrier();
-  if (rank == 0) pick(a, s_keys, out, n, s_cnt);
+  if (rank == 0) pick<WARPS>(a, s_keys, out, n, s_bins);
 }
 
 // ---- in two, where the keys of a sequence may not fit there: scores into the workspace, then the choice
+constexpr int kWideWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kPickWarps * 32, 3) k_page_scores(const SelectArgs a) {
-  __shared__ __align__(16) Codes<D> s_codes;
+__global__ void __launch_bounds__(kWideWarps * 32, 2) k_page_scores(const SelectArgs a) {
+  __shared__ __align__(16) Queries<D> s_q;
   after_last();
   lets_next();
   const unsigned hk = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv;
@@ -513,10 +620,10 @@ __global__ void __launch_bounds__(kPickWarps * 32, 3) k_page_scores(const Select
   uint32_t* keys = a.keys + ((long long)b * a.c.Hkv + hk) * a.c.max_pages;
   auto put = [&](int p, uint32_t k) { keys[p] = k; };
   auto get = [&](int p) { return keys[p]; };
-  score_pages<D, kPickWarps>(a, s_codes, b, hk, L, n, c0, min(n, c0 + a.chunk), put, get);
+  score_pages<D, kWideWarps>(a, s_q, b, hk, L, n, c0, min(n, c0 + a.chunk), [] {}, put, get);
 }
-__global__ void __launch_bounds__(kPickWarps * 32) k_page_pick(const SelectArgs a) {
-  __shared__ __align__(16) Count s_cnt;
+__global__ void __launch_bounds__(kWideWarps * 32) k_page_pick(const SelectArgs a) {
+  __shared__ Bins s_bins;
   after_last();
   lets_next();
   const int b = blockIdx.x / a.c.Hkv;
@@ -524,7 +631,7 @@ __global__ void __launch_bounds__(kPickWarps * 32) k_page_pick(const SelectArgs 
   const int n = pages_of(a.c, len_of(a.c, a.lens, b));
   int32_t* out = a.pages + (long long)blockIdx.x * a.K;
   if (n <= a.K) pick_all(a, out, n);
-  else pick(a, a.keys + (long long)blockIdx.x * a.c.max_pages, out, n, s_cnt);
+  else pick<kWideWarps>(a, a.keys + (long long)blockIdx.x * a.c.max_pages, out, n, s_bins);
 }
 
 static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
@@ -537,26 +644,31 @@ static size_t key_bytes(const Cache& c) {
   if (c.max_pages <= kOnePages) return 256;
   return std::max<size_t>(256, ((size_t)c.B * c.Hkv * c.max_pages * sizeof(uint32_t) + 255) / 256 * 256);
 }
+template <int D, int WARPS>
+static cudaError_t run_clusters(const SelectArgs& a, unsigned C, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
+  if (!allow_smem(reinterpret_cast<const void*>(k_page_select<D, WARPS>), kOnePages * 4, &ready)) return cudaErrorInvalidValue;
+  return launch_clusters(k_page_select<D, WARPS>, (unsigned)a.c.B * a.c.Hkv * C, C, WARPS * 32, (size_t)a.c.max_pages * 4, s, a);
+}
 template <int D>
 static cudaError_t run_select(SelectArgs a, int nsm, cudaStream_t s) {
-  static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
   const long long rows = (long long)a.c.B * a.c.Hkv;
+  constexpr int turn = 8 * 16;  // pages that eight warps take at a time
   if (a.c.max_pages <= kOnePages) {
-    // CTAs of a cluster: as many as give each at least a turn of its warps, and all of them two to an SM
+    // CTAs of a cluster: as many as get a turn each, while all of them run at once, two to an SM; and where even
+    // eight leave SMs free and have more than a turn each, CTAs of twice the warps, one to an SM.
     unsigned C = 1;
-    const int turn = kPickWarps * 32 / (D / 32);
-    while (C < 8 && a.c.max_pages > 2 * (int)C * turn && rows * C * 2 <= 2LL * nsm) C *= 2;
-    if (!allow_smem(reinterpret_cast<const void*>(k_page_select<D>), kOnePages * 4, &ready)) return cudaErrorInvalidValue;
-    return launch_clusters(k_page_select<D>, (unsigned)(rows * C), C, kPickWarps * 32, (size_t)a.c.max_pages * 4, s, a);
+    while (C < 8 && a.c.max_pages > (int)C * turn && rows * C * 2 <= 2LL * nsm) C *= 2;
+    if (C == 8 && a.c.max_pages > (int)C * turn && rows * C <= nsm) return run_clusters<D, 16>(a, C, s);
+    return run_clusters<D, 8>(a, C, s);
   }
-  const long long turn = kPickWarps * 32 / (D / 32), most = (a.c.max_pages + turn - 1) / turn;
-  const long long want = std::min(most, std::max(1LL, 8LL * nsm / rows));
+  const long long most = (a.c.max_pages + turn - 1) / turn, want = std::min(most, std::max(1LL, 8LL * nsm / rows));
   a.chunk = (int)((most + want - 1) / want * turn);
   a.chunks = (a.c.max_pages + a.chunk - 1) / a.chunk;
   if (rows * a.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_next(k_page_scores<D>, dim3((unsigned)(rows * a.chunks)), dim3(kPickWarps * 32), 0, s, a);
+  const cudaError_t e = launch_next(k_page_scores<D>, dim3((unsigned)(rows * a.chunks)), dim3(kWideWarps * 32), 0, s, a);
   if (e != cudaSuccess) return e;
-  return launch_next(k_page_pick, dim3((unsigned)rows), dim3(kPickWarps * 32), 0, s, a);
+  return launch_next(k_page_pick, dim3((unsigned)rows), dim3(kWideWarps * 32), 0, s, a);
 }
 static bool select_range(const Cache& c, int H) {
   return c.max_pages <= (1 << 22) && H <= 65535 && (long long)c.B * c.Hkv < (1 << 22);
@@ -579,7 +691,7 @@ extern "C" fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_b
   if (a.c.B == 0 || a.c.max_pages == 0) return FA_OK;
   a.codes = bounds->codes, a.scales = bounds->scales, a.first = first, a.lens = seq_lens;
   const long long rows = (long long)a.c.B * a.c.Hkv;
-  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, 8LL * nsm / rows));
+  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, (long long)KZ * nsm / rows));
   if (rows * a.Z > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const BoundKernel k = a.c.D == 64 ? pick_bounds<64>(a.c.k_type) : a.c.D == 128 ? pick_bounds<128>(a.c.k_type) : pick_bounds<256>(a.c.k_type);
   return launch_next(k, dim3((unsigned)(rows * a.Z)), dim3(kBoundWarps * 32), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess
@@ -615,6 +727,8 @@ extern "C" fa_status fa_page_select(const void* q, int act, int64_t q_row, int64
   a.codes = bounds->codes, a.scales = bounds->scales, a.q = q, a.act = act, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens;
   a.H = H, a.G = H / a.c.Hkv, a.K = K, a.first = first, a.last = last, a.scale = scale, a.alibi = alibi_slopes;
   a.keys = static_cast<uint32_t*>(workspace), a.pages = pages;
+  const int es = act_bytes(act);
+  a.vec = aligned(q, 16) && (q_row * es) % 16 == 0 && (q_head * es) % 16 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a.c.D == 64 ? run_select<64>(a, nsm, s) : a.c.D == 128 ? run_select<128>(a, nsm, s) : run_select<256>(a, nsm, s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -405,20 +405,24 @@ PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-#define FAST(name, n)                                                                                      \
+// n arguments, of which the last `more` may be left out (None then)
+#define FAST(name, n, more)                                                                                \
   PyObject* py_##name(PyObject* self, PyObject* const* argv, Py_ssize_t argc) {                            \
-    if (argc != n || !fn.norm) return PyErr_Format(PyExc_TypeError, #name ": %d arguments, after bind()", n); \
-    return name(self, argv, argc);                                                                         \
+    if (argc > n || argc < n - more || !fn.norm)                                                           \
+      return PyErr_Format(PyExc_TypeError, #name ": %d arguments, after bind()", n);                       \
+    PyObject* all[n];                                                                                      \
+    for (Py_ssize_t i = 0; i < n; ++i) all[i] = i < argc ? argv[i] : Py_None;                              \
+    return name(self, all, n);                                                                             \
   }
-FAST(norm, 10)
-FAST(norm_back, 11)
-FAST(append, 12)
-FAST(read, 5)
-FAST(decode, 9)
-FAST(extend, 4)
-FAST(trim, 3)
-FAST(bounds, 5)
-FAST(select_pages, 10)
+FAST(norm, 10, 1)
+FAST(norm_back, 11, 1)
+FAST(append, 12, 2)
+FAST(read, 5, 0)
+FAST(decode, 9, 1)
+FAST(extend, 4, 0)
+FAST(trim, 3, 0)
+FAST(bounds, 5, 0)
+FAST(select_pages, 10, 0)
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
