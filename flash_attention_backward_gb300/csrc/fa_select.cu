@@ -34,6 +34,9 @@ __device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 
 // bounds: a lane holds eight components, D / 8 lanes a row.  A warp takes a page of its own, or where there are not as
 // many pages the CTA's warps share one.
 
+#ifndef S128
+#define S128 2
+#endif
 #ifndef KW
 #define KW 4
 #define KU 8
@@ -273,20 +276,29 @@ struct Queries {
 };
 // Query heads h0 .. h0 + ng - 1 in 8 bits: a thread takes the eight components that a lane holds of one head's block.
 template <int D, int WARPS>
-__device__ __forceinline__ void quantise_q(const SelectArgs& a, Queries<D>& s, int b, int h0, int ng) {
-  for (int i = threadIdx.x; i < D; i += WARPS * 32) {  // (D / 32 blocks of 8 heads by 4: whole warps)
-    const int k = i >> 5, g = (i >> 2) & 7, t = i & 3;
-    float x[8];
+struct HeadPart {
+  static_assert(WARPS * 32 >= D, "a part a thread");
+  float x[8];
+  // (D / 32 blocks of 8 heads by 4: whole warps take part or none of their lanes)
+  static __device__ __forceinline__ bool mine() { return threadIdx.x < D; }
+  static __device__ __forceinline__ int block() { return threadIdx.x >> 5; }
+  static __device__ __forceinline__ int head() { return (threadIdx.x >> 2) & 7; }
+
+  __device__ __forceinline__ void ask(const SelectArgs& a, int b, int h0, int ng) {
+    if (!mine()) return;
+    const long long at = b * a.q_row + (h0 + min(head(), ng - 1)) * a.q_head + block() * 32 + 8 * (threadIdx.x & 3);
     auto load = [&](auto* q) {  // (the type is told apart outside, so that the loads are under way together)
-      using T = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
-      const T* p = q + (b * a.q_row + (h0 + min(g, ng - 1)) * a.q_head + k * 32 + 8 * t);
-      Oct<T> o;
-      load8_raw(p, a.vec, o);
+      Oct<std::remove_const_t<std::remove_pointer_t<decltype(q)>>> o;
+      load8_raw(q + at, a.vec, o);
       unpack8(o, x);
     };
     if (a.act == FA_ACT_F32) load(static_cast<const float*>(a.q));
     else if (a.act == FA_ACT_F16) load(static_cast<const __half*>(a.q));
     else load(static_cast<const __nv_bfloat16*>(a.q));
+  }
+  __device__ __forceinline__ void put(Queries<D>& s, int ng) {
+    if (!mine()) return;
+    const int k = block(), g = head(), lane = threadIdx.x & 31;
     uint32_t top = 0;  // largest magnitude, as bits (a NaN is above infinity)
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(fabsf(x[j])));
@@ -311,90 +323,106 @@ __device__ __forceinline__ void quantise_q(const SelectArgs& a, Queries<D>& s, i
       w[2 * st] = pair(max(c0, 0), max(c2, 0)), w[2 * st + 1] = pair(max(c1, 0), max(c3, 0));
       w[4 + 2 * st] = pair(min(c0, 0), min(c2, 0)), w[5 + 2 * st] = pair(min(c1, 0), min(c3, 0));
     }
-    const int lane = i & 31;
     s.b[k][0][lane] = make_uint4(w[0], w[1], w[2], w[3]), s.b[k][1][lane] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (t == 0) {
+    if ((lane & 3) == 0) {
       float* st = reinterpret_cast<float*>(&s.start[k][g >> 1]);
       st[g & 1] = -kCodeBias * (float)sum, st[2 + (g & 1)] = some ? __fdiv_rn(m, 127.f) : 0.f;
     }
   }
-}
-
-// Bounds of pages g and g + 8, the lane's part of a block
-struct Bounds2 {
-  uint2 hi[2], lo[2];
-  float d[2];
 };
+
+// A warp's slots in shared memory: the codes of 16 pages each, brought by asynchronous copies of 16 bytes a lane.
+// (Loaded into registers as the products take them, eight bytes of eight pages at a time, the lookups of their lines bound
+// the kernel: 15.4 us for 48 ragged sequences.)  Rows start 32 bytes, modulo 128, after one another: the words of a
+// fragment load lie in different banks.
 template <int D>
-__device__ __forceinline__ void load_bounds(const SelectArgs& a, const int (&page)[2], unsigned hk, int blk, int t, Bounds2& x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (page[i] >= 0) {
-      const long long rec = (long long)page[i] * a.c.Hkv + hk;
-      const uint2* p = reinterpret_cast<const uint2*>(a.codes + rec * 2 * D) + 4 * blk + t;
-      x.hi[i] = p[0], x.lo[i] = p[D / 8], x.d[i] = a.scales[rec * (D / 32) + blk];
-    } else {  // no page: nothing to read, and none may exist
-      x.hi[i] = x.lo[i] = make_uint2(0, 0), x.d[i] = 0.f;
-    }
-  }
+struct Slots {
+  static constexpr int PITCH = 2 * D + 32, BYTES = 16 * PITCH, N = D == 256 ? 1 : D == 128 ? S128 : 2;
+};
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 __device__ __forceinline__ void step(float (&c)[4], uint32_t w0, uint32_t w1, uint32_t b0, uint32_t b1) {
   constexpr uint32_t kMask = 0x00ff00ffu, kBias = 0x64806480u;  // 1152, 1152; the exclusive or flips the code's sign bit
   mma_f16(c, and_xor(w0, kMask, kBias), and_xor(w1, kMask, kBias), and_xor(w0 >> 8, kMask, kBias), and_xor(w1 >> 8, kMask, kBias), b0, b1);
 }
 
 // The scores of pages [c0, c1) of sequence b (length L, n pages) and KV head hk as keys, through put(page, key) and,
-// where there are more than eight query heads, get(page); ready() is called before the first of them.
-template <int D, int WARPS, typename Ready, typename Put, typename Get>
-__device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, int b, unsigned hk, int L, int n, int c0, int c1, Ready ready, Put put,
-                                            Get get) {
-  constexpr int NB = D / 32;
+// where there are more than eight query heads, get(page); ready() is called before the first of them, and range(least,
+// most) in the end by every warp, with the range of its keys that are not forced.
+template <int D, int WARPS, typename Ready, typename Put, typename Get, typename Range>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, uint8_t* slots, int b, unsigned hk, int L, int n, int c0, int c1, Ready ready,
+                                            Put put, Get get, Range range) {
+  using Sl = Slots<D>;
+  constexpr int NB = D / 32, S = Sl::N, TURN = WARPS * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const uint8_t* mine = slots + warp * S * Sl::BYTES;
+  const uint32_t ring = fab::smem_u32(mine);
+  auto look_up = [&](int p0) {  // page number of page p0 + (lane & 15)
+    const int p = p0 + (lane & 15);
+    if (p >= c1) return -1;
+    const int page = a.c.table[(long long)b * a.c.max_pages + p];
+    if (page >= 0 && page < a.c.num_pages) return page;
+    report_page(a.c.err);
+    return -1;
+  };
+  auto fetch = [&](int slot, int found) {  // their codes into a slot (where there is no page, whatever lies there)
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const int row = (i * 32 + lane) / (D / 8), off = (i * 32 + lane) % (D / 8) * 16, page = __shfl_sync(kFull, found, row);
+      if (page >= 0) copy16(ring + slot * Sl::BYTES + row * Sl::PITCH + off, a.codes + ((long long)page * a.c.Hkv + hk) * 2 * D + off);
+    }
+    copies_end();
+  };
+  auto scales = [&](int found, float (&d)[NB]) {  // page lane & 15's
+    const float* p = a.scales + ((long long)found * a.c.Hkv + hk) * NB;
+#pragma unroll
+    for (int k = 0; k < NB; k += 2) {
+      const float2 v = found >= 0 ? *reinterpret_cast<const float2*>(p + k) : make_float2(0.f, 0.f);
+      d[k] = v.x, d[k + 1] = v.y;
+    }
+  };
   for (int g0 = 0; g0 < a.G; g0 += kHeads) {
     const int ng = min(kHeads, a.G - g0), h0 = (int)hk * a.G + g0;
-    auto look_up = [&](int p0) {  // page number of page p0 + (lane & 15)
-      const int p = p0 + (lane & 15);
-      if (p >= c1) return -1;
-      const int page = a.c.table[(long long)b * a.c.max_pages + p];
-      if (page >= 0 && page < a.c.num_pages) return page;
-      report_page(a.c.err);
-      return -1;
-    };
-    // (small heads: the next pages' bounds are under way while these are scored)
-    constexpr bool AHEAD = NB <= 4;
-    int p0 = c0 + warp * 16, page[2];
-    Bounds2 x[NB], y[AHEAD ? NB : 1];
-    auto fetch = [&](int found, Bounds2* z) {
-      page[0] = __shfl_sync(kFull, found, g), page[1] = __shfl_sync(kFull, found, g + 8);
-#pragma unroll
-      for (int k = 0; k < NB; ++k) load_bounds<D>(a, page, hk, k, t, z[k]);
-    };
-    int found = look_up(p0);
-    if (p0 < c1) fetch(found, x);
-    if (AHEAD) found = look_up(p0 + WARPS * 16);
-    int there[2];
+    int p0 = c0 + warp * 16, slot = 0, now, later = -1;  // pages of this turn, and of the next one where its copies are under way
+    float d[NB], d2[S == 2 ? NB : 1];
+    now = look_up(p0);
+    if constexpr (S == 2) later = look_up(p0 + TURN);
+    HeadPart<D, WARPS> q;
+    q.ask(a, b, h0, ng);
+    fetch(0, now), scales(now, d);
+    if constexpr (S == 2) fetch(1, later), scales(later, d2);
     if (g0) __syncthreads();
-    quantise_q<D, WARPS>(a, s, b, h0, ng);
+    q.put(s, ng);
     __syncthreads();
     ready();
+    uint32_t least = 0xffffffffu, most = 0;
     const float slope[2] = {a.alibi && 2 * t < ng ? a.alibi[h0 + 2 * t] : 0.f, a.alibi && 2 * t + 1 < ng ? a.alibi[h0 + 2 * t + 1] : 0.f};
-    for (; p0 < c1; p0 += WARPS * 16) {
-      there[0] = page[0], there[1] = page[1];
-      const int next = AHEAD ? look_up(p0 + 2 * WARPS * 16) : look_up(p0 + WARPS * 16);
-      if (AHEAD && p0 + WARPS * 16 < c1) fetch(found, y);
+    for (; p0 < c1; p0 += TURN) {
+      const int next = look_up(p0 + S * TURN);
+      copies_wait<S - 1>();
+      __syncwarp();
+      const uint8_t* at = mine + slot * Sl::BYTES + g * Sl::PITCH + 8 * t;
+      auto word2 = [&](int off) { return *reinterpret_cast<const uint2*>(at + off); };
       float l0[4], l1[4], l2[4], sum[4];  // the tree over the blocks, a level each
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const float4 st = s.start[k][t];
         const uint4 b0 = s.b[k][0][lane], b1 = s.b[k][1][lane];
         float c[4] = {st.x, st.y, st.x, st.y};
-        step(c, x[k].hi[0].x, x[k].hi[1].x, b0.x, b0.y);
-        step(c, x[k].hi[0].y, x[k].hi[1].y, b0.z, b0.w);
-        step(c, x[k].lo[0].x, x[k].lo[1].x, b1.x, b1.y);
-        step(c, x[k].lo[0].y, x[k].lo[1].y, b1.z, b1.w);
+        const uint2 h0 = word2(32 * k), h8 = word2(32 * k + 8 * Sl::PITCH);
+        const uint2 o0 = word2(32 * k + D), o8 = word2(32 * k + D + 8 * Sl::PITCH);
+        const float dk[2] = {__shfl_sync(kFull, d[k], g), __shfl_sync(kFull, d[k], g + 8)};
+        step(c, h0.x, h8.x, b0.x, b0.y);
+        step(c, h0.y, h8.y, b0.z, b0.w);
+        step(c, o0.x, o8.x, b1.x, b1.y);
+        step(c, o0.y, o8.y, b1.z, b1.w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float v = __fmul_rn(__fmul_rn(c[i], x[k].d[i >> 1]), i & 1 ? st.w : st.z);
+          float v = __fmul_rn(__fmul_rn(c[i], dk[i >> 1]), i & 1 ? st.w : st.z);
           if (!(k & 1)) {
             l0[i] = v;
             continue;
@@ -429,21 +457,28 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
         best[i] = fmaxf(best[i], __shfl_xor_sync(kFull, best[i], 1));
         best[i] = fmaxf(best[i], __shfl_xor_sync(kFull, best[i], 2));
       }
-      const int p = p0 + g + 8 * t;
+      const int p = p0 + g + 8 * (t & 1), page = __shfl_sync(kFull, now, g + 8 * (t & 1));
       if (t < 2 && p < c1) {
-        uint32_t key = (t ? there[1] : there[0]) < 0 ? kNoPage : key_of(t ? best[1] : best[0]);
+        uint32_t key = page < 0 ? kNoPage : key_of(t ? best[1] : best[0]);
         if (g0 && key != kNoPage) key = max(key, get(p));
         if (p < a.first || p >= n - a.last) key = kForced;
+        else least = min(least, key), most = max(most, key);
         put(p, key);
       }
-      found = next;
-      if (AHEAD) {
+      __syncwarp();  // (the slot has been read)
+      fetch(slot, next);
+      if constexpr (S == 2) {
 #pragma unroll
-        for (int k = 0; k < NB; ++k) x[k] = y[AHEAD ? k : 0];
-      } else if (p0 + WARPS * 16 < c1) {
-        fetch(found, x);
+        for (int k = 0; k < NB; ++k) d[k] = d2[k];
+        scales(next, d2);
+        now = later, later = next, slot ^= 1;
+      } else {
+        scales(next, d);
+        now = next;
       }
     }
+    copies_wait<0>();
+    if (g0 + kHeads >= a.G) range(__reduce_min_sync(kFull, least), __reduce_max_sync(kFull, most));
   }
 }
 
@@ -456,17 +491,22 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
 constexpr int kBins = 256, kHeld = 8;  // kHeld: keys that a thread holds in registers
 
 struct Bins {
-  uint32_t n[kBins];
+  uint32_t n[2][kBins];      // two, so that one is empty again in time
   uint32_t ends[2][16];      // a word a warp
-  uint32_t bin, above, all;  // where the K-th largest is: keys above the bin, and with those in it
+  uint32_t least, most;      // the range of the keys that are not forced
 };
+// Before the keys' range is gathered and before pick(), with a barrier behind it
+__device__ __forceinline__ void clear_bins(Bins& s) {
+  for (int i = threadIdx.x; i < 2 * kBins; i += blockDim.x) (&s.n[0][0])[i] = 0;
+  if (threadIdx.x == 0) s.least = 0xffffffffu, s.most = 0;
+}
 
 template <int WARPS, bool HELD>
 __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, int32_t* out, int n, Bins& s) {
   static_assert(WARPS * 32 >= kBins && WARPS <= 16, "a thread a bin");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rounds = (n + WARPS * 32 - 1) / (WARPS * 32), base = warp * rounds * 32 + lane;
-  const uint32_t K = (uint32_t)a.K, forced = (uint32_t)(a.first + a.last);
+  const uint32_t K = (uint32_t)a.K;
   uint32_t r[HELD ? kHeld : 1];
   if (HELD) {
 #pragma unroll
@@ -483,50 +523,49 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
       for (int i = 0; i < rounds; ++i) f(base + i * 32 < n ? keys[base + i * 32] : 0u, base + i * 32, base + i * 32 < n);
     }
   };
-  // the range of the scores that are not forced
-  uint32_t least = 0xffffffffu, most = 0;
-  each([&](uint32_t k, int, bool in) {
-    if (in && k != kForced) least = min(least, k), most = max(most, k);
-  });
-  least = __reduce_min_sync(kFull, least), most = __reduce_max_sync(kFull, most);
-  if (lane == 0) s.ends[0][warp] = least, s.ends[1][warp] = most;
-  if (tid < kBins) s.n[tid] = 0;
-  __syncthreads();
-  uint32_t lo = __reduce_min_sync(kFull, s.ends[0][lane & (WARPS - 1)]);
-  uint32_t hi = __reduce_max_sync(kFull, s.ends[1][lane & (WARPS - 1)]);
-  uint32_t T = kForced, above = forced;
+  uint32_t lo = s.least, hi = s.most, T = kForced, above = (uint32_t)(a.first + a.last);
   bool ties = false;  // T is shared by more keys than there is room for
+  int use = 0;        // of the two sets of bins
   while (above < K) {  // `above` keys are above hi, and at least K - above in [lo, hi]
     const int shift = max(0, 24 - __clz(hi - lo | 1));  // (hi - lo) >> shift < 256
+    uint32_t* bins = s.n[use];
     each([&](uint32_t k, int, bool in) {
-      if (in && k >= lo && k <= hi) atomicAdd(&s.n[(k - lo) >> shift], 1u);
+      if (in && k >= lo && k <= hi) atomicAdd(&bins[(k - lo) >> shift], 1u);
     });
     __syncthreads();
-    // keys from a bin's start on: a thread a bin, from the highest down
-    const uint32_t own = tid < kBins ? s.n[kBins - 1 - tid] : 0;
-    uint32_t sum = own;
+    // Every warp for itself: a lane eight bins, the highest ones first; keys above each lane's bins, and then each bin's
+    uint32_t c[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = bins[kBins - 1 - 8 * lane - i], sum += c[i];
+    uint32_t upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += x;
+      const uint32_t x = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += x;
     }
-    if (lane == 31) s.ends[0][warp] = sum;
-    __syncthreads();
-    sum += above;
+    upto += above - sum;
+    uint32_t bin = 0, at = 0, all = 0;  // in the lane that holds the K-th largest: its bin, keys above it and with it
 #pragma unroll
-    for (int w = 0; w < kBins / 32; ++w) sum += w < warp ? s.ends[0][w] : 0;
-    if (tid < kBins && sum - own < K && K <= sum) s.bin = kBins - 1 - tid, s.above = sum - own, s.all = sum;
-    if (tid < kBins) s.n[tid] = 0;
-    __syncthreads();
-    lo += s.bin << shift, above = s.above;
+    for (int i = 0; i < 8; ++i) {
+      if (upto < K && K <= upto + c[i]) bin = kBins - 1 - 8 * lane - i, at = upto, all = upto + c[i];
+      upto += c[i];
+    }
+    const int who = __ffs(__ballot_sync(kFull, all != 0)) - 1;
+    bin = __shfl_sync(kFull, bin, who), above = __shfl_sync(kFull, at, who), all = __shfl_sync(kFull, all, who);
+    lo += bin << shift;
     T = lo;
-    if (s.all == K) break;
+    if (all == K) break;
     if (shift == 0) {
       ties = true;
       break;
     }
     hi = min(hi, lo + (1u << shift) - 1);
-    __syncthreads();  // (the three words have been read)
+    use ^= 1;
+    if (use == 0) {  // a third round (of four at most): the first two's bins have to be empty again
+      __syncthreads();
+      for (int i = tid; i < 2 * kBins; i += WARPS * 32) (&s.n[0][0])[i] = 0;
+      __syncthreads();
+    }
   }
   // who is chosen, in order: those above T (or at it), and the first K - above of those at T
   const uint32_t room = ties ? K - above : 0;
@@ -536,7 +575,6 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
     chosen += __popc(__ballot_sync(kFull, in && k >= T && !same));
     equal += __popc(__ballot_sync(kFull, same));
   });
-  __syncthreads();  // (`ends` has been read)
   if (lane == 0) s.ends[0][warp] = chosen, s.ends[1][warp] = equal;
   __syncthreads();
   uint32_t before = 0, eq_before = 0;
@@ -550,7 +588,8 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
     const uint32_t eq = __ballot_sync(kFull, same);
     const bool take = same ? eq_before + __popc(eq & below) < room : in && k >= T;
     const uint32_t all = __ballot_sync(kFull, take);
-    if (take) out[before + __popc(all & below)] = p;
+    const uint32_t at = before + __popc(all & below);
+    if (take && at < K) out[at] = p;
     before += __popc(all), eq_before += __popc(eq);
   });
 }
@@ -573,10 +612,12 @@ __device__ __forceinline__ uint32_t at_first_cta(const void* p) {
   return r;
 }
 template <int D, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const SelectArgs a) {
-  extern __shared__ __align__(16) uint32_t s_keys[];
+__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) k_page_select(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t s_slots[];  // and the keys behind them
   __shared__ __align__(16) Queries<D> s_q;
   __shared__ Bins s_bins;
+  uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_slots + WARPS * Slots<D>::N * Slots<D>::BYTES);
+  if (cluster_rank() == 0) clear_bins(s_bins);
   cluster_arrive();
   after_last();
   lets_next();
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const Se
     if (rank == 0) pick_all(a, out, n);
     return;
   }
-  const uint32_t keys = at_first_cta(s_keys);
+  const uint32_t keys = at_first_cta(s_keys), bins = at_first_cta(&s_bins.least);
   bool there = false;
   auto ready = [&] {  // the first CTA's memory is there
     if (!there) cluster_wait();
@@ -601,7 +642,13 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const Se
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(k) : "r"(keys + 4 * p) : "memory");
     return k;
   };
-  score_pages<D, WARPS>(a, s_q, b, hk, L, n, (int)((long long)n * rank / C), (int)((long long)n * (rank + 1) / C), ready, put, get);
+  score_pages<D, WARPS>(a, s_q, s_slots, b, hk, L, n, (int)((long long)n * rank / C), (int)((long long)n * (rank + 1) / C), ready, put, get,
+                        [&](uint32_t least, uint32_t most) {
+                          if ((threadIdx.x & 31) == 0) {
+                            asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(bins), "r"(least) : "memory");
+                            asm volatile("red.shared::cluster.max.u32 [%0], %1;" ::"r"(bins + 4), "r"(most) : "memory");
+                          }
+                        });
   cluster_barrier();
   if (rank == 0) pick<WARPS>(a, s_keys, out, n, s_bins);
 }
@@ -609,7 +656,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const Se
 // ---- in two, where the keys of a sequence may not fit there: scores into the workspace, then the choice
 constexpr int kWideWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kWideWarps * 32, 2) k_page_scores(const SelectArgs a) {
+__global__ void __launch_bounds__(kWideWarps * 32, 3) k_page_scores(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t s_slots[];
   __shared__ __align__(16) Queries<D> s_q;
   after_last();
   lets_next();
@@ -620,7 +668,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, 2) k_page_scores(const Select
   uint32_t* keys = a.keys + ((long long)b * a.c.Hkv + hk) * a.c.max_pages;
   auto put = [&](int p, uint32_t k) { keys[p] = k; };
   auto get = [&](int p) { return keys[p]; };
-  score_pages<D, kWideWarps>(a, s_q, b, hk, L, n, c0, min(n, c0 + a.chunk), [] {}, put, get);
+  score_pages<D, kWideWarps>(a, s_q, s_slots, b, hk, L, n, c0, min(n, c0 + a.chunk), [] {}, put, get, [](uint32_t, uint32_t) {});
 }
 __global__ void __launch_bounds__(kWideWarps * 32) k_page_pick(const SelectArgs a) {
   __shared__ Bins s_bins;
@@ -631,7 +679,19 @@ __global__ void __launch_bounds__(kWideWarps * 32) k_page_pick(const SelectArgs 
   const int n = pages_of(a.c, len_of(a.c, a.lens, b));
   int32_t* out = a.pages + (long long)blockIdx.x * a.K;
   if (n <= a.K) pick_all(a, out, n);
-  else pick<kWideWarps>(a, a.keys + (long long)blockIdx.x * a.c.max_pages, out, n, s_bins);
+  if (n <= a.K) return;
+  const uint32_t* keys = a.keys + (long long)blockIdx.x * a.c.max_pages;
+  clear_bins(s_bins);
+  __syncthreads();
+  uint32_t least = 0xffffffffu, most = 0;
+#pragma unroll 4
+  for (int p = threadIdx.x; p < n; p += kWideWarps * 32) {
+    const uint32_t k = keys[p];
+    if (k != kForced) least = min(least, k), most = max(most, k);
+  }
+  atomicMin(&s_bins.least, least), atomicMax(&s_bins.most, most);
+  __syncthreads();
+  pick<kWideWarps>(a, keys, out, n, s_bins);
 }
 
 static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
@@ -639,22 +699,29 @@ static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
   if (c.num_pages > 0 && (!p->codes || !p->scales)) return FA_ERR_NULL;
   return aligned(p->codes, 16) && aligned(p->scales, 16) ? FA_OK : FA_ERR_ALIGN;
 }
-constexpr int kOnePages = 49152;  // keys that fit shared memory beside the rest (192 KB)
+// Bytes of the slots of a CTA, and how many keys fit shared memory beside them
+template <int D, int WARPS>
+constexpr int kSlotBytes = WARPS * Slots<D>::N * Slots<D>::BYTES;
+constexpr int kSmemKeys = 208 * 1024;
+static int one_pages(int D) {
+  return (kSmemKeys - (D == 64 ? kSlotBytes<64, 16> : D == 128 ? kSlotBytes<128, 16> : kSlotBytes<256, 16>)) / 4;
+}
 static size_t key_bytes(const Cache& c) {
-  if (c.max_pages <= kOnePages) return 256;
+  if (c.max_pages <= one_pages(c.D)) return 256;
   return std::max<size_t>(256, ((size_t)c.B * c.Hkv * c.max_pages * sizeof(uint32_t) + 255) / 256 * 256);
 }
 template <int D, int WARPS>
 static cudaError_t run_clusters(const SelectArgs& a, unsigned C, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices that the kernel's shared memory has been allowed on
-  if (!allow_smem(reinterpret_cast<const void*>(k_page_select<D, WARPS>), kOnePages * 4, &ready)) return cudaErrorInvalidValue;
-  return launch_clusters(k_page_select<D, WARPS>, (unsigned)a.c.B * a.c.Hkv * C, C, WARPS * 32, (size_t)a.c.max_pages * 4, s, a);
+  if (!allow_smem(reinterpret_cast<const void*>(k_page_select<D, WARPS>), kSmemKeys, &ready)) return cudaErrorInvalidValue;
+  return launch_clusters(k_page_select<D, WARPS>, (unsigned)a.c.B * a.c.Hkv * C, C, WARPS * 32,
+                         kSlotBytes<D, WARPS> + (size_t)a.c.max_pages * 4, s, a);
 }
 template <int D>
 static cudaError_t run_select(SelectArgs a, int nsm, cudaStream_t s) {
   const long long rows = (long long)a.c.B * a.c.Hkv;
   constexpr int turn = 8 * 16;  // pages that eight warps take at a time
-  if (a.c.max_pages <= kOnePages) {
+  if (a.c.max_pages <= one_pages(D)) {
     // CTAs of a cluster: as many as get a turn each, while all of them run at once, two to an SM; and where even
     // eight leave SMs free and have more than a turn each, CTAs of twice the warps, one to an SM.
     unsigned C = 1;
@@ -666,7 +733,10 @@ static cudaError_t run_select(SelectArgs a, int nsm, cudaStream_t s) {
   a.chunk = (int)((most + want - 1) / want * turn);
   a.chunks = (a.c.max_pages + a.chunk - 1) / a.chunk;
   if (rows * a.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_next(k_page_scores<D>, dim3((unsigned)(rows * a.chunks)), dim3(kWideWarps * 32), 0, s, a);
+  static std::atomic<uint64_t> ready{0};
+  constexpr int bytes = kSlotBytes<D, kWideWarps>;
+  if (!allow_smem(reinterpret_cast<const void*>(k_page_scores<D>), bytes, &ready)) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_next(k_page_scores<D>, dim3((unsigned)(rows * a.chunks)), dim3(kWideWarps * 32), bytes, s, a);
   if (e != cudaSuccess) return e;
   return launch_next(k_page_pick, dim3((unsigned)rows), dim3(kWideWarps * 32), 0, s, a);
 }
