@@ -5,6 +5,10 @@
 // CTAs (a cluster, of one for small calls) take the same sums over 1024 requests at a time, then a share of
 // those requests' tokens and pages each.  What is edited in place is written behind a barrier of the cluster, when
 // everyone has read it; table entries and stack entries that are written are read by nobody else in the call.
+//
+// What is read and written is a few kilobytes (a megabyte for 99068 tokens): the calls are launches and chains of latencies,
+// on a GB300 one new token for each of 64 requests 3.6 us of GPU time, giving them up again 2.5; 99068 tokens of 509
+// requests 8 and 3.
 #include <algorithm>
 
 #include "fa_paged.cuh"
@@ -23,10 +27,17 @@ struct ListArgs {
   const int32_t* arg;  // new_tokens, or keep
   int T;
   int32_t *starts, *first, *seq, *pos, *row;
+  bool slots_apart;  // the tokens' slots are another kernel's
+  bool vec;          // seq, pos and row start on 16 bytes
   int* err;
 
   __device__ __forceinline__ int page_of(int j) const { return (int)((uint64_t)(uint32_t)j * page_mul >> page_shift); }
   __device__ __forceinline__ int pages_of(int len) const { return len > 0 ? page_of(len - 1) + 1 : 0; }
+  __device__ __forceinline__ int row_of(int page, int pos, int p) const {  // of position pos, on the request's page p
+    if (page >= 0 && page < num_pages) return page * page_size + (pos - p * page_size);
+    report_page(err);
+    return -1;
+  }
   __device__ __forceinline__ int on_stack() const { return min(max(num_free[0], 0), num_pages); }
 };
 
@@ -103,19 +114,17 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const ListArgs a) {
     if ((tid & 31) == 0) s_scan[tid >> 5].x = top;
     __syncthreads();
     const uint32_t pages_end = max(__reduce_max_sync(kFull, s_scan[tid & 31].x), taken);
-    // tokens of these requests
-    const uint32_t t1 = min(add_cap(tokens, chunk_tokens), T);
+    // tokens of these requests (of a large call: k_page_slots)
+    const uint32_t t1 = a.slots_apart ? 0 : min(add_cap(tokens, chunk_tokens), T);
     for (uint32_t t = tokens + me; t < t1; t += all) {
       const int i = last_at_most(s_start, t), l = s_len[i];
-      int pos = -1, row = -1, seq = -1;
+      int pos = -1, row = -1;
       if (l >= 0) {
-        seq = c0 + i, pos = l + (int)(t - s_start[i]);
+        pos = l + (int)(t - s_start[i]);
         const int p = a.page_of(pos), had = a.pages_of(l);
-        const int page_no = p < had ? a.table[(long long)seq * a.max_pages + p] : a.free[F - 1 - (s_page[i] + (uint32_t)(p - had))];
-        if (page_no >= 0 && page_no < a.num_pages) row = page_no * a.page_size + (pos - p * a.page_size);
-        else report_page(a.err);
+        row = a.row_of(p < had ? a.table[(long long)(c0 + i) * a.max_pages + p] : a.free[F - 1 - (s_page[i] + (uint32_t)(p - had))], pos, p);
       }
-      a.seq[t] = seq, a.pos[t] = pos, a.row[t] = row;
+      a.seq[t] = l >= 0 ? c0 + i : -1, a.pos[t] = pos, a.row[t] = row;
     }
     // and their pages
     for (uint32_t g = asked + me; g < pages_end; g += all) {
@@ -126,8 +135,58 @@ __global__ void __launch_bounds__(kThreads) k_pages_extend(const ListArgs a) {
     cluster_barrier();  // everyone has read these lengths (and the count), and this CTA's arrays
     if (rank == 0 && got) a.lens[b] = len + add;
   }
-  for (uint32_t t = min(tokens, T) + me; t < T; t += all) a.seq[t] = a.pos[t] = a.row[t] = -1;
+  for (uint32_t t = a.slots_apart ? T : min(tokens, T) + me; t < T; t += all) a.seq[t] = a.pos[t] = a.row[t] = -1;
   if (a.B > 0 && rank == 0 && tid == 0) a.num_free[0] = (int)(F - taken);
+}
+
+// The slots of a large call's tokens, from the starts, lengths and tables that k_pages_extend has written: four neighbours
+// a thread, of one request and on one page as a rule.  (99068 tokens in the cluster's eight SMs: 6 us of the call's 13.)
+constexpr int kSlotThreads = 256, kHeldStarts = 8192;  // requests whose starts lie in shared memory
+__global__ void __launch_bounds__(kSlotThreads) k_page_slots(const ListArgs a) {
+  extern __shared__ int s_starts[];
+  after_last();
+  lets_next();
+  const bool held = a.B <= kHeldStarts;
+  if (held) {
+    for (int i = threadIdx.x; i < a.B; i += kSlotThreads) s_starts[i] = a.starts[i];
+    __syncthreads();
+  }
+  auto start = [&](int i) { return held ? s_starts[i] : a.starts[i]; };
+  const int t0 = 4 * (blockIdx.x * kSlotThreads + threadIdx.x), end = a.starts[a.B];
+  if (t0 >= a.T) return;
+  int i = 0;  // the last request that starts at t0 or before
+  for (int n = a.B; n > 1;) {
+    const int half = n >> 1;
+    if (start(i + half) <= t0) i += half, n -= half;
+    else n = half;
+  }
+  int first = a.first[i], at = start(i), next = i + 1 < a.B ? start(i + 1) : end, known = -1, page = -1, seq[4], pos[4], row[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = t0 + k;
+    seq[k] = pos[k] = row[k] = -1;
+    if (t >= end) continue;
+    if (t >= next) {
+      do {
+        ++i, at = next, next = i + 1 < a.B ? start(i + 1) : end;
+      } while (t >= next);
+      first = a.first[i], known = -1;
+    }
+    if (first < 0) continue;
+    seq[k] = i, pos[k] = first + (t - at);
+    const int p = a.page_of(pos[k]);
+    if (p != known) known = p, page = a.table[(long long)i * a.max_pages + p];
+    row[k] = a.row_of(page, pos[k], p);
+  }
+  if (a.vec && t0 + 4 <= a.T) {
+    *reinterpret_cast<int4*>(a.seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+    *reinterpret_cast<int4*>(a.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    *reinterpret_cast<int4*>(a.row + t0) = make_int4(row[0], row[1], row[2], row[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (t0 + k < a.T) a.seq[t0 + k] = seq[k], a.pos[t0 + k] = pos[k], a.row[t0 + k] = row[k];
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) k_pages_trim(const ListArgs a) {
@@ -200,10 +259,10 @@ static fa_status check_lists(const fa_page_lists* l, const int32_t* arg, ListArg
   return fab_device(&nsm, &a->err);
 }
 
-// One cluster; `work`: tokens or pages that there may be, a few for each thread
+// One cluster; `work`: tokens or pages that there may be, one for each thread while there are CTAs
 static cudaError_t launch_lists(void (*k)(const ListArgs), long long work, const ListArgs& a, cudaStream_t s) {
   int ctas = 1;
-  while (ctas < kMostCtas && work > 4LL * kThreads * ctas) ctas *= 2;
+  while (ctas < kMostCtas && work > (long long)kThreads * ctas) ctas *= 2;
   return launch_clusters(k, (unsigned)ctas, (unsigned)ctas, kThreads, 0, s, a);
 }
 
@@ -221,7 +280,17 @@ extern "C" fa_status fa_pages_extend(const fa_page_lists* lists, const int32_t* 
   if (!starts || (a.B > 0 && !first) || (T > 0 && (!seq || !pos || !row))) return FA_ERR_NULL;
   if (!aligned(starts, 4) || !aligned(first, 4) || !aligned(seq, 4) || !aligned(pos, 4) || !aligned(row, 4)) return FA_ERR_ALIGN;
   a.T = T, a.starts = starts, a.first = first, a.seq = seq, a.pos = pos, a.row = row;
-  return launch_lists(k_pages_extend, T, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  a.vec = aligned(seq, 16) && aligned(pos, 16) && aligned(row, 16);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // A token a thread of the cluster; more of them are shared out over all SMs, by a launch of their own.  B = 0 has no
+  // requests to look for.
+  a.slots_apart = T > kThreads * kMostCtas && a.B > 0;
+  if (launch_lists(k_pages_extend, T, a, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (!a.slots_apart) return FA_OK;
+  const unsigned grid = (unsigned)((T + 4LL * kSlotThreads - 1) / (4 * kSlotThreads));
+  return launch_next(k_page_slots, dim3(grid), dim3(kSlotThreads), (size_t)std::min(a.B, kHeldStarts) * sizeof(int), s, a) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 extern "C" fa_status fa_pages_trim(const fa_page_lists* lists, const int32_t* keep, void* stream) {
@@ -229,6 +298,6 @@ extern "C" fa_status fa_pages_trim(const fa_page_lists* lists, const int32_t* ke
   const fa_status rc = check_lists(lists, keep, &a);
   if (rc != FA_OK) return rc;
   if (a.B == 0) return FA_OK;
-  const long long work = std::min<long long>(a.num_pages, (long long)a.B * a.max_pages);
+  const long long work = std::min<long long>(a.num_pages, (long long)a.B * a.max_pages) / 8;  // (few of them come back at a time)
   return launch_lists(k_pages_trim, work, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

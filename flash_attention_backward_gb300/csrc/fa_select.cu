@@ -34,17 +34,7 @@ __device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 
 // bounds: a lane holds eight components, D / 8 lanes a row.  A warp takes a page of its own, or where there are not as
 // many pages the CTA's warps share one.
 
-#ifndef S128
-#define S128 2
-#endif
-#ifndef KW
-#define KW 4
-#define KU 8
-#define KM 1
-#define KZ 8
-#define KA 1
-#endif
-constexpr int kBoundWarps = KW;
+constexpr int kBoundWarps = 4, kBoundCtas = 8;  // CTAs an SM
 
 __device__ __forceinline__ uint32_t load_u32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 // of three; a NaN gives way
@@ -126,7 +116,7 @@ struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
 // Largest and smallest values of rows r0, r0 + step, ... of a page's `rows` (at least one), the lane's components
 template <int TYPE>
 __device__ __forceinline__ void row_range(const uint8_t* page, unsigned cell, int e0, int r0, int step, int rows, float (&hi)[8], float (&lo)[8]) {
-  constexpr int U = TYPE == FA_F32 ? 4 : KU;
+  constexpr int U = 4;  // rows under way at a time
 #pragma unroll
   for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
 #pragma unroll 1
@@ -171,7 +161,7 @@ __device__ __forceinline__ void put_bounds(const BoundArgs& a, long long rec, in
 }
 
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kBoundWarps * 32, KM) k_page_bounds(const BoundArgs a) {
+__global__ void __launch_bounds__(kBoundWarps * 32, kBoundCtas) k_page_bounds(const BoundArgs a) {
   constexpr int LG = D / 8, GW = 32 / LG;  // lanes of a row, rows side by side in a warp
   constexpr int RB = TYPE == FA_F32 ? 4 * D : TYPE == FA_F16 ? 2 * D : TYPE == FA_Q8_0 ? D / 32 * 34 : D / 32 * 18;
   __shared__ float4 s_part[kBoundWarps - 1][4][32];
@@ -182,7 +172,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32, KM) k_page_bounds(const Boun
   const int b = rest / a.Z, L = len_of(a.c, a.lens, b), f = a.first ? a.first[b] : 0;
   if (f < 0 || f >= L) return;
   const int n = pages_of(a.c, L), p0 = page_of(a.c, f);
-  const bool apart = KA * (n - p0) > a.Z;  // a warp a page
+  const bool apart = n - p0 > a.Z;  // a warp a page
   const unsigned cell = (unsigned)a.c.Hkv * RB;
   const int all = apart ? a.Z * kBoundWarps : a.Z;
   for (int p = p0 + (int)(apart ? z * kBoundWarps + warp : z); p < n; p += all) {
@@ -337,7 +327,7 @@ struct HeadPart {
 // fragment load lie in different banks.
 template <int D>
 struct Slots {
-  static constexpr int PITCH = 2 * D + 32, BYTES = 16 * PITCH, N = D == 256 ? 1 : D == 128 ? S128 : 2;
+  static constexpr int PITCH = 2 * D + 32, BYTES = 16 * PITCH, N = D == 256 ? 1 : 2;
 };
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -612,7 +602,7 @@ __device__ __forceinline__ uint32_t at_first_cta(const void* p) {
   return r;
 }
 template <int D, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) k_page_select(const SelectArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t s_slots[];  // and the keys behind them
   __shared__ __align__(16) Queries<D> s_q;
   __shared__ Bins s_bins;
@@ -656,7 +646,7 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) k_page_select(const Se
 // ---- in two, where the keys of a sequence may not fit there: scores into the workspace, then the choice
 constexpr int kWideWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kWideWarps * 32, 3) k_page_scores(const SelectArgs a) {
+__global__ void __launch_bounds__(kWideWarps * 32, 2) k_page_scores(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t s_slots[];
   __shared__ __align__(16) Queries<D> s_q;
   after_last();
@@ -761,7 +751,7 @@ extern "C" fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_b
   if (a.c.B == 0 || a.c.max_pages == 0) return FA_OK;
   a.codes = bounds->codes, a.scales = bounds->scales, a.first = first, a.lens = seq_lens;
   const long long rows = (long long)a.c.B * a.c.Hkv;
-  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, (long long)KZ * nsm / rows));
+  a.Z = (int)std::max(1LL, std::min<long long>(a.c.max_pages, (long long)kBoundCtas * nsm / rows));
   if (rows * a.Z > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const BoundKernel k = a.c.D == 64 ? pick_bounds<64>(a.c.k_type) : a.c.D == 128 ? pick_bounds<128>(a.c.k_type) : pick_bounds<256>(a.c.k_type);
   return launch_next(k, dim3((unsigned)(rows * a.Z)), dim3(kBoundWarps * 32), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess
