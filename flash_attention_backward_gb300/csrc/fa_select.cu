@@ -268,7 +268,7 @@ struct Queries {
 template <int D, int WARPS>
 struct HeadPart {
   static_assert(WARPS * 32 >= D, "a part a thread");
-  float x[8];
+  uint4 raw[2];  // as they lie in memory, not looked at before they are there
   // (D / 32 blocks of 8 heads by 4: whole warps take part or none of their lanes)
   static __device__ __forceinline__ bool mine() { return threadIdx.x < D; }
   static __device__ __forceinline__ int block() { return threadIdx.x >> 5; }
@@ -277,18 +277,22 @@ struct HeadPart {
   __device__ __forceinline__ void ask(const SelectArgs& a, int b, int h0, int ng) {
     if (!mine()) return;
     const long long at = b * a.q_row + (h0 + min(head(), ng - 1)) * a.q_head + block() * 32 + 8 * (threadIdx.x & 3);
-    auto load = [&](auto* q) {  // (the type is told apart outside, so that the loads are under way together)
+    auto load = [&](auto* q) {
       Oct<std::remove_const_t<std::remove_pointer_t<decltype(q)>>> o;
       load8_raw(q + at, a.vec, o);
-      unpack8(o, x);
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(o) / 16; ++i) raw[i] = reinterpret_cast<const uint4*>(&o)[i];
     };
     if (a.act == FA_ACT_F32) load(static_cast<const float*>(a.q));
-    else if (a.act == FA_ACT_F16) load(static_cast<const __half*>(a.q));
-    else load(static_cast<const __nv_bfloat16*>(a.q));
+    else load(static_cast<const __half*>(a.q));  // (two bytes of either kind)
   }
-  __device__ __forceinline__ void put(Queries<D>& s, int ng) {
+  __device__ __forceinline__ void put(const SelectArgs& a, Queries<D>& s, int ng) {
     if (!mine()) return;
     const int k = block(), g = head(), lane = threadIdx.x & 31;
+    float x[8];
+    if (a.act == FA_ACT_F32) unpack8(*reinterpret_cast<const Oct<float>*>(raw), x);
+    else if (a.act == FA_ACT_F16) unpack8(*reinterpret_cast<const Oct<__half>*>(raw), x);
+    else unpack8(*reinterpret_cast<const Oct<__nv_bfloat16>*>(raw), x);
     uint32_t top = 0;  // largest magnitude, as bits (a NaN is above infinity)
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(fabsf(x[j])));
@@ -351,10 +355,13 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint8_t* mine = slots + warp * S * Sl::BYTES;
   const uint32_t ring = fab::smem_u32(mine);
-  auto look_up = [&](int p0) {  // page number of page p0 + (lane & 15)
+  // Page number of page p0 + (lane & 15), not looked at before it is used (that would wait for it); and then: -1 for none.
+  auto look_up = [&](int p0) {
     const int p = p0 + (lane & 15);
-    if (p >= c1) return -1;
-    const int page = a.c.table[(long long)b * a.c.max_pages + p];
+    return p < c1 ? a.c.table[(long long)b * a.c.max_pages + p] : 0;
+  };
+  auto checked = [&](int page, int p0) {
+    if (p0 + (lane & 15) >= c1) return -1;
     if (page >= 0 && page < a.c.num_pages) return page;
     report_page(a.c.err);
     return -1;
@@ -383,16 +390,17 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
     if constexpr (S == 2) later = look_up(p0 + TURN);
     HeadPart<D, WARPS> q;
     q.ask(a, b, h0, ng);
+    now = checked(now, p0);
     fetch(0, now), scales(now, d);
-    if constexpr (S == 2) fetch(1, later), scales(later, d2);
+    if constexpr (S == 2) later = checked(later, p0 + TURN), fetch(1, later), scales(later, d2);
     if (g0) __syncthreads();
-    q.put(s, ng);
+    q.put(a, s, ng);
     __syncthreads();
     ready();
     uint32_t least = 0xffffffffu, most = 0;
     const float slope[2] = {a.alibi && 2 * t < ng ? a.alibi[h0 + 2 * t] : 0.f, a.alibi && 2 * t + 1 < ng ? a.alibi[h0 + 2 * t + 1] : 0.f};
     for (; p0 < c1; p0 += TURN) {
-      const int next = look_up(p0 + S * TURN);
+      int next = look_up(p0 + S * TURN);
       copies_wait<S - 1>();
       __syncwarp();
       const uint8_t* at = mine + slot * Sl::BYTES + g * Sl::PITCH + 8 * t;
@@ -456,6 +464,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
         put(p, key);
       }
       __syncwarp();  // (the slot has been read)
+      next = checked(next, p0 + S * TURN);
       fetch(slot, next);
       if constexpr (S == 2) {
 #pragma unroll
