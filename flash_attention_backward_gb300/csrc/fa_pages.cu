@@ -255,8 +255,7 @@ static fa_status check_lists(const fa_page_lists* l, const int32_t* arg, ListArg
   a->table = l->page_table, a->lens = l->seq_lens, a->free = l->free_pages, a->num_free = l->num_free;
   a->num_pages = l->num_pages, a->page_size = l->page_size, a->B = l->B, a->max_pages = l->max_pages, a->arg = arg;
   page_divisor(l->page_size, &a->page_mul, &a->page_shift);
-  int nsm = 0;
-  return fab_device(&nsm, &a->err);
+  return FA_OK;
 }
 
 // One cluster; `work`: tokens or pages that there may be, one for each thread while there are CTAs
@@ -273,12 +272,14 @@ using namespace fap;
 extern "C" fa_status fa_pages_extend(const fa_page_lists* lists, const int32_t* new_tokens, int T, int32_t* starts,
                                      int32_t* first, int32_t* seq, int32_t* pos, int32_t* row, void* stream) {
   ListArgs a;
-  const fa_status rc = check_lists(lists, new_tokens, &a);
+  fa_status rc = check_lists(lists, new_tokens, &a);
   if (rc != FA_OK) return rc;
   if (T < 0) return FA_ERR_SHAPE;
   if (T > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (!starts || (a.B > 0 && !first) || (T > 0 && (!seq || !pos || !row))) return FA_ERR_NULL;
   if (!aligned(starts, 4) || !aligned(first, 4) || !aligned(seq, 4) || !aligned(pos, 4) || !aligned(row, 4)) return FA_ERR_ALIGN;
+  int nsm = 0;
+  if ((rc = fab_device(&nsm, &a.err)) != FA_OK) return rc;
   a.T = T, a.starts = starts, a.first = first, a.seq = seq, a.pos = pos, a.row = row;
   a.vec = aligned(seq, 16) && aligned(pos, 16) && aligned(row, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -295,8 +296,10 @@ extern "C" fa_status fa_pages_extend(const fa_page_lists* lists, const int32_t* 
 
 extern "C" fa_status fa_pages_trim(const fa_page_lists* lists, const int32_t* keep, void* stream) {
   ListArgs a;
-  const fa_status rc = check_lists(lists, keep, &a);
+  fa_status rc = check_lists(lists, keep, &a);
   if (rc != FA_OK) return rc;
+  int nsm = 0;
+  if ((rc = fab_device(&nsm, &a.err)) != FA_OK) return rc;
   if (a.B == 0) return FA_OK;
   const long long work = std::min<long long>(a.num_pages, (long long)a.B * a.max_pages) / 8;  // (few of them come back at a time)
   return launch_lists(k_pages_trim, work, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
