@@ -525,7 +525,8 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
   uint32_t lo = s.least, hi = s.most, T = kForced, above = (uint32_t)(a.first + a.last);
   bool ties = false;  // T is shared by more keys than there is room for
   int use = 0;        // of the two sets of bins
-  while (above < K) {  // `above` keys are above hi, and at least K - above in [lo, hi]
+  // `above` keys are above hi, and at least K - above in [lo, hi], which a round makes 256 times smaller: four at most
+  for (int round = 0; round < 4 && above < K; ++round) {
     const int shift = max(0, 24 - __clz(hi - lo | 1));  // (hi - lo) >> shift < 256
     uint32_t* bins = s.n[use];
     each([&](uint32_t k, int, bool in) {
@@ -550,6 +551,7 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
       upto += c[i];
     }
     const int who = __ffs(__ballot_sync(kFull, all != 0)) - 1;
+    if (who < 0) break;  // (keys that change meanwhile: a workspace that another call uses)
     bin = __shfl_sync(kFull, bin, who), above = __shfl_sync(kFull, at, who), all = __shfl_sync(kFull, all, who);
     lo += bin << shift;
     T = lo;
@@ -558,7 +560,7 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
       ties = true;
       break;
     }
-    hi = min(hi, lo + (1u << shift) - 1);
+    hi = lo + min(hi - lo, (1u << shift) - 1);
     use ^= 1;
     if (use == 0) {  // a third round (of four at most): the first two's bins have to be empty again
       __syncthreads();

@@ -288,6 +288,31 @@ def test_pages_extend_and_trim(fb, B, width, page, tokens, num_pages):
     assert fb.fa_back_get_error() == 0
 
 
+def test_page_lists_without_requests_or_pages(fb):
+    none = fb.PageLists.empty(0, 3, 5, 16)
+    got = fb.pages_extend(none, torch.empty(0, dtype=torch.int32, device="cuda"), 7)
+    assert got["starts"].tolist() == [0] and got["seq"].tolist() == [-1] * 7 and got["first"].numel() == 0
+    fb.pages_trim(none, torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert none.num_free.tolist() == [5]
+    for lists in (fb.PageLists.empty(2, 0, 5, 16), fb.PageLists.empty(2, 3, 0, 16)):
+        lists.seq_lens.zero_()
+        got = fb.pages_extend(lists, torch.full((2,), 9, dtype=torch.int32, device="cuda"), 10000)
+        assert got["starts"].tolist() == [0, 9, 18] and got["first"].tolist() == [-1, -1] and got["row"].tolist() == [-1] * 10000
+        assert lists.seq_lens.tolist() == [0, 0]
+    assert fb.fa_back_get_error() == 0
+
+
+def test_sums_of_tokens_beyond_32_bits(fb):
+    """Requests for more tokens than an int holds: refused, and those before and behind them that fit T are not disturbed."""
+    lists = fb.PageLists.empty(5, 4, 20, 16)
+    lists.seq_lens.copy_(torch.tensor([0, 0, 0, 5, 0]))
+    lists.page_table[3, 0] = 19
+    news = torch.tensor([20, 0, 2 ** 31 - 1, 2 ** 31 - 1, 2], dtype=torch.int32, device="cuda")
+    got = fb.pages_extend(lists, news, 30)
+    assert got["starts"].tolist() == [0, 20, 20, 30, 30, 30] and got["first"].tolist() == [0, -1, -1, -1, -1]
+    assert got["seq"].tolist() == [0] * 20 + [-1] * 10 and lists.seq_lens.tolist() == [20, 0, 0, 5, 0] and lists.num_free.tolist() == [18]
+
+
 def test_trim_undoes_extend_and_requests_come_and_go(fb):
     lists = fb.PageLists.empty(4, 8, 20, 16)
     assert lists.free[:3].tolist() == [19, 18, 17] and lists.num_free.tolist() == [20]
@@ -453,6 +478,73 @@ def test_page_select_of_many_pages(fb, n, K, first, last):
     assert got[0, 0].tolist() == E.select(qa[0], codes[table[0], 0], scales[table[0], 0], n, n, 1, 3, K, 1.0, first, last)
 
 
+@pytest.mark.parametrize("n, D, Hkv, G", [(1500, 128, 1, 8), (1500, 256, 2, 9), (40000, 64, 1, 20), (60000, 128, 2, 3), (60000, 256, 1, 17), (300, 256, 30, 2)])
+def test_page_select_by_clusters_of_all_sizes_and_without(fb, n, D, Hkv, G):
+    """Few sequences of many pages: clusters of eight CTAs, of twice the warps where SMs are free, and two launches where a
+    sequence's keys do not fit shared memory; more than eight query heads add to what the first ones found."""
+    rng = np.random.default_rng(n + D)
+    cache, bounds, codes, scales, table = bounded_cache(fb, rng, n, D, Hkv, 1)
+    q, qa = act_array(rng, (1, Hkv * G, D), "f16")
+    got = fb.page_select(q, cache, bounds, cuda(np.array([n], np.int32)), 77, scale=0.1, first=2, last=3)
+    for h in range(Hkv):
+        assert got[0, h].tolist() == E.select(qa[0, h * G:(h + 1) * G], codes[table[0], h], scales[table[0], h], n, n, 1, G, 77, 0.1, 2, 3), h
+
+
+def test_page_select_of_queries_that_are_not_finite(fb):
+    """Whatever is chosen is K different pages of the sequence."""
+    rng = np.random.default_rng(9)
+    cache, bounds, *_ = bounded_cache(fb, rng, 600)
+    q, _ = act_array(rng, (1, 4, 64), "f32")
+    for bad in (float("nan"), float("inf"), -3e38):
+        for at in ((0, 0, 5), (0, slice(None), slice(None))):
+            x = q.clone()
+            x[at] = bad
+            got = fb.page_select(x, cache, bounds, cuda(np.array([600], np.int32)), 50, scale=1.0)[0, 0].tolist()
+            assert got == sorted(set(got)) and len(got) == 50 and got[0] == 0 and got[-1] == 599
+
+
+def test_more_pages_asked_for_than_there_are(fb):
+    p = R.Paged(12, (70, 3, 0), 2, 64, 64, 1, 1, 16)
+    cache, n = p.on_gpu(fb, torch), cuda(np.array([70, 3, 0], np.int32))
+    bounds = fb.PageBounds.of(cache)
+    fb.page_bounds(cache, bounds, n)
+    q, qa = act_array(np.random.default_rng(1), (3, 4, 64), "f32")
+    pages = fb.page_select(q, cache, bounds, n, 1000, scale=1.0, first=500, last=500)
+    assert all(pages[b, h].tolist() == list(range(m)) + [-1] * (1000 - m) for b, m in ((0, 5), (1, 1), (2, 0)) for h in range(2))
+    got, want = fb.paged_decode(q, cache, n, scale=1.0, pages=pages), R.decode(p, qa, 1.0)
+    tol_O, tol_lse = R.decode_tolerance(p, want[2], want[3], "f32")
+    within(got["O"].cpu().numpy(), want[0], tol_O), within(got["lse"].cpu().numpy(), want[1], tol_lse)
+
+
+def test_pools_beyond_32_bits(fb):
+    """Page numbers whose rows and whose bounds lie more than 4 GB behind the pools' starts."""
+    n, Hkv, D = (1 << 20) + 40, 8, 256
+    k = torch.zeros(n, 1, Hkv, 2 * D, dtype=torch.uint8, device="cuda")
+    table = torch.arange(n - 30, n, dtype=torch.int32, device="cuda")[None]
+    rows = torch.randn(30, 1, Hkv, D, device="cuda").half()
+    k[n - 30:] = rows.view(torch.uint8).view(30, 1, Hkv, 2 * D)
+    cache = fb.PagedCache(k, fb.FA_F16, k, fb.FA_F16, table, D=D, Dv=D)
+    bounds, L = fb.PageBounds.of(cache), cuda(np.array([30], np.int32))
+    fb.page_bounds(cache, bounds, L)
+    v = rows[:, 0].double().cpu().numpy()
+    for i in (0, 29):
+        for h in range(Hkv):
+            c, s = E.bounds(v[i:i + 1, h])
+            assert np.array_equal(bounds.codes[n - 30 + i, h].cpu().numpy(), c) and np.array_equal(bounds.scales[n - 30 + i, h].cpu().numpy(), s)
+    assert not bounds.codes[:n - 30].any()
+    q, qa = act_array(np.random.default_rng(2), (1, Hkv, D), "f32")
+    pages = fb.page_select(q, cache, bounds, L, 7, scale=0.06)
+    codes, scales = bounds.codes[n - 30:].cpu().numpy(), bounds.scales[n - 30:].cpu().numpy()
+    for h in range(Hkv):
+        assert pages[0, h].tolist() == E.select(qa[0, h:h + 1], codes[:, h], scales[:, h], 30, 30, 1, 1, 7, 0.06, 1, 1)
+    got = fb.paged_decode(q, cache, L, scale=0.06, pages=pages)["O"][0].double().cpu().numpy()
+    for h in range(Hkv):
+        r = v[pages[0, h].cpu().numpy(), h]
+        w = np.exp(0.06 * (r @ qa[0, h].astype(np.float64)))
+        assert np.abs(got[h] - w @ r / w.sum()).max() < 1e-4
+    assert fb.fa_back_get_error() == 0
+
+
 @pytest.mark.parametrize("n, K", [(700, 50), (9000, 300)])
 def test_page_select_takes_the_lowest_of_equal_pages(fb, n, K):
     """Scores of few different values, of one, and of none (a query of zeros: all scores are 0, of either sign)."""
@@ -589,6 +681,37 @@ def test_all_pages_is_the_plain_attention(fb, name):
     for g in (one, two):
         within(g["O"].float().cpu().numpy(), O, tol_O + half_step(act, O), "O")
         within(g["lse"].cpu().numpy(), lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("page", [16, 8, 5])
+def test_selected_pages_on_invalid_page_numbers_are_masked(fb, page):
+    p = R.Paged(page, (200, 33), 2, 64, 64, 1, 0, page)
+    cache, n = p.on_gpu(fb, torch), cuda(np.array([200, 33], np.int32))
+    cache.page_table[0, 3], cache.page_table[1, 0] = -1, 10 ** 9
+    pages = torch.tensor([[[0, 3, 4, 9, 12], [3, -1, -1, -1, -1]], [[0, 1, -1, -1, -1], [1, 0, -1, -1, -1]]], dtype=torch.int32, device="cuda")
+    q, qa = act_array(np.random.default_rng(1), (2, 4, 64), "f32")
+    got = fb.paged_decode(q, cache, n, scale=0.2, pages=pages)
+    assert fb.STATUS[fb.fa_back_get_error()] == "FA_ERR_PAGE"
+    left = {(0, 0): [0, 4, 9, 12], (0, 1): [], (1, 0): [1], (1, 1): [1]}
+    O, lse, mag, smag = over_pages(p, left, qa, 0.2, 0.0, None, None)
+    tol_O, tol_lse = R.decode_tolerance(p, mag, smag, "f32")
+    within(got["O"].cpu().numpy(), O, tol_O), within(got["lse"].cpu().numpy(), lse, tol_lse)
+
+
+def test_a_wait_that_runs_out_over_selected_pages(fb):
+    """The limit that every wait counts as over: the error word says so, and the next call is right."""
+    p = R.Paged(2, (300,), 2, 64, 64, 2, 2, 16)
+    cache, n = p.on_gpu(fb, torch), cuda(np.array([300], np.int32))
+    q, qa = act_array(np.random.default_rng(1), (1, 4, 64), "f32")
+    pages = torch.arange(19, dtype=torch.int32, device="cuda").expand(1, 2, 19).contiguous()
+    assert fb.fa_back_test_wait_limit(0) == 0
+    fb.paged_decode(q, cache, n, scale=0.2, pages=pages)
+    torch.cuda.synchronize()
+    assert fb.STATUS[fb.fa_back_get_error()] == "FA_ERR_TIMEOUT"
+    got, want = fb.paged_decode(q, cache, n, scale=0.2, pages=pages), R.decode(p, qa, 0.2)
+    tol_O, _ = R.decode_tolerance(p, want[2], want[3], "f32")
+    within(got["O"].cpu().numpy(), want[0], tol_O)
+    assert fb.fa_back_get_error() == 0
 
 
 def test_padding_slots_keep_their_rows(fb):
