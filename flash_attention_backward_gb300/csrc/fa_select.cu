@@ -85,7 +85,8 @@ struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
       w[2] = *reinterpret_cast<const uint16_t*>(p - 2 - 8 * (j & 1));
     }
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
+  // top: the largest magnitude of the quantised types' scales so far
+  __device__ __forceinline__ void values(float (&x)[8], float& top) const {
     if (TYPE == FA_F32) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i % (sizeof(w) / 4)]);
@@ -97,9 +98,8 @@ struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
       }
     } else {  // (32768 + code + bias) d - (32768 + bias) d: the second product is exact, and so is the sum
       constexpr uint32_t kMask = TYPE == FA_Q8_0 ? 0xffffffffu : 0x0f0f0f0fu, kFlip = TYPE == FA_Q8_0 ? 0x80808080u : 0;
-      const float d = __half2float(__ushort_as_half((unsigned short)w[2]));
-      // (an infinite scale makes infinities of its block, whose bounds are infinite then)
-      const float off = fabsf(d) < INFINITY ? -(32768.f + (TYPE == FA_Q8_0 ? 128.f : 8.f)) * d : 0.f;
+      const float d = __half2float(__ushort_as_half((unsigned short)w[2])), off = -(32768.f + (TYPE == FA_Q8_0 ? 128.f : 8.f)) * d;
+      top = fmaxf(top, fabsf(d));  // (an infinite one makes NaN here, which gives way, and of its block infinities: row_range)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t u = (w[k] & kMask) ^ kFlip;
@@ -117,20 +117,37 @@ struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
 template <int TYPE>
 __device__ __forceinline__ void row_range(const uint8_t* page, unsigned cell, int e0, int r0, int step, int rows, float (&hi)[8], float (&lo)[8]) {
   constexpr int U = 4;  // rows under way at a time
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
-#pragma unroll 1
-  for (int r = r0; r < rows; r += U * step) {
-    Raw8<TYPE> raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u].load(page + (uint64_t)(unsigned)min(r + u * step, rows - 1) * cell, e0);  // (the last row again does nothing)
+  auto take = [&](const Raw8<TYPE> (&raw)[U]) {
 #pragma unroll
     for (int u = 0; u < U; u += 2) {
       float x[8], y[8];
-      raw[u].values(x), raw[u + 1].values(y);
+      raw[u].values(x, top), raw[u + 1].values(y, top);
 #pragma unroll
       for (int i = 0; i < 8; ++i) hi[i] = most3(hi[i], x[i], y[i]), lo[i] = least3(lo[i], x[i], y[i]);
     }
+  };
+  const uint64_t stride = (uint64_t)(unsigned)step * cell;
+  const uint8_t* at = page + (uint64_t)(unsigned)min(r0, rows - 1) * cell;
+  int r = r0;
+#pragma unroll 1
+  for (; r + (U - 1) * step < rows; r += U * step, at += U * stride) {
+    Raw8<TYPE> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].load(at + u * stride, e0);
+    take(raw);
+  }
+  if (r < rows) {
+    Raw8<TYPE> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].load(page + (uint64_t)(unsigned)min(r + u * step, rows - 1) * cell, e0);  // (the last row again does nothing)
+    take(raw);
+  }
+  if (top == INFINITY) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = INFINITY;
   }
 }
 

@@ -108,6 +108,14 @@ struct Args {
 at::Tensor make(at::IntArrayRef shape, at::ScalarType t, int device) {
   return at::Tensor(at::detail::empty_cuda(shape, t, at::Device(at::kCUDA, device), std::nullopt));
 }
+// n elements of a one-dimensional tensor from `at` on, as a tensor of the same storage (a view's dispatch costs more than
+// an allocation)
+at::Tensor part(const at::Tensor& whole, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  return t;
+}
 void put(PyObject* d, PyObject* key, const at::Tensor& t) {
   PyObject* o = THPVariable_Wrap(t);
   PyDict_SetItem(d, key, o);
@@ -327,8 +335,11 @@ PyObject* extend(PyObject*, PyObject* const* argv, Py_ssize_t) {
     const int32_t* news = a.flat<int32_t>(2, at::kInt, l->B, false);
     const long long T = a.integer(3);
     if (!a.here() || T < 0 || T > INT32_MAX) return nullptr;
-    const at::Tensor seq = make({T}, at::kInt, a.device), pos = make({T}, at::kInt, a.device), row = make({T}, at::kInt, a.device);
-    const at::Tensor starts = make({(int64_t)l->B + 1}, at::kInt, a.device), first = make({l->B}, at::kInt, a.device);
+    // one allocation: each part on 16 bytes
+    const int64_t B = l->B, t4 = (T + 3) / 4 * 4, b4 = (B + 4) / 4 * 4;
+    const at::Tensor whole = make({3 * t4 + 2 * b4}, at::kInt, a.device);
+    const at::Tensor seq = part(whole, 0, T), pos = part(whole, t4, T), row = part(whole, 2 * t4, T);
+    const at::Tensor starts = part(whole, 3 * t4, B + 1), first = part(whole, 3 * t4 + b4, B);
     auto p = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
     if (fn.extend(l, news, (int)T, p(starts), p(first), p(seq), p(pos), p(row), c10::cuda::getCurrentCUDAStream(a.device).stream()) != FA_OK)
       return nullptr;
