@@ -4,6 +4,14 @@
 // max over a page's keys of q . k is at most sum max(q_i hi_i, q_i lo_i).  In 8 bits that sum is whole
 // numbers, exact in any order, and each block of 32 adds two f32 products and one sum in a fixed tree: the score is
 // the same bits wherever and however it is computed, and so are the pages chosen by it.
+//
+// On a GB300 (6754 GB/s measured copy rate), of GPU time.  Bounds of 75520 q8_0 keys of 4 KV heads of 256 in pages of 64 (85 MB)
+// 26 us, 48 % of that rate: some 45 instructions a row and warp, and loads of a row's 272 bytes in words, each touching
+// two or three lines.  Of the last pages of 64 sequences 4.9 us: launch, lengths, page number, rows, one after another.
+// Selection among 1180 pages for 4 KV heads of 256 (6 query heads each, 64 chosen) 8.5 us, for 48 ragged sequences of up to
+// 512 pages and 8 KV heads of 128 (4 query heads each) 14.7 us, where their bytes would take 0.4 and 3.9: a chain of latencies
+// too (lengths, page numbers and queries, bounds, 16 pages a warp at a time, histograms), which the larger batch
+// goes through one and a half times, two CTAs an SM.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -34,7 +42,9 @@ __device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 
 // bounds: a lane holds eight components, D / 8 lanes a row.  A warp takes a page of its own, or where there are not as
 // many pages the CTA's warps share one.
 
-constexpr int kBoundWarps = 4, kBoundCtas = 8;  // CTAs an SM
+// CTAs of four warps, eight an SM, four rows a warp under way: 26.3 us for the 75520 keys above; with eight rows and five
+// CTAs 26.8, with sixteen rows and four CTAs 26.6, a page always shared by the CTA 29.8 and more.
+constexpr int kBoundWarps = 4, kBoundCtas = 8;
 
 __device__ __forceinline__ uint32_t load_u32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 // of three; a NaN gives way
@@ -269,8 +279,8 @@ __device__ __forceinline__ uint32_t key_of(float s) {
 // The whole numbers come from the tensor core: 16 pages by 8 query heads a product, the page's codes (largest ones,
 // then smallest) against q's positive and negative codes.  A code enters as the binary16 number 1152 + code, which is an
 // "and" and an "exclusive or" away from its byte, and 1152 times the sum of q's codes is taken off beforehand: all
-// sums stay whole numbers below 2^24, exact in f32.  (Products of four bytes on the plain units: 12.7 us for 1180 pages of
-// 4 KV heads of 256 with 6 query heads each, and 17.1 for 48 ragged sequences of up to 512 pages of 8 KV heads of 128.)
+// sums stay whole numbers below 2^24, exact in f32.  (With products of four bytes on the plain units instead: 12.8 us for
+// 11.9 with the long sequence above, 17.1 for 16.5 with the ragged ones.)
 //
 // Of a block of 32 components, lane t = lane & 3 holds components 8 t .. 8 t + 7 of pages g and g + 8, g = lane >> 2: a word
 // a k16 step, its bytes 0 and 2 the first pair of the operand, 1 and 3 the second.
@@ -343,9 +353,9 @@ struct HeadPart {
 };
 
 // A warp's slots in shared memory: the codes of 16 pages each, brought by asynchronous copies of 16 bytes a lane.
-// (Loaded into registers as the products take them, eight bytes of eight pages at a time, the lookups of their lines bound
-// the kernel: 15.4 us for 48 ragged sequences.)  Rows start 32 bytes, modulo 128, after one another: the words of a
-// fragment load lie in different banks.
+// (Loaded into registers as the products take them, eight bytes of eight pages at a time: the same times, but a hundred
+// registers more and spills.)  Rows start 32 bytes, modulo 128, after one another: the words of a fragment load lie in
+// different banks.
 template <int D>
 struct Slots {
   static constexpr int PITCH = 2 * D + 32, BYTES = 16 * PITCH, N = D == 256 ? 1 : 2;
@@ -428,13 +438,13 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
         const float4 st = s.start[k][t];
         const uint4 b0 = s.b[k][0][lane], b1 = s.b[k][1][lane];
         float c[4] = {st.x, st.y, st.x, st.y};
-        const uint2 h0 = word2(32 * k), h8 = word2(32 * k + 8 * Sl::PITCH);
-        const uint2 o0 = word2(32 * k + D), o8 = word2(32 * k + D + 8 * Sl::PITCH);
+        const uint2 up0 = word2(32 * k), up8 = word2(32 * k + 8 * Sl::PITCH);
+        const uint2 low0 = word2(32 * k + D), low8 = word2(32 * k + D + 8 * Sl::PITCH);
         const float dk[2] = {__shfl_sync(kFull, d[k], g), __shfl_sync(kFull, d[k], g + 8)};
-        step(c, h0.x, h8.x, b0.x, b0.y);
-        step(c, h0.y, h8.y, b0.z, b0.w);
-        step(c, o0.x, o8.x, b1.x, b1.y);
-        step(c, o0.y, o8.y, b1.z, b1.w);
+        step(c, up0.x, up8.x, b0.x, b0.y);
+        step(c, up0.y, up8.y, b0.z, b0.w);
+        step(c, low0.x, low8.x, b1.x, b1.y);
+        step(c, low0.y, low8.y, b1.z, b1.w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float v = __fmul_rn(__fmul_rn(c[i], dk[i >> 1]), i & 1 ? st.w : st.z);
@@ -502,7 +512,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
 // the K largest of n keys, by a CTA.  Its warps own neighbouring stretches of the pages, so that what they choose is in
 // ascending order.  The K-th largest is found by counting keys in 256 equal bins between the smallest and the largest,
 // then in 256 of the bin that it lies in, and so on: it ends when exactly K are above a bin's start, after two rounds
-// as a rule.  (Bisection, a count a step: 12 steps and 1.5 us more for 1180 pages.)
+// as a rule.  (Bisection, a count a step, took 12 steps for 1180 pages: 3 us.)
 
 constexpr int kBins = 256, kHeld = 8;  // kHeld: keys that a thread holds in registers
 

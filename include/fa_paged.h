@@ -119,7 +119,7 @@ typedef struct fa_paged_cache {
 /*
  * Stores token t's keys k[t] and values v[t] as position pos[t] of sequence seq[t], t < T.  Keys
  * are first normalised (k_norm f32 [D], or NULL: not) and rotated by their position pos[t], as in
- * fa_qk_norm_rope().  A token with seq[t] < 0 or pos[t] < 0 is padding and is skipped.  The
+ * fa_qk_norm_rope(): a key is stored with the same bits as one that fa_qk_norm_rope() gave out in f32.  A token with seq[t] < 0 or pos[t] < 0 is padding and is skipped.  The
  * (sequence, position) pairs of one call must address distinct rows: what a row that two tokens
  * share holds afterwards is not defined.  k [T][Hkv][D] and v [T][Hkv][Dv] (x_type) may be views
  * as above (row, head strides in elements).

@@ -131,7 +131,8 @@ fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_bounds_pool*
  *   I = sum over the block of c * hi code (c > 0) or c * lo code;  term = fl(fl(I d) e)
  *   the terms summed as a tree, neighbours first;  s = fl(scale * sum)
  *   s = fl(s + fl(alibi_slopes[h] * (position of the page's last key - (L - 1)))) where slopes are given
- * A KV head's score is the largest of its query heads'; a NaN counts as infinity.  (scale > 0: a soft cap does not
+ * A KV head's score is the largest of its query heads'; a NaN counts as infinity (q that is not finite: whatever
+ * is chosen is K pages of the sequence).  (scale > 0: a soft cap does not
  * change the order without slopes, and is left out with them.)  seq_lens[b] = 0 gives -1 everywhere; a
  * negative one marks a padding slot, whose row is left as it was; pages on an invalid page number count as the
  * least (FA_ERR_PAGE).

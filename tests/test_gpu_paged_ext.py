@@ -490,6 +490,30 @@ def test_page_select_by_clusters_of_all_sizes_and_without(fb, n, D, Hkv, G):
         assert got[0, h].tolist() == E.select(qa[0, h * G:(h + 1) * G], codes[table[0], h], scales[table[0], h], n, n, 1, G, 77, 0.1, 2, 3), h
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_are_exact_at_the_largest_codes(fb, D, sign):
+    """All codes at the ends of their range, but for one that is one smaller from page to page: the sums of products differ by 127
+    in half a million, and the order of the pages shows each."""
+    rng = np.random.default_rng(D)
+    n = 200
+    codes = np.full((n, 1, 2, D), 127, np.int8)
+    codes[:, :, 1] = -127
+    down = rng.permutation(n)  # page i is down[i] below the largest
+    for i in range(n):
+        left = int(down[i])
+        for j in range(0, 32):  # of the first block, at most 8 a component
+            take = min(left, 8)
+            codes[i, 0, 0 if sign > 0 else 1, j] -= sign * take
+            left -= take
+    cache, bounds, codes, scales, table = bounded_cache(fb, rng, n, D, 1, 1, codes=codes)
+    bounds.scales.fill_(0.25), scales.fill(0.25)
+    table = table[0]
+    q = torch.full((1, 2, D), float(sign), device="cuda")
+    got = fb.page_select(q, cache, bounds, cuda(np.array([n], np.int32)), 61, scale=1.0, first=0, last=0)
+    assert got[0, 0].tolist() == sorted(i for i in range(n) if down[table[i]] < 61)
+
+
 def test_page_select_of_queries_that_are_not_finite(fb):
     """Whatever is chosen is K different pages of the sequence."""
     rng = np.random.default_rng(9)
