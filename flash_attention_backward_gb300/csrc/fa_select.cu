@@ -6,8 +6,8 @@
 // the same bits wherever and however it is computed, and so are the pages chosen by it.
 //
 // On a GB300 (6754 GB/s measured copy rate), of GPU time.  Bounds of 75520 q8_0 keys of 4 KV heads of 256 in pages of 64 (85 MB)
-// 26 us, 48 % of that rate: some 45 instructions a row and warp, and loads of a row's 272 bytes in words, each touching
-// two or three lines.  Of the last pages of 64 sequences 4.9 us: launch, lengths, page number, rows, one after another.
+// 24.6 us, 51 % of that rate: some 45 instructions a row and warp, and loads of a row's 272 bytes in words, each touching
+// two or three lines.  Of the last pages of 64 sequences 5.0 us: launch, lengths, page number, rows, one after another.
 // Selection among 1180 pages for 4 KV heads of 256 (6 query heads each, 64 chosen) 8.5 us, for 48 ragged sequences of up to
 // 512 pages and 8 KV heads of 128 (4 query heads each) 14.7 us, where their bytes would take 0.4 and 3.9: a chain of latencies
 // too (lengths, page numbers and queries, bounds, 16 pages a warp at a time, histograms), which the larger batch
@@ -42,8 +42,8 @@ __device__ __forceinline__ int pages_of(const Cache& c, int len) { return len > 
 // bounds: a lane holds eight components, D / 8 lanes a row.  A warp takes a page of its own, or where there are not as
 // many pages the CTA's warps share one.
 
-// CTAs of four warps, eight an SM, four rows a warp under way: 26.3 us for the 75520 keys above; with eight rows and five
-// CTAs 26.8, with sixteen rows and four CTAs 26.6, a page always shared by the CTA 29.8 and more.
+// CTAs of four warps, eight an SM, eight rows a warp under way: 24.6 us for the 75520 keys above, of which each of those
+// warps takes one page; with four rows 26.0, with sixteen and five CTAs 24.2, with eight and six CTAs (two pages for some) 28.4.
 constexpr int kBoundWarps = 4, kBoundCtas = 8;
 
 __device__ __forceinline__ uint32_t load_u32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -126,7 +126,7 @@ struct Raw8 {  // a row's eight components e0 .. e0 + 7 as they lie in memory
 // Largest and smallest values of rows r0, r0 + step, ... of a page's `rows` (at least one), the lane's components
 template <int TYPE>
 __device__ __forceinline__ void row_range(const uint8_t* page, unsigned cell, int e0, int r0, int step, int rows, float (&hi)[8], float (&lo)[8]) {
-  constexpr int U = 4;  // rows under way at a time
+  constexpr int U = TYPE == FA_F32 ? 4 : 8;  // rows under way at a time
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
