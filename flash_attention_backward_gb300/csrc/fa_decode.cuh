@@ -27,10 +27,10 @@
 // More than eight query heads to a KV head read and decode its rows once for each eight (24 heads, 2 KV heads,
 // f16: 46 us where 12 heads take 36); more than 256 sequences take a launch more (300: 155 us, 83 %).
 //
-// Over selected pages: the 48 sequences above with 64 pages of 16 keys for each KV head (165 MB of rows) 38 us, 64 % of the
-// copy rate: 23 us of tiles at that rate, between 8 us until the first rows are there (launch, lengths, the items, pages and
-// page numbers, queries) and 3 until the last parts are stored.  Each KV head reads pages of its own, 256 bytes a row: with
-// the same pages for all heads 34 us.  64 of 1180 pages of 64 q8_0 keys (4 KV heads of 256) 12.8 us, latencies alone.
+// Over selected pages: the 48 sequences above with 64 pages of 16 keys for each KV head (136 MB of rows) 33 us, 62 % of the
+// copy rate: the tiles run near that rate, between 8 us until the first rows are there (launch, lengths, the items, pages
+// and page numbers, queries) and 3 until the last parts are stored.  64 of 1180 pages of 64 q8_0 keys (4 KV heads of 256)
+// 12.8 us, latencies and first passes over the code alone.
 #pragma once
 #include <algorithm>
 
@@ -630,6 +630,17 @@ __device__ __forceinline__ void tile_rows(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
+// The same from a map whose rows are those of one KV head, [rows][Hkv][row]: what a box is wider than a row is filled with
+// zeros, not read.  Heads that read pages of their own have no use for their neighbour's bytes (48 ragged sequences with 64
+// pages of 16 f16 rows of 256 bytes for each KV head: 175 MB from DRAM for 136 MB of rows without it, and 37.2 us for 32.8).
+__device__ __forceinline__ void tile_rows_of(uint32_t dst, const CUtensorMap* map, int head, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(y), "r"(bar)
+      : "memory");
+}
+__host__ __device__ constexpr bool map_by_head(bool sel, int rb) { return sel && rb % 16 == 0; }
+
 // An untiled bulk copy of a cache row and the bytes up to the 16-byte boundaries around it: those lie
 // in the same page, whose size is a multiple of 16 bytes.
 __device__ __forceinline__ void bulk_row(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
@@ -821,12 +832,16 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT, SEL).
     if (SEL) n = a.box == 16 ? min(16, there) : min(8, there) + (lane & 8);  // (a.box == 8: of the lane's box)
     const CUtensorMap* map = kv ? &map_v : &map_k;
     const int x = kv ? (hk * RBV & ~15) >> map_es(PV) : (hk * RBK & ~15) >> map_es(PK);
+    auto box = [&](uint32_t to) {
+      if (kv ? map_by_head(SEL, RBV) : map_by_head(SEL, RBK)) tile_rows_of(to, map, hk, row, bar);
+      else tile_rows(to, map, x, row, bar);
+    };
     // A slot's mask and its value rows' places are rewritten for a tile with rows missing, and after one.
     const uint32_t bit = 1u << (4 * kv + slot);
     if (a.box == 16) {
       if (lane == 0) {
         bar_expect(bar, row >= 0 ? 16 * pitch : 0);
-        if (row >= 0) tile_rows(dst, map, x, row, bar);
+        if (row >= 0) box(dst);
       }
       const bool part = n < 16 || row < 0;
       if (part || (patched & bit)) {
@@ -843,7 +858,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT, SEL).
       const uint32_t ok = __ballot_sync(kFull, (lane & 15) < n && row >= 0) & 0xffffu;
       if (lane == 0) bar_expect(bar, (((ok & 0xff) ? 1 : 0) + ((ok >> 8) ? 1 : 0)) * 8 * pitch);
       __syncwarp();
-      if (lane == 0 ? ok & 0xff : lane == 8 && (ok >> 8)) tile_rows(dst + lane * pitch, map, x, row, bar);
+      if (lane == 0 ? ok & 0xff : lane == 8 && (ok >> 8)) box(dst + lane * pitch);
       if (ok != 0xffffu || (patched & bit)) {
         patched = ok != 0xffffu ? patched | bit : patched & ~bit;
         if (kv == 0) {

@@ -11,8 +11,9 @@ namespace fap {
 
 // The pool as a matrix of cells [rows][Hkv * rb bytes], read in boxes of `box` rows x `pitch` bytes: the row,
 // what lies before it back to a 16-byte boundary, and padding that spaces the rows in shared memory.
-// Elements are as wide as keeps a box within 256 of them.
-static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, int rb, int pitch, int box_rows) {
+// Elements are as wide as keeps a box within 256 of them.  by_head: as [rows][Hkv][rb bytes], a box a head's rows and zeros
+// behind them.
+static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, int rb, int pitch, int box_rows, bool by_head) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -24,11 +25,12 @@ static bool map_pool(CUtensorMap* m, const void* pool, long long rows, int Hkv, 
   });
   if (!fn) return false;
   const int lg = map_es(pitch);
-  const cuuint64_t dims[2] = {(cuuint64_t)Hkv * rb >> lg, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)Hkv * rb};
-  const cuuint32_t box[2] = {(cuuint32_t)(pitch >> lg), (cuuint32_t)box_rows}, es[2] = {1, 1};
-  return fn(m, lg == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : lg == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT64,
-            2, const_cast<void*>(pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+  const auto type = lg == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : lg == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT64;
+  const cuuint64_t cell = (cuuint64_t)Hkv * rb;
+  const cuuint64_t dims[3] = {by_head ? (cuuint64_t)rb >> lg : cell >> lg, by_head ? (cuuint64_t)Hkv : (cuuint64_t)rows, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {by_head ? (cuuint64_t)rb : cell, cell};
+  const cuuint32_t box[3] = {(cuuint32_t)(pitch >> lg), by_head ? 1u : (cuuint32_t)box_rows, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+  return fn(m, type, by_head ? 3 : 2, const_cast<void*>(pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -119,8 +121,8 @@ static fa_status decode(const void* q, int act, int64_t q_row, int64_t q_head, c
   const long long rows = (long long)a.c.num_pages * a.c.page_size;
   const bool spaced = (a.c.Hkv * a.c.rbk) % 16 == 0 && (a.c.Hkv * a.c.rbv) % 16 == 0 && rows > 0;
   a.box = !spaced ? 0 : a.c.page_size % 16 == 0 ? 16 : a.c.page_size % 8 == 0 ? 8 : 0;
-  if (a.box && (!map_pool(&m.k, a.c.k, rows, a.c.Hkv, a.c.rbk, smem_pitch(a.c.rbk), a.box) ||
-                !map_pool(&m.v, a.c.v, rows, a.c.Hkv, a.c.rbv, smem_pitch(a.c.rbv), a.box)))
+  if (a.box && (!map_pool(&m.k, a.c.k, rows, a.c.Hkv, a.c.rbk, smem_pitch(a.c.rbk), a.box, map_by_head(pages, a.c.rbk)) ||
+                !map_pool(&m.v, a.c.v, rows, a.c.Hkv, a.c.rbv, smem_pitch(a.c.rbv), a.box, map_by_head(pages, a.c.rbv))))
     return FA_ERR_CUDA;
   const DecodeFn run = pages ? pick_decode_d<true>(a.c) : pick_decode_d<false>(a.c);
   return run(a, m, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -352,20 +352,19 @@ struct HeadPart {
   }
 };
 
-// A warp's slots in shared memory: the codes of 16 pages each, brought by asynchronous copies of 16 bytes a lane.
-// (Loaded into registers as the products take them, eight bytes of eight pages at a time: the same times, but a hundred
-// registers more and spills.)  Rows start 32 bytes, modulo 128, after one another: the words of a fragment load lie in
-// different banks.
+// A warp's slot in shared memory: the codes of 16 pages, brought by asynchronous copies of 16 bytes a lane.  (Loaded
+// into registers as the products take them, eight bytes of eight pages at a time: the same times, but a hundred
+// registers more and spills.  Two slots a warp: the same.)  Rows start 32 bytes, modulo 128, after one another: the words
+// of a fragment load lie in different banks.
 template <int D>
-struct Slots {
-  static constexpr int PITCH = 2 * D + 32, BYTES = 16 * PITCH, N = D == 256 ? 1 : 2;
+struct Slot {
+  static constexpr int PITCH = 2 * D + 32, BYTES = 16 * PITCH;
 };
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void step(float (&c)[4], uint32_t w0, uint32_t w1, uint32_t b0, uint32_t b1) {
   constexpr uint32_t kMask = 0x00ff00ffu, kBias = 0x64806480u;  // 1152, 1152; the exclusive or flips the code's sign bit
   mma_f16(c, and_xor(w0, kMask, kBias), and_xor(w1, kMask, kBias), and_xor(w0 >> 8, kMask, kBias), and_xor(w1 >> 8, kMask, kBias), b0, b1);
@@ -377,11 +376,11 @@ __device__ __forceinline__ void step(float (&c)[4], uint32_t w0, uint32_t w1, ui
 template <int D, int WARPS, typename Ready, typename Put, typename Get, typename Range>
 __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, uint8_t* slots, int b, unsigned hk, int L, int n, int c0, int c1, Ready ready,
                                             Put put, Get get, Range range) {
-  using Sl = Slots<D>;
-  constexpr int NB = D / 32, S = Sl::N, TURN = WARPS * 16;
+  using Sl = Slot<D>;
+  constexpr int NB = D / 32, TURN = WARPS * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const uint8_t* mine = slots + warp * S * Sl::BYTES;
-  const uint32_t ring = fab::smem_u32(mine);
+  const uint8_t* mine = slots + warp * Sl::BYTES;
+  const uint32_t slot = fab::smem_u32(mine);
   // Page number of page p0 + (lane & 15), not looked at before it is used (that would wait for it); and then: -1 for none.
   auto look_up = [&](int p0) {
     const int p = p0 + (lane & 15);
@@ -393,11 +392,11 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
     report_page(a.c.err);
     return -1;
   };
-  auto fetch = [&](int slot, int found) {  // their codes into a slot (where there is no page, whatever lies there)
+  auto fetch = [&](int found) {  // their codes into the slot (where there is no page, whatever lies there)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const int row = (i * 32 + lane) / (D / 8), off = (i * 32 + lane) % (D / 8) * 16, page = __shfl_sync(kFull, found, row);
-      if (page >= 0) copy16(ring + slot * Sl::BYTES + row * Sl::PITCH + off, a.codes + ((long long)page * a.c.Hkv + hk) * 2 * D + off);
+      if (page >= 0) copy16(slot + row * Sl::PITCH + off, a.codes + ((long long)page * a.c.Hkv + hk) * 2 * D + off);
     }
     copies_end();
   };
@@ -411,15 +410,12 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
   };
   for (int g0 = 0; g0 < a.G; g0 += kHeads) {
     const int ng = min(kHeads, a.G - g0), h0 = (int)hk * a.G + g0;
-    int p0 = c0 + warp * 16, slot = 0, now, later = -1;  // pages of this turn, and of the next one where its copies are under way
-    float d[NB], d2[S == 2 ? NB : 1];
-    now = look_up(p0);
-    if constexpr (S == 2) later = look_up(p0 + TURN);
+    int p0 = c0 + warp * 16, now = look_up(p0);
+    float d[NB];
     HeadPart<D, WARPS> q;
     q.ask(a, b, h0, ng);
     now = checked(now, p0);
-    fetch(0, now), scales(now, d);
-    if constexpr (S == 2) later = checked(later, p0 + TURN), fetch(1, later), scales(later, d2);
+    fetch(now), scales(now, d);
     if (g0) __syncthreads();
     q.put(a, s, ng);
     __syncthreads();
@@ -427,10 +423,10 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
     uint32_t least = 0xffffffffu, most = 0;
     const float slope[2] = {a.alibi && 2 * t < ng ? a.alibi[h0 + 2 * t] : 0.f, a.alibi && 2 * t + 1 < ng ? a.alibi[h0 + 2 * t + 1] : 0.f};
     for (; p0 < c1; p0 += TURN) {
-      int next = look_up(p0 + S * TURN);
-      copies_wait<S - 1>();
+      const int next = look_up(p0 + TURN);
+      copies_wait();
       __syncwarp();
-      const uint8_t* at = mine + slot * Sl::BYTES + g * Sl::PITCH + 8 * t;
+      const uint8_t* at = mine + g * Sl::PITCH + 8 * t;
       auto word2 = [&](int off) { return *reinterpret_cast<const uint2*>(at + off); };
       float l0[4], l1[4], l2[4], sum[4];  // the tree over the blocks, a level each
 #pragma unroll
@@ -491,19 +487,10 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
         put(p, key);
       }
       __syncwarp();  // (the slot has been read)
-      next = checked(next, p0 + S * TURN);
-      fetch(slot, next);
-      if constexpr (S == 2) {
-#pragma unroll
-        for (int k = 0; k < NB; ++k) d[k] = d2[k];
-        scales(next, d2);
-        now = later, later = next, slot ^= 1;
-      } else {
-        scales(next, d);
-        now = next;
-      }
+      now = checked(next, p0 + TURN);
+      fetch(now), scales(now, d);
     }
-    copies_wait<0>();
+    copies_wait();
     if (g0 + kHeads >= a.G) range(__reduce_min_sync(kFull, least), __reduce_max_sync(kFull, most));
   }
 }
@@ -644,7 +631,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_page_select(const Se
   extern __shared__ __align__(16) uint8_t s_slots[];  // and the keys behind them
   __shared__ __align__(16) Queries<D> s_q;
   __shared__ Bins s_bins;
-  uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_slots + WARPS * Slots<D>::N * Slots<D>::BYTES);
+  uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_slots + WARPS * Slot<D>::BYTES);
   if (cluster_rank() == 0) clear_bins(s_bins);
   cluster_arrive();
   after_last();
@@ -729,7 +716,7 @@ static fa_status check_bounds(const Cache& c, const fa_page_bounds_pool* p) {
 }
 // Bytes of the slots of a CTA, and how many keys fit shared memory beside them
 template <int D, int WARPS>
-constexpr int kSlotBytes = WARPS * Slots<D>::N * Slots<D>::BYTES;
+constexpr int kSlotBytes = WARPS * Slot<D>::BYTES;
 constexpr int kSmemKeys = 208 * 1024;
 static int one_pages(int D) {
   return (kSmemKeys - (D == 64 ? kSlotBytes<64, 16> : D == 128 ? kSlotBytes<128, 16> : kSlotBytes<256, 16>)) / 4;
