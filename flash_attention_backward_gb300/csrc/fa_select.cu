@@ -504,7 +504,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& a, Queries<D>& s, 
 constexpr int kBins = 256, kHeld = 8;  // kHeld: keys that a thread holds in registers
 
 struct Bins {
-  uint32_t n[2][kBins];      // two, so that one is empty again in time
+  alignas(16) uint32_t n[2][kBins];  // two, so that one is empty again in time
   uint32_t ends[2][16];      // a word a warp
   uint32_t least, most;      // the range of the keys that are not forced
 };
@@ -548,9 +548,9 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
     });
     __syncthreads();
     // Every warp for itself: a lane eight bins, the highest ones first; keys above each lane's bins, and then each bin's
-    uint32_t c[8], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = bins[kBins - 1 - 8 * lane - i], sum += c[i];
+    const uint4 low = reinterpret_cast<const uint4*>(bins)[62 - 2 * lane], high = reinterpret_cast<const uint4*>(bins)[63 - 2 * lane];
+    const uint32_t c[8] = {high.w, high.z, high.y, high.x, low.w, low.z, low.y, low.x};
+    const uint32_t sum = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
     uint32_t upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -592,10 +592,8 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* keys, 
   });
   if (lane == 0) s.ends[0][warp] = chosen, s.ends[1][warp] = equal;
   __syncthreads();
-  uint32_t before = 0, eq_before = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w)
-    if (w < warp) before += s.ends[0][w], eq_before += s.ends[1][w];
+  uint32_t before = __reduce_add_sync(kFull, lane < warp ? s.ends[0][lane & 15] : 0);  // (warp < 16)
+  uint32_t eq_before = __reduce_add_sync(kFull, lane < warp ? s.ends[1][lane & 15] : 0);
   before += min(eq_before, room);
   const uint32_t below = (1u << lane) - 1;
   each([&](uint32_t k, int p, bool in) {

@@ -109,8 +109,9 @@ fa_status fa_pages_trim(const fa_page_lists* lists, const int32_t* keep, void* s
  * (d and codes 0 where m <= 1e-30): code * d bounds the keys, but for a rounding.  A NaN does not enter hi and lo
  * (a component of NaNs only has hi = -inf and lo = inf); with m infinite the scale is, and the codes are 127 and -127.
  *   Computed for the pages of positions first[b] .. seq_lens[b]-1 of each sequence b, from all their rows
- * (first NULL: from 0; a negative first[b], or one that is not below the length: none).  Other pages' bounds are
- * left as they were.  D of the cache.  Alignment: codes and scales 16 bytes.
+ * (first NULL: from 0; a negative first[b], or one that is not below the length: none; a length beyond the table counts
+ * as the table's).  Other pages' bounds are left as they were; those of a page that fa_pages_trim() has cut go on covering
+ * what it held until they are computed again.  D of the cache.  Alignment: codes and scales 16 bytes.
  */
 typedef struct fa_page_bounds_pool {
   int8_t* codes;
@@ -136,7 +137,7 @@ fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_bounds_pool*
  * change the order without slopes, and is left out with them.)  seq_lens[b] = 0 gives -1 everywhere; a
  * negative one marks a padding slot, whose row is left as it was; pages on an invalid page number count as the
  * least (FA_ERR_PAGE).
- * The bounds of all n pages have been computed by fa_page_bounds().  q as in fa_paged_decode().  K >= 1.
+ * The bounds of all n pages have been computed by fa_page_bounds(); a length beyond the table counts as the table's.  q as in fa_paged_decode().  K >= 1.
  * max_pages <= 2^22, H <= 65535, B * Hkv < 2^22 (else FA_ERR_UNSUPPORTED).  Alignment: q to its element, pages,
  * seq_lens, alibi_slopes 4 bytes, codes and scales 16, workspace 256 bytes.
  */
