@@ -73,9 +73,11 @@ struct Lane {
   static constexpr int P = D / 64;
 
   __device__ __forceinline__ void place(const Rope& r) {
-    const int p = (threadIdx.x & (D / 8 - 1)) * 4;
-    n = min(max((r.n_rot >> 1) - p, 0), 4);
-    place_eight<D>(STYLE, r.n_rot, ea, eb);
+    const int p = (threadIdx.x & (D / 8 - 1)) * 4, half = r.n_rot >> 1;
+    n = min(max(half - p, 0), 4);
+    if (STYLE == FA_ROPE_PAIRS) ea = 2 * p, eb = ea + 4;
+    else if (p < half) ea = p, eb = p + half;
+    else ea = r.n_rot + (p - half), eb = ea + (D - r.n_rot) / 2;
   }
   __device__ __forceinline__ void weights(const float* weight) {
     norm = weight != nullptr;

@@ -231,7 +231,8 @@ __device__ __forceinline__ void unpack_eight(const Eight<T>& o, float2 (&x)[4]) 
   x[2] = make_float2(to_f32(o.b.v[0]), to_f32(o.b.v[1])), x[3] = make_float2(to_f32(o.b.v[2]), to_f32(o.b.v[3]));
 }
 
-// Where the lane's four pairs lie.
+// Where the lane's four pairs lie.  (The norm kernels say it again in their own words: with this in their place 16411 tokens
+// of 10 heads of 64 took 18.3 us for 17.9.)
 template <int D>
 __device__ __forceinline__ void place_eight(int style, int n_rot, int& ea, int& eb) {
   const int p = (threadIdx.x & (D / 8 - 1)) * 4, half = n_rot >> 1;
