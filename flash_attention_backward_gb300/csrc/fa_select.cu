@@ -8,8 +8,8 @@
 // On a GB300 (6754 GB/s measured copy rate), of GPU time.  Bounds of 75520 q8_0 keys of 4 KV heads of 256 in pages of 64 (85 MB)
 // 24.6 us, 51 % of that rate: some 45 instructions a row and warp, and loads of a row's 272 bytes in words, each touching
 // two or three lines.  Of the last pages of 64 sequences 5.0 us: launch, lengths, page number, rows, one after another.
-// Selection among 1180 pages for 4 KV heads of 256 (6 query heads each, 64 chosen) 8.5 us, for 48 ragged sequences of up to
-// 512 pages and 8 KV heads of 128 (4 query heads each) 14.7 us, where their bytes would take 0.4 and 3.9: a chain of latencies
+// Selection among 1180 pages for 4 KV heads of 256 (6 query heads each, 64 chosen) 8.2 us, for 48 ragged sequences of up to
+// 512 pages and 8 KV heads of 128 (4 query heads each) 14.3 us, where their bytes would take 0.4 and 3.9: a chain of latencies
 // too (lengths, page numbers and queries, bounds, 16 pages a warp at a time, histograms), which the larger batch
 // goes through one and a half times, two CTAs an SM.
 #include <algorithm>
