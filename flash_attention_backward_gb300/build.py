@@ -54,7 +54,7 @@ def _fast_command(out: str):
     inc = [a for p in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                        sysconfig.get_paths()["include"], os.path.join(_cuda_home(), "include")) for a in ("-isystem", p)]
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", abi, *inc, FAST_SRC, "-o", out, "-L", lib,
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-nostartfiles", "-fvisibility=hidden", abi, *inc, FAST_SRC, "-o", out, "-L", lib,
             "-Wl,--no-as-needed", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-Wl,-rpath,{lib}"]
 
 

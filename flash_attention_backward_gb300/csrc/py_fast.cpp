@@ -457,3 +457,8 @@ PyMODINIT_FUNC PyInit__fast(void) {
   for (int i = 0; i < 14; ++i) *names[i] = PyUnicode_InternFromString(text[i]);
   return PyModule_Create(&module);
 }
+
+// Linked without the compiler's start files: their exit routine is all that the module would run when the process ends,
+// and it would run from this file, which may have been written anew under the process by then.  The one symbol of theirs
+// that the headers name (a place that is registered with destructors of function-local objects):
+asm(".pushsection .data\n.hidden __dso_handle\n.globl __dso_handle\n.balign 8\n__dso_handle: .quad __dso_handle\n.popsection");

@@ -152,7 +152,8 @@ fa_status fa_page_select(const void* q, int act, int64_t q_row, int64_t q_head, 
  * seq_lens[b] of the pages pages[b][hk][0 .. K-1], distinct page indices of the sequence (not page numbers) in any
  * order; entries outside 0 .. ceil(seq_lens[b] / page_size)-1 are skipped.  At most the first
  * min(K, ceil(seq_lens[b] / page_size)) entries are read.  Positions, ALiBi distances among them, are those of the
- * whole sequence.  Workspace: fa_paged_decode_workspace_size().
+ * whole sequence; a score is rounded to 32 bits with its bias, so that pages far from the end, attended alone, have
+ * weights off by about 2^-24 of the bias's magnitude.  Workspace: fa_paged_decode_workspace_size().
  */
 fa_status fa_paged_decode_pages(const void* q, int act, int64_t q_row, int64_t q_head, const fa_paged_cache* cache,
                                 const int32_t* seq_lens, const int32_t* pages, int K, int H, float scale,
