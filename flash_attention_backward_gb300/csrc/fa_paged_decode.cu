@@ -83,7 +83,8 @@ extern "C" size_t fa_paged_decode_workspace_size(const fa_paged_cache* cache, in
   if (check_cache(cache, &c) != FA_OK || H < 1 || H % c.Hkv) return 0;
   int nsm = 0;
   if (fab_device(&nsm, nullptr) != FA_OK) nsm = 152;
-  return plan_decode(c, H, c.max_pages, false, nsm).bytes;
+  // of either call: the kernels over selected pages run more CTAs an SM for some types, fewer for others (a plan grows with K)
+  return std::max(plan_decode(c, H, c.max_pages, false, nsm).bytes, plan_decode(c, H, c.max_pages, true, nsm).bytes);
 }
 
 // pages [B][Hkv][K], or NULL: all of them (K is max_pages then)

@@ -1,0 +1,56 @@
+"""Attention over selected pages on the GPU: every kernel of it against 64-bit numpy, with the workspace that callers are told to
+bring.  Tolerances are those of the single-token attention, and a rounding of the output's type."""
+import numpy as np
+import pytest
+
+import paged_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_paged_ext import act_array, cuda, fb, half_step, over_pages, within  # noqa: E402,F401
+
+TYPES = ("f32", "f16", "q8_0", "q4_0")
+
+
+def some_pages(rng, lens, Hkv, page, K):
+    """[B][Hkv][K]: different pages of the sequence in any order, the last one often among them, some places empty."""
+    pages = np.full((len(lens), Hkv, K), -1, np.int32)
+    for b, L in enumerate(lens):
+        n = -(-max(L, 0) // page)
+        for hk in range(Hkv):
+            m = min(K, n)
+            mine = rng.permutation(n)[:m].astype(np.int32)
+            if m and n - 1 not in mine:
+                mine[rng.integers(0, m)] = n - 1
+            mine[rng.random(m) < 0.1] = -1
+            pages[b, hk, :m] = mine
+    return pages
+
+
+def check(fb, p, H, pages, act, softcap=0.0, al=None, sk=None, seed=0, workspace=None):
+    rng = np.random.default_rng(seed)
+    cache, n = p.on_gpu(fb, torch), cuda(np.array(p.lens, np.int32))
+    q, qa = act_array(rng, (len(p.lens), H, p.D), act)
+    scale = p.D ** -0.5
+    got = fb.paged_decode(q, cache, n, scale=scale, softcap=softcap, alibi_slopes=cuda(al), sinks=cuda(sk), pages=cuda(pages), workspace=workspace)
+    live = [b for b, L in enumerate(p.lens) if L >= 0]
+    O, lse, mag, smag = over_pages(p, {(b, hk): pages[b, hk] for b in range(len(p.lens)) for hk in range(p.Hkv)}, qa, scale, softcap, al, sk)
+    tol_O, tol_lse = R.decode_tolerance(p, mag, smag, act)
+    within(got["O"].float().cpu().numpy()[live], O[live], tol_O[live] + half_step(act, O[live]), "O")
+    within(got["lse"].cpu().numpy()[live], lse[live], tol_lse[live], "lse")
+    assert fb.fa_back_get_error() == 0
+    return cache, q, n, got
+
+
+@pytest.mark.parametrize("B, Hkv, H, page, K, L", [(48, 1, 1, 16, 64, 8000), (8, 8, 8, 64, 64, 6000)])
+def test_the_types_whose_kernels_run_more_ctas_than_the_plain_ones(fb, B, Hkv, H, page, K, L):
+    """Keys of 64 components in q8_0 and values of 256 in f32 take three CTAs an SM over selected pages, two over all: more partial
+    sums.  The size that fa_paged_decode_workspace_size() gives does for both."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(L // 2, L, B)]
+    p = R.Paged(B, lens, Hkv, 64, 256, R.synth.TYPE_Q8_0, R.synth.TYPE_F32, page)
+    pages = some_pages(rng, lens, Hkv, page, K)
+    cache, q, n, got = check(fb, p, H, pages, "f32")
+    again = fb.paged_decode(q, cache, n, scale=64 ** -0.5, pages=cuda(pages), workspace=fb.Workspace())
+    assert torch.equal(got["O"], again["O"]) and torch.equal(got["lse"], again["lse"])
