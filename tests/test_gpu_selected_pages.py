@@ -54,3 +54,21 @@ def test_the_types_whose_kernels_run_more_ctas_than_the_plain_ones(fb, B, Hkv, H
     cache, q, n, got = check(fb, p, H, pages, "f32")
     again = fb.paged_decode(q, cache, n, scale=64 ** -0.5, pages=cuda(pages), workspace=fb.Workspace())
     assert torch.equal(got["O"], again["O"]) and torch.equal(got["lse"], again["lse"])
+
+
+@pytest.mark.parametrize("page, K, lens", [(40, 64, (100, 700, 39)), (5, 21, (9, 90)), (12, 7, (3, 300)), (1, 40, (70, 20))])
+def test_distances_where_selected_keys_end_inside_a_tile(fb, page, K, lens):
+    """ALiBi over lists longer than the sequence has pages: what stands behind them does not matter, nor do entries that are
+    no page."""
+    rng = np.random.default_rng(page)
+    p = R.Paged(page, lens, 2, 64, 64, R.synth.TYPE_F16, R.synth.TYPE_F16, page)
+    pages = some_pages(rng, lens, 2, page, K)
+    al = (2.0 ** -np.arange(2, 6)).astype(np.float32)
+    cache, q, n, got = check(fb, p, 4, pages, "f32", al=al)
+    for b, L in enumerate(lens):
+        m = -(-L // page)
+        pages[b, :, m:] = rng.integers(-2 ** 31, 2 ** 31, pages[b, :, m:].shape)  # behind the sequence's pages
+        pages[b, :, :m][pages[b, :, :m] < 0] = 2 ** 31 - 1
+    again = fb.paged_decode(q, cache, n, scale=64 ** -0.5, alibi_slopes=cuda(al), pages=cuda(pages))
+    assert torch.equal(got["O"], again["O"]) and torch.equal(got["lse"], again["lse"])
+    assert fb.fa_back_get_error() == 0

@@ -39,3 +39,35 @@ def test_the_workspace_that_is_asked_for_does_for_every_call(decode):
                               for k in (0, K) for sms in (152, 1)]
     for case, (need, rc) in zip(cases, decode(cases)):
         assert need > 0 and rc == 0, (case, need, rc)
+
+
+@pytest.fixture(scope="module")
+def position(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("position") / "position")
+    checks = [x for f in ("-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=all") for x in ("-Xcompiler", f)]
+    subprocess.run([B.nvcc(), *B.ARCH, "-std=c++17", *checks, "-I", B.INCLUDE, os.path.join(HERE, "selected_position_host.cu"), "-o", exe], check=True)
+
+    def run(L, page, K, at, sel):
+        r = subprocess.run([exe], input=" ".join(map(str, [L, page, K, at, *sel])) + "\n", capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-2000:]
+        return int(r.stdout)
+    return run
+
+
+@pytest.mark.parametrize("L, page, K, sel", [
+    (100, 40, 64, [2, 0, 1]),            # three pages, of 64 entries three are read; 120 keys end inside a tile
+    (9, 5, 21, [1, -1]),
+    (3, 12, 7, [0]),
+    (70, 1, 40, list(range(69, 29, -1))),
+    (300, 16, 4, [2 ** 31 - 1, 3, -2 ** 31, 18]),
+])
+def test_positions_of_selected_keys(position, L, page, K, sel):
+    """At most min(K, ceil(L / page)) entries of a list are read, for the places behind its last key in a tile of 16 too,
+    and entries that are no page of the sequence (any number) do not leave the range of an int."""
+    n = -(-L // page)
+    assert len(sel) == min(K, n)
+    keys = len(sel) * page
+    for at in sorted({0, 1, page - 1, keys // 2, keys - 1, keys, keys + (-keys) % 16, -(-keys // 16) * 16 - 1}):
+        got = position(L, page, K, at, sel)
+        if at < keys and 0 <= sel[at // page] < n:
+            assert got == sel[at // page] * page + at % page, at
