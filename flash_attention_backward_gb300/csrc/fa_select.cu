@@ -262,7 +262,7 @@ struct SelectArgs {
   long long q_row, q_head;
   const int32_t* lens;
   int H, G, K, first, last;
-  float scale;
+  float scale, top;  // |scale|; the code of a block's largest magnitude, 127 with the sign of scale (q changes it with scale)
   bool vec;        // every head of q starts on 16 bytes
   const float* alibi;
   uint32_t* keys;  // [B][Hkv][max_pages]
@@ -327,7 +327,7 @@ struct HeadPart {
     top = max(top, __shfl_xor_sync(kFull, top, 2));
     const float m = __uint_as_float(top);
     const bool some = m > kTinyAmax && g < ng;
-    const float r = __fdiv_rn(127.f, m);
+    const float r = __fdiv_rn(a.top, m);
     int c[8], sum = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -798,7 +798,7 @@ extern "C" fa_status fa_page_select(const void* q, int act, int64_t q_row, int64
   if ((rc = check_bounds(a.c, bounds)) != FA_OK) return rc;
   if (!act_type(act)) return FA_ERR_TYPE;
   if (H < 1 || H % a.c.Hkv != 0 || q_row < 0 || q_head < 0) return FA_ERR_SHAPE;
-  if (K < 1 || first < 0 || last < 0 || (long long)first + last > K) return FA_ERR_SHAPE;
+  if (K < 1 || first < 0 || last < 0 || (long long)first + last > K || !std::isfinite(scale)) return FA_ERR_SHAPE;
   if (!select_range(a.c, H) || (long long)a.c.B * a.c.Hkv * K > (1LL << 40)) return FA_ERR_UNSUPPORTED;
   if (a.c.B > 0 && (!q || !seq_lens || !pages)) return FA_ERR_NULL;
   if (!aligned(q, act_bytes(act)) || !aligned(seq_lens, 4) || !aligned(alibi_slopes, 4) || !aligned(pages, 4)) return FA_ERR_ALIGN;
@@ -808,7 +808,8 @@ extern "C" fa_status fa_page_select(const void* q, int act, int64_t q_row, int64
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
   if (a.c.B == 0) return FA_OK;
   a.codes = bounds->codes, a.scales = bounds->scales, a.q = q, a.act = act, a.q_row = q_row, a.q_head = q_head, a.lens = seq_lens;
-  a.H = H, a.G = H / a.c.Hkv, a.K = K, a.first = first, a.last = last, a.scale = scale, a.alibi = alibi_slopes;
+  a.H = H, a.G = H / a.c.Hkv, a.K = K, a.first = first, a.last = last, a.scale = std::fabs(scale), a.top = std::copysign(127.f, scale);
+  a.alibi = alibi_slopes;
   a.keys = static_cast<uint32_t*>(workspace), a.pages = pages;
   const int es = act_bytes(act);
   a.vec = aligned(q, 16) && (q_row * es) % 16 == 0 && (q_head * es) % 16 == 0;

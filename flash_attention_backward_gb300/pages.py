@@ -153,8 +153,8 @@ def page_select(q: torch.Tensor, cache: "paged.PagedCache", bounds: PageBounds, 
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """For each query q [B][H][D] (as paged_decode() takes it) and KV head, the K pages of its sequence whose bounds promise
     the largest scores, the sequence's `first` first and `last` last ones always among them: int32 [B][Hkv][K], ascending,
-    -1 behind the last where the sequence has fewer; what paged_decode() takes as pages.  The choice is exact: the
-    score is defined to the bit, and of equal ones the lowest page is taken."""
+    -1 behind the last where the sequence has fewer; what paged_decode() takes as pages, with the same scale (finite, of
+    either sign).  The choice is exact: the score is defined to the bit, and of equal ones the lowest page is taken."""
     bounds._fits(cache)
     if stream is None and out is None and workspace is None and cache._index is not None and (paged._plain or paged._bind()):
         got = paged._fast.select(q, cache._at, cache._index, bounds._at, seq_lens, K, scale, first, last, alibi_slopes)

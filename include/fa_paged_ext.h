@@ -133,10 +133,10 @@ fa_status fa_page_bounds(const fa_paged_cache* cache, const fa_page_bounds_pool*
  *   the terms summed as a tree, neighbours first;  s = fl(scale * sum)
  *   s = fl(s + fl(alibi_slopes[h] * (position of the page's last key - (L - 1)))) where slopes are given
  * A KV head's score is the largest of its query heads'; a NaN counts as infinity (q that is not finite: whatever
- * is chosen is K pages of the sequence).  (scale > 0: a soft cap does not
- * change the order without slopes, and is left out with them.)  seq_lens[b] = 0 gives -1 everywhere; a
- * negative one marks a padding slot, whose row is left as it was; pages on an invalid page number count as the
- * least (FA_ERR_PAGE).
+ * is chosen is K pages of the sequence).  A negative scale counts as -scale with -q; one that is not finite is refused
+ * (FA_ERR_SHAPE).  A soft cap does not change the order without slopes, and is left out with them.
+ * seq_lens[b] = 0 gives -1 everywhere; a negative one marks a padding slot, whose row is left as it was; pages on an
+ * invalid page number count as the least (FA_ERR_PAGE).
  * The bounds of all n pages have been computed by fa_page_bounds(); a length beyond the table counts as the table's.  q as in fa_paged_decode().  K >= 1.
  * max_pages <= 2^22, H <= 65535, B * Hkv < 2^22 (else FA_ERR_UNSUPPORTED).  Alignment: q to its element, pages,
  * seq_lens, alibi_slopes 4 bytes, codes and scales 16, workspace 256 bytes.
