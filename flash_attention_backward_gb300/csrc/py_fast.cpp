@@ -87,7 +87,7 @@ struct Args {
     const uint8_t* axis = flat<uint8_t>(i, at::kByte, r.n_rot / 2, false);
     const at::Tensor* x = ok ? tensor(j) : nullptr;
     if (!ok) return nullptr;
-    if (x->dim() != 2 || x->scalar_type() != at::kInt || x->size(1) != n || (n > 1 && x->stride(1) != 1)) return ok = false, nullptr;
+    if (x->dim() != 2 || x->scalar_type() != at::kInt || x->size(0) > INT32_MAX || x->size(1) != n || (n > 1 && x->stride(1) != 1)) return ok = false, nullptr;
     *out = fa_rope_axes{r.freqs, axis, x->stride(0), r.n_rot, r.style, (int32_t)x->size(0)};
     return static_cast<const int32_t*>(x->data_ptr());
   }

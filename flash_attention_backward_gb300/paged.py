@@ -103,6 +103,12 @@ def _heads(name: str, t: torch.Tensor, N: int, D: int, dtype, device):
                       f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
+def _int32(name: str, what: str, v: int, least: int = -2 ** 31) -> None:
+    """The C entry points take v as an int: one beyond it would be cut to another."""
+    if not least <= v < 2 ** 31:
+        raise FaBackError(f"{name}: {what} expected, got {v}")
+
+
 class _On:
     """Around a call: its stream's device is current, and with `stream` given, what it allocates belongs
     to that stream.  Only made where that is not so already."""
@@ -166,6 +172,7 @@ def _axes(rope: Optional[torch.Tensor], axes: Optional[torch.Tensor], style: int
             N > 1 and pos.stride(1) != 1):
         raise FaBackError(f"{name}: int32 [axes][{N}] with rows of neighbouring elements on {device} expected, got " + (
             "None" if pos is None else f"{pos.dtype} {tuple(pos.shape)}, strides {pos.stride()}, on {pos.device}"))
+    _int32(name, "positions of one to eight axes", pos.shape[0])
     return nat.fa_rope_axes(r.freqs, p_axes, pos.stride(0), r.n_rot, style, pos.shape[0]), pos.data_ptr()
 
 
@@ -296,6 +303,7 @@ def paged_decode(q: torch.Tensor, cache: PagedCache, seq_lens: torch.Tensor, *, 
     p_sinks = None if sinks is None else _expect("sinks", sinks, _F32, (H,), dev)
     if pages is not None:
         K = pages.shape[2] if pages.dim() == 3 else 0
+        _int32("pages", "fewer than 2^31 of a KV head", K)
         p_pages = _expect("pages", pages, _I32, (B, cache.Hkv, K), dev)
     _index(dev)
 

@@ -14,7 +14,7 @@ import torch
 from . import _native as nat
 from . import paged
 from .api import FaBackError, Workspace, _check
-from .paged import _F32, _I32, _act, _call, _empty, _expect, _heads, _index
+from .paged import _F32, _I32, _act, _call, _empty, _expect, _heads, _index, _int32
 
 
 def rope_sections(sections: Sequence[int], *, interleaved: bool = False, device="cuda") -> torch.Tensor:
@@ -57,6 +57,8 @@ class PageLists(_Held):
         self.page_table, self.seq_lens, self.free, self.num_free, self.page_size = page_table, seq_lens, free, num_free, page_size
         self.B, self.max_pages = page_table.shape
         self.num_pages, self.device = free.shape[0], page_table.device
+        for name, n in (("page_table", max(page_table.shape)), ("free", self.num_pages), ("page_size", page_size)):
+            _int32(name, "sizes below 2^31", n)
         self.c = nat.fa_page_lists(
             _expect("page_table", page_table, _I32, tuple(page_table.shape), self.device),
             _expect("seq_lens", seq_lens, _I32, (self.B,), self.device), _expect("free", free, _I32, tuple(free.shape), self.device),
@@ -84,8 +86,7 @@ def pages_extend(lists: PageLists, new_tokens: torch.Tensor, T: int, *, stream: 
             return got
     dev = lists.device
     p_new = _expect("new_tokens", new_tokens, _I32, (lists.B,), dev)
-    if T < 0:
-        raise FaBackError(f"T: a number of tokens expected, got {T}")
+    _int32("T", "a number of tokens", T, 0)
     _index(dev)
 
     def run(s):
@@ -165,6 +166,8 @@ def page_select(q: torch.Tensor, cache: "paged.PagedCache", bounds: PageBounds, 
     H, q_row, q_head = _heads("q", q, B, cache.D, dtype, dev)
     p_len = _expect("seq_lens", seq_lens, _I32, (B,), dev)
     p_alibi = None if alibi_slopes is None else _expect("alibi_slopes", alibi_slopes, _F32, (H,), dev)
+    for name, n in (("K", K), ("first", first), ("last", last)):
+        _int32(name, "a number of pages", n)
     _index(dev)
 
     def run(s):
