@@ -72,3 +72,23 @@ def test_distances_where_selected_keys_end_inside_a_tile(fb, page, K, lens):
     again = fb.paged_decode(q, cache, n, scale=64 ** -0.5, alibi_slopes=cuda(al), pages=cuda(pages))
     assert torch.equal(got["O"], again["O"]) and torch.equal(got["lse"], again["lse"])
     assert fb.fa_back_get_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Dv", [64, 128, 256])
+def test_every_pair_of_types(fb, D, Dv):
+    """Each kernel over selected pages: seeded lengths, page sizes (boxes of 16 and 8 rows, single rows), lists and extensions."""
+    r = np.random.default_rng(D + 3 * Dv)
+    pick = lambda *a: a[int(r.integers(len(a)))]  # noqa: E731
+    for kt in range(4):
+        for vt in range(4):
+            Hkv, G, K, act = pick(1, 2, 3), pick(1, 3, 8, 9), pick(1, 5, 20, 60), pick("f32", "f16", "bf16")
+            page = pick(8, 16, 24, 64, 5, 12)
+            if page * Hkv * R.synth.row_bytes(kt, D) % 16 or page * Hkv * R.synth.row_bytes(vt, Dv) % 16:
+                page = 16
+            lens = [int(x) for x in np.exp(r.uniform(-0.5, np.log(3000), int(r.integers(1, 6))))] + [0]
+            p = R.Paged(16 * D + 4 * kt + vt, lens, Hkv, D, Dv, kt, vt, page)
+            H = G * Hkv
+            al = (2.0 ** -np.linspace(2, 9, H)).astype(np.float32) if pick(True, False) else None
+            sk = r.standard_normal(H).astype(np.float32) if pick(True, False) else None
+            check(fb, p, H, some_pages(r, lens, Hkv, page, K), act, pick(0.0, 0.0, 20.0), al, sk, seed=kt)
