@@ -479,7 +479,7 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) {
   const int L = a.lens[b];
   return min(max(L, 0), a.c.max_pages * a.c.page_size);
 }
-__host__ __device__ __forceinline__ int pages_of(const Cache& c, int len) {
+__device__ __forceinline__ int pages_of(const Cache& c, int len) {
   return len > 0 ? (int)((uint64_t)(len - 1) * c.page_mul >> c.page_shift) + 1 : 0;
 }
 // Keys of sequence b: its length; with selected pages the keys of as many of them as there can be, the places of
@@ -678,20 +678,20 @@ static __device__ __noinline__ float4 cap_and_bias(float4 x, float cap, float sl
                      fmaf(slope, (float)(d + 9), x.w));
 }
 
-// The position of place `at` among the keys of selected pages of a sequence of L keys.  Only the list's first entries that
-// can be pages are read, for places behind the last of their keys too, and an entry that is no page of the sequence counts
-// as its first: those keys are masked.
-__host__ __device__ __forceinline__ int selected_position(const Cache& c, const int32_t* sel, int K, int at, int L) {
-  const int p = (int)((uint64_t)at * c.page_mul >> c.page_shift), n = pages_of(c, L), page = sel[min(p, min(K, n) - 1)];
-  return (page >= 0 && page < n ? page * c.page_size : 0) + (at - p * c.page_size);
+// The position of place `at` among the keys of selected pages (keys: how many places there are, whole pages).  Places behind the
+// last one count as the last, so that no more of the list is read, and an entry that is no page as some page: those keys are masked.
+__host__ __device__ __forceinline__ int selected_position(const Cache& c, const int32_t* sel, int keys, int at) {
+  at = min(at, keys - 1);
+  const int p = (int)((uint64_t)at * c.page_mul >> c.page_shift);
+  return (int)min((uint32_t)sel[p], (uint32_t)c.max_pages - 1) * c.page_size + (at - p * c.page_size);
 }
 // The same where the keys are those of selected pages, whose positions the list says (places j, j + 1, j + 8, j + 9 of
 // its keys; those behind its end are masked, whatever they get).
-static __device__ __noinline__ float4 cap_and_bias_sel(float4 x, float cap, float slope, const Cache& c, const int32_t* sel, int K, int j, int L) {
+static __device__ __noinline__ float4 cap_and_bias_sel(float4 x, float cap, float slope, const Cache& c, const int32_t* sel, int keys, int j, int L) {
   float4 y = cap_and_bias(x, cap, 0.f, 0);
   float far[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) far[i] = (float)(selected_position(c, sel, K, j + (i & 1) + 8 * (i >> 1), L) - (L - 1));
+  for (int i = 0; i < 4; ++i) far[i] = (float)(selected_position(c, sel, keys, j + (i & 1) + 8 * (i >> 1)) - (L - 1));
   y.x = fmaf(slope, far[0], y.x), y.y = fmaf(slope, far[1], y.y), y.z = fmaf(slope, far[2], y.z), y.w = fmaf(slope, far[3], y.w);
   return y;
 }
@@ -993,7 +993,7 @@ __global__ void __launch_bounds__(kWarps * 32, decode_shape(D, DV, KT, VT, SEL).
       for (int i = 0; i < 4; ++i) s[i] *= qscale;
       if (ext) {
         const float4 y = make_float4(s[0], s[1], s[2], s[3]);
-        const float4 x = SEL && a.alibi ? cap_and_bias_sel(y, a.softcap, slope, a.c, sel, a.K, j0 + tile * 16 + 2 * t, len)
+        const float4 x = SEL && a.alibi ? cap_and_bias_sel(y, a.softcap, slope, a.c, sel, keys, j0 + tile * 16 + 2 * t, len)
                                         : cap_and_bias(y, a.softcap, slope, j0 + tile * 16 + 2 * t - (keys - 1));
         s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
       }

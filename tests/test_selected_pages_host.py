@@ -47,8 +47,8 @@ def position(tmp_path_factory):
     checks = [x for f in ("-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=all") for x in ("-Xcompiler", f)]
     subprocess.run([B.nvcc(), *B.ARCH, "-std=c++17", *checks, "-I", B.INCLUDE, os.path.join(HERE, "selected_position_host.cu"), "-o", exe], check=True)
 
-    def run(L, page, K, at, sel):
-        r = subprocess.run([exe], input=" ".join(map(str, [L, page, K, at, *sel])) + "\n", capture_output=True, text=True)
+    def run(page, max_pages, at, sel):
+        r = subprocess.run([exe], input=" ".join(map(str, [page, max_pages, at, *sel])) + "\n", capture_output=True, text=True)
         assert r.returncode == 0, r.stderr[-2000:]
         return int(r.stdout)
     return run
@@ -68,6 +68,6 @@ def test_positions_of_selected_keys(position, L, page, K, sel):
     assert len(sel) == min(K, n)
     keys = len(sel) * page
     for at in sorted({0, 1, page - 1, keys // 2, keys - 1, keys, keys + (-keys) % 16, -(-keys // 16) * 16 - 1}):
-        got = position(L, page, K, at, sel)
+        got = position(page, n + 2, at, sel)
         if at < keys and 0 <= sel[at // page] < n:
             assert got == sel[at // page] * page + at % page, at
