@@ -459,6 +459,8 @@ PyMODINIT_FUNC PyInit__fast(void) {
 }
 
 // Linked without the compiler's start files: their exit routine is all that the module would run when the process ends,
-// and it would run from this file, which may have been written anew under the process by then.  The one symbol of theirs
-// that the headers name (a place that is registered with destructors of function-local objects):
+// and it would run from this file.  A process whose file was written anew in place after its last call ends in order so;
+// nothing else about such a process is safe, a call into the module least of all (build.py writes beside the old file
+// and renames, which leaves a process the file that it has loaded).  The one symbol of the start files that the headers name (a
+// place that is registered with destructors of function-local objects):
 asm(".pushsection .data\n.hidden __dso_handle\n.globl __dso_handle\n.balign 8\n__dso_handle: .quad __dso_handle\n.popsection");

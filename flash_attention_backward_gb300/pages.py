@@ -47,7 +47,8 @@ class _Held:
 class PageLists(_Held):
     """Who holds which page of a pool of free.numel() pages of page_size positions: page_table (int32 [B][max_pages]) and
     seq_lens (int32 [B]; negative: a slot without a request), which PagedCache and paged_decode() take, and the pages that
-    nobody holds, free[:num_free] (int32 [num_pages], [1]), the last one to be taken first.  Holds the tensors, which
+    nobody holds, free[:num_free] (int32 [num_pages], [1]), the last one to be taken first.  num_pages and page_size are those
+    of the cache that the pages are of; no call sees both to compare them.  Holds the tensors, which
     pages_extend() and pages_trim() edit in place; a request is taken in by setting its length to 0."""
 
     def __init__(self, page_table: torch.Tensor, seq_lens: torch.Tensor, free: torch.Tensor, num_free: torch.Tensor, *,
@@ -110,8 +111,10 @@ def pages_trim(lists: PageLists, keep: torch.Tensor, *, stream: Optional[torch.c
 
 class PageBounds(_Held):
     """The bounds of a cache's keys page by page: codes (int8 [num_pages][Hkv][2][D]) and scales (f32
-    [num_pages][Hkv][D / 32]); the largest value of a component in a page is at most codes[..., 0, :] times its block's
-    scale, the smallest at least codes[..., 1, :] times it.  Holds the tensors."""
+    [num_pages][Hkv][D / 32]): the largest value of a component in a page is about codes[..., 0, :] times its block's
+    scale, the smallest codes[..., 1, :] times it, rounded outward.  They bound the keys but for f32's roundings of scale and
+    quotient (2^-22 of the block's largest magnitude); a block without a magnitude above 1e-30 counts as zeros, and a NaN is
+    left out.  Holds the tensors."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         if codes.dim() != 4 or codes.shape[2] != 2 or codes.shape[3] % 32:

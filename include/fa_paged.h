@@ -119,9 +119,10 @@ typedef struct fa_paged_cache {
 /*
  * Stores token t's keys k[t] and values v[t] as position pos[t] of sequence seq[t], t < T.  Keys
  * are first normalised (k_norm f32 [D], or NULL: not) and rotated by their position pos[t], as in
- * fa_qk_norm_rope(): a key is stored with the same bits as one that fa_qk_norm_rope() gave out in f32.  A token with seq[t] < 0 or pos[t] < 0 is padding and is skipped.  The
- * (sequence, position) pairs of one call must address distinct rows: what a row that two tokens
- * share holds afterwards is not defined.  k [T][Hkv][D] and v [T][Hkv][Dv] (x_type) may be views
+ * fa_qk_norm_rope(): a key is stored with the same bits as one that fa_qk_norm_rope() gave out in f32
+ * (but for the sign of a zero that is not rotated, with FA_ROPE_PAIRS).  A token with seq[t] < 0 or
+ * pos[t] < 0 is padding and is skipped.  The (sequence, position) pairs of one call must address
+ * distinct rows: what a row that two tokens share holds afterwards is not defined.  k [T][Hkv][D] and v [T][Hkv][Dv] (x_type) may be views
  * as above (row, head strides in elements).
  *   FA_F32, FA_F16  the value, rounded to nearest.
  *   FA_Q8_0  d = amax / 127; code = x / d to the nearest, ties away from zero.

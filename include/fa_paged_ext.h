@@ -111,7 +111,8 @@ fa_status fa_pages_trim(const fa_page_lists* lists, const int32_t* keep, void* s
  *   Computed for the pages of positions first[b] .. seq_lens[b]-1 of each sequence b, from all their rows
  * (first NULL: from 0; a negative first[b], or one that is not below the length: none; a length beyond the table counts
  * as the table's).  Other pages' bounds are left as they were; those of a page that fa_pages_trim() has cut go on covering
- * what it held until they are computed again.  D of the cache.  Alignment: codes and scales 16 bytes.
+ * what it held until they are computed again.  Sequences of a call that hold the same page hold as many of its rows each (a
+ * common prefix of whole pages); otherwise its bounds are not defined.  D of the cache.  Alignment: codes and scales 16 bytes.
  */
 typedef struct fa_page_bounds_pool {
   int8_t* codes;
