@@ -108,6 +108,7 @@ fa_status fa_pages_trim(const fa_page_lists* lists, const int32_t* keep, void* s
  *   m = max(|hi|, |lo|);  d = fl(m / 127);  codes ceil(fl(hi / d)) and floor(fl(lo / d)), within -127 .. 127
  * (d and codes 0 where m <= 1e-30): code * d bounds the keys, but for a rounding.  A NaN does not enter hi and lo
  * (a component of NaNs only has hi = -inf and lo = inf); with m infinite the scale is, and the codes are 127 and -127.
+ * (A q8_0 or q4_0 block whose stored scale is infinite counts as infinite, whatever its codes.)
  *   Computed for the pages of positions first[b] .. seq_lens[b]-1 of each sequence b, from all their rows
  * (first NULL: from 0; a negative first[b], or one that is not below the length: none; a length beyond the table counts
  * as the table's).  Other pages' bounds are left as they were; those of a page that fa_pages_trim() has cut go on covering
