@@ -44,7 +44,7 @@ def test_the_workspace_that_is_asked_for_does_for_every_call(decode):
 @pytest.fixture(scope="module")
 def position(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("position") / "position")
-    checks = [x for f in ("-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=all") for x in ("-Xcompiler", f)]
+    checks = [x for f in ("-fsanitize=undefined", "-fno-sanitize-recover=all") for x in ("-Xcompiler", f)]
     subprocess.run([B.nvcc(), *B.ARCH, "-std=c++17", *checks, "-I", B.INCLUDE, os.path.join(HERE, "selected_position_host.cu"), "-o", exe], check=True)
 
     def run(page, max_pages, at, sel):
